@@ -22,6 +22,19 @@ class MoEConfig(ctypes.Structure):
                 ("max_top_k", ctypes.c_int32), ("device", ctypes.c_int32)]
 
 
+class AttnConfig(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("max_sms", ctypes.c_int32),
+                ("device", ctypes.c_int32), ("rope_freqs", ctypes.c_void_p)]
+
+
+class PagedKVDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + \
+               [(n, ctypes.c_int64) for n in ("n_pages", "page_stride", "head_stride", "slot_stride",
+                                              "scale_page_stride", "scale_head_stride", "scale_slot_stride")] + \
+               [("page_size", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
 def _constants() -> dict:
     """#define MOE_* integer constants of the header."""
     out = {}
@@ -48,7 +61,7 @@ def lib():
         raise RuntimeError(f"{LIB_PATH} is not built; run `python -c 'import __graft_entry__ as g; g.build()'` "
                            "or `python -m fp8_routed_expert_gb300.build`")
     L = ctypes.CDLL(LIB_PATH)
-    vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
     sig = {
         "moe_init": ([ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(MoEConfig)], ctypes.c_int),
         "moe_layer_forward": ([vp, vp, i64, vp, vp, vp, vp, vp, vp, i32, vp, vp], ctypes.c_int),
@@ -78,6 +91,17 @@ def lib():
         "moe_attention_workspace_bytes": ([i64, i64, i32, i32], i64),
         "moe_decode_attention": ([vp, vp, vp, i64, i64, i32, i32, i32, vp, vp, i64, vp],
                                  ctypes.c_int),
+        "moe_attn_init": ([ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(AttnConfig)], ctypes.c_int),
+        "moe_attn_free": ([vp], None),
+        "moe_attn_status": ([vp], ctypes.c_int),
+        "moe_attn_norm_rope": ([vp, vp, i64, vp, i64, vp, i64, vp, vp, f32, vp, i64, vp, i64, vp],
+                               ctypes.c_int),
+        "moe_attn_append": ([vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, vp, f32, vp, i64, vp],
+                            ctypes.c_int),
+        "moe_attn_write": ([vp, vp, vp, i64, vp, i64, vp, i64, vp], ctypes.c_int),
+        "moe_attn_read": ([vp, vp, vp, i64, vp, i64, vp, i64, vp], ctypes.c_int),
+        "moe_attn_decode": ([vp, vp, vp, i64, vp, i64, i64, vp, vp, i64, f32, f32, vp, i32, vp, vp, vp],
+                            ctypes.c_int),
         "moe_route_noalloc": ([vp, i64, i64, vp, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp],
                               ctypes.c_int),
         "moe_debug_copy": ([vp, ctypes.c_char_p, vp, i64, ctypes.POINTER(ctypes.c_int64), vp],

@@ -1,0 +1,249 @@
+"""Attention over a paged key/value cache: the serving form of the attention
+beside the MoE.  ``PagedKVCache`` describes the cache, ``DecodeAttention`` is
+the context whose calls norm and rotate heads, write and read the cache and
+attend to it (moe_attn_* of include/fp8moe.h, where each call's arithmetic,
+layouts and errors are stated).  Every step runs in the library's kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from ._lib import C, AttnConfig, PagedKVDesc, check, lib
+from .layer import _stream_handle
+
+_BF16 = torch.bfloat16
+
+
+def rope_frequencies(rope_dim: int, theta: float = 10000.0) -> list[float]:
+    """The usual frequencies theta^(-2i/R), i < R/2, in radians per position."""
+    return [theta ** (-2.0 * i / rope_dim) for i in range(rope_dim // 2)]
+
+
+class PagedKVCache:
+    """Key/value pages in device memory: ``k`` and ``v`` of shape [n_pages,
+    n_kv_heads, page_size, head_dim], bf16, or uint8 (e4m3 codes) with f32
+    ``k_scale`` / ``v_scale`` [n_pages, n_kv_heads, page_size].  The tensors
+    may be views with any strides whose rows are contiguous (a permuted
+    layout, one layer of a larger allocation); ``v`` has ``k``'s strides."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        if k.dim() != 4 or not k.is_cuda or k.dtype not in (_BF16, torch.uint8):
+            raise ValueError("k must be a cuda bf16 or uint8 tensor [n_pages, n_kv_heads, page_size, head_dim]")
+        if v.dtype != k.dtype or v.shape != k.shape or v.device != k.device or v.stride() != k.stride():
+            raise ValueError("v must match k in type, shape, strides and device")
+        if k.stride(3) != 1:
+            raise ValueError("the rows of k and v must be contiguous")
+        e4m3 = k.dtype == torch.uint8
+        if e4m3:
+            for s in (k_scale, v_scale):
+                if s is None or s.dtype != torch.float32 or s.shape != k.shape[:3] or s.device != k.device:
+                    raise ValueError(f"an e4m3 cache needs f32 scales {tuple(k.shape[:3])} on its device")
+            if k_scale.stride() != v_scale.stride():
+                raise ValueError("v_scale must have k_scale's strides")
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bf16 cache has no scales")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        self.format = "e4m3" if e4m3 else "bf16"
+        self.device = k.device
+        ss = k_scale.stride() if e4m3 else (0, 0, 0)
+        self._desc = PagedKVDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
+                                 v_scale.data_ptr() if e4m3 else None, self.n_pages, *k.stride()[:3], *ss,
+                                 self.page_size, C["MOE_KV_E4M3"] if e4m3 else C["MOE_KV_BF16"])
+        self._ref = ctypes.addressof(self._desc)
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, format: str = "bf16",
+              device: int = 0) -> "PagedKVCache":
+        """A new cache, rows of one (page, head) next to each other.  Memory is
+        not initialised: positions are attended to only once written."""
+        if format not in ("bf16", "e4m3"):
+            raise ValueError(f"format must be 'bf16' or 'e4m3', got {format!r}")
+        dev = torch.device("cuda", device)
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        dt = _BF16 if format == "bf16" else torch.uint8
+        kv = [torch.empty(shape, dtype=dt, device=dev) for _ in range(2)]
+        sc = [torch.empty(shape[:3], dtype=torch.float32, device=dev) for _ in range(2)] if format == "e4m3" else []
+        return cls(*kv, *sc)
+
+
+class DecodeAttention:
+    """A context for one head layout (moe_attn_init).  ``rope_freqs``: radians
+    per position of each rotated pair (``rope_frequencies``), None for no
+    rotation; its length is half the rotated elements of a head.  One context
+    serves one stream at a time."""
+
+    def __init__(self, n_heads: int, n_kv_heads: int, head_dim: int, rope_freqs=None,
+                 interleaved: bool = False, device: int = 0, max_sms: int = 0):
+        freqs = [] if rope_freqs is None else [float(f) for f in rope_freqs]
+        arr = (ctypes.c_double * max(len(freqs), 1))(*freqs)
+        self.cfg = AttnConfig(n_heads, n_kv_heads, head_dim, 2 * len(freqs), int(interleaved), max_sms, device,
+                              ctypes.addressof(arr) if freqs else None)
+        self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
+        self.rope_dim = 2 * len(freqs)
+        self.device = torch.device("cuda", device)
+        self._scale = 1.0 / math.sqrt(head_dim) if head_dim > 0 else 0.0
+        h = ctypes.c_void_p()
+        check(lib().moe_attn_init(ctypes.byref(h), ctypes.byref(self.cfg)), "moe_attn_init")
+        self.cfg.rope_freqs = None  # read during the call only
+        self._h = h
+
+    def close(self) -> None:
+        if getattr(self, "_h", None) is not None and self._h.value:
+            lib().moe_attn_free(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def handle(self):
+        return self._h
+
+    def status(self) -> int:
+        return lib().moe_attn_status(self._h)
+
+    # -- argument checks -------------------------------------------------
+
+    def _rows(self, t: torch.Tensor, T: int, heads: int, name: str) -> int:
+        """Token stride of bf16 head rows [T, heads, head_dim]."""
+        d = self.head_dim
+        if t.dtype is not _BF16 or t.shape != (T, heads, d) or t.device != self.device:
+            raise ValueError(f"{name} must be bf16 [{T}, {heads}, {d}] on {self.device}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        s0, s1, s2 = t.stride()
+        if s2 != 1 or (s1 != d and heads > 1):
+            raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
+        return s0 if T > 1 else heads * d
+
+    def _vec(self, t: torch.Tensor | None, dtype: torch.dtype, n: int, name: str) -> int | None:
+        if t is None:
+            return None
+        if t.dtype is not dtype or t.shape != (n,) or t.device != self.device or (n > 1 and t.stride(0) != 1):
+            raise ValueError(f"{name} must be contiguous {dtype} [{n}] on {self.device}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
+
+    def _cache(self, cache: PagedKVCache) -> int:
+        if cache.n_kv_heads != self.n_kv_heads or cache.head_dim != self.head_dim or cache.device != self.device:
+            raise ValueError(f"the cache holds {cache.n_kv_heads} heads of {cache.head_dim} on {cache.device}; "
+                             f"the context has {self.n_kv_heads} of {self.head_dim} on {self.device}")
+        return cache._ref
+
+    # -- operators -------------------------------------------------------
+
+    def norm_rope(self, q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor | None,
+                  q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                  eps: float = 1e-6, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                  stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+        """RMS norm (where a weight f32 [d] is given) and rotation of q bf16
+        [T, n_heads, d] and k bf16 [T, n_kv_heads, d]; positions int32 [T].
+        q_out / k_out may be q / k."""
+        T, d = q.shape[0], self.head_dim
+        qs, ks = self._rows(q, T, self.n_heads, "q"), self._rows(k, T, self.n_kv_heads, "k")
+        if positions is None and self.rope_dim:
+            raise ValueError("positions are needed to rotate")
+        if q_out is None:
+            q_out = torch.empty((T, self.n_heads, d), dtype=_BF16, device=self.device)
+        if k_out is None:
+            k_out = torch.empty((T, self.n_kv_heads, d), dtype=_BF16, device=self.device)
+        qos, kos = self._rows(q_out, T, self.n_heads, "q_out"), self._rows(k_out, T, self.n_kv_heads, "k_out")
+        rc = lib().moe_attn_norm_rope(self._h, q.data_ptr(), qs, k.data_ptr(), ks,
+                                      self._vec(positions, torch.int32, T, "positions"), T,
+                                      self._vec(q_weight, torch.float32, d, "q_weight"),
+                                      self._vec(k_weight, torch.float32, d, "k_weight"), eps,
+                                      q_out.data_ptr(), qos, k_out.data_ptr(), kos, _stream_handle(stream))
+        check(rc, "moe_attn_norm_rope")
+        return q_out, k_out
+
+    def append(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
+               slots: torch.Tensor, cache: PagedKVCache, q_weight: torch.Tensor | None = None,
+               k_weight: torch.Tensor | None = None, eps: float = 1e-6, q_out: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+        """norm_rope whose keys, and the values as they are, go into the
+        cache's slots (int64 [T]: page * page_size + slot, negative to store
+        nothing).  Returns the queries."""
+        T, d = q.shape[0], self.head_dim
+        qs, ks = self._rows(q, T, self.n_heads, "q"), self._rows(k, T, self.n_kv_heads, "k")
+        vs = self._rows(v, T, self.n_kv_heads, "v")
+        if positions is None and self.rope_dim:
+            raise ValueError("positions are needed to rotate")
+        if q_out is None:
+            q_out = torch.empty((T, self.n_heads, d), dtype=_BF16, device=self.device)
+        qos = self._rows(q_out, T, self.n_heads, "q_out")
+        rc = lib().moe_attn_append(self._h, self._cache(cache), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                                   self._vec(positions, torch.int32, T, "positions"),
+                                   self._vec(slots, torch.int64, T, "slots"), T,
+                                   self._vec(q_weight, torch.float32, d, "q_weight"),
+                                   self._vec(k_weight, torch.float32, d, "k_weight"), eps,
+                                   q_out.data_ptr(), qos, _stream_handle(stream))
+        check(rc, "moe_attn_append")
+        return q_out
+
+    def write(self, cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+        """k and v bf16 [T, n_kv_heads, d] into the cache's slots, quantised
+        if it is e4m3."""
+        T = k.shape[0]
+        ks, vs = self._rows(k, T, self.n_kv_heads, "k"), self._rows(v, T, self.n_kv_heads, "v")
+        rc = lib().moe_attn_write(self._h, self._cache(cache), k.data_ptr(), ks, v.data_ptr(), vs,
+                                  self._vec(slots, torch.int64, T, "slots"), T, _stream_handle(stream))
+        check(rc, "moe_attn_write")
+
+    def read(self, cache: PagedKVCache, slots: torch.Tensor, k_out: torch.Tensor | None = None,
+             v_out: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+        """The rows of the slots as bf16 [T, n_kv_heads, d] (zeros for a
+        negative slot)."""
+        T = slots.shape[0]
+        shape = (T, self.n_kv_heads, self.head_dim)
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=_BF16, device=self.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=_BF16, device=self.device)
+        ks, vs = self._rows(k_out, T, self.n_kv_heads, "k_out"), self._rows(v_out, T, self.n_kv_heads, "v_out")
+        rc = lib().moe_attn_read(self._h, self._cache(cache), self._vec(slots, torch.int64, T, "slots"), T,
+                                 k_out.data_ptr(), ks, v_out.data_ptr(), vs, _stream_handle(stream))
+        check(rc, "moe_attn_read")
+        return k_out, v_out
+
+    def decode(self, q: torch.Tensor, cache: PagedKVCache, page_table: torch.Tensor, seq_lens: torch.Tensor,
+               scale: float | None = None, softcap: float = 0.0, slopes: torch.Tensor | None = None,
+               window: int = 0, starts: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               lse: torch.Tensor | None = None, stream=None):
+        """Attention of one new token per sequence: q bf16 [B, n_heads, d],
+        page_table int32 [B, max_pages], seq_lens int32 [B] (the new token
+        counted).  ``scale`` is 1/sqrt(d) by default; softcap > 0 caps the
+        scores by a tanh, ``slopes`` f32 [n_heads] adds slope * (j - newest
+        position), ``window`` > 0 and ``starts`` int32 [B] hide earlier
+        positions.  Returns out bf16 [B, n_heads, d], or (out, lse) if ``lse``
+        f32 [B, n_heads] is given."""
+        B = q.shape[0]
+        qs = self._rows(q, B, self.n_heads, "q")
+        dev = self.device
+        if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
+                page_table.device != dev or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError(f"page_table must be int32 [{B}, max_pages] on {dev} with contiguous rows")
+        if out is None:
+            out = torch.empty((B, self.n_heads, self.head_dim), dtype=_BF16, device=dev)
+        elif self._rows(out, B, self.n_heads, "out") != self.n_heads * self.head_dim:
+            raise ValueError("out must be contiguous")
+        if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (B, self.n_heads) or
+                                lse.device != dev or not lse.is_contiguous()):
+            raise ValueError(f"lse must be contiguous f32 [{B}, {self.n_heads}] on {dev}")
+        if seq_lens is None:
+            raise ValueError("seq_lens are needed")
+        rc = lib().moe_attn_decode(self._h, self._cache(cache), q.data_ptr(), qs, page_table.data_ptr(),
+                                   page_table.stride(0), page_table.shape[1],
+                                   self._vec(seq_lens, torch.int32, B, "seq_lens"),
+                                   self._vec(starts, torch.int32, B, "starts"), B,
+                                   self._scale if scale is None else scale, softcap,
+                                   self._vec(slopes, torch.float32, self.n_heads, "slopes"), window, out.data_ptr(),
+                                   None if lse is None else lse.data_ptr(), _stream_handle(stream))
+        check(rc, "moe_attn_decode")
+        return out if lse is None else (out, lse)

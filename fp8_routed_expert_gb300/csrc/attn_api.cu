@@ -1,0 +1,362 @@
+// C ABI of the attention over a paged key/value cache: context, argument
+// checks and launches.  See include/fp8moe.h for the contract.
+#include <cmath>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "common.cuh"
+#include "fp8moe.h"
+#include "paged_attn.h"
+
+using namespace fp8moe;
+
+struct moe_attn {
+  moe_attn_config cfg{};
+  int sms = 0;
+  char *ws = nullptr;         // one allocation: turns, error flag
+  uint64_t *turns = nullptr;  // [rope_dim / 2]
+  int *err = nullptr;
+  cudaStream_t last_stream = nullptr;
+};
+
+namespace {
+
+#define ATTN_TRY(x)                              \
+  do {                                           \
+    if ((x) != cudaSuccess) return MOE_ERR_CUDA; \
+  } while (0)
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+constexpr int64_t kMaxBatch = 1 << 20;
+constexpr int64_t kMaxPositions = 0x7fffffff - 63;
+constexpr int64_t kMaxTokens = 0x7fffffff;
+
+int check_config(const moe_attn_config &c) {
+  if (c.n_kv_heads < 1 || c.n_heads < c.n_kv_heads || c.n_heads > 1024 ||
+      c.n_heads % c.n_kv_heads != 0)
+    return MOE_ERR_SHAPE;
+  if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return MOE_ERR_SHAPE;
+  if (c.rope_dim < 0 || c.rope_dim > c.head_dim || c.rope_dim % 16 != 0) return MOE_ERR_SHAPE;
+  if (c.max_sms < 0 || c.device < 0) return MOE_ERR_SHAPE;
+  if (c.interleaved != 0 && c.interleaved != 1) return MOE_ERR_ARG;
+  if (c.rope_dim > 0 && c.rope_freqs == nullptr) return MOE_ERR_ARG;
+  for (int i = 0; i < c.rope_dim / 2; ++i)
+    if (!std::isfinite(c.rope_freqs[i])) return MOE_ERR_ARG;
+  return MOE_OK;
+}
+
+// freq / (2 pi) modulo 1 in units of 2^-64 turns.  1 / (2 pi) is held as the
+// sum of two doubles, and the product's rounding error is recovered with an
+// fma, so the result is within a unit or two for |freq| <= 1.
+uint64_t turns_of(double freq) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+  const double p = freq * kHi;
+  const double e = std::fma(freq, kHi, -p) + freq * kLo;
+  const double f = p - std::floor(p);  // exact, in [0, 1)
+  // the fraction's high and low 32 bits, then the (signed) remainder
+  const double hi = std::floor(std::ldexp(f, 32));
+  const double lo = std::ldexp(std::ldexp(f, 32) - hi, 32);
+  const double r = std::ldexp(std::remainder(e, 1.0), 32);  // in [-2^31, 2^31]
+  const double rhi = std::floor(r), rlo = std::ldexp(r - rhi, 32);
+  return ((uint64_t)hi << 32) + (uint64_t)std::nearbyint(lo) + ((uint64_t)(int64_t)rhi << 32) +
+         (uint64_t)std::nearbyint(rlo);
+}
+
+// The caller's cache, checked against the context, as the kernels take it.
+int view_of(const moe_attn *a, const moe_paged_kv *kv, KvView *v) {
+  if (kv == nullptr) return MOE_ERR_ARG;
+  if (kv->format != MOE_KV_BF16 && kv->format != MOE_KV_E4M3) return MOE_ERR_ARG;
+  const bool q = kv->format == MOE_KV_E4M3;
+  if (kv->n_pages < 1 || kv->n_pages > 0x7fffffff || kv->page_size < 1) return MOE_ERR_SHAPE;
+  if (kv->k == nullptr || kv->v == nullptr) return MOE_ERR_ARG;
+  if (q && (kv->k_scale == nullptr || kv->v_scale == nullptr)) return MOE_ERR_ARG;
+  const int es = q ? 1 : 2;
+  // bounds that keep every offset within 63 bits
+  const int64_t most = INT64_C(1) << 40;
+  for (int64_t st : {kv->page_stride, kv->head_stride, kv->slot_stride}) {
+    if (st < 0 || st > most) return MOE_ERR_SHAPE;
+    if ((st * es) % 16 != 0) return MOE_ERR_ALIGN;
+  }
+  if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return MOE_ERR_ALIGN;
+  if (q) {
+    for (int64_t st : {kv->scale_page_stride, kv->scale_head_stride, kv->scale_slot_stride})
+      if (st < 0 || st > most) return MOE_ERR_SHAPE;
+    if (!aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4)) return MOE_ERR_ALIGN;
+  }
+  *v = KvView{static_cast<uint8_t *>(kv->k),
+              static_cast<uint8_t *>(kv->v),
+              q ? kv->k_scale : nullptr,
+              q ? kv->v_scale : nullptr,
+              kv->n_pages,
+              kv->page_stride * es,
+              kv->head_stride * es,
+              kv->slot_stride * es,
+              q ? kv->scale_page_stride : 0,
+              q ? kv->scale_head_stride : 0,
+              q ? kv->scale_slot_stride : 0,
+              kv->page_size};
+  (void)a;
+  return MOE_OK;
+}
+
+// Head rows of T tokens: `heads` rows of d elements within each stride.
+int check_rows(const void *p, int64_t stride, int heads, int d) {
+  if (p == nullptr) return MOE_ERR_ARG;
+  if (stride < (int64_t)heads * d || stride > (INT64_C(1) << 31)) return MOE_ERR_SHAPE;
+  if (!aligned(p, 16) || stride % 8 != 0) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+int check_norm(const moe_attn *a, const int32_t *positions, const float *wq, const float *wk,
+               float eps) {
+  if (a->cfg.rope_dim > 0 && positions == nullptr) return MOE_ERR_ARG;
+  if (!std::isfinite(eps) || eps < 0.f) return MOE_ERR_ARG;
+  if (!aligned(positions, 4) || !aligned(wq, 16) || !aligned(wk, 16)) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+int check_T(const moe_attn *a, int64_t T) {
+  if (a == nullptr || T < 0) return MOE_ERR_ARG;
+  return T > kMaxTokens ? MOE_ERR_SHAPE : MOE_OK;
+}
+
+#define CHECK(x)                  \
+  do {                            \
+    const int rc_ = (x);          \
+    if (rc_ != MOE_OK) return rc_; \
+  } while (0)
+
+int run_rows(moe_attn *a, const RowArgs &r, cudaStream_t s) {
+  ATTN_TRY(cudaSetDevice(a->cfg.device));
+  a->last_stream = s;
+  ATTN_TRY(launch_rows(r, a->cfg.head_dim, s));
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_attn_init(moe_attn **out, const moe_attn_config *cfg) {
+  if (out == nullptr) return MOE_ERR_ARG;
+  *out = nullptr;
+  if (cfg == nullptr) return MOE_ERR_ARG;
+  CHECK(check_config(*cfg));
+  int count = 0;
+  if (cudaGetDeviceCount(&count) != cudaSuccess || cfg->device >= count) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  if (cudaSetDevice(cfg->device) != cudaSuccess) return MOE_ERR_CUDA;
+  int major = 0, minor = 0, sms = 0;
+  ATTN_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, cfg->device));
+  ATTN_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, cfg->device));
+  ATTN_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, cfg->device));
+  if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
+  moe_attn *a = new (std::nothrow) moe_attn();
+  if (a == nullptr) return MOE_ERR_NOMEM;
+  a->cfg = *cfg;
+  a->cfg.rope_freqs = nullptr;  // the caller's array is not kept
+  a->sms = cfg->max_sms > 0 && cfg->max_sms < sms ? cfg->max_sms : sms;
+  const int half = cfg->rope_dim / 2;
+  uint64_t turns[128];
+  for (int i = 0; i < half; ++i) turns[i] = turns_of(cfg->rope_freqs[i]);
+  const size_t bytes = 256 + sizeof(turns);
+  if (cudaMalloc(&a->ws, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    delete a;
+    return MOE_ERR_NOMEM;
+  }
+  a->err = reinterpret_cast<int *>(a->ws);
+  a->turns = reinterpret_cast<uint64_t *>(a->ws + 256);
+  if (cudaMemset(a->ws, 0, bytes) != cudaSuccess ||
+      cudaMemcpy(a->turns, turns, (size_t)half * sizeof(uint64_t), cudaMemcpyHostToDevice) !=
+          cudaSuccess ||
+      cudaDeviceSynchronize() != cudaSuccess) {  // ready for any stream
+    moe_attn_free(a);
+    return MOE_ERR_CUDA;
+  }
+  *out = a;
+  return MOE_OK;
+}
+
+void moe_attn_free(moe_attn *a) {
+  if (a == nullptr) return;
+  cudaSetDevice(a->cfg.device);
+  if (a->ws) cudaFree(a->ws);
+  delete a;
+}
+
+int moe_attn_status(moe_attn *a) {
+  if (a == nullptr) return MOE_ERR_ARG;
+  ATTN_TRY(cudaSetDevice(a->cfg.device));
+  ATTN_TRY(cudaStreamSynchronize(a->last_stream));
+  int flag = 0;
+  ATTN_TRY(cudaMemcpy(&flag, a->err, sizeof(int), cudaMemcpyDeviceToHost));
+  ATTN_TRY(cudaMemset(a->err, 0, sizeof(int)));
+  return flag ? MOE_ERR_DEVICE : MOE_OK;
+}
+
+int moe_attn_norm_rope(moe_attn *a, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                       const int32_t *positions, int64_t T, const float *q_weight,
+                       const float *k_weight, float eps, void *q_out, int64_t q_out_stride,
+                       void *k_out, int64_t k_out_stride, void *stream) {
+  CHECK(check_T(a, T));
+  if (T == 0) return MOE_OK;
+  const moe_attn_config &c = a->cfg;
+  CHECK(check_rows(q, q_stride, c.n_heads, c.head_dim));
+  CHECK(check_rows(k, k_stride, c.n_kv_heads, c.head_dim));
+  CHECK(check_rows(q_out, q_out_stride, c.n_heads, c.head_dim));
+  CHECK(check_rows(k_out, k_out_stride, c.n_kv_heads, c.head_dim));
+  CHECK(check_norm(a, positions, q_weight, k_weight, eps));
+  RowArgs r{};
+  r.q = {static_cast<const __nv_bfloat16 *>(q), q_stride};
+  r.k = {static_cast<const __nv_bfloat16 *>(k), k_stride};
+  r.q_out = {static_cast<__nv_bfloat16 *>(q_out), q_out_stride};
+  r.k_out = {static_cast<__nv_bfloat16 *>(k_out), k_out_stride};
+  r.n_q = c.n_heads;
+  r.n_k = c.n_kv_heads;
+  r.T = T;
+  r.positions = positions;
+  r.q_weight = q_weight;
+  r.k_weight = k_weight;
+  r.turns = a->turns;
+  r.half = c.rope_dim / 2;
+  r.interleaved = c.interleaved;
+  r.eps = eps;
+  r.err = a->err;
+  return run_rows(a, r, static_cast<cudaStream_t>(stream));
+}
+
+int moe_attn_append(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t q_stride,
+                    const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                    const int32_t *positions, const int64_t *slots, int64_t T,
+                    const float *q_weight, const float *k_weight, float eps, void *q_out,
+                    int64_t q_out_stride, void *stream) {
+  CHECK(check_T(a, T));
+  RowArgs r{};
+  CHECK(view_of(a, kv, &r.kv));
+  if (T == 0) return MOE_OK;
+  const moe_attn_config &c = a->cfg;
+  CHECK(check_rows(q, q_stride, c.n_heads, c.head_dim));
+  CHECK(check_rows(k, k_stride, c.n_kv_heads, c.head_dim));
+  CHECK(check_rows(v, v_stride, c.n_kv_heads, c.head_dim));
+  CHECK(check_rows(q_out, q_out_stride, c.n_heads, c.head_dim));
+  CHECK(check_norm(a, positions, q_weight, k_weight, eps));
+  if (slots == nullptr) return MOE_ERR_ARG;
+  if (!aligned(slots, 8)) return MOE_ERR_ALIGN;
+  r.q = {static_cast<const __nv_bfloat16 *>(q), q_stride};
+  r.k = {static_cast<const __nv_bfloat16 *>(k), k_stride};
+  r.v = {static_cast<const __nv_bfloat16 *>(v), v_stride};
+  r.q_out = {static_cast<__nv_bfloat16 *>(q_out), q_out_stride};
+  r.n_q = c.n_heads;
+  r.n_k = r.n_v = c.n_kv_heads;
+  r.T = T;
+  r.positions = positions;
+  r.slots = slots;
+  r.q_weight = q_weight;
+  r.k_weight = k_weight;
+  r.turns = a->turns;
+  r.half = c.rope_dim / 2;
+  r.interleaved = c.interleaved;
+  r.eps = eps;
+  r.cache = true;
+  r.e4m3 = kv->format == MOE_KV_E4M3;
+  r.err = a->err;
+  return run_rows(a, r, static_cast<cudaStream_t>(stream));
+}
+
+int moe_attn_write(moe_attn *a, const moe_paged_kv *kv, const void *k, int64_t k_stride,
+                   const void *v, int64_t v_stride, const int64_t *slots, int64_t T, void *stream) {
+  CHECK(check_T(a, T));
+  RowArgs r{};
+  CHECK(view_of(a, kv, &r.kv));
+  if (T == 0) return MOE_OK;
+  const moe_attn_config &c = a->cfg;
+  CHECK(check_rows(k, k_stride, c.n_kv_heads, c.head_dim));
+  CHECK(check_rows(v, v_stride, c.n_kv_heads, c.head_dim));
+  if (slots == nullptr) return MOE_ERR_ARG;
+  if (!aligned(slots, 8)) return MOE_ERR_ALIGN;
+  r.k = {static_cast<const __nv_bfloat16 *>(k), k_stride};
+  r.v = {static_cast<const __nv_bfloat16 *>(v), v_stride};
+  r.n_k = r.n_v = c.n_kv_heads;
+  r.T = T;
+  r.slots = slots;
+  r.cache = true;
+  r.e4m3 = kv->format == MOE_KV_E4M3;
+  r.err = a->err;
+  return run_rows(a, r, static_cast<cudaStream_t>(stream));
+}
+
+int moe_attn_read(moe_attn *a, const moe_paged_kv *kv, const int64_t *slots, int64_t T, void *k_out,
+                  int64_t k_out_stride, void *v_out, int64_t v_out_stride, void *stream) {
+  CHECK(check_T(a, T));
+  ReadArgs r{};
+  CHECK(view_of(a, kv, &r.kv));
+  if (T == 0) return MOE_OK;
+  const moe_attn_config &c = a->cfg;
+  CHECK(check_rows(k_out, k_out_stride, c.n_kv_heads, c.head_dim));
+  CHECK(check_rows(v_out, v_out_stride, c.n_kv_heads, c.head_dim));
+  if (slots == nullptr) return MOE_ERR_ARG;
+  if (!aligned(slots, 8)) return MOE_ERR_ALIGN;
+  r.e4m3 = kv->format == MOE_KV_E4M3;
+  r.slots = slots;
+  r.T = T;
+  r.n_kv = c.n_kv_heads;
+  r.k_out = {static_cast<__nv_bfloat16 *>(k_out), k_out_stride};
+  r.v_out = {static_cast<__nv_bfloat16 *>(v_out), v_out_stride};
+  r.err = a->err;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ATTN_TRY(cudaSetDevice(c.device));
+  a->last_stream = s;
+  ATTN_TRY(launch_read(r, c.head_dim, s));
+  return MOE_OK;
+}
+
+int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t q_stride,
+                    const int32_t *page_table, int64_t table_stride, int64_t max_pages,
+                    const int32_t *seq_lens, const int32_t *starts, int64_t B, float scale,
+                    float softcap, const float *slopes, int32_t window, void *out, float *lse,
+                    void *stream) {
+  if (a == nullptr || B < 0) return MOE_ERR_ARG;
+  if (B > kMaxBatch) return MOE_ERR_SHAPE;
+  DecodeArgs r{};
+  CHECK(view_of(a, kv, &r.kv));
+  if (max_pages < 1 || table_stride < 0 || max_pages > kMaxPositions / kv->page_size)
+    return MOE_ERR_SHAPE;
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0)
+    return MOE_ERR_ARG;
+  if (B == 0) return MOE_OK;
+  const moe_attn_config &c = a->cfg;
+  CHECK(check_rows(q, q_stride, c.n_heads, c.head_dim));
+  if (!page_table || !seq_lens || !out) return MOE_ERR_ARG;
+  if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(starts, 4) ||
+      !aligned(slopes, 4) || !aligned(out, 16) || !aligned(lse, 4))
+    return MOE_ERR_ALIGN;
+  r.q = static_cast<const __nv_bfloat16 *>(q);
+  r.q_stride = q_stride;
+  r.table = page_table;
+  r.table_stride = table_stride;
+  r.capacity = max_pages * kv->page_size;
+  r.lens = seq_lens;
+  r.starts = starts;
+  r.B = (int)B;
+  r.n_heads = c.n_heads;
+  r.n_kv = c.n_kv_heads;
+  r.scale = scale;
+  r.softcap = softcap;
+  r.slopes = slopes;
+  r.window = window;
+  r.out = static_cast<__nv_bfloat16 *>(out);
+  r.lse = lse;
+  r.err = a->err;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ATTN_TRY(cudaSetDevice(c.device));
+  a->last_stream = s;
+  ATTN_TRY(launch_paged_decode(r, c.head_dim, kv->format == MOE_KV_E4M3, s));
+  return MOE_OK;
+}
+
+}  // extern "C"

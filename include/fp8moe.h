@@ -333,6 +333,161 @@ int moe_decode_attention(const void *q, const void *k_cache, const void *v_cache
                          void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
+ * Attention over a paged key/value cache: the serving form of the attention
+ * beside the MoE (dragon.c, "Shortcut-connected MoE").  Many sequences of
+ * different lengths share one cache of fixed-size pages; a decode step norms
+ * and rotates the new token's query and key heads, puts its key and value
+ * rows into the cache (bf16, or quantised to e4m3) and attends to the
+ * sequence's pages.  No counterpart in the pages beyond the role.
+ *
+ * The cache is the caller's memory, described by moe_paged_kv.  The row of
+ * page p, key/value head c and slot s starts at element
+ *   p * page_stride + c * head_stride + s * slot_stride
+ * of k and of v (head_dim elements, contiguous), its scale at element
+ *   p * scale_page_stride + c * scale_head_stride + s * scale_slot_stride
+ * of k_scale and of v_scale.  Any order of the three is allowed, and a slice
+ * of a larger allocation too.
+ *   MOE_KV_BF16 : rows of bf16; the scales are not used (may be NULL).
+ *   MOE_KV_E4M3 : rows of e4m3 codes, value = code * the row's f32 scale
+ *                 (scales are >= 0).
+ * Alignment: k and v 16 bytes, and the three row strides multiples of 16
+ * bytes; scales 4 bytes.
+ */
+#define MOE_KV_BF16 0
+#define MOE_KV_E4M3 1
+typedef struct moe_paged_kv {
+  void *k, *v;                 /* device */
+  float *k_scale, *v_scale;    /* device; MOE_KV_E4M3 only */
+  int64_t n_pages;             /* >= 1 */
+  int64_t page_stride, head_stride, slot_stride;                   /* elements */
+  int64_t scale_page_stride, scale_head_stride, scale_slot_stride; /* elements */
+  int32_t page_size;           /* tokens per page, any number >= 1 */
+  int32_t format;              /* MOE_KV_* */
+} moe_paged_kv;
+
+typedef struct moe_attn moe_attn; /* opaque; owned by the library */
+
+typedef struct moe_attn_config {
+  int32_t n_heads;     /* query heads, a multiple of n_kv_heads, <= 1024     */
+  int32_t n_kv_heads;  /* key/value heads, >= 1; query head h reads key/value */
+                       /* head h / (n_heads / n_kv_heads)                    */
+  int32_t head_dim;    /* d: 64, 128 or 256                                  */
+  int32_t rope_dim;    /* R: leading elements of a head that are rotated;    */
+                       /* 0 for none, else a multiple of 16, <= head_dim     */
+  int32_t interleaved; /* rotated pairs: 0 (i, i + R/2), 1 (2i, 2i + 1)      */
+  int32_t max_sms;     /* SMs moe_attn_decode may fill; 0 for all            */
+  int32_t device;      /* CUDA device ordinal the context lives on           */
+  const double *rope_freqs; /* host, f64 [R/2]: radians per position, finite; */
+                            /* read during moe_attn_init only; NULL if R = 0  */
+} moe_attn_config;
+
+/*
+ * moe_attn_init - validate `cfg` and allocate a context: the frequencies as
+ * 64-bit fractions of a turn and moe_attn_decode's workspace, whose size does
+ * not depend on the batch or the lengths.
+ * Errors: MOE_ERR_ARG (NULL, a frequency that is not finite), MOE_ERR_SHAPE
+ * (both before any CUDA call), MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA,
+ * MOE_ERR_NOMEM.  On error *out is set to NULL and nothing is leaked.
+ */
+int moe_attn_init(moe_attn **out, const moe_attn_config *cfg);
+
+/* moe_attn_free - release the context; NULL is a no-op. */
+void moe_attn_free(moe_attn *a);
+
+/*
+ * moe_attn_status - synchronise the context's last stream and return MOE_OK,
+ * or MOE_ERR_DEVICE if a call since the previous moe_attn_status met a slot,
+ * page or length outside the cache or the page table (the flag is cleared).
+ * Such a slot is neither written nor read, rows of such a page count as
+ * zeros, and such a length is cut to the page table.
+ */
+int moe_attn_status(moe_attn *a);
+
+/*
+ * moe_attn_norm_rope - norm and rotate the query and key heads of T tokens.
+ * Per head row x of d elements, in f32:
+ *   y = x / sqrt(mean(x^2) + eps) * weight        (skipped if weight is NULL)
+ *   rotate pair i < R/2 of y by the angle position * rope_freqs[i]
+ * and one rounding to bf16.  Angles are exact to 2^-33 of a turn at every
+ * int32 position.
+ *   q, k       : device bf16; row h of token t at t * q_stride + h * d (elements),
+ *                strides multiples of 8, pointers 16-byte aligned.  Slices of
+ *                a fused projection's rows are fine.
+ *   positions  : device int32 [T]; may be NULL if R = 0.
+ *   q_weight, k_weight : device f32 [d], 16-byte aligned, or NULL.
+ *   eps        : >= 0 and finite.
+ *   q_out, k_out : like q and k; may be q and k themselves (same stride),
+ *                must not overlap them otherwise.
+ */
+int moe_attn_norm_rope(moe_attn *a, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                       const int32_t *positions, int64_t T, const float *q_weight,
+                       const float *k_weight, float eps, void *q_out, int64_t q_out_stride,
+                       void *k_out, int64_t k_out_stride, void *stream);
+
+/*
+ * moe_attn_append - moe_attn_norm_rope whose key rows, and the value rows as
+ * they are, go into the cache.
+ *   v     : device bf16 [T, n_kv_heads, d] rows like k.
+ *   slots : device int64 [T]: page * page_size + slot of each token's place,
+ *           negative to store nothing for that token.  Two tokens of a call
+ *           must not share a slot.
+ * Storing a row as e4m3: e is the smallest integer >= -126 with max|v| <=
+ * 448 * 2^e over the row's finite values (0 if they are all zero), scale =
+ * 2^e, code = e4m3(v / 2^e) rounded to nearest even; a NaN or an infinity
+ * becomes the NaN code.  The f32 value is rounded once, to the cache's type.
+ */
+int moe_attn_append(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t q_stride,
+                    const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                    const int32_t *positions, const int64_t *slots, int64_t T,
+                    const float *q_weight, const float *k_weight, float eps, void *q_out,
+                    int64_t q_out_stride, void *stream);
+
+/*
+ * moe_attn_write - put key and value rows into the cache as they are
+ * (arguments and storing as for moe_attn_append).
+ */
+int moe_attn_write(moe_attn *a, const moe_paged_kv *kv, const void *k, int64_t k_stride,
+                   const void *v, int64_t v_stride, const int64_t *slots, int64_t T, void *stream);
+
+/*
+ * moe_attn_read - read key and value rows back from the cache as bf16 rows
+ * [T, n_kv_heads, d] (strides as for k); a negative slot gives a row of zeros.
+ */
+int moe_attn_read(moe_attn *a, const moe_paged_kv *kv, const int64_t *slots, int64_t T, void *k_out,
+                  int64_t k_out_stride, void *v_out, int64_t v_out_stride, void *stream);
+
+/*
+ * moe_attn_decode - attention of one new token per sequence over its pages.
+ * With p = seq_lens[b] - 1 the new token's position and c = h / (n_heads /
+ * n_kv_heads):
+ *   s_j = scale * q[b, h] . K[b, j, c]
+ *   s_j = softcap * tanh(s_j / softcap)              if softcap > 0
+ *   s_j = s_j + slopes[h] * (j - p)                  if slopes is given
+ * for the visible positions: j <= p, j >= starts[b] if given, and j > p -
+ * window if window > 0;
+ *   out[b, h] = softmax(s) V,  lse[b, h] = log(sum_j exp(s_j)).
+ * Position j is slot j % page_size of page page_table[b, j / page_size].
+ * A sequence with no visible position gives out = 0 and lse = -infinity.
+ * Sums and softmax statistics are f32; out is rounded once.
+ *   q          : device bf16 [B, n_heads, d], token stride q_stride (elements,
+ *                a multiple of 8), 16-byte aligned.
+ *   page_table : device int32 [B, max_pages], row stride table_stride.
+ *   seq_lens   : device int32 [B], at most max_pages * page_size (which is at
+ *                most 2^31 - 64) tokens each, counting the new token.
+ *   starts     : device int32 [B] or NULL.
+ *   slopes     : device f32 [n_heads] or NULL.
+ *   out        : device bf16 [B, n_heads, d] contiguous, 16-byte aligned.
+ *   lse        : device f32 [B, n_heads] or NULL.
+ * B <= 2^20.  B = 0 is a no-op.  The calls on one context share its
+ * workspace: they must not overlap on the GPU.
+ */
+int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t q_stride,
+                    const int32_t *page_table, int64_t table_stride, int64_t max_pages,
+                    const int32_t *seq_lens, const int32_t *starts, int64_t B, float scale,
+                    float softcap, const float *slopes, int32_t window, void *out, float *lse,
+                    void *stream);
+
+/*
  * moe_selftest_wait_timeout - exercise the bounded device-side waits.  Every
  * wait inside the layer's kernels (mbarriers of TMA copies and tensor-core
  * work, cross-CTA counters) gives up after a time limit and records

@@ -1,0 +1,565 @@
+"""Paged-cache attention on the GPU against the f64 oracle: norm and rotation,
+cache write and read-back, decode attention.
+
+Tolerances, from the arithmetic (u = 2^-24, half a step of f32):
+  * bf16 outputs: half a bf16 step, 2^-8 |exact| (subnormals aside, which the
+    data avoids), plus the f32 error of the value itself;
+  * norm and rotation: y = x * r * w carries the mean's error (at most 12
+    additions deep, halved by the root) and about six more roundings, cos and
+    sin 2 u each: 24 u of |a| + |b|, the pair's sizes;
+  * e4m3 rows of bf16 input: exact (a power-of-two scale, one rounding), so
+    codes and scales are equal.  For normed keys the f32 error may move a value
+    over a rounding border, so the read-back is held to half a step, 2^-4
+    relative or 2^-10 of the scale below the normal range, plus that error;
+  * scores: a d-term f32 sum through 16-wide matrix steps, each charged 8
+    units u of the running sum of magnitudes: eps_s = (d / 2 + 16) u reach,
+    plus 16 u cap for the tanh and 2 u per unit of distance bias;
+  * out: exp and the weights' own rounding are relative errors of p (2^-20
+    and, where weights are kept in f16, half a step 2^-11), the sum over n
+    keys another (n / 2 + 64) u: all times sum_j p_j |v_j|; lse: eps_s +
+    2^-20 + 64 u + 2 u |lse|.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from fp8_routed_expert_gb300 import C, DecodeAttention, PagedKVCache, lib, rope_frequencies
+from oracle import E4M3_TABLE, bf16_to_f64
+from oracle import paged_attention as P
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DEV = torch.device("cuda", 0)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def f64(t: torch.Tensor) -> np.ndarray:
+    return t.detach().double().cpu().numpy()
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape, dtype=torch.bfloat16, spread=0.0):
+    x = torch.randn(*shape, generator=g, device=DEV)
+    if spread:
+        x = x * torch.exp(spread * torch.randn(*shape[:-1], 1, generator=g, device=DEV))
+    return x.to(dtype)
+
+
+def close(got, want, tol):
+    got = f64(got)
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), got[bad][:4], want[bad][:4], tol[bad][:4])
+
+
+# ---------------------------------------------------------- norm, rotation
+
+def _pairs(y, half, inter):
+    """Size of each element's pair: |a| + |b| (|a| alone where not rotated)."""
+    m = np.abs(y)
+    if half:
+        i = np.arange(half)
+        a, b = (2 * i, 2 * i + 1) if inter else (i, i + half)
+        s = m[..., a] + m[..., b]
+        m[..., a] = s
+        m[..., b] = s
+    return m
+
+
+def _want_rows(x, w, pos, freqs, inter, eps):
+    want = P.norm_rope(f64(x), None if w is None else f64(w), None if pos is None else pos.cpu().numpy(), freqs, inter, eps)
+    size = P.norm_rope(f64(x), None if w is None else f64(w), None, [], inter, eps)
+    return want, 24 * U * _pairs(size, len(freqs), inter)
+
+
+@pytest.mark.parametrize("T,nh,nkv,d,R,inter,norm", [
+    (1, 16, 16, 128, 128, False, True), (3, 1, 1, 64, 64, True, True), (33, 5, 5, 64, 16, False, True),
+    (7, 24, 2, 256, 256, True, True), (130, 9, 3, 256, 64, False, True), (257, 32, 8, 128, 96, False, True),
+    (5, 48, 8, 128, 0, False, True), (9, 40, 1, 128, 32, True, False), (2, 256, 16, 64, 48, False, True),
+    (1031, 6, 2, 128, 128, False, True)])
+def test_norm_rope(T, nh, nkv, d, R, inter, norm):
+    g = gen(T + nh)
+    fused = randn(g, T, nh + 2 * nkv + 1, d, spread=1.0)  # heads of one projection's rows: strided views
+    q, k = fused[:, 1:nh + 1], fused[:, nh + 1:nh + nkv + 1]
+    wq, wk = (randn(g, d, dtype=torch.float32) for _ in range(2)) if norm else (None, None)
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (T,), generator=g, device=DEV).to(torch.int32) if R else None
+    freqs = rope_frequencies(R) if R else []
+    attn = DecodeAttention(nh, nkv, d, rope_freqs=freqs or None, interleaved=inter)
+    want_q, tq = _want_rows(q, wq, pos, freqs, inter, 1e-5)
+    want_k, tk = _want_rows(k, wk, pos, freqs, inter, 1e-5)
+    # an f64 angle at 2^31 is itself off by up to 2^31 * 2^-53 radians
+    tq, tk = (t + 2.0 ** -21 * t / (24 * U) for t in (tq, tk)) if R else (tq, tk)
+    qo, ko = attn.norm_rope(q, k, pos, wq, wk, eps=1e-5)
+    close(qo, want_q, 2.0 ** -8 * np.abs(want_q) + tq)
+    close(ko, want_k, 2.0 ** -8 * np.abs(want_k) + tk)
+    assert attn.status() == 0
+    # in place, and into strided rows whose neighbours stay as they are
+    keep = fused.clone()
+    attn.norm_rope(q, k, pos, wq, wk, eps=1e-5, q_out=q, k_out=k)
+    assert torch.equal(q, qo) and torch.equal(k, ko)
+    assert torch.equal(fused[:, 0], keep[:, 0]) and torch.equal(fused[:, nh + nkv + 1:], keep[:, nh + nkv + 1:])
+
+
+def test_norm_rope_special_rows():
+    """Zeros stay zeros, large and tiny rows are normed within f32, NaN stays
+    within its row."""
+    attn = DecodeAttention(4, 2, 64)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=DEV)
+    q[0, 1] = 1e18
+    q[0, 2] = 1e-15
+    q[1, 0, 5] = float("nan")
+    k = torch.ones(2, 2, 64, dtype=torch.bfloat16, device=DEV)
+    w = torch.ones(64, device=DEV)
+    qo, ko = attn.norm_rope(q, k, None, w, w, eps=0.0)
+    assert torch.isnan(qo[0, 0]).all() and torch.isnan(qo[1, 0]).all()  # 0 / 0 without an eps
+    assert (qo[0, 1] == 1).all() and (qo[0, 2] == 1).all() and (ko == 1).all()
+    qo, _ = attn.norm_rope(q, k, None, w, w, eps=1e-6)
+    assert (qo[0, 0] == 0).all() and (qo[1, 1:] == 0).all()
+
+
+# ------------------------------------------------------------------- cache
+
+def make_cache(n_pages, page, nkv, d, fmt, layout="head", fill=None):
+    """A cache whose tensors are views of a larger block: pages outermost and
+    heads or slots next, or one layer of two interleaved per slot."""
+    dt = torch.bfloat16 if fmt == "bf16" else torch.uint8
+
+    def block(last, dtype):
+        if layout == "head":
+            t = torch.empty(n_pages, nkv, page, *last, dtype=dtype, device=DEV)
+        elif layout == "slot":
+            t = torch.empty(n_pages, page, nkv, *last, dtype=dtype, device=DEV).transpose(1, 2)
+        else:
+            t = torch.empty(n_pages, page, 2, nkv, *last, dtype=dtype, device=DEV)[:, :, 1].transpose(1, 2)
+        return t
+
+    kv = [block((d,), dt) for _ in range(2)]
+    sc = [block((), torch.float32) for _ in range(2)] if fmt == "e4m3" else []
+    if fill is not None:
+        for t in kv:
+            t.fill_(fill if fmt == "bf16" else 0x7F)
+        for t in sc:
+            t.fill_(fill)
+    return PagedKVCache(*kv, *sc)
+
+
+def cache_values(cache, which):
+    """f64 [n_pages, n_kv, page, d] that the cache stands for."""
+    t, s = (cache.k, cache.k_scale) if which == 0 else (cache.v, cache.v_scale)
+    if cache.format == "bf16":
+        return f64(t)
+    table = np.asarray(E4M3_TABLE, dtype=np.float64)
+    return table[t.cpu().numpy()] * f64(s)[..., None]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,nkv,d,page,layout", [(1, 16, 128, 16, "head"), (37, 3, 64, 24, "slot"), (65, 1, 256, 1, "head"),
+                                                 (513, 8, 128, 100, "layer"), (2, 32, 64, 7, "slot"), (1500, 2, 128, 64, "head")])
+def test_write_and_read(T, nkv, d, page, layout, fmt):
+    g = gen(T)
+    kv = randn(g, T, 2 * nkv, d, spread=2.0)
+    k, v = kv[:, :nkv], kv[:, nkv:]
+    v[0, 0] = 0.0
+    n_pages = -(-2 * T // page) + 1
+    slots = torch.randperm(n_pages * page, generator=g, device=DEV)[:T].contiguous()
+    slots[T // 2] = -1 - T if T > 1 else slots[0]
+    cache = make_cache(n_pages, page, nkv, d, fmt, layout, fill=3.0)
+    before = cache.k.clone()
+    attn = DecodeAttention(nkv, nkv, d)
+    attn.write(cache, k, v, slots)
+    assert attn.status() == 0
+    sl = slots.cpu().numpy()
+    on = sl >= 0
+    p, r = sl[on] // page, sl[on] % page
+    for x, t, s in ((k, cache.k, cache.k_scale), (v, cache.v, cache.v_scale)):
+        if fmt == "bf16":
+            assert torch.equal(t[p, :, r], x[torch.from_numpy(on).to(DEV)])
+        else:
+            codes, scale = P.e4m3_row(f64(x)[on])
+            assert np.array_equal(t[p, :, r].cpu().numpy(), codes)
+            assert np.array_equal(f64(s[p, :, r]), scale)
+    # nothing else was touched
+    rest = np.ones((n_pages, page), bool)
+    rest[p, r] = False
+    rp, rr = np.nonzero(rest)
+    assert torch.equal(cache.k[rp, :, rr].view(torch.uint8), before[rp, :, rr].view(torch.uint8))
+    # reading back: the values, rounded once
+    for x, o in zip((k, v), attn.read(cache, slots)):
+        if fmt == "bf16":
+            want = torch.where((slots >= 0)[:, None, None], x, torch.zeros_like(x))
+        else:
+            codes, scale = P.e4m3_row(f64(x))
+            val = np.asarray(E4M3_TABLE)[codes] * scale[..., None] * on[:, None, None]
+            want = torch.from_numpy(val).to(torch.bfloat16).to(DEV)
+        assert torch.equal(o, want)
+
+
+def test_write_rows_that_are_not_finite():
+    attn = DecodeAttention(1, 1, 64)
+    cache = make_cache(2, 4, 1, 64, "e4m3", fill=1.0)
+    k = torch.full((3, 1, 64), 2.0, dtype=torch.bfloat16, device=DEV)
+    k[0, 0, 3] = float("inf")
+    k[1, 0, 60] = float("nan")
+    k[2] = float("-inf")
+    attn.write(cache, k, k, torch.tensor([1, 2, 3], device=DEV))
+    ko, vo = attn.read(cache, torch.tensor([1, 2, 3], device=DEV))
+    assert torch.equal(torch.isnan(ko), ~torch.isfinite(k)) and torch.equal(torch.isnan(vo), ~torch.isfinite(k))
+    assert (ko[torch.isfinite(k)] == 2.0).all() and (cache.k_scale[0, 0, 3] == 1.0)
+
+
+def test_slots_outside_the_cache_are_left_out_and_reported():
+    attn = DecodeAttention(2, 1, 64)
+    for fmt in ("bf16", "e4m3"):
+        cache = make_cache(2, 8, 1, 64, fmt, fill=1.0)
+        before = cache.k.clone()
+        x = randn(gen(1), 4, 1, 64)
+        bad = torch.tensor([16, 2 ** 31, 2 ** 62, -5], device=DEV)
+        attn.write(cache, x, x, bad)
+        assert attn.status() == C["MOE_ERR_DEVICE"] and attn.status() == 0
+        assert torch.equal(cache.k.view(torch.uint8), before.view(torch.uint8))
+        ko, vo = attn.read(cache, bad)
+        assert (ko == 0).all() and (vo == 0).all() and attn.status() == C["MOE_ERR_DEVICE"]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,nh,nkv,d,R,inter", [(1, 16, 16, 128, 128, False), (40, 12, 4, 64, 32, True), (257, 7, 1, 256, 128, False)])
+def test_append(T, nh, nkv, d, R, inter, fmt):
+    g = gen(T + d)
+    fused = randn(g, T, nh + 2 * nkv, d, spread=1.0)
+    q, k, v = fused[:, :nh], fused[:, nh:nh + nkv], fused[:, nh + nkv:]
+    wq, wk = 1 + 0.3 * randn(g, d, dtype=torch.float32), 1 + 0.3 * randn(g, d, dtype=torch.float32)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device=DEV).to(torch.int32)
+    freqs = rope_frequencies(R)
+    cache = make_cache(T + 2, 3, nkv, d, fmt, "slot", fill=7.0)
+    slots = torch.randperm(3 * (T + 2), generator=g, device=DEV)[:T].contiguous()
+    if T > 1:
+        slots[1] = -1
+    attn = DecodeAttention(nh, nkv, d, rope_freqs=freqs, interleaved=inter)
+    qo = attn.append(q, k, v, pos, slots, cache, wq, wk)
+    assert attn.status() == 0
+    qn, kn = attn.norm_rope(q, k, pos, wq, wk)
+    assert torch.equal(qo, qn)
+    on = (slots >= 0).cpu().numpy()
+    sl = slots.cpu().numpy()[on]
+    at = (sl // 3, slice(None), sl % 3)
+    want, tol = _want_rows(k, wk, pos, freqs, inter, 1e-6)
+    if fmt == "bf16":
+        assert torch.equal(cache.k[at], kn[torch.from_numpy(on).to(DEV)])
+        assert torch.equal(cache.v[at], v[torch.from_numpy(on).to(DEV)])
+        return
+    codes, scale = P.e4m3_row(f64(v)[on])
+    assert np.array_equal(cache.v[at].cpu().numpy(), codes) and np.array_equal(f64(cache.v_scale[at]), scale)
+    got, sc = cache_values(cache, 0)[at], f64(cache.k_scale[at])
+    want, tol = want[on], tol[on]
+    # the row's scale: the smallest power of two that holds the largest value, to its error
+    amax, slack = np.abs(want).max(-1), tol.max(-1)
+    assert (amax - slack <= 448 * sc).all() and (amax + slack > 224 * sc).all() and (np.log2(sc) % 1 == 0).all()
+    half = np.maximum(2.0 ** -4 * np.abs(want), 2.0 ** -10 * sc[..., None])
+    bad = np.abs(got - want) > half + tol * (1 + 2.0 ** -4)
+    assert not bad.any(), np.argwhere(bad)[:4]
+
+
+# ------------------------------------------------------------------ decode
+
+class Batch:
+    """Sequences over a shared cache, everything that no sequence sees set to NaN."""
+
+    def __init__(self, lens, nh, nkv, d, fmt, page, layout="head", seed=0, width=None, hidden=None):
+        self.lens, self.nh, self.nkv, self.d, self.fmt, self.page = list(lens), nh, nkv, d, fmt, page
+        g = gen(seed)
+        B = len(self.lens)
+        used = [-(-max(n, 0) // page) for n in self.lens]
+        n_pages = sum(used) + 2
+        self.width = width or max(1, max(used))
+        self.cache = make_cache(n_pages, page, nkv, d, fmt, layout, fill=float("nan"))
+        order = torch.randperm(n_pages, generator=g, device=DEV).cpu().numpy()
+        table = np.full((B, self.width + 3), 2 ** 30, np.int32)  # never read: past each length
+        self.q = randn(g, B, nh + 1, d, spread=0.5)[:, :nh]
+        self.K, self.V = [], []
+        attn = DecodeAttention(nkv, nkv, d)
+        at = 0
+        for b, n in enumerate(self.lens):
+            mine = order[at:at + used[b]]
+            at += used[b]
+            table[b, :used[b]] = mine
+            j = np.arange(n)
+            slots = mine[j // page].astype(np.int64) * page + j % page if n else np.zeros(0, np.int64)
+            k, v = (randn(g, n, nkv, d, spread=0.7) for _ in range(2))
+            if n:
+                attn.write(self.cache, k, v, torch.from_numpy(slots).to(DEV))
+            if fmt == "e4m3" and n:
+                (kc, ks), (vc, vs) = P.e4m3_row(f64(k)), P.e4m3_row(f64(v))
+                tab = np.asarray(E4M3_TABLE, np.float64)
+                self.K.append(tab[kc] * ks[..., None])
+                self.V.append(tab[vc] * vs[..., None])
+            else:
+                self.K.append(f64(k))
+                self.V.append(f64(v))
+        assert attn.status() == 0
+        self.table = torch.from_numpy(table).to(DEV)[:, :self.width]  # rows with a stride
+        self.seq_lens = torch.tensor(self.lens, dtype=torch.int32, device=DEV)
+
+    def run(self, attn=None, **kw):
+        attn = attn or DecodeAttention(self.nh, self.nkv, self.d)
+        lse = torch.full((len(self.lens), self.nh), 123.0, device=DEV)
+        out, lse = attn.decode(self.q, self.cache, self.table, self.seq_lens, lse=lse, **kw)
+        assert attn.status() == 0
+        return out, lse
+
+    def check(self, attn=None, **kw):
+        out, lse = self.run(attn, **kw)
+        host = {k: (f64(v) if isinstance(v, torch.Tensor) else v) for k, v in kw.items()}
+        want, wl, mag, reach = P.decode(f64(self.q), self.K, self.V, self.lens, **host)
+        cap, slopes = kw.get("softcap", 0.0), host.get("slopes")
+        n = max(max(self.lens), 1)
+        eps_s = (self.d / 2 + 16) * U * reach + 16 * U * cap
+        if slopes is not None:
+            eps_s = eps_s + 2 * U * np.abs(slopes) * n
+        rel = 2 * eps_s + 2.0 ** -20 + (n / 2 + 64) * U + (2.0 ** -11 if self.fmt == "e4m3" else 2.0 ** -16)
+        close(out, want, 2.0 ** -8 * np.abs(want) + rel[..., None] * mag + 1e-30)
+        got = f64(lse)
+        empty = np.isneginf(wl)
+        assert (np.isneginf(got) == empty).all()
+        err = np.abs(got[~empty] - wl[~empty])
+        tol = (eps_s + 2.0 ** -20 + 64 * U + 2 * U * np.abs(np.where(empty, 0, wl)))[~empty]
+        assert (err <= tol).all(), (err.max(), tol[err.argmax()])
+        return out, lse
+
+
+EDGES = [0, 1, 2, 15, 16, 17, 63, 64, 65, 100, 127, 128, 129, 200]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nh,nkv,d,page,layout", [
+    (16, 16, 128, 16, "head"), (8, 8, 64, 1, "head"), (4, 2, 256, 24, "slot"), (15, 3, 128, 64, "layer"),
+    (32, 4, 64, 7, "slot"), (12, 1, 128, 100, "head"), (16, 1, 256, 8, "head"), (48, 2, 64, 32, "slot"),
+    (17, 1, 128, 16, "layer"), (9, 1, 256, 256, "head")])
+def test_decode_edges(nh, nkv, d, page, layout, fmt):
+    """Lengths around every tile and page border, every head grouping, masks
+    that leave rows empty, and NaN wherever no sequence looks."""
+    b = Batch(EDGES, nh, nkv, d, fmt, page, layout, seed=nh + d)
+    attn = DecodeAttention(nh, nkv, d)
+    b.check(attn)
+    starts = torch.tensor([0, 1, 0, 3, 16, 5, 62, 64, 1, 99, -7, 16, 300, 65], dtype=torch.int32, device=DEV)
+    slopes = torch.linspace(0.01, 0.5, nh, device=DEV)
+    b.check(attn, starts=starts, softcap=30.0)
+    b.check(attn, slopes=slopes, window=17)
+    b.check(attn, starts=starts, window=1, scale=0.3)
+    b.check(attn, starts=starts, window=64, slopes=slopes, softcap=5.0, scale=-0.1)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,nh,nkv,d,page", [
+    ([5000], 4, 1, 128, 16), ([4096, 3], 16, 16, 64, 64), ([777, 20000, 1, 0, 333], 8, 2, 128, 48),
+    ([2500] * 3, 10, 1, 256, 128)])
+def test_decode_split_over_the_length(lens, nh, nkv, d, page, fmt):
+    b = Batch(lens, nh, nkv, d, fmt, page, seed=len(lens))
+    attn = DecodeAttention(nh, nkv, d)
+    one = b.check(attn)
+    b.check(attn, window=1999, softcap=20.0)
+    # the same bits again, whatever ran in between, and on fewer SMs the same result to rounding
+    again = b.run(attn)
+    assert torch.equal(one[0], again[0]) and torch.equal(one[1], again[1])
+    b.check(DecodeAttention(nh, nkv, d, max_sms=7))
+
+
+def test_decode_one_very_long_sequence():
+    """One key/value head, 150001 keys: the split's deepest join."""
+    for fmt in ("bf16", "e4m3"):
+        Batch([150001], 2, 1, 64, fmt, 128, seed=5).check()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_decode_many_sequences(fmt):
+    lens = [(i * 37) % 150 for i in range(700)]
+    Batch(lens, 4, 2, 64, fmt, 16, seed=9).check()
+
+
+def test_decode_sharp_and_extreme_scores():
+    """One key far above the rest, late or early; scores beyond f32 exp; value
+    rows of very different sizes."""
+    for fmt in ("bf16", "e4m3"):
+        b = Batch([300, 300], 4, 2, 128, fmt, 16, seed=3)
+        b.check(scale=60.0)
+        b.check(scale=1e-30)
+        b = Batch([200], 2, 2, 64, fmt, 16, seed=4)
+        # the largest value row is one that no weight falls on
+        attn = DecodeAttention(2, 2, 64)
+        big = torch.full((1, 2, 64), 1.0e9, dtype=torch.bfloat16, device=DEV)
+        key = (-1e3 * torch.sign(b.q[0].float())).to(torch.bfloat16)[None]
+        slot = b.table[0, 0].long().view(1) * 16 + 3
+        attn.write(b.cache, key, big, slot)
+        b.K[0][3] = f64(key)[0] if fmt == "bf16" else cache_values(b.cache, 0)[int(b.table[0, 0]), :, 3]
+        b.V[0][3] = cache_values(b.cache, 1)[int(b.table[0, 0]), :, 3]
+        b.check()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_decode_nan_stays_in_its_sequence(fmt):
+    b = Batch([40, 80, 200], 4, 2, 64, fmt, 16, seed=8)
+    clean, _ = b.run()
+    attn = DecodeAttention(4, 2, 64)
+    x = randn(gen(2), 1, 2, 64)
+    y = x.clone()
+    y[0, 1, 7] = float("nan")
+    attn.write(b.cache, x, y, b.table[1, 2].long().view(1) * 16 + 5)  # position 37 of sequence 1
+    out, _ = b.run()
+    assert torch.equal(out[0], clean[0]) and torch.equal(out[2], clean[2])
+    assert torch.isfinite(out[1, :2]).all()
+    assert torch.isnan(out[1, 2:, 7]).all() and torch.isfinite(out[1, 2:, :7]).all()
+    # hidden by a start, it is not seen
+    seen, _ = b.run(starts=torch.tensor([0, 38, 0], dtype=torch.int32, device=DEV))
+    assert torch.isfinite(seen).all()
+    # a NaN key makes its heads NaN
+    attn.write(b.cache, y, x, b.table[1, 2].long().view(1) * 16 + 5)
+    out, lse = b.run()
+    assert torch.isnan(out[1, 2:]).all() and torch.isnan(lse[1, 2:]).all() and torch.isfinite(out[1, :2]).all()
+
+
+def test_decode_reports_pages_and_lengths_outside():
+    for fmt in ("bf16", "e4m3"):
+        b = Batch([50, 70, 33], 4, 4, 64, fmt, 16, seed=6, width=6)
+        attn = DecodeAttention(4, 4, 64)
+        clean = attn.decode(b.q, b.cache, b.table, b.seq_lens)
+        assert attn.status() == 0
+        for bad in (-1, b.cache.n_pages, 2 ** 31 - 1):
+            table = b.table.clone()
+            table[1, 2] = bad
+            out = attn.decode(b.q, b.cache, table, b.seq_lens)
+            assert attn.status() == C["MOE_ERR_DEVICE"]
+            assert torch.equal(out[0], clean[0]) and torch.equal(out[2], clean[2])
+            K, V = b.K[1].copy(), b.V[1].copy()
+            K[32:48] = V[32:48] = 0  # a page outside counts as zeros
+            want, _, mag, _ = P.decode(f64(b.q)[1:2], [K], [V], [70])
+            close(out[1:2], want, 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * mag)
+        # a length outside the table is cut to it, a negative one is empty
+        table = b.table.clone()
+        table[:, 5:] = 0
+        table[0, 4:] = 0
+        attn.decode(b.q, b.cache, table.clamp(0, b.cache.n_pages - 1), torch.tensor([50, 97, -3], dtype=torch.int32, device=DEV))
+        assert attn.status() == C["MOE_ERR_DEVICE"]
+        out = attn.decode(b.q, b.cache, b.table, torch.tensor([50, 70, -3], dtype=torch.int32, device=DEV))
+        assert attn.status() == C["MOE_ERR_DEVICE"] and (out[2] == 0).all() and torch.equal(out[:2], clean[:2])
+
+
+def test_decode_far_offsets():
+    """Rows beyond 2^32 elements into the cache."""
+    n_pages, page, d = 300, 64, 128
+    stride = 1 << 24  # elements between pages: 300 pages span 5e9
+    big = [torch.empty(n_pages * stride, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    kv = [t.as_strided((n_pages, 1, page, d), (stride, page * d, d, 1)) for t in big]
+    sc = [torch.empty(n_pages, 1, page, device=DEV) for _ in range(2)]
+    cache = PagedKVCache(*kv, *sc)
+    attn = DecodeAttention(3, 1, d)
+    g = gen(1)
+    k, v, q = randn(g, 100, 1, d), randn(g, 100, 1, d), randn(g, 1, 3, d)
+    table = torch.tensor([[299, 290]], dtype=torch.int32, device=DEV)
+    j = torch.arange(100, device=DEV)
+    slots = table[0].long()[j // page] * page + j % page
+    attn.write(cache, k, v, slots)
+    out = attn.decode(q, cache, table, torch.tensor([100], dtype=torch.int32, device=DEV))
+    ko, vo = attn.read(cache, slots)
+    assert attn.status() == 0
+    (kc, ks), (vc, vs) = P.e4m3_row(f64(k)), P.e4m3_row(f64(v))
+    tab = np.asarray(E4M3_TABLE)
+    K, V = tab[kc] * ks[..., None], tab[vc] * vs[..., None]
+    assert np.array_equal(f64(ko), K) and np.array_equal(f64(vo), V)  # e4m3 times 2^e fits bf16
+    want, _, mag, _ = P.decode(f64(q), [K], [V], [100])
+    close(out, want, 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * mag)
+
+
+def test_step_in_a_graph_and_on_another_stream():
+    """append and decode captured once, replayed as the sequences grow, give
+    the eager bits."""
+    B, nh, nkv, d, page = 3, 8, 2, 128, 16
+    g = gen(3)
+    attn = DecodeAttention(nh, nkv, d, rope_freqs=rope_frequencies(d))
+    w = torch.ones(d, device=DEV)
+    table = torch.randperm(B * 40, generator=g, device=DEV).to(torch.int32).view(B, 40)
+    steps = [randn(g, B, nh + 2 * nkv, d) for _ in range(5)]
+    caches = [make_cache(B * 40, page, nkv, d, "e4m3", fill=1.0) for _ in range(2)]
+    for c in caches:
+        c.k.zero_()
+        c.v.zero_()
+    x = steps[0].clone()
+    pos = torch.tensor([0, 30, 500], dtype=torch.int32, device=DEV)
+    start_pos = pos.clone()
+    lens = torch.empty_like(pos)
+    out = torch.empty(B, nh, d, dtype=torch.bfloat16, device=DEV)
+
+    def step(cache, stream=None):
+        torch.add(pos, 1, out=lens)
+        page_of = table.gather(1, (pos // page).long()[:, None])[:, 0].long()
+        slots = page_of * page + pos % page
+        q = attn.append(x[:, :nh], x[:, nh:nh + nkv], x[:, nh + nkv:], pos, slots, cache, w, w, stream=stream)
+        attn.decode(q, cache, table, lens, out=out, stream=stream)
+        pos.add_(1)
+
+    eager = []
+    for s in steps:
+        x.copy_(s)
+        step(caches[0])
+        eager.append(out.clone())
+    assert attn.status() == 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        pos.copy_(start_pos)
+        step(caches[1], stream=side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(caches[1])
+    pos.copy_(start_pos)
+    for s, want in zip(steps, eager):
+        x.copy_(s)
+        graph.replay()
+        assert torch.equal(out, want)
+    assert attn.status() == 0
+
+
+def test_python_layer_refusals():
+    attn = DecodeAttention(4, 2, 64, rope_freqs=rope_frequencies(64))
+    cache = PagedKVCache.empty(4, 16, 2, 64, "e4m3")
+    bf = torch.bfloat16
+    q, k = torch.zeros(3, 4, 64, dtype=bf, device=DEV), torch.zeros(3, 2, 64, dtype=bf, device=DEV)
+    pos, slots = torch.zeros(3, dtype=torch.int32, device=DEV), torch.arange(3, device=DEV)
+    table, lens = torch.zeros(3, 2, dtype=torch.int32, device=DEV), torch.ones(3, dtype=torch.int32, device=DEV)
+    for bad in (lambda: attn.norm_rope(q.float(), k, pos), lambda: attn.norm_rope(q, k[:2], pos),
+                lambda: attn.norm_rope(q.transpose(0, 1).contiguous().transpose(0, 1), k, pos),
+                lambda: attn.norm_rope(q, k, None), lambda: attn.norm_rope(q, k, pos.long()),
+                lambda: attn.norm_rope(q.cpu(), k, pos), lambda: attn.norm_rope(q, k, pos, torch.ones(32, device=DEV)),
+                lambda: attn.append(q, k, k, pos, slots.int(), cache), lambda: attn.write(cache, k, k[:, :1], slots),
+                lambda: attn.write(cache, k, k, slots[:2]), lambda: attn.read(cache, slots, k_out=q),
+                lambda: attn.decode(q, cache, table.long(), lens), lambda: attn.decode(q, cache, table[:2], lens),
+                lambda: attn.decode(q, cache, table, lens.long()), lambda: attn.decode(q, cache, table, lens[:1]),
+                lambda: attn.decode(q, cache, table, lens, slopes=torch.ones(2, device=DEV)),
+                lambda: attn.decode(q, cache, table, lens, out=k), lambda: attn.decode(q, cache, table, None),
+                lambda: attn.decode(q, cache, table, lens, lse=torch.ones(3, 4, dtype=torch.float64, device=DEV)),
+                lambda: DecodeAttention(8, 4, 64).decode(q, cache, table, lens),
+                lambda: PagedKVCache(cache.k, cache.v), lambda: PagedKVCache(cache.k.float(), cache.v.float()),
+                lambda: PagedKVCache(cache.k, cache.v[:, :1], cache.k_scale, cache.v_scale),
+                lambda: PagedKVCache.empty(1, 16, 2, 64, "fp4")):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(Exception, match="moe_attn_decode"):
+        attn.decode(q, cache, table, lens, softcap=-1.0)
+    with pytest.raises(Exception, match="moe_attn_init"):
+        DecodeAttention(4, 3, 64)
+    # nothing to do
+    none = torch.zeros(0, 4, 64, dtype=bf, device=DEV)
+    assert attn.decode(none, cache, table[:0], lens[:0]).shape == (0, 4, 64)
+    attn.write(cache, none[:, :2], none[:, :2], slots[:0])
+    assert attn.status() == 0
