@@ -13,10 +13,15 @@ using namespace fp8moe;
 
 struct moe_attn {
   moe_attn_config cfg{};
-  int sms = 0;
-  char *ws = nullptr;         // one allocation: turns, error flag
-  uint64_t *turns = nullptr;  // [rope_dim / 2]
+  char *ws = nullptr;         // one allocation, the views below
   int *err = nullptr;
+  uint64_t *turns = nullptr;  // [rope_dim / 2]
+  // moe_attn_decode: CTAs of a launch (by format), and its workspace
+  int ctas[2] = {0, 0};
+  int group = 1, max_ctas = 0;
+  int *counters = nullptr;    // [3][max_ctas], zero between calls
+  float *part_ml = nullptr;   // [2 * max_ctas][group][2]
+  float *part = nullptr;      // [2 * max_ctas][group][head_dim]
   cudaStream_t last_stream = nullptr;
 };
 
@@ -159,19 +164,39 @@ int moe_attn_init(moe_attn **out, const moe_attn_config *cfg) {
   if (a == nullptr) return MOE_ERR_NOMEM;
   a->cfg = *cfg;
   a->cfg.rope_freqs = nullptr;  // the caller's array is not kept
-  a->sms = cfg->max_sms > 0 && cfg->max_sms < sms ? cfg->max_sms : sms;
+  const int use = cfg->max_sms > 0 && cfg->max_sms < sms ? cfg->max_sms : sms;
+  a->group = decode_group(cfg->n_heads / cfg->n_kv_heads);
+  for (int f = 0; f < 2; ++f) {
+    int per_sm = 0;
+    if (plan_paged_decode(cfg->head_dim, f == MOE_KV_E4M3, a->group, &per_sm) != cudaSuccess ||
+        per_sm < 1) {
+      cudaGetLastError();
+      delete a;
+      return MOE_ERR_CUDA;
+    }
+    a->ctas[f] = per_sm * use;
+    if (a->ctas[f] > a->max_ctas) a->max_ctas = a->ctas[f];
+  }
   const int half = cfg->rope_dim / 2;
   uint64_t turns[128];
   for (int i = 0; i < half; ++i) turns[i] = turns_of(cfg->rope_freqs[i]);
-  const size_t bytes = 256 + sizeof(turns);
-  if (cudaMalloc(&a->ws, bytes) != cudaSuccess) {
+  auto up256 = [](size_t n) { return (n + 255) / 256 * 256; };
+  const size_t n = (size_t)a->max_ctas, g = (size_t)a->group;
+  const size_t b_counters = up256(3 * n * sizeof(int)), b_ml = up256(2 * n * g * 2 * sizeof(float));
+  const size_t b_part = up256(2 * n * g * (size_t)cfg->head_dim * sizeof(float));
+  const size_t cleared = 256 + up256(sizeof(turns)) + b_counters;
+  if (cudaMalloc(&a->ws, cleared + b_ml + b_part) != cudaSuccess) {
     cudaGetLastError();
     delete a;
     return MOE_ERR_NOMEM;
   }
-  a->err = reinterpret_cast<int *>(a->ws);
-  a->turns = reinterpret_cast<uint64_t *>(a->ws + 256);
-  if (cudaMemset(a->ws, 0, bytes) != cudaSuccess ||
+  char *p = a->ws;
+  a->err = reinterpret_cast<int *>(p);
+  a->turns = reinterpret_cast<uint64_t *>(p += 256);
+  a->counters = reinterpret_cast<int *>(p += up256(sizeof(turns)));
+  a->part_ml = reinterpret_cast<float *>(p += b_counters);
+  a->part = reinterpret_cast<float *>(p += b_ml);
+  if (cudaMemset(a->ws, 0, cleared) != cudaSuccess ||
       cudaMemcpy(a->turns, turns, (size_t)half * sizeof(uint64_t), cudaMemcpyHostToDevice) !=
           cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess) {  // ready for any stream
@@ -345,6 +370,13 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   r.B = (int)B;
   r.n_heads = c.n_heads;
   r.n_kv = c.n_kv_heads;
+  r.group = a->group;
+  r.groups_per_kv = (c.n_heads / c.n_kv_heads + a->group - 1) / a->group;
+  r.n_groups = c.n_kv_heads * r.groups_per_kv;
+  r.part = a->part;
+  r.part_ml = a->part_ml;
+  r.counters = a->counters;
+  r.max_ctas = a->max_ctas;
   r.scale = scale;
   r.softcap = softcap;
   r.slopes = slopes;
@@ -355,7 +387,10 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   ATTN_TRY(cudaSetDevice(c.device));
   a->last_stream = s;
-  ATTN_TRY(launch_paged_decode(r, c.head_dim, kv->format == MOE_KV_E4M3, s));
+  const int64_t tiles = B * r.n_groups * decode_tiles(r.capacity);
+  const int ctas = a->ctas[kv->format];
+  const int grid = tiles < ctas ? (int)tiles : ctas;
+  ATTN_TRY(launch_paged_decode(r, c.head_dim, kv->format == MOE_KV_E4M3, grid, s));
   return MOE_OK;
 }
 

@@ -69,13 +69,28 @@ struct DecodeArgs {
   int64_t capacity;  // positions a row of the page table covers
   const int32_t *lens, *starts;
   int B, n_heads, n_kv;
+  // query heads of a key/value head are taken `group` (<= 16) at a time, in
+  // groups_per_kv groups; n_groups = n_kv * groups_per_kv
+  int group, groups_per_kv, n_groups;
   float scale, softcap;
   const float *slopes;
   int window;
   __nv_bfloat16 *out;
   float *lse;
+  // workspace: 2 * max_ctas pieces of group * d outputs and group (m, l)
+  // pairs, 3 * max_ctas counters (zero between calls)
+  float *part, *part_ml;
+  int *counters;
+  int max_ctas;
   int *err;
 };
-cudaError_t launch_paged_decode(const DecodeArgs &a, int d, bool e4m3, cudaStream_t s);
+// Query heads taken at a time when `heads_per_kv` share a key/value head.
+int decode_group(int heads_per_kv);
+// Tiles of the split that `positions` positions fill.
+int64_t decode_tiles(int64_t positions);
+// Readies the kernel and tells how many CTAs of it fit on an SM; grid: at most
+// max_ctas, and not more than there are tiles at the longest lengths.
+cudaError_t plan_paged_decode(int d, bool e4m3, int group, int *ctas_per_sm);
+cudaError_t launch_paged_decode(const DecodeArgs &a, int d, bool e4m3, int grid, cudaStream_t s);
 
 }  // namespace fp8moe
