@@ -387,6 +387,7 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   ATTN_TRY(cudaSetDevice(c.device));
   a->last_stream = s;
+  decode_page_division(&r);
   const int64_t tiles = B * r.n_groups * decode_tiles(r.capacity);
   const int ctas = a->ctas[kv->format];
   const int grid = tiles < ctas ? (int)tiles : ctas;

@@ -22,23 +22,29 @@
 //
 // Tile.  Each of a CTA's four warps takes 16 of a tile's 64 keys through its
 // own ring of cp.async stages and keeps its own (m, l, output), so the loop
-// has no CTA-wide barrier.  S = Q K^T and O = P V run as mma.sync m16n8k16
-// with the query heads as the 16 rows.  The order of the contraction and of
-// the output columns is free, so both operands are read from shared memory as
-// whole 16-byte pieces of a row: element order inside an instruction follows
-// the lanes' pieces, not the row.  A score's accumulator is in the layout the
-// next product wants its weights in.
+// has no CTA-wide barrier.  S^T = K Q^T and O^T = V^T P^T run as mma.sync
+// m16n8k16: 16 keys, then 16 output columns, against 8 query heads (twice for
+// groups of 9 to 16), so that few heads leave few lanes idle.  The order of
+// the contraction over d and of the output columns is free, so both operands
+// are read from shared memory as whole 16-byte pieces of a row: the order
+// inside an instruction follows the lanes' pieces, not the row.  Weights pass
+// from the scores' layout to the second product's by 8x8 transposes in
+// registers (movmatrix).
+//
+// Maximum.  The reference m of the exponentials is only moved when a score
+// exceeds it by 2^8: until then weights are at most 2^8 and every sum is as
+// exact as with the true maximum.  Most tiles then cost one vote instead of
+// the shuffles and the scaling of the output.
+//
+// Precision of the weights.
 //   bf16 rows: weights need more than bf16's 8 bits, so they are split into a
-//   high and a low bf16 part (16 bits together).  With at most 8 heads the low
-//   parts are the rows 8-15 that would otherwise be padding; with 9 to 16
-//   heads they are a second product.
+//   high and a low bf16 part (16 bits together) with a product each.
 //   e4m3 rows: codes become f16 (exact), q becomes f16 with a power-of-two
 //   shift per head that puts its largest value at 2^14 (exact down to 2^-28 of
 //   it), a key's scale multiplies its score, and a value's scale joins the
-//   exponent: weights e^(s_j - m') vs_j with a second running maximum m' of
-//   s_j + log2(vs_j), so that they fit f16 whatever the scales.  Weights are
-//   then at most 2^15 and kept to f16's 11 bits, with low parts for up to 8
-//   heads as above.
+//   exponent: weights e^(s_j - m') vs_j with a second reference m' for
+//   s_j + log2(vs_j), so that they fit f16 whatever the scales.  They are
+//   rounded once to f16's 11 bits, an eighth of the step of the bf16 output.
 #include "common.cuh"
 #include "paged_attn.h"
 
@@ -52,12 +58,14 @@ constexpr int kKeys = 16;              // keys of a warp's tile
 constexpr int kTile = kWarps * kKeys;  // keys of a CTA's tile
 constexpr int kJoin = 16;              // pieces joined at a time
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kWeightBits = 15.f;    // e4m3: weights are scaled by 2^15
+constexpr float kLag = 8.f;            // log2 of the largest weight, before its scale
+constexpr float kWeightBits = 7.f;     // e4m3: weights are scaled by 2^7, to 2^15 at most
 
-template <int D_, bool E4M3_, int MH_, int NS_>
+template <int D_, bool E4M3_, int MH_, int NS_, int CTAS_>
 struct Shape {
-  static constexpr int D = D_, MH = MH_, NS = NS_;
+  static constexpr int D = D_, MH = MH_, NS = NS_, CTAS = CTAS_;
   static constexpr bool E4M3 = E4M3_;
+  static constexpr int NT = MH / 8;                           // columns of 8 heads
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kPieces = kRowBytes / 16;              // 16-byte pieces of a row
   static constexpr int kHalfTile = kKeys * kRowBytes;         // a warp's K or V rows
@@ -66,8 +74,9 @@ struct Shape {
   // values per lane and value row: a 16-byte piece, 8 bytes for the shortest row
   static constexpr int EV = E4M3 && D > 64 ? 16 : 8;
   static constexpr int H = D / (8 * EV);
-  static constexpr int kMerge = kWarps * MH * D * 4;          // f32 outputs of the warps
-  static constexpr int kSmem = kRing + kMerge + kWarps * MH * 8 + 64;
+  static constexpr int kMergeRow = D + 4;                     // floats; the odd pieces spread banks
+  static constexpr int kMerge = kWarps * MH * kMergeRow * 4;  // f32 outputs of the warps
+  static constexpr int kSmem = kRing + kMerge + kWarps * MH * 8 + 16;
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
@@ -100,6 +109,26 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   return v;
 }
 
+// Four e4m3 codes as two f16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t &lo, uint32_t &hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
+}
+
+// Transpose of an 8x8 matrix of 16-bit values held two per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ float lds4(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -125,7 +154,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float lg2(float x) {
   float r;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -150,19 +179,15 @@ __device__ __forceinline__ float tanh_f32(float y) {
   return fabsf(y) < 0.6f ? small : large;
 }
 
-// Two weights of neighbouring keys as the high part, and what it leaves.
+// Two weights in 16 bits each, and what the bf16 pair leaves of them.
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if (F16) return pack_f16x2(a, b);
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-template <bool F16>
 __device__ __forceinline__ uint32_t pack2_rest(float a, float b, uint32_t high) {
-  float2 h;
-  if (F16) h = unpack_f16x2(high);
-  else h = make_float2(__uint_as_float(high << 16), __uint_as_float(high & 0xffff0000u));
-  return pack2<F16>(a - h.x, b - h.y);
+  return pack2<false>(a - __uint_as_float(high << 16), b - __uint_as_float(high & 0xffff0000u));
 }
 
 // Visible positions of a sequence.
@@ -182,29 +207,30 @@ __device__ __forceinline__ Span span_of(const DecodeArgs &a, int b) {
   return s;
 }
 
-// A place in the list of all tiles: tile `tile` of group `vh` of sequence b.
+// A place in the list of all tiles: tile `tile` of head group `hg` of
+// key/value head `ch` of sequence b.
 struct Cursor {
-  int b, vh, tile;
+  int b, ch, hg, tile;
   Span s;
   __device__ __forceinline__ void next(const DecodeArgs &a) {
     if (++tile < s.n) return;
     tile = 0;
-    if (++vh < a.n_groups) return;
-    vh = 0;
-    ++b;
-    if (b < a.B) s = span_of(a, b);
+    if (++hg < a.groups_per_kv) return;
+    hg = 0;
+    if (++ch < a.n_kv) return;
+    ch = 0;
+    if (++b < a.B) s = span_of(a, b);
   }
 };
 
 template <class S>
-__global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
-  constexpr int D = S::D, MH = S::MH, NS = S::NS, EV = S::EV;
+__global__ void __launch_bounds__(kThreads, S::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
+  constexpr int D = S::D, MH = S::MH, NT = S::NT, NS = S::NS, EV = S::EV;
   constexpr bool Q8 = S::E4M3;
-  constexpr int kQRegs = MH == 8 ? 2 : 4;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;  // row and column of the matrix instructions
-  float4 *merge = reinterpret_cast<float4 *>(smem + S::kRing);          // [warp][MH][D / 4]
+  float *merge = reinterpret_cast<float *>(smem + S::kRing);            // [warp][MH][kMergeRow]
   float2 *ml = reinterpret_cast<float2 *>(smem + S::kRing + S::kMerge);  // [warp][MH]
   int *misc = reinterpret_cast<int *>(smem + S::kRing + S::kMerge + kWarps * MH * 8);
 
@@ -254,73 +280,90 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
     __syncthreads();
     cu.b = (int)place[0];
     cu.s = span_of(a, cu.b);
-    cu.vh = (int)(place[1] / cu.s.n);
-    cu.tile = (int)(place[1] - (int64_t)cu.vh * cu.s.n);
+    const int vh = (int)(place[1] / cu.s.n);
+    cu.tile = (int)(place[1] - (int64_t)vh * cu.s.n);
+    cu.ch = vh / a.groups_per_kv;
+    cu.hg = vh - cu.ch * a.groups_per_kv;
     __syncthreads();  // the merge buffer is free again
   }
   const int n_tiles = (int)(t1 - t0);
   const int G = a.n_heads / a.n_kv;
 
-  // ---- loads: the rows of a warp's 16 keys, a stage ahead of their use
+  // ---- loads: the rows of a warp's 16 keys, NS stages ahead of their use
+  constexpr int kRowsAtOnce = 32 / S::kPieces;  // rows of one copy instruction
   const uint32_t ring = smem_addr(smem) + warp * (NS * S::kStage);
+  const int my_row = lane / S::kPieces, my_piece = lane % S::kPieces;
+  const int64_t my_off = my_row * a.kv.slot_stride + my_piece * 16;
   Cursor ld = cu;
   int ld_left = n_tiles;
-  int32_t page = -1;     // page of this lane's key (lane & 15) of the next tile to load
-  int64_t row = 0, srow = 0;
-  bool row_on = false;
+  int32_t page = -1;        // of the next tile to load: its page, or that of this lane's key
+  int64_t row = 0, srow = 0;  // offsets of the tile's first key, or of this lane's key
+  uint32_t on = 0;          // keys of the tile that are loaded
   auto key_of = [&](const Cursor &k) { return (k.s.first + k.tile) * kTile + warp * kKeys; };
   auto touches = [&](const Cursor &k) {
     const int base = key_of(k);
     return base < k.s.hi && base + kKeys > k.s.lo;
   };
+  auto page_index = [&](int j) { return (int)(((uint64_t)(uint32_t)j * a.page_mul) >> a.page_shift); };
   auto fetch_page = [&]() {
-    if (ld_left <= 0) return;
-    const int j = key_of(ld) + (lane & 15);
-    if (j >= ld.s.lo && j < ld.s.hi)
-      page = a.table[ld.b * a.table_stride + (uint32_t)j / (uint32_t)a.kv.page_size];
+    if (ld_left <= 0 || !touches(ld)) return;
+    int j = key_of(ld);
+    // with pages of a multiple of 16 a tile's keys share one
+    if (!a.whole_pages) j = min(max(j + (lane & 15), ld.s.lo), ld.s.hi - 1);
+    if (j < ld.s.hi) page = a.table[ld.b * a.table_stride + page_index(j)];
   };
   auto load_half = [&](int stage, bool is_v) {
     if (ld_left > 0 && touches(ld)) {
       const uint32_t dst = ring + stage * S::kStage + (is_v ? S::kHalfTile : 0);
-      if (!is_v) {  // where the lane's key lies; the same for its value row
-        const int j = key_of(ld) + (lane & 15);
-        row_on = j >= ld.s.lo && j < ld.s.hi;
-        if (row_on && (uint64_t)(uint32_t)page >= (uint64_t)a.kv.n_pages) {
-          set_error(a.err, DEV_ERR_BOUNDS);
-          row_on = false;
-        }
-        const int slot = (uint32_t)j % (uint32_t)a.kv.page_size;
-        const int ch = ld.vh / a.groups_per_kv;
-        row = row_on ? page * a.kv.page_stride + ch * a.kv.head_stride + slot * a.kv.slot_stride : 0;
+      if (!is_v) {  // where the keys lie; the same for their value rows
+        const int j0 = key_of(ld);
+        const int from = max(ld.s.lo - j0, 0), to = min(ld.s.hi - j0, kKeys);
+        on = to > from ? (1u << to) - (1u << from) : 0u;
+        const int j = a.whole_pages ? j0 : j0 + (lane & 15);
+        const bool good = (uint32_t)page < (uint32_t)a.kv.n_pages;
+        const int slot = j - page_index(j) * a.kv.page_size;
+        row = page * a.kv.page_stride + ld.ch * a.kv.head_stride + slot * a.kv.slot_stride;
         if (Q8)
-          srow = row_on ? page * a.kv.scale_page_stride + ch * a.kv.scale_head_stride +
-                              slot * a.kv.scale_slot_stride
-                        : 0;
+          srow = page * a.kv.scale_page_stride + ld.ch * a.kv.scale_head_stride +
+                 slot * a.kv.scale_slot_stride;
+        const bool wanted = (on >> (lane & 15)) & 1;
+        if (!good) {
+          if (wanted) set_error(a.err, DEV_ERR_BOUNDS);
+          row = srow = 0;
+        }
+        if (a.whole_pages) {
+          if (!good) on = 0;
+        } else {
+          if (!wanted) row = srow = 0;
+          on &= __ballot_sync(0xffffffffu, good);
+        }
       }
-      const uint32_t on = __ballot_sync(0xffffffffu, row_on);
-      const uint8_t *base = is_v ? a.kv.v : a.kv.k;
-      constexpr int kRowsAtOnce = 32 / S::kPieces;
+      const uint8_t *base = (is_v ? a.kv.v : a.kv.k);
 #pragma unroll
       for (int i = 0; i < kKeys / kRowsAtOnce; ++i) {
-        const int r = i * kRowsAtOnce + lane / S::kPieces, p = lane % S::kPieces;
-        const int64_t off = __shfl_sync(0xffffffffu, row, r);
+        const int r = i * kRowsAtOnce + my_row;
+        int64_t off;
+        if (a.whole_pages) off = row + my_off + i * kRowsAtOnce * a.kv.slot_stride;
+        else off = __shfl_sync(0xffffffffu, row, r) + my_piece * 16;
         // pieces are exchanged within a row so that the reads below hit all banks
-        int q = p;
+        int q = my_piece;
         if (S::kPieces >= 8) q ^= is_v ? (r & 6) : ((r & 1) << 2);
         else if (is_v) q ^= (r >> 1) & 3;
-        copy16(dst + r * S::kRowBytes + q * 16, base + off + p * 16, (on >> r) & 1);
+        const bool take = (on >> r) & 1;
+        copy16(dst + r * S::kRowBytes + q * 16, base + (take ? off : 0), take);
       }
       if (Q8 && !is_v) {  // both scales of a key come with its key row
-        const float *from = (lane < kKeys ? a.kv.k_scale : a.kv.v_scale) + srow;
-        copy4(ring + stage * S::kStage + 2 * S::kHalfTile + 4 * lane, from, row_on);
+        const int r = lane & 15;
+        const bool take = (on >> r) & 1;
+        const float *from = lane < kKeys ? a.kv.k_scale : a.kv.v_scale;
+        const int64_t at = a.whole_pages ? srow + r * a.kv.scale_slot_stride : srow;
+        copy4(ring + stage * S::kStage + 2 * S::kHalfTile + 4 * lane, from + (take ? at : 0), take);
       }
     }
     copy_commit();
-    if (is_v) {
-      if (--ld_left > 0) {
-        ld.next(a);
-        fetch_page();
-      }
+    if (is_v && --ld_left > 0) {
+      ld.next(a);
+      fetch_page();
     }
   };
   fetch_page();
@@ -330,41 +373,37 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
     load_half(s, true);
   }
 
-  // ---- the segment's state
-  uint32_t qf[D / 16][kQRegs];
-  float o[D / 8][4];
-  float m[MH / 8], l[MH / 8], mv[MH / 8];  // mv: the maximum of the weights with value scales
-  float qs[MH / 8], sl[MH / 8];            // scale of a raw score, slope * log2(e)
+  // ---- the segment's state; heads 8n + 2c and 8n + 2c + 1 are this lane's
+  uint32_t qf[NT][D / 16][2];
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2], mv[NT][2];  // mv: the reference of weights with value scales
+  float qs[NT][2], sl[NT][2];           // scale of a raw score, slope * log2(e)
   const float cap2 = a.softcap * kLog2e;
+  const bool plain = !(a.softcap > 0.f) && a.slopes == nullptr;
   auto start_segment = [&]() {
-    const int ch = cu.vh / a.groups_per_kv, hg = cu.vh - ch * a.groups_per_kv;
-    const int in_kv = hg * a.group;
-    const int heads = min(a.group, G - in_kv);
+    const int in_kv = cu.hg * a.group;
+    const int heads = min(a.group, G - in_kv), head0 = cu.ch * G + in_kv;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-    for (int r = 0; r < MH / 8; ++r) {
-      m[r] = mv[r] = -INFINITY;
-      l[r] = 0.f;
-      const int h = g + 8 * r;
-      const bool on = h < heads;
-      const int head = ch * G + in_kv + h;
-      const __nv_bfloat16 *qp = a.q + (int64_t)cu.b * a.q_stride + (int64_t)head * D;
+      for (int i = 0; i < D / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+      const int h = g + 8 * n;  // the head whose q this lane holds
+      const __nv_bfloat16 *qp = a.q + (int64_t)cu.b * a.q_stride + (int64_t)(head0 + h) * D;
       uint4 w[D / 32];
 #pragma unroll
       for (int s = 0; s < D / 32; ++s) {
         // bf16: piece c + 4s of 8 elements; e4m3: halves of piece c + 4 (s / 2) of 16
         const int at = Q8 ? (c + 4 * (s / 2)) * 16 + 8 * (s & 1) : (c + 4 * s) * 8;
-        w[s] = on ? *reinterpret_cast<const uint4 *>(qp + at) : make_uint4(0, 0, 0, 0);
+        w[s] = h < heads ? *reinterpret_cast<const uint4 *>(qp + at) : make_uint4(0, 0, 0, 0);
       }
       float unit = a.scale;
       if (!Q8) {
 #pragma unroll
         for (int s = 0; s < D / 32; ++s) {
-          qf[2 * s][r] = w[s].x;
-          qf[2 * s + 1][r] = w[s].z;
-          qf[2 * s][MH / 8 + r] = w[s].y;
-          qf[2 * s + 1][MH / 8 + r] = w[s].w;
+          qf[n][2 * s][0] = w[s].x;
+          qf[n][2 * s][1] = w[s].y;
+          qf[n][2 * s + 1][0] = w[s].z;
+          qf[n][2 * s + 1][1] = w[s].w;
         }
       } else {
         float big = 0.f;
@@ -389,142 +428,144 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t v = u4_word(w[s], i);
-            const uint32_t f = pack_f16x2(up(__uint_as_float(v << 16)), up(__uint_as_float(v & 0xffff0000u)));
-            qf[2 * s + i / 2][(i & 1) * (MH / 8) + r] = f;
+            qf[n][2 * s + i / 2][i & 1] =
+                pack_f16x2(up(__uint_as_float(v << 16)), up(__uint_as_float(v & 0xffff0000u)));
           }
       }
-      qs[r] = a.softcap > 0.f ? unit / a.softcap : unit * kLog2e;
-      sl[r] = a.slopes && on ? a.slopes[head] * kLog2e : 0.f;
+      unit = a.softcap > 0.f ? unit / a.softcap : unit * kLog2e;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        m[n][u] = mv[n][u] = -INFINITY;
+        l[n][u] = 0.f;
+        qs[n][u] = __shfl_sync(0xffffffffu, unit, 8 * c + 4 * u);
+        const int hh = 8 * n + 2 * c + u;
+        sl[n][u] = a.slopes && hh < heads ? a.slopes[head0 + hh] * kLog2e : 0.f;
+      }
     }
   };
 
   // ---- one tile of 16 keys
-  // raw scores, and the scales of this lane's keys (2c and 2c + 1 of both
-  // halves of the tile): after this the stage's key rows and scales are free
-  auto scores = [&](int stage, float (&s)[2][4], float (&ks)[4], float (&vs)[4]) {
+  // Raw scores of keys g (values 0, 1) and g + 8 (2, 3), and those keys'
+  // scales (vs: log2): after this the stage's key rows and scales are free.
+  auto scores = [&](int stage, float (&s)[NT][4], float (&ks)[2], float (&vs)[2]) {
     const uint32_t base = ring + stage * S::kStage;
     if (Q8) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const uint2 x = lds8(base + 2 * S::kHalfTile + 4 * (8 * t + 2 * c));
-        const uint2 y = lds8(base + 2 * S::kHalfTile + 4 * (kKeys + 8 * t + 2 * c));
-        ks[2 * t] = __uint_as_float(x.x);
-        ks[2 * t + 1] = __uint_as_float(x.y);
-        vs[2 * t] = lg2(__uint_as_float(y.x));
-        vs[2 * t + 1] = lg2(__uint_as_float(y.y));
+        const uint32_t at = base + 2 * S::kHalfTile + 4 * (g + 8 * t);
+        ks[t] = lds4(at);
+        vs[t] = lg2(lds4(at + 4 * kKeys));
       }
     }
+    // two chains of sums per column of heads
+    float z[NT][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-      const int r = t * 8 + g;
-      const uint32_t row_at = base + r * S::kRowBytes;
-      const int swz = S::kPieces >= 8 ? (r & 1) << 2 : 0;
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] = z[n][i] = 0.f;
+    const int swz = S::kPieces >= 8 ? (g & 1) << 2 : 0;  // the same for rows g and g + 8
+    const uint32_t row0 = base + g * S::kRowBytes, row1 = row0 + 8 * S::kRowBytes;
+#pragma unroll
+    for (int i = 0; i < S::kPieces / 4; ++i) {
+      const uint4 k0 = lds16(row0 + (((c + 4 * i) ^ swz) << 4));
+      const uint4 k1 = lds16(row1 + (((c + 4 * i) ^ swz) << 4));
       if (!Q8) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 k = lds16(row_at + (((c + 4 * i) ^ swz) << 4));
-          const int f = 2 * i;
-          mma16816<false>(s[t], qf[f][0], MH == 16 ? qf[f][1] : 0u, qf[f][MH / 8],
-                          MH == 16 ? qf[f][kQRegs - 1] : 0u, k.x, k.y);
-          mma16816<false>(s[t], qf[f + 1][0], MH == 16 ? qf[f + 1][1] : 0u, qf[f + 1][MH / 8],
-                          MH == 16 ? qf[f + 1][kQRegs - 1] : 0u, k.z, k.w);
+        for (int n = 0; n < NT; ++n) {
+          mma16816<false>(s[n], k0.x, k1.x, k0.y, k1.y, qf[n][2 * i][0], qf[n][2 * i][1]);
+          mma16816<false>(z[n], k0.z, k1.z, k0.w, k1.w, qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const uint4 k = lds16(row_at + (((c + 4 * i) ^ swz) << 4));
+        for (int w = 0; w < 4; ++w) {
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16(u4_word(k0, w), a0, a2);
+          e4m3x4_to_f16(u4_word(k1, w), a1, a3);
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t x = u4_word(k, w);
-            const int f = 4 * i + w;
-            mma16816<true>(s[t], qf[f][0], MH == 16 ? qf[f][1] : 0u, qf[f][MH / 8],
-                           MH == 16 ? qf[f][kQRegs - 1] : 0u, e4m3x2_to_f16x2(x),
-                           e4m3x2_to_f16x2(x >> 16));
-          }
+          for (int n = 0; n < NT; ++n)
+            mma16816<true>(w & 1 ? z[n] : s[n], a0, a1, a2, a3, qf[n][4 * i + w][0], qf[n][4 * i + w][1]);
         }
       }
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] += z[n][i];
   };
-  // weights of the tile's keys (vs: log2 of their value scales), and the sums
-  auto weights = [&](const float (&s)[2][4], const float (&ks)[4], const float (&vs)[4],
-                     uint32_t (&p_hi)[MH / 8][2], uint32_t (&p_lo)[MH / 8][2]) {
+  // Weights of the tile's keys, transposed to (head g; keys 2c, 2c + 1) and
+  // (.., keys 8 + 2c, 9 + 2c): high parts, and what they leave.
+  auto weights = [&](float (&s)[NT][4], const float (&ks)[2], const float (&vs)[2],
+                     uint32_t (&p_hi)[NT][2], uint32_t (&p_lo)[NT][2]) {
     const int base = key_of(cu);
     const bool edge = base < cu.s.lo || base + kKeys > cu.s.hi;
+    bool high = false;
 #pragma unroll
-    for (int r = 0; r < MH / 8; ++r) {
-      float x[4], xv[4];
-      float top = m[r], top_v = mv[r];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int key = base + (i >> 1) * 8 + 2 * c + (i & 1);
-        float raw = s[i >> 1][2 * r + (i & 1)] * qs[r];
-        if (Q8) raw *= ks[i];
-        if (a.softcap > 0.f) raw = cap2 * tanh_f32(raw);
-        raw = fmaf(sl[r], (float)(key - (cu.s.hi - 1)), raw);
-        if (edge && (key < cu.s.lo || key >= cu.s.hi)) raw = -INFINITY;
-        x[i] = raw;
-        top = fmaxf(top, raw);
-        if (Q8) {
-          xv[i] = raw == -INFINITY ? -INFINITY : raw + vs[i];
-          top_v = fmaxf(top_v, xv[i]);
+        float x = s[n][i] * qs[n][i & 1];
+        if (Q8) x *= ks[i >> 1];
+        const int key = base + g + 8 * (i >> 1);
+        if (!plain) {
+          if (a.softcap > 0.f) x = cap2 * tanh_f32(x);
+          x = fmaf(sl[n][i & 1], (float)(key - (cu.s.hi - 1)), x);
         }
+        if (edge && (key < cu.s.lo || key >= cu.s.hi)) x = -INFINITY;
+        s[n][i] = x;
+        high |= x > m[n][i & 1] + kLag;
+        if (Q8) high |= x + vs[i >> 1] > mv[n][i & 1] + kLag;
       }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float keep = rescale(m[r], top);
-      l[r] *= keep;
-      float keep_o = keep;
-      bool grew = top > m[r];
-      m[r] = top;
-      if (Q8) {
-        top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, 1));
-        top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, 2));
-        keep_o = rescale(mv[r], top_v);
-        grew = top_v > mv[r];
-        mv[r] = top_v;
-      }
-      if (__any_sync(0xffffffffu, grew)) {
+    if (__any_sync(0xffffffffu, high)) {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][2 * r] *= keep_o;
-          o[i][2 * r + 1] *= keep_o;
-          if (MH == 8) {  // rows 8-15 are the same heads' low parts
-            o[i][2] *= keep_o;
-            o[i][3] *= keep_o;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float top = fmaxf(s[n][u], s[n][2 + u]), top_v = 0.f;
+          if (Q8) top_v = fmaxf(s[n][u] + vs[0], s[n][2 + u] + vs[1]);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            if (Q8) top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, x));
+          }
+          top = fmaxf(top, m[n][u]);
+          float keep = rescale(m[n][u], top);
+          l[n][u] *= keep;
+          m[n][u] = top;
+          if (Q8) {
+            top_v = fmaxf(top_v, mv[n][u]);
+            keep = rescale(mv[n][u], top_v);
+            mv[n][u] = top_v;
+          }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            o[n][i][u] *= keep;
+            o[n][i][2 + u] *= keep;
           }
         }
-      }
-      const float zero = top == -INFINITY ? 0.f : top;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
       float p[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        p[i] = ex2(x[i] - zero);
-        l[r] += p[i];
-      }
-      if (Q8) {
-        const float zero_v = (top_v == -INFINITY ? 0.f : top_v) - kWeightBits;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = ex2(xv[i] - zero_v);
+        const float zero = m[n][i & 1] == -INFINITY ? 0.f : m[n][i & 1];
+        p[i] = ex2(s[n][i] - zero);
+        l[n][i & 1] += p[i];
+        if (Q8) {
+          const float zero_v = (mv[n][i & 1] == -INFINITY ? 0.f : mv[n][i & 1]) - kWeightBits;
+          p[i] = ex2(s[n][i] + vs[i >> 1] - zero_v);
+        }
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        p_hi[r][t] = pack2<Q8>(p[2 * t], p[2 * t + 1]);
-        p_lo[r][t] = pack2_rest<Q8>(p[2 * t], p[2 * t + 1], p_hi[r][t]);
+        const uint32_t hi = pack2<Q8>(p[2 * t], p[2 * t + 1]);
+        p_hi[n][t] = transpose8(hi);
+        if (!Q8) p_lo[n][t] = transpose8(pack2_rest(p[2 * t], p[2 * t + 1], hi));
       }
     }
   };
-  auto add_values = [&](int stage, const uint32_t (&p_hi)[MH / 8][2], const uint32_t (&p_lo)[MH / 8][2]) {
+  auto add_values = [&](int stage, const uint32_t (&p_hi)[NT][2], const uint32_t (&p_lo)[NT][2]) {
     const uint32_t vb = ring + stage * S::kStage + S::kHalfTile;
-    auto product = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
-      if (MH == 8) {
-        mma16816<Q8>(acc, p_hi[0][0], p_lo[0][0], p_hi[0][1], p_lo[0][1], b0, b1);
-      } else {
-        mma16816<Q8>(acc, p_hi[0][0], p_hi[MH / 8 - 1][0], p_hi[0][1], p_hi[MH / 8 - 1][1], b0, b1);
-        if (!Q8)
-          mma16816<Q8>(acc, p_lo[0][0], p_lo[MH / 8 - 1][0], p_lo[0][1], p_lo[MH / 8 - 1][1], b0, b1);
-      }
-    };
 #pragma unroll
     for (int h = 0; h < S::H; ++h) {
       uint4 v[4];
@@ -539,25 +580,27 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
           v[i] = make_uint4(x.x, x.y, 0, 0);
         }
       }
-      if (!Q8) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t v0 = u4_word(v[0], w), v1 = u4_word(v[1], w), v2 = u4_word(v[2], w),
-                         v3 = u4_word(v[3], w);
-          product(o[8 * h + 2 * w], __byte_perm(v0, v1, 0x5410), __byte_perm(v2, v3, 0x5410));
-          product(o[8 * h + 2 * w + 1], __byte_perm(v0, v1, 0x7632), __byte_perm(v2, v3, 0x7632));
-        }
-      } else {
+      for (int w = 0; w < (Q8 ? EV / 4 : 4); ++w) {
+        const uint32_t v0 = u4_word(v[0], w), v1 = u4_word(v[1], w), v2 = u4_word(v[2], w),
+                       v3 = u4_word(v[3], w);
+        if (!Q8) {  // columns 2w, 2w + 1 of the piece, keys paired
+          const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
+          const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
 #pragma unroll
-        for (int w = 0; w < EV / 4; ++w) {
-          const uint32_t v0 = u4_word(v[0], w), v1 = u4_word(v[1], w), v2 = u4_word(v[2], w),
-                         v3 = u4_word(v[3], w);
+          for (int n = 0; n < NT; ++n) {
+            mma16816<false>(o[n][4 * h + w], a0, a1, a2, a3, p_hi[n][0], p_hi[n][1]);
+            mma16816<false>(o[n][4 * h + w], a0, a1, a2, a3, p_lo[n][0], p_lo[n][1]);
+          }
+        } else {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {  // codes 2u, 2u + 1 of the word, keys paired
-            const uint32_t x = __byte_perm(v0, v1, u ? 0x7362 : 0x5140);
-            const uint32_t y = __byte_perm(v2, v3, u ? 0x7362 : 0x5140);
-            product(o[EV * h + 4 * w + 2 * u], e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y));
-            product(o[EV * h + 4 * w + 2 * u + 1], e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y >> 16));
+          for (int u = 0; u < 2; ++u) {  // columns 4w + 2u, + 1
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16(__byte_perm(v0, v1, u ? 0x7362 : 0x5140), a0, a1);
+            e4m3x4_to_f16(__byte_perm(v2, v3, u ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816<true>(o[n][EV / 2 * h + 2 * w + u], a0, a1, a2, a3, p_hi[n][0], p_hi[n][1]);
           }
         }
       }
@@ -565,49 +608,42 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
   };
 
   // ---- end of a segment, or of this CTA's piece of it
-  // Outputs are kept as float4 items: item i of a head is elements d(i) .. d(i) + 3.
-  auto element_of = [&](int i) {
-    const int cc = i & 3, q = i >> 2, jj = q % (EV / 4), hu = q / (EV / 4);
-    return (2 * cc + (hu & 1) + 8 * (hu >> 1)) * EV + 4 * jj;
-  };
+  // Outputs are handled as float4 items: item i of a head is elements 4i .. 4i + 3.
   auto write_out = [&](int b, int head, int item, float4 v, float mm, float ll) {
     const float inv = ll == 0.f ? 0.f : 1.f / ll;
     const int64_t bh = (int64_t)b * a.n_heads + head;
     uint2 w;
     w.x = pack2<false>(v.x * inv, v.y * inv);
     w.y = pack2<false>(v.z * inv, v.w * inv);
-    *reinterpret_cast<uint2 *>(a.out + bh * D + element_of(item)) = w;
+    *reinterpret_cast<uint2 *>(a.out + bh * D + 4 * item) = w;
     if (item == 0 && a.lse) a.lse[bh] = (mm + log2f(ll)) * kLn2;
   };
   auto finish_segment = [&](int64_t seg0, int64_t seg1) {
-    const int ch = cu.vh / a.groups_per_kv, hg = cu.vh - ch * a.groups_per_kv;
-    const int in_kv = hg * a.group, heads = min(a.group, G - in_kv);
-    const int head0 = ch * G + in_kv;
+    const int in_kv = cu.hg * a.group, heads = min(a.group, G - in_kv);
+    const int head0 = cu.ch * G + in_kv;
 #pragma unroll
-    for (int r = 0; r < MH / 8; ++r) {
-      float sum = l[r];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      float f = 1.f;
-      if (Q8 && m[r] != -INFINITY && mv[r] != -INFINITY) f = ex2(mv[r] - m[r] - kWeightBits);
-      const int h = g + 8 * r;
-      float4 *dst = merge + (warp * MH + h) * (D / 4);
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int hh = 0; hh < S::H; ++hh)
+      for (int u = 0; u < 2; ++u) {
+        float sum = l[n][u];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        float f = 1.f;
+        if (Q8 && m[n][u] != -INFINITY && mv[n][u] != -INFINITY) f = ex2(mv[n][u] - m[n][u] - kWeightBits);
+        const int h = 8 * n + 2 * c + u;
+        if (h < heads) {
+          float *dst = merge + (warp * MH + h) * S::kMergeRow;
 #pragma unroll
-          for (int jj = 0; jj < EV / 4; ++jj) {
-            float v[4];
+          for (int hh = 0; hh < S::H; ++hh)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float *x = o[EV * hh + 4 * jj + i];
-              v[i] = (MH == 8 ? x[u] + x[2 + u] : x[2 * r + u]) * f;
+            for (int jj = 0; jj < EV / 4; ++jj) {
+              const float *x = o[n][EV / 2 * hh + 2 * jj], *y = o[n][EV / 2 * hh + 2 * jj + 1];
+              *reinterpret_cast<float4 *>(dst + (g + 8 * hh) * EV + 4 * jj) =
+                  make_float4(x[u] * f, x[2 + u] * f, y[u] * f, y[2 + u] * f);
             }
-            dst[((hh * 2 + u) * (EV / 4) + jj) * 4 + c] = make_float4(v[0], v[1], v[2], v[3]);
-          }
-      if (c == 0) ml[warp * MH + h] = make_float2(m[r], sum);
-    }
+          if (g == 0) ml[warp * MH + h] = make_float2(m[n][u], sum);
+        }
+      }
     __syncthreads();
     // which CTAs hold pieces of this segment
     int first = blockIdx.x, pieces = 1;
@@ -632,7 +668,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
       for (int w = 0; w < kWarps; ++w) {
         const float2 s = ml[w * MH + h];
         const float f = rescale(s.x, mm);
-        const float4 x = merge[(w * MH + h) * (D / 4) + it];
+        const float4 x = *reinterpret_cast<const float4 *>(merge + (w * MH + h) * S::kMergeRow + 4 * it);
         ll = fmaf(f, s.y, ll);
         v.x = fmaf(f, x.x, v.x);
         v.y = fmaf(f, x.y, v.y);
@@ -731,8 +767,8 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
   for (int i = 0; i < n_tiles; ++i) {
     if (i == 0 || cu.tile == 0) start_segment();
     const bool on = touches(cu);
-    uint32_t p_hi[MH / 8][2], p_lo[MH / 8][2];
-    float s[2][4], ks[4], vs[4];
+    uint32_t p_hi[NT][2], p_lo[NT][2];
+    float s[NT][4], ks[2], vs[2];
     copy_wait<2 * NS - 1>();  // the key rows
     __syncwarp();
     if (on) scores(stage, s, ks, vs);
@@ -770,14 +806,14 @@ cudaError_t with_shape(int d, bool e4m3, int group, F f) {
   const bool wide = group > 8;
   switch (d) {
     case 64:
-      if (e4m3) return wide ? f(Shape<64, true, 16, 4>{}) : f(Shape<64, true, 8, 4>{});
-      return wide ? f(Shape<64, false, 16, 3>{}) : f(Shape<64, false, 8, 3>{});
+      if (e4m3) return wide ? f(Shape<64, true, 16, 4, 3>{}) : f(Shape<64, true, 8, 4, 4>{});
+      return wide ? f(Shape<64, false, 16, 3, 3>{}) : f(Shape<64, false, 8, 3, 4>{});
     case 128:
-      if (e4m3) return wide ? f(Shape<128, true, 16, 3>{}) : f(Shape<128, true, 8, 3>{});
-      return wide ? f(Shape<128, false, 16, 2>{}) : f(Shape<128, false, 8, 2>{});
+      if (e4m3) return wide ? f(Shape<128, true, 16, 3, 2>{}) : f(Shape<128, true, 8, 3, 3>{});
+      return wide ? f(Shape<128, false, 16, 2, 2>{}) : f(Shape<128, false, 8, 2, 2>{});
     case 256:
-      if (e4m3) return wide ? f(Shape<256, true, 16, 2>{}) : f(Shape<256, true, 8, 2>{});
-      return wide ? f(Shape<256, false, 16, 1>{}) : f(Shape<256, false, 8, 1>{});
+      if (e4m3) return wide ? f(Shape<256, true, 16, 2, 1>{}) : f(Shape<256, true, 8, 2, 2>{});
+      return wide ? f(Shape<256, false, 16, 1, 1>{}) : f(Shape<256, false, 8, 1, 2>{});
     default: return cudaErrorInvalidValue;
   }
 }
@@ -787,6 +823,17 @@ cudaError_t with_shape(int d, bool e4m3, int group, F f) {
 int decode_group(int heads_per_kv) {
   const int n = (heads_per_kv + 15) / 16;
   return (heads_per_kv + n - 1) / n;
+}
+
+// With 2^k >= d > 2^(k - 1) and mul = floor(2^(31 + k) / d) + 1, mul * d exceeds
+// 2^(31 + k) by at most d <= 2^k, so j * mul >> (31 + k) is j / d for every j < 2^31.
+void decode_page_division(DecodeArgs *a) {
+  const uint64_t d = (uint64_t)a->kv.page_size;
+  int k = 0;
+  while ((UINT64_C(1) << k) < d) ++k;
+  a->page_mul = (uint32_t)((UINT64_C(1) << (31 + k)) / d + 1);
+  a->page_shift = 31 + k;
+  a->whole_pages = d % kKeys == 0;
 }
 
 int64_t decode_tiles(int64_t positions) { return (positions + kTile - 1) / kTile; }

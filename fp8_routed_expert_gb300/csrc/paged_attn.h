@@ -77,6 +77,11 @@ struct DecodeArgs {
   int window;
   __nv_bfloat16 *out;
   float *lse;
+  // position / page_size = position * page_mul >> page_shift; whole_pages: the
+  // page size is a multiple of 16
+  uint32_t page_mul;
+  int page_shift;
+  bool whole_pages;
   // workspace: 2 * max_ctas pieces of group * d outputs and group (m, l)
   // pairs, 3 * max_ctas counters (zero between calls)
   float *part, *part_ml;
@@ -86,6 +91,8 @@ struct DecodeArgs {
 };
 // Query heads taken at a time when `heads_per_kv` share a key/value head.
 int decode_group(int heads_per_kv);
+// Fills in page_mul, page_shift and whole_pages.
+void decode_page_division(DecodeArgs *a);
 // Tiles of the split that `positions` positions fill.
 int64_t decode_tiles(int64_t positions);
 // Readies the kernel and tells how many CTAs of it fit on an SM; grid: at most
