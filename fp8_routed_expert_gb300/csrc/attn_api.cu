@@ -16,8 +16,8 @@ struct moe_attn {
   char *ws = nullptr;         // one allocation, the views below
   int *err = nullptr;
   uint64_t *turns = nullptr;  // [rope_dim / 2]
-  // moe_attn_decode: CTAs of a launch (by format), and its workspace
-  int ctas[2] = {0, 0};
+  // moe_attn_decode: CTAs of a launch and positions of a tile (by format), workspace
+  int ctas[2] = {0, 0}, tile[2] = {1, 1};
   int group = 1, max_ctas = 0;
   int *counters = nullptr;    // [3][max_ctas], zero between calls
   float *part_ml = nullptr;   // [2 * max_ctas][group][2]
@@ -168,7 +168,7 @@ int moe_attn_init(moe_attn **out, const moe_attn_config *cfg) {
   a->group = decode_group(cfg->n_heads / cfg->n_kv_heads);
   for (int f = 0; f < 2; ++f) {
     int per_sm = 0;
-    if (plan_paged_decode(cfg->head_dim, f == MOE_KV_E4M3, a->group, &per_sm) != cudaSuccess ||
+    if (plan_paged_decode(cfg->head_dim, f == MOE_KV_E4M3, a->group, &per_sm, &a->tile[f]) != cudaSuccess ||
         per_sm < 1) {
       cudaGetLastError();
       delete a;
@@ -388,7 +388,9 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   ATTN_TRY(cudaSetDevice(c.device));
   a->last_stream = s;
   decode_page_division(&r);
-  const int64_t tiles = B * r.n_groups * decode_tiles(r.capacity);
+  const int tile = a->tile[kv->format];
+  const int64_t tiles = B * r.n_groups * ((r.capacity + tile - 1) / tile);  // < 2^62
+  if (tiles > INT32_MAX) return MOE_ERR_SHAPE;
   const int ctas = a->ctas[kv->format];
   const int grid = tiles < ctas ? (int)tiles : ctas;
   ATTN_TRY(launch_paged_decode(r, c.head_dim, kv->format == MOE_KV_E4M3, grid, s));

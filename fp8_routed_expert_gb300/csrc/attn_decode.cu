@@ -9,8 +9,7 @@
 // The launch reads each visible key and value row once and is bound by HBM;
 // the design keeps loads in flight and everything else out of their way.
 //
-// Split.  A sequence's visible positions are cut into tiles of 64, a segment
-// is the tiles of one (sequence, group of up to 16 query heads that share a
+// Split.  A sequence's visible positions are cut into tiles, a segment is the tiles of one (sequence, group of up to 16 query heads that share a
 // key/value head), and the list of all segments' tiles is cut evenly over the
 // CTAs, whatever the lengths: every CTA finds its piece from the lengths
 // themselves.  A CTA that holds a segment's whole list writes its result; the
@@ -20,8 +19,8 @@
 // pieces' places, so results do not depend on the order of arrival.  No CTA
 // waits for another.
 //
-// Tile.  Each of a CTA's four warps takes 16 of a tile's 64 keys through its
-// own ring of cp.async stages and keeps its own (m, l, output), so the loop
+// Tile.  Each warp takes 16 or 32 of a tile's keys through its own ring of
+// cp.async stages and keeps its own (m, l, output), so the loop
 // has no CTA-wide barrier.  S^T = K Q^T and O^T = V^T P^T run as mma.sync
 // m16n8k16: 16 keys, then 16 output columns, against 8 query heads (twice for
 // groups of 9 to 16), so that few heads leave few lanes idle.  The order of
@@ -52,18 +51,19 @@ namespace fp8moe {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kKeys = 16;              // keys of a warp's tile
-constexpr int kTile = kWarps * kKeys;  // keys of a CTA's tile
-constexpr int kJoin = 16;              // pieces joined at a time
+constexpr int kJoin = 16;              // pieces joined by one CTA
+constexpr int kBatch = 8;              // pieces whose loads are in flight together
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLag = 8.f;            // log2 of the largest weight, before its scale
 constexpr float kWeightBits = 7.f;     // e4m3: weights are scaled by 2^7, to 2^15 at most
 
-template <int D_, bool E4M3_, int MH_, int NS_, int CTAS_>
+// MH: query heads of a group at most; KM: 16-key steps of a warp's tile; NS:
+// stages of a warp's ring; CTAS: that fit on an SM.
+template <int D_, bool E4M3_, int MH_, int KM_, int kWarps_, int NS_, int CTAS_>
 struct Shape {
-  static constexpr int D = D_, MH = MH_, NS = NS_, CTAS = CTAS_;
+  static constexpr int D = D_, MH = MH_, KM = KM_, NS = NS_, CTAS = CTAS_;
+  static constexpr int kWarps = kWarps_, kThreads = 32 * kWarps;
+  static constexpr int kKeys = 16 * KM, kTile = kWarps * kKeys;  // keys of a warp's and a CTA's tile
   static constexpr bool E4M3 = E4M3_;
   static constexpr int NT = MH / 8;                           // columns of 8 heads
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
@@ -87,6 +87,9 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
                : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool on) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0)
@@ -190,11 +193,12 @@ __device__ __forceinline__ uint32_t pack2_rest(float a, float b, uint32_t high) 
   return pack2<false>(a - __uint_as_float(high << 16), b - __uint_as_float(high & 0xffff0000u));
 }
 
-// Visible positions of a sequence.
+// Visible positions of a sequence, and the tiles of T positions they touch.
 struct Span {
   int lo, hi;      // [lo, hi); hi is the length
-  int first, n;    // first tile of 64, number of tiles (one, all hidden, if none is visible)
+  int first, n;    // first tile, number of tiles (one, all hidden, if none is visible)
 };
+template <int T>
 __device__ __forceinline__ Span span_of(const DecodeArgs &a, int b) {
   int len = a.lens[b];
   if (len < 0) len = 0;
@@ -202,13 +206,14 @@ __device__ __forceinline__ Span span_of(const DecodeArgs &a, int b) {
   int lo = a.starts ? a.starts[b] : 0;
   if (lo < 0) lo = 0;
   if (a.window > 0 && lo < len - a.window) lo = len - a.window;
-  Span s{lo, len, lo / kTile, 1};
-  if (lo < len) s.n = (len + kTile - 1) / kTile - s.first;
+  Span s{lo, len, lo / T, 1};
+  if (lo < len) s.n = (len + T - 1) / T - s.first;
   return s;
 }
 
 // A place in the list of all tiles: tile `tile` of head group `hg` of
 // key/value head `ch` of sequence b.
+template <int T>
 struct Cursor {
   int b, ch, hg, tile;
   Span s;
@@ -219,13 +224,25 @@ struct Cursor {
     hg = 0;
     if (++ch < a.n_kv) return;
     ch = 0;
-    if (++b < a.B) s = span_of(a, b);
+    if (++b < a.B) s = span_of<T>(a, b);
+  }
+};
+
+// The even cut of W tiles over N CTAs: the first W % N take one more.
+struct Cut {
+  uint32_t each, more;
+  __device__ __forceinline__ Cut(uint32_t W, uint32_t N) : each(W / N), more(W % N) {}
+  __device__ __forceinline__ uint32_t start(uint32_t cta) const { return each * cta + min(cta, more); }
+  __device__ __forceinline__ uint32_t owner(uint32_t tile) const {
+    const uint32_t big = more * (each + 1);
+    return tile < big ? tile / (each + 1) : more + (tile - big) / each;
   }
 };
 
 template <class S>
-__global__ void __launch_bounds__(kThreads, S::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
-  constexpr int D = S::D, MH = S::MH, NT = S::NT, NS = S::NS, EV = S::EV;
+__global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
+  constexpr int D = S::D, MH = S::MH, NT = S::NT, NS = S::NS, EV = S::EV, KM = S::KM;
+  constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kKeys = S::kKeys, kTile = S::kTile;
   constexpr bool Q8 = S::E4M3;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -235,26 +252,46 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) decode_kernel(const __grid_
   int *misc = reinterpret_cast<int *>(smem + S::kRing + S::kMerge + kWarps * MH * 8);
 
   // ---- this CTA's piece [t0, t1) of the W tiles of all sequences
-  int64_t W, t0, t1;
-  int n_ctas;
-  Cursor cu;
-  {
-    int64_t *sums = reinterpret_cast<int64_t *>(merge);  // one per warp
-    int64_t *place = sums + kWarps;
-    const int per = (a.B + kThreads - 1) / kThreads;
-    const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-      const int len = a.lens[b];
-      if (len < 0 || len > a.capacity) set_error(a.err, DEV_ERR_BOUNDS);
-      mine += (int64_t)span_of(a, b).n * a.n_groups;
-    }
-    int64_t incl = mine;
+  uint32_t W, before;  // tiles of all sequences, and of those before this piece's first
+  Cursor<kTile> cu;
+  const auto count = [&](int b, Span *sp) {
+    const int len = a.lens[b];
+    if (len < 0 || len > a.capacity) set_error(a.err, DEV_ERR_BOUNDS);
+    *sp = span_of<kTile>(a, b);
+    return (uint32_t)(sp->n * a.n_groups);
+  };
+  const auto scan = [&](uint32_t v) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const uint32_t w = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += w;
     }
+    return v;
+  };
+  if (a.B <= 32) {  // a sequence per lane, every warp for itself
+    Span sp{0, 0, 0, 0};
+    const uint32_t n = lane < a.B ? count(lane, &sp) : 0;
+    const uint32_t incl = scan(n);
+    W = __shfl_sync(0xffffffffu, incl, 31);
+    const uint32_t N = min(W, gridDim.x);
+    if (blockIdx.x >= N) return;
+    const uint32_t t0 = Cut(W, N).start(blockIdx.x);
+    const uint32_t mask = __ballot_sync(0xffffffffu, incl > t0);
+    const int at = __ffs((int)mask) - 1;
+    before = __shfl_sync(0xffffffffu, incl - n, at);
+    cu.b = at;
+    cu.s.lo = __shfl_sync(0xffffffffu, sp.lo, at);
+    cu.s.hi = __shfl_sync(0xffffffffu, sp.hi, at);
+    cu.s.first = __shfl_sync(0xffffffffu, sp.first, at);
+    cu.s.n = __shfl_sync(0xffffffffu, sp.n, at);
+  } else {  // a run of sequences per thread
+    uint32_t *sums = reinterpret_cast<uint32_t *>(merge), *place = sums + kWarps;
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
+    Span sp;
+    uint32_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += count(b, &sp);
+    uint32_t incl = scan(mine);
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
     W = 0;
@@ -262,102 +299,109 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) decode_kernel(const __grid_
       if (w < warp) incl += sums[w];
       W += sums[w];
     }
-    n_ctas = W < (int64_t)gridDim.x ? (int)W : (int)gridDim.x;
-    if ((int)blockIdx.x >= n_ctas) return;
-    t0 = W * blockIdx.x / n_ctas;
-    t1 = W * (blockIdx.x + 1) / n_ctas;
+    const uint32_t N = min(W, gridDim.x);
+    if (blockIdx.x >= N) return;
+    const uint32_t t0 = Cut(W, N).start(blockIdx.x);
     if (incl - mine <= t0 && t0 < incl) {
-      int64_t at = incl - mine;
+      uint32_t at = incl - mine;
       int b = b0;
       for (;; ++b) {
-        const int64_t n = (int64_t)span_of(a, b).n * a.n_groups;
+        const uint32_t n = (uint32_t)(span_of<kTile>(a, b).n * a.n_groups);
         if (t0 < at + n) break;
         at += n;
       }
       place[0] = b;
-      place[1] = t0 - at;
+      place[1] = at;
     }
     __syncthreads();
-    cu.b = (int)place[0];
-    cu.s = span_of(a, cu.b);
-    const int vh = (int)(place[1] / cu.s.n);
-    cu.tile = (int)(place[1] - (int64_t)vh * cu.s.n);
+    cu.b = place[0];
+    before = place[1];
+    cu.s = span_of<kTile>(a, cu.b);
+    __syncthreads();  // the merge buffer is free again
+  }
+  const uint32_t n_ctas = min(W, gridDim.x);
+  const Cut cut(W, n_ctas);
+  const uint32_t t0 = cut.start(blockIdx.x), t1 = cut.start(blockIdx.x + 1);
+  {
+    const int vh = (int)((t0 - before) / (uint32_t)cu.s.n);
+    cu.tile = (int)(t0 - before) - vh * cu.s.n;
     cu.ch = vh / a.groups_per_kv;
     cu.hg = vh - cu.ch * a.groups_per_kv;
-    __syncthreads();  // the merge buffer is free again
   }
   const int n_tiles = (int)(t1 - t0);
   const int G = a.n_heads / a.n_kv;
 
-  // ---- loads: the rows of a warp's 16 keys, NS stages ahead of their use
+  // ---- loads: the rows of a warp's keys, NS stages ahead of their use
   constexpr int kRowsAtOnce = 32 / S::kPieces;  // rows of one copy instruction
+  constexpr uint32_t kAll = kKeys == 32 ? 0xffffffffu : (1u << kKeys) - 1;
   const uint32_t ring = smem_addr(smem) + warp * (NS * S::kStage);
-  const int my_row = lane / S::kPieces, my_piece = lane % S::kPieces;
+  const int my_key = lane & (kKeys - 1), my_row = lane / S::kPieces, my_piece = lane % S::kPieces;
   const int64_t my_off = my_row * a.kv.slot_stride + my_piece * 16;
-  Cursor ld = cu;
+  const int64_t row_step = kRowsAtOnce * a.kv.slot_stride;
+  Cursor<kTile> ld = cu;
   int ld_left = n_tiles;
-  int32_t page = -1;        // of the next tile to load: its page, or that of this lane's key
-  int64_t row = 0, srow = 0;  // offsets of the tile's first key, or of this lane's key
-  uint32_t on = 0;          // keys of the tile that are loaded
-  auto key_of = [&](const Cursor &k) { return (k.s.first + k.tile) * kTile + warp * kKeys; };
-  auto touches = [&](const Cursor &k) {
+  int32_t page = -1;          // page of this lane's key in the next tile to load
+  int64_t row = 0, srow = 0;  // offsets of its row and its scales
+  uint32_t on = 0;            // keys of the tile that are loaded
+  auto key_of = [&](const Cursor<kTile> &k) { return (k.s.first + k.tile) * kTile + warp * kKeys; };
+  auto touches = [&](const Cursor<kTile> &k) {
     const int base = key_of(k);
     return base < k.s.hi && base + kKeys > k.s.lo;
   };
   auto page_index = [&](int j) { return (int)(((uint64_t)(uint32_t)j * a.page_mul) >> a.page_shift); };
   auto fetch_page = [&]() {
-    if (ld_left <= 0 || !touches(ld)) return;
-    int j = key_of(ld);
-    // with pages of a multiple of 16 a tile's keys share one
-    if (!a.whole_pages) j = min(max(j + (lane & 15), ld.s.lo), ld.s.hi - 1);
-    if (j < ld.s.hi) page = a.table[ld.b * a.table_stride + page_index(j)];
+    if (ld_left <= 0) return;
+    const int j = key_of(ld) + my_key;
+    page = -1;
+    if (j >= ld.s.lo && j < ld.s.hi) page = a.table[ld.b * a.table_stride + page_index(j)];
   };
   auto load_half = [&](int stage, bool is_v) {
     if (ld_left > 0 && touches(ld)) {
       const uint32_t dst = ring + stage * S::kStage + (is_v ? S::kHalfTile : 0);
       if (!is_v) {  // where the keys lie; the same for their value rows
-        const int j0 = key_of(ld);
-        const int from = max(ld.s.lo - j0, 0), to = min(ld.s.hi - j0, kKeys);
-        on = to > from ? (1u << to) - (1u << from) : 0u;
-        const int j = a.whole_pages ? j0 : j0 + (lane & 15);
+        const int j = key_of(ld) + my_key;
         const bool good = (uint32_t)page < (uint32_t)a.kv.n_pages;
+        if (!good && j >= ld.s.lo && j < ld.s.hi) set_error(a.err, DEV_ERR_BOUNDS);
+        on = __ballot_sync(0xffffffffu, good) & kAll;
         const int slot = j - page_index(j) * a.kv.page_size;
-        row = page * a.kv.page_stride + ld.ch * a.kv.head_stride + slot * a.kv.slot_stride;
+        row = good ? page * a.kv.page_stride + ld.ch * a.kv.head_stride + slot * a.kv.slot_stride : 0;
         if (Q8)
-          srow = page * a.kv.scale_page_stride + ld.ch * a.kv.scale_head_stride +
-                 slot * a.kv.scale_slot_stride;
-        const bool wanted = (on >> (lane & 15)) & 1;
-        if (!good) {
-          if (wanted) set_error(a.err, DEV_ERR_BOUNDS);
-          row = srow = 0;
-        }
-        if (a.whole_pages) {
-          if (!good) on = 0;
-        } else {
-          if (!wanted) row = srow = 0;
-          on &= __ballot_sync(0xffffffffu, good);
-        }
+          srow = good ? page * a.kv.scale_page_stride + ld.ch * a.kv.scale_head_stride +
+                            slot * a.kv.scale_slot_stride
+                      : 0;
       }
-      const uint8_t *base = (is_v ? a.kv.v : a.kv.k);
-#pragma unroll
-      for (int i = 0; i < kKeys / kRowsAtOnce; ++i) {
+      const uint8_t *base = is_v ? a.kv.v : a.kv.k;
+      // 16-byte pieces are exchanged within a row so that the reads below hit
+      // all banks
+      const auto place_of = [&](int i) {
         const int r = i * kRowsAtOnce + my_row;
-        int64_t off;
-        if (a.whole_pages) off = row + my_off + i * kRowsAtOnce * a.kv.slot_stride;
-        else off = __shfl_sync(0xffffffffu, row, r) + my_piece * 16;
-        // pieces are exchanged within a row so that the reads below hit all banks
         int q = my_piece;
         if (S::kPieces >= 8) q ^= is_v ? (r & 6) : ((r & 1) << 2);
         else if (is_v) q ^= (r >> 1) & 3;
-        const bool take = (on >> r) & 1;
-        copy16(dst + r * S::kRowBytes + q * 16, base + (take ? off : 0), take);
+        return dst + r * S::kRowBytes + q * 16;
+      };
+      if (a.whole_pages && on == kAll) {  // each 16 keys lie in one page
+#pragma unroll
+        for (int t = 0; t < KM; ++t) {
+          const uint8_t *p = base + __shfl_sync(0xffffffffu, row, 16 * t) + my_off;
+#pragma unroll
+          for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
+            copy16(place_of(t * (16 / kRowsAtOnce) + i), p);
+            p += row_step;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kKeys / kRowsAtOnce; ++i) {
+          const int r = i * kRowsAtOnce + my_row;
+          copy16(place_of(i), base + __shfl_sync(0xffffffffu, row, r) + my_piece * 16, (on >> r) & 1);
+        }
       }
       if (Q8 && !is_v) {  // both scales of a key come with its key row
-        const int r = lane & 15;
-        const bool take = (on >> r) & 1;
-        const float *from = lane < kKeys ? a.kv.k_scale : a.kv.v_scale;
-        const int64_t at = a.whole_pages ? srow + r * a.kv.scale_slot_stride : srow;
-        copy4(ring + stage * S::kStage + 2 * S::kHalfTile + 4 * lane, from + (take ? at : 0), take);
+        const uint32_t sdst = ring + stage * S::kStage + 2 * S::kHalfTile + 4 * my_key;
+        const bool take = (on >> my_key) & 1;
+        if (kKeys == 32 || lane < kKeys) copy4(sdst, a.kv.k_scale + srow, take);
+        if (kKeys == 32 || lane >= kKeys) copy4(sdst + 4 * kKeys, a.kv.v_scale + srow, take);
       }
     }
     copy_commit();
@@ -444,84 +488,120 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) decode_kernel(const __grid_
     }
   };
 
-  // ---- one tile of 16 keys
-  // Raw scores of keys g (values 0, 1) and g + 8 (2, 3), and those keys'
-  // scales (vs: log2): after this the stage's key rows and scales are free.
-  auto scores = [&](int stage, float (&s)[NT][4], float (&ks)[2], float (&vs)[2]) {
+  // ---- one tile of a warp
+  // Raw scores, and the keys' scales (vs: log2): value i of step t is key
+  // 16t + g + 8 (i / 2).  After this the stage's key rows and scales are free.
+  auto scores = [&](int stage, float (&s)[KM][NT][4], float (&ks)[KM][2], float (&vs)[KM][2]) {
     const uint32_t base = ring + stage * S::kStage;
     if (Q8) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const uint32_t at = base + 2 * S::kHalfTile + 4 * (g + 8 * t);
-        ks[t] = lds4(at);
-        vs[t] = lg2(lds4(at + 4 * kKeys));
-      }
+      for (int t = 0; t < KM; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t at = base + 2 * S::kHalfTile + 4 * (16 * t + g + 8 * u);
+          ks[t][u] = lds4(at);
+          vs[t][u] = lg2(lds4(at + 4 * kKeys));
+        }
     }
-    // two chains of sums per column of heads
-    float z[NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int t = 0; t < KM; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] = z[n][i] = 0.f;
-    const int swz = S::kPieces >= 8 ? (g & 1) << 2 : 0;  // the same for rows g and g + 8
-    const uint32_t row0 = base + g * S::kRowBytes, row1 = row0 + 8 * S::kRowBytes;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[t][n][i] = 0.f;
+    const int swz = S::kPieces >= 8 ? (g & 1) << 2 : 0;  // the same for all of this lane's rows
+    const uint32_t row0 = base + g * S::kRowBytes;
 #pragma unroll
     for (int i = 0; i < S::kPieces / 4; ++i) {
-      const uint4 k0 = lds16(row0 + (((c + 4 * i) ^ swz) << 4));
-      const uint4 k1 = lds16(row1 + (((c + 4 * i) ^ swz) << 4));
-      if (!Q8) {
+      const uint32_t at = row0 + (((c + 4 * i) ^ swz) << 4);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma16816<false>(s[n], k0.x, k1.x, k0.y, k1.y, qf[n][2 * i][0], qf[n][2 * i][1]);
-          mma16816<false>(z[n], k0.z, k1.z, k0.w, k1.w, qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
-        }
-      } else {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16(u4_word(k0, w), a0, a2);
-          e4m3x4_to_f16(u4_word(k1, w), a1, a3);
+      for (int t = 0; t < KM; ++t) {
+        const uint4 k0 = lds16(at + 16 * t * S::kRowBytes);
+        const uint4 k1 = lds16(at + (16 * t + 8) * S::kRowBytes);
+        if (!Q8) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            mma16816<true>(w & 1 ? z[n] : s[n], a0, a1, a2, a3, qf[n][4 * i + w][0], qf[n][4 * i + w][1]);
+            mma16816<false>(s[t][n], k0.x, k1.x, k0.y, k1.y, qf[n][2 * i][0], qf[n][2 * i][1]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma16816<false>(s[t][n], k0.z, k1.z, k0.w, k1.w, qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
+        } else {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16(u4_word(k0, w), a0, a2);
+            e4m3x4_to_f16(u4_word(k1, w), a1, a3);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816<true>(s[t][n], a0, a1, a2, a3, qf[n][4 * i + w][0], qf[n][4 * i + w][1]);
+          }
         }
       }
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] += z[n][i];
   };
-  // Weights of the tile's keys, transposed to (head g; keys 2c, 2c + 1) and
-  // (.., keys 8 + 2c, 9 + 2c): high parts, and what they leave.
-  auto weights = [&](float (&s)[NT][4], const float (&ks)[2], const float (&vs)[2],
-                     uint32_t (&p_hi)[NT][2], uint32_t (&p_lo)[NT][2]) {
+  // Weights of the tile's keys, transposed to (head g; keys 16t + 2c, + 1) and
+  // (.., keys 16t + 8 + 2c, + 1): high parts, and what they leave.
+  auto weights = [&](float (&s)[KM][NT][4], const float (&ks)[KM][2], const float (&vs)[KM][2],
+                     uint32_t (&p_hi)[KM][NT][2], uint32_t (&p_lo)[KM][NT][2]) {
     const int base = key_of(cu);
-    const bool edge = base < cu.s.lo || base + kKeys > cu.s.hi;
+#pragma unroll
+    for (int t = 0; t < KM; ++t)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[t][n][i] *= Q8 ? qs[n][i & 1] * ks[t][i >> 1] : qs[n][i & 1];
+    if (!plain) {
+#pragma unroll
+      for (int t = 0; t < KM; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float x = s[t][n][i];
+            if (a.softcap > 0.f) x = cap2 * tanh_f32(x);
+            const int key = base + 16 * t + g + 8 * (i >> 1);
+            s[t][n][i] = fmaf(sl[n][i & 1], (float)(key - (cu.s.hi - 1)), x);
+          }
+    }
+    if (base < cu.s.lo || base + kKeys > cu.s.hi) {
+#pragma unroll
+      for (int t = 0; t < KM; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = base + 16 * t + g + 8 * (i >> 1);
+          if (key < cu.s.lo || key >= cu.s.hi) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[t][n][i] = -INFINITY;
+          }
+        }
+    }
     bool high = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x = s[n][i] * qs[n][i & 1];
-        if (Q8) x *= ks[i >> 1];
-        const int key = base + g + 8 * (i >> 1);
-        if (!plain) {
-          if (a.softcap > 0.f) x = cap2 * tanh_f32(x);
-          x = fmaf(sl[n][i & 1], (float)(key - (cu.s.hi - 1)), x);
+      for (int u = 0; u < 2; ++u) {
+        float top = fmaxf(s[0][n][u], s[0][n][2 + u]);
+        if (KM == 2) top = fmaxf(top, fmaxf(s[KM - 1][n][u], s[KM - 1][n][2 + u]));
+        high |= top > m[n][u] + kLag;
+        if (Q8) {
+          top = fmaxf(s[0][n][u] + vs[0][0], s[0][n][2 + u] + vs[0][1]);
+          if (KM == 2) top = fmaxf(top, fmaxf(s[KM - 1][n][u] + vs[KM - 1][0], s[KM - 1][n][2 + u] + vs[KM - 1][1]));
+          high |= top > mv[n][u] + kLag;
         }
-        if (edge && (key < cu.s.lo || key >= cu.s.hi)) x = -INFINITY;
-        s[n][i] = x;
-        high |= x > m[n][i & 1] + kLag;
-        if (Q8) high |= x + vs[i >> 1] > mv[n][i & 1] + kLag;
       }
     if (__any_sync(0xffffffffu, high)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          float top = fmaxf(s[n][u], s[n][2 + u]), top_v = 0.f;
-          if (Q8) top_v = fmaxf(s[n][u] + vs[0], s[n][2 + u] + vs[1]);
+          float top = -INFINITY, top_v = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < KM; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              top = fmaxf(top, s[t][n][2 * i + u]);
+              if (Q8) top_v = fmaxf(top_v, s[t][n][2 * i + u] + vs[t][i]);
+            }
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) {
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -545,66 +625,73 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) decode_kernel(const __grid_
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float p[4];
+      float zero[2], zero_v[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float zero = m[n][i & 1] == -INFINITY ? 0.f : m[n][i & 1];
-        p[i] = ex2(s[n][i] - zero);
-        l[n][i & 1] += p[i];
-        if (Q8) {
-          const float zero_v = (mv[n][i & 1] == -INFINITY ? 0.f : mv[n][i & 1]) - kWeightBits;
-          p[i] = ex2(s[n][i] + vs[i >> 1] - zero_v);
-        }
+      for (int u = 0; u < 2; ++u) {
+        zero[u] = m[n][u] == -INFINITY ? 0.f : m[n][u];
+        if (Q8) zero_v[u] = (mv[n][u] == -INFINITY ? 0.f : mv[n][u]) - kWeightBits;
       }
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const uint32_t hi = pack2<Q8>(p[2 * t], p[2 * t + 1]);
-        p_hi[n][t] = transpose8(hi);
-        if (!Q8) p_lo[n][t] = transpose8(pack2_rest(p[2 * t], p[2 * t + 1], hi));
+      for (int t = 0; t < KM; ++t) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[i] = ex2(s[t][n][i] - zero[i & 1]);
+          l[n][i & 1] += p[i];
+          if (Q8) p[i] = ex2(s[t][n][i] + (vs[t][i >> 1] - zero_v[i & 1]));
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t hi = pack2<Q8>(p[2 * u], p[2 * u + 1]);
+          p_hi[t][n][u] = transpose8(hi);
+          if (!Q8) p_lo[t][n][u] = transpose8(pack2_rest(p[2 * u], p[2 * u + 1], hi));
+        }
       }
     }
   };
-  auto add_values = [&](int stage, const uint32_t (&p_hi)[NT][2], const uint32_t (&p_lo)[NT][2]) {
+  auto add_values = [&](int stage, const uint32_t (&p_hi)[KM][NT][2], const uint32_t (&p_lo)[KM][NT][2]) {
     const uint32_t vb = ring + stage * S::kStage + S::kHalfTile;
 #pragma unroll
-    for (int h = 0; h < S::H; ++h) {
-      uint4 v[4];
+    for (int t = 0; t < KM; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 2 * c + (i & 1) + 8 * (i >> 1);
-        const uint32_t row_at = vb + r * S::kRowBytes;
-        if (S::kPieces >= 8) {
-          v[i] = lds16(row_at + (((g + 8 * h) ^ (r & 6)) << 4));
-        } else {  // rows of 64 bytes, half a piece per lane
-          const uint2 x = lds8(row_at + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + 8 * (g & 1));
-          v[i] = make_uint4(x.x, x.y, 0, 0);
-        }
-      }
+      for (int h = 0; h < S::H; ++h) {
+        uint4 v[4];
 #pragma unroll
-      for (int w = 0; w < (Q8 ? EV / 4 : 4); ++w) {
-        const uint32_t v0 = u4_word(v[0], w), v1 = u4_word(v[1], w), v2 = u4_word(v[2], w),
-                       v3 = u4_word(v[3], w);
-        if (!Q8) {  // columns 2w, 2w + 1 of the piece, keys paired
-          const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
-          const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma16816<false>(o[n][4 * h + w], a0, a1, a2, a3, p_hi[n][0], p_hi[n][1]);
-            mma16816<false>(o[n][4 * h + w], a0, a1, a2, a3, p_lo[n][0], p_lo[n][1]);
-          }
-        } else {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {  // columns 4w + 2u, + 1
-            uint32_t a0, a1, a2, a3;
-            e4m3x4_to_f16(__byte_perm(v0, v1, u ? 0x7362 : 0x5140), a0, a1);
-            e4m3x4_to_f16(__byte_perm(v2, v3, u ? 0x7362 : 0x5140), a2, a3);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma16816<true>(o[n][EV / 2 * h + 2 * w + u], a0, a1, a2, a3, p_hi[n][0], p_hi[n][1]);
+        for (int i = 0; i < 4; ++i) {
+          const int r = 2 * c + (i & 1) + 8 * (i >> 1);  // r & 6 is 2c for all four
+          const uint32_t row_at = vb + (16 * t + r) * S::kRowBytes;
+          if (S::kPieces >= 8) {
+            v[i] = lds16(row_at + (((g + 8 * h) ^ (2 * c)) << 4));
+          } else {  // rows of 64 bytes, half a piece per lane
+            const uint2 x = lds8(row_at + (((g >> 1) ^ c) << 4) + 8 * (g & 1));
+            v[i] = make_uint4(x.x, x.y, 0, 0);
           }
         }
+#pragma unroll
+        for (int w = 0; w < (Q8 ? EV / 4 : 4); ++w) {
+          const uint32_t v0 = u4_word(v[0], w), v1 = u4_word(v[1], w), v2 = u4_word(v[2], w),
+                         v3 = u4_word(v[3], w);
+          if (!Q8) {  // columns 2w, 2w + 1 of the piece, keys paired
+            const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
+            const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816<false>(o[n][4 * h + w], a0, a1, a2, a3, p_hi[t][n][0], p_hi[t][n][1]);
+              mma16816<false>(o[n][4 * h + w], a0, a1, a2, a3, p_lo[t][n][0], p_lo[t][n][1]);
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {  // columns 4w + 2u, + 1
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16(__byte_perm(v0, v1, u ? 0x7362 : 0x5140), a0, a1);
+              e4m3x4_to_f16(__byte_perm(v2, v3, u ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma16816<true>(o[n][EV / 2 * h + 2 * w + u], a0, a1, a2, a3, p_hi[t][n][0], p_hi[t][n][1]);
+            }
+          }
+        }
       }
-    }
   };
 
   // ---- end of a segment, or of this CTA's piece of it
@@ -618,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) decode_kernel(const __grid_
     *reinterpret_cast<uint2 *>(a.out + bh * D + 4 * item) = w;
     if (item == 0 && a.lse) a.lse[bh] = (mm + log2f(ll)) * kLn2;
   };
-  auto finish_segment = [&](int64_t seg0, int64_t seg1) {
+  auto finish_segment = [&](uint32_t seg0, uint32_t seg1) {
     const int in_kv = cu.hg * a.group, heads = min(a.group, G - in_kv);
     const int head0 = cu.ch * G + in_kv;
 #pragma unroll
@@ -648,8 +735,8 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) decode_kernel(const __grid_
     // which CTAs hold pieces of this segment
     int first = blockIdx.x, pieces = 1;
     if (seg0 < t0 || seg1 > t1) {
-      first = (int)(((seg0 + 1) * n_ctas - 1) / W);
-      pieces = (int)((seg1 * n_ctas - 1) / W) - first + 1;
+      first = (int)cut.owner(seg0);
+      pieces = (int)cut.owner(seg1 - 1) - first + 1;
     }
     const int items = heads * (D / 4);
     float4 *part = reinterpret_cast<float4 *>(a.part);
@@ -702,23 +789,22 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) decode_kernel(const __grid_
           const int h = i / (D / 4), it = i % (D / 4);
           float mm = -INFINITY, ll = 0.f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int p = 0; p < n; p += 4) {
-            float2 s[4];
-            float4 x[4];
+          for (int p = 0; p < n; p += kBatch) {
+            float2 s[kBatch];
+            float4 x[kBatch];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const bool on = p + k < n;
-              const int64_t at = (int64_t)slot_of(p0 + (on ? p + k : 0) * step) * a.group + h;
-              s[k] = __ldcg(part_ml + at);
-              x[k] = __ldcg(part + at * (D / 4) + it);
-              if (!on) {
-                s[k] = make_float2(-INFINITY, 0.f);
-                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < kBatch; ++k) {
+              s[k] = make_float2(-INFINITY, 0.f);
+              x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (p + k < n) {
+                const int64_t at = (int64_t)slot_of(p0 + (p + k) * step) * a.group + h;
+                s[k] = __ldcg(part_ml + at);
+                x[k] = __ldcg(part + at * (D / 4) + it);
               }
             }
             float top = mm;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) top = fmaxf(top, s[k].x);
+            for (int k = 0; k < kBatch; ++k) top = fmaxf(top, s[k].x);
             const float f0 = rescale(mm, top);
             ll *= f0;
             v.x *= f0;
@@ -727,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) decode_kernel(const __grid_
             v.w *= f0;
             mm = top;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kBatch; ++k) {
               const float f = rescale(s[k].x, top);
               ll = fmaf(f, s[k].y, ll);
               v.x = fmaf(f, x[k].x, v.x);
@@ -763,26 +849,34 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) decode_kernel(const __grid_
     __syncthreads();  // the merge buffer is free again
   };
 
+  start_segment();
   int stage = 0;
   for (int i = 0; i < n_tiles; ++i) {
-    if (i == 0 || cu.tile == 0) start_segment();
-    const bool on = touches(cu);
-    uint32_t p_hi[NT][2], p_lo[NT][2];
-    float s[NT][4], ks[2], vs[2];
+    const bool busy = touches(cu);
+    uint32_t p_hi[KM][NT][2], p_lo[KM][NT][2];
+    float s[KM][NT][4], ks[KM][2], vs[KM][2];
     copy_wait<2 * NS - 1>();  // the key rows
     __syncwarp();
-    if (on) scores(stage, s, ks, vs);
+    if (busy) scores(stage, s, ks, vs);
     __syncwarp();
     load_half(stage, false);
-    if (on) weights(s, ks, vs, p_hi, p_lo);
+    if (busy) weights(s, ks, vs, p_hi, p_lo);
     copy_wait<2 * NS - 1>();  // the value rows
     __syncwarp();
-    if (on) add_values(stage, p_hi, p_lo);
+    if (busy) add_values(stage, p_hi, p_lo);
     __syncwarp();
     load_half(stage, true);
-    if (cu.tile == cu.s.n - 1 || i == n_tiles - 1)
-      finish_segment(t0 + i - cu.tile, t0 + i - cu.tile + cu.s.n);
-    if (i + 1 < n_tiles) cu.next(a);
+    const bool last = i == n_tiles - 1;
+    if (last || cu.tile == cu.s.n - 1) {
+      const uint32_t seg0 = t0 + i - cu.tile;
+      finish_segment(seg0, seg0 + cu.s.n);
+      if (!last) {
+        cu.next(a);
+        start_segment();
+      }
+    } else {
+      cu.next(a);
+    }
     stage = stage + 1 == NS ? 0 : stage + 1;
   }
   copy_wait<0>();
@@ -790,14 +884,15 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) decode_kernel(const __grid_
 
 template <class S>
 cudaError_t launch_shape(const DecodeArgs &a, int grid, cudaStream_t s) {
-  decode_kernel<S><<<grid, kThreads, S::kSmem, s>>>(a);
+  decode_kernel<S><<<grid, S::kThreads, S::kSmem, s>>>(a);
   return cudaGetLastError();
 }
 template <class S>
-cudaError_t plan_shape(int *ctas_per_sm) {
+cudaError_t plan_shape(int *ctas_per_sm, int *tile) {
+  *tile = S::kTile;
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_kernel<S>, kThreads, S::kSmem);
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_kernel<S>, S::kThreads, S::kSmem);
 }
 
 // Calls f with the shape of (d, e4m3, heads of a group).
@@ -806,14 +901,14 @@ cudaError_t with_shape(int d, bool e4m3, int group, F f) {
   const bool wide = group > 8;
   switch (d) {
     case 64:
-      if (e4m3) return wide ? f(Shape<64, true, 16, 4, 3>{}) : f(Shape<64, true, 8, 4, 4>{});
-      return wide ? f(Shape<64, false, 16, 3, 3>{}) : f(Shape<64, false, 8, 3, 4>{});
+      if (e4m3) return wide ? f(Shape<64, true, 16, 2, 8, 2, 1>{}) : f(Shape<64, true, 8, 2, 4, 2, 3>{});
+      return wide ? f(Shape<64, false, 16, 2, 8, 2, 1>{}) : f(Shape<64, false, 8, 2, 4, 2, 3>{});
     case 128:
-      if (e4m3) return wide ? f(Shape<128, true, 16, 3, 2>{}) : f(Shape<128, true, 8, 3, 3>{});
-      return wide ? f(Shape<128, false, 16, 2, 2>{}) : f(Shape<128, false, 8, 2, 2>{});
+      if (e4m3) return wide ? f(Shape<128, true, 16, 2, 8, 2, 1>{}) : f(Shape<128, true, 8, 2, 4, 2, 2>{});
+      return wide ? f(Shape<128, false, 16, 2, 8, 1, 1>{}) : f(Shape<128, false, 8, 2, 4, 1, 2>{});
     case 256:
-      if (e4m3) return wide ? f(Shape<256, true, 16, 2, 1>{}) : f(Shape<256, true, 8, 2, 2>{});
-      return wide ? f(Shape<256, false, 16, 1, 1>{}) : f(Shape<256, false, 8, 1, 2>{});
+      if (e4m3) return wide ? f(Shape<256, true, 16, 1, 8, 1, 1>{}) : f(Shape<256, true, 8, 2, 4, 1, 2>{});
+      return wide ? f(Shape<256, false, 16, 1, 4, 1, 1>{}) : f(Shape<256, false, 8, 1, 4, 1, 2>{});
     default: return cudaErrorInvalidValue;
   }
 }
@@ -833,13 +928,11 @@ void decode_page_division(DecodeArgs *a) {
   while ((UINT64_C(1) << k) < d) ++k;
   a->page_mul = (uint32_t)((UINT64_C(1) << (31 + k)) / d + 1);
   a->page_shift = 31 + k;
-  a->whole_pages = d % kKeys == 0;
+  a->whole_pages = d % 16 == 0;
 }
 
-int64_t decode_tiles(int64_t positions) { return (positions + kTile - 1) / kTile; }
-
-cudaError_t plan_paged_decode(int d, bool e4m3, int group, int *ctas_per_sm) {
-  return with_shape(d, e4m3, group, [&](auto s) { return plan_shape<decltype(s)>(ctas_per_sm); });
+cudaError_t plan_paged_decode(int d, bool e4m3, int group, int *ctas_per_sm, int *tile) {
+  return with_shape(d, e4m3, group, [&](auto s) { return plan_shape<decltype(s)>(ctas_per_sm, tile); });
 }
 
 cudaError_t launch_paged_decode(const DecodeArgs &a, int d, bool e4m3, int grid, cudaStream_t s) {

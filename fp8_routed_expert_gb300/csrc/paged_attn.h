@@ -93,11 +93,9 @@ struct DecodeArgs {
 int decode_group(int heads_per_kv);
 // Fills in page_mul, page_shift and whole_pages.
 void decode_page_division(DecodeArgs *a);
-// Tiles of the split that `positions` positions fill.
-int64_t decode_tiles(int64_t positions);
-// Readies the kernel and tells how many CTAs of it fit on an SM; grid: at most
-// max_ctas, and not more than there are tiles at the longest lengths.
-cudaError_t plan_paged_decode(int d, bool e4m3, int group, int *ctas_per_sm);
+// Readies the kernel; tells how many CTAs of it fit on an SM, and the positions
+// of a tile.  Launches take at most max_ctas CTAs and need fewer than 2^31 tiles.
+cudaError_t plan_paged_decode(int d, bool e4m3, int group, int *ctas_per_sm, int *tile);
 cudaError_t launch_paged_decode(const DecodeArgs &a, int d, bool e4m3, int grid, cudaStream_t s);
 
 }  // namespace fp8moe
