@@ -14,6 +14,7 @@ using namespace fp8moe;
 struct moe_attn {
   moe_attn_config cfg{};
   char *ws = nullptr;         // one allocation, the views below
+  int sms = 0;                // of the device
   int *err = nullptr;
   uint64_t *turns = nullptr;  // [rope_dim / 2]
   // moe_attn_decode: CTAs of a launch and positions of a tile (by format), workspace
@@ -133,7 +134,9 @@ int check_T(const moe_attn *a, int64_t T) {
     if (rc_ != MOE_OK) return rc_; \
   } while (0)
 
-int run_rows(moe_attn *a, const RowArgs &r, cudaStream_t s) {
+int run_rows(moe_attn *a, RowArgs &r, cudaStream_t s) {
+  r.sms = a->sms;
+  r.err = a->err;
   ATTN_TRY(cudaSetDevice(a->cfg.device));
   a->last_stream = s;
   ATTN_TRY(launch_rows(r, a->cfg.head_dim, s));
@@ -164,6 +167,7 @@ int moe_attn_init(moe_attn **out, const moe_attn_config *cfg) {
   if (a == nullptr) return MOE_ERR_NOMEM;
   a->cfg = *cfg;
   a->cfg.rope_freqs = nullptr;  // the caller's array is not kept
+  a->sms = sms;
   const int use = cfg->max_sms > 0 && cfg->max_sms < sms ? cfg->max_sms : sms;
   a->group = decode_group(cfg->n_heads / cfg->n_kv_heads);
   for (int f = 0; f < 2; ++f) {
@@ -251,7 +255,6 @@ int moe_attn_norm_rope(moe_attn *a, const void *q, int64_t q_stride, const void 
   r.half = c.rope_dim / 2;
   r.interleaved = c.interleaved;
   r.eps = eps;
-  r.err = a->err;
   return run_rows(a, r, static_cast<cudaStream_t>(stream));
 }
 
@@ -289,7 +292,6 @@ int moe_attn_append(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   r.eps = eps;
   r.cache = true;
   r.e4m3 = kv->format == MOE_KV_E4M3;
-  r.err = a->err;
   return run_rows(a, r, static_cast<cudaStream_t>(stream));
 }
 
@@ -311,7 +313,6 @@ int moe_attn_write(moe_attn *a, const moe_paged_kv *kv, const void *k, int64_t k
   r.slots = slots;
   r.cache = true;
   r.e4m3 = kv->format == MOE_KV_E4M3;
-  r.err = a->err;
   return run_rows(a, r, static_cast<cudaStream_t>(stream));
 }
 
@@ -332,6 +333,7 @@ int moe_attn_read(moe_attn *a, const moe_paged_kv *kv, const int64_t *slots, int
   r.n_kv = c.n_kv_heads;
   r.k_out = {static_cast<__nv_bfloat16 *>(k_out), k_out_stride};
   r.v_out = {static_cast<__nv_bfloat16 *>(v_out), v_out_stride};
+  r.sms = a->sms;
   r.err = a->err;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   ATTN_TRY(cudaSetDevice(c.device));

@@ -67,184 +67,295 @@ __device__ __forceinline__ int e4m3_row_exponent(float amax) {
   return e < -126 ? -126 : e;
 }
 
-// Where a token's rows go: page and slot within it, or page -1 for nowhere.
+// Where a token's rows go: byte offset of its row in key/value head 0, offset
+// of that row's scale; row < 0 for nowhere.
 struct Place {
-  int64_t page;
-  int slot;
+  int64_t row, scale;
 };
 __device__ __forceinline__ Place place_of(int64_t slot, const KvView &kv, int *err) {
   if (slot < 0) return Place{-1, 0};
-  Place p;
+  int64_t page;
+  int at;
   if (slot <= 0x7fffffff) {  // the usual case, without a 64-bit division
     const uint32_t q = (uint32_t)slot / (uint32_t)kv.page_size;
-    p = Place{(int64_t)q, (int)((uint32_t)slot - q * (uint32_t)kv.page_size)};
+    page = q;
+    at = (int)((uint32_t)slot - q * (uint32_t)kv.page_size);
   } else {
-    p.page = slot / kv.page_size;
-    p.slot = (int)(slot - p.page * kv.page_size);
+    page = slot / kv.page_size;
+    at = (int)(slot - page * kv.page_size);
   }
-  if (p.page >= kv.n_pages) {
+  if (page >= kv.n_pages) {
     set_error(err, DEV_ERR_BOUNDS);
     return Place{-1, 0};
   }
-  return p;
+  return Place{page * kv.page_stride + at * kv.slot_stride,
+               page * kv.scale_page_stride + at * kv.scale_slot_stride};
 }
 
-// One CTA per (token, block of rows): grid (T, row blocks).
+// How a launch cuts T tokens of n_rows rows each over CTAs that take at most
+// kDepth rows per group of lanes: `tokens` whole tokens per CTA, or (tokens ==
+// 1) `rows` rows of one token, the others in further CTAs along y.
+constexpr int kDepth = 4;       // rows of a lane group, all loaded before the first is used
+constexpr int kMaxTokens = 8;
+struct RowCut {
+  int tokens, rows;
+  uint32_t mul;  // item / n_rows = item * mul >> 20 for items of several tokens
+};
 template <int D>
-__global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowArgs a, int rows_per_cta) {
-  constexpr int L = D / 8, kRows = kRowThreads / L;
-  __shared__ float2 turn[D / 2];  // (cos, sin) of the token's angles
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x % L, slot0 = threadIdx.x / L;
-  const int n_rows = a.n_q + a.n_k + a.n_v;
-  const int r0 = blockIdx.y * rows_per_cta;
-  const int r1 = min(r0 + rows_per_cta, n_rows);
-  if (a.half > 0) {
-    const uint64_t pos = (uint64_t)(int64_t)a.positions[t];
-    for (int i = threadIdx.x; i < a.half; i += kRowThreads) {
-      // signed fraction of a turn in [-1/2, 1/2), as half turns for sincospi
-      const float x = (float)(int64_t)(pos * a.turns[i]) * 0x1p-63f;
-      float s, c;
-      sincospif(x, &s, &c);
-      turn[i] = make_float2(c, s);
+RowCut cut_rows(int64_t T, int n_rows, int sms) {
+  constexpr int kRows = kRowThreads / (D / 8);
+  const int64_t want = 2 * (int64_t)sms;  // CTAs that keep every SM busy
+  RowCut c{1, kRows, 0};
+  int depth = kDepth;
+  while (depth > 1 && T * ((n_rows + depth * kRows - 1) / (depth * kRows)) < want) depth /= 2;
+  c.rows = depth * kRows;
+  if (n_rows <= c.rows) {
+    c.rows = n_rows;
+    int64_t n = kDepth * kRows / n_rows;
+    if (n > kMaxTokens) n = kMaxTokens;
+    if (n > T / want) n = T / want;
+    if (n > 1) {
+      c.tokens = (int)n;
+      c.mul = ((1u << 20) + n_rows - 1) / n_rows;  // exact while items * n_rows < 2^20
     }
   }
-  const Place at = a.cache ? place_of(a.slots[t], a.kv, a.err) : Place{-1, 0};
+  return c;
+}
+
+// Grid (token groups, row blocks); items of a CTA: (token, row).  Bound by HBM:
+// every row is read and written once, a lane's rows are all in flight before
+// the angles are computed, and the angles of a token are computed once for all
+// its heads.
+template <int D>
+__global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_constant__ RowArgs a,
+                                                                const RowCut cut) {
+  constexpr int L = D / 8, kRows = kRowThreads / L;
+  // cos and sin of the tokens' angles, pieces of four swapped so that lanes 32
+  // bytes apart use all banks
+  __shared__ __align__(16) float cs[kMaxTokens][2][D / 2];
+  __shared__ Place at[kMaxTokens];
+  const int lane = threadIdx.x % L, slot0 = threadIdx.x / L;
+  const int n_rows = a.n_q + a.n_k + a.n_v;
+  const int64_t t_base = (int64_t)blockIdx.x * cut.tokens;
+  const int tokens = (int)min((int64_t)cut.tokens, a.T - t_base);
+  const int r_base = blockIdx.y * cut.rows;
+  const int items = cut.tokens > 1 ? tokens * n_rows : min(cut.rows, n_rows - r_base);
+  const auto token_of = [&](int i) { return cut.tokens > 1 ? (int)((i * cut.mul) >> 20) : 0; };
+  uint4 raw[kDepth];
+#pragma unroll
+  for (int k = 0; k < kDepth; ++k) {
+    const int i = slot0 + k * kRows;
+    raw[k] = make_uint4(0, 0, 0, 0);
+    if (i < items) {
+      const int tl = token_of(i), r = r_base + i - tl * n_rows;
+      const bool is_q = r < a.n_q, is_k = !is_q && r < a.n_q + a.n_k;
+      const int h = is_q ? r : (is_k ? r - a.n_q : r - a.n_q - a.n_k);
+      const RowsIn &in = is_q ? a.q : (is_k ? a.k : a.v);
+      raw[k] = *reinterpret_cast<const uint4 *>(in.p + (t_base + tl) * in.stride + h * D + lane * 8);
+    }
+  }
+  if (a.half > 0) {
+    for (int i = threadIdx.x; i < tokens * a.half; i += kRowThreads) {
+      const int tl = i / a.half, f = i - tl * a.half;
+      const uint64_t pos = (uint64_t)(int64_t)a.positions[t_base + tl];
+      // signed fraction of a turn in [-1/2, 1/2), as half turns for sincospi
+      const float x = (float)(int64_t)(pos * a.turns[f]) * 0x1p-63f;
+      float sn, cn;
+      sincospif(x, &sn, &cn);
+      const int piece = f / 4, place = (piece ^ ((piece >> 3) & 1)) * 4 + f % 4;
+      cs[tl][0][place] = cn;
+      cs[tl][1][place] = sn;
+    }
+  }
+  if (a.cache && threadIdx.x < tokens) at[threadIdx.x] = place_of(a.slots[t_base + threadIdx.x], a.kv, a.err);
   __syncthreads();
-  // every thread runs every iteration: the shuffles below take whole warps
-  for (int base = r0; base < r1; base += kRows) {
-    const int r = base + slot0;
-    const bool on = r < r1;
+  const int step = a.half / 8;  // lanes between the two halves of a rotated row
+  const bool second = lane >= step;
+  const int partner = (second ? lane - step : lane + step) & (L - 1);
+  const auto angles = [&](int tl, int which, int piece) {
+    return *reinterpret_cast<const float4 *>(&cs[tl][which][(piece ^ ((piece >> 3) & 1)) * 4]);
+  };
+#pragma unroll
+  for (int k = 0; k < kDepth; ++k) {
+    if (k * kRows >= items) break;  // the same for the whole CTA: shuffles take whole warps
+    const int i = slot0 + k * kRows;
+    const bool on = i < items;
+    const int tl = on ? token_of(i) : 0, r = r_base + i - tl * n_rows;
+    const int64_t t = t_base + tl;
     const bool is_q = r < a.n_q, is_k = !is_q && r < a.n_q + a.n_k;
     const int h = is_q ? r : (is_k ? r - a.n_q : r - a.n_q - a.n_k);
-    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (on) {
-      const RowsIn &in = is_q ? a.q : (is_k ? a.k : a.v);
-      unpack8(*reinterpret_cast<const uint4 *>(in.p + t * in.stride + h * D + lane * 8), y);
-    }
-    const float *w = is_q ? a.q_weight : (is_k ? a.k_weight : nullptr);
-    float ss = 0.f;
+    float y[8];
+    unpack8(raw[k], y);
+    if (a.q_weight != nullptr || a.k_weight != nullptr) {
+      float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
-    ss = row_sum<L>(ss);
-    if (w != nullptr) {
-      const float rms = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = y[i] * rms * w[lane * 8 + i];
+      for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
+      ss = row_sum<L>(ss);
+      const float *w = is_q ? a.q_weight : (is_k ? a.k_weight : nullptr);
+      if (w != nullptr) {
+        const float rms = __frsqrt_rn(fmaf(ss, 1.0f / D, a.eps));
+        const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w) + 2 * lane);
+        const float4 w1 = __ldg(reinterpret_cast<const float4 *>(w) + 2 * lane + 1);
+        y[0] = y[0] * rms * w0.x;
+        y[1] = y[1] * rms * w0.y;
+        y[2] = y[2] * rms * w0.z;
+        y[3] = y[3] * rms * w0.w;
+        y[4] = y[4] * rms * w1.x;
+        y[5] = y[5] * rms * w1.y;
+        y[6] = y[6] * rms * w1.z;
+        y[7] = y[7] * rms * w1.w;
+      }
     }
     if (a.half > 0) {
-      const int step = a.half / 8;  // lanes between the two halves
-      const bool second = lane >= step;
-      const int from = second ? lane - step : lane + step;
-      float z[8];
+      const bool turned = (is_q || is_k) && lane * 8 < 2 * a.half;
+      if (a.interleaved) {
+        if (turned) {
+          const float4 cn = angles(tl, 0, lane), sn = angles(tl, 1, lane);
+          const float cc[4] = {cn.x, cn.y, cn.z, cn.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = __shfl_sync(0xffffffffu, y[i], from & (L - 1), L);
-      if ((is_q || is_k) && lane * 8 < 2 * a.half) {
-        if (a.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 cs = turn[lane * 4 + i];
-            const float u = y[2 * i], v = y[2 * i + 1];
-            y[2 * i] = u * cs.x - v * cs.y;
-            y[2 * i + 1] = v * cs.x + u * cs.y;
+          for (int j = 0; j < 4; ++j) {
+            const float u = y[2 * j], v = y[2 * j + 1];
+            y[2 * j] = u * cc[j] - v * ss[j];
+            y[2 * j + 1] = v * cc[j] + u * ss[j];
           }
-        } else {
+        }
+      } else {
+        float z[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 cs = turn[(second ? lane - step : lane) * 8 + i];
-            y[i] = second ? y[i] * cs.x + z[i] * cs.y : y[i] * cs.x - z[i] * cs.y;
+        for (int j = 0; j < 8; ++j) z[j] = __shfl_sync(0xffffffffu, y[j], partner, L);
+        if (turned) {
+          const int p = 2 * (second ? lane - step : lane);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float4 cn = angles(tl, 0, p + q), sn = angles(tl, 1, p + q);
+            const float cc[4] = {cn.x, cn.y, cn.z, cn.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float s1 = second ? ss[j] : -ss[j];
+              y[4 * q + j] = fmaf(z[4 * q + j], s1, y[4 * q + j] * cc[j]);
+            }
           }
         }
       }
     }
     if (is_q || !a.cache) {
       if (on) {
-        const RowsOut &o = is_q ? a.q_out : a.k_out;
-        *reinterpret_cast<uint4 *>(o.p + t * o.stride + h * D + lane * 8) = pack8(y);
+        const RowsOut &out = is_q ? a.q_out : a.k_out;
+        *reinterpret_cast<uint4 *>(out.p + t * out.stride + h * D + lane * 8) = pack8(y);
       }
       if (!a.cache || !a.e4m3) continue;
     }
-    uint8_t *rows = is_k ? a.kv.k : a.kv.v;
-    const int64_t off = at.page * a.kv.page_stride + h * a.kv.head_stride + at.slot * a.kv.slot_stride;
-    const bool store = on && !is_q && at.page >= 0;
+    const Place place = at[tl];
+    const bool store = on && !is_q && place.row >= 0;
+    uint8_t *row = (is_k ? a.kv.k : a.kv.v) + (store ? place.row + h * a.kv.head_stride : 0);
     if (!a.e4m3) {
-      if (store) *reinterpret_cast<uint4 *>(rows + off + lane * 16) = pack8(y);
+      if (store) *reinterpret_cast<uint4 *>(row + lane * 16) = pack8(y);
       continue;
     }
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float m = fabsf(y[i]);
+    for (int j = 0; j < 8; ++j) {
+      const float m = fabsf(y[j]);
       if (m < INFINITY) amax = fmaxf(amax, m);
-      else y[i] = NAN;  // an infinity has no code; a NaN stays one
+      else y[j] = NAN;  // an infinity has no code; a NaN stays one
     }
     amax = row_max<L>(amax);
-    const int e = e4m3_row_exponent(amax);
     if (store) {
-      const Pow2 down = pow2_factors(-e);
+      const int e = e4m3_row_exponent(amax);  // in [-126, 120]
+      const float down = exp2i(-e);
       uint32_t c[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        c[i] = __nv_cvt_float2_to_fp8x2(make_float2(down(y[2 * i]), down(y[2 * i + 1])),
+      for (int j = 0; j < 4; ++j)
+        c[j] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * j] * down, y[2 * j + 1] * down),
                                         __NV_SATFINITE, __NV_E4M3);
-      *reinterpret_cast<uint2 *>(rows + off + lane * 8) =
-          make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+      *reinterpret_cast<uint2 *>(row + lane * 8) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
       if (lane == 0)
-        (is_k ? a.kv.k_scale : a.kv.v_scale)[at.page * a.kv.scale_page_stride +
-                                             h * a.kv.scale_head_stride +
-                                             at.slot * a.kv.scale_slot_stride] = exp2i(e);
+        (is_k ? a.kv.k_scale : a.kv.v_scale)[place.scale + h * a.kv.scale_head_stride] = exp2i(e);
     }
   }
 }
 
-// Rows out of the cache: one CTA per token, a row's 8-element pieces over the
-// lanes.
+// Rows out of the cache, cut over CTAs like the rows in.
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kRowThreads) read_rows_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kRowThreads) read_rows_kernel(const __grid_constant__ ReadArgs a,
+                                                                const RowCut cut) {
   constexpr int L = D / 8, kRows = kRowThreads / L;
-  const int64_t t = blockIdx.x;
+  __shared__ Place at[kMaxTokens];
   const int lane = threadIdx.x % L, slot0 = threadIdx.x / L;
-  const Place at = place_of(a.slots[t], a.kv, a.err);
-  for (int r = slot0; r < 2 * a.n_kv; r += kRows) {
-    const bool is_k = r < a.n_kv;
-    const int h = is_k ? r : r - a.n_kv;
-    uint4 o = make_uint4(0, 0, 0, 0);
-    if (at.page >= 0) {
-      const uint8_t *row = (is_k ? a.kv.k : a.kv.v) + at.page * a.kv.page_stride +
-                           h * a.kv.head_stride + at.slot * a.kv.slot_stride;
-      if (!E4M3) {
-        o = *reinterpret_cast<const uint4 *>(row + lane * 16);
-      } else {
-        const float scale = (is_k ? a.kv.k_scale : a.kv.v_scale)[at.page * a.kv.scale_page_stride +
-                                                                 h * a.kv.scale_head_stride +
-                                                                 at.slot * a.kv.scale_slot_stride];
-        const uint2 c = *reinterpret_cast<const uint2 *>(row + lane * 8);
-        float f[8];
+  const int n_rows = 2 * a.n_kv;
+  const int64_t t_base = (int64_t)blockIdx.x * cut.tokens;
+  const int tokens = (int)min((int64_t)cut.tokens, a.T - t_base);
+  const int r_base = blockIdx.y * cut.rows;
+  const int items = cut.tokens > 1 ? tokens * n_rows : min(cut.rows, n_rows - r_base);
+  const auto token_of = [&](int i) { return cut.tokens > 1 ? (int)((i * cut.mul) >> 20) : 0; };
+  if (threadIdx.x < tokens) at[threadIdx.x] = place_of(a.slots[t_base + threadIdx.x], a.kv, a.err);
+  __syncthreads();
+  uint4 raw[kDepth];
+  float scale[kDepth];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = unpack_f16x2(e4m3x2_to_f16x2((i < 2 ? c.x : c.y) >> (16 * (i & 1))));
-          f[2 * i] = v.x * scale;
-          f[2 * i + 1] = v.y * scale;
+  for (int k = 0; k < kDepth; ++k) {
+    const int i = slot0 + k * kRows;
+    raw[k] = make_uint4(0, 0, 0, 0);
+    scale[k] = 0.f;
+    if (i < items) {
+      const int tl = token_of(i), r = r_base + i - tl * n_rows;
+      const bool is_k = r < a.n_kv;
+      const int h = is_k ? r : r - a.n_kv;
+      const Place place = at[tl];
+      if (place.row >= 0) {
+        const uint8_t *row = (is_k ? a.kv.k : a.kv.v) + place.row + h * a.kv.head_stride;
+        if (E4M3) {
+          const uint2 c = *reinterpret_cast<const uint2 *>(row + lane * 8);
+          raw[k].x = c.x;
+          raw[k].y = c.y;
+          scale[k] = (is_k ? a.kv.k_scale : a.kv.v_scale)[place.scale + h * a.kv.scale_head_stride];
+        } else {
+          raw[k] = *reinterpret_cast<const uint4 *>(row + lane * 16);
         }
-        o = pack8(f);
       }
     }
-    const RowsOut &out = is_k ? a.k_out : a.v_out;
-    *reinterpret_cast<uint4 *>(out.p + t * out.stride + h * D + lane * 8) = o;
   }
+#pragma unroll
+  for (int k = 0; k < kDepth; ++k) {
+    const int i = slot0 + k * kRows;
+    if (i >= items) break;
+    const int tl = token_of(i), r = r_base + i - tl * n_rows;
+    const bool is_k = r < a.n_kv;
+    const int h = is_k ? r : r - a.n_kv;
+    if (E4M3) {
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = unpack_f16x2(e4m3x2_to_f16x2((j < 2 ? raw[k].x : raw[k].y) >> (16 * (j & 1))));
+        f[2 * j] = v.x * scale[k];
+        f[2 * j + 1] = v.y * scale[k];
+      }
+      raw[k] = pack8(f);
+    }
+    const RowsOut &out = is_k ? a.k_out : a.v_out;
+    *reinterpret_cast<uint4 *>(out.p + (t_base + tl) * out.stride + h * D + lane * 8) = raw[k];
+  }
+}
+
+dim3 grid_of(const RowCut &c, int64_t T, int n_rows) {
+  return dim3((unsigned)((T + c.tokens - 1) / c.tokens),
+              c.tokens > 1 ? 1u : (unsigned)((n_rows + c.rows - 1) / c.rows));
 }
 
 template <int D>
 cudaError_t rows_of(const RowArgs &a, cudaStream_t s) {
   const int n_rows = a.n_q + a.n_k + a.n_v;
-  head_rows_kernel<D><<<dim3((unsigned)a.T, 1), kRowThreads, 0, s>>>(a, n_rows);
+  const RowCut c = cut_rows<D>(a.T, n_rows, a.sms);
+  head_rows_kernel<D><<<grid_of(c, a.T, n_rows), kRowThreads, 0, s>>>(a, c);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t read_of(const ReadArgs &a, cudaStream_t s) {
-  if (a.e4m3) read_rows_kernel<D, true><<<(unsigned)a.T, kRowThreads, 0, s>>>(a);
-  else read_rows_kernel<D, false><<<(unsigned)a.T, kRowThreads, 0, s>>>(a);
+  const RowCut c = cut_rows<D>(a.T, 2 * a.n_kv, a.sms);
+  const dim3 grid = grid_of(c, a.T, 2 * a.n_kv);
+  if (a.e4m3) read_rows_kernel<D, true><<<grid, kRowThreads, 0, s>>>(a, c);
+  else read_rows_kernel<D, false><<<grid, kRowThreads, 0, s>>>(a, c);
   return cudaGetLastError();
 }
 

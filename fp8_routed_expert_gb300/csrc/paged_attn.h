@@ -45,6 +45,7 @@ struct RowArgs {
   float eps;
   KvView kv;
   bool cache, e4m3;
+  int sms;  // of the device
   int *err;
 };
 cudaError_t launch_rows(const RowArgs &a, int d, cudaStream_t s);
@@ -56,6 +57,7 @@ struct ReadArgs {
   int64_t T;
   int n_kv;
   RowsOut k_out, v_out;
+  int sms;
   int *err;
 };
 cudaError_t launch_read(const ReadArgs &a, int d, cudaStream_t s);
