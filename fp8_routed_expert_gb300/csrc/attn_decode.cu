@@ -9,15 +9,19 @@
 // The launch reads each visible key and value row once and is bound by HBM;
 // the design keeps loads in flight and everything else out of their way.
 //
-// Split.  A sequence's visible positions are cut into tiles, a segment is the tiles of one (sequence, group of up to 16 query heads that share a
-// key/value head), and the list of all segments' tiles is cut evenly over the
-// CTAs, whatever the lengths: every CTA finds its piece from the lengths
-// themselves.  A CTA that holds a segment's whole list writes its result; the
-// pieces of a segment that several CTAs share go to the workspace as (m, l,
-// unnormalised output) and the last CTA to arrive joins them, in groups of 16
-// pieces, then the groups.  The order of a join's sums is fixed by the
-// pieces' places, so results do not depend on the order of arrival.  No CTA
-// waits for another.
+// Split.  A sequence's visible positions are cut into tiles, a segment is the
+// tiles of one (sequence, group of up to 16 query heads that share a key/value
+// head), and the list of all segments' tiles is cut evenly over the CTAs,
+// whatever the lengths: every CTA finds its piece from the lengths themselves.
+// In longer lists a segment counts one tile more, about what its start and end
+// cost, or the CTAs that got many short segments would be the last to finish
+// (64 sequences of up to 8192: 73 to 100 us at a median of 81 without it).
+// A CTA that holds a whole segment writes its result; the parts of a segment
+// that several CTAs share go to the workspace as (m, l, unnormalised output)
+// and the CTA whose part came last joins them when it is done with its own
+// piece, in groups of 16 parts, then the groups.  The order of a join's sums is
+// fixed by the parts' places, so results do not depend on the order of arrival.
+// No CTA waits for another.
 //
 // Tile.  Each warp takes 16 or 32 of a tile's keys through its own ring of
 // cp.async stages and keeps its own (m, l, output), so the loop
@@ -53,12 +57,15 @@ namespace {
 
 constexpr int kJoin = 16;              // pieces joined by one CTA
 constexpr int kBatch = 8;              // pieces whose loads are in flight together
+constexpr int kWeighFrom = 4;          // tiles per CTA from which on a segment counts one more
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLag = 8.f;            // log2 of the largest weight, before its scale
 constexpr float kWeightBits = 7.f;     // e4m3: weights are scaled by 2^7, to 2^15 at most
 
 // MH: query heads of a group at most; KM: 16-key steps of a warp's tile; NS:
 // stages of a warp's ring; CTAS: that fit on an SM.
+constexpr int kSharedBytes = 32;
+
 template <int D_, bool E4M3_, int MH_, int KM_, int kWarps_, int NS_, int CTAS_>
 struct Shape {
   static constexpr int D = D_, MH = MH_, KM = KM_, NS = NS_, CTAS = CTAS_;
@@ -76,7 +83,7 @@ struct Shape {
   static constexpr int H = D / (8 * EV);
   static constexpr int kMergeRow = D + 4;                     // floats; the odd pieces spread banks
   static constexpr int kMerge = kWarps * MH * kMergeRow * 4;  // f32 outputs of the warps
-  static constexpr int kSmem = kRing + kMerge + kWarps * MH * 8 + 16;
+  static constexpr int kSmem = kRing + kMerge + kWarps * MH * 8 + MH * D * 2 + 2 * kSharedBytes;
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
@@ -228,15 +235,23 @@ struct Cursor {
   }
 };
 
-// The even cut of W tiles over N CTAs: the first W % N take one more.
+// The even cut of W units over N CTAs: the first W % N take one more.
 struct Cut {
   uint32_t each, more;
   __device__ __forceinline__ Cut(uint32_t W, uint32_t N) : each(W / N), more(W % N) {}
   __device__ __forceinline__ uint32_t start(uint32_t cta) const { return each * cta + min(cta, more); }
-  __device__ __forceinline__ uint32_t owner(uint32_t tile) const {
+  __device__ __forceinline__ uint32_t owner(uint32_t unit) const {
     const uint32_t big = more * (each + 1);
-    return tile < big ? tile / (each + 1) : more + (tile - big) / each;
+    return unit < big ? unit / (each + 1) : more + (unit - big) / each;
   }
+};
+
+// A segment that other CTAs hold parts of, written to the workspace: it is
+// joined when this CTA is done, if its part was the last to arrive.
+struct Shared {
+  int b, ch, hg;
+  uint32_t first, parts, last;  // CTA of the first part, number of parts, whether to join
+  uint32_t unused[2];
 };
 
 template <class S>
@@ -249,11 +264,11 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
   const int g = lane >> 2, c = lane & 3;  // row and column of the matrix instructions
   float *merge = reinterpret_cast<float *>(smem + S::kRing);            // [warp][MH][kMergeRow]
   float2 *ml = reinterpret_cast<float2 *>(smem + S::kRing + S::kMerge);  // [warp][MH]
-  int *misc = reinterpret_cast<int *>(smem + S::kRing + S::kMerge + kWarps * MH * 8);
+  uint4 *qbuf = reinterpret_cast<uint4 *>(smem + S::kRing + S::kMerge + kWarps * MH * 8);  // [MH][D / 8]
+  Shared *shared = reinterpret_cast<Shared *>(qbuf + MH * D / 8);                         // [2]
+  static_assert(sizeof(Shared) == kSharedBytes, "two of them fit");
 
   // ---- this CTA's piece [t0, t1) of the W tiles of all sequences
-  uint32_t W, before;  // tiles of all sequences, and of those before this piece's first
-  Cursor<kTile> cu;
   const auto count = [&](int b, Span *sp) {
     const int len = a.lens[b];
     if (len < 0 || len > a.capacity) set_error(a.err, DEV_ERR_BOUNDS);
@@ -268,24 +283,47 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
     }
     return v;
   };
+  // The place of a unit: the tile it is or comes before, and the cursor there.
+  // `before`: tiles of the sequences before k.b, whose span is k.s.
+  uint32_t extra = 0;  // units of a segment beyond its tiles
+  const auto place = [&](uint32_t unit, uint32_t before, Cursor<kTile> &k) {
+    const uint32_t r = unit - before - extra * (uint32_t)(a.n_groups * k.b);
+    const int vh = (int)(r / (k.s.n + extra));
+    k.tile = (int)r - vh * (int)(k.s.n + extra);
+    k.ch = vh / a.groups_per_kv;
+    k.hg = vh - k.ch * a.groups_per_kv;
+    return before + vh * k.s.n + k.tile;
+  };
+  uint32_t W, t0, t1, n_ctas;
+  Cursor<kTile> cu;
   if (a.B <= 32) {  // a sequence per lane, every warp for itself
     Span sp{0, 0, 0, 0};
     const uint32_t n = lane < a.B ? count(lane, &sp) : 0;
     const uint32_t incl = scan(n);
     W = __shfl_sync(0xffffffffu, incl, 31);
-    const uint32_t N = min(W, gridDim.x);
-    if (blockIdx.x >= N) return;
-    const uint32_t t0 = Cut(W, N).start(blockIdx.x);
-    const uint32_t mask = __ballot_sync(0xffffffffu, incl > t0);
-    const int at = __ffs((int)mask) - 1;
-    before = __shfl_sync(0xffffffffu, incl - n, at);
-    cu.b = at;
-    cu.s.lo = __shfl_sync(0xffffffffu, sp.lo, at);
-    cu.s.hi = __shfl_sync(0xffffffffu, sp.hi, at);
-    cu.s.first = __shfl_sync(0xffffffffu, sp.first, at);
-    cu.s.n = __shfl_sync(0xffffffffu, sp.n, at);
+    n_ctas = min(W, gridDim.x);
+    if (blockIdx.x >= n_ctas) return;
+    extra = W >= kWeighFrom * gridDim.x ? 1 : 0;
+    const uint32_t units = W + extra * (uint32_t)(a.n_groups * a.B);
+    const Cut cut(units, n_ctas);
+    const uint32_t end = incl + extra * (uint32_t)(a.n_groups * (lane + 1));  // in units
+    const auto at = [&](uint32_t unit, Cursor<kTile> &k) {
+      const int b = __ffs((int)__ballot_sync(0xffffffffu, end > unit && lane < a.B)) - 1;
+      k.b = b;
+      k.s.lo = __shfl_sync(0xffffffffu, sp.lo, b);
+      k.s.hi = __shfl_sync(0xffffffffu, sp.hi, b);
+      k.s.first = __shfl_sync(0xffffffffu, sp.first, b);
+      k.s.n = __shfl_sync(0xffffffffu, sp.n, b);
+      return place(unit, __shfl_sync(0xffffffffu, incl - n, b), k);
+    };
+    t0 = at(cut.start(blockIdx.x), cu);
+    t1 = W;
+    if (blockIdx.x + 1 < n_ctas) {
+      Cursor<kTile> k;
+      t1 = at(cut.start(blockIdx.x + 1), k);
+    }
   } else {  // a run of sequences per thread
-    uint32_t *sums = reinterpret_cast<uint32_t *>(merge), *place = sums + kWarps;
+    uint32_t *sums = reinterpret_cast<uint32_t *>(merge), *found = sums + kWarps;
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
     Span sp;
@@ -299,36 +337,46 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
       if (w < warp) incl += sums[w];
       W += sums[w];
     }
-    const uint32_t N = min(W, gridDim.x);
-    if (blockIdx.x >= N) return;
-    const uint32_t t0 = Cut(W, N).start(blockIdx.x);
-    if (incl - mine <= t0 && t0 < incl) {
-      uint32_t at = incl - mine;
-      int b = b0;
-      for (;; ++b) {
-        const uint32_t n = (uint32_t)(span_of<kTile>(a, b).n * a.n_groups);
-        if (t0 < at + n) break;
-        at += n;
+    n_ctas = min(W, gridDim.x);
+    if (blockIdx.x >= n_ctas) return;
+    extra = W >= kWeighFrom * gridDim.x ? 1 : 0;
+    const uint32_t units = W + extra * (uint32_t)(a.n_groups * a.B);
+    const Cut cut(units, n_ctas);
+    const auto in_units = [&](uint32_t tiles, int b) { return tiles + extra * (uint32_t)(a.n_groups * b); };
+    for (int i = 0; i < 2; ++i) {  // the thread whose run holds it finds the first unit, and the next CTA's
+      const uint32_t unit = cut.start(blockIdx.x + i);
+      if (in_units(incl - mine, b0) <= unit && unit < in_units(incl, b1)) {
+        uint32_t at = incl - mine;
+        int b = b0;
+        for (;; ++b) {
+          const uint32_t n = (uint32_t)(span_of<kTile>(a, b).n * a.n_groups);
+          if (unit < in_units(at + n, b + 1)) break;
+          at += n;
+        }
+        found[2 * i] = b;
+        found[2 * i + 1] = at;
       }
-      place[0] = b;
-      place[1] = at;
     }
     __syncthreads();
-    cu.b = place[0];
-    before = place[1];
+    cu.b = found[0];
     cu.s = span_of<kTile>(a, cu.b);
+    t0 = place(cut.start(blockIdx.x), found[1], cu);
+    t1 = W;
+    if (blockIdx.x + 1 < n_ctas) {
+      Cursor<kTile> k;
+      k.b = found[2];
+      k.s = span_of<kTile>(a, k.b);
+      t1 = place(cut.start(blockIdx.x + 1), found[3], k);
+    }
     __syncthreads();  // the merge buffer is free again
   }
-  const uint32_t n_ctas = min(W, gridDim.x);
-  const Cut cut(W, n_ctas);
-  const uint32_t t0 = cut.start(blockIdx.x), t1 = cut.start(blockIdx.x + 1);
-  {
-    const int vh = (int)((t0 - before) / (uint32_t)cu.s.n);
-    cu.tile = (int)(t0 - before) - vh * cu.s.n;
-    cu.ch = vh / a.groups_per_kv;
-    cu.hg = vh - cu.ch * a.groups_per_kv;
+  if (t0 >= t1) return;  // a piece of nothing but a segment's end
+  if (cu.tile == cu.s.n) {  // it begins with one
+    --cu.tile;
+    cu.next(a);
   }
   const int n_tiles = (int)(t1 - t0);
+  const Cut cut(W + extra * (uint32_t)(a.n_groups * a.B), n_ctas);
   const int G = a.n_heads / a.n_kv;
 
   // ---- loads: the rows of a warp's keys, NS stages ahead of their use
@@ -424,6 +472,23 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
   float qs[NT][2], sl[NT][2];           // scale of a raw score, slope * log2(e)
   const float cap2 = a.softcap * kLog2e;
   const bool plain = !(a.softcap > 0.f) && a.slopes == nullptr;
+  // a segment's queries on their way to shared memory: loaded while the one
+  // before it is finished
+  constexpr int kQPieces = (MH * D / 8 + kThreads - 1) / kThreads;
+  const auto fetch_q = [&](const Cursor<kTile> &k, uint4 (&w)[kQPieces]) {
+    const int in_kv = k.hg * a.group, heads = min(a.group, G - in_kv);
+    const __nv_bfloat16 *q = a.q + (int64_t)k.b * a.q_stride + (int64_t)(k.ch * G + in_kv) * D;
+#pragma unroll
+    for (int i = 0; i < kQPieces; ++i) {
+      const int p = threadIdx.x + i * kThreads;
+      w[i] = p < heads * (D / 8) ? reinterpret_cast<const uint4 *>(q)[p] : make_uint4(0, 0, 0, 0);
+    }
+  };
+  const auto put_q = [&](const uint4 (&w)[kQPieces]) {
+#pragma unroll
+    for (int i = 0; i < kQPieces; ++i)
+      if ((int)threadIdx.x + i * kThreads < MH * (D / 8)) qbuf[threadIdx.x + i * kThreads] = w[i];
+  };
   auto start_segment = [&]() {
     const int in_kv = cu.hg * a.group;
     const int heads = min(a.group, G - in_kv), head0 = cu.ch * G + in_kv;
@@ -432,13 +497,12 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
       const int h = g + 8 * n;  // the head whose q this lane holds
-      const __nv_bfloat16 *qp = a.q + (int64_t)cu.b * a.q_stride + (int64_t)(head0 + h) * D;
       uint4 w[D / 32];
 #pragma unroll
       for (int s = 0; s < D / 32; ++s) {
         // bf16: piece c + 4s of 8 elements; e4m3: halves of piece c + 4 (s / 2) of 16
         const int at = Q8 ? (c + 4 * (s / 2)) * 16 + 8 * (s & 1) : (c + 4 * s) * 8;
-        w[s] = h < heads ? *reinterpret_cast<const uint4 *>(qp + at) : make_uint4(0, 0, 0, 0);
+        w[s] = qbuf[(h * D + at) / 8];
       }
       float unit = a.scale;
       if (!Q8) {
@@ -705,7 +769,21 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
     *reinterpret_cast<uint2 *>(a.out + bh * D + 4 * item) = w;
     if (item == 0 && a.lse) a.lse[bh] = (mm + log2f(ll)) * kLn2;
   };
-  auto finish_segment = [&](uint32_t seg0, uint32_t seg1) {
+  float4 *part = reinterpret_cast<float4 *>(a.part);
+  float2 *part_ml = reinterpret_cast<float2 *>(a.part_ml);
+  // a CTA's own slots: 0 for a segment that began before its piece, 1 otherwise
+  const auto slot_of = [&](int first, int nth) { return 2 * (first + nth) + (nth == 0 ? 1 : 0); };
+  // Thread 0: counts a part that all threads have written; true for the last.
+  const auto arrive = [&](int *counter, int n) {
+    __threadfence();
+    const bool last = atomicAdd(counter, 1) == n - 1;
+    if (last) *counter = 0;  // for the next call
+    __threadfence();
+    return last;
+  };
+  int n_shared = 0;
+  // Ends the segment of tiles [seg0, seg1), or this CTA's part of it; w: the next one's queries.
+  auto finish_segment = [&](uint32_t seg0, uint32_t seg1, const uint4 (&w)[kQPieces]) {
     const int in_kv = cu.hg * a.group, heads = min(a.group, G - in_kv);
     const int head0 = cu.ch * G + in_kv;
 #pragma unroll
@@ -732,18 +810,16 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
         }
       }
     __syncthreads();
-    // which CTAs hold pieces of this segment
-    int first = blockIdx.x, pieces = 1;
+    put_q(w);
+    // the CTAs that hold parts of this segment
+    int first = blockIdx.x, parts = 1;
     if (seg0 < t0 || seg1 > t1) {
-      first = (int)cut.owner(seg0);
-      pieces = (int)cut.owner(seg1 - 1) - first + 1;
+      const uint32_t ends = extra * (uint32_t)(cu.b * a.n_groups + cu.ch * a.groups_per_kv + cu.hg);
+      first = (int)cut.owner(seg0 + ends);
+      parts = (int)cut.owner(seg1 - 1 + ends) - first + 1;
     }
     const int items = heads * (D / 4);
-    float4 *part = reinterpret_cast<float4 *>(a.part);
-    float2 *part_ml = reinterpret_cast<float2 *>(a.part_ml);
-    // a CTA's own slots: 0 for a segment that began before its piece, 1 otherwise
-    auto slot_of = [&](int piece) { return 2 * (first + piece) + (piece == 0 ? 1 : 0); };
-    const int mine = slot_of(blockIdx.x - first);
+    const int mine = slot_of(first, blockIdx.x - first);
     for (int i = threadIdx.x; i < items; i += kThreads) {
       const int h = i / (D / 4), it = i % (D / 4);
       float mm = -INFINITY;
@@ -762,93 +838,99 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
         v.z = fmaf(f, x.z, v.z);
         v.w = fmaf(f, x.w, v.w);
       }
-      if (pieces == 1) {
+      if (parts == 1) {
         write_out(cu.b, head0 + h, it, v, mm, ll);
       } else {
         part[((int64_t)mine * a.group + h) * (D / 4) + it] = v;
         if (it == 0) part_ml[(int64_t)mine * a.group + h] = make_float2(mm, ll);
       }
     }
-    if (pieces > 1) {
-      // joins `n` pieces, every `step`-th from piece p0 on; true where this CTA arrived last
-      auto arrive = [&](int *counter, int n) {
-        __syncthreads();
-        if (threadIdx.x == 0) {
-          __threadfence();
-          const int before = atomicAdd(counter, 1);
-          const bool last = before == n - 1;
-          if (last) *counter = 0;  // for the next call
-          __threadfence();
-          misc[0] = last;
-        }
-        __syncthreads();
-        return misc[0] != 0;
-      };
-      auto join = [&](int p0, int step, int n, bool final) {
-        for (int i = threadIdx.x; i < items; i += kThreads) {
-          const int h = i / (D / 4), it = i % (D / 4);
-          float mm = -INFINITY, ll = 0.f;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int p = 0; p < n; p += kBatch) {
-            float2 s[kBatch];
-            float4 x[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              s[k] = make_float2(-INFINITY, 0.f);
-              x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (p + k < n) {
-                const int64_t at = (int64_t)slot_of(p0 + (p + k) * step) * a.group + h;
-                s[k] = __ldcg(part_ml + at);
-                x[k] = __ldcg(part + at * (D / 4) + it);
-              }
-            }
-            float top = mm;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) top = fmaxf(top, s[k].x);
-            const float f0 = rescale(mm, top);
-            ll *= f0;
-            v.x *= f0;
-            v.y *= f0;
-            v.z *= f0;
-            v.w *= f0;
-            mm = top;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              const float f = rescale(s[k].x, top);
-              ll = fmaf(f, s[k].y, ll);
-              v.x = fmaf(f, x[k].x, v.x);
-              v.y = fmaf(f, x[k].y, v.y);
-              v.z = fmaf(f, x[k].z, v.z);
-              v.w = fmaf(f, x[k].w, v.w);
-            }
-          }
-          if (final) {
-            write_out(cu.b, head0 + h, it, v, mm, ll);
-          } else {  // in place of the group's first piece, which only this thread has read ..
-            part[((int64_t)slot_of(p0) * a.group + h) * (D / 4) + it] = v;
-            if (it == 0) ml[h] = make_float2(mm, ll);  // .. except for its statistics
-          }
-        }
-        if (!final) {
-          __syncthreads();
-          for (int h = threadIdx.x; h < heads; h += kThreads)
-            part_ml[(int64_t)slot_of(p0) * a.group + h] = ml[h];
-        }
-      };
-      // Counters: a CTA is the first of at most one shared segment and a later
-      // piece's holder of at most one other, so three arrays by CTA do.
-      const int piece = blockIdx.x - first, grp = piece / kJoin;
-      const int p0 = grp * kJoin, in_grp = min(kJoin, pieces - p0);
-      const int groups = (pieces + kJoin - 1) / kJoin;
-      if (arrive(a.counters + (grp == 0 ? 0 : a.max_ctas) + first + p0, in_grp)) {
-        join(p0, 1, in_grp, groups == 1);
-        if (groups > 1 && arrive(a.counters + 2 * a.max_ctas + first, groups))
-          join(0, kJoin, groups, true);
+    __syncthreads();  // the part is written, and the merge buffer free again
+    if (parts > 1) {
+      if (threadIdx.x == 0) {
+        const int grp = (blockIdx.x - first) / kJoin, p0 = grp * kJoin;
+        shared[n_shared] = Shared{cu.b, cu.ch, cu.hg, (uint32_t)first, (uint32_t)parts,
+                                  arrive(a.counters + (grp == 0 ? 0 : a.max_ctas) + first + p0,
+                                         min(kJoin, parts - p0)), {0, 0}};
       }
+      ++n_shared;
     }
-    __syncthreads();  // the merge buffer is free again
+  };
+  // Joins this CTA's group of the segment's parts, then, if that was the last
+  // group, the groups.  Counters: a CTA is the first of at most one shared
+  // segment and a later one of at most one other, so three arrays by CTA do.
+  auto join_shared = [&](const Shared &sh) {
+    const int first = sh.first, parts = sh.parts;
+    const int in_kv = sh.hg * a.group, heads = min(a.group, G - in_kv);
+    const int head0 = sh.ch * G + in_kv, items = heads * (D / 4);
+    auto join = [&](int p0, int step, int n, bool final) {
+      for (int i = threadIdx.x; i < items; i += kThreads) {
+        const int h = i / (D / 4), it = i % (D / 4);
+        float mm = -INFINITY, ll = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < n; p += kBatch) {
+          float2 s[kBatch];
+          float4 x[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            s[k] = make_float2(-INFINITY, 0.f);
+            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p + k < n) {
+              const int64_t at = (int64_t)slot_of(first, p0 + (p + k) * step) * a.group + h;
+              s[k] = __ldcg(part_ml + at);
+              x[k] = __ldcg(part + at * (D / 4) + it);
+            }
+          }
+          float top = mm;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) top = fmaxf(top, s[k].x);
+          const float f0 = rescale(mm, top);
+          ll *= f0;
+          v.x *= f0;
+          v.y *= f0;
+          v.z *= f0;
+          v.w *= f0;
+          mm = top;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const float f = rescale(s[k].x, top);
+            ll = fmaf(f, s[k].y, ll);
+            v.x = fmaf(f, x[k].x, v.x);
+            v.y = fmaf(f, x[k].y, v.y);
+            v.z = fmaf(f, x[k].z, v.z);
+            v.w = fmaf(f, x[k].w, v.w);
+          }
+        }
+        if (final) {
+          write_out(sh.b, head0 + h, it, v, mm, ll);
+        } else {  // in place of the group's first piece, which only this thread has read ..
+          part[((int64_t)slot_of(first, p0) * a.group + h) * (D / 4) + it] = v;
+          if (it == 0) ml[h] = make_float2(mm, ll);  // .. except for its statistics
+        }
+      }
+      if (!final) {
+        __syncthreads();
+        for (int h = threadIdx.x; h < heads; h += kThreads)
+          part_ml[(int64_t)slot_of(first, p0) * a.group + h] = ml[h];
+      }
+    };
+    const int p0 = ((int)blockIdx.x - first) / kJoin * kJoin, in_grp = min(kJoin, parts - p0);
+    const int groups = (parts + kJoin - 1) / kJoin;
+    join(p0, 1, in_grp, groups == 1);
+    if (groups > 1) {
+      __syncthreads();
+      if (threadIdx.x == 0) shared[0].last = arrive(a.counters + 2 * a.max_ctas + first, groups);
+      __syncthreads();
+      if (shared[0].last) join(0, kJoin, groups, true);
+    }
   };
 
+  {
+    uint4 w[kQPieces];
+    fetch_q(cu, w);
+    put_q(w);
+    __syncthreads();
+  }
   start_segment();
   int stage = 0;
   for (int i = 0; i < n_tiles; ++i) {
@@ -868,18 +950,29 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
     load_half(stage, true);
     const bool last = i == n_tiles - 1;
     if (last || cu.tile == cu.s.n - 1) {
-      const uint32_t seg0 = t0 + i - cu.tile;
-      finish_segment(seg0, seg0 + cu.s.n);
+      Cursor<kTile> nx = cu;
+      uint4 w[kQPieces] = {};
       if (!last) {
-        cu.next(a);
-        start_segment();
+        nx.next(a);
+        fetch_q(nx, w);
       }
+      const uint32_t seg0 = t0 + i - cu.tile;
+      finish_segment(seg0, seg0 + cu.s.n, w);
+      if (last) break;
+      cu = nx;
+      start_segment();
     } else {
       cu.next(a);
     }
     stage = stage + 1 == NS ? 0 : stage + 1;
   }
   copy_wait<0>();
+  if (n_shared == 0) return;
+  __syncthreads();
+  const Shared sh0 = shared[0], sh1 = shared[1];
+  __syncthreads();
+  if (sh0.last) join_shared(sh0);
+  if (n_shared == 2 && sh1.last) join_shared(sh1);
 }
 
 template <class S>

@@ -375,6 +375,22 @@ def test_decode_split_over_the_length(lens, nh, nkv, d, page, fmt):
     b.check(DecodeAttention(nh, nkv, d, max_sms=7))
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,nh,nkv,d,page", [
+    ([9000, 10, 0, 4000], 6, 2, 128, 16), ([700] * 40, 5, 1, 64, 24), ([30001], 16, 1, 256, 64),
+    ([i * 53 % 1500 for i in range(150)], 4, 2, 64, 32), ([6000, 6001], 12, 1, 128, 32)])
+def test_decode_small_pieces(lens, nh, nkv, d, page, fmt):
+    """Few SMs, so that most of the list is cut into small pieces that CTAs take
+    as they come: the same bits every time, and correct."""
+    b = Batch(lens, nh, nkv, d, fmt, page, seed=len(lens) + d)
+    for sms in (1, 3):
+        attn = DecodeAttention(nh, nkv, d, max_sms=sms)
+        one = b.check(attn, softcap=25.0)
+        for _ in range(3):
+            again = b.run(attn, softcap=25.0)
+            assert torch.equal(one[0], again[0]) and torch.equal(one[1], again[1])
+
+
 def test_decode_one_very_long_sequence():
     """One key/value head, 150001 keys: the split's deepest join."""
     for fmt in ("bf16", "e4m3"):
