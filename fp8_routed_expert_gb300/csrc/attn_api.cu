@@ -392,7 +392,7 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   decode_page_division(&r);
   const int tile = a->tile[kv->format];
   const int64_t tiles = B * r.n_groups * ((r.capacity + tile - 1) / tile);  // < 2^62
-  if (tiles > INT32_MAX) return MOE_ERR_SHAPE;
+  if (tiles > INT64_C(1) << 29) return MOE_ERR_SHAPE;
   const int ctas = a->ctas[kv->format];
   const int grid = tiles < ctas ? (int)tiles : ctas;
   ATTN_TRY(launch_paged_decode(r, c.head_dim, kv->format == MOE_KV_E4M3, grid, s));

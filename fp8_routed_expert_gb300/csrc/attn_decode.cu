@@ -9,30 +9,29 @@
 // The launch reads each visible key and value row once and is bound by HBM;
 // the design keeps loads in flight and everything else out of their way.
 //
-// Split.  A sequence's visible positions are cut into tiles, a segment is the
-// tiles of one (sequence, group of up to 16 query heads that share a key/value
-// head), and the list of all segments' tiles is cut evenly over the CTAs,
-// whatever the lengths: every CTA finds its piece from the lengths themselves.
-// In longer lists a segment counts one tile more, about what its start and end
-// cost, or the CTAs that got many short segments would be the last to finish
-// (64 sequences of up to 8192: 73 to 100 us at a median of 81 without it).
-// A CTA that holds a whole segment writes its result; the parts of a segment
-// that several CTAs share go to the workspace as (m, l, unnormalised output)
-// and the CTA whose part came last joins them when it is done with its own
-// piece, in groups of 16 parts, then the groups.  The order of a join's sums is
-// fixed by the parts' places, so results do not depend on the order of arrival.
-// No CTA waits for another.
+// Split.  A sequence's visible positions are cut into tiles of 16 or 32 keys, a
+// segment is the tiles of one (sequence, group of up to 16 query heads that
+// share a key/value head), and the list of all segments' tiles is cut evenly
+// over the warps, whatever the lengths: every warp finds its piece from the
+// lengths themselves.  In longer lists a segment counts one tile more, about
+// what its start and end cost.  A warp writes the result of a segment that is
+// all its own.  Of a piece at most the first and the last segment are shared
+// with other warps; their parts (m, l, unnormalised output) stay in shared
+// memory until all warps of the CTA are done, so the loop over tiles has no
+// CTA-wide barrier, and are then joined.  A segment that several CTAs share
+// goes to the workspace, and the CTA whose part came last joins it, in groups
+// of 16 parts, then the groups.  The order of a join's sums is fixed by the
+// parts' places, so results do not depend on the order of arrival.  No CTA
+// waits for another.
 //
-// Tile.  Each warp takes 16 or 32 of a tile's keys through its own ring of
-// cp.async stages and keeps its own (m, l, output), so the loop
-// has no CTA-wide barrier.  S^T = K Q^T and O^T = V^T P^T run as mma.sync
-// m16n8k16: 16 keys, then 16 output columns, against 8 query heads (twice for
-// groups of 9 to 16), so that few heads leave few lanes idle.  The order of
-// the contraction over d and of the output columns is free, so both operands
-// are read from shared memory as whole 16-byte pieces of a row: the order
-// inside an instruction follows the lanes' pieces, not the row.  Weights pass
-// from the scores' layout to the second product's by 8x8 transposes in
-// registers (movmatrix).
+// Tile.  Rows come through a ring of cp.async stages of each warp's own.
+// S^T = K Q^T and O^T = V^T P^T run as mma.sync m16n8k16: 16 keys, then 16
+// output columns, against 8 query heads (twice for groups of 9 to 16), so that
+// few heads leave few lanes idle.  The order of the contraction over d and of
+// the output columns is free, so both operands are read from shared memory as
+// whole 16-byte pieces of a row: the order inside an instruction follows the
+// lanes' pieces, not the row.  Weights pass from the scores' layout to the
+// second product's by 8x8 transposes in registers (movmatrix).
 //
 // Maximum.  The reference m of the exponentials is only moved when a score
 // exceeds it by 2^8: until then weights are at most 2^8 and every sum is as
@@ -49,6 +48,7 @@
 //   s_j + log2(vs_j), so that they fit f16 whatever the scales.  They are
 //   rounded once to f16's 11 bits, an eighth of the step of the bf16 output.
 #include "common.cuh"
+#include "kernels.h"
 #include "paged_attn.h"
 
 namespace fp8moe {
@@ -57,20 +57,18 @@ namespace {
 
 constexpr int kJoin = 16;              // pieces joined by one CTA
 constexpr int kBatch = 8;              // pieces whose loads are in flight together
-constexpr int kWeighFrom = 4;          // tiles per CTA from which on a segment counts one more
+constexpr int kWeighFrom = 4;          // tiles per warp from which on a segment counts one more
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLag = 8.f;            // log2 of the largest weight, before its scale
 constexpr float kWeightBits = 7.f;     // e4m3: weights are scaled by 2^7, to 2^15 at most
 
 // MH: query heads of a group at most; KM: 16-key steps of a warp's tile; NS:
 // stages of a warp's ring; CTAS: that fit on an SM.
-constexpr int kSharedBytes = 32;
-
 template <int D_, bool E4M3_, int MH_, int KM_, int kWarps_, int NS_, int CTAS_>
 struct Shape {
   static constexpr int D = D_, MH = MH_, KM = KM_, NS = NS_, CTAS = CTAS_;
   static constexpr int kWarps = kWarps_, kThreads = 32 * kWarps;
-  static constexpr int kKeys = 16 * KM, kTile = kWarps * kKeys;  // keys of a warp's and a CTA's tile
+  static constexpr int kKeys = 16 * KM;                          // keys of a tile
   static constexpr bool E4M3 = E4M3_;
   static constexpr int NT = MH / 8;                           // columns of 8 heads
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
@@ -81,9 +79,16 @@ struct Shape {
   // values per lane and value row: a 16-byte piece, 8 bytes for the shortest row
   static constexpr int EV = E4M3 && D > 64 ? 16 : 8;
   static constexpr int H = D / (8 * EV);
-  static constexpr int kMergeRow = D + 4;                     // floats; the odd pieces spread banks
-  static constexpr int kMerge = kWarps * MH * kMergeRow * 4;  // f32 outputs of the warps
-  static constexpr int kSmem = kRing + kMerge + kWarps * MH * 8 + MH * D * 2 + 2 * kSharedBytes;
+  // a warp's part of a shared segment, f32: the first of its piece has a place
+  // of its own, the last one takes the place of the ring
+  static constexpr int kPartRow = MH * (D + 4) * 4 <= NS * kStage ? D + 4 : D;
+  static constexpr int kPart = MH * kPartRow * 4;
+  static_assert(kPart <= NS * kStage, "a part fits the ring");
+  // shared memory: rings, first parts, (m, l) of both parts, their segments,
+  // the segments shared with other CTAs, running sums of tiles
+  static constexpr int kParts = kRing, kMl = kParts + kWarps * kPart, kSegs = kMl + 2 * kWarps * MH * 8;
+  static constexpr int kShared = kSegs + 2 * kWarps * 32, kRuns = kShared + 2 * 32;
+  static constexpr int kSmem = kRuns + (kThreads + kWarps) * 4;
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
@@ -235,45 +240,71 @@ struct Cursor {
   }
 };
 
-// The even cut of W units over N CTAs: the first W % N take one more.
+// The even cut of W units over N warps: the first W % N take one more.
 struct Cut {
   uint32_t each, more;
   __device__ __forceinline__ Cut(uint32_t W, uint32_t N) : each(W / N), more(W % N) {}
-  __device__ __forceinline__ uint32_t start(uint32_t cta) const { return each * cta + min(cta, more); }
+  __device__ __forceinline__ uint32_t start(uint32_t warp) const { return each * warp + min(warp, more); }
   __device__ __forceinline__ uint32_t owner(uint32_t unit) const {
     const uint32_t big = more * (each + 1);
     return unit < big ? unit / (each + 1) : more + (unit - big) / each;
   }
 };
 
-// A segment that other CTAs hold parts of, written to the workspace: it is
-// joined when this CTA is done, if its part was the last to arrive.
+// A segment that a warp holds a part of: its group of heads, its first unit and
+// its number of tiles.
+struct Segment {
+  int b, ch, hg, n;
+  uint32_t unit0;
+  int valid;
+  int unused[2];
+};
+// A segment that other CTAs hold parts of too: the CTA of the first part, the
+// number of parts, and whether this CTA's part came last.
 struct Shared {
   int b, ch, hg;
-  uint32_t first, parts, last;  // CTA of the first part, number of parts, whether to join
-  uint32_t unused[2];
+  int first, parts, last;
+  int unused[2];
 };
+static_assert(sizeof(Segment) == 32 && sizeof(Shared) == 32, "as laid out in Shape");
+
+// Adds N parts (m, l, output piece) to (mm, ll, v), under their common maximum top.
+template <int N>
+__device__ __forceinline__ void add_parts(float &mm, float &ll, float4 &v, float top, const float2 (&st)[N],
+                                          const float4 (&x)[N]) {
+  const float f0 = rescale(mm, top);
+  ll *= f0;
+  v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
+  mm = top;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float f = rescale(st[i].x, top);
+    ll = fmaf(f, st[i].y, ll);
+    v = make_float4(fmaf(f, x[i].x, v.x), fmaf(f, x[i].y, v.y), fmaf(f, x[i].z, v.z), fmaf(f, x[i].w, v.w));
+  }
+}
 
 template <class S>
 __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int D = S::D, MH = S::MH, NT = S::NT, NS = S::NS, EV = S::EV, KM = S::KM;
-  constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kKeys = S::kKeys, kTile = S::kTile;
+  constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kKeys = S::kKeys;
   constexpr bool Q8 = S::E4M3;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;  // row and column of the matrix instructions
-  float *merge = reinterpret_cast<float *>(smem + S::kRing);            // [warp][MH][kMergeRow]
-  float2 *ml = reinterpret_cast<float2 *>(smem + S::kRing + S::kMerge);  // [warp][MH]
-  uint4 *qbuf = reinterpret_cast<uint4 *>(smem + S::kRing + S::kMerge + kWarps * MH * 8);  // [MH][D / 8]
-  Shared *shared = reinterpret_cast<Shared *>(qbuf + MH * D / 8);                         // [2]
-  static_assert(sizeof(Shared) == kSharedBytes, "two of them fit");
+  float2 *ml = reinterpret_cast<float2 *>(smem + S::kMl);          // [2 * warp + which][MH]
+  Segment *segs = reinterpret_cast<Segment *>(smem + S::kSegs);    // [2 * warp + which]
+  Shared *shared = reinterpret_cast<Shared *>(smem + S::kShared);  // [2]
+  uint32_t *runs = reinterpret_cast<uint32_t *>(smem + S::kRuns);  // [kThreads], then a sum per warp
+  const int G = a.n_heads / a.n_kv;
+  pdl_wait();
+  pdl_trigger();
 
-  // ---- this CTA's piece [t0, t1) of the W tiles of all sequences
-  const auto count = [&](int b, Span *sp) {
+  // ---- the W tiles of all sequences: running sums over runs of `per` sequences
+  const auto count = [&](int b) {
     const int len = a.lens[b];
     if (len < 0 || len > a.capacity) set_error(a.err, DEV_ERR_BOUNDS);
-    *sp = span_of<kTile>(a, b);
-    return (uint32_t)(sp->n * a.n_groups);
+    return (uint32_t)(span_of<kKeys>(a, b).n * a.n_groups);
   };
   const auto scan = [&](uint32_t v) {
 #pragma unroll
@@ -283,101 +314,81 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
     }
     return v;
   };
-  // The place of a unit: the tile it is or comes before, and the cursor there.
-  // `before`: tiles of the sequences before k.b, whose span is k.s.
-  uint32_t extra = 0;  // units of a segment beyond its tiles
-  const auto place = [&](uint32_t unit, uint32_t before, Cursor<kTile> &k) {
-    const uint32_t r = unit - before - extra * (uint32_t)(a.n_groups * k.b);
-    const int vh = (int)(r / (k.s.n + extra));
-    k.tile = (int)r - vh * (int)(k.s.n + extra);
-    k.ch = vh / a.groups_per_kv;
-    k.hg = vh - k.ch * a.groups_per_kv;
-    return before + vh * k.s.n + k.tile;
-  };
-  uint32_t W, t0, t1, n_ctas;
-  Cursor<kTile> cu;
-  if (a.B <= 32) {  // a sequence per lane, every warp for itself
-    Span sp{0, 0, 0, 0};
-    const uint32_t n = lane < a.B ? count(lane, &sp) : 0;
-    const uint32_t incl = scan(n);
+  const int per = a.B <= kThreads ? 1 : (a.B + kThreads - 1) / kThreads;
+  uint32_t W;
+  if (a.B <= 32) {  // every warp for itself, to the same result
+    const uint32_t incl = scan(lane < a.B ? count(lane) : 0);
     W = __shfl_sync(0xffffffffu, incl, 31);
-    n_ctas = min(W, gridDim.x);
-    if (blockIdx.x >= n_ctas) return;
-    extra = W >= kWeighFrom * gridDim.x ? 1 : 0;
-    const uint32_t units = W + extra * (uint32_t)(a.n_groups * a.B);
-    const Cut cut(units, n_ctas);
-    const uint32_t end = incl + extra * (uint32_t)(a.n_groups * (lane + 1));  // in units
-    const auto at = [&](uint32_t unit, Cursor<kTile> &k) {
-      const int b = __ffs((int)__ballot_sync(0xffffffffu, end > unit && lane < a.B)) - 1;
-      k.b = b;
-      k.s.lo = __shfl_sync(0xffffffffu, sp.lo, b);
-      k.s.hi = __shfl_sync(0xffffffffu, sp.hi, b);
-      k.s.first = __shfl_sync(0xffffffffu, sp.first, b);
-      k.s.n = __shfl_sync(0xffffffffu, sp.n, b);
-      return place(unit, __shfl_sync(0xffffffffu, incl - n, b), k);
-    };
-    t0 = at(cut.start(blockIdx.x), cu);
-    t1 = W;
-    if (blockIdx.x + 1 < n_ctas) {
-      Cursor<kTile> k;
-      t1 = at(cut.start(blockIdx.x + 1), k);
-    }
-  } else {  // a run of sequences per thread
-    uint32_t *sums = reinterpret_cast<uint32_t *>(merge), *found = sums + kWarps;
-    const int per = (a.B + kThreads - 1) / kThreads;
+    runs[lane] = incl;
+    __syncwarp();
+  } else {
     const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
-    Span sp;
     uint32_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += count(b, &sp);
+    for (int b = b0; b < b1; ++b) mine += count(b);
     uint32_t incl = scan(mine);
-    if (lane == 31) sums[warp] = incl;
+    if (lane == 31) runs[kThreads + warp] = incl;
     __syncthreads();
     W = 0;
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) incl += sums[w];
-      W += sums[w];
+      if (w < warp) incl += runs[kThreads + w];
+      W += runs[kThreads + w];
     }
-    n_ctas = min(W, gridDim.x);
-    if (blockIdx.x >= n_ctas) return;
-    extra = W >= kWeighFrom * gridDim.x ? 1 : 0;
-    const uint32_t units = W + extra * (uint32_t)(a.n_groups * a.B);
-    const Cut cut(units, n_ctas);
-    const auto in_units = [&](uint32_t tiles, int b) { return tiles + extra * (uint32_t)(a.n_groups * b); };
-    for (int i = 0; i < 2; ++i) {  // the thread whose run holds it finds the first unit, and the next CTA's
-      const uint32_t unit = cut.start(blockIdx.x + i);
-      if (in_units(incl - mine, b0) <= unit && unit < in_units(incl, b1)) {
-        uint32_t at = incl - mine;
-        int b = b0;
-        for (;; ++b) {
-          const uint32_t n = (uint32_t)(span_of<kTile>(a, b).n * a.n_groups);
-          if (unit < in_units(at + n, b + 1)) break;
-          at += n;
-        }
-        found[2 * i] = b;
-        found[2 * i + 1] = at;
+    runs[threadIdx.x] = incl;
+    __syncthreads();
+  }
+  // ---- this warp's piece.  A segment has a unit for each tile and `extra`
+  // ones after them.
+  const uint32_t n_warps = min(W, gridDim.x * kWarps), me = blockIdx.x * kWarps + warp;
+  if (blockIdx.x * kWarps >= n_warps) return;
+  const int extra = W >= kWeighFrom * kWarps * gridDim.x ? 1 : 0;
+  const auto units_of = [&](uint32_t tiles, int segments) { return tiles + (uint32_t)(extra * segments); };
+  const Cut cut(units_of(W, a.n_groups * a.B), n_warps);
+  uint32_t unit = cut.start(me);
+  int left = me < n_warps ? (int)(cut.start(me + 1) - unit) : 0;  // units
+  Cursor<kKeys> cu{};
+  if (left > 0) {  // the sequence of the first unit, and the place within it
+    int run = 0;
+    for (int base = 0;; base += 32) {
+      const int r = base + lane, end = min((r + 1) * per, a.B);
+      const bool beyond = r * per >= a.B || units_of(runs[min(r, kThreads - 1)], a.n_groups * end) > unit;
+      const uint32_t found = __ballot_sync(0xffffffffu, beyond);
+      if (found != 0) {
+        run = base + __ffs((int)found) - 1;
+        break;
       }
     }
-    __syncthreads();
-    cu.b = found[0];
-    cu.s = span_of<kTile>(a, cu.b);
-    t0 = place(cut.start(blockIdx.x), found[1], cu);
-    t1 = W;
-    if (blockIdx.x + 1 < n_ctas) {
-      Cursor<kTile> k;
-      k.b = found[2];
-      k.s = span_of<kTile>(a, k.b);
-      t1 = place(cut.start(blockIdx.x + 1), found[3], k);
+    uint32_t before = run > 0 ? runs[run - 1] : 0;  // tiles of the sequences before cu.b
+    cu.b = run * per;
+    if (per > 1) {
+      const int end = min(cu.b + per, a.B);
+      for (int base = cu.b;; base += 32) {
+        const uint32_t n = base + lane < end ? (uint32_t)(span_of<kKeys>(a, base + lane).n * a.n_groups) : 0;
+        const uint32_t incl = scan(n);
+        const uint32_t found = __ballot_sync(
+            0xffffffffu, base + lane >= end - 1 ||
+                             units_of(before + incl, a.n_groups * (base + lane + 1)) > unit);
+        if (found != 0) {
+          const int at = __ffs((int)found) - 1;
+          cu.b = base + at;
+          before += __shfl_sync(0xffffffffu, incl - n, at);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+      }
     }
-    __syncthreads();  // the merge buffer is free again
+    cu.s = span_of<kKeys>(a, cu.b);
+    const uint32_t r = unit - units_of(before, a.n_groups * cu.b);
+    const int vh = (int)(r / (cu.s.n + extra));
+    cu.tile = (int)r - vh * (cu.s.n + extra);
+    cu.ch = vh / a.groups_per_kv;
+    cu.hg = vh - cu.ch * a.groups_per_kv;
+    if (cu.tile == cu.s.n) {  // it begins with a segment's extra unit
+      --left;
+      ++unit;
+      --cu.tile;
+      cu.next(a);
+    }
   }
-  if (t0 >= t1) return;  // a piece of nothing but a segment's end
-  if (cu.tile == cu.s.n) {  // it begins with one
-    --cu.tile;
-    cu.next(a);
-  }
-  const int n_tiles = (int)(t1 - t0);
-  const Cut cut(W + extra * (uint32_t)(a.n_groups * a.B), n_ctas);
-  const int G = a.n_heads / a.n_kv;
 
   // ---- loads: the rows of a warp's keys, NS stages ahead of their use
   constexpr int kRowsAtOnce = 32 / S::kPieces;  // rows of one copy instruction
@@ -386,28 +397,29 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
   const int my_key = lane & (kKeys - 1), my_row = lane / S::kPieces, my_piece = lane % S::kPieces;
   const int64_t my_off = my_row * a.kv.slot_stride + my_piece * 16;
   const int64_t row_step = kRowsAtOnce * a.kv.slot_stride;
-  Cursor<kTile> ld = cu;
-  int ld_left = n_tiles;
+  Cursor<kKeys> ld = cu;
+  int ld_left = left;
   int32_t page = -1;          // page of this lane's key in the next tile to load
   int64_t row = 0, srow = 0;  // offsets of its row and its scales
   uint32_t on = 0;            // keys of the tile that are loaded
-  auto key_of = [&](const Cursor<kTile> &k) { return (k.s.first + k.tile) * kTile + warp * kKeys; };
-  auto touches = [&](const Cursor<kTile> &k) {
-    const int base = key_of(k);
-    return base < k.s.hi && base + kKeys > k.s.lo;
-  };
   auto page_index = [&](int j) { return (int)(((uint64_t)(uint32_t)j * a.page_mul) >> a.page_shift); };
   auto fetch_page = [&]() {
     if (ld_left <= 0) return;
-    const int j = key_of(ld) + my_key;
+    const int j = (ld.s.first + ld.tile) * kKeys + my_key;
     page = -1;
     if (j >= ld.s.lo && j < ld.s.hi) page = a.table[ld.b * a.table_stride + page_index(j)];
   };
+  // brings the queries of a segment near, ahead of its first tile
+  const auto fetch_q = [&](const Cursor<kKeys> &k) {
+    const int in_kv = k.hg * a.group, heads = min(a.group, G - in_kv);
+    const __nv_bfloat16 *q = a.q + (int64_t)k.b * a.q_stride + (int64_t)(k.ch * G + in_kv) * D;
+    for (int i = lane * 64; i < heads * D; i += 32 * 64) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
+  };
   auto load_half = [&](int stage, bool is_v) {
-    if (ld_left > 0 && touches(ld)) {
+    if (ld_left > 0 && ld.s.lo < ld.s.hi) {
       const uint32_t dst = ring + stage * S::kStage + (is_v ? S::kHalfTile : 0);
       if (!is_v) {  // where the keys lie; the same for their value rows
-        const int j = key_of(ld) + my_key;
+        const int j = (ld.s.first + ld.tile) * kKeys + my_key;
         const bool good = (uint32_t)page < (uint32_t)a.kv.n_pages;
         if (!good && j >= ld.s.lo && j < ld.s.hi) set_error(a.err, DEV_ERR_BOUNDS);
         on = __ballot_sync(0xffffffffu, good) & kAll;
@@ -453,9 +465,14 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
       }
     }
     copy_commit();
-    if (is_v && --ld_left > 0) {
-      ld.next(a);
-      fetch_page();
+    if (is_v && ld_left > 0) {
+      --ld_left;
+      if (ld.tile == ld.s.n - 1) ld_left -= extra;
+      if (ld_left > 0) {
+        ld.next(a);
+        fetch_page();
+        if (ld.tile == 0) fetch_q(ld);
+      }
     }
   };
   fetch_page();
@@ -472,23 +489,6 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
   float qs[NT][2], sl[NT][2];           // scale of a raw score, slope * log2(e)
   const float cap2 = a.softcap * kLog2e;
   const bool plain = !(a.softcap > 0.f) && a.slopes == nullptr;
-  // a segment's queries on their way to shared memory: loaded while the one
-  // before it is finished
-  constexpr int kQPieces = (MH * D / 8 + kThreads - 1) / kThreads;
-  const auto fetch_q = [&](const Cursor<kTile> &k, uint4 (&w)[kQPieces]) {
-    const int in_kv = k.hg * a.group, heads = min(a.group, G - in_kv);
-    const __nv_bfloat16 *q = a.q + (int64_t)k.b * a.q_stride + (int64_t)(k.ch * G + in_kv) * D;
-#pragma unroll
-    for (int i = 0; i < kQPieces; ++i) {
-      const int p = threadIdx.x + i * kThreads;
-      w[i] = p < heads * (D / 8) ? reinterpret_cast<const uint4 *>(q)[p] : make_uint4(0, 0, 0, 0);
-    }
-  };
-  const auto put_q = [&](const uint4 (&w)[kQPieces]) {
-#pragma unroll
-    for (int i = 0; i < kQPieces; ++i)
-      if ((int)threadIdx.x + i * kThreads < MH * (D / 8)) qbuf[threadIdx.x + i * kThreads] = w[i];
-  };
   auto start_segment = [&]() {
     const int in_kv = cu.hg * a.group;
     const int heads = min(a.group, G - in_kv), head0 = cu.ch * G + in_kv;
@@ -497,12 +497,13 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
       const int h = g + 8 * n;  // the head whose q this lane holds
+      const __nv_bfloat16 *qp = a.q + (int64_t)cu.b * a.q_stride + (int64_t)(head0 + h) * D;
       uint4 w[D / 32];
 #pragma unroll
       for (int s = 0; s < D / 32; ++s) {
         // bf16: piece c + 4s of 8 elements; e4m3: halves of piece c + 4 (s / 2) of 16
         const int at = Q8 ? (c + 4 * (s / 2)) * 16 + 8 * (s & 1) : (c + 4 * s) * 8;
-        w[s] = qbuf[(h * D + at) / 8];
+        w[s] = h < heads ? *reinterpret_cast<const uint4 *>(qp + at) : make_uint4(0, 0, 0, 0);
       }
       float unit = a.scale;
       if (!Q8) {
@@ -607,7 +608,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
   // (.., keys 16t + 8 + 2c, + 1): high parts, and what they leave.
   auto weights = [&](float (&s)[KM][NT][4], const float (&ks)[KM][2], const float (&vs)[KM][2],
                      uint32_t (&p_hi)[KM][NT][2], uint32_t (&p_lo)[KM][NT][2]) {
-    const int base = key_of(cu);
+    const int base = (cu.s.first + cu.tile) * kKeys;
 #pragma unroll
     for (int t = 0; t < KM; ++t)
 #pragma unroll
@@ -758,231 +759,259 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
       }
   };
 
-  // ---- end of a segment, or of this CTA's piece of it
+  // ---- end of a segment, or of this warp's part of it
+  // Sums over the lanes of a column, and the factor of the outputs under m.
+  const auto total = [&](int n, int u) {
+    float sum = l[n][u];
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    return sum;
+  };
+  const auto under_m = [&](int n, int u) {
+    return Q8 && m[n][u] != -INFINITY && mv[n][u] != -INFINITY ? ex2(mv[n][u] - m[n][u] - kWeightBits) : 1.f;
+  };
+  const auto lse_of = [](float mm, float ll) { return (mm + log2f(ll)) * kLn2; };
+  auto write_whole = [&]() {
+    const int in_kv = cu.hg * a.group, heads = min(a.group, G - in_kv);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float ll = total(n, u), f = under_m(n, u) * (ll == 0.f ? 0.f : 1.f / ll);
+        const int h = 8 * n + 2 * c + u;
+        if (h >= heads) continue;
+        const int64_t bh = (int64_t)cu.b * a.n_heads + cu.ch * G + in_kv + h;
+#pragma unroll
+        for (int hh = 0; hh < S::H; ++hh)
+#pragma unroll
+          for (int jj = 0; jj < EV / 8; ++jj) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float *x = o[n][EV / 2 * hh + 4 * jj + i];
+              w[i] = pack2<false>(x[u] * f, x[2 + u] * f);
+            }
+            *reinterpret_cast<uint4 *>(a.out + bh * D + (g + 8 * hh) * EV + 8 * jj) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        if (g == 0 && a.lse) a.lse[bh] = lse_of(m[n][u], ll);
+      }
+  };
+  // Where part `which` (0: the first of a piece, 1: the last) of a warp lies.
+  const auto part_at = [&](int w, int which) {
+    return reinterpret_cast<float *>(smem + (which == 0 ? S::kParts + w * S::kPart : w * (NS * S::kStage)));
+  };
+  auto keep_part = [&](int which, uint32_t unit0) {
+    const int heads = min(a.group, G - cu.hg * a.group);
+    float *const to = part_at(warp, which);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float ll = total(n, u), f = under_m(n, u);
+        const int h = 8 * n + 2 * c + u;
+        if (h >= heads) continue;
+#pragma unroll
+        for (int hh = 0; hh < S::H; ++hh)
+#pragma unroll
+          for (int jj = 0; jj < EV / 4; ++jj) {
+            const float *x = o[n][EV / 2 * hh + 2 * jj], *y = o[n][EV / 2 * hh + 2 * jj + 1];
+            *reinterpret_cast<float4 *>(to + h * S::kPartRow + (g + 8 * hh) * EV + 4 * jj) =
+                make_float4(x[u] * f, x[2 + u] * f, y[u] * f, y[2 + u] * f);
+          }
+        if (g == 0) ml[(2 * warp + which) * MH + h] = make_float2(m[n][u], ll);
+      }
+    if (lane == 0) segs[2 * warp + which] = Segment{cu.b, cu.ch, cu.hg, cu.s.n, unit0, 1, {0, 0}};
+  };
+
+  if (lane < 2) segs[2 * warp + lane].valid = 0;
+  __syncwarp();
+  int stage = 0;
+  while (left > 0) {  // the parts of segments in this piece
+    const int from = cu.tile, to = min(cu.s.n, from + left);
+    const bool busy = cu.s.lo < cu.s.hi;
+    start_segment();
+    for (; cu.tile < to; ++cu.tile) {
+      uint32_t p_hi[KM][NT][2], p_lo[KM][NT][2];
+      float s[KM][NT][4], ks[KM][2], vs[KM][2];
+      copy_wait<2 * NS - 1>();  // the key rows
+      __syncwarp();
+      if (busy) scores(stage, s, ks, vs);
+      __syncwarp();
+      load_half(stage, false);
+      if (busy) weights(s, ks, vs, p_hi, p_lo);
+      copy_wait<2 * NS - 1>();  // the value rows
+      __syncwarp();
+      if (busy) add_values(stage, p_hi, p_lo);
+      __syncwarp();
+      load_half(stage, true);
+      stage = stage + 1 == NS ? 0 : stage + 1;
+    }
+    const uint32_t unit0 = unit - from;
+    unit += to - from + extra;
+    left -= to - from + (to == cu.s.n ? extra : 0);
+    if (from == 0 && to == cu.s.n) {
+      write_whole();
+    } else {
+      const int which = left > 0 ? 0 : 1;
+      if (which == 1) {
+        copy_wait<0>();
+        __syncwarp();  // the ring is free
+      }
+      keep_part(which, unit0);
+    }
+    --cu.tile;
+    if (left > 0) cu.next(a);
+  }
+  copy_wait<0>();
+  __syncthreads();
+
+  // ---- the CTA's shared segments
+  float4 *part = reinterpret_cast<float4 *>(a.part);
+  float2 *part_ml = reinterpret_cast<float2 *>(a.part_ml);
   // Outputs are handled as float4 items: item i of a head is elements 4i .. 4i + 3.
-  auto write_out = [&](int b, int head, int item, float4 v, float mm, float ll) {
+  const auto write_out = [&](int b, int head, int item, float4 v, float mm, float ll) {
     const float inv = ll == 0.f ? 0.f : 1.f / ll;
     const int64_t bh = (int64_t)b * a.n_heads + head;
     uint2 w;
     w.x = pack2<false>(v.x * inv, v.y * inv);
     w.y = pack2<false>(v.z * inv, v.w * inv);
     *reinterpret_cast<uint2 *>(a.out + bh * D + 4 * item) = w;
-    if (item == 0 && a.lse) a.lse[bh] = (mm + log2f(ll)) * kLn2;
+    if (item == 0 && a.lse) a.lse[bh] = lse_of(mm, ll);
   };
-  float4 *part = reinterpret_cast<float4 *>(a.part);
-  float2 *part_ml = reinterpret_cast<float2 *>(a.part_ml);
-  // a CTA's own slots: 0 for a segment that began before its piece, 1 otherwise
+  // A CTA's slots of the workspace: 0 for a segment that began in another CTA,
+  // 1 for one that begins here.
   const auto slot_of = [&](int first, int nth) { return 2 * (first + nth) + (nth == 0 ? 1 : 0); };
-  // Thread 0: counts a part that all threads have written; true for the last.
+  // Counts a part that all threads have written; true for the last.
   const auto arrive = [&](int *counter, int n) {
-    __threadfence();
-    const bool last = atomicAdd(counter, 1) == n - 1;
-    if (last) *counter = 0;  // for the next call
-    __threadfence();
-    return last;
+    int before;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    if (before == n - 1) *counter = 0;  // for the next call
+    return before == n - 1;
   };
   int n_shared = 0;
-  // Ends the segment of tiles [seg0, seg1), or this CTA's part of it; w: the next one's queries.
-  auto finish_segment = [&](uint32_t seg0, uint32_t seg1, const uint4 (&w)[kQPieces]) {
-    const int in_kv = cu.hg * a.group, heads = min(a.group, G - in_kv);
-    const int head0 = cu.ch * G + in_kv;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float sum = l[n][u];
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        float f = 1.f;
-        if (Q8 && m[n][u] != -INFINITY && mv[n][u] != -INFINITY) f = ex2(mv[n][u] - m[n][u] - kWeightBits);
-        const int h = 8 * n + 2 * c + u;
-        if (h < heads) {
-          float *dst = merge + (warp * MH + h) * S::kMergeRow;
-#pragma unroll
-          for (int hh = 0; hh < S::H; ++hh)
-#pragma unroll
-            for (int jj = 0; jj < EV / 4; ++jj) {
-              const float *x = o[n][EV / 2 * hh + 2 * jj], *y = o[n][EV / 2 * hh + 2 * jj + 1];
-              *reinterpret_cast<float4 *>(dst + (g + 8 * hh) * EV + 4 * jj) =
-                  make_float4(x[u] * f, x[2 + u] * f, y[u] * f, y[2 + u] * f);
-            }
-          if (g == 0) ml[warp * MH + h] = make_float2(m[n][u], sum);
-        }
-      }
-    __syncthreads();
-    put_q(w);
-    // the CTAs that hold parts of this segment
-    int first = blockIdx.x, parts = 1;
-    if (seg0 < t0 || seg1 > t1) {
-      const uint32_t ends = extra * (uint32_t)(cu.b * a.n_groups + cu.ch * a.groups_per_kv + cu.hg);
-      first = (int)cut.owner(seg0 + ends);
-      parts = (int)cut.owner(seg1 - 1 + ends) - first + 1;
-    }
-    const int items = heads * (D / 4);
+  const uint32_t valid = __ballot_sync(0xffffffffu, lane < 2 * kWarps && segs[lane & (2 * kWarps - 1)].valid);
+  for (uint32_t rest = valid; rest != 0;) {
+    const Segment sg = segs[__ffs((int)rest) - 1];
+    // the warps' parts of this segment
+    const uint32_t same = rest & __ballot_sync(0xffffffffu, segs[lane & (2 * kWarps - 1)].unit0 == sg.unit0);
+    rest &= ~same;
+    const int in_kv = sg.hg * a.group, heads = min(a.group, G - in_kv);
+    const int head0 = sg.ch * G + in_kv, items = heads * (D / 4);
+    const int first = (int)(cut.owner(sg.unit0) / kWarps);
+    const int parts = (int)(cut.owner(sg.unit0 + sg.n - 1) / kWarps) - first + 1;
     const int mine = slot_of(first, blockIdx.x - first);
+#pragma unroll 1
     for (int i = threadIdx.x; i < items; i += kThreads) {
       const int h = i / (D / 4), it = i % (D / 4);
-      float mm = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w * MH + h].x);
-      float ll = 0.f;
+      float mm = -INFINITY, ll = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (uint32_t set = same; set != 0;) {  // four at a time
+        float2 st[4];
+        float4 x[4];
+        float top = mm;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 s = ml[w * MH + h];
-        const float f = rescale(s.x, mm);
-        const float4 x = *reinterpret_cast<const float4 *>(merge + (w * MH + h) * S::kMergeRow + 4 * it);
-        ll = fmaf(f, s.y, ll);
-        v.x = fmaf(f, x.x, v.x);
-        v.y = fmaf(f, x.y, v.y);
-        v.z = fmaf(f, x.z, v.z);
-        v.w = fmaf(f, x.w, v.w);
+        for (int q = 0; q < 4; ++q) {
+          const int p = __ffs((int)set) - 1;
+          st[q] = make_float2(-INFINITY, 0.f);
+          x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (set != 0) {
+            st[q] = ml[p * MH + h];
+            x[q] = *reinterpret_cast<const float4 *>(part_at(p / 2, p & 1) + h * S::kPartRow + 4 * it);
+          }
+          set &= set - 1;
+          top = fmaxf(top, st[q].x);
+        }
+        add_parts<4>(mm, ll, v, top, st, x);
       }
       if (parts == 1) {
-        write_out(cu.b, head0 + h, it, v, mm, ll);
+        write_out(sg.b, head0 + h, it, v, mm, ll);
       } else {
         part[((int64_t)mine * a.group + h) * (D / 4) + it] = v;
         if (it == 0) part_ml[(int64_t)mine * a.group + h] = make_float2(mm, ll);
       }
     }
-    __syncthreads();  // the part is written, and the merge buffer free again
     if (parts > 1) {
-      if (threadIdx.x == 0) {
-        const int grp = (blockIdx.x - first) / kJoin, p0 = grp * kJoin;
-        shared[n_shared] = Shared{cu.b, cu.ch, cu.hg, (uint32_t)first, (uint32_t)parts,
-                                  arrive(a.counters + (grp == 0 ? 0 : a.max_ctas) + first + p0,
-                                         min(kJoin, parts - p0)), {0, 0}};
-      }
+      if (threadIdx.x == 0) shared[n_shared] = Shared{sg.b, sg.ch, sg.hg, first, parts, 0, {0, 0}};
       ++n_shared;
     }
-  };
-  // Joins this CTA's group of the segment's parts, then, if that was the last
-  // group, the groups.  Counters: a CTA is the first of at most one shared
-  // segment and a later one of at most one other, so three arrays by CTA do.
-  auto join_shared = [&](const Shared &sh) {
-    const int first = sh.first, parts = sh.parts;
-    const int in_kv = sh.hg * a.group, heads = min(a.group, G - in_kv);
+  }
+  if (n_shared == 0) return;
+  // Counters: a CTA is the first of at most one shared segment and a later one
+  // of at most one other, so three arrays by CTA do.
+  __syncthreads();
+  if (lane == 0 && warp < n_shared) {
+    const int first = shared[warp].first, grp = ((int)blockIdx.x - first) / kJoin;
+    shared[warp].last = arrive(a.counters + (grp == 0 ? 0 : a.max_ctas) + first + grp * kJoin,
+                               min(kJoin, shared[warp].parts - grp * kJoin));
+  }
+  __syncthreads();
+  for (int i = 0; i < n_shared; ++i) {
+    const Shared sh = shared[i];
+    if (!sh.last) continue;
+    // this CTA's group of the segment's parts, then, if that was the last
+    // group, the groups
+    const int first = sh.first, in_kv = sh.hg * a.group, heads = min(a.group, G - in_kv);
     const int head0 = sh.ch * G + in_kv, items = heads * (D / 4);
-    auto join = [&](int p0, int step, int n, bool final) {
-      for (int i = threadIdx.x; i < items; i += kThreads) {
-        const int h = i / (D / 4), it = i % (D / 4);
+    const int groups = (sh.parts + kJoin - 1) / kJoin;
+    int p0 = ((int)blockIdx.x - first) / kJoin * kJoin, step = 1, n = min(kJoin, sh.parts - p0);
+    bool final = groups == 1;
+    for (;;) {  // n parts, every `step`-th from p0 on
+#pragma unroll 1
+      for (int j = threadIdx.x; j < items; j += kThreads) {
+        const int h = j / (D / 4), it = j % (D / 4);
         float mm = -INFINITY, ll = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
         for (int p = 0; p < n; p += kBatch) {
-          float2 s[kBatch];
+          float2 st[kBatch];
           float4 x[kBatch];
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            s[k] = make_float2(-INFINITY, 0.f);
-            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (p + k < n) {
-              const int64_t at = (int64_t)slot_of(first, p0 + (p + k) * step) * a.group + h;
-              s[k] = __ldcg(part_ml + at);
-              x[k] = __ldcg(part + at * (D / 4) + it);
+          for (int q = 0; q < kBatch; ++q) {
+            st[q] = make_float2(-INFINITY, 0.f);
+            x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p + q < n) {
+              const int64_t at = (int64_t)slot_of(first, p0 + (p + q) * step) * a.group + h;
+              st[q] = __ldcg(part_ml + at);
+              x[q] = __ldcg(part + at * (D / 4) + it);
             }
           }
           float top = mm;
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) top = fmaxf(top, s[k].x);
-          const float f0 = rescale(mm, top);
-          ll *= f0;
-          v.x *= f0;
-          v.y *= f0;
-          v.z *= f0;
-          v.w *= f0;
-          mm = top;
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const float f = rescale(s[k].x, top);
-            ll = fmaf(f, s[k].y, ll);
-            v.x = fmaf(f, x[k].x, v.x);
-            v.y = fmaf(f, x[k].y, v.y);
-            v.z = fmaf(f, x[k].z, v.z);
-            v.w = fmaf(f, x[k].w, v.w);
-          }
+          for (int q = 0; q < kBatch; ++q) top = fmaxf(top, st[q].x);
+          add_parts<kBatch>(mm, ll, v, top, st, x);
         }
         if (final) {
           write_out(sh.b, head0 + h, it, v, mm, ll);
-        } else {  // in place of the group's first piece, which only this thread has read ..
+        } else {  // in place of the group's first part, which only this thread has read ..
           part[((int64_t)slot_of(first, p0) * a.group + h) * (D / 4) + it] = v;
           if (it == 0) ml[h] = make_float2(mm, ll);  // .. except for its statistics
         }
       }
-      if (!final) {
-        __syncthreads();
-        for (int h = threadIdx.x; h < heads; h += kThreads)
-          part_ml[(int64_t)slot_of(first, p0) * a.group + h] = ml[h];
-      }
-    };
-    const int p0 = ((int)blockIdx.x - first) / kJoin * kJoin, in_grp = min(kJoin, parts - p0);
-    const int groups = (parts + kJoin - 1) / kJoin;
-    join(p0, 1, in_grp, groups == 1);
-    if (groups > 1) {
+      if (final) break;
       __syncthreads();
-      if (threadIdx.x == 0) shared[0].last = arrive(a.counters + 2 * a.max_ctas + first, groups);
+      for (int h = threadIdx.x; h < heads; h += kThreads)
+        part_ml[(int64_t)slot_of(first, p0) * a.group + h] = ml[h];
       __syncthreads();
-      if (shared[0].last) join(0, kJoin, groups, true);
+      if (threadIdx.x == 0) shared[i].last = arrive(a.counters + 2 * a.max_ctas + first, groups);
+      __syncthreads();
+      if (!shared[i].last) break;
+      p0 = 0;
+      step = kJoin;
+      n = groups;
+      final = true;
     }
-  };
-
-  {
-    uint4 w[kQPieces];
-    fetch_q(cu, w);
-    put_q(w);
-    __syncthreads();
   }
-  start_segment();
-  int stage = 0;
-  for (int i = 0; i < n_tiles; ++i) {
-    const bool busy = touches(cu);
-    uint32_t p_hi[KM][NT][2], p_lo[KM][NT][2];
-    float s[KM][NT][4], ks[KM][2], vs[KM][2];
-    copy_wait<2 * NS - 1>();  // the key rows
-    __syncwarp();
-    if (busy) scores(stage, s, ks, vs);
-    __syncwarp();
-    load_half(stage, false);
-    if (busy) weights(s, ks, vs, p_hi, p_lo);
-    copy_wait<2 * NS - 1>();  // the value rows
-    __syncwarp();
-    if (busy) add_values(stage, p_hi, p_lo);
-    __syncwarp();
-    load_half(stage, true);
-    const bool last = i == n_tiles - 1;
-    if (last || cu.tile == cu.s.n - 1) {
-      Cursor<kTile> nx = cu;
-      uint4 w[kQPieces] = {};
-      if (!last) {
-        nx.next(a);
-        fetch_q(nx, w);
-      }
-      const uint32_t seg0 = t0 + i - cu.tile;
-      finish_segment(seg0, seg0 + cu.s.n, w);
-      if (last) break;
-      cu = nx;
-      start_segment();
-    } else {
-      cu.next(a);
-    }
-    stage = stage + 1 == NS ? 0 : stage + 1;
-  }
-  copy_wait<0>();
-  if (n_shared == 0) return;
-  __syncthreads();
-  const Shared sh0 = shared[0], sh1 = shared[1];
-  __syncthreads();
-  if (sh0.last) join_shared(sh0);
-  if (n_shared == 2 && sh1.last) join_shared(sh1);
 }
 
 template <class S>
 cudaError_t launch_shape(const DecodeArgs &a, int grid, cudaStream_t s) {
-  decode_kernel<S><<<grid, S::kThreads, S::kSmem, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(decode_kernel<S>, dim3((unsigned)grid), dim3(S::kThreads), S::kSmem, s, a);
 }
 template <class S>
 cudaError_t plan_shape(int *ctas_per_sm, int *tile) {
-  *tile = S::kTile;
+  *tile = S::kKeys;
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_kernel<S>, S::kThreads, S::kSmem);
@@ -1000,7 +1029,7 @@ cudaError_t with_shape(int d, bool e4m3, int group, F f) {
       if (e4m3) return wide ? f(Shape<128, true, 16, 2, 8, 2, 1>{}) : f(Shape<128, true, 8, 2, 4, 2, 2>{});
       return wide ? f(Shape<128, false, 16, 2, 8, 1, 1>{}) : f(Shape<128, false, 8, 2, 4, 1, 2>{});
     case 256:
-      if (e4m3) return wide ? f(Shape<256, true, 16, 1, 8, 1, 1>{}) : f(Shape<256, true, 8, 2, 4, 1, 2>{});
+      if (e4m3) return wide ? f(Shape<256, true, 16, 1, 4, 3, 1>{}) : f(Shape<256, true, 8, 2, 4, 1, 2>{});
       return wide ? f(Shape<256, false, 16, 1, 4, 1, 1>{}) : f(Shape<256, false, 8, 1, 4, 1, 2>{});
     default: return cudaErrorInvalidValue;
   }

@@ -16,6 +16,7 @@
 // end of the int32 range) where an f32 product would lose the angle of a far
 // position altogether.
 #include "common.cuh"
+#include "kernels.h"
 #include "paged_attn.h"
 
 namespace fp8moe {
@@ -156,6 +157,8 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_con
     it.h = r - (it.is_q ? 0 : (it.is_k ? a.n_q : a.n_q + a.n_k));
     return it;
   };
+  pdl_wait();
+  pdl_trigger();
   uint4 raw[kDepth][2];
 #pragma unroll
   for (int k = 0; k < kDepth; ++k) {
@@ -301,6 +304,8 @@ __global__ void __launch_bounds__(kRowThreads) read_rows_kernel(const __grid_con
   const int tokens = (int)min((int64_t)cut.tokens, a.T - t_base);
   const int r_base = blockIdx.y * cut.rows;
   const int items = cut.tokens > 1 ? tokens * n_rows : min(cut.rows, n_rows - r_base);
+  pdl_wait();
+  pdl_trigger();
   if (threadIdx.x < tokens) at[threadIdx.x] = place_of(a.slots[t_base + threadIdx.x], a.kv, a.err);
   __syncthreads();
   uint4 raw[kDepth][2];
@@ -363,17 +368,15 @@ template <int D>
 cudaError_t rows_of(const RowArgs &a, cudaStream_t s) {
   const int n_rows = a.n_q + a.n_k + a.n_v;
   const RowCut c = cut_rows<D>(a.T, n_rows, a.sms);
-  head_rows_kernel<D><<<grid_of(c, a.T, n_rows), kRowThreads, 0, s>>>(a, c);
-  return cudaGetLastError();
+  return launch_pdl(head_rows_kernel<D>, grid_of(c, a.T, n_rows), dim3(kRowThreads), 0, s, a, c);
 }
 
 template <int D>
 cudaError_t read_of(const ReadArgs &a, cudaStream_t s) {
   const RowCut c = cut_rows<D>(a.T, 2 * a.n_kv, a.sms);
   const dim3 grid = grid_of(c, a.T, 2 * a.n_kv);
-  if (a.e4m3) read_rows_kernel<D, true><<<grid, kRowThreads, 0, s>>>(a, c);
-  else read_rows_kernel<D, false><<<grid, kRowThreads, 0, s>>>(a, c);
-  return cudaGetLastError();
+  return launch_pdl(a.e4m3 ? read_rows_kernel<D, true> : read_rows_kernel<D, false>, grid,
+                    dim3(kRowThreads), 0, s, a, c);
 }
 
 }  // namespace

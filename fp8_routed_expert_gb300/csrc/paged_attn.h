@@ -96,7 +96,7 @@ int decode_group(int heads_per_kv);
 // Fills in page_mul, page_shift and whole_pages.
 void decode_page_division(DecodeArgs *a);
 // Readies the kernel; tells how many CTAs of it fit on an SM, and the positions
-// of a tile.  Launches take at most max_ctas CTAs and need fewer than 2^31 tiles.
+// of a tile.  Launches take at most max_ctas CTAs and at most 2^29 tiles.
 cudaError_t plan_paged_decode(int d, bool e4m3, int group, int *ctas_per_sm, int *tile);
 cudaError_t launch_paged_decode(const DecodeArgs &a, int d, bool e4m3, int grid, cudaStream_t s);
 

@@ -478,8 +478,9 @@ int moe_attn_read(moe_attn *a, const moe_paged_kv *kv, const int64_t *slots, int
  *   slopes     : device f32 [n_heads] or NULL.
  *   out        : device bf16 [B, n_heads, d] contiguous, 16-byte aligned.
  *   lse        : device f32 [B, n_heads] or NULL.
- * B <= 2^20, and B * n_kv_heads * max_pages * page_size at most 2^36 or so (2^31
- * tiles of the split), else MOE_ERR_SHAPE.  B = 0 is a no-op.  The calls on one context share its
+ * B <= 2^20 and B * n_kv_heads * max_pages * page_size <= 2^33 (times ceil(n_heads
+ * / n_kv_heads / 16) beyond 16 heads per key/value head), else MOE_ERR_SHAPE.
+ * B = 0 is a no-op.  The calls on one context share its
  * workspace: they must not overlap on the GPU.
  */
 int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t q_stride,
