@@ -16,6 +16,11 @@ from .layer import _stream_handle
 
 _BF16 = torch.bfloat16
 
+# The current stream's handle of a device.  A small decode step is a few
+# microseconds, and building a torch.cuda.Stream object for each call costs
+# about three (on Grace); this query costs a tenth of one.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
 
 def rope_frequencies(rope_dim: int, theta: float = 10000.0) -> list[float]:
     """The usual frequencies theta^(-2i/R), i < R/2, in radians per position."""
@@ -50,6 +55,7 @@ class PagedKVCache:
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self.format = "e4m3" if e4m3 else "bf16"
         self.device = k.device
+        self.layout = (self.n_kv_heads, self.head_dim, k.get_device())
         ss = k_scale.stride() if e4m3 else (0, 0, 0)
         self._desc = PagedKVDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
                                  v_scale.data_ptr() if e4m3 else None, self.n_pages, *k.stride()[:3], *ss,
@@ -85,7 +91,11 @@ class DecodeAttention:
                               ctypes.addressof(arr) if freqs else None)
         self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
         self.rope_dim = 2 * len(freqs)
-        self.device = torch.device("cuda", device)
+        self.device, self._index = torch.device("cuda", device), device
+        self._layout = (n_kv_heads, head_dim, device)
+        L = lib()
+        self._norm_rope, self._append, self._write = L.moe_attn_norm_rope, L.moe_attn_append, L.moe_attn_write
+        self._read, self._decode = L.moe_attn_read, L.moe_attn_decode
         self._scale = 1.0 / math.sqrt(head_dim) if head_dim > 0 else 0.0
         h = ctypes.c_void_p()
         check(lib().moe_attn_init(ctypes.byref(h), ctypes.byref(self.cfg)), "moe_attn_init")
@@ -115,7 +125,7 @@ class DecodeAttention:
     def _rows(self, t: torch.Tensor, T: int, heads: int, name: str) -> int:
         """Token stride of bf16 head rows [T, heads, head_dim]."""
         d = self.head_dim
-        if t.dtype is not _BF16 or t.shape != (T, heads, d) or t.device != self.device:
+        if t.dtype is not _BF16 or t.shape != (T, heads, d) or t.get_device() != self._index:
             raise ValueError(f"{name} must be bf16 [{T}, {heads}, {d}] on {self.device}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
         s0, s1, s2 = t.stride()
@@ -126,16 +136,21 @@ class DecodeAttention:
     def _vec(self, t: torch.Tensor | None, dtype: torch.dtype, n: int, name: str) -> int | None:
         if t is None:
             return None
-        if t.dtype is not dtype or t.shape != (n,) or t.device != self.device or (n > 1 and t.stride(0) != 1):
+        if t.dtype is not dtype or t.shape != (n,) or t.get_device() != self._index or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous {dtype} [{n}] on {self.device}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
         return t.data_ptr()
 
     def _cache(self, cache: PagedKVCache) -> int:
-        if cache.n_kv_heads != self.n_kv_heads or cache.head_dim != self.head_dim or cache.device != self.device:
+        if cache.layout != self._layout:
             raise ValueError(f"the cache holds {cache.n_kv_heads} heads of {cache.head_dim} on {cache.device}; "
                              f"the context has {self.n_kv_heads} of {self.head_dim} on {self.device}")
         return cache._ref
+
+    def _stream(self, stream) -> int:
+        if stream is None and _current_raw_stream is not None:
+            return _current_raw_stream(self._index)
+        return _stream_handle(stream)
 
     # -- operators -------------------------------------------------------
 
@@ -155,12 +170,13 @@ class DecodeAttention:
         if k_out is None:
             k_out = torch.empty((T, self.n_kv_heads, d), dtype=_BF16, device=self.device)
         qos, kos = self._rows(q_out, T, self.n_heads, "q_out"), self._rows(k_out, T, self.n_kv_heads, "k_out")
-        rc = lib().moe_attn_norm_rope(self._h, q.data_ptr(), qs, k.data_ptr(), ks,
-                                      self._vec(positions, torch.int32, T, "positions"), T,
-                                      self._vec(q_weight, torch.float32, d, "q_weight"),
-                                      self._vec(k_weight, torch.float32, d, "k_weight"), eps,
-                                      q_out.data_ptr(), qos, k_out.data_ptr(), kos, _stream_handle(stream))
-        check(rc, "moe_attn_norm_rope")
+        rc = self._norm_rope(self._h, q.data_ptr(), qs, k.data_ptr(), ks,
+                             self._vec(positions, torch.int32, T, "positions"), T,
+                             self._vec(q_weight, torch.float32, d, "q_weight"),
+                             self._vec(k_weight, torch.float32, d, "k_weight"), eps,
+                             q_out.data_ptr(), qos, k_out.data_ptr(), kos, self._stream(stream))
+        if rc:
+            check(rc, "moe_attn_norm_rope")
         return q_out, k_out
 
     def append(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
@@ -178,13 +194,14 @@ class DecodeAttention:
         if q_out is None:
             q_out = torch.empty((T, self.n_heads, d), dtype=_BF16, device=self.device)
         qos = self._rows(q_out, T, self.n_heads, "q_out")
-        rc = lib().moe_attn_append(self._h, self._cache(cache), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                                   self._vec(positions, torch.int32, T, "positions"),
-                                   self._vec(slots, torch.int64, T, "slots"), T,
-                                   self._vec(q_weight, torch.float32, d, "q_weight"),
-                                   self._vec(k_weight, torch.float32, d, "k_weight"), eps,
-                                   q_out.data_ptr(), qos, _stream_handle(stream))
-        check(rc, "moe_attn_append")
+        rc = self._append(self._h, self._cache(cache), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                          self._vec(positions, torch.int32, T, "positions"),
+                          self._vec(slots, torch.int64, T, "slots"), T,
+                          self._vec(q_weight, torch.float32, d, "q_weight"),
+                          self._vec(k_weight, torch.float32, d, "k_weight"), eps,
+                          q_out.data_ptr(), qos, self._stream(stream))
+        if rc:
+            check(rc, "moe_attn_append")
         return q_out
 
     def write(self, cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
@@ -192,9 +209,10 @@ class DecodeAttention:
         if it is e4m3."""
         T = k.shape[0]
         ks, vs = self._rows(k, T, self.n_kv_heads, "k"), self._rows(v, T, self.n_kv_heads, "v")
-        rc = lib().moe_attn_write(self._h, self._cache(cache), k.data_ptr(), ks, v.data_ptr(), vs,
-                                  self._vec(slots, torch.int64, T, "slots"), T, _stream_handle(stream))
-        check(rc, "moe_attn_write")
+        rc = self._write(self._h, self._cache(cache), k.data_ptr(), ks, v.data_ptr(), vs,
+                         self._vec(slots, torch.int64, T, "slots"), T, self._stream(stream))
+        if rc:
+            check(rc, "moe_attn_write")
 
     def read(self, cache: PagedKVCache, slots: torch.Tensor, k_out: torch.Tensor | None = None,
              v_out: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
@@ -207,9 +225,10 @@ class DecodeAttention:
         if v_out is None:
             v_out = torch.empty(shape, dtype=_BF16, device=self.device)
         ks, vs = self._rows(k_out, T, self.n_kv_heads, "k_out"), self._rows(v_out, T, self.n_kv_heads, "v_out")
-        rc = lib().moe_attn_read(self._h, self._cache(cache), self._vec(slots, torch.int64, T, "slots"), T,
-                                 k_out.data_ptr(), ks, v_out.data_ptr(), vs, _stream_handle(stream))
-        check(rc, "moe_attn_read")
+        rc = self._read(self._h, self._cache(cache), self._vec(slots, torch.int64, T, "slots"), T,
+                        k_out.data_ptr(), ks, v_out.data_ptr(), vs, self._stream(stream))
+        if rc:
+            check(rc, "moe_attn_read")
         return k_out, v_out
 
     def decode(self, q: torch.Tensor, cache: PagedKVCache, page_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -226,24 +245,26 @@ class DecodeAttention:
         B = q.shape[0]
         qs = self._rows(q, B, self.n_heads, "q")
         dev = self.device
-        if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
-                page_table.device != dev or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        width = page_table.shape[-1] if page_table.dim() == 2 else 0
+        t0, t1 = page_table.stride() if width else (0, 0)
+        if page_table.dtype is not torch.int32 or page_table.shape != (B, width) or \
+                page_table.get_device() != self._index or (t1 != 1 and width > 1):
             raise ValueError(f"page_table must be int32 [{B}, max_pages] on {dev} with contiguous rows")
         if out is None:
             out = torch.empty((B, self.n_heads, self.head_dim), dtype=_BF16, device=dev)
         elif self._rows(out, B, self.n_heads, "out") != self.n_heads * self.head_dim:
             raise ValueError("out must be contiguous")
         if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (B, self.n_heads) or
-                                lse.device != dev or not lse.is_contiguous()):
+                                lse.get_device() != self._index or not lse.is_contiguous()):
             raise ValueError(f"lse must be contiguous f32 [{B}, {self.n_heads}] on {dev}")
         if seq_lens is None:
             raise ValueError("seq_lens are needed")
-        rc = lib().moe_attn_decode(self._h, self._cache(cache), q.data_ptr(), qs, page_table.data_ptr(),
-                                   page_table.stride(0), page_table.shape[1],
-                                   self._vec(seq_lens, torch.int32, B, "seq_lens"),
-                                   self._vec(starts, torch.int32, B, "starts"), B,
-                                   self._scale if scale is None else scale, softcap,
-                                   self._vec(slopes, torch.float32, self.n_heads, "slopes"), window, out.data_ptr(),
-                                   None if lse is None else lse.data_ptr(), _stream_handle(stream))
-        check(rc, "moe_attn_decode")
+        rc = self._decode(self._h, self._cache(cache), q.data_ptr(), qs, page_table.data_ptr(), t0, width,
+                          self._vec(seq_lens, torch.int32, B, "seq_lens"),
+                          self._vec(starts, torch.int32, B, "starts"), B,
+                          self._scale if scale is None else scale, softcap,
+                          self._vec(slopes, torch.float32, self.n_heads, "slopes"), window, out.data_ptr(),
+                          None if lse is None else lse.data_ptr(), self._stream(stream))
+        if rc:
+            check(rc, "moe_attn_decode")
         return out if lse is None else (out, lse)
