@@ -17,8 +17,9 @@ struct moe_attn {
   int sms = 0;                // of the device
   int *err = nullptr;
   uint64_t *turns = nullptr;  // [rope_dim / 2]
-  // moe_attn_decode: CTAs of a launch and positions of a tile (by format), workspace
-  int ctas[2] = {0, 0}, tile[2] = {1, 1};
+  // moe_attn_decode: CTAs of a launch, positions of a tile and warps of a CTA (by
+  // format), and its workspace
+  int ctas[2] = {0, 0}, tile[2] = {1, 1}, warps[2] = {1, 1};
   int group = 1, max_ctas = 0;
   int *counters = nullptr;    // [3][max_ctas], zero between calls
   float *part_ml = nullptr;   // [2 * max_ctas][group][2]
@@ -38,6 +39,7 @@ bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 constexpr int64_t kMaxBatch = 1 << 20;
 constexpr int64_t kMaxPositions = 0x7fffffff - 63;
 constexpr int64_t kMaxTokens = 0x7fffffff;
+constexpr int64_t kClusterTiles = 4;
 
 int check_config(const moe_attn_config &c) {
   if (c.n_kv_heads < 1 || c.n_heads < c.n_kv_heads || c.n_heads > 1024 ||
@@ -172,7 +174,8 @@ int moe_attn_init(moe_attn **out, const moe_attn_config *cfg) {
   a->group = decode_group(cfg->n_heads / cfg->n_kv_heads);
   for (int f = 0; f < 2; ++f) {
     int per_sm = 0;
-    if (plan_paged_decode(cfg->head_dim, f == MOE_KV_E4M3, a->group, &per_sm, &a->tile[f]) != cudaSuccess ||
+    if (plan_paged_decode(cfg->head_dim, f == MOE_KV_E4M3, a->group, &per_sm, &a->tile[f],
+                          &a->warps[f]) != cudaSuccess ||
         per_sm < 1) {
       cudaGetLastError();
       delete a;
@@ -393,8 +396,18 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   const int tile = a->tile[kv->format];
   const int64_t tiles = B * r.n_groups * ((r.capacity + tile - 1) / tile);  // < 2^62
   if (tiles > INT64_C(1) << 29) return MOE_ERR_SHAPE;
-  const int ctas = a->ctas[kv->format];
-  const int grid = tiles < ctas ? (int)tiles : ctas;
+  const int ctas = a->ctas[kv->format], warps = a->warps[kv->format];
+  int grid = tiles < ctas ? (int)tiles : ctas;
+  // Clusters of CTAs per segment, as many CTAs as give each warp a tile of the
+  // longest sequence, up to 8; where they would not all be resident, or a warp
+  // would have more than kClusterTiles, the list is cut instead.
+  const int64_t per_segment = (r.capacity + tile - 1) / tile;
+  int size = 1;
+  while (size < 8 && size * warps < 32 && size * warps < per_segment) size *= 2;
+  if (per_segment <= kClusterTiles * size * warps && B * r.n_groups * size <= ctas) {
+    r.cluster = size;
+    grid = (int)B * r.n_groups * size;
+  }
   ATTN_TRY(launch_paged_decode(r, c.head_dim, kv->format == MOE_KV_E4M3, grid, s));
   return MOE_OK;
 }

@@ -24,6 +24,11 @@
 // parts' places, so results do not depend on the order of arrival.  No CTA
 // waits for another.
 //
+// Small calls.  Where every segment can have CTAs of its own, and no warp more
+// than a few tiles, what counts is the time before the first key and after the
+// last.  Then a cluster of up to 8 CTAs takes one segment: no list and no
+// workspace, its 32 warps' parts are joined through distributed shared memory.
+//
 // Tile.  Rows come through a ring of cp.async stages of each warp's own.
 // S^T = K Q^T and O^T = V^T P^T run as mma.sync m16n8k16: 16 keys, then 16
 // output columns, against 8 query heads (twice for groups of 9 to 16), so that
@@ -84,6 +89,7 @@ struct Shape {
   static constexpr int kPartRow = MH * (D + 4) * 4 <= NS * kStage ? D + 4 : D;
   static constexpr int kPart = MH * kPartRow * 4;
   static_assert(kPart <= NS * kStage, "a part fits the ring");
+  static_assert(kWarps <= 8, "parts of a cluster have a lane each");
   // shared memory: rings, first parts, (m, l) of both parts, their segments,
   // the segments shared with other CTAs, running sums of tiles
   static constexpr int kParts = kRing, kMl = kParts + kWarps * kPart, kSegs = kMl + 2 * kWarps * MH * 8;
@@ -242,7 +248,8 @@ struct Cursor {
 
 // The even cut of W units over N warps: the first W % N take one more.
 struct Cut {
-  uint32_t each, more;
+  uint32_t each = 0, more = 0;
+  Cut() = default;
   __device__ __forceinline__ Cut(uint32_t W, uint32_t N) : each(W / N), more(W % N) {}
   __device__ __forceinline__ uint32_t start(uint32_t warp) const { return each * warp + min(warp, more); }
   __device__ __forceinline__ uint32_t owner(uint32_t unit) const {
@@ -314,79 +321,96 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
     }
     return v;
   };
-  const int per = a.B <= kThreads ? 1 : (a.B + kThreads - 1) / kThreads;
-  uint32_t W;
-  if (a.B <= 32) {  // every warp for itself, to the same result
-    const uint32_t incl = scan(lane < a.B ? count(lane) : 0);
-    W = __shfl_sync(0xffffffffu, incl, 31);
-    runs[lane] = incl;
-    __syncwarp();
-  } else {
-    const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
-    uint32_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += count(b);
-    uint32_t incl = scan(mine);
-    if (lane == 31) runs[kThreads + warp] = incl;
-    __syncthreads();
-    W = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) incl += runs[kThreads + w];
-      W += runs[kThreads + w];
-    }
-    runs[threadIdx.x] = incl;
-    __syncthreads();
-  }
-  // ---- this warp's piece.  A segment has a unit for each tile and `extra`
-  // ones after them.
-  const uint32_t n_warps = min(W, gridDim.x * kWarps), me = blockIdx.x * kWarps + warp;
-  if (blockIdx.x * kWarps >= n_warps) return;
-  const int extra = W >= kWeighFrom * kWarps * gridDim.x ? 1 : 0;
-  const auto units_of = [&](uint32_t tiles, int segments) { return tiles + (uint32_t)(extra * segments); };
-  const Cut cut(units_of(W, a.n_groups * a.B), n_warps);
-  uint32_t unit = cut.start(me);
-  int left = me < n_warps ? (int)(cut.start(me + 1) - unit) : 0;  // units
+  uint32_t unit = 0;
+  int left = 0, extra = 0;  // tiles and units of this warp's piece that are left
+  Cut cut;
   Cursor<kKeys> cu{};
-  if (left > 0) {  // the sequence of the first unit, and the place within it
-    int run = 0;
-    for (int base = 0;; base += 32) {
-      const int r = base + lane, end = min((r + 1) * per, a.B);
-      const bool beyond = r * per >= a.B || units_of(runs[min(r, kThreads - 1)], a.n_groups * end) > unit;
-      const uint32_t found = __ballot_sync(0xffffffffu, beyond);
-      if (found != 0) {
-        run = base + __ffs((int)found) - 1;
-        break;
-      }
-    }
-    uint32_t before = run > 0 ? runs[run - 1] : 0;  // tiles of the sequences before cu.b
-    cu.b = run * per;
-    if (per > 1) {
-      const int end = min(cu.b + per, a.B);
-      for (int base = cu.b;; base += 32) {
-        const uint32_t n = base + lane < end ? (uint32_t)(span_of<kKeys>(a, base + lane).n * a.n_groups) : 0;
-        const uint32_t incl = scan(n);
-        const uint32_t found = __ballot_sync(
-            0xffffffffu, base + lane >= end - 1 ||
-                             units_of(before + incl, a.n_groups * (base + lane + 1)) > unit);
-        if (found != 0) {
-          const int at = __ffs((int)found) - 1;
-          cu.b = base + at;
-          before += __shfl_sync(0xffffffffu, incl - n, at);
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, incl, 31);
-      }
-    }
-    cu.s = span_of<kKeys>(a, cu.b);
-    const uint32_t r = unit - units_of(before, a.n_groups * cu.b);
-    const int vh = (int)(r / (cu.s.n + extra));
-    cu.tile = (int)r - vh * (cu.s.n + extra);
+  if (a.cluster > 0) {  // ---- a cluster per segment, its tiles cut over its warps
+    const int seg = blockIdx.x / a.cluster, vh = seg % a.n_groups;
+    cu.b = seg / a.n_groups;
     cu.ch = vh / a.groups_per_kv;
     cu.hg = vh - cu.ch * a.groups_per_kv;
-    if (cu.tile == cu.s.n) {  // it begins with a segment's extra unit
-      --left;
-      ++unit;
-      --cu.tile;
-      cu.next(a);
+    count(cu.b);
+    cu.s = span_of<kKeys>(a, cu.b);
+    const Cut tiles(cu.s.n, a.cluster * kWarps);
+    const int me = (blockIdx.x - seg * a.cluster) * kWarps + warp;
+    cu.tile = (int)tiles.start(me);
+    left = (int)tiles.start(me + 1) - cu.tile;
+    unit = cu.tile;
+  } else {
+    const int per = a.B <= kThreads ? 1 : (a.B + kThreads - 1) / kThreads;
+    uint32_t W;
+    if (a.B <= 32) {  // every warp for itself, to the same result
+      const uint32_t incl = scan(lane < a.B ? count(lane) : 0);
+      W = __shfl_sync(0xffffffffu, incl, 31);
+      runs[lane] = incl;
+      __syncwarp();
+    } else {
+      const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
+      uint32_t mine = 0;
+      for (int b = b0; b < b1; ++b) mine += count(b);
+      uint32_t incl = scan(mine);
+      if (lane == 31) runs[kThreads + warp] = incl;
+      __syncthreads();
+      W = 0;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) incl += runs[kThreads + w];
+        W += runs[kThreads + w];
+      }
+      runs[threadIdx.x] = incl;
+      __syncthreads();
+    }
+    // ---- this warp's piece.  A segment has a unit for each tile and `extra`
+    // ones after them.
+    const uint32_t n_warps = min(W, gridDim.x * kWarps), me = blockIdx.x * kWarps + warp;
+    if (blockIdx.x * kWarps >= n_warps) return;
+    extra = W >= kWeighFrom * kWarps * gridDim.x ? 1 : 0;
+    const auto units_of = [&](uint32_t tiles, int segments) { return tiles + (uint32_t)(extra * segments); };
+    cut = Cut(units_of(W, a.n_groups * a.B), n_warps);
+    unit = cut.start(me);
+    left = me < n_warps ? (int)(cut.start(me + 1) - unit) : 0;  // units
+    if (left > 0) {  // the sequence of the first unit, and the place within it
+      int run = 0;
+      for (int base = 0;; base += 32) {
+        const int r = base + lane, end = min((r + 1) * per, a.B);
+        const bool beyond = r * per >= a.B || units_of(runs[min(r, kThreads - 1)], a.n_groups * end) > unit;
+        const uint32_t found = __ballot_sync(0xffffffffu, beyond);
+        if (found != 0) {
+          run = base + __ffs((int)found) - 1;
+          break;
+        }
+      }
+      uint32_t before = run > 0 ? runs[run - 1] : 0;  // tiles of the sequences before cu.b
+      cu.b = run * per;
+      if (per > 1) {
+        const int end = min(cu.b + per, a.B);
+        for (int base = cu.b;; base += 32) {
+          const uint32_t n = base + lane < end ? (uint32_t)(span_of<kKeys>(a, base + lane).n * a.n_groups) : 0;
+          const uint32_t incl = scan(n);
+          const uint32_t found = __ballot_sync(
+              0xffffffffu, base + lane >= end - 1 ||
+                               units_of(before + incl, a.n_groups * (base + lane + 1)) > unit);
+          if (found != 0) {
+            const int at = __ffs((int)found) - 1;
+            cu.b = base + at;
+            before += __shfl_sync(0xffffffffu, incl - n, at);
+            break;
+          }
+          before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+      }
+      cu.s = span_of<kKeys>(a, cu.b);
+      const uint32_t r = unit - units_of(before, a.n_groups * cu.b);
+      const int vh = (int)(r / (cu.s.n + extra));
+      cu.tile = (int)r - vh * (cu.s.n + extra);
+      cu.ch = vh / a.groups_per_kv;
+      cu.hg = vh - cu.ch * a.groups_per_kv;
+      if (cu.tile == cu.s.n) {  // it begins with a segment's extra unit
+        --left;
+        ++unit;
+        --cu.tile;
+        cu.next(a);
+      }
     }
   }
 
@@ -866,6 +890,66 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
   copy_wait<0>();
   __syncthreads();
 
+  if (a.cluster > 0) {
+    const int parts = min(cu.s.n, a.cluster * kWarps);  // the first warps have one each
+    if (parts == 1) return;                             // written whole
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const int in_kv = cu.hg * a.group, heads = min(a.group, G - in_kv);
+    const int64_t head0 = (int64_t)cu.b * a.n_heads + cu.ch * G + in_kv;
+    // a lane per part, as many lanes as the cluster has warps (a power of two)
+    // per float4 item of a head
+    const int width = a.cluster * kWarps, mine = lane & (width - 1);
+    uint32_t x_at, ml_at;
+    const uint32_t rank = mine / kWarps, w = mine % kWarps;
+    // all five steps, without branches, so that the sums below overlap
+    const auto sum = [&](float v) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, v, o);
+        v = o < width ? v + x : v;
+      }
+      return v;
+    };
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x_at) : "r"(smem_addr(part_at(w, 1))), "r"(rank));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ml_at) : "r"(smem_addr(ml + (2 * w + 1) * MH)), "r"(rank));
+    const int at_once = 32 / width, items = heads * (D / 4);
+    const int first = ((blockIdx.x % a.cluster) * kWarps + warp) * at_once;
+#pragma unroll 2
+    for (int base = first; base < items; base += width * at_once) {
+      const int i = base + lane / width;
+      const int h = i / (D / 4), it = i % (D / 4);
+      float mm = -INFINITY, ll = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (mine < parts && i < items) {
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(mm), "=f"(ll) : "r"(ml_at + 8 * h));
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(x_at + (h * S::kPartRow + 4 * it) * 4));
+      }
+      float top = mm;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, top, o);
+        top = o < width ? fmaxf(top, x) : top;
+      }
+      const float f = rescale(mm, top);
+      ll = sum(f * ll);
+      const float inv = ll == 0.f ? 0.f : 1.f / ll;
+      v = make_float4(sum(v.x * f) * inv, sum(v.y * f) * inv, sum(v.z * f) * inv, sum(v.w * f) * inv);
+      if (mine == 0 && i < items) {
+        uint2 o2;
+        o2.x = pack2<false>(v.x, v.y);
+        o2.y = pack2<false>(v.z, v.w);
+        *reinterpret_cast<uint2 *>(a.out + (head0 + h) * D + 4 * it) = o2;
+        if (it == 0 && a.lse) a.lse[head0 + h] = lse_of(top, ll);
+      }
+    }
+    __syncwarp();
+    // nobody leaves while its parts are read
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    return;
+  }
   // ---- the CTA's shared segments
   float4 *part = reinterpret_cast<float4 *>(a.part);
   float2 *part_ml = reinterpret_cast<float2 *>(a.part_ml);
@@ -1007,11 +1091,25 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
 
 template <class S>
 cudaError_t launch_shape(const DecodeArgs &a, int grid, cudaStream_t s) {
-  return launch_pdl(decode_kernel<S>, dim3((unsigned)grid), dim3(S::kThreads), S::kSmem, s, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, decode_kernel<S>, a);
 }
 template <class S>
-cudaError_t plan_shape(int *ctas_per_sm, int *tile) {
+cudaError_t plan_shape(int *ctas_per_sm, int *tile, int *warps) {
   *tile = S::kKeys;
+  *warps = S::kWarps;
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_kernel<S>, S::kThreads, S::kSmem);
@@ -1053,8 +1151,8 @@ void decode_page_division(DecodeArgs *a) {
   a->whole_pages = d % 16 == 0;
 }
 
-cudaError_t plan_paged_decode(int d, bool e4m3, int group, int *ctas_per_sm, int *tile) {
-  return with_shape(d, e4m3, group, [&](auto s) { return plan_shape<decltype(s)>(ctas_per_sm, tile); });
+cudaError_t plan_paged_decode(int d, bool e4m3, int group, int *ctas_per_sm, int *tile, int *warps) {
+  return with_shape(d, e4m3, group, [&](auto s) { return plan_shape<decltype(s)>(ctas_per_sm, tile, warps); });
 }
 
 cudaError_t launch_paged_decode(const DecodeArgs &a, int d, bool e4m3, int grid, cudaStream_t s) {
