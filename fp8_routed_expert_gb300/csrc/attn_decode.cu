@@ -61,7 +61,7 @@ namespace fp8moe {
 namespace {
 
 constexpr int kJoin = 16;              // pieces joined by one CTA
-constexpr int kBatch = 8;              // pieces whose loads are in flight together
+constexpr int kBatch = 4;              // pieces whose loads are in flight together
 constexpr int kWeighFrom = 4;          // tiles per warp from which on a segment counts one more
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLag = 8.f;            // log2 of the largest weight, before its scale
