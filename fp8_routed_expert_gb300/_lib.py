@@ -13,6 +13,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libfp8moe.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "fp8moe.h")
 
+BINDING_PATH = os.path.join(PKG, "_torch_binding.so")
+
 _lib = None
 
 
@@ -113,6 +115,15 @@ def lib():
         f.restype = res
     _lib = L
     return L
+
+
+def torch_binding():
+    """The native binding of the paged attention's calls (csrc/torch_binding.cpp)."""
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"{BINDING_PATH} is not built; run `python -m fp8_routed_expert_gb300.build`")
+    lib()  # the C ABI that it calls
+    from . import _torch_binding
+    return _torch_binding
 
 
 class MoEError(RuntimeError):

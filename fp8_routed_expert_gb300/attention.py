@@ -11,14 +11,15 @@ import math
 
 import torch
 
-from ._lib import C, AttnConfig, PagedKVDesc, check, lib
+from ._lib import C, AttnConfig, PagedKVDesc, check, lib, torch_binding
 from .layer import _stream_handle
 
 _BF16 = torch.bfloat16
 
 # The current stream's handle of a device.  A small decode step is a few
 # microseconds, and building a torch.cuda.Stream object for each call costs
-# about three (on Grace); this query costs a tenth of one.
+# about three (on Grace); this query costs a tenth of one.  For the same reason
+# the calls go through the native binding, which checks their tensors.
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -55,12 +56,11 @@ class PagedKVCache:
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self.format = "e4m3" if e4m3 else "bf16"
         self.device = k.device
-        self.layout = (self.n_kv_heads, self.head_dim, k.get_device())
         ss = k_scale.stride() if e4m3 else (0, 0, 0)
         self._desc = PagedKVDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
                                  v_scale.data_ptr() if e4m3 else None, self.n_pages, *k.stride()[:3], *ss,
                                  self.page_size, C["MOE_KV_E4M3"] if e4m3 else C["MOE_KV_BF16"])
-        self._ref = ctypes.addressof(self._desc)
+        self._native = (ctypes.addressof(self._desc), self.n_kv_heads, self.head_dim, k.get_device())
 
     @classmethod
     def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, format: str = "bf16",
@@ -92,17 +92,17 @@ class DecodeAttention:
         self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
         self.rope_dim = 2 * len(freqs)
         self.device, self._index = torch.device("cuda", device), device
-        self._layout = (n_kv_heads, head_dim, device)
-        L = lib()
-        self._norm_rope, self._append, self._write = L.moe_attn_norm_rope, L.moe_attn_append, L.moe_attn_write
-        self._read, self._decode = L.moe_attn_read, L.moe_attn_decode
+        self._ctx = None  # what the binding takes, while the context is open
+        self._b = torch_binding()
         self._scale = 1.0 / math.sqrt(head_dim) if head_dim > 0 else 0.0
         h = ctypes.c_void_p()
         check(lib().moe_attn_init(ctypes.byref(h), ctypes.byref(self.cfg)), "moe_attn_init")
         self.cfg.rope_freqs = None  # read during the call only
         self._h = h
+        self._ctx = (h.value, n_heads, n_kv_heads, head_dim, self.rope_dim, device)
 
     def close(self) -> None:
+        self._ctx = None
         if getattr(self, "_h", None) is not None and self._h.value:
             lib().moe_attn_free(self._h)
             self._h = None
@@ -120,37 +120,13 @@ class DecodeAttention:
     def status(self) -> int:
         return lib().moe_attn_status(self._h)
 
-    # -- argument checks -------------------------------------------------
-
-    def _rows(self, t: torch.Tensor, T: int, heads: int, name: str) -> int:
-        """Token stride of bf16 head rows [T, heads, head_dim]."""
-        d = self.head_dim
-        if t.dtype is not _BF16 or t.shape != (T, heads, d) or t.get_device() != self._index:
-            raise ValueError(f"{name} must be bf16 [{T}, {heads}, {d}] on {self.device}, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
-        s0, s1, s2 = t.stride()
-        if s2 != 1 or (s1 != d and heads > 1):
-            raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
-        return s0 if T > 1 else heads * d
-
-    def _vec(self, t: torch.Tensor | None, dtype: torch.dtype, n: int, name: str) -> int | None:
-        if t is None:
-            return None
-        if t.dtype is not dtype or t.shape != (n,) or t.get_device() != self._index or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {dtype} [{n}] on {self.device}, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
-        return t.data_ptr()
-
-    def _cache(self, cache: PagedKVCache) -> int:
-        if cache.layout != self._layout:
-            raise ValueError(f"the cache holds {cache.n_kv_heads} heads of {cache.head_dim} on {cache.device}; "
-                             f"the context has {self.n_kv_heads} of {self.head_dim} on {self.device}")
-        return cache._ref
-
-    def _stream(self, stream) -> int:
+    def _stream(self, stream) -> int | None:
         if stream is None and _current_raw_stream is not None:
             return _current_raw_stream(self._index)
         return _stream_handle(stream)
+
+    def _new(self, T: int, heads: int) -> torch.Tensor:
+        return torch.empty((T, heads, self.head_dim), dtype=_BF16, device=self.device)
 
     # -- operators -------------------------------------------------------
 
@@ -161,20 +137,12 @@ class DecodeAttention:
         """RMS norm (where a weight f32 [d] is given) and rotation of q bf16
         [T, n_heads, d] and k bf16 [T, n_kv_heads, d]; positions int32 [T].
         q_out / k_out may be q / k."""
-        T, d = q.shape[0], self.head_dim
-        qs, ks = self._rows(q, T, self.n_heads, "q"), self._rows(k, T, self.n_kv_heads, "k")
-        if positions is None and self.rope_dim:
-            raise ValueError("positions are needed to rotate")
         if q_out is None:
-            q_out = torch.empty((T, self.n_heads, d), dtype=_BF16, device=self.device)
+            q_out = self._new(q.shape[0], self.n_heads)
         if k_out is None:
-            k_out = torch.empty((T, self.n_kv_heads, d), dtype=_BF16, device=self.device)
-        qos, kos = self._rows(q_out, T, self.n_heads, "q_out"), self._rows(k_out, T, self.n_kv_heads, "k_out")
-        rc = self._norm_rope(self._h, q.data_ptr(), qs, k.data_ptr(), ks,
-                             self._vec(positions, torch.int32, T, "positions"), T,
-                             self._vec(q_weight, torch.float32, d, "q_weight"),
-                             self._vec(k_weight, torch.float32, d, "k_weight"), eps,
-                             q_out.data_ptr(), qos, k_out.data_ptr(), kos, self._stream(stream))
+            k_out = self._new(k.shape[0], self.n_kv_heads)
+        rc = self._b.norm_rope(self._ctx, q, k, positions, q_weight, k_weight, eps, q_out, k_out,
+                               self._stream(stream))
         if rc:
             check(rc, "moe_attn_norm_rope")
         return q_out, k_out
@@ -186,20 +154,10 @@ class DecodeAttention:
         """norm_rope whose keys, and the values as they are, go into the
         cache's slots (int64 [T]: page * page_size + slot, negative to store
         nothing).  Returns the queries."""
-        T, d = q.shape[0], self.head_dim
-        qs, ks = self._rows(q, T, self.n_heads, "q"), self._rows(k, T, self.n_kv_heads, "k")
-        vs = self._rows(v, T, self.n_kv_heads, "v")
-        if positions is None and self.rope_dim:
-            raise ValueError("positions are needed to rotate")
         if q_out is None:
-            q_out = torch.empty((T, self.n_heads, d), dtype=_BF16, device=self.device)
-        qos = self._rows(q_out, T, self.n_heads, "q_out")
-        rc = self._append(self._h, self._cache(cache), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                          self._vec(positions, torch.int32, T, "positions"),
-                          self._vec(slots, torch.int64, T, "slots"), T,
-                          self._vec(q_weight, torch.float32, d, "q_weight"),
-                          self._vec(k_weight, torch.float32, d, "k_weight"), eps,
-                          q_out.data_ptr(), qos, self._stream(stream))
+            q_out = self._new(q.shape[0], self.n_heads)
+        rc = self._b.append(self._ctx, cache._native, q, k, v, positions, slots, q_weight, k_weight, eps, q_out,
+                            self._stream(stream))
         if rc:
             check(rc, "moe_attn_append")
         return q_out
@@ -207,10 +165,7 @@ class DecodeAttention:
     def write(self, cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
         """k and v bf16 [T, n_kv_heads, d] into the cache's slots, quantised
         if it is e4m3."""
-        T = k.shape[0]
-        ks, vs = self._rows(k, T, self.n_kv_heads, "k"), self._rows(v, T, self.n_kv_heads, "v")
-        rc = self._write(self._h, self._cache(cache), k.data_ptr(), ks, v.data_ptr(), vs,
-                         self._vec(slots, torch.int64, T, "slots"), T, self._stream(stream))
+        rc = self._b.write(self._ctx, cache._native, k, v, slots, self._stream(stream))
         if rc:
             check(rc, "moe_attn_write")
 
@@ -218,15 +173,11 @@ class DecodeAttention:
              v_out: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
         """The rows of the slots as bf16 [T, n_kv_heads, d] (zeros for a
         negative slot)."""
-        T = slots.shape[0]
-        shape = (T, self.n_kv_heads, self.head_dim)
         if k_out is None:
-            k_out = torch.empty(shape, dtype=_BF16, device=self.device)
+            k_out = self._new(slots.shape[0], self.n_kv_heads)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=_BF16, device=self.device)
-        ks, vs = self._rows(k_out, T, self.n_kv_heads, "k_out"), self._rows(v_out, T, self.n_kv_heads, "v_out")
-        rc = self._read(self._h, self._cache(cache), self._vec(slots, torch.int64, T, "slots"), T,
-                        k_out.data_ptr(), ks, v_out.data_ptr(), vs, self._stream(stream))
+            v_out = self._new(slots.shape[0], self.n_kv_heads)
+        rc = self._b.read(self._ctx, cache._native, slots, k_out, v_out, self._stream(stream))
         if rc:
             check(rc, "moe_attn_read")
         return k_out, v_out
@@ -242,29 +193,11 @@ class DecodeAttention:
         position), ``window`` > 0 and ``starts`` int32 [B] hide earlier
         positions.  Returns out bf16 [B, n_heads, d], or (out, lse) if ``lse``
         f32 [B, n_heads] is given."""
-        B = q.shape[0]
-        qs = self._rows(q, B, self.n_heads, "q")
-        dev = self.device
-        width = page_table.shape[-1] if page_table.dim() == 2 else 0
-        t0, t1 = page_table.stride() if width else (0, 0)
-        if page_table.dtype is not torch.int32 or page_table.shape != (B, width) or \
-                page_table.get_device() != self._index or (t1 != 1 and width > 1):
-            raise ValueError(f"page_table must be int32 [{B}, max_pages] on {dev} with contiguous rows")
         if out is None:
-            out = torch.empty((B, self.n_heads, self.head_dim), dtype=_BF16, device=dev)
-        elif self._rows(out, B, self.n_heads, "out") != self.n_heads * self.head_dim:
-            raise ValueError("out must be contiguous")
-        if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (B, self.n_heads) or
-                                lse.get_device() != self._index or not lse.is_contiguous()):
-            raise ValueError(f"lse must be contiguous f32 [{B}, {self.n_heads}] on {dev}")
-        if seq_lens is None:
-            raise ValueError("seq_lens are needed")
-        rc = self._decode(self._h, self._cache(cache), q.data_ptr(), qs, page_table.data_ptr(), t0, width,
-                          self._vec(seq_lens, torch.int32, B, "seq_lens"),
-                          self._vec(starts, torch.int32, B, "starts"), B,
-                          self._scale if scale is None else scale, softcap,
-                          self._vec(slopes, torch.float32, self.n_heads, "slopes"), window, out.data_ptr(),
-                          None if lse is None else lse.data_ptr(), self._stream(stream))
+            out = self._new(q.shape[0], self.n_heads)
+        rc = self._b.decode(self._ctx, cache._native, q, page_table, seq_lens, starts,
+                            self._scale if scale is None else scale, softcap, slopes, window, out, lse,
+                            self._stream(stream))
         if rc:
             check(rc, "moe_attn_decode")
         return out if lse is None else (out, lse)

@@ -1,8 +1,9 @@
-"""Build libfp8moe.so (the layer's C ABI and its sm_103a kernels) in-tree.
+"""Build libfp8moe.so (the layer's C ABI and its sm_103a kernels) and
+_torch_binding.so (the native Python binding of the paged attention) in-tree.
 
 Each .cu file is compiled separately and in parallel with nvcc for
 compute_103a / sm_103a only, then linked into one shared library next to
-this file.  ``python -m fp8_routed_expert_gb300.build`` runs it by hand.
+this file; the binding is one C++ file against torch's headers.  ``python -m fp8_routed_expert_gb300.build`` runs it by hand.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8moe.so")
+BINDING = os.path.join(PKG, "_torch_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -41,8 +44,38 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _compile_binding() -> str:
+    """Object file of csrc/torch_binding.cpp."""
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "torch_binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", base,
+           "-isystem", os.path.join(base, "torch", "csrc", "api", "include"),
+           "-c", os.path.join(CSRC, "torch_binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed on torch_binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    tmp = BINDING + f".tmp{os.getpid()}"
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-L", PKG,
+           "-l:libfp8moe.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("link of _torch_binding.so failed")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    built = [f for f in (LIB, BINDING) if os.path.exists(f)]
+    if not force and len(built) == 2 and min(map(os.path.getmtime, built)) >= _deps_mtime():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -59,8 +92,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cudalib = os.path.join(os.path.dirname(os.path.dirname(cc)), "lib64")
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart", "-L", cudalib,
@@ -70,6 +105,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("link of libfp8moe.so failed")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
 
 
