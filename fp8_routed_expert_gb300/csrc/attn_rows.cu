@@ -110,24 +110,46 @@ RowCut cut_rows(int64_t T, int n_rows, int sms) {
   return c;
 }
 
-__device__ __forceinline__ uint2 e4m3x8(const float (&y)[16], int from, float scale) {
+// Two f32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 x, x, y;\n"
+      " mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ uint2 e4m3x8(const float2 (&y)[8], int from, float2 scale) {
   uint32_t c[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    c[j] = __nv_cvt_float2_to_fp8x2(make_float2(y[from + 2 * j] * scale, y[from + 2 * j + 1] * scale),
-                                    __NV_SATFINITE, __NV_E4M3);
+    c[j] = __nv_cvt_float2_to_fp8x2(mul2(y[from + j], scale), __NV_SATFINITE, __NV_E4M3);
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
+
+// Where key and value rows go.
+enum class Dest { kRows, kBf16Cache, kE4m3Cache };
 
 // Grid (token groups, row blocks); items of a CTA: (token, row).  Every row is
 // read and written once; a lane's rows are all in flight before the angles are
 // computed, and the angles of a token are computed once for all its heads.
 // Issue slots bound it next to HBM, hence the layout above without shuffles of
-// the row itself.
-template <int D>
+// the row itself, and arithmetic on pairs.
+template <int D, Dest kDest>
 __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_constant__ RowArgs a,
                                                                 const RowCut cut) {
   constexpr int L = D / 16, kRows = kRowThreads / L;
+  constexpr bool kCache = kDest != Dest::kRows;
   // cos and sin of the tokens' angles, pieces of four swapped so that lanes 32
   // bytes apart use all banks
   __shared__ __align__(16) float cs[kMaxTokens][2][D / 2];
@@ -142,32 +164,22 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_con
   const bool turned = lane * 8 < a.half;
   const int o0 = turned && !a.interleaved ? 8 * lane : 16 * lane;
   const int o1 = turned && !a.interleaved ? a.half + 8 * lane : 16 * lane + 8;
-  struct Item {
-    int tl, h;
-    bool on, is_q, is_k;
-  };
-  const auto item = [&](int k) {
-    Item it;
-    const int i = slot0 + k * kRows;
-    it.on = i < items;
-    it.tl = cut.tokens > 1 && it.on ? (int)((i * cut.mul) >> 20) : 0;
-    const int r = r_base + i - it.tl * n_rows;
-    it.is_q = r < a.n_q;
-    it.is_k = !it.is_q && r < a.n_q + a.n_k;
-    it.h = r - (it.is_q ? 0 : (it.is_k ? a.n_q : a.n_q + a.n_k));
-    return it;
-  };
   pdl_wait();
   pdl_trigger();
+  enum : int { kNone, kQ, kK, kV };
   uint4 raw[kDepth][2];
+  int kind[kDepth], head[kDepth], tok[kDepth];
 #pragma unroll
   for (int k = 0; k < kDepth; ++k) {
-    const Item it = item(k);
+    const int i = slot0 + k * kRows;
+    tok[k] = cut.tokens > 1 && i < items ? (int)((i * cut.mul) >> 20) : 0;
+    const int r = r_base + i - tok[k] * n_rows;
+    kind[k] = i >= items ? kNone : r < a.n_q ? kQ : r < a.n_q + a.n_k ? kK : kV;
+    head[k] = r - (kind[k] == kQ ? 0 : kind[k] == kK ? a.n_q : a.n_q + a.n_k);
     raw[k][0] = raw[k][1] = make_uint4(0, 0, 0, 0);
-    if (it.on) {
-      const __nv_bfloat16 *p = it.is_q ? a.q.p : (it.is_k ? a.k.p : a.v.p);
-      const int64_t stride = it.is_q ? a.q.stride : (it.is_k ? a.k.stride : a.v.stride);
-      p += (t_base + it.tl) * stride + it.h * D;
+    if (kind[k] != kNone) {
+      const RowsIn &in = kind[k] == kQ ? a.q : kind[k] == kK ? a.k : a.v;
+      const __nv_bfloat16 *p = in.p + (t_base + tok[k]) * in.stride + head[k] * D;
       raw[k][0] = *reinterpret_cast<const uint4 *>(p + o0);
       raw[k][1] = *reinterpret_cast<const uint4 *>(p + o1);
     }
@@ -185,108 +197,108 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_con
       cs[tl][1][place] = sn;
     }
   }
-  if (a.cache && threadIdx.x < tokens) at[threadIdx.x] = place_of(a.slots[t_base + threadIdx.x], a.kv, a.err);
+  if (kCache && threadIdx.x < tokens) at[threadIdx.x] = place_of(a.slots[t_base + threadIdx.x], a.kv, a.err);
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kDepth; ++k) {
     if (k * kRows >= items) break;  // the same for the whole CTA: shuffles take whole warps
-    const Item it = item(k);
-    float y[16];
+    float2 y[8];
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t w = u4_word(raw[k][p], j);
-        y[8 * p + 2 * j] = __uint_as_float(w << 16);
-        y[8 * p + 2 * j + 1] = __uint_as_float(w & 0xffff0000u);
+        y[4 * p + j] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
       }
     if (a.q_weight != nullptr || a.k_weight != nullptr) {
-      float ss = 0.f;
+      float2 s2 = both(0.f);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) ss = fmaf(y[j], y[j], ss);
-      ss = row_sum<L>(ss);
-      const float *w = it.is_q ? a.q_weight : (it.is_k ? a.k_weight : nullptr);
+      for (int j = 0; j < 8; ++j) s2 = fma2(y[j], y[j], s2);
+      const float ss = row_sum<L>(s2.x + s2.y);
+      const float *w = kind[k] == kQ ? a.q_weight : kind[k] == kK ? a.k_weight : nullptr;
       if (w != nullptr) {
-        const float rms = __frsqrt_rn(fmaf(ss, 1.0f / D, a.eps));
+        const float2 rms = both(__frsqrt_rn(fmaf(ss, 1.0f / D, a.eps)));
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const float4 v = __ldg(reinterpret_cast<const float4 *>(w + (p < 2 ? o0 : o1)) + (p & 1));
-          y[4 * p] = y[4 * p] * rms * v.x;
-          y[4 * p + 1] = y[4 * p + 1] * rms * v.y;
-          y[4 * p + 2] = y[4 * p + 2] * rms * v.z;
-          y[4 * p + 3] = y[4 * p + 3] * rms * v.w;
+          y[2 * p] = mul2(mul2(y[2 * p], rms), make_float2(v.x, v.y));
+          y[2 * p + 1] = mul2(mul2(y[2 * p + 1], rms), make_float2(v.z, v.w));
         }
       }
     }
-    if (turned && (it.is_q || it.is_k)) {
+    if (turned && (kind[k] == kQ || kind[k] == kK)) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int piece = 2 * lane + q, place = (piece ^ ((piece >> 3) & 1)) * 4;
-        const float4 c4 = *reinterpret_cast<const float4 *>(&cs[it.tl][0][place]);
-        const float4 s4 = *reinterpret_cast<const float4 *>(&cs[it.tl][1][place]);
-        const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
-        if (a.interleaved) {
+        const float4 c4 = *reinterpret_cast<const float4 *>(&cs[tok[k]][0][place]);
+        const float4 s4 = *reinterpret_cast<const float4 *>(&cs[tok[k]][1][place]);
+        if (a.interleaved) {  // pairs (u, v): (u c - v s, v c + u s)
+          const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float &u = y[8 * q + 2 * j], &v = y[8 * q + 2 * j + 1];
-            const float u0 = u;
-            u = fmaf(-v, ss[j], u * cc[j]);
-            v = fmaf(u0, ss[j], v * cc[j]);
+            float2 &uv = y[4 * q + j];
+            uv = fma2(make_float2(uv.y, uv.x), make_float2(-ss[j], ss[j]), mul2(uv, both(cc[j])));
           }
-        } else {
+        } else {  // two pairs at a time, u in the first piece and v in the second
+          const float2 cc[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+          const float2 ss[2] = {make_float2(s4.x, s4.y), make_float2(s4.z, s4.w)};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float &u = y[4 * q + j], &v = y[8 + 4 * q + j];
-            const float u0 = u;
-            u = fmaf(-v, ss[j], u * cc[j]);
-            v = fmaf(u0, ss[j], v * cc[j]);
+          for (int j = 0; j < 2; ++j) {
+            float2 &u = y[2 * q + j], &v = y[4 + 2 * q + j];
+            const float2 u0 = u;
+            u = fma2(v, make_float2(-ss[j].x, -ss[j].y), mul2(u, cc[j]));
+            v = fma2(u0, ss[j], mul2(v, cc[j]));
           }
         }
       }
     }
-    const bool to_cache = a.cache && !it.is_q;
-    if (it.on && (!to_cache || !a.e4m3)) {
+    const bool to_cache = kCache && kind[k] != kQ;
+    if (kind[k] != kNone && (kDest != Dest::kE4m3Cache || !to_cache)) {
       uint4 w[2];
 #pragma unroll
       for (int p = 0; p < 2; ++p)
-        w[p] = make_uint4(pack_bf16x2(y[8 * p], y[8 * p + 1]), pack_bf16x2(y[8 * p + 2], y[8 * p + 3]),
-                          pack_bf16x2(y[8 * p + 4], y[8 * p + 5]), pack_bf16x2(y[8 * p + 6], y[8 * p + 7]));
+        w[p] = make_uint4(pack_bf16x2(y[4 * p].x, y[4 * p].y), pack_bf16x2(y[4 * p + 1].x, y[4 * p + 1].y),
+                          pack_bf16x2(y[4 * p + 2].x, y[4 * p + 2].y), pack_bf16x2(y[4 * p + 3].x, y[4 * p + 3].y));
       __nv_bfloat16 *out;
+      bool store = true;
       if (to_cache) {
-        out = reinterpret_cast<__nv_bfloat16 *>((it.is_k ? a.kv.k : a.kv.v) + at[it.tl].row +
-                                                it.h * a.kv.head_stride);
+        const Place place = at[tok[k]];
+        out = reinterpret_cast<__nv_bfloat16 *>((kind[k] == kK ? a.kv.k : a.kv.v) + place.row +
+                                                head[k] * a.kv.head_stride);
+        store = place.row >= 0;
       } else {
-        out = it.is_q ? a.q_out.p : a.k_out.p;
-        out += (t_base + it.tl) * (it.is_q ? a.q_out.stride : a.k_out.stride) + it.h * D;
+        const RowsOut &o = kind[k] == kQ ? a.q_out : a.k_out;
+        out = o.p + (t_base + tok[k]) * o.stride + head[k] * D;
       }
-      if (!to_cache || at[it.tl].row >= 0) {
+      if (store) {
         *reinterpret_cast<uint4 *>(out + o0) = w[0];
         *reinterpret_cast<uint4 *>(out + o1) = w[1];
       }
     }
-    if (!a.e4m3) continue;
+    if (kDest != Dest::kE4m3Cache) continue;
     float amax = 0.f;  // fmaxf passes over a NaN, which stays one in its code
 #pragma unroll
-    for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(y[j]));
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(fabsf(y[j].x), fabsf(y[j].y)));
     amax = row_max<L>(amax);
     if (__any_sync(0xffffffffu, amax == INFINITY)) {  // an infinity has no code: it becomes a NaN
       float fin = 0.f;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        if (fabsf(y[j]) == INFINITY) y[j] = NAN;
-        fin = fmaxf(fin, fabsf(y[j]));
+      for (int j = 0; j < 8; ++j) {
+        if (fabsf(y[j].x) == INFINITY) y[j].x = NAN;
+        if (fabsf(y[j].y) == INFINITY) y[j].y = NAN;
+        fin = fmaxf(fin, fmaxf(fabsf(y[j].x), fabsf(y[j].y)));
       }
       amax = row_max<L>(fin);
     }
-    const Place place = at[it.tl];
-    if (it.on && to_cache && place.row >= 0) {
+    const Place place = at[tok[k]];
+    if (kind[k] != kNone && to_cache && place.row >= 0) {
       const int e = e4m3_row_exponent(amax);  // in [-126, 120]
-      const float down = exp2i(-e);
-      uint8_t *row = (it.is_k ? a.kv.k : a.kv.v) + place.row + it.h * a.kv.head_stride;
+      const float2 down = both(exp2i(-e));
+      uint8_t *row = (kind[k] == kK ? a.kv.k : a.kv.v) + place.row + head[k] * a.kv.head_stride;
       *reinterpret_cast<uint2 *>(row + o0) = e4m3x8(y, 0, down);
-      *reinterpret_cast<uint2 *>(row + o1) = e4m3x8(y, 8, down);
+      *reinterpret_cast<uint2 *>(row + o1) = e4m3x8(y, 4, down);
       if (lane == 0)
-        (it.is_k ? a.kv.k_scale : a.kv.v_scale)[place.scale + it.h * a.kv.scale_head_stride] = exp2i(e);
+        (kind[k] == kK ? a.kv.k_scale : a.kv.v_scale)[place.scale + head[k] * a.kv.scale_head_stride] = exp2i(e);
     }
   }
 }
@@ -368,7 +380,10 @@ template <int D>
 cudaError_t rows_of(const RowArgs &a, cudaStream_t s) {
   const int n_rows = a.n_q + a.n_k + a.n_v;
   const RowCut c = cut_rows<D>(a.T, n_rows, a.sms);
-  return launch_pdl(head_rows_kernel<D>, grid_of(c, a.T, n_rows), dim3(kRowThreads), 0, s, a, c);
+  const auto kernel = !a.cache ? head_rows_kernel<D, Dest::kRows>
+                      : a.e4m3 ? head_rows_kernel<D, Dest::kE4m3Cache>
+                               : head_rows_kernel<D, Dest::kBf16Cache>;
+  return launch_pdl(kernel, grid_of(c, a.T, n_rows), dim3(kRowThreads), 0, s, a, c);
 }
 
 template <int D>
