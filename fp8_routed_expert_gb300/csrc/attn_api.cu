@@ -171,7 +171,7 @@ int moe_attn_init(moe_attn **out, const moe_attn_config *cfg) {
   a->cfg.rope_freqs = nullptr;  // the caller's array is not kept
   a->sms = sms;
   const int use = cfg->max_sms > 0 && cfg->max_sms < sms ? cfg->max_sms : sms;
-  a->group = decode_group(cfg->n_heads / cfg->n_kv_heads);
+  a->group = decode_group(cfg->n_heads / cfg->n_kv_heads, cfg->head_dim);
   for (int f = 0; f < 2; ++f) {
     int per_sm = 0;
     if (plan_paged_decode(cfg->head_dim, f == MOE_KV_E4M3, a->group, &per_sm, &a->tile[f],

@@ -1124,19 +1124,25 @@ cudaError_t with_shape(int d, bool e4m3, int group, F f) {
       if (e4m3) return wide ? f(Shape<64, true, 16, 2, 8, 2, 1>{}) : f(Shape<64, true, 8, 2, 4, 2, 3>{});
       return wide ? f(Shape<64, false, 16, 2, 8, 2, 1>{}) : f(Shape<64, false, 8, 2, 4, 2, 3>{});
     case 128:
-      if (e4m3) return wide ? f(Shape<128, true, 16, 2, 8, 2, 1>{}) : f(Shape<128, true, 8, 2, 4, 2, 2>{});
+      if (e4m3) return wide ? f(Shape<128, true, 16, 2, 8, 1, 1>{}) : f(Shape<128, true, 8, 2, 4, 2, 2>{});
       return wide ? f(Shape<128, false, 16, 2, 8, 1, 1>{}) : f(Shape<128, false, 8, 2, 4, 1, 2>{});
     case 256:
-      if (e4m3) return wide ? f(Shape<256, true, 16, 1, 4, 3, 1>{}) : f(Shape<256, true, 8, 2, 4, 1, 2>{});
-      return wide ? f(Shape<256, false, 16, 1, 4, 1, 1>{}) : f(Shape<256, false, 8, 1, 4, 1, 2>{});
+      if (e4m3) return f(Shape<256, true, 8, 2, 4, 1, 2>{});
+      return f(Shape<256, false, 8, 1, 4, 1, 2>{});
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-int decode_group(int heads_per_kv) {
-  const int n = (heads_per_kv + 15) / 16;
+// Up to 16 heads at a time: a second pass over the rows costs more than wider
+// steps (16 heads of 128 elements, 32 sequences of up to 4096 tokens, 4
+// key/value heads: e4m3 28 us, against 32 in groups of 8; bf16 33 against 47).
+// At 256 elements 16 heads' outputs do not fit the registers of enough warps
+// (sequences of up to 2048: e4m3 50 us, in groups of 8 that read from L2 the
+// second time 32; bf16 52 against 42).
+int decode_group(int heads_per_kv, int d) {
+  const int most = d == 256 ? 8 : 16, n = (heads_per_kv + most - 1) / most;
   return (heads_per_kv + n - 1) / n;
 }
 

@@ -71,7 +71,7 @@ struct DecodeArgs {
   int64_t capacity;  // positions a row of the page table covers
   const int32_t *lens, *starts;
   int B, n_heads, n_kv;
-  // query heads of a key/value head are taken `group` (<= 16) at a time, in
+  // query heads of a key/value head are taken `group` at a time, in
   // groups_per_kv groups; n_groups = n_kv * groups_per_kv
   int group, groups_per_kv, n_groups;
   float scale, softcap;
@@ -93,7 +93,7 @@ struct DecodeArgs {
   int *err;
 };
 // Query heads taken at a time when `heads_per_kv` share a key/value head.
-int decode_group(int heads_per_kv);
+int decode_group(int heads_per_kv, int d);
 // Fills in page_mul, page_shift and whole_pages.
 void decode_page_division(DecodeArgs *a);
 // Readies the kernel; tells how many CTAs of it fit on an SM, the positions of
