@@ -13,7 +13,7 @@
 // segment is the tiles of one (sequence, group of up to 16 query heads that
 // share a key/value head), and the list of all segments' tiles is cut evenly
 // over the warps, whatever the lengths: every warp finds its piece from the
-// lengths themselves.  In longer lists a segment counts one tile more, about
+// lengths themselves.  In longer lists a segment counts a tile or two more, about
 // what its start and end cost.  A warp writes the result of a segment that is
 // all its own.  Of a piece at most the first and the last segment are shared
 // with other warps; their parts (m, l, unnormalised output) stay in shared
@@ -62,7 +62,7 @@ namespace {
 
 constexpr int kJoin = 16;              // pieces joined by one CTA
 constexpr int kBatch = 4;              // pieces whose loads are in flight together
-constexpr int kWeighFrom = 4;          // tiles per warp from which on a segment counts one more
+constexpr int kWeighFrom = 4;          // tiles per warp from which on segments count more than their tiles
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLag = 8.f;            // log2 of the largest weight, before its scale
 constexpr float kWeightBits = 7.f;     // e4m3: weights are scaled by 2^7, to 2^15 at most
@@ -74,6 +74,7 @@ struct Shape {
   static constexpr int D = D_, MH = MH_, KM = KM_, NS = NS_, CTAS = CTAS_;
   static constexpr int kWarps = kWarps_, kThreads = 32 * kWarps;
   static constexpr int kKeys = 16 * KM;                          // keys of a tile
+  static constexpr int kExtra = MH > 8 ? 2 : 1;                  // what a segment's start and end count for, in tiles
   static constexpr bool E4M3 = E4M3_;
   static constexpr int NT = MH / 8;                           // columns of 8 heads
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
     // ones after them.
     const uint32_t n_warps = min(W, gridDim.x * kWarps), me = blockIdx.x * kWarps + warp;
     if (blockIdx.x * kWarps >= n_warps) return;
-    extra = W >= kWeighFrom * kWarps * gridDim.x ? 1 : 0;
+    extra = W >= kWeighFrom * kWarps * gridDim.x ? S::kExtra : 0;
     const auto units_of = [&](uint32_t tiles, int segments) { return tiles + (uint32_t)(extra * segments); };
     cut = Cut(units_of(W, a.n_groups * a.B), n_warps);
     unit = cut.start(me);
@@ -405,11 +406,12 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
       cu.tile = (int)r - vh * (cu.s.n + extra);
       cu.ch = vh / a.groups_per_kv;
       cu.hg = vh - cu.ch * a.groups_per_kv;
-      if (cu.tile == cu.s.n) {  // it begins with a segment's extra unit
-        --left;
-        ++unit;
-        --cu.tile;
-        cu.next(a);
+      if (cu.tile >= cu.s.n) {  // it begins with a segment's extra units
+        const int skip = cu.s.n + extra - cu.tile;
+        left -= skip;
+        unit += skip;
+        cu.tile = cu.s.n - 1;
+        if (left > 0) cu.next(a);
       }
     }
   }
