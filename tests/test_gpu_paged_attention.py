@@ -579,3 +579,71 @@ def test_python_layer_refusals():
     assert attn.decode(none, cache, table[:0], lens[:0]).shape == (0, 4, 64)
     attn.write(cache, none[:, :2], none[:, :2], slots[:0])
     assert attn.status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nh,nkv,d", [(8, 2, 64), (12, 12, 128), (16, 1, 128), (5, 1, 256), (40, 2, 64), (18, 1, 256)])
+def test_decode_both_ways_of_small_calls(nh, nkv, d, fmt):
+    """A page table that only just covers the lengths (clusters of CTAs per
+    segment) and one that could hold far longer sequences (the cut list): the
+    oracle's result both times, to the same bits every time."""
+    attn = DecodeAttention(nh, nkv, d)
+    for lens in ([1, 1000], [500, 0, 33], [64], [2, 31, 32, 33]):
+        for width in (None, 2000):
+            b = Batch(lens, nh, nkv, d, fmt, 16, seed=nh + len(lens), width=width)
+            one = b.check(attn, softcap=20.0)
+            again = b.run(attn, softcap=20.0)
+            assert torch.equal(one[0], again[0]) and torch.equal(one[1], again[1])
+            b.check(attn, starts=torch.tensor([5] * len(lens), dtype=torch.int32, device=DEV), window=300)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_contexts_on_two_streams(fmt):
+    """Contexts of their own on streams of their own, at the same time: the
+    bits that each gives alone."""
+    batches = [Batch([3000, 10, 700], 8, 2, 128, fmt, 32, seed=1), Batch([900] * 6, 4, 4, 64, fmt, 16, seed=2)]
+    attns = [DecodeAttention(b.nh, b.nkv, b.d) for b in batches]
+    alone = [b.run(a)[0].clone() for a, b in zip(attns, batches)]
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    outs = [[torch.empty_like(w) for _ in range(10)] for w in alone]
+    for i in range(10):
+        for a, b, s, o in zip(attns, batches, streams, outs):
+            a.decode(b.q, b.cache, b.table, b.seq_lens, out=o[i], stream=s)
+    torch.cuda.synchronize()
+    for w, o in zip(alone, outs):
+        assert all(torch.equal(w, x) for x in o)
+    assert all(a.status() == 0 for a in attns)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_example_step(fmt):
+    """The example block: MoE beside the attention on another stream gives the
+    bits of one stream, and the attention the oracle's result."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "scmoe_paged_decode.py")
+    spec = importlib.util.spec_from_file_location("scmoe_paged_decode", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    blocks = [ex.Block(3, 200, fmt, seed=4) for _ in range(2)]
+    x = randn(gen(5), 3, blocks[0].hidden)
+    for b in blocks:
+        b.prompt(torch.tensor([150, 0, 33]))
+    for _ in range(3):
+        y = [b.step(x, overlap=i == 0) for i, b in enumerate(blocks)]
+        assert torch.equal(y[0], y[1]) and torch.isfinite(y[0]).all()
+    b = blocks[0]
+    assert b.attn.status() == 0 and b.moe.status() == 0 and b.pos.tolist() == [153, 3, 36]
+    # the third step's attention again, from what the cache holds
+    qkv = (x @ b.w_qkv.T).view(3, -1, b.d)
+    q, _ = b.attn.norm_rope(*b._heads(qkv)[:2], b.pos - 1, b.q_norm, b.k_norm)
+    out = b.attn.decode(q, b.cache, b.table, b.pos)
+    K, V = [], []
+    for s, n in enumerate(b.pos.tolist()):
+        j = torch.arange(n, device=DEV)
+        k, v = b.attn.read(b.cache, b.table[s].long()[j // ex.PAGE] * ex.PAGE + j % ex.PAGE)
+        K.append(f64(k))
+        V.append(f64(v))
+    want, _, mag, _ = P.decode(f64(q), K, V, b.pos.tolist())
+    close(out, want, 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * mag)
