@@ -27,7 +27,11 @@
 // Small calls.  Where every segment can have CTAs of its own, and no warp more
 // than a few tiles, what counts is the time before the first key and after the
 // last.  Then a cluster of up to 8 CTAs takes one segment: no list and no
-// workspace, its 32 warps' parts are joined through distributed shared memory.
+// workspace.  Each CTA of the cluster joins a share of the outputs, and every warp
+// pushes its part of each share into that CTA's shared memory, so that one barrier
+// of the cluster is all that stands between the last key and the result (one
+// sequence of 1000, 32 heads over 8, bf16: 6.0 us; parts kept and pulled by the
+// joining CTA, with a second barrier before the end, 7.9).
 //
 // Tile.  Rows come through a ring of cp.async stages of each warp's own.
 // S^T = K Q^T and O^T = V^T P^T run as mma.sync m16n8k16: 16 keys, then 16
@@ -90,7 +94,8 @@ struct Shape {
   static constexpr int kPartRow = MH * (D + 4) * 4 <= NS * kStage ? D + 4 : D;
   static constexpr int kPart = MH * kPartRow * 4;
   static_assert(kPart <= NS * kStage, "a part fits the ring");
-  static_assert(kWarps <= 8, "parts of a cluster have a lane each");
+  static_assert(MH * D / 4 < 1024, "items of a segment");
+  static_assert(kWarps <= 8, "a cluster has up to 32 warps");
   // shared memory: rings, first parts, (m, l) of both parts, their segments,
   // the segments shared with other CTAs, running sums of tiles
   static constexpr int kParts = kRing, kMl = kParts + kWarps * kPart, kSegs = kMl + 2 * kWarps * MH * 8;
@@ -292,7 +297,8 @@ __device__ __forceinline__ void add_parts(float &mm, float &ll, float4 &v, float
   }
 }
 
-template <class S>
+// CLUSTER: a cluster of a.cluster CTAs per segment, else the list of tiles.
+template <class S, bool CLUSTER>
 __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int D = S::D, MH = S::MH, NT = S::NT, NS = S::NS, EV = S::EV, KM = S::KM;
   constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kKeys = S::kKeys;
@@ -323,10 +329,13 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
     return v;
   };
   uint32_t unit = 0;
+  int my_part = 0;          // of a cluster's segment
   int left = 0, extra = 0;  // tiles and units of this warp's piece that are left
   Cut cut;
   Cursor<kKeys> cu{};
-  if (a.cluster > 0) {  // ---- a cluster per segment, its tiles cut over its warps
+  if constexpr (CLUSTER) {  // ---- a cluster per segment, its tiles cut over its warps
+    // (waited for before anything is pushed to a CTA that may not have begun)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int seg = blockIdx.x / a.cluster, vh = seg % a.n_groups;
     cu.b = seg / a.n_groups;
     cu.ch = vh / a.groups_per_kv;
@@ -334,9 +343,9 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
     count(cu.b);
     cu.s = span_of<kKeys>(a, cu.b);
     const Cut tiles(cu.s.n, a.cluster * kWarps);
-    const int me = (blockIdx.x - seg * a.cluster) * kWarps + warp;
-    cu.tile = (int)tiles.start(me);
-    left = (int)tiles.start(me + 1) - cu.tile;
+    my_part = (blockIdx.x - seg * a.cluster) * kWarps + warp;
+    cu.tile = (int)tiles.start(my_part);
+    left = (int)tiles.start(my_part + 1) - cu.tile;
     unit = cu.tile;
   } else {
     const int per = a.B <= kThreads ? 1 : (a.B + kThreads - 1) / kThreads;
@@ -501,6 +510,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
       }
     }
   };
+  if (CLUSTER && left > 0) fetch_q(cu);
   fetch_page();
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
@@ -823,6 +833,56 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
         if (g == 0 && a.lse) a.lse[bh] = lse_of(m[n][u], ll);
       }
   };
+  // How a cluster shares a segment's float4 items out: `share` to a CTA, which
+  // touch at most `span` heads.
+  struct Shares {
+    int items, share, span;
+    uint32_t mul;  // the CTA of item i is i * mul >> 20 (items < 1024)
+  };
+  const auto shares_of = [&](int heads) {
+    Shares z;
+    z.items = heads * (D / 4);
+    z.share = z.items / a.cluster;
+    z.span = z.share / (D / 4) + (z.share % (D / 4) == 0 ? 0 : 2);
+    z.mul = ((1u << 20) * a.cluster + z.items - 1) / z.items;
+    return z;
+  };
+  const auto in_cta = [&](int byte, int rank) {  // a place in the shared memory of a CTA of the cluster
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(smem) + byte), "r"(rank));
+    return at;
+  };
+  auto push_part = [&]() {
+    const int heads = min(a.group, G - cu.hg * a.group);
+    const Shares z = shares_of(heads);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float ll = total(n, u), f = under_m(n, u);
+        const int h = 8 * n + 2 * c + u;
+        if (h >= heads) continue;
+#pragma unroll
+        for (int hh = 0; hh < S::H; ++hh)
+#pragma unroll
+          for (int jj = 0; jj < EV / 4; ++jj) {
+            const int i = h * (D / 4) + (g + 8 * hh) * (EV / 4) + jj, rank = (int)((i * z.mul) >> 20);
+            const float *x = o[n][EV / 2 * hh + 2 * jj], *y = o[n][EV / 2 * hh + 2 * jj + 1];
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             in_cta(S::kParts + (my_part * z.share + i - rank * z.share) * 16, rank)),
+                         "f"(x[u] * f), "f"(x[2 + u] * f), "f"(y[u] * f), "f"(y[2 + u] * f)
+                         : "memory");
+          }
+        if (g == 0) {  // (m, l) to all that share the head
+          const int last = (int)(((h * (D / 4) + D / 4 - 1) * z.mul) >> 20);
+          for (int rank = (int)((h * (D / 4) * z.mul) >> 20); rank <= last; ++rank)
+            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
+                             in_cta(S::kMl + (my_part * z.span + h - rank * z.share / (D / 4)) * 8, rank)),
+                         "f"(m[n][u]), "f"(ll)
+                         : "memory");
+        }
+      }
+  };
   // Where part `which` (0: the first of a piece, 1: the last) of a warp lies.
   const auto part_at = [&](int w, int which) {
     return reinterpret_cast<float *>(smem + (which == 0 ? S::kParts + w * S::kPart : w * (NS * S::kStage)));
@@ -880,78 +940,92 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
       write_whole();
     } else {
       const int which = left > 0 ? 0 : 1;
-      if (which == 1) {
-        copy_wait<0>();
-        __syncwarp();  // the ring is free
+      if constexpr (CLUSTER) {
+        __syncwarp();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        push_part();
+      } else {
+        if (which == 1) {
+          copy_wait<0>();
+          __syncwarp();  // the ring is free
+        }
+        keep_part(which, unit0);
       }
-      keep_part(which, unit0);
     }
     --cu.tile;
     if (left > 0) cu.next(a);
   }
   copy_wait<0>();
-  __syncthreads();
-
-  if (a.cluster > 0) {
+  if constexpr (CLUSTER) {
     const int parts = min(cu.s.n, a.cluster * kWarps);  // the first warps have one each
-    if (parts == 1) return;                             // written whole
     __syncwarp();
+    // those without a part, or with the whole, have not waited yet
+    if (my_part >= parts || parts == 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (parts == 1) return;
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
     const int in_kv = cu.hg * a.group, heads = min(a.group, G - in_kv);
     const int64_t head0 = (int64_t)cu.b * a.n_heads + cu.ch * G + in_kv;
-    // a lane per part, as many lanes as the cluster has warps (a power of two)
-    // per float4 item of a head
-    const int width = a.cluster * kWarps, mine = lane & (width - 1);
-    uint32_t x_at, ml_at;
-    const uint32_t rank = mine / kWarps, w = mine % kWarps;
-    // all five steps, without branches, so that the sums below overlap
-    const auto sum = [&](float v) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float x = __shfl_xor_sync(0xffffffffu, v, o);
-        v = o < width ? v + x : v;
-      }
-      return v;
-    };
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x_at) : "r"(smem_addr(part_at(w, 1))), "r"(rank));
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ml_at) : "r"(smem_addr(ml + (2 * w + 1) * MH)), "r"(rank));
-    const int at_once = 32 / width, items = heads * (D / 4);
-    const int first = ((blockIdx.x % a.cluster) * kWarps + warp) * at_once;
-#pragma unroll 2
-    for (int base = first; base < items; base += width * at_once) {
-      const int i = base + lane / width;
+    const Shares z = shares_of(heads);
+    const int rank = blockIdx.x % a.cluster, i0 = rank * z.share;
+    // `lanes` (a power of two) neighbouring lanes per item, a part each at a time
+    int lanes = 1;
+    while (2 * lanes * z.share <= kThreads && 2 * lanes <= min(32, parts)) lanes *= 2;
+    const int sub = threadIdx.x & (lanes - 1);
+#pragma unroll 1
+    for (int base = 0; base < z.share; base += kThreads / lanes) {
+      const int j = base + threadIdx.x / lanes, i = i0 + min(j, z.share - 1);
       const int h = i / (D / 4), it = i % (D / 4);
+      const float4 *x_at = reinterpret_cast<const float4 *>(smem + S::kParts) + (i - i0);
+      const float2 *ml_at = ml + (h - i0 / (D / 4));
       float mm = -INFINITY, ll = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (mine < parts && i < items) {
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(mm), "=f"(ll) : "r"(ml_at + 8 * h));
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                     : "r"(x_at + (h * S::kPartRow + 4 * it) * 4));
+#pragma unroll 1
+      for (int p = sub; p < parts; p += 4 * lanes) {
+        float2 st[4];
+        float4 x[4];
+        float top = mm;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int k = p + q * lanes;
+          st[q] = k < parts ? ml_at[k * z.span] : make_float2(-INFINITY, 0.f);
+          x[q] = k < parts ? x_at[k * z.share] : make_float4(0.f, 0.f, 0.f, 0.f);
+          top = fmaxf(top, st[q].x);
+        }
+        add_parts<4>(mm, ll, v, top, st, x);
       }
+      // all five steps, without branches, so that the sums overlap
       float top = mm;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
-        const float x = __shfl_xor_sync(0xffffffffu, top, o);
-        top = o < width ? fmaxf(top, x) : top;
+        const float t = __shfl_xor_sync(0xffffffffu, top, o);
+        top = o < lanes ? fmaxf(top, t) : top;
       }
       const float f = rescale(mm, top);
-      ll = sum(f * ll);
-      const float inv = ll == 0.f ? 0.f : 1.f / ll;
-      v = make_float4(sum(v.x * f) * inv, sum(v.y * f) * inv, sum(v.z * f) * inv, sum(v.w * f) * inv);
-      if (mine == 0 && i < items) {
-        uint2 o2;
-        o2.x = pack2<false>(v.x, v.y);
-        o2.y = pack2<false>(v.z, v.w);
-        *reinterpret_cast<uint2 *>(a.out + (head0 + h) * D + 4 * it) = o2;
+      ll *= f;
+      v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float t = __shfl_xor_sync(0xffffffffu, ll, o), tx = __shfl_xor_sync(0xffffffffu, v.x, o),
+                    ty = __shfl_xor_sync(0xffffffffu, v.y, o), tz = __shfl_xor_sync(0xffffffffu, v.z, o),
+                    tw = __shfl_xor_sync(0xffffffffu, v.w, o);
+        if (o < lanes) {
+          ll += t;
+          v = make_float4(v.x + tx, v.y + ty, v.z + tz, v.w + tw);
+        }
+      }
+      if (sub == 0 && j < z.share) {
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        uint2 w;
+        w.x = pack2<false>(v.x * inv, v.y * inv);
+        w.y = pack2<false>(v.z * inv, v.w * inv);
+        *reinterpret_cast<uint2 *>(a.out + (head0 + h) * D + 4 * it) = w;
         if (it == 0 && a.lse) a.lse[head0 + h] = lse_of(top, ll);
       }
     }
-    __syncwarp();
-    // nobody leaves while its parts are read
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
     return;
   }
+  __syncthreads();
+
   // ---- the CTA's shared segments
   float4 *part = reinterpret_cast<float4 *>(a.part);
   float2 *part_ml = reinterpret_cast<float2 *>(a.part_ml);
@@ -1091,7 +1165,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
   }
 }
 
-template <class S>
+template <class S, bool CLUSTER>
 cudaError_t launch_shape(const DecodeArgs &a, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -1106,15 +1180,22 @@ cudaError_t launch_shape(const DecodeArgs &a, int grid, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, decode_kernel<S>, a);
+  return cudaLaunchKernelEx(&cfg, decode_kernel<S, CLUSTER>, a);
 }
 template <class S>
 cudaError_t plan_shape(int *ctas_per_sm, int *tile, int *warps) {
   *tile = S::kKeys;
   *warps = S::kWarps;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-  if (e != cudaSuccess) return e;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_kernel<S>, S::kThreads, S::kSmem);
+  int n[2] = {0, 0};
+  const auto plan = [](auto kernel, int *fit) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(fit, kernel, S::kThreads, S::kSmem);
+  };
+  cudaError_t e = plan(decode_kernel<S, false>, &n[0]);
+  if (e == cudaSuccess) e = plan(decode_kernel<S, true>, &n[1]);
+  *ctas_per_sm = n[0] < n[1] ? n[0] : n[1];
+  return e;
 }
 
 // Calls f with the shape of (d, e4m3, heads of a group).
@@ -1164,7 +1245,10 @@ cudaError_t plan_paged_decode(int d, bool e4m3, int group, int *ctas_per_sm, int
 }
 
 cudaError_t launch_paged_decode(const DecodeArgs &a, int d, bool e4m3, int grid, cudaStream_t s) {
-  return with_shape(d, e4m3, a.group, [&](auto sh) { return launch_shape<decltype(sh)>(a, grid, s); });
+  return with_shape(d, e4m3, a.group, [&](auto sh) {
+    return a.cluster > 0 ? launch_shape<decltype(sh), true>(a, grid, s)
+                         : launch_shape<decltype(sh), false>(a, grid, s);
+  });
 }
 
 }  // namespace fp8moe
