@@ -39,7 +39,6 @@ bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 constexpr int64_t kMaxBatch = 1 << 20;
 constexpr int64_t kMaxPositions = 0x7fffffff - 63;
 constexpr int64_t kMaxTokens = 0x7fffffff;
-constexpr int64_t kClusterTiles = 4;
 
 int check_config(const moe_attn_config &c) {
   if (c.n_kv_heads < 1 || c.n_heads < c.n_kv_heads || c.n_heads > 1024 ||
@@ -398,15 +397,24 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   if (tiles > INT64_C(1) << 29) return MOE_ERR_SHAPE;
   const int ctas = a->ctas[kv->format], warps = a->warps[kv->format];
   int grid = tiles < ctas ? (int)tiles : ctas;
-  // Clusters of CTAs per segment, as many CTAs as give each warp a tile of the
-  // longest sequence, up to 8; where they would not all be resident, or a warp
-  // would have more than kClusterTiles, the list is cut instead.
-  const int64_t per_segment = (r.capacity + tile - 1) / tile;
+  // Clusters of CTAs per segment: as many CTAs as give each warp a tile of the
+  // longest sequence, 32 warps at most, and no more than are resident.  The list,
+  // which balances lengths and uses all SMs, is cut instead where a warp would
+  // have more than 4 tiles, or 8 with clusters on a third of the SMs or more.
+  // Four heads of 128 elements per key/value head, bf16, list against cluster:
+  //   one sequence of 2000, 8 key/value heads    10.8 us,  7.1 (2 tiles per warp)
+  //   of 8000                                    16.5,    14.1 (8)
+  //   of 16000                                   21.8,    23.8 (16)
+  //   of 4000, 4 key/value heads (32 CTAs)       12.0,     9.1 (4)
+  //   of 6000                                    10.2,    11.1 (6)
+  //   32 sequences of up to 500, 8 heads         11.8,    10.0 (4, clusters of one)
+  const int64_t per_segment = (r.capacity + tile - 1) / tile, segments = B * r.n_groups;
   int size = 1;
-  while (size < 8 && size * warps < 32 && size * warps < per_segment) size *= 2;
-  if (per_segment <= kClusterTiles * size * warps && B * r.n_groups * size <= ctas) {
+  while (size < 8 && size * warps < 32 && size * warps < per_segment && 2 * size * segments <= ctas) size *= 2;
+  const int64_t most = 3 * size * segments >= a->sms ? 8 : 4;
+  if (per_segment <= most * size * warps && size * segments <= ctas) {
     r.cluster = size;
-    grid = (int)B * r.n_groups * size;
+    grid = (int)(size * segments);
   }
   ATTN_TRY(launch_paged_decode(r, c.head_dim, kv->format == MOE_KV_E4M3, grid, s));
   return MOE_OK;

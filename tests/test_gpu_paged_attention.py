@@ -598,6 +598,22 @@ def test_decode_both_ways_of_small_calls(nh, nkv, d, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nh,nkv,d,B", [(32, 8, 64, 5), (12, 6, 128, 12), (36, 4, 128, 9), (8, 8, 64, 30), (60, 4, 64, 35),
+                                        (5, 5, 256, 25), (16, 16, 128, 19)])
+def test_decode_clusters_of_all_sizes(nh, nkv, d, B, fmt):
+    """As many segments as leave clusters of eight, four, two CTAs or one,
+    lengths from none to some tiles per warp: the oracle's result, to the same
+    bits every time."""
+    attn = DecodeAttention(nh, nkv, d)
+    for S in (40, 300, 900):
+        lens = [S * (i + 1) // B if i % 5 != 3 else i % 2 for i in range(B)]
+        b = Batch(lens, nh, nkv, d, fmt, 16, seed=S + B)
+        one = b.check(attn)
+        again = b.run(attn)
+        assert torch.equal(one[0], again[0]) and torch.equal(one[1], again[1])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_contexts_on_two_streams(fmt):
     """Contexts of their own on streams of their own, at the same time: the
     bits that each gives alone."""
