@@ -1,5 +1,6 @@
 // C ABI of the attention over a paged key/value cache: context, argument
 // checks and launches.  See include/fp8moe.h for the contract.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -20,6 +21,7 @@ struct moe_attn {
   // moe_attn_decode: CTAs of a launch, positions of a tile and warps of a CTA (by
   // format), and its workspace
   int ctas[2] = {0, 0}, tile[2] = {1, 1}, warps[2] = {1, 1};
+  int clusters[2][4] = {};    // resident clusters of 1, 2, 4 and 8 CTAs
   int group = 1, max_ctas = 0;
   int *counters = nullptr;    // [3][max_ctas], zero between calls
   float *part_ml = nullptr;   // [2 * max_ctas][group][2]
@@ -174,13 +176,15 @@ int moe_attn_init(moe_attn **out, const moe_attn_config *cfg) {
   for (int f = 0; f < 2; ++f) {
     int per_sm = 0;
     if (plan_paged_decode(cfg->head_dim, f == MOE_KV_E4M3, a->group, &per_sm, &a->tile[f],
-                          &a->warps[f]) != cudaSuccess ||
+                          &a->warps[f], a->clusters[f]) != cudaSuccess ||
         per_sm < 1) {
       cudaGetLastError();
       delete a;
       return MOE_ERR_CUDA;
     }
     a->ctas[f] = per_sm * use;
+    a->clusters[f][0] = a->ctas[f];
+    for (int i = 1; i < 4; ++i) a->clusters[f][i] = std::min(a->clusters[f][i], a->ctas[f] >> i);
     if (a->ctas[f] > a->max_ctas) a->max_ctas = a->ctas[f];
   }
   const int half = cfg->rope_dim / 2;
@@ -398,23 +402,40 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   const int ctas = a->ctas[kv->format], warps = a->warps[kv->format];
   int grid = tiles < ctas ? (int)tiles : ctas;
   // Clusters of CTAs per segment: as many CTAs as give each warp a tile of the
-  // longest sequence, 32 warps at most, and no more than are resident.  The list,
-  // which balances lengths and uses all SMs, is cut instead where a warp would
-  // have more than 4 tiles, or 8 with clusters on a third of the SMs or more.
-  // Four heads of 128 elements per key/value head, bf16, list against cluster:
+  // longest sequence, 32 warps at most, and no more than are resident.  Where a
+  // warp would have more than 4 tiles, several clusters share a segment, so that
+  // it has 3; but not for groups of more than 8 heads, whose tiles take twice as
+  // long, and no more than 8/9 of the clusters that fit, since those that wait for
+  // the launch before to leave come too late.  The list, which balances lengths
+  // and uses all SMs, is cut instead where a warp would have more than 8 tiles,
+  // 16 of a sequence alone, or 4 with clusters on less than a third of the SMs.
+  // Four heads of 128 elements per key/value head, bf16, list against clusters:
   //   one sequence of 2000, 8 key/value heads    10.8 us,  7.1 (2 tiles per warp)
-  //   of 8000                                    16.5,    14.1 (8)
-  //   of 16000                                   21.8,    23.8 (16)
+  //   of 8000                                    16.5,    11.8 (13.6 unsplit)
+  //   of 16000                                   22.3,    17.9
+  //   of 64000                                   47.5,    44.6 (16 tiles)
   //   of 4000, 4 key/value heads (32 CTAs)       12.0,     9.1 (4)
-  //   of 6000                                    10.2,    11.1 (6)
+  //   4 sequences of up to 16000, 4 heads        23.4,    20.9 (8)
+  //   of up to 32000                             32.6,    33.4 (16)
   //   32 sequences of up to 500, 8 heads         11.8,    10.0 (4, clusters of one)
+  // and with 16 heads, one key/value head, e4m3:
+  //   one sequence of 16000                      15.1,    15.3
+  //   of 200001                                  26.7,    27.8
   const int64_t per_segment = (r.capacity + tile - 1) / tile, segments = B * r.n_groups;
-  int size = 1;
-  while (size < 8 && size * warps < 32 && size * warps < per_segment && 2 * size * segments <= ctas) size *= 2;
-  const int64_t most = 3 * size * segments >= a->sms ? 8 : 4;
-  if (per_segment <= most * size * warps && size * segments <= ctas) {
-    r.cluster = size;
-    grid = (int)(size * segments);
+  const int *fit = a->clusters[kv->format];
+  int k = 0;
+  while (k < 3 && (warps << k) < 32 && (warps << k) < per_segment && segments <= fit[k + 1]) ++k;
+  if (segments <= fit[k]) {
+    const int64_t wide = warps << k;
+    int64_t splits = 1;
+    if (per_segment > 4 * wide && a->group <= 8)
+      splits = std::max<int64_t>(1, std::min((per_segment + 3 * wide - 1) / (3 * wide), (fit[k] - fit[k] / 9) / segments));
+    const int64_t most = 3 * (splits * segments << k) < a->sms ? 4 : B == 1 ? 16 : 8;
+    if (per_segment <= most * wide * splits) {
+      r.cluster = 1 << k;
+      r.splits = (int)splits;
+      grid = (int)(splits * segments << k);
+    }
   }
   ATTN_TRY(launch_paged_decode(r, c.head_dim, kv->format == MOE_KV_E4M3, grid, s));
   return MOE_OK;

@@ -24,14 +24,17 @@
 // parts' places, so results do not depend on the order of arrival.  No CTA
 // waits for another.
 //
-// Small calls.  Where every segment can have CTAs of its own, and no warp more
-// than a few tiles, what counts is the time before the first key and after the
-// last.  Then a cluster of up to 8 CTAs takes one segment: no list and no
-// workspace.  Each CTA of the cluster joins a share of the outputs, and every warp
-// pushes its part of each share into that CTA's shared memory, so that one barrier
-// of the cluster is all that stands between the last key and the result (one
-// sequence of 1000, 32 heads over 8, bf16: 6.0 us; parts kept and pulled by the
-// joining CTA, with a second barrier before the end, 7.9).
+// Few sequences.  Where every segment can have CTAs of its own, and no warp more
+// than some tiles, what counts is the time before the first key and after the
+// last.  Then a cluster of up to 8 CTAs takes one segment, or several clusters
+// do: no list to search.  Each CTA of a cluster joins a share of the outputs, and
+// every warp pushes its part of each share into that CTA's shared memory, so that
+// one barrier of the cluster is all that stands between the last key and the
+// cluster's result (one sequence of 1000, 32 heads over 8, bf16: 6.0 us; parts
+// kept and pulled by the joining CTA, with a second barrier before the end, 7.9).
+// Several clusters leave their results in the workspace, and the last CTA of
+// those with the same share joins them (one sequence of 16000: 18.2 us, cut as a
+// list 22.3).
 //
 // Tile.  Rows come through a ring of cp.async stages of each warp's own.
 // S^T = K Q^T and O^T = V^T P^T run as mma.sync m16n8k16: 16 keys, then 16
@@ -297,7 +300,7 @@ __device__ __forceinline__ void add_parts(float &mm, float &ll, float4 &v, float
   }
 }
 
-// CLUSTER: a cluster of a.cluster CTAs per segment, else the list of tiles.
+// CLUSTER: a.splits clusters of a.cluster CTAs per segment, else the list of tiles.
 template <class S, bool CLUSTER>
 __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int D = S::D, MH = S::MH, NT = S::NT, NS = S::NS, EV = S::EV, KM = S::KM;
@@ -333,19 +336,20 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
   int left = 0, extra = 0;  // tiles and units of this warp's piece that are left
   Cut cut;
   Cursor<kKeys> cu{};
-  if constexpr (CLUSTER) {  // ---- a cluster per segment, its tiles cut over its warps
+  if constexpr (CLUSTER) {  // ---- the tiles of a segment, cut over the warps of its clusters
     // (waited for before anything is pushed to a CTA that may not have begun)
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    const int seg = blockIdx.x / a.cluster, vh = seg % a.n_groups;
+    const int seg = blockIdx.x / (a.splits * a.cluster), vh = seg % a.n_groups;
     cu.b = seg / a.n_groups;
     cu.ch = vh / a.groups_per_kv;
     cu.hg = vh - cu.ch * a.groups_per_kv;
     count(cu.b);
     cu.s = span_of<kKeys>(a, cu.b);
-    const Cut tiles(cu.s.n, a.cluster * kWarps);
-    my_part = (blockIdx.x - seg * a.cluster) * kWarps + warp;
-    cu.tile = (int)tiles.start(my_part);
-    left = (int)tiles.start(my_part + 1) - cu.tile;
+    const Cut tiles(cu.s.n, a.splits * a.cluster * kWarps);
+    const int me = (blockIdx.x - seg * a.splits * a.cluster) * kWarps + warp;
+    cu.tile = (int)tiles.start(me);
+    left = (int)tiles.start(me + 1) - cu.tile;
+    my_part = me % (a.cluster * kWarps);
     unit = cu.tile;
   } else {
     const int per = a.B <= kThreads ? 1 : (a.B + kThreads - 1) / kThreads;
@@ -955,73 +959,116 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
     --cu.tile;
     if (left > 0) cu.next(a);
   }
+  // Counts a part that all threads have written; true for the last.
+  const auto arrive = [&](int *counter, int n) {
+    int before;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    if (before == n - 1) *counter = 0;  // for the next call
+    return before == n - 1;
+  };
   copy_wait<0>();
   if constexpr (CLUSTER) {
-    const int parts = min(cu.s.n, a.cluster * kWarps);  // the first warps have one each
+    // the segment's first warps have a part each
+    const int warps = a.cluster * kWarps, clusters = min((cu.s.n + warps - 1) / warps, a.splits);
+    const int cluster_at = blockIdx.x / a.cluster, nth = cluster_at % a.splits;
+    const int parts = min(max(cu.s.n - nth * warps, 0), warps);
+    const bool whole = cu.s.n == 1;
     __syncwarp();
     // those without a part, or with the whole, have not waited yet
-    if (my_part >= parts || parts == 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (parts == 1) return;
+    if (my_part >= parts || whole) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (parts == 0 || whole) return;
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
     const int in_kv = cu.hg * a.group, heads = min(a.group, G - in_kv);
     const int64_t head0 = (int64_t)cu.b * a.n_heads + cu.ch * G + in_kv;
     const Shares z = shares_of(heads);
     const int rank = blockIdx.x % a.cluster, i0 = rank * z.share;
-    // `lanes` (a power of two) neighbouring lanes per item, a part each at a time
-    int lanes = 1;
-    while (2 * lanes * z.share <= kThreads && 2 * lanes <= min(32, parts)) lanes *= 2;
-    const int sub = threadIdx.x & (lanes - 1);
+    // Joins n parts of this CTA's items with `lanes` (a power of two) neighbouring
+    // lanes per item, a part each at a time; load(part, head, item of the segment,
+    // (m, l), piece), store(head, item of the head, piece, m, l).
+    const auto join = [&](int n, const auto &load, const auto &store) {
+      int lanes = 1;
+      while (2 * lanes * z.share <= kThreads && 2 * lanes <= min(32, n)) lanes *= 2;
+      const int sub = threadIdx.x & (lanes - 1);
 #pragma unroll 1
-    for (int base = 0; base < z.share; base += kThreads / lanes) {
-      const int j = base + threadIdx.x / lanes, i = i0 + min(j, z.share - 1);
-      const int h = i / (D / 4), it = i % (D / 4);
-      const float4 *x_at = reinterpret_cast<const float4 *>(smem + S::kParts) + (i - i0);
-      const float2 *ml_at = ml + (h - i0 / (D / 4));
-      float mm = -INFINITY, ll = 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int base = 0; base < z.share; base += kThreads / lanes) {
+        const int j = base + threadIdx.x / lanes, i = i0 + min(j, z.share - 1);
+        const int h = i / (D / 4), it = i % (D / 4);
+        float mm = -INFINITY, ll = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-      for (int p = sub; p < parts; p += 4 * lanes) {
-        float2 st[4];
-        float4 x[4];
+        for (int p = sub; p < n; p += 4 * lanes) {
+          float2 st[4];
+          float4 x[4];
+          float top = mm;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            st[q] = make_float2(-INFINITY, 0.f);
+            x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p + q * lanes < n) load(p + q * lanes, h, i, st[q], x[q]);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) top = fmaxf(top, st[q].x);
+          add_parts<4>(mm, ll, v, top, st, x);
+        }
+        // all five steps, without branches, so that the sums overlap
         float top = mm;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int k = p + q * lanes;
-          st[q] = k < parts ? ml_at[k * z.span] : make_float2(-INFINITY, 0.f);
-          x[q] = k < parts ? x_at[k * z.share] : make_float4(0.f, 0.f, 0.f, 0.f);
-          top = fmaxf(top, st[q].x);
+        for (int o = 16; o > 0; o >>= 1) {
+          const float t = __shfl_xor_sync(0xffffffffu, top, o);
+          top = o < lanes ? fmaxf(top, t) : top;
         }
-        add_parts<4>(mm, ll, v, top, st, x);
-      }
-      // all five steps, without branches, so that the sums overlap
-      float top = mm;
+        const float f = rescale(mm, top);
+        ll *= f;
+        v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float t = __shfl_xor_sync(0xffffffffu, top, o);
-        top = o < lanes ? fmaxf(top, t) : top;
-      }
-      const float f = rescale(mm, top);
-      ll *= f;
-      v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float t = __shfl_xor_sync(0xffffffffu, ll, o), tx = __shfl_xor_sync(0xffffffffu, v.x, o),
-                    ty = __shfl_xor_sync(0xffffffffu, v.y, o), tz = __shfl_xor_sync(0xffffffffu, v.z, o),
-                    tw = __shfl_xor_sync(0xffffffffu, v.w, o);
-        if (o < lanes) {
-          ll += t;
-          v = make_float4(v.x + tx, v.y + ty, v.z + tz, v.w + tw);
+        for (int o = 16; o > 0; o >>= 1) {
+          const float t = __shfl_xor_sync(0xffffffffu, ll, o), tx = __shfl_xor_sync(0xffffffffu, v.x, o),
+                      ty = __shfl_xor_sync(0xffffffffu, v.y, o), tz = __shfl_xor_sync(0xffffffffu, v.z, o),
+                      tw = __shfl_xor_sync(0xffffffffu, v.w, o);
+          if (o < lanes) {
+            ll += t;
+            v = make_float4(v.x + tx, v.y + ty, v.z + tz, v.w + tw);
+          }
         }
+        if (sub == 0 && j < z.share) store(h, it, i, v, top, ll);
       }
-      if (sub == 0 && j < z.share) {
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        uint2 w;
-        w.x = pack2<false>(v.x * inv, v.y * inv);
-        w.y = pack2<false>(v.z * inv, v.w * inv);
-        *reinterpret_cast<uint2 *>(a.out + (head0 + h) * D + 4 * it) = w;
-        if (it == 0 && a.lse) a.lse[head0 + h] = lse_of(top, ll);
-      }
+    };
+    const auto write = [&](int h, int it, int, float4 v, float mm, float ll) {
+      const float inv = ll == 0.f ? 0.f : 1.f / ll;
+      uint2 w;
+      w.x = pack2<false>(v.x * inv, v.y * inv);
+      w.y = pack2<false>(v.z * inv, v.w * inv);
+      *reinterpret_cast<uint2 *>(a.out + (head0 + h) * D + 4 * it) = w;
+      if (it == 0 && a.lse) a.lse[head0 + h] = lse_of(mm, ll);
+    };
+    const float4 *x_at = reinterpret_cast<const float4 *>(smem + S::kParts) - i0;
+    const float2 *ml_at = ml - i0 / (D / 4);
+    const auto pushed = [&](int p, int h, int i, float2 &st, float4 &x) {
+      st = ml_at[p * z.span + h];
+      x = x_at[p * z.share + i];
+    };
+    if (clusters == 1) {
+      join(parts, pushed, write);
+      return;
     }
+    // Several clusters: each CTA leaves what it joined in the workspace, the last
+    // of those with the same share joins them.
+    float4 *const part = reinterpret_cast<float4 *>(a.part);    // [cluster][group * D / 4]
+    float2 *const part_ml = reinterpret_cast<float2 *>(a.part_ml);  // [CTA][group]
+    const int64_t row = (int64_t)a.group * (D / 4);
+    join(parts, pushed, [&](int h, int it, int i, float4 v, float mm, float ll) {
+      part[cluster_at * row + i] = v;
+      if (it == 0 || i == i0) part_ml[(int64_t)blockIdx.x * a.group + h] = make_float2(mm, ll);
+    });
+    __syncthreads();
+    if (threadIdx.x == 0) shared[0].last = arrive(a.counters + cluster_at / a.splits * a.cluster + rank, clusters);
+    __syncthreads();
+    if (!shared[0].last) return;
+    const int64_t first = cluster_at - nth;
+    join(clusters, [&](int p, int h, int i, float2 &st, float4 &x) {
+      st = __ldcg(part_ml + ((first + p) * a.cluster + rank) * a.group + h);
+      x = __ldcg(part + (first + p) * row + i);
+    }, write);
     return;
   }
   __syncthreads();
@@ -1042,13 +1089,6 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
   // A CTA's slots of the workspace: 0 for a segment that began in another CTA,
   // 1 for one that begins here.
   const auto slot_of = [&](int first, int nth) { return 2 * (first + nth) + (nth == 0 ? 1 : 0); };
-  // Counts a part that all threads have written; true for the last.
-  const auto arrive = [&](int *counter, int n) {
-    int before;
-    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
-    if (before == n - 1) *counter = 0;  // for the next call
-    return before == n - 1;
-  };
   int n_shared = 0;
   const uint32_t valid = __ballot_sync(0xffffffffu, lane < 2 * kWarps && segs[lane & (2 * kWarps - 1)].valid);
   for (uint32_t rest = valid; rest != 0;) {
@@ -1165,14 +1205,13 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
   }
 }
 
-template <class S, bool CLUSTER>
-cudaError_t launch_shape(const DecodeArgs &a, int grid, cudaStream_t s) {
+template <class S>
+cudaLaunchConfig_t launch_config(const DecodeArgs &a, int grid, cudaStream_t s, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -1180,10 +1219,16 @@ cudaError_t launch_shape(const DecodeArgs &a, int grid, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+  return cfg;
+}
+template <class S, bool CLUSTER>
+cudaError_t launch_shape(const DecodeArgs &a, int grid, cudaStream_t s) {
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = launch_config<S>(a, grid, s, attr);
   return cudaLaunchKernelEx(&cfg, decode_kernel<S, CLUSTER>, a);
 }
 template <class S>
-cudaError_t plan_shape(int *ctas_per_sm, int *tile, int *warps) {
+cudaError_t plan_shape(int *ctas_per_sm, int *tile, int *warps, int (&clusters)[4]) {
   *tile = S::kKeys;
   *warps = S::kWarps;
   int n[2] = {0, 0};
@@ -1195,6 +1240,13 @@ cudaError_t plan_shape(int *ctas_per_sm, int *tile, int *warps) {
   cudaError_t e = plan(decode_kernel<S, false>, &n[0]);
   if (e == cudaSuccess) e = plan(decode_kernel<S, true>, &n[1]);
   *ctas_per_sm = n[0] < n[1] ? n[0] : n[1];
+  for (int i = 1; i < 4 && e == cudaSuccess; ++i) {
+    DecodeArgs a = {};
+    a.cluster = 1 << i;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = launch_config<S>(a, 1 << i, nullptr, attr);
+    e = cudaOccupancyMaxActiveClusters(&clusters[i], decode_kernel<S, true>, &cfg);
+  }
   return e;
 }
 
@@ -1240,8 +1292,10 @@ void decode_page_division(DecodeArgs *a) {
   a->whole_pages = d % 16 == 0;
 }
 
-cudaError_t plan_paged_decode(int d, bool e4m3, int group, int *ctas_per_sm, int *tile, int *warps) {
-  return with_shape(d, e4m3, group, [&](auto s) { return plan_shape<decltype(s)>(ctas_per_sm, tile, warps); });
+cudaError_t plan_paged_decode(int d, bool e4m3, int group, int *ctas_per_sm, int *tile, int *warps,
+                              int (&clusters)[4]) {
+  return with_shape(d, e4m3, group,
+                    [&](auto s) { return plan_shape<decltype(s)>(ctas_per_sm, tile, warps, clusters); });
 }
 
 cudaError_t launch_paged_decode(const DecodeArgs &a, int d, bool e4m3, int grid, cudaStream_t s) {

@@ -84,7 +84,8 @@ struct DecodeArgs {
   uint32_t page_mul;
   int page_shift;
   bool whole_pages;
-  int cluster;  // CTAs of a segment; 0: the list of all tiles is cut over the CTAs
+  int cluster;  // CTAs of a cluster; 0: the list of all tiles is cut over the CTAs
+  int splits;   // clusters of a segment
   // workspace: 2 * max_ctas pieces of group * d outputs and group (m, l)
   // pairs, 3 * max_ctas counters (zero between calls)
   float *part, *part_ml;
@@ -97,9 +98,10 @@ int decode_group(int heads_per_kv, int d);
 // Fills in page_mul, page_shift and whole_pages.
 void decode_page_division(DecodeArgs *a);
 // Readies the kernel; tells how many CTAs of it fit on an SM, the positions of
-// a tile and the warps of a CTA.  Launches take at most max_ctas CTAs and at most 2^29 tiles.
+// a tile, the warps of a CTA and how many clusters of 1, 2, 4 and 8 CTAs fit on
+// the device.  Launches take at most max_ctas CTAs and at most 2^29 tiles.
 cudaError_t plan_paged_decode(int d, bool e4m3, int group, int *ctas_per_sm, int *tile,
-                              int *warps);
+                              int *warps, int (&clusters)[4]);
 cudaError_t launch_paged_decode(const DecodeArgs &a, int d, bool e4m3, int grid, cudaStream_t s);
 
 }  // namespace fp8moe

@@ -614,6 +614,21 @@ def test_decode_clusters_of_all_sizes(nh, nkv, d, B, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nh,nkv,d,lens", [(4, 1, 64, [5000]), (7, 1, 128, [9000]), (6, 3, 128, [4097]), (8, 4, 256, [5001, 20]),
+                                           (16, 4, 64, [9001, 0, 129])])
+def test_decode_clusters_that_share_a_segment(nh, nkv, d, lens, fmt):
+    """Sequences long enough for several clusters, and lengths that leave some of
+    them nothing: the oracle's result, to the same bits every time."""
+    attn = DecodeAttention(nh, nkv, d)
+    for n in (lens, [x - x // 3 for x in lens], [min(x, 700) for x in lens], [min(x, 1) for x in lens]):
+        b = Batch(n, nh, nkv, d, fmt, 16, seed=nh + d, width=(max(lens) + 15) // 16)
+        one = b.check(attn)
+        again = b.run(attn)
+        assert torch.equal(one[0], again[0]) and torch.equal(one[1], again[1])
+        b.check(attn, starts=torch.tensor([9] * len(lens), dtype=torch.int32, device=DEV), window=3000)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_contexts_on_two_streams(fmt):
     """Contexts of their own on streams of their own, at the same time: the
     bits that each gives alone."""
