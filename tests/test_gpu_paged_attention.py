@@ -112,6 +112,23 @@ def test_norm_rope(T, nh, nkv, d, R, inter, norm):
     assert torch.equal(fused[:, 0], keep[:, 0]) and torch.equal(fused[:, nh + nkv + 1:], keep[:, nh + nkv + 1:])
 
 
+def test_rotation_close_to_quarter_turns():
+    """Positions whose angles lie next to quarter turns, where a sine or cosine
+    is small: right to its own bf16 digits.  Besides their rounding, the angle
+    is off by two units of 2^-64 turns per position and by f32 roundings of the
+    rest of a quarter turn, of which it and its sine are some 2^-22."""
+    pos = [11, 22, 333, 355, 710, 51819, 52174, 103993, 104348, 208341, 260515, 312689, 573204, 833719, 1146408, 4272943, 5419351]
+    pos = np.array(pos + [-p for p in pos], np.int32)
+    attn = {i: DecodeAttention(1, 1, 64, rope_freqs=[1.0] + [0.0] * 7, interleaved=i) for i in (False, True)}
+    x = torch.zeros(len(pos), 1, 64, dtype=torch.bfloat16, device=DEV)
+    x[..., 0] = 1.0
+    far = np.abs(pos.astype(np.float64)) * (2 * np.pi * 2.0 ** -63)
+    for inter, second in ((False, 8), (True, 1)):
+        for y in attn[inter].norm_rope(x, x, torch.from_numpy(pos).to(DEV)):
+            for at, want in ((0, np.cos(pos.astype(np.float64))), (second, np.sin(pos.astype(np.float64)))):
+                close(y[:, 0, at], want, (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + far)
+
+
 def test_norm_rope_special_rows():
     """Zeros stay zeros, large and tiny rows are normed within f32, NaN stays
     within its row."""
