@@ -8,13 +8,24 @@
 //
 // The launch reads each visible key and value row once and is bound by HBM;
 // the design keeps loads in flight and everything else out of their way.
+// Measured, of the measured copy rate (6.70 TB/s), a few us of each being the
+// launch, the search for the first tile, and the join:
+//   64 sequences of up to 8192, 32 heads over 8, 128 elements, e4m3: 88.3 us, 6.07 TB/s, 91%
+//   24 windows of up to 4096, 16 over 8, 256, bf16, capped scores:   61.6 us, 6.06 TB/s, 90%
+//   8 of up to 4096, 16 over 16, 128, bf16:                          30.3 us, 5.20 TB/s, 78%
+//   200 of up to 700, 24 over 6, 64, bf16, slopes:                   22.2 us, 3.42 TB/s, 51%
+//   1 of 200001, 16 over 1, 128, e4m3:                               26.6 us, 1.98 TB/s, 30%
+//   1 of 1000, 16 over 16, 128, bf16:                                 6.0 us, 1.37 TB/s, 20%
+// The last ones are latency: the chain launch, length, page, rows, two products,
+// join, and in groups of 16 heads the issue of the matrix instructions.
 //
 // Split.  A sequence's visible positions are cut into tiles of 16 or 32 keys, a
 // segment is the tiles of one (sequence, group of up to 16 query heads that
 // share a key/value head), and the list of all segments' tiles is cut evenly
 // over the warps, whatever the lengths: every warp finds its piece from the
 // lengths themselves.  In longer lists a segment counts a tile or two more, about
-// what its start and end cost.  A warp writes the result of a segment that is
+// what its start and end cost (weighed, with joins at a CTA's end: 64 sequences of
+// up to 8192, e4m3, 103 us -> 89).  A warp writes the result of a segment that is
 // all its own.  Of a piece at most the first and the last segment are shared
 // with other warps; their parts (m, l, unnormalised output) stay in shared
 // memory until all warps of the CTA are done, so the loop over tiles has no
@@ -67,15 +78,18 @@ namespace fp8moe {
 
 namespace {
 
-constexpr int kJoin = 16;              // pieces joined by one CTA
-constexpr int kBatch = 4;              // pieces whose loads are in flight together
+constexpr int kJoin = 16;              // parts joined by one CTA
+constexpr int kBatch = 4;              // parts whose loads are in flight together (8 and 16: no faster)
 constexpr int kWeighFrom = 4;          // tiles per warp from which on segments count more than their tiles
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLag = 8.f;            // log2 of the largest weight, before its scale
 constexpr float kWeightBits = 7.f;     // e4m3: weights are scaled by 2^7, to 2^15 at most
 
 // MH: query heads of a group at most; KM: 16-key steps of a warp's tile; NS:
-// stages of a warp's ring; CTAS: that fit on an SM.
+// stages of a warp's ring; CTAS: that fit on an SM.  Tiles of 32 keys, 16 where
+// more do not fit the registers (256 elements in bf16); two stages where rows are
+// short, one where a tile is 16 KB, or 8 KB for 8 warps (16 heads over 1 of 128
+// elements, e4m3, one sequence of 200001: one stage 26.7 us, two 27.9).
 template <int D_, bool E4M3_, int MH_, int KM_, int kWarps_, int NS_, int CTAS_>
 struct Shape {
   static constexpr int D = D_, MH = MH_, KM = KM_, NS = NS_, CTAS = CTAS_;

@@ -146,7 +146,9 @@ enum class Dest { kRows, kBf16Cache, kE4m3Cache };
 // read and written once; a lane's rows are all in flight before the angles are
 // computed, and the angles of a token are computed once for all its heads.
 // Issue slots bound it next to HBM, hence the layout above without shuffles of
-// the row itself, and arithmetic on pairs.
+// the row itself, and arithmetic on pairs.  4096 tokens of 56 heads of 128
+// elements: 23.5 us, 5.0 TB/s, 75% of the measured copy rate (two rows per lane
+// group exchanged by shuffles 37 us, one f32 per instruction 25.5).
 template <int D, Dest kDest>
 __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_constant__ RowArgs a,
                                                                 const RowCut cut) {
@@ -310,7 +312,9 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_con
 }
 
 // Rows out of the cache, cut over CTAs like the rows in: a lane takes 16
-// consecutive elements.
+// consecutive elements.  Bound by HBM and the latency of slot, scale and row.
+// Writing and reading back 8192 tokens of 16 rows of 128 elements, e4m3: 21.5 us
+// for both launches, 4.7 TB/s, 71% of the measured copy rate.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kRowThreads) read_rows_kernel(const __grid_constant__ ReadArgs a,
                                                                 const RowCut cut) {

@@ -468,7 +468,8 @@ int moe_attn_read(moe_attn *a, const moe_paged_kv *kv, const int64_t *slots, int
  *   out[b, h] = softmax(s) V,  lse[b, h] = log(sum_j exp(s_j)).
  * Position j is slot j % page_size of page page_table[b, j / page_size].
  * A sequence with no visible position gives out = 0 and lse = -infinity.
- * Sums and softmax statistics are f32; out is rounded once.
+ * Sums and softmax statistics are f32; weights are rounded to 16 bits (bf16
+ * cache) or 11 (e4m3 cache) for their products with the values, out to bf16.
  *   q          : device bf16 [B, n_heads, d], token stride q_stride (elements,
  *                a multiple of 8), 16-byte aligned.
  *   page_table : device int32 [B, max_pages], row stride table_stride.
@@ -478,10 +479,13 @@ int moe_attn_read(moe_attn *a, const moe_paged_kv *kv, const int64_t *slots, int
  *   slopes     : device f32 [n_heads] or NULL.
  *   out        : device bf16 [B, n_heads, d] contiguous, 16-byte aligned.
  *   lse        : device f32 [B, n_heads] or NULL.
- * B <= 2^20 and B * n_kv_heads * max_pages * page_size <= 2^33 (times ceil(n_heads
- * / n_kv_heads / 16) beyond 16 heads per key/value head), else MOE_ERR_SHAPE.
- * B = 0 is a no-op.  The calls on one context share its
- * workspace: they must not overlap on the GPU.
+ * B <= 2^20; B * n_kv_heads * g * ceil(max_pages * page_size / 16) up to 2^29 is
+ * taken (what is more may be refused with MOE_ERR_SHAPE), g = ceil(n_heads /
+ * n_kv_heads / 16), or / 8 with d = 256.  B = 0 is a no-op.
+ * How the work is split, and with it the order of the sums, follows from B, the
+ * heads, the format, max_pages * page_size, the lengths and max_sms: the same call
+ * gives the same bits.  The calls on one context share its workspace: they must
+ * not overlap on the GPU.
  */
 int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t q_stride,
                     const int32_t *page_table, int64_t table_stride, int64_t max_pages,

@@ -397,8 +397,8 @@ def test_decode_split_over_the_length(lens, nh, nkv, d, page, fmt):
     ([9000, 10, 0, 4000], 6, 2, 128, 16), ([700] * 40, 5, 1, 64, 24), ([30001], 16, 1, 256, 64),
     ([i * 53 % 1500 for i in range(150)], 4, 2, 64, 32), ([6000, 6001], 12, 1, 128, 32)])
 def test_decode_small_pieces(lens, nh, nkv, d, page, fmt):
-    """Few SMs, so that most of the list is cut into small pieces that CTAs take
-    as they come: the same bits every time, and correct."""
+    """Few SMs, so that each warp's piece of the list holds many segments: the same
+    bits every time, and correct."""
     b = Batch(lens, nh, nkv, d, fmt, page, seed=len(lens) + d)
     for sms in (1, 3):
         attn = DecodeAttention(nh, nkv, d, max_sms=sms)
