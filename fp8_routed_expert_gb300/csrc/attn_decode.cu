@@ -345,6 +345,23 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
     }
     return v;
   };
+  // The queries of a segment as a lane holds them: heads g + 8n.  The first
+  // segment's are asked for ahead of its pages and rows, whose latency covers theirs.
+  uint4 qw[NT][D / 32];
+  const auto load_q = [&](int b, int ch, int hg) {
+    const int in_kv = hg * a.group, heads = min(a.group, G - in_kv);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int h = g + 8 * n;
+      const __nv_bfloat16 *qp = a.q + (int64_t)b * a.q_stride + (int64_t)(ch * G + in_kv + h) * D;
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s) {
+        // bf16: piece c + 4s of 8 elements; e4m3: halves of piece c + 4 (s / 2) of 16
+        const int at = Q8 ? (c + 4 * (s / 2)) * 16 + 8 * (s & 1) : (c + 4 * s) * 8;
+        qw[n][s] = h < heads ? *reinterpret_cast<const uint4 *>(qp + at) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
   uint32_t unit = 0;
   int my_part = 0;          // of a cluster's segment
   int left = 0, extra = 0;  // tiles and units of this warp's piece that are left
@@ -357,6 +374,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
     cu.b = seg / a.n_groups;
     cu.ch = vh / a.groups_per_kv;
     cu.hg = vh - cu.ch * a.groups_per_kv;
+    load_q(cu.b, cu.ch, cu.hg);
     count(cu.b);
     cu.s = span_of<kKeys>(a, cu.b);
     const Cut tiles(cu.s.n, a.splits * a.cluster * kWarps);
@@ -528,7 +546,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
       }
     }
   };
-  if (CLUSTER && left > 0) fetch_q(cu);
+  if (!CLUSTER && left > 0) load_q(cu.b, cu.ch, cu.hg);
   fetch_page();
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
@@ -550,15 +568,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
-      const int h = g + 8 * n;  // the head whose q this lane holds
-      const __nv_bfloat16 *qp = a.q + (int64_t)cu.b * a.q_stride + (int64_t)(head0 + h) * D;
-      uint4 w[D / 32];
-#pragma unroll
-      for (int s = 0; s < D / 32; ++s) {
-        // bf16: piece c + 4s of 8 elements; e4m3: halves of piece c + 4 (s / 2) of 16
-        const int at = Q8 ? (c + 4 * (s / 2)) * 16 + 8 * (s & 1) : (c + 4 * s) * 8;
-        w[s] = h < heads ? *reinterpret_cast<const uint4 *>(qp + at) : make_uint4(0, 0, 0, 0);
-      }
+      const auto &w = qw[n];
       float unit = a.scale;
       if (!Q8) {
 #pragma unroll
@@ -971,7 +981,10 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
       }
     }
     --cu.tile;
-    if (left > 0) cu.next(a);
+    if (left > 0) {
+      cu.next(a);
+      load_q(cu.b, cu.ch, cu.hg);
+    }
   }
   // Counts a part that all threads have written; true for the last.
   const auto arrive = [&](int *counter, int n) {
