@@ -1116,7 +1116,8 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
   // A CTA's slots of the workspace: 0 for a segment that began in another CTA,
   // 1 for one that begins here.
   const auto slot_of = [&](int first, int nth) { return 2 * (first + nth) + (nth == 0 ? 1 : 0); };
-  int n_shared = 0;
+  // Warps take 32 items at a time, the next segment's after this one's.
+  int n_shared = 0, i0 = threadIdx.x;
   const uint32_t valid = __ballot_sync(0xffffffffu, lane < 2 * kWarps && segs[lane & (2 * kWarps - 1)].valid);
   for (uint32_t rest = valid; rest != 0;) {
     const Segment sg = segs[__ffs((int)rest) - 1];
@@ -1129,7 +1130,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
     const int parts = (int)(cut.owner(sg.unit0 + sg.n - 1) / kWarps) - first + 1;
     const int mine = slot_of(first, blockIdx.x - first);
 #pragma unroll 1
-    for (int i = threadIdx.x; i < items; i += kThreads) {
+    for (int i = i0; i < items; i += kThreads) {
       const int h = i / (D / 4), it = i % (D / 4);
       float mm = -INFINITY, ll = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1159,6 +1160,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
         if (it == 0) part_ml[(int64_t)mine * a.group + h] = make_float2(mm, ll);
       }
     }
+    i0 = (i0 - ((items + 31) & ~31)) & (kThreads - 1);
     if (parts > 1) {
       if (threadIdx.x == 0) shared[n_shared] = Shared{sg.b, sg.ch, sg.hg, first, parts, 0, {0, 0}};
       ++n_shared;
