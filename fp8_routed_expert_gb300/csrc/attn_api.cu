@@ -12,16 +12,22 @@
 
 using namespace fp8moe;
 
+// How moe_attn_decode takes the query heads of a key/value head: `group` at a
+// time; and by format, the CTAs that are resident, the positions of a tile, the
+// warps of a CTA, and the resident clusters of 1, 2, 4 and 8 CTAs.
+struct DecodePlan {
+  int group = 1;
+  int ctas[2] = {0, 0}, tile[2] = {1, 1}, warps[2] = {1, 1}, clusters[2][4] = {};
+};
+
 struct moe_attn {
   moe_attn_config cfg{};
   char *ws = nullptr;         // one allocation, the views below
   int sms = 0;                // of the device
   int *err = nullptr;
   uint64_t *turns = nullptr;  // [rope_dim / 2]
-  // moe_attn_decode: CTAs of a launch, positions of a tile and warps of a CTA (by
-  // format), and its workspace
-  int ctas[2] = {0, 0}, tile[2] = {1, 1}, warps[2] = {1, 1};
-  int clusters[2][4] = {};    // resident clusters of 1, 2, 4 and 8 CTAs
+  DecodePlan wide, narrow;    // groups as large as may be, and of 8 heads at most
+  // moe_attn_decode's workspace
   int group = 1, max_ctas = 0;
   int *counters = nullptr;    // [3][max_ctas], zero between calls
   float *part_ml = nullptr;   // [2 * max_ctas][group][2]
@@ -71,6 +77,56 @@ uint64_t turns_of(double freq) {
   const double rhi = std::floor(r), rlo = std::ldexp(r - rhi, 32);
   return ((uint64_t)hi << 32) + (uint64_t)std::nearbyint(lo) + ((uint64_t)(int64_t)rhi << 32) +
          (uint64_t)std::nearbyint(rlo);
+}
+
+// moe_attn_decode's groups of a key/value head, and tiles of all sequences at
+// the longest.
+int groups_of(const DecodePlan &p, const moe_attn_config &c) {
+  return (c.n_heads / c.n_kv_heads + p.group - 1) / p.group;
+}
+int64_t list_tiles(const DecodePlan &p, int format, const moe_attn_config &c, const DecodeArgs &r) {
+  const int tile = p.tile[format];
+  return (int64_t)r.B * c.n_kv_heads * groups_of(p, c) * ((r.capacity + tile - 1) / tile);  // < 2^62
+}
+
+// Sets *r to clusters of CTAs per segment and returns their grid, or 0 where the
+// list of tiles is better or a warp would have more than `limit` tiles.  As many
+// CTAs as give each warp a tile of the longest sequence, 32 warps at most, and no
+// more than are resident; where a warp would have more than 4 tiles, several
+// clusters share a segment, so that it has 3, but no more than 8/9 of the clusters
+// that fit, since those that wait for the launch before to leave come too late.
+// The list, which balances lengths and uses all SMs, is better where a warp would
+// have more than 8 tiles, 16 of a sequence alone, or 4 with clusters on less than
+// a third of the SMs.  Four heads of 128 elements per key/value head, bf16, list
+// against clusters:
+//   one sequence of 2000, 8 key/value heads    11.1 us,  7.0 (2 tiles per warp)
+//   of 8000                                    15.5,    11.4
+//   of 16000                                   21.6,    17.2
+//   of 64000                                   47.1,    44.4 (16)
+//   of 4000, 4 key/value heads (32 CTAs)       11.8,     9.0 (4)
+//   4 sequences of up to 16000, 4 heads        23.2,    20.3 (8)
+//   of up to 32000                             32.4,    33.4 (16)
+//   32 sequences of up to 500, 8 heads         11.9,     9.8 (4, clusters of one)
+int take_clusters(const moe_attn *a, const DecodePlan &p, int format, int64_t limit, DecodeArgs *r) {
+  r->group = p.group;
+  r->groups_per_kv = groups_of(p, a->cfg);
+  r->n_groups = a->cfg.n_kv_heads * r->groups_per_kv;
+  const int tile = p.tile[format], warps = p.warps[format];
+  const int *fit = p.clusters[format];
+  const int64_t per_segment = (r->capacity + tile - 1) / tile, segments = (int64_t)r->B * r->n_groups;
+  int k = 0;
+  while (k < 3 && (warps << k) < 32 && (warps << k) < per_segment && segments <= fit[k + 1]) ++k;
+  if (segments > fit[k]) return 0;
+  const int64_t wide = warps << k;
+  int64_t splits = 1;
+  if (per_segment > 4 * wide)
+    splits = std::max<int64_t>(
+        1, std::min((per_segment + 3 * wide - 1) / (3 * wide), (fit[k] - fit[k] / 9) / segments));
+  const int64_t most = 3 * (splits * segments << k) < a->sms ? 4 : r->B == 1 ? 16 : 8;
+  if (per_segment > std::min(most, limit) * wide * splits) return 0;
+  r->cluster = 1 << k;
+  r->splits = (int)splits;
+  return (int)(splits * segments << k);
 }
 
 // The caller's cache, checked against the context, as the kernels take it.
@@ -172,21 +228,26 @@ int moe_attn_init(moe_attn **out, const moe_attn_config *cfg) {
   a->cfg.rope_freqs = nullptr;  // the caller's array is not kept
   a->sms = sms;
   const int use = cfg->max_sms > 0 && cfg->max_sms < sms ? cfg->max_sms : sms;
-  a->group = decode_group(cfg->n_heads / cfg->n_kv_heads, cfg->head_dim);
-  for (int f = 0; f < 2; ++f) {
-    int per_sm = 0;
-    if (plan_paged_decode(cfg->head_dim, f == MOE_KV_E4M3, a->group, &per_sm, &a->tile[f],
-                          &a->warps[f], a->clusters[f]) != cudaSuccess ||
-        per_sm < 1) {
-      cudaGetLastError();
-      delete a;
-      return MOE_ERR_CUDA;
+  const int per_kv = cfg->n_heads / cfg->n_kv_heads;
+  a->wide.group = decode_group(per_kv, cfg->head_dim, false);
+  a->narrow.group = decode_group(per_kv, cfg->head_dim, true);
+  a->group = a->wide.group;
+  for (DecodePlan *plan : {&a->wide, &a->narrow})
+    for (int f = 0; f < 2; ++f) {
+      int per_sm = 0;
+      if (plan_paged_decode(cfg->head_dim, f == MOE_KV_E4M3, plan->group, &per_sm, &plan->tile[f],
+                            &plan->warps[f], plan->clusters[f]) != cudaSuccess ||
+          per_sm < 1) {
+        cudaGetLastError();
+        delete a;
+        return MOE_ERR_CUDA;
+      }
+      plan->ctas[f] = per_sm * use;
+      plan->clusters[f][0] = plan->ctas[f];
+      for (int i = 1; i < 4; ++i)
+        plan->clusters[f][i] = std::min(plan->clusters[f][i], plan->ctas[f] >> i);
+      a->max_ctas = std::max(a->max_ctas, plan->ctas[f]);
     }
-    a->ctas[f] = per_sm * use;
-    a->clusters[f][0] = a->ctas[f];
-    for (int i = 1; i < 4; ++i) a->clusters[f][i] = std::min(a->clusters[f][i], a->ctas[f] >> i);
-    if (a->ctas[f] > a->max_ctas) a->max_ctas = a->ctas[f];
-  }
   const int half = cfg->rope_dim / 2;
   uint64_t turns[128];
   for (int i = 0; i < half; ++i) turns[i] = turns_of(cfg->rope_freqs[i]);
@@ -378,9 +439,6 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   r.B = (int)B;
   r.n_heads = c.n_heads;
   r.n_kv = c.n_kv_heads;
-  r.group = a->group;
-  r.groups_per_kv = (c.n_heads / c.n_kv_heads + a->group - 1) / a->group;
-  r.n_groups = c.n_kv_heads * r.groups_per_kv;
   r.part = a->part;
   r.part_ml = a->part_ml;
   r.counters = a->counters;
@@ -396,47 +454,21 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   ATTN_TRY(cudaSetDevice(c.device));
   a->last_stream = s;
   decode_page_division(&r);
-  const int tile = a->tile[kv->format];
-  const int64_t tiles = B * r.n_groups * ((r.capacity + tile - 1) / tile);  // < 2^62
-  if (tiles > INT64_C(1) << 29) return MOE_ERR_SHAPE;
-  const int ctas = a->ctas[kv->format], warps = a->warps[kv->format];
-  int grid = tiles < ctas ? (int)tiles : ctas;
-  // Clusters of CTAs per segment: as many CTAs as give each warp a tile of the
-  // longest sequence, 32 warps at most, and no more than are resident.  Where a
-  // warp would have more than 4 tiles, several clusters share a segment, so that
-  // it has 3; but not for groups of more than 8 heads, whose tiles take twice as
-  // long, and no more than 8/9 of the clusters that fit, since those that wait for
-  // the launch before to leave come too late.  The list, which balances lengths
-  // and uses all SMs, is cut instead where a warp would have more than 8 tiles,
-  // 16 of a sequence alone, or 4 with clusters on less than a third of the SMs.
-  // Four heads of 128 elements per key/value head, bf16, list against clusters:
-  //   one sequence of 2000, 8 key/value heads    10.8 us,  7.1 (2 tiles per warp)
-  //   of 8000                                    16.5,    11.8 (13.6 unsplit)
-  //   of 16000                                   22.3,    17.9
-  //   of 64000                                   47.5,    44.6 (16 tiles)
-  //   of 4000, 4 key/value heads (32 CTAs)       12.0,     9.1 (4)
-  //   4 sequences of up to 16000, 4 heads        23.4,    20.9 (8)
-  //   of up to 32000                             32.6,    33.4 (16)
-  //   32 sequences of up to 500, 8 heads         11.8,    10.0 (4, clusters of one)
-  // and with 16 heads, one key/value head, e4m3:
-  //   one sequence of 16000                      15.1,    15.3
-  //   of 200001                                  26.7,    27.8
-  const int64_t per_segment = (r.capacity + tile - 1) / tile, segments = B * r.n_groups;
-  const int *fit = a->clusters[kv->format];
-  int k = 0;
-  while (k < 3 && (warps << k) < 32 && (warps << k) < per_segment && segments <= fit[k + 1]) ++k;
-  if (segments <= fit[k]) {
-    const int64_t wide = warps << k;
-    int64_t splits = 1;
-    if (per_segment > 4 * wide && a->group <= 8)
-      splits = std::max<int64_t>(1, std::min((per_segment + 3 * wide - 1) / (3 * wide), (fit[k] - fit[k] / 9) / segments));
-    const int64_t most = 3 * (splits * segments << k) < a->sms ? 4 : B == 1 ? 16 : 8;
-    if (per_segment <= most * wide * splits) {
-      r.cluster = 1 << k;
-      r.splits = (int)splits;
-      grid = (int)(splits * segments << k);
-    }
-  }
+  if (list_tiles(a->wide, kv->format, c, r) > INT64_C(1) << 29) return MOE_ERR_SHAPE;
+  // More than 8 heads per key/value head: where clusters have few tiles per warp,
+  // groups of 8, which read the rows again from L2, are faster than the products of
+  // up to 16 heads in a warp.  16 heads of 128 elements, bf16, list against clusters
+  // of groups of 8 and of 16:
+  //   one sequence of 1000, 1 key/value head      -,      5.7,  8.9 us
+  //   of 16000                                   15.1,   10.3, 14.6
+  //   of 64000                                   20.0,   17.3, 18.1
+  //   of 128000                                  26.1,   23.4, 22.3 (7 and 4 tiles per warp)
+  //   of 32000, 4 key/value heads                27.5,   22.2, 19.7 (7 and 8)
+  //   2 of up to 64000, 2 heads of 64 elements   17.7,     -,  19.1
+  int grid = 0;
+  if (a->narrow.group < a->wide.group) grid = take_clusters(a, a->narrow, kv->format, 4, &r);
+  if (grid == 0) grid = take_clusters(a, a->wide, kv->format, 16, &r);
+  if (grid == 0) grid = (int)std::min<int64_t>(list_tiles(a->wide, kv->format, c, r), a->wide.ctas[kv->format]);
   ATTN_TRY(launch_paged_decode(r, c.head_dim, kv->format == MOE_KV_E4M3, grid, s));
   return MOE_OK;
 }

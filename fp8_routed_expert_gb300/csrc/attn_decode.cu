@@ -44,8 +44,8 @@
 // cluster's result (one sequence of 1000, 32 heads over 8, bf16: 6.0 us; parts
 // kept and pulled by the joining CTA, with a second barrier before the end, 7.9).
 // Several clusters leave their results in the workspace, and the last CTA of
-// those with the same share joins them (one sequence of 16000: 18.2 us, cut as a
-// list 22.3).
+// those with the same share joins them (one sequence of 16000: 17.2 us, cut as a
+// list 21.6).
 //
 // Tile.  Rows come through a ring of cp.async stages of each warp's own.
 // S^T = K Q^T and O^T = V^T P^T run as mma.sync m16n8k16: 16 keys, then 16
@@ -1299,14 +1299,14 @@ cudaError_t with_shape(int d, bool e4m3, int group, F f) {
 
 }  // namespace
 
-// Up to 16 heads at a time: a second pass over the rows costs more than wider
-// steps (16 heads of 128 elements, 32 sequences of up to 4096 tokens, 4
-// key/value heads: e4m3 28 us, against 32 in groups of 8; bf16 33 against 47).
+// Up to 16 heads at a time: in long lists a second pass over the rows costs more
+// than wider steps (16 heads of 128 elements, 32 sequences of up to 4096 tokens, 4
+// key/value heads: e4m3 23.9 us, against 29.2 in groups of 8; bf16 31.2 against 35.5).
 // At 256 elements 16 heads' outputs do not fit the registers of enough warps
-// (sequences of up to 2048: e4m3 50 us, in groups of 8 that read from L2 the
-// second time 32; bf16 52 against 42).
-int decode_group(int heads_per_kv, int d) {
-  const int most = d == 256 ? 8 : 16, n = (heads_per_kv + most - 1) / most;
+// (sequences of up to 2048, before later steps: e4m3 50 us, in groups of 8 that
+// read from L2 the second time 32; bf16 52 against 42).
+int decode_group(int heads_per_kv, int d, bool narrow) {
+  const int most = narrow || d == 256 ? 8 : 16, n = (heads_per_kv + most - 1) / most;
   return (heads_per_kv + n - 1) / n;
 }
 

@@ -93,8 +93,9 @@ struct DecodeArgs {
   int max_ctas;
   int *err;
 };
-// Query heads taken at a time when `heads_per_kv` share a key/value head.
-int decode_group(int heads_per_kv, int d);
+// Query heads taken at a time when `heads_per_kv` share a key/value head: as many
+// as a kernel takes, or (narrow) 8 at most.
+int decode_group(int heads_per_kv, int d, bool narrow);
 // Fills in page_mul, page_shift and whole_pages.
 void decode_page_division(DecodeArgs *a);
 // Readies the kernel; tells how many CTAs of it fit on an SM, the positions of

@@ -632,7 +632,8 @@ def test_decode_clusters_of_all_sizes(nh, nkv, d, B, fmt):
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("nh,nkv,d,lens", [(4, 1, 64, [5000]), (7, 1, 128, [9000]), (6, 3, 128, [4097]), (8, 4, 256, [5001, 20]),
-                                           (16, 4, 64, [9001, 0, 129])])
+                                           (16, 4, 64, [9001, 0, 129]), (64, 4, 128, [30000, 2001]),
+                                           (18, 2, 64, [9000, 1]), (64, 4, 128, [6000, 100, 3000, 0, 5999, 31])])
 def test_decode_clusters_that_share_a_segment(nh, nkv, d, lens, fmt):
     """Sequences long enough for several clusters, and lengths that leave some of
     them nothing: the oracle's result, to the same bits every time."""
