@@ -10,12 +10,12 @@
 // the design keeps loads in flight and everything else out of their way.
 // Measured, of the measured copy rate (6.70 TB/s), a few us of each being the
 // launch, the search for the first tile, and the join:
-//   64 sequences of up to 8192, 32 heads over 8, 128 elements, e4m3: 88.3 us, 6.07 TB/s, 91%
-//   24 windows of up to 4096, 16 over 8, 256, bf16, capped scores:   61.6 us, 6.06 TB/s, 90%
-//   8 of up to 4096, 16 over 16, 128, bf16:                          30.3 us, 5.20 TB/s, 78%
-//   200 of up to 700, 24 over 6, 64, bf16, slopes:                   22.2 us, 3.42 TB/s, 51%
-//   1 of 200001, 16 over 1, 128, e4m3:                               26.6 us, 1.98 TB/s, 30%
-//   1 of 1000, 16 over 16, 128, bf16:                                 6.0 us, 1.37 TB/s, 20%
+//   64 sequences of up to 8192, 32 heads over 8, 128 elements, e4m3: 88.0 us, 6.10 TB/s, 91%
+//   24 windows of up to 4096, 16 over 8, 256, bf16, capped scores:   61.0 us, 6.12 TB/s, 91%
+//   8 of up to 4096, 16 over 16, 128, bf16:                          29.7 us, 5.30 TB/s, 79%
+//   200 of up to 700, 24 over 6, 64, bf16, slopes:                   21.5 us, 3.52 TB/s, 53%
+//   1 of 200001, 16 over 1, 128, e4m3:                               24.9 us, 2.12 TB/s, 32%
+//   1 of 1000, 16 over 16, 128, bf16:                                 5.8 us, 1.41 TB/s, 21%
 // The last ones are latency: the chain launch, length, page, rows, two products,
 // join, and in groups of 16 heads the issue of the matrix instructions.
 //
@@ -41,7 +41,7 @@
 // do: no list to search.  Each CTA of a cluster joins a share of the outputs, and
 // every warp pushes its part of each share into that CTA's shared memory, so that
 // one barrier of the cluster is all that stands between the last key and the
-// cluster's result (one sequence of 1000, 32 heads over 8, bf16: 6.0 us; parts
+// cluster's result (one sequence of 1000, 32 heads over 8, bf16: 5.9 us; parts
 // kept and pulled by the joining CTA, with a second barrier before the end, 7.9).
 // Several clusters leave their results in the workspace, and the last CTA of
 // those with the same share joins them (one sequence of 16000: 17.2 us, cut as a
@@ -79,7 +79,10 @@ namespace fp8moe {
 namespace {
 
 constexpr int kJoin = 16;              // parts joined by one CTA
-constexpr int kBatch = 4;              // parts whose loads are in flight together (8 and 16: no faster)
+// Parts whose loads are in flight together: 2 take longer where parts are many (16
+// heads over one, 200001 tokens cut as a list: 26.5 -> 29.0 us), 16 by the size of
+// their code in every call (32 sequences of up to 4096, 16 heads: 24.7 -> 27.3).
+constexpr int kBatch = 4;
 constexpr int kWeighFrom = 4;          // tiles per warp from which on segments count more than their tiles
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLag = 8.f;            // log2 of the largest weight, before its scale
@@ -88,8 +91,8 @@ constexpr float kWeightBits = 7.f;     // e4m3: weights are scaled by 2^7, to 2^
 // MH: query heads of a group at most; KM: 16-key steps of a warp's tile; NS:
 // stages of a warp's ring; CTAS: that fit on an SM.  Tiles of 32 keys, 16 where
 // more do not fit the registers (256 elements in bf16); two stages where rows are
-// short, one where a tile is 16 KB, or 8 KB for 8 warps (16 heads over 1 of 128
-// elements, e4m3, one sequence of 200001: one stage 26.7 us, two 27.9).
+// short, one where a tile is 16 KB, or 8 KB for 8 warps (16 heads of 128 elements,
+// e4m3, 32 sequences of up to 4096: one stage 25.0 us, two 26.2, before later steps).
 template <int D_, bool E4M3_, int MH_, int KM_, int kWarps_, int NS_, int CTAS_>
 struct Shape {
   static constexpr int D = D_, MH = MH_, KM = KM_, NS = NS_, CTAS = CTAS_;
