@@ -68,8 +68,13 @@
 //   shift per head that puts its largest value at 2^14 (exact down to 2^-28 of
 //   it), a key's scale multiplies its score, and a value's scale joins the
 //   exponent: weights e^(s_j - m') vs_j with a second reference m' for
-//   s_j + log2(vs_j), so that they fit f16 whatever the scales.  They are
-//   rounded once to f16's 11 bits, an eighth of the step of the bf16 output.
+//   s_j + log2(vs_j), so that they fit f16 whatever the scales.  Weights that are
+//   small next to the largest may be all that a column has, and one f16 product
+//   would lose those below 2^-21 of it (and hold the others to 11 bits), so what it
+//   leaves, scaled by 2^12, is multiplied too and added apart: 22 bits together,
+//   down to 2^-48 of the largest weight.  (The rest's product with scaled codes
+//   instead: 64 x 8192 92.6 us, this way 89.3, one product alone 88.1.  Weights and
+//   codes in bf16, which has no such limit: 103, most of it conversions.)
 #include "common.cuh"
 #include "kernels.h"
 #include "paged_attn.h"
@@ -86,7 +91,9 @@ constexpr int kBatch = 4;
 constexpr int kWeighFrom = 4;          // tiles per warp from which on segments count more than their tiles
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLag = 8.f;            // log2 of the largest weight, before its scale
-constexpr float kWeightBits = 7.f;     // e4m3: weights are scaled by 2^7, to 2^15 at most
+constexpr float kLagV = 4.f;           // the same with its scale
+constexpr float kWeightBits = 11.f;    // e4m3: weights are scaled by 2^11, to 2^15 at most
+constexpr float kRest = 0x1p12f;       // what f16 leaves of them (2^3 at most) by 2^12, to the same
 
 // MH: query heads of a group at most; KM: 16-key steps of a warp's tile; NS:
 // stages of a warp's ring; CTAS: that fit on an SM.  Tiles of 32 keys, 16 where
@@ -226,14 +233,19 @@ __device__ __forceinline__ float tanh_f32(float y) {
   return fabsf(y) < 0.6f ? small : large;
 }
 
-// Two weights in 16 bits each, and what the bf16 pair leaves of them.
+// Two weights in 16 bits each, and what the pair leaves of them (f16: times 2^12).
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if (F16) return pack_f16x2(a, b);
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
+template <bool F16>
 __device__ __forceinline__ uint32_t pack2_rest(float a, float b, uint32_t high) {
+  if (F16) {
+    const float2 h = unpack_f16x2(high);
+    return pack_f16x2((a - h.x) * kRest, (b - h.y) * kRest);
+  }
   return pack2<false>(a - __uint_as_float(high << 16), b - __uint_as_float(high & 0xffff0000u));
 }
 
@@ -718,7 +730,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
         if (Q8) {
           top = fmaxf(s[0][n][u] + vs[0][0], s[0][n][2 + u] + vs[0][1]);
           if (KM == 2) top = fmaxf(top, fmaxf(s[KM - 1][n][u] + vs[KM - 1][0], s[KM - 1][n][2 + u] + vs[KM - 1][1]));
-          high |= top > mv[n][u] + kLag;
+          high |= top > mv[n][u] + kLagV;
         }
       }
     if (__any_sync(0xffffffffu, high)) {
@@ -776,34 +788,37 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
         for (int u = 0; u < 2; ++u) {
           const uint32_t hi = pack2<Q8>(p[2 * u], p[2 * u + 1]);
           p_hi[t][n][u] = transpose8(hi);
-          if (!Q8) p_lo[t][n][u] = transpose8(pack2_rest(p[2 * u], p[2 * u + 1], hi));
+          p_lo[t][n][u] = transpose8(pack2_rest<Q8>(p[2 * u], p[2 * u + 1], hi));
         }
       }
     }
   };
   auto add_values = [&](int stage, const uint32_t (&p_hi)[KM][NT][2], const uint32_t (&p_lo)[KM][NT][2]) {
     const uint32_t vb = ring + stage * S::kStage + S::kHalfTile;
+    const auto load = [&](uint4 (&v)[4], int t, int h) {
 #pragma unroll
-    for (int t = 0; t < KM; ++t)
-#pragma unroll
-      for (int h = 0; h < S::H; ++h) {
-        uint4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 2 * c + (i & 1) + 8 * (i >> 1);  // r & 6 is 2c for all four
-          const uint32_t row_at = vb + (16 * t + r) * S::kRowBytes;
-          if (S::kPieces >= 8) {
-            v[i] = lds16(row_at + (((g + 8 * h) ^ (2 * c)) << 4));
-          } else {  // rows of 64 bytes, half a piece per lane
-            const uint2 x = lds8(row_at + (((g >> 1) ^ c) << 4) + 8 * (g & 1));
-            v[i] = make_uint4(x.x, x.y, 0, 0);
-          }
+      for (int i = 0; i < 4; ++i) {
+        const int r = 2 * c + (i & 1) + 8 * (i >> 1);  // r & 6 is 2c for all four
+        const uint32_t row_at = vb + (16 * t + r) * S::kRowBytes;
+        if (S::kPieces >= 8) {
+          v[i] = lds16(row_at + (((g + 8 * h) ^ (2 * c)) << 4));
+        } else {  // rows of 64 bytes, half a piece per lane
+          const uint2 x = lds8(row_at + (((g >> 1) ^ c) << 4) + 8 * (g & 1));
+          v[i] = make_uint4(x.x, x.y, 0, 0);
         }
+      }
+    };
+    if constexpr (!Q8) {
 #pragma unroll
-        for (int w = 0; w < (Q8 ? EV / 4 : 4); ++w) {
-          const uint32_t v0 = u4_word(v[0], w), v1 = u4_word(v[1], w), v2 = u4_word(v[2], w),
-                         v3 = u4_word(v[3], w);
-          if (!Q8) {  // columns 2w, 2w + 1 of the piece, keys paired
+      for (int t = 0; t < KM; ++t)
+#pragma unroll
+        for (int h = 0; h < S::H; ++h) {
+          uint4 v[4];
+          load(v, t, h);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {  // columns 2w, 2w + 1 of the piece, keys paired
+            const uint32_t v0 = u4_word(v[0], w), v1 = u4_word(v[1], w), v2 = u4_word(v[2], w),
+                           v3 = u4_word(v[3], w);
             const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
             const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
 #pragma unroll
@@ -811,19 +826,44 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) decode_kernel(const __gr
               mma16816<false>(o[n][4 * h + w], a0, a1, a2, a3, p_hi[t][n][0], p_hi[t][n][1]);
               mma16816<false>(o[n][4 * h + w], a0, a1, a2, a3, p_lo[t][n][0], p_lo[t][n][1]);
             }
-          } else {
+          }
+        }
+    } else {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {  // columns 4w + 2u, + 1
+      for (int h = 0; h < S::H; ++h) {
+        uint4 v[KM][4];
+#pragma unroll
+        for (int t = 0; t < KM; ++t) load(v[t], t, h);
+#pragma unroll
+        for (int w = 0; w < EV / 4; ++w)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {  // columns 4w + 2u, + 1
+            float rest[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) rest[n][0] = rest[n][1] = rest[n][2] = rest[n][3] = 0.f;
+#pragma unroll
+            for (int t = 0; t < KM; ++t) {
+              const uint32_t v0 = u4_word(v[t][0], w), v1 = u4_word(v[t][1], w), v2 = u4_word(v[t][2], w),
+                             v3 = u4_word(v[t][3], w);
               uint32_t a0, a1, a2, a3;
               e4m3x4_to_f16(__byte_perm(v0, v1, u ? 0x7362 : 0x5140), a0, a1);
               e4m3x4_to_f16(__byte_perm(v2, v3, u ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
+              for (int n = 0; n < NT; ++n) {
                 mma16816<true>(o[n][EV / 2 * h + 2 * w + u], a0, a1, a2, a3, p_hi[t][n][0], p_hi[t][n][1]);
+                mma16816<true>(rest[n], a0, a1, a2, a3, p_lo[t][n][0], p_lo[t][n][1]);
+              }
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float &to = o[n][EV / 2 * h + 2 * w + u][i];
+                to = fmaf(rest[n][i], 1.f / kRest, to);
+              }
           }
-        }
       }
+    }
   };
 
   // ---- end of a segment, or of this warp's part of it

@@ -468,8 +468,11 @@ int moe_attn_read(moe_attn *a, const moe_paged_kv *kv, const int64_t *slots, int
  *   out[b, h] = softmax(s) V,  lse[b, h] = log(sum_j exp(s_j)).
  * Position j is slot j % page_size of page page_table[b, j / page_size].
  * A sequence with no visible position gives out = 0 and lse = -infinity.
- * Sums and softmax statistics are f32; weights are rounded to 16 bits (bf16
- * cache) or 11 (e4m3 cache) for their products with the values, out to bf16.
+ * Sums and softmax statistics are f32.  For their products with the values, weights
+ * are rounded to 16 bits (bf16 cache), or weights times the value's scale to 22 bits
+ * and to 2^-48 of the head's largest (e4m3 cache); out is rounded to bf16.  With an
+ * e4m3 cache, elements of q below 2^-28 of their head's largest are rounded to 2^-39
+ * of it.
  *   q          : device bf16 [B, n_heads, d], token stride q_stride (elements,
  *                a multiple of 8), 16-byte aligned.
  *   page_table : device int32 [B, max_pages], row stride table_stride.

@@ -696,3 +696,34 @@ def test_example_step(fmt):
         V.append(f64(v))
     want, _, mag, _ = P.decode(f64(q), K, V, b.pos.tolist())
     close(out, want, 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * mag)
+
+
+@pytest.mark.parametrize("fmt,big,nats", [("bf16", 1e9, 0.0), ("bf16", 1e30, 0.0), ("bf16", 1.0, 30.0),
+                                          ("e4m3", 1e9, 0.0), ("e4m3", 1.0, 20.0)])
+@pytest.mark.parametrize("nh,nkv,d", [(4, 2, 64), (16, 1, 64), (6, 2, 128), (12, 1, 128), (3, 1, 256)])
+def test_decode_columns_that_the_heaviest_rows_leave_empty(nh, nkv, d, fmt, big, nats):
+    """A value row that is far larger than the others, or whose key is far ahead,
+    with zeros in all columns but one: the other columns are the sums of much
+    smaller weights and keep their digits, each for itself.  Weights in 16 bits
+    (2^-16), and for e4m3 off by 2^-48 of the largest weight times its value's
+    scale, 448 of which are at most twice the large value; the rest as for all
+    decode tests."""
+    b = Batch([150, 700], nh, nkv, d, fmt, 16, seed=nh + d)
+    b.q.copy_(b.q[:, :1].clone().expand(-1, nh, -1))
+    attn = DecodeAttention(nh, nkv, d)
+    for s, at in ((0, 3), (1, 411)):
+        q = b.q[s, 0].double()
+        key = (q * (nats * d ** 0.5 / float(q @ q))).to(torch.bfloat16).expand(1, nkv, d).contiguous()
+        row = torch.zeros(1, nkv, d, dtype=torch.bfloat16, device=DEV)
+        row[..., 1] = big
+        page = int(b.table[s, at // 16])
+        attn.write(b.cache, key, row, torch.tensor([16 * page + at % 16], device=DEV))
+        b.K[s][at] = cache_values(b.cache, 0)[page, :, at % 16]
+        b.V[s][at] = cache_values(b.cache, 1)[page, :, at % 16]
+    out, _ = b.run(attn)
+    want, _, mag, reach = P.decode(f64(b.q), b.K, b.V, b.lens)
+    rel = 2 * (d / 2 + 16) * U * reach + 2.0 ** -20 + (700 / 2 + 64) * U + 2.0 ** -16
+    tol = 2.0 ** -8 * np.abs(want) + rel[..., None] * mag
+    if fmt == "e4m3":
+        tol = tol + 2.0 ** -47 * 700 * mag[..., 1:2]
+    close(out, want, tol)
