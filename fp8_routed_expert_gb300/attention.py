@@ -12,7 +12,7 @@ import math
 import torch
 
 from ._lib import C, AttnConfig, PagedKVDesc, check, lib, torch_binding
-from .layer import _stream_handle
+from .layer import _memory_of, _stream_handle
 
 _BF16 = torch.bfloat16
 
@@ -81,7 +81,13 @@ class DecodeAttention:
     """A context for one head layout (moe_attn_init).  ``rope_freqs``: radians
     per position of each rotated pair (``rope_frequencies``), None for no
     rotation; its length is half the rotated elements of a head.  One context
-    serves one stream at a time."""
+    serves one stream at a time.
+
+    ``stream`` of a call is the torch stream, or its handle, that its kernels run
+    on (None: the current one).  Outputs that are not given are allocated from
+    that stream's memory.  Other tensors of the call, and its outputs where they
+    are used elsewhere, are the caller's to order (``wait_stream``) and to keep
+    (``record_stream``)."""
 
     def __init__(self, n_heads: int, n_kv_heads: int, head_dim: int, rope_freqs=None,
                  interleaved: bool = False, device: int = 0, max_sms: int = 0):
@@ -125,7 +131,10 @@ class DecodeAttention:
             return _current_raw_stream(self._index)
         return _stream_handle(stream)
 
-    def _new(self, T: int, heads: int) -> torch.Tensor:
+    def _new(self, T: int, heads: int, stream) -> torch.Tensor:
+        if stream is not None:
+            with _memory_of(stream, self._index):
+                return self._new(T, heads, None)
         return torch.empty((T, heads, self.head_dim), dtype=_BF16, device=self.device)
 
     # -- operators -------------------------------------------------------
@@ -138,9 +147,9 @@ class DecodeAttention:
         [T, n_heads, d] and k bf16 [T, n_kv_heads, d]; positions int32 [T].
         q_out / k_out may be q / k."""
         if q_out is None:
-            q_out = self._new(q.shape[0], self.n_heads)
+            q_out = self._new(q.shape[0], self.n_heads, stream)
         if k_out is None:
-            k_out = self._new(k.shape[0], self.n_kv_heads)
+            k_out = self._new(k.shape[0], self.n_kv_heads, stream)
         rc = self._b.norm_rope(self._ctx, q, k, positions, q_weight, k_weight, eps, q_out, k_out,
                                self._stream(stream))
         if rc:
@@ -155,7 +164,7 @@ class DecodeAttention:
         cache's slots (int64 [T]: page * page_size + slot, negative to store
         nothing).  Returns the queries."""
         if q_out is None:
-            q_out = self._new(q.shape[0], self.n_heads)
+            q_out = self._new(q.shape[0], self.n_heads, stream)
         rc = self._b.append(self._ctx, cache._native, q, k, v, positions, slots, q_weight, k_weight, eps, q_out,
                             self._stream(stream))
         if rc:
@@ -174,9 +183,9 @@ class DecodeAttention:
         """The rows of the slots as bf16 [T, n_kv_heads, d] (zeros for a
         negative slot)."""
         if k_out is None:
-            k_out = self._new(slots.shape[0], self.n_kv_heads)
+            k_out = self._new(slots.shape[0], self.n_kv_heads, stream)
         if v_out is None:
-            v_out = self._new(slots.shape[0], self.n_kv_heads)
+            v_out = self._new(slots.shape[0], self.n_kv_heads, stream)
         rc = self._b.read(self._ctx, cache._native, slots, k_out, v_out, self._stream(stream))
         if rc:
             check(rc, "moe_attn_read")
@@ -194,7 +203,7 @@ class DecodeAttention:
         positions.  Returns out bf16 [B, n_heads, d], or (out, lse) if ``lse``
         f32 [B, n_heads] is given."""
         if out is None:
-            out = self._new(q.shape[0], self.n_heads)
+            out = self._new(q.shape[0], self.n_heads, stream)
         rc = self._b.decode(self._ctx, cache._native, q, page_table, seq_lens, starts,
                             self._scale if scale is None else scale, softcap, slopes, window, out, lse,
                             self._stream(stream))

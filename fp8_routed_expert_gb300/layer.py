@@ -5,6 +5,7 @@ checks dtypes/shapes of torch tensors and passes their device pointers.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -26,6 +27,17 @@ def _stream_handle(stream) -> int | None:
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _memory_of(stream, device: int):
+    """The context in which torch allocates from the memory of a call's stream
+    (None: the current one).  A kernel may write an output without waiting for
+    another stream only if no other stream's work still uses its memory."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_handle(stream), device=torch.device("cuda", device))
+    return torch.cuda.stream(stream)
 
 
 class MoELayer:

@@ -148,3 +148,51 @@ def test_decode_refusals(L, ctx, kw, rc):
 def test_rope_frequencies():
     f = moe.rope_frequencies(64)
     assert len(f) == 32 and f[0] == 1.0 and math.isclose(f[31], 10000.0 ** (-62 / 64))
+
+
+def test_outputs_come_from_the_memory_of_the_calls_stream(monkeypatch):
+    """An output that a call makes is allocated while its stream is the current
+    one.  Streams, memory and the native calls are stand-ins."""
+    import torch
+
+    from fp8_routed_expert_gb300 import attention
+
+    class Stream:
+        def __init__(self, handle, device=None):
+            self.cuda_stream = handle
+
+    class Use:
+        def __init__(self, stream):
+            self.handle = stream.cuda_stream
+
+        def __enter__(self):
+            current.append(self.handle)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    class Rows:
+        shape = (3,)
+
+    current, made, ran = [5], [], []
+    monkeypatch.setattr(torch.cuda, "stream", Use)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made.append(current[-1]))
+    monkeypatch.setattr(attention, "_current_raw_stream", lambda index: current[-1])
+
+    class Native:
+        def __getattr__(self, name):
+            return lambda *a: ran.append(a[-1]) or 0
+
+    a = object.__new__(moe.DecodeAttention)
+    a.n_heads, a.n_kv_heads, a.head_dim, a.device, a._index = NH, NKV, D, None, 0
+    a._ctx, a._b, a._scale = (), Native(), 1.0
+    cache = type("Cache", (), {"_native": ()})()
+    x = Rows()
+    calls = (lambda s: a.norm_rope(x, x, x, stream=s), lambda s: a.append(x, x, x, x, x, cache, stream=s),
+             lambda s: a.read(cache, x, stream=s), lambda s: a.decode(x, cache, x, x, stream=s))
+    for given, used in ((None, 5), (Stream(7), 7), (9, 9)):
+        for call, outputs in zip(calls, (2, 1, 2, 1)):
+            made.clear(), ran.clear()
+            call(given)
+            assert made == [used] * outputs and ran == [used] and current == [5]

@@ -727,3 +727,36 @@ def test_decode_columns_that_the_heaviest_rows_leave_empty(nh, nkv, d, fmt, big,
     if fmt == "e4m3":
         tol = tol + 2.0 ** -47 * 700 * mag[..., 1:2]
     close(out, want, tol)
+
+
+def test_outputs_are_of_the_calls_stream():
+    """A call on another stream than the current one: memory that the current
+    stream's queued work still uses is not handed out for its outputs."""
+    T, nh, nkv, d = 64, 8, 2, 128
+    b = Batch([40] * T, nh, nkv, d, "bf16", 16, seed=11)
+    attn = DecodeAttention(nh, nkv, d)
+    want, rows = b.run(attn)[0].clone(), randn(gen(4), T, nkv, d)
+    slots = torch.arange(T, device=DEV)
+    nowhere = -1 - slots
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    calls = {"norm_rope": lambda **k: attn.norm_rope(b.q, rows, None, **k)[0],
+             "append": lambda **k: attn.append(b.q, rows, rows, None, nowhere, b.cache, **k),
+             "decode": lambda **k: attn.decode(b.q, b.cache, b.table, b.seq_lens, **k),
+             "read": lambda **k: attn.read(b.cache, slots, **k)[0]}
+    for name, call in calls.items():
+        for stream in (side, side.cuda_stream):
+            old = torch.empty(T, nh if name != "read" else nkv, d, dtype=torch.bfloat16, device=DEV)
+            at = old.data_ptr()
+            torch.cuda._sleep(2_000_000)
+            old.fill_(1.0)  # queued behind the sleep
+            del old
+            out = call(stream=stream)
+            assert out.data_ptr() != at
+            side.synchronize()
+            if name == "decode":
+                assert torch.equal(out, want)
+            elif name != "read":
+                assert torch.equal(out, b.q)
+            torch.cuda.synchronize()
+    assert attn.status() == 0
