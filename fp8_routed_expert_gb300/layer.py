@@ -41,7 +41,11 @@ def _memory_of(stream, device: int):
 
 
 class MoELayer:
-    """One routed-MoE layer context (workspace sized for max_tokens x max_top_k)."""
+    """One routed-MoE layer context (workspace sized for max_tokens x max_top_k).
+
+    ``stream`` of a call is the torch stream, or its handle, that its kernels run
+    on (None: the current one); outputs that are not given are allocated from that
+    stream's memory."""
 
     def __init__(self, max_tokens: int, hidden: int, n_experts: int, inter: int, max_top_k: int,
                  device: int = 0):
@@ -85,7 +89,8 @@ class MoELayer:
             raise ValueError("x must be a contiguous bf16 [T, H] tensor")
         self._check_weights(router_w, router_bias, w13, s13, w2, s2)
         if out is None:
-            out = torch.empty_like(x)
+            with _memory_of(stream, self.device):
+                out = torch.empty_like(x)
         rc = lib().moe_layer_forward(self._h, _ptr(x), x.shape[0], _ptr(router_w), _ptr(router_bias),
                                      _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), top_k, _ptr(out),
                                      _stream_handle(stream))
@@ -111,7 +116,8 @@ class MoELayer:
             if t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
                 raise ValueError(f"expected contiguous cuda {dt} {shape}, got {t.dtype} {tuple(t.shape)}")
         if out is None:
-            out = torch.empty_like(x)
+            with _memory_of(stream, self.device):
+                out = torch.empty_like(x)
         rc = lib().moe_layer_forward_nvfp4(self._h, _ptr(x), x.shape[0], _ptr(router_w),
                                            _ptr(router_bias), _ptr(w13), _ptr(sf13), _ptr(g13),
                                            _ptr(w2), _ptr(sf2), _ptr(g2), top_k, _ptr(out),
@@ -135,12 +141,13 @@ class MoELayer:
         """Routing of the last forward (T tokens, top-k) as torch tensors on the device."""
         dev = torch.device("cuda", self.device)
         E, P = self.cfg.n_experts, T * k
-        r = dict(idx=torch.empty((T, k), dtype=torch.int32, device=dev),
-                 wts=torch.empty((T, k), dtype=torch.float32, device=dev),
-                 counts=torch.empty(E, dtype=torch.int32, device=dev),
-                 offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
-                 perm=torch.empty(P, dtype=torch.int32, device=dev),
-                 inv=torch.empty(P, dtype=torch.int32, device=dev))
+        with _memory_of(stream, self.device):
+            r = dict(idx=torch.empty((T, k), dtype=torch.int32, device=dev),
+                     wts=torch.empty((T, k), dtype=torch.float32, device=dev),
+                     counts=torch.empty(E, dtype=torch.int32, device=dev),
+                     offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
+                     perm=torch.empty(P, dtype=torch.int32, device=dev),
+                     inv=torch.empty(P, dtype=torch.int32, device=dev))
         rc = lib().moe_get_routing(self._h, _ptr(r["idx"]), _ptr(r["wts"]), _ptr(r["counts"]),
                                    _ptr(r["offsets"]), _ptr(r["perm"]), _ptr(r["inv"]),
                                    _stream_handle(stream))
@@ -179,7 +186,8 @@ class MoELayer:
 
     def debug_buffer(self, name: str, dtype: torch.dtype, shape, stream=None) -> torch.Tensor:
         """Copy of a workspace buffer of the last forward ('logits', 'h', 'y', 'x16')."""
-        out = torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.device))
+        with _memory_of(stream, self.device):
+            out = torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.device))
         n = ctypes.c_int64()
         cap = out.numel() * out.element_size()
         check(lib().moe_debug_copy(self._h, name.encode(), _ptr(out), cap, ctypes.byref(n),
@@ -224,7 +232,8 @@ class ExpertCache:
     def forward(self, x: torch.Tensor, router_w, router_bias, s13, s2, top_k: int,
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         if out is None:
-            out = torch.empty_like(x)
+            with _memory_of(stream, self.layer.device):
+                out = torch.empty_like(x)
         rc = lib().moe_cache_forward(self._h, _ptr(x), x.shape[0], _ptr(router_w), _ptr(router_bias),
                                      _ptr(s13), _ptr(s2), top_k, _ptr(out), _stream_handle(stream))
         check(rc, "moe_cache_forward")

@@ -83,3 +83,82 @@ def test_init_without_gpu_reports_cuda_error(L):
     rc, h = _init(L)
     assert rc in (moe.C["MOE_ERR_CUDA"], moe.C["MOE_ERR_UNSUPPORTED"])
     assert h.value is None
+
+
+def test_outputs_come_from_the_memory_of_the_calls_stream(monkeypatch):
+    """An output that a call makes is allocated while its stream is the current
+    one.  Streams, memory, tensors and the library are stand-ins."""
+    import torch
+
+    from fp8_routed_expert_gb300 import layer
+
+    class Stream:
+        def __init__(self, handle, device=None):
+            self.cuda_stream = handle
+
+    class Use:
+        def __init__(self, stream):
+            self.handle = stream.cuda_stream
+
+        def __enter__(self):
+            current.append(self.handle)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    class Tensor:
+        is_cuda = True
+
+        def __init__(self, dtype, *shape):
+            self.dtype, self.shape = dtype, shape
+
+        def dim(self):
+            return len(self.shape)
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 0
+
+        def numel(self):
+            return 0
+
+        def element_size(self):
+            return 0
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: ran.append(a[-1]) or 0
+
+    def make(*a, **k):
+        made.append(current[-1])
+        return Tensor(None)
+
+    current, made, ran = [5], [], []
+    monkeypatch.setattr(torch.cuda, "stream", Use)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream(current[-1]))
+    monkeypatch.setattr(torch, "empty", make)
+    monkeypatch.setattr(torch, "empty_like", make)
+    monkeypatch.setattr(layer, "lib", Library)
+    H, E, I = 256, 8, 128
+    u8, f32 = torch.uint8, torch.float32
+    m = object.__new__(moe.MoELayer)
+    m.cfg, m.device, m._h = MoEConfig(8, H, E, I, 2, 0), 0, None
+    c = object.__new__(moe.ExpertCache)
+    c.layer, c._h = m, None
+    x, rw = Tensor(torch.bfloat16, 3, H), Tensor(f32, E, H)
+    fp8 = (Tensor(u8, E, 2 * I, H), Tensor(f32, E, 2 * I // 128, H // 128), Tensor(u8, E, H, I),
+           Tensor(f32, E, H // 128, I // 128))
+    fp4 = (Tensor(u8, E, 2 * I, H // 2), Tensor(u8, E, 2 * I, H // 16), Tensor(f32, E), Tensor(u8, E, H, I // 2),
+           Tensor(u8, E, H, I // 16), Tensor(f32, E))
+    calls = ((lambda s: m.forward(x, rw, None, *fp8, 2, stream=s), 1),
+             (lambda s: m.forward_nvfp4(x, rw, None, *fp4, 2, stream=s), 1),
+             (lambda s: m.routing(3, 2, stream=s), 6), (lambda s: m.debug_buffer("h", f32, 1, stream=s), 1),
+             (lambda s: c.forward(x, rw, None, fp8[1], fp8[3], 2, stream=s), 1))
+    for given, used in ((None, 5), (Stream(7), 7), (9, 9)):
+        for call, outputs in calls:
+            made.clear(), ran.clear()
+            call(given)
+            assert made == [used] * outputs and ran == [used] and current == [5]
