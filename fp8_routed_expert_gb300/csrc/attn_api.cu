@@ -64,8 +64,10 @@ int check_config(const moe_attn_config &c) {
 
 // freq / (2 pi) modulo 1 in units of 2^-64 turns.  1 / (2 pi) is held as the
 // sum of two doubles, and the product's rounding error is recovered with an
-// fma, so the result is within a unit or two for |freq| <= 1.
+// fma, so the result is within a unit for |freq| <= 1.  A negative frequency's
+// fraction would be rounded to 2^-53: it is the opposite of the positive one's.
 uint64_t turns_of(double freq) {
+  if (freq < 0.0) return 0 - turns_of(-freq);
   constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
   const double p = freq * kHi;
   const double e = std::fma(freq, kHi, -p) + freq * kLo;

@@ -12,7 +12,7 @@
 //
 // Angles.  position * freq / 2 pi is only needed modulo 1.  With the frequency
 // as a 64-bit fraction of a turn, the 64-bit integer product wraps exactly
-// modulo one turn: the error is 2^-65 turns times the position (2^-34 at the
+// modulo one turn: the error is 2^-64 turns times the position (2^-33 at the
 // end of the int32 range) where an f32 product would lose the angle of a far
 // position altogether.  Quarter turns are taken off before the rest becomes f32,
 // so that sines and cosines keep their own digits (converted whole, 1704 of 29

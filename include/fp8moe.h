@@ -408,8 +408,9 @@ int moe_attn_status(moe_attn *a);
  * Per head row x of d elements, in f32:
  *   y = x / sqrt(mean(x^2) + eps) * weight        (skipped if weight is NULL)
  *   rotate pair i < R/2 of y by the angle position * rope_freqs[i]
- * and one rounding to bf16.  Angles are exact to 2^-33 of a turn at every
- * int32 position.
+ * and one rounding to bf16.  Angles are taken modulo a turn to 2^-33 of one at
+ * every int32 position, for frequencies of either sign up to 1 radian, and what is
+ * left beside the nearest quarter turn is rounded to f32 (2^-28 of a turn at most).
  *   q, k       : device bf16; row h of token t at t * q_stride + h * d (elements),
  *                strides multiples of 8, pointers 16-byte aligned.  Slices of
  *                a fused projection's rows are fine.

@@ -760,3 +760,31 @@ def test_outputs_are_of_the_calls_stream():
                 assert torch.equal(out, b.q)
             torch.cuda.synchronize()
     assert attn.status() == 0
+
+
+def test_rotation_by_negative_frequencies():
+    """A negative frequency undoes what its opposite does, at positions up to the
+    ends of the int32 range: each angle lies 2^-17 or so beside a half turn, so that
+    its sine shows an error of the angle in its own bf16 digits.  The angle is off
+    by 2^-64 turns per position, and by f32 roundings of its rest."""
+    from fractions import Fraction
+    pi = Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+    at = [2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, 10 ** 9 + 7]
+    freqs = [-(float(pi) * (2 * i + 1) + 1e-5 * (i + 1)) / abs(p) for p in at for i in range(2)]
+    x = torch.zeros(len(at), 1, 64, dtype=torch.bfloat16, device=DEV)
+    x[..., :8] = 1.0  # the first elements of the pairs
+    pos = torch.tensor(at, dtype=torch.int32, device=DEV)
+    back = DecodeAttention(1, 1, 64, rope_freqs=freqs)
+    forth = DecodeAttention(1, 1, 64, rope_freqs=[-f for f in freqs])
+    want = np.zeros((len(at), 8))
+    for t, p in enumerate(at):
+        for i, f in enumerate(freqs):
+            a = Fraction(f) * p
+            turns = round(a / pi)
+            want[t, i] = (-1) ** turns * np.sin(float(a - turns * pi))
+    assert (np.abs(want) < 2e-5).sum() >= 8
+    far = np.abs(np.array(at, np.float64))[:, None] * (2 * np.pi * 2.0 ** -64)
+    y, z = back.norm_rope(x, x, pos)[0], forth.norm_rope(x, x, pos)[0]
+    close(y[:, 0, 8:16], want, (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + far)
+    close(z[:, 0, 8:16], -want, (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + far)
+    assert torch.equal(y[:, 0, :8], z[:, 0, :8]) and torch.equal(y[:, 0, 8:16], -z[:, 0, 8:16])
