@@ -47,6 +47,7 @@ bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 constexpr int64_t kMaxBatch = 1 << 20;
 constexpr int64_t kMaxPositions = 0x7fffffff - 63;
 constexpr int64_t kMaxTokens = 0x7fffffff;
+constexpr int64_t kMaxStride = INT64_C(1) << 40;
 
 int check_config(const moe_attn_config &c) {
   if (c.n_kv_heads < 1 || c.n_heads < c.n_kv_heads || c.n_heads > 1024 ||
@@ -140,16 +141,22 @@ int view_of(const moe_attn *a, const moe_paged_kv *kv, KvView *v) {
   if (kv->k == nullptr || kv->v == nullptr) return MOE_ERR_ARG;
   if (q && (kv->k_scale == nullptr || kv->v_scale == nullptr)) return MOE_ERR_ARG;
   const int es = q ? 1 : 2;
-  // bounds that keep every offset within 63 bits
-  const int64_t most = INT64_C(1) << 40;
+  // Every offset in bytes is kept within 62 bits: strides alone do not, 2^31 pages
+  // of 2^41 bytes would wrap to another address.
+  const auto far = [&](int64_t page, int64_t head, int64_t slot, int64_t row, int bytes) {
+    return ((__int128)(kv->n_pages - 1) * page + (__int128)(a->cfg.n_kv_heads - 1) * head +
+            (__int128)(kv->page_size - 1) * slot + row) * bytes > INT64_C(1) << 62;
+  };
   for (int64_t st : {kv->page_stride, kv->head_stride, kv->slot_stride}) {
-    if (st < 0 || st > most) return MOE_ERR_SHAPE;
+    if (st < 0 || st > kMaxStride) return MOE_ERR_SHAPE;
     if ((st * es) % 16 != 0) return MOE_ERR_ALIGN;
   }
+  if (far(kv->page_stride, kv->head_stride, kv->slot_stride, a->cfg.head_dim, es)) return MOE_ERR_SHAPE;
   if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return MOE_ERR_ALIGN;
   if (q) {
     for (int64_t st : {kv->scale_page_stride, kv->scale_head_stride, kv->scale_slot_stride})
-      if (st < 0 || st > most) return MOE_ERR_SHAPE;
+      if (st < 0 || st > kMaxStride) return MOE_ERR_SHAPE;
+    if (far(kv->scale_page_stride, kv->scale_head_stride, kv->scale_slot_stride, 1, 4)) return MOE_ERR_SHAPE;
     if (!aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4)) return MOE_ERR_ALIGN;
   }
   *v = KvView{static_cast<uint8_t *>(kv->k),
@@ -164,7 +171,6 @@ int view_of(const moe_attn *a, const moe_paged_kv *kv, KvView *v) {
               q ? kv->scale_head_stride : 0,
               q ? kv->scale_slot_stride : 0,
               kv->page_size};
-  (void)a;
   return MOE_OK;
 }
 
@@ -420,7 +426,7 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   if (B > kMaxBatch) return MOE_ERR_SHAPE;
   DecodeArgs r{};
   CHECK(view_of(a, kv, &r.kv));
-  if (max_pages < 1 || table_stride < 0 || max_pages > kMaxPositions / kv->page_size)
+  if (max_pages < 1 || table_stride < 0 || table_stride > kMaxStride || max_pages > kMaxPositions / kv->page_size)
     return MOE_ERR_SHAPE;
   if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0)
     return MOE_ERR_ARG;

@@ -351,7 +351,8 @@ int moe_decode_attention(const void *q, const void *k_cache, const void *v_cache
  *   MOE_KV_E4M3 : rows of e4m3 codes, value = code * the row's f32 scale
  *                 (scales are >= 0).
  * Alignment: k and v 16 bytes, and the three row strides multiples of 16
- * bytes; scales 4 bytes.
+ * bytes; scales 4 bytes.  A stride is at most 2^40 elements, and the last row
+ * and scale lie within 2^62 bytes of the first (MOE_ERR_SHAPE).
  */
 #define MOE_KV_BF16 0
 #define MOE_KV_E4M3 1

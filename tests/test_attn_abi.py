@@ -196,3 +196,33 @@ def test_outputs_come_from_the_memory_of_the_calls_stream(monkeypatch):
             made.clear(), ran.clear()
             call(given)
             assert made == [used] * outputs and ran == [used] and current == [5]
+
+
+def _refused_by_all(L, ctx, kv, T=1):
+    ref = ctypes.addressof(kv)
+    return {L.moe_attn_write(ctx, ref, P, NKV * D, P, NKV * D, P, T, None),
+            L.moe_attn_read(ctx, ref, P, T, P, NKV * D, P, NKV * D, None),
+            L.moe_attn_append(ctx, ref, P, NH * D, P, NKV * D, P, NKV * D, P, P, T, None, None, 0.0, P, NH * D, None),
+            L.moe_attn_decode(ctx, ref, P, NH * D, P, 4, 4, P, None, T, 1.0, 0.0, None, 0, P, None, None)}
+
+
+@pytest.mark.parametrize("fmt", ["BF16", "E4M3"])
+def test_caches_whose_offsets_leave_the_address_range(L, ctx, fmt):
+    """Strides that each are within bounds, but whose products with the numbers of
+    pages, heads or slots are not; the largest that still fit are taken (no tokens:
+    no work)."""
+    row = dict(BF16=2, E4M3=1)[fmt]
+    base = dict(format=moe.C["MOE_KV_" + fmt], n_pages=1, page_size=1, page_stride=0, head_stride=0, slot_stride=0,
+                scale_page_stride=0, scale_head_stride=0, scale_slot_stride=0)
+    top = (1 << 31) - 1
+    for kw in (dict(n_pages=top, page_stride=1 << 40), dict(page_size=top, slot_stride=1 << 40),
+               dict(n_pages=1 << 22, page_stride=1 << 40, page_size=1 << 22, slot_stride=1 << 40)):
+        assert _refused_by_all(L, ctx, _kv(**{**base, **kw})) == {SHAPE}
+    for kw in (dict(scale_page_stride=1 << 40, n_pages=top), dict(scale_slot_stride=1 << 40, page_size=top)):
+        if fmt == "E4M3":
+            assert _refused_by_all(L, ctx, _kv(**{**base, **kw})) == {SHAPE}
+    # (2^31 - 2) pages of 2^31 bytes, less a row
+    fits = _kv(**{**base, "n_pages": top, "page_stride": (1 << 31) // row})
+    assert _refused_by_all(L, ctx, fits, T=0) == {0}
+    assert L.moe_attn_decode(ctx, ctypes.addressof(_kv()), P, NH * D, P, 1 << 41, 4, P, None, 1, 1.0, 0.0, None, 0, P,
+                             None, None) == SHAPE
