@@ -139,6 +139,25 @@ __device__ __forceinline__ uint2 e4m3x8(const float2 (&y)[8], int from, float2 s
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// 1 / sqrt(mean of squares + eps) of a row whose sum of squares ss is beyond f32, or
+// so small that squares may have vanished: at a scale that brings them back.  Right
+// for root mean squares down to f32's smallest normal number.
+template <int L, int D>
+__device__ __forceinline__ float rms_at_scale(const float2 (&y)[8], float ss, float eps) {
+  const float scale = ss == INFINITY ? 0x1p-72f : ss < 1.f ? 0x1p64f : 1.f;  // 1: NaN
+  float2 s2 = both(0.f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 v = mul2(y[j], both(scale));
+    s2 = fma2(v, v, s2);
+  }
+  ss = s2.x + s2.y;
+  const uint32_t row = (uint32_t)((UINT64_C(1) << L) - 1) << (threadIdx.x & 31 & ~(L - 1));  // its lanes
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(row, ss, o);
+  return __frsqrt_rn(fmaf(ss, 1.0f / D, eps * scale * scale)) * scale;
+}
+
 // Where key and value rows go.
 enum class Dest { kRows, kBf16Cache, kE4m3Cache };
 
@@ -166,6 +185,8 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_con
   const int items = cut.tokens > 1 ? tokens * n_rows : min(cut.rows, n_rows - r_base);
   // this lane's pieces
   const bool turned = lane * 8 < a.half;
+  // the least sum of squares that f32 holds well enough; any, next to a larger eps
+  const float least = a.eps < 0x1p-60f ? 0x1p-100f : 0.f;
   const int o0 = turned && !a.interleaved ? 8 * lane : 16 * lane;
   const int o1 = turned && !a.interleaved ? a.half + 8 * lane : 16 * lane + 8;
   pdl_wait();
@@ -225,7 +246,8 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_con
       const float ss = row_sum<L>(s2.x + s2.y);
       const float *w = kind[k] == kQ ? a.q_weight : kind[k] == kK ? a.k_weight : nullptr;
       if (w != nullptr) {
-        const float2 rms = both(__frsqrt_rn(fmaf(ss, 1.0f / D, a.eps)));
+        float2 rms = both(__frsqrt_rn(fmaf(ss, 1.0f / D, a.eps)));
+        if (!(ss >= least && ss < INFINITY)) rms = both(rms_at_scale<L, D>(y, ss, a.eps));
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const float4 v = __ldg(reinterpret_cast<const float4 *>(w + (p < 2 ? o0 : o1)) + (p & 1));

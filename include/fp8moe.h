@@ -407,7 +407,8 @@ int moe_attn_status(moe_attn *a);
 /*
  * moe_attn_norm_rope - norm and rotate the query and key heads of T tokens.
  * Per head row x of d elements, in f32:
- *   y = x / sqrt(mean(x^2) + eps) * weight        (skipped if weight is NULL)
+ *   y = x / sqrt(mean(x^2) + eps) * weight        (skipped if weight is NULL;
+ *       right where x^2 is beyond f32 too, for a root of 2^-126 and more)
  *   rotate pair i < R/2 of y by the angle position * rope_freqs[i]
  * and one rounding to bf16.  Angles are taken modulo a turn to 2^-33 of one at
  * every int32 position, for frequencies of either sign up to 1 radian, and what is

@@ -788,3 +788,42 @@ def test_rotation_by_negative_frequencies():
     close(y[:, 0, 8:16], want, (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + far)
     close(z[:, 0, 8:16], -want, (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + far)
     assert torch.equal(y[:, 0, :8], z[:, 0, :8]) and torch.equal(y[:, 0, 8:16], -z[:, 0, 8:16])
+
+
+@pytest.mark.parametrize("d,R,inter", [(64, 0, False), (128, 128, False), (256, 64, True)])
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-30])
+def test_norm_of_rows_whose_squares_leave_f32(d, R, inter, eps):
+    """Rows up to bf16's largest value and down to its smallest: their sum of
+    squares is beyond f32 or below it, their norm is not.  Large rows (and tiny
+    ones where eps is as small) have outputs like any other's; ordinary rows and
+    rows with infinities beside them stay as they are."""
+    nh = nkv = 6
+    g = gen(d)
+    sizes = torch.tensor([2.0 ** 126, 2.0 ** 64, 1.0, 2.0 ** -60, 2.0 ** -80, 2.0 ** -120], device=DEV)
+    x = torch.rand(7, nh, d, generator=g, device=DEV) + 0.5  # within a factor of three
+    x = x * torch.where(torch.rand(7, nh, d, generator=g, device=DEV) < 0.5, -1.0, 1.0) * sizes[None, :, None]
+    q = x.to(torch.bfloat16)
+    k = q.flip(1).contiguous()
+    w = 1 + 0.2 * torch.rand(d, generator=g, device=DEV)
+    pos = torch.arange(7, dtype=torch.int32, device=DEV) * 1000 if R else None
+    freqs = rope_frequencies(R) if R else []
+    attn = DecodeAttention(nh, nkv, d, rope_freqs=freqs or None, interleaved=inter)
+    qo, ko = attn.norm_rope(q, k, pos, w, w, eps=eps)
+    e = float(np.float32(eps))
+    for got, x in ((qo, q), (ko, k)):
+        want, tol = _want_rows(x, w, pos, freqs, inter, e)
+        close(got, want, 2.0 ** -8 * np.abs(want) + 2.0 ** -134 + tol)
+    cache = make_cache(7, 1, nkv, d, "bf16", fill=0.0)
+    assert torch.equal(attn.append(q, k, k, pos, torch.arange(7, device=DEV), cache, w, w, eps=eps), qo)
+    assert torch.equal(cache.k[:, :, 0], ko) and torch.equal(cache.v[:, :, 0], k)
+    # without a weight nothing is scaled; an infinity makes its row zeros and a NaN
+    plain = DecodeAttention(nh, nkv, d)
+    assert all(torch.equal(a, b) for a, b in zip(plain.norm_rope(q, k, None), (q, k)))
+    q[3, 2, 5], q[4, 0, 7], q[5, 1] = float("inf"), float("-inf"), 0.0
+    zero = torch.zeros((), dtype=torch.bfloat16, device=DEV)
+    qi, ki = plain.norm_rope(q, k, None, w, w, eps=eps)
+    for t, h, i in ((3, 2, 5), (4, 0, 7)):
+        bad = torch.zeros(d, dtype=torch.bool, device=DEV)
+        bad[i] = True
+        assert torch.equal(torch.isnan(qi[t, h]), bad) and (qi[t, h][~bad] == zero).all()
+    assert (torch.isnan(qi[5, 1]) if eps == 0 else qi[5, 1] == zero).all() and torch.isfinite(ki).all()
