@@ -300,6 +300,8 @@ int moe_attn_status(moe_attn *a) {
   int flag = 0;
   ATTN_TRY(cudaMemcpy(&flag, a->err, sizeof(int), cudaMemcpyDeviceToHost));
   ATTN_TRY(cudaMemset(a->err, 0, sizeof(int)));
+  // a kernel on a stream that does not wait for the default one must find it cleared
+  ATTN_TRY(cudaStreamSynchronize(nullptr));
   return flag ? MOE_ERR_DEVICE : MOE_OK;
 }
 

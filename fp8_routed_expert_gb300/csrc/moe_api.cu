@@ -660,6 +660,8 @@ int moe_status(moe_ctx *c) {
   int flag = 0;
   CUDA_TRY(cudaMemcpy(&flag, c->err, sizeof(int), cudaMemcpyDeviceToHost));
   CUDA_TRY(cudaMemset(c->err, 0, sizeof(int)));
+  // a kernel on a stream that does not wait for the default one must find it cleared
+  CUDA_TRY(cudaStreamSynchronize(nullptr));
   if (flag & DEV_ERR_TIMEOUT) return MOE_ERR_DEVICE_TIMEOUT;
   if (flag & DEV_ERR_NONFINITE) return MOE_ERR_NONFINITE;
   if (flag) return MOE_ERR_DEVICE;

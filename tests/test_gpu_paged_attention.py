@@ -827,3 +827,18 @@ def test_norm_of_rows_whose_squares_leave_f32(d, R, inter, eps):
         bad[i] = True
         assert torch.equal(torch.isnan(qi[t, h]), bad) and (qi[t, h][~bad] == zero).all()
     assert (torch.isnan(qi[5, 1]) if eps == 0 else qi[5, 1] == zero).all() and torch.isfinite(ki).all()
+
+
+def test_errors_right_after_a_status_are_kept():
+    """The flag is cleared before moe_attn_status returns: an error on a stream
+    that does not wait for the default one, right after it, is reported."""
+    attn = DecodeAttention(2, 1, 64)
+    cache = make_cache(2, 8, 1, 64, "bf16", fill=1.0)
+    x, bad = randn(gen(1), 1, 1, 64), torch.tensor([16], device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    assert attn.status() == 0
+    for _ in range(200):
+        attn.write(cache, x, x, bad, stream=side)
+        assert attn.status() == C["MOE_ERR_DEVICE"]
+    assert attn.status() == 0 and (cache.k == 1).all()
