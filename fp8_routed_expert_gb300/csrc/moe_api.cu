@@ -538,7 +538,8 @@ int moe_init(moe_ctx **out, const moe_config *cfg) {
     *s.p = c->ws + off;
     off += align_up(s.bytes, 256);
   }
-  if (cudaMemset(c->ws, 0, total) != cudaSuccess) {
+  if (cudaMemset(c->ws, 0, total) != cudaSuccess ||
+      cudaDeviceSynchronize() != cudaSuccess) {  // ready for any stream
     cudaFree(c->ws);
     delete c;
     return MOE_ERR_CUDA;

@@ -90,3 +90,19 @@ def test_moe_and_attention_overlap_bit_identical(budget):
         assert torch.equal(moe.view(torch.int16), moe_ref.view(torch.int16))
         assert torch.equal(att.view(torch.int16), att_ref.view(torch.int16))
     assert lib().moe_set_sm_budget(layer.handle, 0) == 0
+
+
+def test_first_forward_on_another_stream():
+    """The context's cleared workspace is ready for a stream that does not wait
+    for the default one."""
+    fam = W.family("tiny")
+    dw = DeviceWeights(W.make_weights(fam))
+    x = x_dev(W.make_x(fam, 4))
+    want = make_layer(fam, 4).forward(x, *dw.args(), fam.top_k)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        layer = make_layer(fam, 65536)
+        out = layer.forward(x, *dw.args(), fam.top_k, stream=side)
+        assert layer.status() == 0 and torch.equal(out, want)
+        layer.close()
