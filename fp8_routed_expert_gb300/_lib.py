@@ -6,16 +6,17 @@ missing, ``lib()`` raises with the command that builds it.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import re
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libfp8moe.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "fp8moe.h")
 
-BINDING_PATH = os.path.join(PKG, "_torch_binding.so")
-
 _lib = None
+_binding = None
 
 
 class MoEConfig(ctypes.Structure):
@@ -117,13 +118,25 @@ def lib():
     return L
 
 
+def binding_path() -> str:
+    """The native binding's file, which serves one Python and one torch: its name
+    tells them, so that another one's is never loaded."""
+    import torch
+    return os.path.join(PKG, f"_torch_binding-torch{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def torch_binding():
     """The native binding of the paged attention's calls (csrc/torch_binding.cpp)."""
-    if not os.path.exists(BINDING_PATH):
-        raise RuntimeError(f"{BINDING_PATH} is not built; run `python -m fp8_routed_expert_gb300.build`")
-    lib()  # the C ABI that it calls
-    from . import _torch_binding
-    return _torch_binding
+    global _binding
+    if _binding is None:
+        path = binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is not built; run `python -m fp8_routed_expert_gb300.build`")
+        lib()  # the C ABI that it calls
+        spec = importlib.util.spec_from_file_location(f"{__package__}._torch_binding", path)
+        _binding = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_binding)
+    return _binding
 
 
 class MoEError(RuntimeError):

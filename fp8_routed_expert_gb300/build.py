@@ -1,9 +1,11 @@
 """Build libfp8moe.so (the layer's C ABI and its sm_103a kernels) and
-_torch_binding.so (the native Python binding of the paged attention) in-tree.
+_torch_binding-torch*.so (the native Python binding of the paged attention,
+for the Python and torch that run this) in-tree.
 
 Each .cu file is compiled separately and in parallel with nvcc for
 compute_103a / sm_103a only, then linked into one shared library next to
-this file; the binding is one C++ file against torch's headers.  ``python -m fp8_routed_expert_gb300.build`` runs it by hand.
+this file; the binding is one C++ file against torch's headers.  ``python -m
+fp8_routed_expert_gb300.build`` runs it by hand.
 """
 from __future__ import annotations
 
@@ -14,13 +16,14 @@ import subprocess
 import sys
 import sysconfig
 
+from ._lib import binding_path
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8moe.so")
-BINDING = os.path.join(PKG, "_torch_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -60,26 +63,22 @@ def _compile_binding() -> str:
     return obj
 
 
-def _link_binding(obj: str) -> None:
+def _link_binding(obj: str, path: str) -> None:
     import torch
-    tmp = BINDING + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-L", PKG,
            "-l:libfp8moe.so", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("link of _torch_binding.so failed")
-    os.replace(tmp, BINDING)
+        raise RuntimeError("link of the Python binding failed")
+    os.replace(tmp, path)
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    built = [f for f in (LIB, BINDING) if os.path.exists(f)]
-    if not force and len(built) == 2 and min(map(os.path.getmtime, built)) >= _deps_mtime():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
+def _build_lib(verbose: bool, extra_flags: list[str]) -> None:
     cc = nvcc()
-    flags = NVCC_FLAGS + (extra_flags or [])
+    flags = NVCC_FLAGS + extra_flags
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
@@ -92,10 +91,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_compile_binding)
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
         objs = list(ex.map(compile_one, srcs))
-        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cudalib = os.path.join(os.path.dirname(os.path.dirname(cc)), "lib64")
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart", "-L", cudalib,
@@ -105,7 +102,29 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("link of libfp8moe.so failed")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
+    """The C ABI's library, then the Python binding, each where it is missing or
+    older than its sources.  The library needs nvcc alone: where the binding
+    cannot be built the error says so, and the library is there."""
+    def fresh(path: str) -> bool:
+        return not force and os.path.exists(path) and os.path.getmtime(path) >= _deps_mtime()
+
+    binding = binding_path()
+    with_lib, with_binding = not fresh(LIB), not fresh(binding)
+    if not (with_lib or with_binding):
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        obj = ex.submit(_compile_binding) if with_binding else None
+        if with_lib:
+            _build_lib(verbose, extra_flags or [])
+        if obj is not None:
+            try:
+                _link_binding(obj.result(), binding)
+            except Exception as e:
+                raise RuntimeError(f"{LIB} is built, the paged attention's Python binding is not: {e}") from e
     return LIB
 
 
