@@ -105,6 +105,7 @@ def lib():
         "moe_attn_read": ([vp, vp, vp, i64, vp, i64, vp, i64, vp], ctypes.c_int),
         "moe_attn_decode": ([vp, vp, vp, i64, vp, i64, i64, vp, vp, i64, f32, f32, vp, i32, vp, vp, vp],
                             ctypes.c_int),
+        "moe_attn_decode_clusters": ([vp, vp, i64, i64], ctypes.c_int),
         "moe_route_noalloc": ([vp, i64, i64, vp, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp],
                               ctypes.c_int),
         "moe_debug_copy": ([vp, ctypes.c_char_p, vp, i64, ctypes.POINTER(ctypes.c_int64), vp],

@@ -210,3 +210,17 @@ class DecodeAttention:
         if rc:
             check(rc, "moe_attn_decode")
         return out if lse is None else (out, lse)
+
+    def decode_clusters(self, cache: PagedKVCache, batch: int, max_pages: int) -> int:
+        """How ``decode`` splits a call of ``batch`` sequences with page tables of
+        ``max_pages`` columns: clusters of CTAs per sequence and group of heads, or
+        0 where all sequences' tiles are cut evenly over the device."""
+        if self._ctx is None:
+            raise ValueError("the context is closed")
+        if (cache.n_kv_heads, cache.head_dim) != (self.n_kv_heads, self.head_dim):
+            raise ValueError(f"the cache holds {cache.n_kv_heads} heads of {cache.head_dim}; "
+                             f"the context has {self.n_kv_heads} of {self.head_dim}")
+        n = lib().moe_attn_decode_clusters(self._h, ctypes.addressof(cache._desc), batch, max_pages)
+        if n < 0:
+            check(n, "moe_attn_decode_clusters")
+        return n

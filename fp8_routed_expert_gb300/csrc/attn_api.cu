@@ -132,6 +132,26 @@ int take_clusters(const moe_attn *a, const DecodePlan &p, int format, int64_t li
   return (int)(splits * segments << k);
 }
 
+// Chooses how moe_attn_decode splits a call with r->B and r->capacity, and returns
+// the grid; r->cluster is 0 for the list of tiles.
+// More than 8 heads per key/value head: where clusters have few tiles per warp,
+// groups of 8, which read the rows again from L2, are faster than the products of
+// up to 16 heads in a warp.  16 heads of 128 elements, bf16, list against clusters
+// of groups of 8 and of 16:
+//   one sequence of 1000, 1 key/value head      -,      5.7,  8.9 us
+//   of 16000                                   15.1,   10.3, 14.6
+//   of 64000                                   20.0,   17.3, 18.1
+//   of 128000                                  26.1,   23.4, 22.3 (7 and 4 tiles per warp)
+//   of 32000, 4 key/value heads                27.5,   22.2, 19.7 (7 and 8)
+//   2 of up to 64000, 2 heads of 64 elements   17.7,     -,  19.1
+int split_decode(const moe_attn *a, int format, DecodeArgs *r) {
+  int grid = 0;
+  if (a->narrow.group < a->wide.group) grid = take_clusters(a, a->narrow, format, 4, r);
+  if (grid == 0) grid = take_clusters(a, a->wide, format, 16, r);
+  if (grid == 0) grid = (int)std::min<int64_t>(list_tiles(a->wide, format, a->cfg, *r), a->wide.ctas[format]);
+  return grid;
+}
+
 // The caller's cache, checked against the context, as the kernels take it.
 int view_of(const moe_attn *a, const moe_paged_kv *kv, KvView *v) {
   if (kv == nullptr) return MOE_ERR_ARG;
@@ -419,6 +439,20 @@ int moe_attn_read(moe_attn *a, const moe_paged_kv *kv, const int64_t *slots, int
   return MOE_OK;
 }
 
+int moe_attn_decode_clusters(const moe_attn *a, const moe_paged_kv *kv, int64_t B, int64_t max_pages) {
+  if (a == nullptr || B < 0) return MOE_ERR_ARG;
+  if (B > kMaxBatch) return MOE_ERR_SHAPE;
+  DecodeArgs r{};
+  CHECK(view_of(a, kv, &r.kv));
+  if (max_pages < 1 || max_pages > kMaxPositions / kv->page_size) return MOE_ERR_SHAPE;
+  if (B == 0) return 0;
+  r.B = (int)B;
+  r.capacity = max_pages * kv->page_size;
+  if (list_tiles(a->wide, kv->format, a->cfg, r) > INT64_C(1) << 29) return MOE_ERR_SHAPE;
+  split_decode(a, kv->format, &r);
+  return r.cluster > 0 ? r.splits : 0;
+}
+
 int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t q_stride,
                     const int32_t *page_table, int64_t table_stride, int64_t max_pages,
                     const int32_t *seq_lens, const int32_t *starts, int64_t B, float scale,
@@ -465,20 +499,7 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   a->last_stream = s;
   decode_page_division(&r);
   if (list_tiles(a->wide, kv->format, c, r) > INT64_C(1) << 29) return MOE_ERR_SHAPE;
-  // More than 8 heads per key/value head: where clusters have few tiles per warp,
-  // groups of 8, which read the rows again from L2, are faster than the products of
-  // up to 16 heads in a warp.  16 heads of 128 elements, bf16, list against clusters
-  // of groups of 8 and of 16:
-  //   one sequence of 1000, 1 key/value head      -,      5.7,  8.9 us
-  //   of 16000                                   15.1,   10.3, 14.6
-  //   of 64000                                   20.0,   17.3, 18.1
-  //   of 128000                                  26.1,   23.4, 22.3 (7 and 4 tiles per warp)
-  //   of 32000, 4 key/value heads                27.5,   22.2, 19.7 (7 and 8)
-  //   2 of up to 64000, 2 heads of 64 elements   17.7,     -,  19.1
-  int grid = 0;
-  if (a->narrow.group < a->wide.group) grid = take_clusters(a, a->narrow, kv->format, 4, &r);
-  if (grid == 0) grid = take_clusters(a, a->wide, kv->format, 16, &r);
-  if (grid == 0) grid = (int)std::min<int64_t>(list_tiles(a->wide, kv->format, c, r), a->wide.ctas[kv->format]);
+  const int grid = split_decode(a, kv->format, &r);
   ATTN_TRY(launch_paged_decode(r, c.head_dim, kv->format == MOE_KV_E4M3, grid, s));
   return MOE_OK;
 }

@@ -500,6 +500,15 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
                     void *stream);
 
 /*
+ * moe_attn_decode_clusters - how moe_attn_decode splits a call of B sequences with
+ * page tables of max_pages columns: the clusters of CTAs that share each sequence
+ * and group of heads (few sequences whose tables are not long), or 0 where the
+ * tiles of all sequences are cut evenly over the device.  Negative: MOE_ERR_*, as
+ * for the call.
+ */
+int moe_attn_decode_clusters(const moe_attn *a, const moe_paged_kv *kv, int64_t B, int64_t max_pages);
+
+/*
  * moe_selftest_wait_timeout - exercise the bounded device-side waits.  Every
  * wait inside the layer's kernels (mbarriers of TMA copies and tensor-core
  * work, cross-CTA counters) gives up after a time limit and records

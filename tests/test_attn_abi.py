@@ -226,3 +226,14 @@ def test_caches_whose_offsets_leave_the_address_range(L, ctx, fmt):
     assert _refused_by_all(L, ctx, fits, T=0) == {0}
     assert L.moe_attn_decode(ctx, ctypes.addressof(_kv()), P, NH * D, P, 1 << 41, 4, P, None, 1, 1.0, 0.0, None, 0, P,
                              None, None) == SHAPE
+
+
+def test_decode_clusters_refusals(L, ctx):
+    desc = _kv()
+    kv = ctypes.addressof(desc)
+    assert L.moe_attn_decode_clusters(None, kv, 1, 4) == ARG and L.moe_attn_decode_clusters(ctx, None, 1, 4) == ARG
+    assert L.moe_attn_decode_clusters(ctx, kv, -1, 4) == ARG and L.moe_attn_decode_clusters(ctx, kv, 0, 4) == 0
+    for B, pages in (((1 << 20) + 1, 4), (1, 0), (1, 1 << 27)):
+        assert L.moe_attn_decode_clusters(ctx, kv, B, pages) == SHAPE
+    bad = _kv(slot_stride=D + 8)
+    assert L.moe_attn_decode_clusters(ctx, ctypes.addressof(bad), 1, 4) == ALIGN

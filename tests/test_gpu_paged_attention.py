@@ -842,3 +842,75 @@ def test_errors_right_after_a_status_are_kept():
         attn.write(cache, x, x, bad, stream=side)
         assert attn.status() == C["MOE_ERR_DEVICE"]
     assert attn.status() == 0 and (cache.k == 1).all()
+
+
+# Page tables so wide that every call of few sequences is cut as a list.
+WIDE = 1 << 21
+
+
+def cut_as_a_list(b, attn):
+    """b's calls on attn are cut as a list of tiles."""
+    return attn.decode_clusters(b.cache, len(b.lens), b.width) == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nh,nkv,d,sms", [(5, 1, 64, 14), (8, 1, 128, 20), (3, 1, 256, 20), (16, 1, 64, 40), (12, 1, 128, 40),
+                                          (4, 2, 64, 28)])
+@pytest.mark.parametrize("lens", [[20000], [50000, 20, 0, 4000, 1]])
+def test_decode_list_joins_many_groups_of_parts(lens, nh, nkv, d, sms, fmt):
+    """A list whose longest segment spans some 40 CTAs: parts are joined in groups
+    of 16, then three groups.  Pieces of less than four tiles per warp, and, in the
+    longer list, of more, where segments count for more than their tiles.  The
+    oracle's result, to the same bits every time."""
+    b = Batch(lens, nh, nkv, d, fmt, 64, seed=nh + d + len(lens), width=WIDE // 64)
+    attn = DecodeAttention(nh, nkv, d, max_sms=sms)
+    assert cut_as_a_list(b, attn)
+    one = b.check(attn)
+    for _ in range(2):
+        again = b.run(attn)
+        assert torch.equal(one[0], again[0]) and torch.equal(one[1], again[1])
+    b.check(attn, softcap=25.0, window=19000)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens", [[150001], [150001, 20000, 0, 90000, 7]])
+def test_decode_list_over_the_device(lens, fmt):
+    """The list on all SMs, segments of hundreds of CTAs."""
+    b = Batch(lens, 2, 1, 64, fmt, 128, seed=len(lens), width=WIDE // 128)
+    attn = DecodeAttention(2, 1, 64)
+    assert cut_as_a_list(b, attn)
+    one = b.check(attn)
+    again = b.run(attn)
+    assert torch.equal(one[0], again[0]) and torch.equal(one[1], again[1])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nh,nkv,d", [(8, 2, 64), (12, 12, 128), (16, 1, 128), (5, 1, 256), (40, 2, 64), (18, 1, 256)])
+def test_decode_lists_of_small_calls(nh, nkv, d, fmt):
+    """Few short sequences with page tables that could hold far longer ones: the
+    list; with tables that only just cover them, clusters."""
+    attn = DecodeAttention(nh, nkv, d)
+    for lens in ([1, 1000], [500, 0, 33], [64], [2, 31, 32, 33]):
+        b = Batch(lens, nh, nkv, d, fmt, 16, seed=nh + len(lens), width=WIDE // 16)
+        assert cut_as_a_list(b, attn)
+        one = b.check(attn, softcap=20.0)
+        again = b.run(attn, softcap=20.0)
+        assert torch.equal(one[0], again[0]) and torch.equal(one[1], again[1])
+        b.check(attn, starts=torch.tensor([5] * len(lens), dtype=torch.int32, device=DEV), window=300)
+        b.table, b.width = b.table[:, :(max(lens) + 15) // 16], (max(lens) + 15) // 16
+        assert not cut_as_a_list(b, attn)
+        b.check(attn, softcap=20.0)
+
+
+def test_decode_clusters_tells_the_way():
+    attn = DecodeAttention(32, 8, 128)
+    cache = PagedKVCache.empty(4, 16, 8, 128, "bf16")
+    assert attn.decode_clusters(cache, 0, 10) == 0 and attn.decode_clusters(cache, 1, 64) == 1
+    assert attn.decode_clusters(cache, 1, 1000) > 1 and attn.decode_clusters(cache, 512, 1000) == 0
+    with pytest.raises(Exception, match="moe_attn_decode_clusters"):
+        attn.decode_clusters(cache, 1, 0)
+    with pytest.raises(ValueError):
+        attn.decode_clusters(PagedKVCache.empty(4, 16, 4, 128, "bf16"), 1, 64)
+    attn.close()
+    with pytest.raises(ValueError):
+        attn.decode_clusters(cache, 1, 64)
