@@ -444,7 +444,7 @@ int moe_attn_decode_clusters(const moe_attn *a, const moe_paged_kv *kv, int64_t 
   if (B > kMaxBatch) return MOE_ERR_SHAPE;
   DecodeArgs r{};
   CHECK(view_of(a, kv, &r.kv));
-  if (max_pages < 1 || max_pages > kMaxPositions / kv->page_size) return MOE_ERR_SHAPE;
+  if (max_pages < (B > 0 ? 1 : 0) || max_pages > kMaxPositions / kv->page_size) return MOE_ERR_SHAPE;
   if (B == 0) return 0;
   r.B = (int)B;
   r.capacity = max_pages * kv->page_size;
@@ -462,7 +462,7 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   if (B > kMaxBatch) return MOE_ERR_SHAPE;
   DecodeArgs r{};
   CHECK(view_of(a, kv, &r.kv));
-  if (max_pages < 1 || table_stride < 0 || table_stride > kMaxStride || max_pages > kMaxPositions / kv->page_size)
+  if (max_pages < (B > 0 ? 1 : 0) || table_stride < 0 || table_stride > kMaxStride || max_pages > kMaxPositions / kv->page_size)
     return MOE_ERR_SHAPE;
   if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0)
     return MOE_ERR_ARG;

@@ -237,3 +237,13 @@ def test_decode_clusters_refusals(L, ctx):
         assert L.moe_attn_decode_clusters(ctx, kv, B, pages) == SHAPE
     bad = _kv(slot_stride=D + 8)
     assert L.moe_attn_decode_clusters(ctx, ctypes.addressof(bad), 1, 4) == ALIGN
+
+
+def test_no_sequences_need_no_page_table(L, ctx):
+    """B = 0 is no work whatever the page table's width, none included."""
+    desc = _kv()
+    kv = ctypes.addressof(desc)
+    for pages in (0, 1, 9):
+        assert L.moe_attn_decode(ctx, kv, None, 0, None, 0, pages, None, None, 0, 1.0, 0.0, None, 0, None, None, None) == 0
+        assert L.moe_attn_decode_clusters(ctx, kv, 0, pages) == 0
+    assert L.moe_attn_decode(ctx, kv, None, 0, None, 0, -1, None, None, 0, 1.0, 0.0, None, 0, None, None, None) == SHAPE

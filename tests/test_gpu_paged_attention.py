@@ -914,3 +914,14 @@ def test_decode_clusters_tells_the_way():
     attn.close()
     with pytest.raises(ValueError):
         attn.decode_clusters(cache, 1, 64)
+
+
+def test_decode_of_an_empty_batch():
+    attn = DecodeAttention(4, 2, 64)
+    cache = PagedKVCache.empty(4, 16, 2, 64)
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device=DEV)
+    for width in (0, 3):
+        table, lens = torch.empty(0, width, dtype=torch.int32, device=DEV), torch.empty(0, dtype=torch.int32, device=DEV)
+        out, lse = attn.decode(q, cache, table, lens, lse=torch.empty(0, 4, device=DEV))
+        assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    assert attn.status() == 0
