@@ -10,12 +10,12 @@
 // the design keeps loads in flight and everything else out of their way.
 // Measured, of the measured copy rate (6.70 TB/s), a few us of each being the
 // launch, the search for the first tile, and the join:
-//   64 sequences of up to 8192, 32 heads over 8, 128 elements, e4m3: 88.0 us, 6.10 TB/s, 91%
-//   24 windows of up to 4096, 16 over 8, 256, bf16, capped scores:   61.0 us, 6.12 TB/s, 91%
-//   8 of up to 4096, 16 over 16, 128, bf16:                          29.7 us, 5.30 TB/s, 79%
-//   200 of up to 700, 24 over 6, 64, bf16, slopes:                   21.5 us, 3.52 TB/s, 53%
-//   1 of 200001, 16 over 1, 128, e4m3:                               24.9 us, 2.12 TB/s, 32%
-//   1 of 1000, 16 over 16, 128, bf16:                                 5.8 us, 1.41 TB/s, 21%
+//   64 sequences of up to 8192, 32 heads over 8, 128 elements, e4m3: 89.2 us, 6.01 TB/s, 90%
+//   24 windows of up to 4096, 16 over 8, 256, bf16, capped scores:   61.2 us, 6.10 TB/s, 91%
+//   8 of up to 4096, 16 over 16, 128, bf16:                          29.7 us, 5.31 TB/s, 79%
+//   200 of up to 700, 24 over 6, 64, bf16, slopes:                   21.6 us, 3.52 TB/s, 53%
+//   1 of 200001, 16 over 1, 128, e4m3:                               28.4 us, 1.86 TB/s, 28%
+//   1 of 1000, 16 over 16, 128, bf16:                                 5.7 us, 1.43 TB/s, 21%
 // The last ones are latency: the chain launch, length, page, rows, two products,
 // join, and in groups of 16 heads the issue of the matrix instructions.
 //
@@ -24,8 +24,8 @@
 // share a key/value head), and the list of all segments' tiles is cut evenly
 // over the warps, whatever the lengths: every warp finds its piece from the
 // lengths themselves.  In longer lists a segment counts a tile or two more, about
-// what its start and end cost (weighed, with joins at a CTA's end: 64 sequences of
-// up to 8192, e4m3, 103 us -> 89).  A warp writes the result of a segment that is
+// what its start and end cost (64 sequences of up to 8192, e4m3, 89.4 us, not
+// weighed 93.4; 200 of up to 700 21.6 and 24.3).  A warp writes the result of a segment that is
 // all its own.  Of a piece at most the first and the last segment are shared
 // with other warps; their parts (m, l, unnormalised output) stay in shared
 // memory until all warps of the CTA are done, so the loop over tiles has no
@@ -84,9 +84,9 @@ namespace fp8moe {
 namespace {
 
 constexpr int kJoin = 16;              // parts joined by one CTA
-// Parts whose loads are in flight together: 2 take longer where parts are many (16
-// heads over one, 200001 tokens cut as a list: 26.5 -> 29.0 us), 16 by the size of
-// their code in every call (32 sequences of up to 4096, 16 heads: 24.7 -> 27.3).
+// Parts whose loads are in flight together: 2 take longer where parts are many (3
+// sequences of up to 200000, 16 heads over one, e4m3: 40.9 -> 43.3 us), 16 by the
+// size of their code in every call (32 of up to 4096, 16 heads: 27.5 -> 30.1).
 constexpr int kBatch = 4;
 constexpr int kWeighFrom = 4;          // tiles per warp from which on segments count more than their tiles
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -98,8 +98,10 @@ constexpr float kRest = 0x1p12f;       // what f16 leaves of them (2^3 at most) 
 // MH: query heads of a group at most; KM: 16-key steps of a warp's tile; NS:
 // stages of a warp's ring; CTAS: that fit on an SM.  Tiles of 32 keys, 16 where
 // more do not fit the registers (256 elements in bf16); two stages where rows are
-// short, one where a tile is 16 KB, or 8 KB for 8 warps (16 heads of 128 elements,
-// e4m3, 32 sequences of up to 4096: one stage 25.0 us, two 26.2, before later steps).
+// short (e4m3, 64 x 8192, 8 heads of 128 elements at most: 89.4 us, one 91.5), one
+// where a tile is 16 KB, or 8 KB for 8 warps (32 x 4096, 16 heads: 27.5, two 29.8).
+// 16 heads of 128 elements, and 256 elements in e4m3, take all 255 registers and
+// spill (16 to 320 bytes a thread).
 template <int D_, bool E4M3_, int MH_, int KM_, int kWarps_, int NS_, int CTAS_>
 struct Shape {
   static constexpr int D = D_, MH = MH_, KM = KM_, NS = NS_, CTAS = CTAS_;
@@ -1344,10 +1346,10 @@ cudaError_t with_shape(int d, bool e4m3, int group, F f) {
 
 // Up to 16 heads at a time: in long lists a second pass over the rows costs more
 // than wider steps (16 heads of 128 elements, 32 sequences of up to 4096 tokens, 4
-// key/value heads: e4m3 23.9 us, against 29.2 in groups of 8; bf16 31.2 against 35.5).
-// At 256 elements 16 heads' outputs do not fit the registers of enough warps
-// (sequences of up to 2048, before later steps: e4m3 50 us, in groups of 8 that
-// read from L2 the second time 32; bf16 52 against 42).
+// key/value heads: e4m3 27.5 us, against 31.3 in groups of 8; bf16 31.3 against 35.6).
+// 16 heads of 256 elements would take 128 registers for the outputs and 64 for the
+// queries, which leaves too few for a tile; groups of 8 read their rows from L2 the
+// second time (32 sequences of up to 2048: e4m3 35.1 us, bf16 40.0).
 int decode_group(int heads_per_kv, int d, bool narrow) {
   const int most = narrow || d == 256 ? 8 : 16, n = (heads_per_kv + most - 1) / most;
   return (heads_per_kv + n - 1) / n;

@@ -164,10 +164,12 @@ enum class Dest { kRows, kBf16Cache, kE4m3Cache };
 // Grid (token groups, row blocks); items of a CTA: (token, row).  Every row is
 // read and written once; a lane's rows are all in flight before the angles are
 // computed, and the angles of a token are computed once for all its heads.
-// Issue slots bound it next to HBM, hence the layout above without shuffles of
-// the row itself, and arithmetic on pairs.  4096 tokens of 56 heads of 128
-// elements: 23.5 us, 5.0 TB/s, 75% of the measured copy rate (two rows per lane
-// group exchanged by shuffles 37 us, one f32 per instruction 25.5).
+// Issue slots are its busiest unit (68%; the memory's 57%) and the barrier after
+// the angles its longest stall, hence the layout above without shuffles of the row
+// itself, and arithmetic on pairs.  4096 tokens of 56 heads of 128 elements:
+// 24.1 us, 4.9 TB/s, 73% of the measured copy rate (two rows per lane group
+// exchanged by shuffles 37 us, one f32 per instruction 2 us more).  The same with
+// 8 value heads into the cache: 29.6 us bf16, 29.7 e4m3.
 template <int D, Dest kDest>
 __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_constant__ RowArgs a,
                                                                 const RowCut cut) {
@@ -334,9 +336,9 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_con
 }
 
 // Rows out of the cache, cut over CTAs like the rows in: a lane takes 16
-// consecutive elements.  Bound by HBM and the latency of slot, scale and row.
-// Writing and reading back 8192 tokens of 16 rows of 128 elements, e4m3: 21.5 us
-// for both launches, 4.7 TB/s, 71% of the measured copy rate.
+// consecutive elements.  The chain of slot, barrier, row and scale bounds it (the
+// memory is 42% busy).  8192 tokens of 16 rows of 128 elements: written in 12.1 us
+// bf16, 11.6 e4m3, read in 12.5 and 10.4, 83 to 65% of the measured copy rate.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kRowThreads) read_rows_kernel(const __grid_constant__ ReadArgs a,
                                                                 const RowCut cut) {
