@@ -36,7 +36,9 @@ def _memory_of(stream, device: int):
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream_handle(stream), device=torch.device("cuda", device))
+        handle, dev = _stream_handle(stream), torch.device("cuda", device)
+        # an ExternalStream of handle 0 would be a new stream, not the default one
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
     return torch.cuda.stream(stream)
 
 

@@ -162,3 +162,14 @@ def test_outputs_come_from_the_memory_of_the_calls_stream(monkeypatch):
             made.clear(), ran.clear()
             call(given)
             assert made == [used] * outputs and ran == [used] and current == [5]
+
+
+def test_handle_zero_is_the_default_stream(monkeypatch):
+    """The memory of a call on handle 0 is the default stream's."""
+    import torch
+
+    from fp8_routed_expert_gb300.layer import _memory_of
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: ("external", handle, device.index))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: ("default", device.index))
+    assert _memory_of(0, 3) == ("default", 3) and _memory_of(7, 2) == ("external", 7, 2)

@@ -925,3 +925,22 @@ def test_decode_of_an_empty_batch():
         out, lse = attn.decode(q, cache, table, lens, lse=torch.empty(0, 4, device=DEV))
         assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
     assert attn.status() == 0
+
+
+def test_outputs_of_calls_on_the_default_streams_handle():
+    """Handle 0, while another stream is the current one: outputs are of the
+    default stream's memory."""
+    attn = DecodeAttention(8, 2, 128)
+    q, k = randn(gen(1), 64, 8, 128), randn(gen(2), 64, 2, 128)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        old = torch.empty(64, 8, 128, dtype=torch.bfloat16, device=DEV)
+        at = old.data_ptr()
+        torch.cuda._sleep(2_000_000)
+        old.fill_(1.0)
+        del old
+        out, _ = attn.norm_rope(q, k, None, stream=0)
+    assert out.data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(out, q) and attn.status() == 0
