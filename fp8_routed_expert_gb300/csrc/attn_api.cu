@@ -462,7 +462,8 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   if (B > kMaxBatch) return MOE_ERR_SHAPE;
   DecodeArgs r{};
   CHECK(view_of(a, kv, &r.kv));
-  if (max_pages < (B > 0 ? 1 : 0) || table_stride < 0 || table_stride > kMaxStride || max_pages > kMaxPositions / kv->page_size)
+  if (max_pages < (B > 0 ? 1 : 0) || max_pages > kMaxPositions / kv->page_size || table_stride < 0 ||
+      table_stride > kMaxStride)
     return MOE_ERR_SHAPE;
   if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0)
     return MOE_ERR_ARG;

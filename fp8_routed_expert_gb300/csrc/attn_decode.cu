@@ -25,8 +25,8 @@
 // over the warps, whatever the lengths: every warp finds its piece from the
 // lengths themselves.  In longer lists a segment counts a tile or two more, about
 // what its start and end cost (64 sequences of up to 8192, e4m3, 89.4 us, not
-// weighed 93.4; 200 of up to 700 21.6 and 24.3).  A warp writes the result of a segment that is
-// all its own.  Of a piece at most the first and the last segment are shared
+// weighed 93.4; 200 of up to 700 21.6 and 24.3).  A warp writes the result of a
+// segment that is all its own.  Of a piece at most the first and the last segment are shared
 // with other warps; their parts (m, l, unnormalised output) stay in shared
 // memory until all warps of the CTA are done, so the loop over tiles has no
 // CTA-wide barrier, and are then joined.  A segment that several CTAs share
