@@ -106,6 +106,14 @@ def lib():
         "moe_attn_decode": ([vp, vp, vp, i64, vp, i64, i64, vp, vp, i64, f32, f32, vp, i32, vp, vp, vp],
                             ctypes.c_int),
         "moe_attn_decode_clusters": ([vp, vp, i64, i64], ctypes.c_int),
+        "moe_attn_prefill": ([vp, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i64, i32, f32, f32, vp, i32, vp, i64, vp,
+                              vp], ctypes.c_int),
+        "moe_proj_init": ([ctypes.POINTER(ctypes.c_void_p), i32, i32], ctypes.c_int),
+        "moe_proj_free": ([vp], None),
+        "moe_proj_status": ([vp], ctypes.c_int),
+        "moe_proj_norm": ([vp, vp, i64, vp, i64, i64, i64, vp, f32, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp],
+                          ctypes.c_int),
+        "moe_proj_matmul": ([vp, vp, i64, vp, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp], ctypes.c_int),
         "moe_route_noalloc": ([vp, i64, i64, vp, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp],
                               ctypes.c_int),
         "moe_debug_copy": ([vp, ctypes.c_char_p, vp, i64, ctypes.POINTER(ctypes.c_int64), vp],
@@ -127,7 +135,8 @@ def binding_path() -> str:
 
 
 def torch_binding():
-    """The native binding of the paged attention's calls (csrc/torch_binding.cpp)."""
+    """The native binding of the attention's and the projections' calls
+    (csrc/torch_binding.cpp)."""
     global _binding
     if _binding is None:
         path = binding_path()

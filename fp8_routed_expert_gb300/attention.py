@@ -1,8 +1,8 @@
 """Attention over a paged key/value cache: the serving form of the attention
 beside the MoE.  ``PagedKVCache`` describes the cache, ``DecodeAttention`` is
-the context whose calls norm and rotate heads, write and read the cache and
-attend to it (moe_attn_* of include/fp8moe.h, where each call's arithmetic,
-layouts and errors are stated).  Every step runs in the library's kernels.
+the context whose calls norm and rotate heads, write and read the cache, attend
+to it and attend within whole prompts (moe_attn_* of include/fp8moe.h, where each
+call's arithmetic, layouts and errors are stated).  Every step runs in the library's kernels.
 """
 from __future__ import annotations
 
@@ -209,6 +209,27 @@ class DecodeAttention:
                             self._stream(stream))
         if rc:
             check(rc, "moe_attn_decode")
+        return out if lse is None else (out, lse)
+
+    def prefill(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: torch.Tensor,
+                k_starts: torch.Tensor | None = None, causal: bool = True, scale: float | None = None,
+                softcap: float = 0.0, slopes: torch.Tensor | None = None, window: int = 0,
+                out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
+        """Attention of prompts packed one after another: q bf16 [Tq, n_heads, d],
+        k and v bf16 [Tk, n_kv_heads, d]; sequence b's rows begin at q_starts[b] and
+        k_starts[b] (int32 [B + 1], the last one the end; k_starts None: q_starts).
+        Its last query is its last key's token, so a chunk of a prompt comes with the
+        keys and values before it (``read``).  Options as for ``decode``; without
+        ``causal`` later keys are visible too.  Returns out bf16 [Tq, n_heads, d], or
+        (out, lse) if ``lse`` f32 [Tq, n_heads] is given; rows outside the sequences
+        are left as they are."""
+        if out is None:
+            out = self._new(q.shape[0], self.n_heads, stream)
+        rc = self._b.prefill(self._ctx, q, k, v, q_starts, q_starts if k_starts is None else k_starts, causal,
+                             self._scale if scale is None else scale, softcap, slopes, window, out, lse,
+                             self._stream(stream))
+        if rc:
+            check(rc, "moe_attn_prefill")
         return out if lse is None else (out, lse)
 
     def decode_clusters(self, cache: PagedKVCache, batch: int, max_pages: int) -> int:

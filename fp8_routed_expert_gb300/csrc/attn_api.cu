@@ -6,6 +6,7 @@
 #include <new>
 #include <vector>
 
+#include "attn_prefill.h"
 #include "common.cuh"
 #include "fp8moe.h"
 #include "paged_attn.h"
@@ -250,6 +251,7 @@ int moe_attn_init(moe_attn **out, const moe_attn_config *cfg) {
   ATTN_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, cfg->device));
   ATTN_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, cfg->device));
   if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
+  ATTN_TRY(ready_prefill(cfg->head_dim));
   moe_attn *a = new (std::nothrow) moe_attn();
   if (a == nullptr) return MOE_ERR_NOMEM;
   a->cfg = *cfg;
@@ -322,7 +324,7 @@ int moe_attn_status(moe_attn *a) {
   ATTN_TRY(cudaMemset(a->err, 0, sizeof(int)));
   // a kernel on a stream that does not wait for the default one must find it cleared
   ATTN_TRY(cudaStreamSynchronize(nullptr));
-  return flag ? MOE_ERR_DEVICE : MOE_OK;
+  return flag & DEV_ERR_TIMEOUT ? MOE_ERR_DEVICE_TIMEOUT : flag ? MOE_ERR_DEVICE : MOE_OK;
 }
 
 int moe_attn_norm_rope(moe_attn *a, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
@@ -502,6 +504,58 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
   if (list_tiles(a->wide, kv->format, c, r) > INT64_C(1) << 29) return MOE_ERR_SHAPE;
   const int grid = split_decode(a, kv->format, &r);
   ATTN_TRY(launch_paged_decode(r, c.head_dim, kv->format == MOE_KV_E4M3, grid, s));
+  return MOE_OK;
+}
+
+int moe_attn_prefill(moe_attn *a, const void *q, int64_t q_stride, int64_t Tq, const void *k, int64_t k_stride,
+                     const void *v, int64_t v_stride, int64_t Tk, const int32_t *q_starts,
+                     const int32_t *k_starts, int64_t B, int32_t causal, float scale, float softcap,
+                     const float *slopes, int32_t window, void *out, int64_t out_stride, float *lse,
+                     void *stream) {
+  CHECK(check_T(a, Tq));
+  CHECK(check_T(a, Tk));
+  if (B < 0) return MOE_ERR_ARG;
+  if (B > kMaxBatch) return MOE_ERR_SHAPE;
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0 || (causal != 0 && causal != 1))
+    return MOE_ERR_ARG;
+  if (B == 0 || Tq == 0) return MOE_OK;
+  const moe_attn_config &c = a->cfg;
+  CHECK(check_rows(q, q_stride, c.n_heads, c.head_dim));
+  if (Tk > 0) {
+    CHECK(check_rows(k, k_stride, c.n_kv_heads, c.head_dim));
+    CHECK(check_rows(v, v_stride, c.n_kv_heads, c.head_dim));
+  }
+  CHECK(check_rows(out, out_stride, c.n_heads, c.head_dim));
+  if (!q_starts || !k_starts) return MOE_ERR_ARG;
+  if (!aligned(q_starts, 4) || !aligned(k_starts, 4) || !aligned(slopes, 4) || !aligned(lse, 4)) return MOE_ERR_ALIGN;
+  PrefillArgs r{};
+  r.q = static_cast<const __nv_bfloat16 *>(q);
+  r.k = static_cast<const __nv_bfloat16 *>(k);
+  r.v = static_cast<const __nv_bfloat16 *>(v);
+  r.q_stride = q_stride;
+  r.k_stride = k_stride;
+  r.v_stride = v_stride;
+  r.Tq = (int)Tq;
+  r.Tk = (int)Tk;
+  r.q_starts = q_starts;
+  r.k_starts = k_starts;
+  r.B = (int)B;
+  r.n_heads = c.n_heads;
+  r.n_kv = c.n_kv_heads;
+  r.scale = scale;
+  r.softcap = softcap;
+  r.slopes = slopes;
+  r.window = window;
+  r.causal = causal;
+  r.out = static_cast<__nv_bfloat16 *>(out);
+  r.out_stride = out_stride;
+  r.lse = lse;
+  r.err = a->err;
+  plan_prefill(&r, c.head_dim);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ATTN_TRY(cudaSetDevice(c.device));
+  a->last_stream = s;
+  ATTN_TRY(launch_prefill(r, c.head_dim, c.max_sms > 0 && c.max_sms < a->sms ? c.max_sms : a->sms, s));
   return MOE_OK;
 }
 

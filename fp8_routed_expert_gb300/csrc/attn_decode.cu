@@ -75,6 +75,7 @@
 //   down to 2^-48 of the largest weight.  (The rest's product with scaled codes
 //   instead: 64 x 8192 92.6 us, this way 89.3, one product alone 88.1.  Weights and
 //   codes in bf16, which has no such limit: 103, most of it conversions.)
+#include "attn_math.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "paged_attn.h"
@@ -89,7 +90,6 @@ constexpr int kJoin = 16;              // parts joined by one CTA
 // size of their code in every call (32 of up to 4096, 16 heads: 27.5 -> 30.1).
 constexpr int kBatch = 4;
 constexpr int kWeighFrom = 4;          // tiles per warp from which on segments count more than their tiles
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLag = 8.f;            // log2 of the largest weight, before its scale
 constexpr float kLagV = 4.f;           // the same with its scale
 constexpr float kWeightBits = 11.f;    // e4m3: weights are scaled by 2^11, to 2^15 at most
@@ -219,20 +219,6 @@ __device__ __forceinline__ float lg2(float x) {
 // which any factor keeps.
 __device__ __forceinline__ float rescale(float from, float to) {
   return from == -INFINITY ? 1.f : ex2(from - to);
-}
-
-// tanh: an odd polynomial below 0.6 (least-squares fit of the relative error
-// over Chebyshev points, 3e-9), (1 - t) / (1 + t) with t = e^(-2|y|) above.
-__device__ __forceinline__ float tanh_f32(float y) {
-  const float z = y * y;
-  float p = fmaf(z, -0.005895158741623163f, 0.020795973017811775f);
-  p = fmaf(z, p, -0.053783830255270004f);
-  p = fmaf(z, p, 0.13331924378871918f);
-  p = fmaf(z, p, -0.33333298563957214f);
-  const float small = fmaf(y * z, p, y);
-  const float t = ex2(-2.f * kLog2e * fabsf(y));
-  const float large = copysignf(__fdividef(1.f - t, 1.f + t), y);
-  return fabsf(y) < 0.6f ? small : large;
 }
 
 // Two weights in 16 bits each, and what the pair leaves of them (f16: times 2^12).

@@ -1,0 +1,309 @@
+// Product of e4m3 rows with e4m3 weights, a f32 scale for each 1 x 128 of the rows
+// and each 128 x 128 of the weights (moe_proj_matmul of the C ABI):
+//   out[m, n] = bf16( sum over K blocks b of a_scale[m, b] * w_scale[n / 128, b] *
+//                     sum over k in b of a[m, k] * w[n, k] )
+//
+// Tile: 128 rows x Columns columns, K in steps of one block.  TMA brings 128-byte
+// rows of both operands (zeros outside the matrices, so any M, N and K), the
+// 128-byte swizzle is what tcgen05.mma kind::f8f6f4 reads, and a block's sum lands
+// in one of two TMEM buffers.  Eight warps take it from there and add it, times the
+// product of the two scales, to f32 registers while the other buffer fills: lane =
+// row, so a thread's scale is one number per block (and 128 columns).
+//
+// A tile's K blocks may be split over the CTAs of a cluster (few tiles): each
+// leaves its sums in its shared memory, and every CTA adds a share of the tile over
+// all of them, in rank order.  Nothing is added in order of arrival, and no call
+// needs a workspace.
+//
+// Warps: 0 issues TMA, 1 allocates TMEM and issues the products, 2..9 add up.
+#include "common.cuh"
+#include "kernels.h"
+#include "proj.h"
+#include "tcgen05_ops.cuh"
+
+namespace fp8moe {
+using namespace sm100;
+namespace {
+
+constexpr int kRows = 128, kBlock = 128, kSumWarps = 8, kThreads = 64 + 32 * kSumWarps;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+template <int Columns>
+struct Ring {
+  static constexpr int kA = kRows * kBlock, kStage = kA + Columns * kBlock;
+  static constexpr int kStages = 196608 / kStage;
+  static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+};
+
+struct Item {
+  int64_t m0, n0;
+  int b0, b1;  // K blocks
+};
+
+template <int Columns>
+__device__ __forceinline__ Item item_of(const MatmulArgs &p, int64_t tile, int rank) {
+  const int64_t m_tiles = (p.M + kRows - 1) / kRows;
+  Item it;
+  it.m0 = tile % m_tiles * kRows;
+  it.n0 = tile / m_tiles * Columns;
+  it.b0 = (int)((int64_t)p.blocks * rank / p.splits);
+  it.b1 = (int)((int64_t)p.blocks * (rank + 1) / p.splits);
+  return it;
+}
+
+__device__ __forceinline__ void give_up(volatile int *stop, int *err) {
+  *stop = 1;
+  set_error(err, DEV_ERR_TIMEOUT);
+}
+
+// Eight neighbouring columns of a row, as far as the matrix goes.
+__device__ __forceinline__ void store8(const MatmulArgs &p, int64_t row, int64_t col, const float (&v)[8]) {
+  __nv_bfloat16 *o = p.out + row * p.out_stride + col;
+  if (col + 8 <= p.N) {
+    *reinterpret_cast<uint4 *>(o) =
+        make_uint4(bf16x2_of(v[0], v[1]), bf16x2_of(v[2], v[3]), bf16x2_of(v[4], v[5]), bf16x2_of(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j < p.N) o[j] = __float2bfloat16_rn(v[j]);
+  }
+}
+
+template <int Columns>
+__global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_constant__ CUtensorMap ta,
+                                                             const __grid_constant__ CUtensorMap tw, const MatmulArgs p) {
+  using R = Ring<Columns>;
+  constexpr int kHalf = Columns / 2;  // columns of a summing warp
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[R::kStages], empty[R::kStages], sum_full[2], sum_empty[2];
+  __shared__ uint32_t tmem_sh;
+  __shared__ volatile int stop;
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < R::kStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+    for (int b = 0; b < 2; ++b) mbar_init(&sum_full[b], 1), mbar_init(&sum_empty[b], kSumWarps);
+    stop = 0;
+    fence_mbar_init();
+    prefetch_tmap(&ta);
+    prefetch_tmap(&tw);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_sh, 2 * Columns);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  pdl_wait();
+  pdl_trigger();
+  const int rank = p.splits > 1 ? (int)cluster_rank() : 0;
+  const int64_t first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int64_t tile = first; tile < p.tiles && !stop; tile += step) {
+        const Item it = item_of<Columns>(p, tile, rank);
+        for (int b = it.b0; b < it.b1; ++b) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, &stop, kWaitNs)) {
+            give_up(&stop, p.err);
+            break;
+          }
+          uint8_t *s = smem + (size_t)stage * R::kStage;
+          mbar_arrive_expect_tx(&full[stage], (uint32_t)(p.a_rows + Columns) * kBlock);
+          tma_load_2d(s, &ta, b * kBlock, (int32_t)it.m0, &full[stage]);
+          tma_load_2d(s + R::kA, &tw, b * kBlock, (int32_t)it.n0, &full[stage]);
+          if (++stage == R::kStages) stage = 0, phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3_f32(kRows, Columns);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, bphase = 0;
+      for (int64_t tile = first; tile < p.tiles && !stop; tile += step) {
+        const Item it = item_of<Columns>(p, tile, rank);
+        for (int b = it.b0; b < it.b1; ++b) {
+          if (!mbar_wait(&sum_empty[buf], bphase ^ 1u, &stop, kWaitNs) || !mbar_wait(&full[stage], phase, &stop, kWaitNs)) {
+            give_up(&stop, p.err);
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(smem + (size_t)stage * R::kStage);
+#pragma unroll
+          for (int k = 0; k < kBlock / 32; ++k)
+            mma_f8f6f4(tmem + (uint32_t)(buf * Columns), sw128_kmajor_desc(a + k * 32), sw128_kmajor_desc(a + R::kA + k * 32), idesc,
+                       k > 0 ? 1u : 0u);
+          mma_commit(&empty[stage]);
+          mma_commit(&sum_full[buf]);
+          if (++stage == R::kStages) stage = 0, phase ^= 1u;
+          buf ^= 1;
+          if (buf == 0) bphase ^= 1u;
+        }
+      }
+    }
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;  // TMEM lanes and columns of this warp
+    const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * kHalf);
+    const int n_blocks = (int)((p.N + 127) / 128);
+    int buf = 0;
+    uint32_t bphase = 0;
+    bool ok = true;
+    for (int64_t tile = first; ok && tile < p.tiles; tile += step) {
+      const Item it = item_of<Columns>(p, tile, rank);
+      const int64_t row = it.m0 + quarter * 32 + lane, col = it.n0 + half * kHalf;
+      const bool any = it.m0 + quarter * 32 < p.M && col < p.N;  // of the warp
+      const float *sa = p.a_scale + (row < p.M ? row : p.M - 1) * p.a_row;
+      const int nb = (int)(col / 128);
+      const float *sw = p.w_scale + (int64_t)(nb < n_blocks ? nb : n_blocks - 1) * p.blocks;
+      uint64_t acc[kHalf / 2];
+#pragma unroll
+      for (int j = 0; j < kHalf / 2; ++j) acc[j] = 0;
+      // the next block's scales are loaded while this one is added
+      float sa_next = it.b0 < it.b1 ? __ldg(sa + it.b0 * p.a_block) : 0.f, sw_next = it.b0 < it.b1 ? __ldg(sw + it.b0) : 0.f;
+      for (int b = it.b0; b < it.b1; ++b) {
+        const float c = sa_next * sw_next;
+        const uint64_t cc = pack_f32x2(c, c);
+        if (b + 1 < it.b1) {
+          sa_next = __ldg(sa + (b + 1) * p.a_block);
+          sw_next = __ldg(sw + b + 1);
+        }
+        if (!mbar_wait(&sum_full[buf], bphase, &stop, kWaitNs)) {
+          give_up(&stop, p.err);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (any) {
+#pragma unroll
+          for (int ch = 0; ch < kHalf / 16; ++ch) {
+            float v[16];
+            tmem_ld_32x32b_x16(t_lane + (uint32_t)(buf * Columns + ch * 16), v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[ch * 8 + j] = fma_f32x2(pack_f32x2(v[2 * j], v[2 * j + 1]), cc, acc[ch * 8 + j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sum_empty[buf]);
+        buf ^= 1;
+        if (buf == 0) bphase ^= 1u;
+      }
+      if (!ok || !any || row >= p.M) continue;
+      if (p.splits == 1) {
+#pragma unroll
+        for (int j = 0; j < kHalf; j += 8) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack_f32x2(acc[j / 2 + i]);
+            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+          }
+          if (col + j < p.N) store8(p, row, col + j, v);
+        }
+      } else {
+        // [128][Columns] f32, the 16-byte pieces of a row exchanged by its number
+        // so that a warp's rows do not meet in one bank
+        float *mine = reinterpret_cast<float *>(smem) + (quarter * 32 + lane) * Columns;
+#pragma unroll
+        for (int j = 0; j < kHalf; j += 4) {
+          const float2 f = unpack_f32x2(acc[j / 2]), g = unpack_f32x2(acc[j / 2 + 1]);
+          const int piece = (half * kHalf + j) / 4 ^ (lane & (Columns / 4 - 1));
+          *reinterpret_cast<float4 *>(mine + 4 * piece) = make_float4(f.x, f.y, g.x, g.y);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (p.splits > 1) {
+    cluster_sync_all();
+    const Item it = item_of<Columns>(p, first, rank);
+    const int rows = (int)(p.M - it.m0 < kRows ? p.M - it.m0 : kRows);
+    const uint32_t base = smem_u32(smem);
+    // unit u: 8 columns of a row
+    for (int u = rank + p.splits * threadIdx.x; u < rows * (Columns / 8); u += p.splits * kThreads) {
+      const int r = u / (Columns / 8), c = u % (Columns / 8) * 2;
+      if (it.n0 + 4 * c >= p.N) continue;
+      const int swap = r & 31 & (Columns / 4 - 1);
+      const uint32_t at0 = base + (uint32_t)(r * Columns + 4 * (c ^ swap)) * 4, at1 = base + (uint32_t)(r * Columns + 4 * (c + 1 ^ swap)) * 4;
+      float v[8] = {};
+      for (int q = 0; q < p.splits; ++q) {
+        const float4 f = ld_cluster16(map_to_rank(at0, (uint32_t)q)), g = ld_cluster16(map_to_rank(at1, (uint32_t)q));
+        v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w, v[4] += g.x, v[5] += g.y, v[6] += g.z, v[7] += g.w;
+      }
+      store8(p, it.m0 + r, it.n0 + 4 * c, v);
+    }
+    cluster_sync_all();  // no CTA leaves while its sums are read
+  }
+  __syncthreads();
+  if (stop) {
+    // copies and products in flight land before the memory goes away
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 50000ull) {
+    }
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * Columns);
+  }
+}
+
+template <int Columns>
+cudaError_t launch_columns(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, int sms, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(m.splits > 1 ? m.tiles * m.splits : m.tiles < sms ? m.tiles : sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Ring<Columns>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)m.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = m.splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, matmul_kernel<Columns>, a, w, m);
+}
+
+template <int Columns>
+cudaError_t ready_columns() {
+  return cudaFuncSetAttribute(matmul_kernel<Columns>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Ring<Columns>::kSmem);
+}
+
+}  // namespace
+
+void split_matmul(int64_t M, int64_t N, int64_t K, int sms, int *columns, int *splits) {
+  const int64_t rows = (M + kRows - 1) / kRows, blocks = (K + kBlock - 1) / kBlock;
+  const auto tiles = [&](int c) { return rows * ((N + c - 1) / c); };
+  *splits = 1;
+  if (tiles(256) >= sms) {
+    *columns = 256;
+    return;
+  }
+  *columns = tiles(128) * 8 >= sms ? 128 : 64;
+  const int64_t room = sms / tiles(*columns);
+  *splits = (int)(room < 1 ? 1 : room > 8 ? 8 : room);
+  if (*splits > blocks) *splits = (int)(blocks < 1 ? 1 : blocks);
+}
+
+cudaError_t ready_matmul() {
+  for (cudaError_t e : {ready_columns<64>(), ready_columns<128>(), ready_columns<256>()})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
+}
+
+cudaError_t launch_matmul(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, int columns, int sms, cudaStream_t s) {
+  switch (columns) {
+    case 64: return launch_columns<64>(a, w, m, sms, s);
+    case 128: return launch_columns<128>(a, w, m, sms, s);
+    default: return launch_columns<256>(a, w, m, sms, s);
+  }
+}
+
+}  // namespace fp8moe

@@ -1,5 +1,6 @@
-// Python binding of the paged attention's calls (moe_attn_*): checks torch
-// tensors and passes their pointers and strides to the C ABI.
+// Python binding of the attention's and the projections' calls (moe_attn_*,
+// moe_proj_*): checks torch tensors and passes their pointers and strides to the C
+// ABI.
 //
 // A decode step's calls run for a few microseconds on the GPU; reading types,
 // shapes, strides and pointers of their tensors attribute by attribute from
@@ -7,7 +8,7 @@
 // 2, most of it the launch.  The functions take the context as (handle,
 // n_heads, n_kv_heads, head_dim, rope_dim, device index) and a cache as
 // (descriptor's address, n_kv_heads, head_dim, device index), tuples that
-// attention.py makes once.  They raise ValueError for a tensor that does not
+// attention.py makes once; the projections take (handle, device index).  They raise ValueError for a tensor that does not
 // fit, and return the C ABI's code.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -232,9 +233,114 @@ PyObject *decode(PyObject *, PyObject *const *args, Py_ssize_t n) {
   });
 }
 
+// (context, q, k, v, q_starts, k_starts, causal, scale, softcap, slopes, window, out, lse, stream)
+PyObject *prefill(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  return call<14>(args, n, [](PyObject *const *p) {
+    const Context c = context_of(p[0]);
+    const int64_t Tq = tokens_of(p[1], "q"), Tk = tokens_of(p[2], "k"), starts = tokens_of(p[4], "q_starts");
+    if (starts < 1) raise("q_starts must hold one more start than there are sequences");
+    const Rows q = rows_of(c, p[1], Tq, c.n_heads, "q"), k = rows_of(c, p[2], Tk, c.n_kv, "k"),
+               v = rows_of(c, p[3], Tk, c.n_kv, "v"), out = rows_of(c, p[11], Tq, c.n_heads, "out");
+    const int32_t *qs = ints(c, p[4], starts, "q_starts");
+    const int32_t *ks = p[5] == Py_None ? nullptr : ints(c, p[5], starts, "k_starts");
+    if (ks == nullptr) raise("k_starts are needed");
+    float *lse = nullptr;
+    if (p[12] != Py_None) {
+      const at::Tensor &t = tensor_of(p[12], "lse");
+      if (t.scalar_type() != at::kFloat || t.dim() != 2 || t.size(0) != Tq || t.size(1) != c.n_heads || !on(t, c) ||
+          !t.is_contiguous())
+        misfit(c, p[12], "lse", "contiguous f32 " + dims({Tq, c.n_heads}));
+      lse = static_cast<float *>(t.data_ptr());
+    }
+    const int64_t window = to_int(p[10]);
+    if (window < 0 || window > INT32_MAX) raise("window must be 0 or a positive int32");
+    const int causal = PyObject_IsTrue(p[6]);
+    if (causal < 0) throw Raised();
+    return moe_attn_prefill(c.handle, q.p, q.stride, Tq, k.p, k.stride, v.p, v.stride, Tk, qs, ks, starts - 1, causal,
+                            to_float(p[7]), to_float(p[8]), floats(c, p[9], c.n_heads, "slopes"), (int32_t)window, out.p,
+                            out.stride, lse, to_ptr(p[13]));
+  });
+}
+
+struct Proj {
+  moe_proj *handle;
+  Context on;  // for the checks of tensors
+};
+Proj proj_of(PyObject *t) {
+  if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 2) raise("the context is closed");
+  return Proj{static_cast<moe_proj *>(to_ptr(PyTuple_GET_ITEM(t, 0))), Context{nullptr, 0, 0, 0, 0, to_int(PyTuple_GET_ITEM(t, 1))}};
+}
+
+// A matrix [rows, columns] whose rows are contiguous, or a null pointer for None.
+Rows matrix_of(const Context &c, PyObject *o, at::ScalarType type, const char *what, int64_t rows, int64_t columns, const char *name) {
+  if (o == Py_None) return Rows{nullptr, 0};
+  const at::Tensor &t = tensor_of(o, name);
+  if (t.scalar_type() != type || t.dim() != 2 || t.size(0) != rows || t.size(1) != columns || !on(t, c) ||
+      (t.stride(1) != 1 && columns > 1))
+    misfit(c, o, name, what + (" " + dims({rows, columns})) + " with contiguous rows");
+  // a single row has no stride of its own: any one that fits the alignment
+  return Rows{t.data_ptr(), rows > 1 ? t.stride(0) : (columns + 15) / 16 * 16};
+}
+struct Scales {
+  float *p;
+  int64_t row, block;
+};
+Scales scales_of(const Context &c, PyObject *o, int64_t rows, int64_t blocks, const char *name) {
+  if (o == Py_None) return Scales{nullptr, 0, 0};
+  const at::Tensor &t = tensor_of(o, name);
+  if (t.scalar_type() != at::kFloat || t.dim() != 2 || t.size(0) != rows || t.size(1) != blocks || !on(t, c))
+    misfit(c, o, name, "f32 " + dims({rows, blocks}));
+  return Scales{static_cast<float *>(t.data_ptr()), rows > 1 ? t.stride(0) : 1, blocks > 1 ? t.stride(1) : 1};
+}
+// [rows, columns] of a tensor.
+void sizes_of(PyObject *o, const char *name, int64_t *rows, int64_t *columns) {
+  const at::Tensor &t = tensor_of(o, name);
+  if (t.dim() != 2) raise("%s must have two dimensions", name);
+  *rows = t.size(0), *columns = t.size(1);
+}
+
+// (context, x, residual, weight, eps, residual_out, out, codes, scales, stream)
+PyObject *norm(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  return call<10>(args, n, [](PyObject *const *p) {
+    const Proj pr = proj_of(p[0]);
+    const Context &c = pr.on;
+    int64_t T, H;
+    sizes_of(p[1], "x", &T, &H);
+    const Rows x = matrix_of(c, p[1], at::kBFloat16, "bf16", T, H, "x"),
+               r = matrix_of(c, p[2], at::kBFloat16, "bf16", T, H, "residual"),
+               ro = matrix_of(c, p[5], at::kBFloat16, "bf16", T, H, "residual_out"),
+               o = matrix_of(c, p[6], at::kBFloat16, "bf16", T, H, "out"),
+               codes = matrix_of(c, p[7], at::kByte, "uint8", T, H, "codes");
+    const Scales sc = scales_of(c, p[8], T, (H + 127) / 128, "scales");
+    return moe_proj_norm(pr.handle, x.p, x.stride, r.p, r.stride, T, H, floats(c, p[3], H, "weight"), to_float(p[4]), ro.p,
+                         ro.stride, o.p, o.stride, static_cast<uint8_t *>(codes.p), codes.stride, sc.p, sc.row, sc.block,
+                         to_ptr(p[9]));
+  });
+}
+
+// (context, codes, scales, w, w_scale, out, stream)
+PyObject *matmul(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  return call<7>(args, n, [](PyObject *const *p) {
+    const Proj pr = proj_of(p[0]);
+    const Context &c = pr.on;
+    int64_t M, N, K, k;
+    sizes_of(p[1], "codes", &M, &K);
+    sizes_of(p[3], "w", &N, &k);
+    const Rows a = matrix_of(c, p[1], at::kByte, "uint8", M, K, "codes"), w = matrix_of(c, p[3], at::kByte, "uint8", N, K, "w"),
+               o = matrix_of(c, p[5], at::kBFloat16, "bf16", M, N, "out");
+    const int64_t blocks = (K + 127) / 128;
+    if (p[2] == Py_None || p[4] == Py_None || p[5] == Py_None) raise("scales, w_scale and out are needed");
+    const Scales sa = scales_of(c, p[2], M, blocks, "scales"), sw = scales_of(c, p[4], (N + 127) / 128, blocks, "w_scale");
+    if (!tensor_of(p[4], "w_scale").is_contiguous()) raise("w_scale must be contiguous");
+    return moe_proj_matmul(pr.handle, static_cast<const uint8_t *>(a.p), a.stride, sa.p, sa.row, sa.block, M,
+                           static_cast<const uint8_t *>(w.p), w.stride, sw.p, N, K, o.p, o.stride, to_ptr(p[6]));
+  });
+}
+
 #define FASTCALL(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FASTCALL(norm_rope), FASTCALL(append), FASTCALL(write),
-                         FASTCALL(read),      FASTCALL(decode), {nullptr, nullptr, 0, nullptr}};
+                         FASTCALL(read),      FASTCALL(decode), FASTCALL(prefill),
+                         FASTCALL(norm),      FASTCALL(matmul), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -376,7 +376,7 @@ typedef struct moe_attn_config {
   int32_t rope_dim;    /* R: leading elements of a head that are rotated;    */
                        /* 0 for none, else a multiple of 16, <= head_dim     */
   int32_t interleaved; /* rotated pairs: 0 (i, i + R/2), 1 (2i, 2i + 1)      */
-  int32_t max_sms;     /* SMs moe_attn_decode may fill; 0 for all            */
+  int32_t max_sms;     /* SMs moe_attn_decode and _prefill may fill; 0: all  */
   int32_t device;      /* CUDA device ordinal the context lives on           */
   const double *rope_freqs; /* host, f64 [R/2]: radians per position, finite; */
                             /* read during moe_attn_init only; NULL if R = 0  */
@@ -398,7 +398,8 @@ void moe_attn_free(moe_attn *a);
 /*
  * moe_attn_status - synchronise the context's last stream and return MOE_OK,
  * or MOE_ERR_DEVICE if a call since the previous moe_attn_status met a slot,
- * page or length outside the cache or the page table (the flag is cleared).
+ * page or length outside the cache or the page table (the flag is cleared), or
+ * MOE_ERR_DEVICE_TIMEOUT if a wait of moe_attn_prefill gave up.
  * Such a slot is neither written nor read, rows of such a page count as
  * zeros, and such a length is cut to the page table.
  */
@@ -507,6 +508,125 @@ int moe_attn_decode(moe_attn *a, const moe_paged_kv *kv, const void *q, int64_t 
  * for the call.
  */
 int moe_attn_decode_clusters(const moe_attn *a, const moe_paged_kv *kv, int64_t B, int64_t max_pages);
+
+/*
+ * moe_attn_prefill - attention of whole prompts, or of chunks of them whose
+ * earlier keys are given too, packed one after another.  Sequence b has the query
+ * rows [q_starts[b], q_starts[b + 1]) and the key and value rows [k_starts[b],
+ * k_starts[b + 1]); its last query is its last key's token.  With Lq and Lk rows,
+ * query i of the sequence at position p = i + Lk - Lq, and c = h / (n_heads /
+ * n_kv_heads):
+ *   s_j = scale * q[i, h] . K[j, c]
+ *   s_j = softcap * tanh(s_j / softcap)              if softcap > 0
+ *   s_j = s_j + slopes[h] * (j - p)                  if slopes is given
+ * for the visible keys j of the sequence: j <= p if causal, and j > p - window if
+ * window > 0;
+ *   out[i, h] = softmax(s) V,  lse[i, h] = log(sum_j exp(s_j)).
+ * A query with no visible key gives out = 0 and lse = -infinity.  Rows outside the
+ * sequences are not read as keys or values of any, and out and lse are left as they
+ * are there.  What hidden keys and values hold does not matter, NaN included.
+ * Sums and softmax statistics are f32; for their product with the values, weights
+ * are rounded to bf16 (2^-8 of each at most, as the output is); out is rounded to bf16.
+ *   q       : device bf16 [Tq, n_heads, d] rows as for moe_attn_norm_rope (a slice of
+ *             a fused projection's rows is fine), Tq <= 2^31 - 1.
+ *   k, v    : device bf16 [Tk, n_kv_heads, d] rows like q, Tk <= 2^31 - 1.
+ *   q_starts, k_starts : device int32 [B + 1], non-decreasing, within [0, Tq] and
+ *             [0, Tk].  Others are cut to these ranges, never followed, and
+ *             moe_attn_status reports them (the outputs mean nothing then).
+ *   causal  : 0 or 1.
+ *   slopes  : device f32 [n_heads] or NULL.
+ *   out     : device bf16 rows like q; must not overlap q, k or v.
+ *   lse     : device f32 [Tq, n_heads] contiguous, or NULL.
+ * B <= 2^20.  The order of the sums follows from the sizes, the lengths and the
+ * options alone: the same call gives the same bits.  No workspace is used but the
+ * context's error flag.
+ */
+int moe_attn_prefill(moe_attn *a, const void *q, int64_t q_stride, int64_t Tq, const void *k, int64_t k_stride,
+                     const void *v, int64_t v_stride, int64_t Tk, const int32_t *q_starts,
+                     const int32_t *k_starts, int64_t B, int32_t causal, float scale, float softcap,
+                     const float *slopes, int32_t window, void *out, int64_t out_stride, float *lse,
+                     void *stream);
+
+/*
+ * Projections around the attention and the MoE, in the experts' weight format
+ * (dragon.c, "Precision": e4m3 codes with one f32 scale per 128x128 block, the
+ * dense branches too): the hidden states' norm with the residual's addition and an
+ * e4m3 output, and the product of such rows with such weights.  Unlike the routed
+ * experts, whose activations are exact, a projection's activations are one e4m3
+ * term with a f32 scale per row and 128 columns.
+ */
+typedef struct moe_proj moe_proj; /* opaque; owned by the library */
+
+/*
+ * moe_proj_init - a context of `device` (its error flag is all it owns); max_sms:
+ * the SMs a call may fill, 0 for all.  Errors: MOE_ERR_ARG (out NULL),
+ * MOE_ERR_SHAPE (negative; both before any CUDA call), MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_CUDA, MOE_ERR_NOMEM.  On error *out is set to NULL and nothing is leaked.
+ * Calls on one context may overlap on the GPU.
+ */
+int moe_proj_init(moe_proj **out, int32_t device, int32_t max_sms);
+
+/* moe_proj_free - release the context; NULL is a no-op. */
+void moe_proj_free(moe_proj *p);
+
+/*
+ * moe_proj_status - synchronise the context's last stream and return MOE_OK, or
+ * MOE_ERR_DEVICE_TIMEOUT if a wait of a call since the previous moe_proj_status
+ * gave up (the flag is cleared).
+ */
+int moe_proj_status(moe_proj *p);
+
+/*
+ * moe_proj_norm - residual addition, RMS norm and quantisation of T rows of H
+ * columns.  Per row, in f32:
+ *   r' = bf16(x + residual)                     (x itself if residual is NULL)
+ *   y  = r' / sqrt(mean(r'^2) + eps) * weight   (r' itself if weight is NULL; right
+ *        where r'^2 is beyond f32 too)
+ *   residual_out = r'; out = bf16(y); and per block of 128 columns (the last one may
+ *   be shorter) scale = max(max|y| / 448, 2^-126) over its finite values (1 if they
+ *   are all zero), code = e4m3(y / scale) rounded to nearest even (the quotient to
+ *   f32); a NaN or an infinity becomes the NaN code.
+ *   x, residual   : device bf16; row t at t * stride (elements, a multiple of 8, at
+ *                   least H), 16-byte aligned.  residual may be NULL.
+ *   T, H          : T >= 0; H a multiple of 8, 8..16384.
+ *   weight        : device f32 [H], 16-byte aligned, or NULL.
+ *   eps           : >= 0 and finite.
+ *   residual_out  : like x; NULL if and only if residual is.  May be residual or x
+ *                   (same stride).
+ *   out           : like x, or NULL.  May be x (same stride).
+ *   codes         : device u8, row t at t * codes_stride (a multiple of 8, at least
+ *                   H), 8-byte aligned, or NULL.
+ *   scales        : device f32; that of row t and block b at t * scale_row_stride +
+ *                   b * scale_block_stride (elements, positive).  NULL if and only
+ *                   if codes is.
+ * One of out, codes and residual_out at least is given; outputs must not overlap
+ * each other or the inputs otherwise.
+ */
+int moe_proj_norm(moe_proj *p, const void *x, int64_t x_stride, const void *residual,
+                  int64_t residual_stride, int64_t T, int64_t H, const float *weight, float eps,
+                  void *residual_out, int64_t residual_out_stride, void *out, int64_t out_stride,
+                  uint8_t *codes, int64_t codes_stride, float *scales, int64_t scale_row_stride,
+                  int64_t scale_block_stride, void *stream);
+
+/*
+ * moe_proj_matmul - product of e4m3 rows with e4m3 weights:
+ *   out[m, n] = bf16( sum over blocks b of 128 of K of
+ *       a_scale[m, b] * w_scale[n / 128, b] * sum over k in b of a[m, k] * w[n, k] )
+ * Sums are f32, rounded once at the end.
+ *   a       : device u8 e4m3 codes, row m at m * a_stride, 16-byte aligned, a_stride
+ *             a multiple of 16 and at least K.
+ *   a_scale : device f32, as moe_proj_norm writes them.
+ *   w       : device u8 e4m3 codes, row n at n * w_stride; alignment as for a.
+ *   w_scale : device f32 [ceil(N / 128), ceil(K / 128)] contiguous, 4-byte aligned.
+ *   out     : device bf16, row m at m * out_stride (a multiple of 8, at least N),
+ *             16-byte aligned; must not overlap the inputs.
+ * M, N, K: any from 0 up to 2^31 - 256 (K = 0 gives zeros); M or N = 0 is a no-op.
+ * The order of the sums follows from the sizes and max_sms alone.
+ */
+int moe_proj_matmul(moe_proj *p, const uint8_t *a, int64_t a_stride, const float *a_scale,
+                    int64_t scale_row_stride, int64_t scale_block_stride, int64_t M, const uint8_t *w,
+                    int64_t w_stride, const float *w_scale, int64_t N, int64_t K, void *out,
+                    int64_t out_stride, void *stream);
 
 /*
  * moe_selftest_wait_timeout - exercise the bounded device-side waits.  Every

@@ -1,0 +1,291 @@
+"""Attention of packed prompts on the GPU against the f64 oracle.
+
+Tolerances, from the arithmetic (u = 2^-24, half a step of f32):
+  * scores: a d-term f32 sum through 16-wide matrix steps, each charged 8 units u
+    of the running sum of magnitudes, and the products with the scale: eps_s =
+    (d / 2 + 16) u reach, plus 16 u cap for the tanh, 4 u per unit of distance bias;
+  * out: a weight is off by eps_s, 2^-20 for exp and half a step of bf16, 2^-8, and
+    the sum over n keys by (n / 2 + 64) u: all times sum_j p_j |v_j|, and half a step
+    of the output, 2^-8 |exact|;
+  * lse: eps_s + 2^-20 + (n / 2 + 64) u + 2 u |lse|.
+"""
+import numpy as np
+import pytest
+import torch
+
+from fp8_routed_expert_gb300 import C, DecodeAttention, PagedKVCache
+from oracle import prefill_attention as A
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DEV = torch.device("cuda", 0)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def starts_of(lens, first=0):
+    return np.concatenate([[first], first + np.cumsum(lens)]).astype(np.int32)
+
+
+def inputs(nq, nk, nh, nkv, d, seed, before=0, behind=0, size=1.0):
+    """Packed rows with `before` and `behind` rows of NaN that no sequence has."""
+    g = gen(seed)
+    q0, k0 = starts_of(nq, before), starts_of(nk, before)
+    q = torch.randn(q0[-1] + behind, nh, d, generator=g, device=DEV) * size
+    kv = torch.randn(k0[-1] + behind, 2 * nkv, d, generator=g, device=DEV)
+    for t, end in ((q, q0[-1]), (kv, k0[-1])):
+        t[:before], t[end:] = float("nan"), float("nan")
+    kv = kv.to(torch.bfloat16)
+    return q.to(torch.bfloat16), kv[:, :nkv], kv[:, nkv:], q0, k0
+
+
+def dev(a):
+    return torch.from_numpy(np.asarray(a, np.int32)).to(DEV)
+
+
+def check(q, k, v, q0, k0, causal=True, softcap=0.0, slopes=None, window=0, scale=None, attn=None):
+    Tq, nh, d = q.shape
+    attn = attn or DecodeAttention(nh, k.shape[1], d)
+    out = torch.full((Tq, nh, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((Tq, nh), 7.0, device=DEV)
+    attn.prefill(q, k, v, dev(q0), dev(k0), causal=causal, softcap=softcap, slopes=slopes, window=window, scale=scale, out=out, lse=lse)
+    assert attn.status() == 0
+    real = d ** -0.5 if scale is None else scale
+    sl = None if slopes is None else f64(slopes)
+    Q, K, V = f64(q), f64(k), f64(v)
+    want, wlse, size = A.prefill(Q, K, V, q0, k0, real, causal, softcap, sl, window)
+    rows = ~np.isnan(wlse[:, 0])
+    o, z = f64(out), f64(lse)
+    assert (o[~rows] == 7).all() and (z[~rows] == 7).all()  # rows of no sequence
+    # reach: the largest sum of magnitudes of a product, over a sequence's heads
+    tol_s = np.zeros(wlse.shape)
+    n_keys = np.zeros(Tq)
+    g = nh // k.shape[1]
+    for b in range(len(q0) - 1):
+        a, e, c, f = q0[b], q0[b + 1], k0[b], k0[b + 1]
+        if e == a or f == c:
+            continue
+        n_keys[a:e] = f - c
+        for h in range(nh):
+            reach = (np.abs(Q[a:e, h]) @ np.abs(K[c:f, h // g]).T).max() * abs(real)
+            far = 0.0 if sl is None else abs(sl[h]) * max(f - c, e - a)
+            tol_s[a:e, h] = (d / 2 + 16) * U * reach + 16 * U * softcap + 4 * U * far
+    tol_w = tol_s + 2.0 ** -20 + ((n_keys / 2 + 64) * U)[:, None]
+    empty = rows[:, None] & np.isneginf(wlse)
+    assert (np.isneginf(z) == empty).all() and (o[empty] == 0).all()
+    ok = rows[:, None] & ~empty
+    tol_l = tol_w + 2 * U * np.abs(np.where(ok, wlse, 0))
+    bad = ok & ~(np.abs(z - np.where(ok, wlse, 0)) <= tol_l)
+    assert not bad.any(), (np.argwhere(bad)[:4], z[bad][:4], wlse[bad][:4])
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + tol_w)[:, :, None] * size
+    bad = ok[:, :, None] & ~(np.abs(o - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), o[bad][:4], want[bad][:4], tol[bad][:4])
+    return out, lse
+
+
+@pytest.mark.parametrize("d", [128, 64, 256])
+@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257, 700])
+def test_one_prompt(d, n):
+    check(*inputs([n], [n], 2, 2, d, n + d))
+
+
+@pytest.mark.parametrize("nq,nk,nh,nkv,d", [
+    ([5, 0, 300, 1, 64], [5, 0, 300, 1, 64], 4, 2, 128), ([3, 130, 17], [40, 130, 500], 8, 1, 128),
+    ([70, 9, 200], [0, 5, 100], 6, 2, 64), ([1] * 20, list(range(1, 21)), 16, 2, 128), ([33, 500], [600, 513], 5, 5, 256),
+    ([128, 128, 128], [128, 256, 64], 21, 7, 64), ([40, 41], [90, 41], 17, 1, 128), ([19, 200], [19, 333], 33, 1, 64),
+    ([77], [200], 128, 2, 64), ([300, 2], [300, 900], 24, 2, 256), ([2000, 1, 0, 555], [2000, 1000, 3, 555], 12, 1, 128)])
+def test_packed(nq, nk, nh, nkv, d):
+    """Groups that do and do not divide a tile, chunks of prompts, empty sequences,
+    fewer keys than queries (rows without a visible key), rows around the sequences."""
+    q, k, v, q0, k0 = inputs(nq, nk, nh, nkv, d, sum(nk) + nh, before=3, behind=5)
+    check(q, k, v, q0, k0)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal,window,softcap,slopes,scale", [
+    (False, 0, 0.0, False, None), (True, 1, 0.0, False, None), (True, 100, 0.0, False, None), (False, 37, 0.0, False, None),
+    (True, 0, 20.0, False, None), (True, 0, 0.0, True, None), (True, 300, 5.0, True, 0.3), (False, 0, 0.0, True, None),
+    (True, 0, 0.0, False, -0.1), (True, 0, 0.0, False, 0.0), (True, 2 ** 31 - 1, 0.0, False, None)])
+def test_options(d, causal, window, softcap, slopes, scale):
+    q, k, v, q0, k0 = inputs([150, 1, 0, 260, 40], [420, 1, 9, 260, 10], 6, 2, d, window % 1000 + d, behind=2, size=2.0)
+    sl = torch.tensor([0.5, 0.25, 0.125, -0.3, 0.0, 2.0], device=DEV) if slopes else None
+    check(q, k, v, q0, k0, causal, softcap, sl, window, scale)
+
+
+def test_strided_rows_and_heads():
+    """Slices of a fused projection's rows, and outputs within wider rows."""
+    g = gen(11)
+    T, nh, nkv, d = 333, 8, 2, 128
+    fused = torch.randn(T, nh + 2 * nkv + 1, d, generator=g, device=DEV).to(torch.bfloat16)
+    q, k, v = fused[:, 1:nh + 1], fused[:, nh + 1:nh + nkv + 1], fused[:, nh + nkv + 1:]
+    s = dev([0, 100, 333])
+    attn = DecodeAttention(nh, nkv, d)
+    want = attn.prefill(q.contiguous(), k.contiguous(), v.contiguous(), s)
+    wide = torch.zeros(T, nh + 2, d, dtype=torch.bfloat16, device=DEV)
+    out = attn.prefill(q, k, v, s, out=wide[:, 1:-1])
+    assert torch.equal(out, want) and (wide[:, 0] == 0).all() and (wide[:, -1] == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_sharp_and_shifting_scores(d):
+    """Scores that rise by hundreds along the keys (the reference moves in every
+    block), and one key that has nearly all of the weight."""
+    q, k, v, q0, k0 = inputs([400], [400], 2, 1, d, 5)
+    k = k.clone()
+    k[..., 0] = torch.arange(400, device=DEV).view(-1, 1) * 0.5
+    q[:, 0, 0], q[:, 1, 0] = 8.0, -8.0
+    check(q, k, v, q0, k0, scale=0.5)
+    k[..., 0] = 0
+    k[200] = q[300, 0].float().mul(3).to(torch.bfloat16)
+    check(q, k, v, q0, k0)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("what", ["value", "key", "inf", "query"])
+def test_nan_and_infinity(d, what):
+    """A NaN or an infinity reaches the rows that see it and no other: earlier rows of
+    the same tile, later rows beyond the window, other heads, other sequences."""
+    q, k, v, q0, k0 = inputs([300, 50], [300, 50], 4, 2, d, 3)
+    attn = DecodeAttention(4, 2, d)
+    clean = attn.prefill(q, k, v, dev(q0), dev(k0), window=150).clone()
+    q, k, v = q.clone(), k.clone(), v.clone()
+    if what == "query":
+        q[100, 1, 3] = float("nan")
+        hit = np.zeros((350, 4), bool)
+        hit[100, 1] = True
+    else:
+        t = k if what == "key" else v
+        t[100, 0, 3] = float("inf") if what == "inf" else float("nan")
+        hit = np.zeros((350, 4), bool)
+        hit[100:250, :2] = True
+    lse = torch.empty(350, 4, device=DEV)
+    out = attn.prefill(q, k, v, dev(q0), dev(k0), window=150, lse=lse)[0]
+    assert attn.status() == 0
+    o, c = f64(out), f64(clean)
+    assert (np.abs(o[~hit] - c[~hit]) <= 2.0 ** -6 * np.abs(c).max()).all()  # same rows, at most summed in another order
+    if what in ("value", "inf"):
+        lane = o[hit][:, 3]
+        assert np.isnan(lane).all() if what == "value" else (lane == np.inf).all()
+        rest = np.delete(o[hit], 3, 1)
+        assert (np.abs(rest - np.delete(c[hit], 3, 1)) <= 2.0 ** -6 * np.abs(c).max()).all()
+        assert torch.isfinite(lse).all()
+    else:
+        assert np.isnan(o[hit]).all() and np.isnan(f64(lse)[hit]).all() and np.isfinite(f64(lse)[~hit]).all()
+
+
+def test_masked_values_of_the_lowest_and_highest():
+    """Hidden keys that would win by far, hidden values at the end of bf16's range."""
+    q, k, v, q0, k0 = inputs([200], [200], 2, 2, 128, 9)
+    k, v = k.clone(), v.clone()
+    k[150:] = 3e38
+    v[150:] = -3.38e38
+    out = DecodeAttention(2, 2, 128).prefill(q, k, v, dev(q0), dev(k0))
+    want, _, _ = A.prefill(f64(q)[:150], f64(k)[:150], f64(v)[:150], [0, 150], [0, 150], 128 ** -0.5)
+    assert np.abs(f64(out)[:150] - want).max() < 2.0 ** -6
+
+
+def test_bad_starts_are_reported_and_never_followed():
+    attn = DecodeAttention(2, 2, 64)
+    q, k, v, q0, k0 = inputs([30, 30], [30, 30], 2, 2, 64, 1)
+    good = attn.prefill(q, k, v, dev([0, 30, 60]), dev([0, 30, 60]))
+    assert attn.status() == 0
+    for qs, ks in (([0, 30, 61], [0, 30, 60]), ([-5, 30, 60], [0, 30, 60]), ([0, 40, 30], [0, 30, 60]),
+                   ([0, 30, 60], [0, 2 ** 31 - 1, 60]), ([0, 30, 60], [0, 30, -2 ** 31]), ([2 ** 31 - 1, 0, 1], [0, 0, 0])):
+        attn.prefill(q, k, v, dev(qs), dev(ks))
+        assert attn.status() == C["MOE_ERR_DEVICE"]
+    assert torch.equal(attn.prefill(q, k, v, dev([0, 30, 60])), good) and attn.status() == 0
+
+
+def test_no_keys_no_queries_no_sequences():
+    attn = DecodeAttention(4, 2, 128)
+    e = lambda t, h: torch.empty(t, h, 128, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    out, lse = attn.prefill(e(5, 4), e(0, 2), e(0, 2), dev([0, 2, 5]), dev([0, 0, 0]), lse=torch.empty(5, 4, device=DEV))
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    assert attn.prefill(e(0, 4), e(3, 2), e(3, 2), dev([0, 0]), dev([0, 3])).shape == (0, 4, 128)
+    o = torch.full((5, 4, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+    attn.prefill(e(5, 4), e(3, 2), e(3, 2), dev([0]), dev([0]), out=o)
+    assert (o == 3).all() and attn.status() == 0
+
+
+def test_same_bits_twice_in_a_graph_and_on_streams():
+    q, k, v, q0, k0 = inputs([900, 77, 300], [1200, 77, 300], 8, 2, 128, 21)
+    qs, ks = dev(q0), dev(k0)
+    attn = DecodeAttention(8, 2, 128)
+    want = attn.prefill(q, k, v, qs, ks).clone()
+    assert torch.equal(attn.prefill(q, k, v, qs, ks), want)
+    out = torch.empty_like(want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    attn.prefill(q, k, v, qs, ks, out=out, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        attn.prefill(q, k, v, qs, ks, out=out)
+    out.zero_()
+    g.replay()
+    assert torch.equal(out, want)
+    # other lengths in the same graph: they are read on the device
+    qs.copy_(dev([0, 10, 500, 1277]))
+    ks.copy_(dev([0, 10, 600, 1577]))
+    g.replay()
+    assert torch.equal(out, attn.prefill(q, k, v, qs, ks)) and attn.status() == 0
+
+
+def test_few_sms_give_the_same_bits():
+    q, k, v, q0, k0 = inputs([500, 300], [500, 800], 4, 4, 128, 22)
+    want = DecodeAttention(4, 4, 128).prefill(q, k, v, dev(q0), dev(k0))
+    assert torch.equal(DecodeAttention(4, 4, 128, max_sms=3).prefill(q, k, v, dev(q0), dev(k0)), want)
+
+
+def test_chunks_of_a_prompt_through_the_cache():
+    """A prompt in chunks, each with the keys and values read back from the pages, is
+    the prompt at once; its last token is the decode step's."""
+    nh, nkv, d, n = 8, 2, 128, 333
+    q, k, v, _, _ = inputs([n], [n], nh, nkv, d, 31)
+    attn = DecodeAttention(nh, nkv, d)
+    cache = PagedKVCache.empty(16, 32, nkv, d)
+    order = torch.randperm(16, generator=gen(1), device=DEV)
+    j = torch.arange(n, device=DEV)
+    slots = order[j // 32] * 32 + j % 32
+    attn.write(cache, k, v, slots)
+    whole = attn.prefill(q, k, v, dev([0, n]))
+    for a, e in ((0, 100), (100, 101), (101, 333)):
+        kc, vc = attn.read(cache, slots[:e].contiguous())
+        part = attn.prefill(q[a:e], kc, vc, dev([0, e - a]), dev([0, e]))
+        assert (part.float() - whole[a:e].float()).abs().max() <= 2.0 ** -6 * whole.float().abs().max()
+    one = attn.decode(q[n - 1:], cache, order.to(torch.int32).view(1, -1), dev([n]))
+    assert (one.float() - whole[n - 1:].float()).abs().max() <= 2.0 ** -6 * whole.float().abs().max()
+    assert attn.status() == 0
+
+
+def test_refusals():
+    attn = DecodeAttention(4, 2, 128)
+    q, k, v, q0, k0 = inputs([9], [9], 4, 2, 128, 1)
+    qs, ks = dev(q0), dev(k0)
+    for bad in (dict(q=q[:, :3]), dict(k=q), dict(v=v[:5]), dict(q=q.float()), dict(q=q.cpu()), dict(q_starts=qs.long()),
+                dict(k_starts=ks[:1]), dict(q_starts=qs[:0]), dict(window=-1), dict(window=2 ** 31), dict(out=q[:4]),
+                dict(lse=torch.empty(9, 3, device=DEV)), dict(slopes=torch.zeros(3, device=DEV)), dict(q=q.transpose(0, 1))):
+        with pytest.raises(ValueError):
+            attn.prefill(**{**dict(q=q, k=k, v=v, q_starts=qs, k_starts=ks), **bad})
+    for bad in (dict(softcap=-1.0), dict(scale=float("nan"))):
+        with pytest.raises(RuntimeError):
+            attn.prefill(q, k, v, qs, ks, **bad)
+    attn.close()
+    with pytest.raises(ValueError):
+        attn.prefill(q, k, v, qs, ks)
