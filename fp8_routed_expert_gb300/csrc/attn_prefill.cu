@@ -42,6 +42,7 @@ using namespace sm100;
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kFew = 88, kMany = 208;
 constexpr float kMove = 8.f;  // log2 of how far a score may exceed the reference
 
 template <int D>
@@ -56,9 +57,10 @@ struct Shape {
   static constexpr uint32_t kS = 0, kO = 2 * kKeys;  // TMEM columns: two S, then O of each tile
 };
 
+// Positions and rows fit 32 bits (Tq and Tk do); sums that may not are 64-bit.
 template <int D>
 struct Item {
-  int64_t q0, k0;    // first rows of the sequence
+  int q0, k0;        // first rows of the sequence
   int n, m;          // its queries and keys
   int tok0;          // the item's first token
   int kv, head0;     // key/value head, first query head
@@ -135,7 +137,7 @@ __device__ __forceinline__ float option_score(float s, float scale, float cap, f
 // elements l * D / 32 ... of their values.
 template <int D>
 __device__ __noinline__ void row_again(const PrefillArgs &p, const __nv_bfloat16 *q, const __nv_bfloat16 *k, const __nv_bfloat16 *v,
-                                       int lo, int hi, int64_t pos, float slope, __nv_bfloat16 *out, float *lse) {
+                                       int lo, int hi, int pos, float slope, __nv_bfloat16 *out, float *lse) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   float acc[E], m = -INFINITY, l = 0.f;
@@ -156,7 +158,7 @@ __device__ __noinline__ void row_again(const PrefillArgs &p, const __nv_bfloat16
           s = fmaf(__uint_as_float(u4_word(a, x) & 0xffff0000u), __uint_as_float(u4_word(b, x) & 0xffff0000u), s);
         }
       }
-      s = option_score(s, p.scale, p.softcap, slope, (int)(j0 + lane - pos));
+      s = option_score(s, p.scale, p.softcap, slope, j0 + lane - pos);
     }
     const float ref = fmaxf(m, warp_max(s));
     const float keep = m == ref ? 1.f : exp2_fast(m - ref), w = s == -INFINITY ? 0.f : exp2_fast(s - ref);
@@ -217,6 +219,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
   pdl_wait();
   pdl_trigger();
 
+  // 384 threads start with 168 registers each; the eight softmax warps hold a row of
+  // scores: 128 * 88 + 256 * 208 = 384 * 168 (checked against the build in ready_d).
+  // (Each role's branch says so itself, which is where the compiler looks.)
+  if (warp < 4) {
+  if constexpr (kTiles == 2) fewer_registers<kFew>();
   if (warp == 0) {
     if (lane == 0) {
       int slot = 0;
@@ -229,7 +236,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         mbar_arrive_expect_tx(&kv_full[slot], Z::kSlot);
 #pragma unroll
         for (int c = 0; c < Z::kChunks; ++c)
-          tma_load_3d(ring + (size_t)slot * Z::kSlot + c * (kKeys * 128), map, 64 * c, it.kv, (int32_t)(it.k0 + (int64_t)block * kKeys),
+          tma_load_3d(ring + (size_t)slot * Z::kSlot + c * (kKeys * 128), map, 64 * c, it.kv, it.k0 + block * kKeys,
                       &kv_full[slot]);
         if (++slot == kSlots) slot = 0, phase ^= 1u;
         return true;
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
           mbar_arrive_expect_tx(&q_full[t], (uint32_t)(p.tokens * p.heads * 128 * Z::kChunks));
 #pragma unroll
           for (int c = 0; c < Z::kChunks; ++c)
-            tma_load_3d(smem + t * Z::kQTile + c * (128 * 128), &tq, 64 * c, it.head0, (int32_t)(it.q0 + it.tok0 + t * p.tokens),
+            tma_load_3d(smem + t * Z::kQTile + c * (128 * 128), &tq, 64 * c, it.head0, it.q0 + it.tok0 + t * p.tokens,
                         &q_full[t]);
         }
         // in the order of their first use: keys one block ahead (with one tile, two)
@@ -276,20 +283,26 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         }
         return ok;
       };
+      // Descriptors differ from the first tile's and slot's in their start address
+      // (16-byte units) alone; the asm keeps the compiler from holding all of them in
+      // registers.
+      const uint64_t q_desc = sw128_kmajor_desc(smem_u32(smem)), k_desc = sw128_kmajor_desc(smem_u32(ring)),
+                     v_desc = sw128_rows_k_desc(smem_u32(ring), kKeys * 128);
       const auto scores = [&](int t, int buf, int s) {  // S[buf] = Q[t] K[slot s]^T
-        const uint32_t a = smem_u32(smem + t * Z::kQTile), b = smem_u32(ring + (size_t)s * Z::kSlot);
+        uint64_t a = q_desc + (uint64_t)(t * (Z::kQTile / 16)), b = k_desc + (uint64_t)(s * (Z::kSlot / 16));
+        asm volatile("" : "+l"(a), "+l"(b));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_bf16_ss(tmem + Z::kS + buf * kKeys, sw128_kmajor_desc(a + (k >> 2) * (128 * 128) + (k & 3) * 32),
-                      sw128_kmajor_desc(b + (k >> 2) * (kKeys * 128) + (k & 3) * 32), i_s, k > 0 ? 1u : 0u);
+          mma_bf16_ss(tmem + Z::kS + buf * kKeys, a + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16,
+                      b + ((k >> 2) * (kKeys * 128) + (k & 3) * 32) / 16, i_s, k > 0 ? 1u : 0u);
         mma_commit(&s_full[buf]);
       };
       const auto values = [&](int t, int buf, int s, bool more) {  // O[t] (+)= P[buf] V[slot s]
-        const uint32_t b = smem_u32(ring + (size_t)s * Z::kSlot);
+        uint64_t b = v_desc + (uint64_t)(s * (Z::kSlot / 16));
+        asm volatile("" : "+l"(b));
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
-          mma_bf16_ts(tmem + Z::kO + t * D, tmem + Z::kS + buf * kKeys + k * 8, sw128_rows_k_desc(b + k * 2048, kKeys * 128), i_o,
-                      more || k > 0 ? 1u : 0u);
+          mma_bf16_ts(tmem + Z::kO + t * D, tmem + Z::kS + buf * kKeys + k * 8, b + k * (2048 / 16), i_o, more || k > 0 ? 1u : 0u);
         mma_commit(&o_full[t]);
       };
       const auto advance = [&] {
@@ -378,7 +391,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
       if (b < p.B) bad |= __ldg(p.q_starts + b + 1) < qs || __ldg(p.k_starts + b + 1) < ks;
     }
     if (bad) set_error(p.err, DEV_ERR_BOUNDS);
-  } else if (warp >= 4) {
+  }
+  } else {
+    if constexpr (kTiles == 2) more_registers<kMany>();
     const int t = (warp - 4) >> 2;  // tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int row = (warp & 3) * 32 + lane;  // of the tile
@@ -390,14 +405,23 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     bool ok = true;
     for (int64_t i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
       const Item<D> it = item_of<D>(p, i);
-      const int64_t tok = (int64_t)it.tok0 + t * p.tokens + r_tok;  // of the sequence
-      const bool mine = it.any && r_tok < p.tokens && r_head < it.heads && tok < it.n;
-      const int64_t pos = tok + it.m - it.n;
+      if (!it.any) continue;
+      // of the sequence (past its end: a row of no use); a row's position is below the
+      // last key's by the tokens that follow it
+      const uint32_t tok = (uint32_t)(it.tok0 + t * p.tokens) + (uint32_t)r_tok;
+      const bool mine = r_tok < p.tokens && r_head < it.heads && tok < (uint32_t)it.n;
+      const int pos = it.m - (int)((uint32_t)it.n - tok);
       // the keys that this row sees, and those that all of the tile's rows do
-      const int64_t a = (int64_t)it.tok0 + t * p.tokens, e = min(a + p.tokens, (int64_t)it.n) - 1, off = (int64_t)it.m - it.n;
       int see_lo = 0, see_hi = it.m, all_lo = 0, all_hi = it.m;
-      if (p.causal) see_hi = (int)max((int64_t)0, min((int64_t)it.m, pos + 1)), all_hi = (int)max((int64_t)0, min((int64_t)it.m, a + off + 1));
-      if (p.window > 0) see_lo = (int)max((int64_t)0, min((int64_t)it.m, pos - p.window + 1)), all_lo = (int)max((int64_t)0, min((int64_t)it.m, e + off - p.window + 1));
+      if (p.causal) {
+        see_hi = max(0, min(it.m, pos + 1));
+        all_hi = max(0, min(it.m, it.m - (it.n - (it.tok0 + t * p.tokens)) + 1));
+      }
+      if (p.window > 0) {
+        const int behind = it.n - it.tok0 - (t + 1) * p.tokens;  // tokens after the tile's
+        see_lo = (int)max(INT64_C(0), min((int64_t)it.m, (int64_t)pos - p.window + 1));
+        all_lo = (int)max(INT64_C(0), (int64_t)it.m - max(behind, 0) - p.window);
+      }
       const float slope = Option && p.slopes != nullptr && mine ? __ldg(p.slopes + it.head0 + r_head) : 0.f;
       float ref = -INFINITY;
       uint64_t sum2 = 0;
@@ -421,7 +445,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         if constexpr (Option) {
 #pragma unroll
           for (int c = 0; c < kKeys; ++c)
-            s[c] = __float_as_uint(option_score(__uint_as_float(s[c]), p.scale, p.softcap, slope, (int)(key0 + c - pos)));
+            s[c] = __float_as_uint(option_score(__uint_as_float(s[c]), p.scale, p.softcap, slope, key0 + c - pos));
         }
         if (key0 < all_lo || key0 + kKeys > all_hi) {
           const int from = see_lo - key0, to = see_hi - key0;
@@ -486,7 +510,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         ++o_count;
       }
       if (!ok) break;
-      if (!it.any) continue;
       const float2 sums = unpack_f32x2(sum2);
       const float sum = sums.x + sums.y;
       const float inv = sum > 0.f || !(sum == sum) ? 1.f / sum : 0.f;
@@ -497,8 +520,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         }
         tc_fence_after();
       }
-      __nv_bfloat16 *out = p.out + (it.q0 + tok) * p.out_stride + (int64_t)(it.head0 + r_head) * D;
-      float *lse = p.lse == nullptr ? nullptr : p.lse + (it.q0 + tok) * p.n_heads + it.head0 + r_head;
+      __nv_bfloat16 *out = p.out + (it.q0 + (int64_t)tok) * p.out_stride + (int64_t)(it.head0 + r_head) * D;
       bool odd = false;
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
@@ -518,15 +540,17 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
           for (int x = 0; x < 16; x += 4) *reinterpret_cast<uint4 *>(out + c + 2 * x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
         }
       }
-      if (mine && lse != nullptr) *lse = inv == 0.f ? -INFINITY : kLn2 * (ref + log2f(sum));
+      if (mine && p.lse != nullptr)
+        p.lse[(it.q0 + (int64_t)tok) * p.n_heads + it.head0 + r_head] = inv == 0.f ? -INFINITY : kLn2 * (ref + log2f(sum));
       __syncwarp();
       for (uint32_t left = __ballot_sync(0xffffffffu, odd && mine); left != 0; left &= left - 1) {
         const int from = __ffs(left) - 1;
-        const int64_t r = __shfl_sync(0xffffffffu, it.q0 + tok, from), at = __shfl_sync(0xffffffffu, pos, from);
+        const int64_t r = it.q0 + (int64_t)__shfl_sync(0xffffffffu, tok, from);
+        const int at = __shfl_sync(0xffffffffu, pos, from);
         const int head = it.head0 + __shfl_sync(0xffffffffu, r_head, from);
         const int l = __shfl_sync(0xffffffffu, see_lo, from), h = __shfl_sync(0xffffffffu, see_hi, from);
-        row_again<D>(p, p.q + r * p.q_stride + (int64_t)head * D, p.k + it.k0 * p.k_stride + (int64_t)it.kv * D,
-                     p.v + it.k0 * p.v_stride + (int64_t)it.kv * D, l, h, at, __shfl_sync(0xffffffffu, slope, from),
+        row_again<D>(p, p.q + r * p.q_stride + (int64_t)head * D, p.k + (int64_t)it.k0 * p.k_stride + (int64_t)it.kv * D,
+                     p.v + (int64_t)it.k0 * p.v_stride + (int64_t)it.kv * D, l, h, at, __shfl_sync(0xffffffffu, slope, from),
                      p.out + r * p.out_stride + (int64_t)head * D, p.lse == nullptr ? nullptr : p.lse + r * p.n_heads + head);
       }
     }
@@ -569,8 +593,13 @@ cudaError_t launch_d(const PrefillArgs &a, int sms, cudaStream_t s) {
 template <int D>
 cudaError_t ready_d() {
   for (auto k : {prefill_kernel<D, true>, prefill_kernel<D, false>}) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kSmem);
     if (e != cudaSuccess) return e;
+    // the softmax warps would wait forever for registers that the launch does not have
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, k);
+    if (e != cudaSuccess) return e;
+    if (Shape<D>::kTiles == 2 && at.numRegs * 3 < kFew + 2 * kMany) return cudaErrorInvalidKernelImage;
   }
   return cudaSuccess;
 }
