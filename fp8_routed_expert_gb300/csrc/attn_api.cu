@@ -552,10 +552,11 @@ int moe_attn_prefill(moe_attn *a, const void *q, int64_t q_stride, int64_t Tq, c
   r.lse = lse;
   r.err = a->err;
   plan_prefill(&r, c.head_dim);
+  if (r.items > INT64_C(0x7fffffff)) return MOE_ERR_SHAPE;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   ATTN_TRY(cudaSetDevice(c.device));
   a->last_stream = s;
-  ATTN_TRY(launch_prefill(r, c.head_dim, c.max_sms > 0 && c.max_sms < a->sms ? c.max_sms : a->sms, s));
+  ATTN_TRY(launch_prefill(r, c.head_dim, c.max_sms > 0 && c.max_sms < a->sms ? c.max_sms : 0, s));
   return MOE_OK;
 }
 

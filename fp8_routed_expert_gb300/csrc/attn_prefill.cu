@@ -11,11 +11,14 @@
 // whose output takes half of tensor memory).  Per block of 128 keys (64 with 256
 // elements):
 //   S = Q K^T     tcgen05.mma kind::f16, both operands in shared memory, f32 in TMEM
-//   P = exp2(S * scale - ref)    in registers: one thread per row, no shuffles;
-//                 back to TMEM as bf16 over S
+//   P = exp2(S * scale - ref)    in registers, half a row per thread, no shuffles; back
+//                 to TMEM as bf16 over S
 //   O += P V      tcgen05.mma with P from TMEM; V as it lies (rows along K)
 // The two tiles (or, with one tile, two S buffers of neighbouring blocks) alternate:
-// one is in its softmax while the other's products run.
+// one is in its softmax while the other's products run.  A block's softmax has to take
+// no longer than the other's products, about 1300 cycles: a row is two threads' work,
+// which exchange their largest score (one thread per row took 1700, and held or read
+// again twice as many scores).
 //
 // The softmax reference moves only when a score exceeds it by 2^8 (sums then hold
 // weights up to 2^8, as exact in f32 as below 1); only then is O read, scaled and
@@ -28,8 +31,12 @@
 // NaN is not: a row whose output is not finite is computed again from its visible
 // keys alone, one warp per row (row_again).
 //
-// Warps: 0 issues TMA, 1 allocates TMEM and issues the products, 2 checks the starts,
-// 4.. are the softmax and output warps, four per tile.
+// A launch has a block per item, the longest first; a running one asks for the next
+// item that has not started (cluster launch control), so no counter in memory is
+// needed and the last items are short.
+//
+// Warps: 0 asks for items and issues TMA, 1 allocates TMEM and issues the products, 4..
+// are the softmax and output warps, eight per tile.
 #include "attn_math.cuh"
 #include "attn_prefill.h"
 #include "common.cuh"
@@ -42,7 +49,7 @@ using namespace sm100;
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kFew = 88, kMany = 208;
+constexpr int kFew = 56, kMany = 104;
 constexpr float kMove = 8.f;  // log2 of how far a score may exceed the reference
 
 template <int D>
@@ -52,23 +59,39 @@ struct Shape {
   static constexpr int kChunks = D / 64;           // boxes of 64 elements
   static constexpr int kQTile = 128 * D * 2, kSlot = kKeys * D * 2;
   static constexpr int kSlots = D == 64 ? 8 : 5;
-  static constexpr int kThreads = 128 + 128 * kTiles;
-  static constexpr size_t kSmem = (size_t)kTiles * kQTile + (size_t)kSlots * kSlot + 1024;
+  static constexpr int kThreads = 128 + 256 * kTiles;
   static constexpr uint32_t kS = 0, kO = 2 * kKeys;  // TMEM columns: two S, then O of each tile
 };
 
 // Positions and rows fit 32 bits (Tq and Tk do); sums that may not are 64-bit.
-template <int D>
 struct Item {
-  int q0, k0;        // first rows of the sequence
-  int n, m;          // its queries and keys
-  int tok0;          // the item's first token
-  int kv, head0;     // key/value head, first query head
-  int heads;         // of head0's on, that are the tile's own
-  int lo[Shape<D>::kTiles], hi[Shape<D>::kTiles];  // blocks of each tile
-  int first, last;   // blocks of all tiles
-  bool any;          // tokens
+  int q0, k0;      // first rows of the sequence
+  int n, m;        // its queries and keys; n = 0: no more items
+  int tok0;        // the item's first token
+  int kv, head0;   // key/value head, first query head
+  int heads;       // of head0's on, that are the tile's own
+  int lo[2], hi[2];            // blocks that each tile's tokens see some keys of
+  int whole_lo[2], whole_hi[2];  // and those that all of them see all of
+  int first, last;             // blocks of all tiles
 };
+
+constexpr int kAhead = 2;  // items asked for ahead
+
+template <int D>
+struct Control {
+  static constexpr int kTiles = Shape<D>::kTiles, kSlots = Shape<D>::kSlots;
+  uint8_t answer[16];
+  Item items[kAhead];
+  uint64_t q_full[kTiles], q_empty[kTiles], kv_full[kSlots], kv_empty[kSlots], s_full[2], p_full[2], o_full[2], answered,
+      item_full[kAhead], item_empty[kAhead];
+  float exchange[3 - kTiles][kTiles * 256];
+  uint32_t tmem;
+  int stop;
+};
+template <int D>
+constexpr size_t smem_bytes() {
+  return (size_t)Shape<D>::kTiles * Shape<D>::kQTile + (size_t)Shape<D>::kSlots * Shape<D>::kSlot + sizeof(Control<D>);
+}
 
 __device__ __forceinline__ int clamp_start(const int32_t *starts, int b, int total) {
   const int v = __ldg(starts + b);
@@ -79,9 +102,8 @@ __device__ __forceinline__ int clamp_start(const int32_t *starts, int b, int tot
 // Sequence b owns the places [q_starts[b] / T + b, q_starts[b + 1] / T + b + 1) for
 // its ceil(n / T) tiles of T tokens: found from the starts alone.
 template <int D>
-__device__ __forceinline__ Item<D> item_of(const PrefillArgs &p, int64_t i) {
+__device__ __forceinline__ bool item_of(const PrefillArgs &p, int64_t i, Item *it) {
   constexpr int kTiles = Shape<D>::kTiles, kKeys = Shape<D>::kKeys;
-  Item<D> it;
   const int groups = p.n_kv * p.chunks, T = kTiles * p.tokens;
   const int group = (int)(i % groups), place = (int)(p.items / groups - 1 - i / groups);
   int b = 0;
@@ -92,37 +114,39 @@ __device__ __forceinline__ Item<D> item_of(const PrefillArgs &p, int64_t i) {
   }
   const int q0 = clamp_start(p.q_starts, b, p.Tq), q1 = clamp_start(p.q_starts, b + 1, p.Tq);
   const int k0 = clamp_start(p.k_starts, b, p.Tk), k1 = clamp_start(p.k_starts, b + 1, p.Tk);
-  it.q0 = q0;
-  it.k0 = k0;
-  it.n = q1 > q0 ? q1 - q0 : 0;
-  it.m = k1 > k0 ? k1 - k0 : 0;
+  const int n = q1 - q0, m = max(k1 - k0, 0);
   const int64_t tok0 = (int64_t)(place - (q0 / T + b)) * T;
-  it.any = tok0 >= 0 && tok0 < it.n;
-  it.tok0 = it.any ? (int)tok0 : 0;
+  if (tok0 < 0 || tok0 >= n) return false;
+  it->q0 = q0;
+  it->k0 = k0;
+  it->n = n;
+  it->m = m;
+  it->tok0 = (int)tok0;
   const int per_kv = p.n_heads / p.n_kv, chunk = group % p.chunks;
-  it.kv = group / p.chunks;
-  it.head0 = it.kv * per_kv + chunk * p.heads;
-  it.heads = min(p.heads, per_kv - chunk * p.heads);
-  it.first = it.last = 0;
+  it->kv = group / p.chunks;
+  it->head0 = it->kv * per_kv + chunk * p.heads;
+  it->heads = min(p.heads, per_kv - chunk * p.heads);
+  int first = 0, last = 0;
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
-    const int64_t a = (int64_t)it.tok0 + t * p.tokens;
-    const int64_t e = min(a + p.tokens, (int64_t)it.n);
-    it.lo[t] = it.hi[t] = 0;
-    if (!it.any || a >= e) continue;
-    // the keys that the tile's tokens see
-    const int64_t off = (int64_t)it.m - it.n;
-    int64_t hi = it.m, lo = 0;
-    if (p.causal) hi = min(hi, e + off);
-    if (p.window > 0) lo = max((int64_t)0, a + off - p.window + 1);
-    if (lo >= hi) continue;
-    it.lo[t] = (int)(lo / kKeys);
-    it.hi[t] = (int)((hi + kKeys - 1) / kKeys);
-    if (it.last == 0) it.first = it.lo[t];
-    it.first = min(it.first, it.lo[t]);
-    it.last = max(it.last, it.hi[t]);
+    // the tile's tokens [a, e), and the keys that some and that all of them see
+    const int64_t a = tok0 + t * p.tokens, e = min(a + p.tokens, (int64_t)n), off = (int64_t)m - n;
+    int64_t hi = m, lo = 0, all_hi = m, all_lo = 0;
+    if (p.causal) hi = min(hi, e + off), all_hi = min(all_hi, a + off + 1);
+    if (p.window > 0) lo = max(lo, a + off - p.window + 1), all_lo = max(all_lo, e + off - p.window);
+    const bool some = a < e && lo < hi;
+    it->lo[t] = some ? (int)(lo / kKeys) : 0;
+    it->hi[t] = some ? (int)((hi + kKeys - 1) / kKeys) : 0;
+    it->whole_lo[t] = (int)((all_lo + kKeys - 1) / kKeys);
+    it->whole_hi[t] = all_hi > 0 ? (int)(all_hi / kKeys) : 0;
+    if (some) {
+      first = last == 0 ? it->lo[t] : min(first, it->lo[t]);
+      last = max(last, it->hi[t]);
+    }
   }
-  return it;
+  it->first = first;
+  it->last = last;
+  return true;
 }
 
 // A row's score after the products: in units of log2, options applied.
@@ -132,12 +156,48 @@ __device__ __forceinline__ float option_score(float s, float scale, float cap, f
   return fmaf(slope, (float)back, s) * kLog2e;
 }
 
+// The same for 32 neighbouring keys, the first `back` beyond the row's position.
+// Scores within 0.6 of the cap, which nearly all are, take tanh's polynomial two at a
+// time and no special-function instructions; else the warp takes tanh_f32's both ways.
+__device__ __forceinline__ void option_scores(uint32_t (&s)[32], float scale, float cap, float slope, int back) {
+  if (cap > 0.f) {
+    const float unit = __fdividef(scale, cap);
+    float most = 0.f;
+#pragma unroll
+    for (int c = 0; c < 32; c += 2)
+      most = max3(most, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
+    const uint64_t u2 = pack_f32x2(unit, unit), cap2 = pack_f32x2(cap * kLog2e, cap * kLog2e);
+    if (__all_sync(0xffffffffu, most * fabsf(unit) < 0.6f)) {
+      const auto both = [](float f) { return pack_f32x2(f, f); };
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        const uint64_t y = mul_f32x2(pack_f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), u2), z = mul_f32x2(y, y);
+        uint64_t t = fma_f32x2(z, both(kTanh[4]), both(kTanh[3]));
+        t = fma_f32x2(z, t, both(kTanh[2]));
+        t = fma_f32x2(z, t, both(kTanh[1]));
+        t = fma_f32x2(z, t, both(kTanh[0]));
+        const float2 f = unpack_f32x2(mul_f32x2(fma_f32x2(mul_f32x2(y, z), t, y), cap2));
+        s[c] = __float_as_uint(f.x), s[c + 1] = __float_as_uint(f.y);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(cap * kLog2e * tanh_f32(__uint_as_float(s[c]) * unit));
+    }
+    scale = 1.f;
+  } else {
+    scale *= kLog2e;
+  }
+  slope *= kLog2e;
+#pragma unroll
+  for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(fmaf(__uint_as_float(s[c]), scale, slope * (float)(back + c)));
+}
+
 // One row from its visible keys alone, by a warp: for rows that met values which are
 // not finite.  32 keys at a time, a lane scoring one; then lane l adds up the
-// elements l * D / 32 ... of their values.
+// elements l * D / 32 ... of their values.  Elements [from, to) are written.
 template <int D>
 __device__ __noinline__ void row_again(const PrefillArgs &p, const __nv_bfloat16 *q, const __nv_bfloat16 *k, const __nv_bfloat16 *v,
-                                       int lo, int hi, int pos, float slope, __nv_bfloat16 *out, float *lse) {
+                                       int lo, int hi, int pos, float slope, int from, int to, __nv_bfloat16 *out, float *lse) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   float acc[E], m = -INFINITY, l = 0.f;
@@ -173,8 +233,10 @@ __device__ __noinline__ void row_again(const PrefillArgs &p, const __nv_bfloat16
       for (int e = 0; e < E; ++e) acc[e] = fmaf(wj, __bfloat162float(row[e]), acc[e]);
     }
   }
+  if (lane * E >= from && lane * E < to) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[lane * E + e] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[e] / l);
+    for (int e = 0; e < E; ++e) out[lane * E + e] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[e] / l);
+  }
   if (lse != nullptr && lane == 0) *lse = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
 }
 
@@ -186,22 +248,27 @@ __device__ __forceinline__ void give_up(volatile int *stop, int *err) {
 // Option: scores need more than a positive scale (a cap, slopes, another scale).
 template <int D, bool Option>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tq,
-                                                                       const __grid_constant__ CUtensorMap tk,
-                                                                       const __grid_constant__ CUtensorMap tv, const PrefillArgs p) {
+                                                             const __grid_constant__ CUtensorMap tk,
+                                                             const __grid_constant__ CUtensorMap tv, const PrefillArgs p) {
   using Z = Shape<D>;
   constexpr int kTiles = Z::kTiles, kKeys = Z::kKeys, kSlots = Z::kSlots;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t q_full[kTiles], q_empty[kTiles], kv_full[kSlots], kv_empty[kSlots], s_full[2], p_full[2],
-      o_full[kTiles];
-  __shared__ uint32_t tmem_sh;
-  __shared__ volatile int stop;
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // query tiles, key and value slots, control
   uint8_t *ring = smem + kTiles * Z::kQTile;
+  using Ctl = Control<D>;
+  Ctl &ctl = *reinterpret_cast<Ctl *>(ring + kSlots * Z::kSlot);
+  auto &q_full = ctl.q_full, &q_empty = ctl.q_empty;
+  auto &kv_full = ctl.kv_full, &kv_empty = ctl.kv_empty;
+  auto &s_full = ctl.s_full, &p_full = ctl.p_full, &o_full = ctl.o_full;
+  auto &item_full = ctl.item_full, &item_empty = ctl.item_empty;
+  auto &exchange = ctl.exchange;
+  volatile int &stop = ctl.stop;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int t = 0; t < kTiles; ++t) mbar_init(&q_full[t], 1), mbar_init(&q_empty[t], 1), mbar_init(&o_full[t], 1);
+    for (int t = 0; t < kTiles; ++t) mbar_init(&q_full[t], 1), mbar_init(&q_empty[t], 1);
     for (int s = 0; s < kSlots; ++s) mbar_init(&kv_full[s], 1), mbar_init(&kv_empty[s], 1);
-    for (int b = 0; b < 2; ++b) mbar_init(&s_full[b], 1), mbar_init(&p_full[b], 4);
+    for (int b = 0; b < 2; ++b) mbar_init(&s_full[b], 1), mbar_init(&p_full[b], 8), mbar_init(&o_full[b], 1);
+    for (int b = 0; b < kAhead; ++b) mbar_init(&item_full[b], 1), mbar_init(&item_empty[b], 1 + 8 * kTiles);
+    mbar_init(&ctl.answered, 1);
     stop = 0;
     fence_mbar_init();
     prefetch_tmap(&tq);
@@ -209,26 +276,41 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     prefetch_tmap(&tv);
   }
   if (warp == 1) {
-    tmem_alloc(&tmem_sh, 512);
+    tmem_alloc(&ctl.tmem, 512);
     tmem_relinquish();
     tc_fence_before();
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_sh;
+  const uint32_t tmem = ctl.tmem;
   pdl_wait();
   pdl_trigger();
 
-  // 384 threads start with 168 registers each; the eight softmax warps hold a row of
-  // scores: 128 * 88 + 256 * 208 = 384 * 168 (checked against the build in ready_d).
-  // (Each role's branch says so itself, which is where the compiler looks.)
+  // The items, which warp 0 writes one after another: the other roles take each once.
+  int turn = 0;
+  uint32_t turn_phase = 0;
+  const auto item_ready = [&] {  // false: it gave up
+    if (mbar_wait(&item_full[turn], turn_phase, nullptr, kWaitNs)) return true;
+    give_up(&stop, p.err);
+    return false;
+  };
+  const auto item_done = [&] {
+    mbar_arrive(&item_empty[turn]);
+    if (++turn == kAhead) turn = 0, turn_phase ^= 1u;
+  };
+
+  // Two tiles: 640 threads start with 96 registers each, of which the softmax warps,
+  // who hold 64 scores each, take more: 128 * 56 + 512 * 104 <= 640 * 96 (checked
+  // against the build in ready_d).  Each branch asks for itself, which is where the
+  // compiler looks.
   if (warp < 4) {
   if constexpr (kTiles == 2) fewer_registers<kFew>();
   if (warp == 0) {
     if (lane == 0) {
       int slot = 0;
-      uint32_t phase = 0, q_phase = 0;  // a bit per tile
-      const auto load = [&](const CUtensorMap *map, const Item<D> &it, int block) {
+      uint32_t phase = 0, q_phase = 0, answer_phase = 0;  // q_phase: a bit per tile
+      int64_t i = blockIdx.x;
+      const auto load = [&](const CUtensorMap *map, const Item &it, int block) {
         if (!mbar_wait(&kv_empty[slot], phase ^ 1u, &stop, kWaitNs)) {
           give_up(&stop, p.err);
           return false;
@@ -236,15 +318,48 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         mbar_arrive_expect_tx(&kv_full[slot], Z::kSlot);
 #pragma unroll
         for (int c = 0; c < Z::kChunks; ++c)
-          tma_load_3d(ring + (size_t)slot * Z::kSlot + c * (kKeys * 128), map, 64 * c, it.kv, it.k0 + block * kKeys,
-                      &kv_full[slot]);
+          tma_load_3d(ring + (size_t)slot * Z::kSlot + c * (kKeys * 128), map, 64 * c, it.kv, it.k0 + block * kKeys, &kv_full[slot]);
         if (++slot == kSlots) slot = 0, phase ^= 1u;
         return true;
       };
       bool ok = true;
-      for (int64_t i = blockIdx.x; ok && i < p.items && !stop; i += gridDim.x) {
-        const Item<D> it = item_of<D>(p, i);
-        if (it.last == 0) continue;
+      while (ok) {
+        ok = mbar_wait(&item_empty[turn], turn_phase ^ 1u, &stop, kWaitNs);
+        if (!ok) {
+          give_up(&stop, p.err);
+          break;
+        }
+        Item &it = ctl.items[turn];
+        // the next place with tokens; the one after is asked for meanwhile
+        bool some = false, asked = false;
+        while (ok && i >= 0 && !some) {
+          if (asked) {
+            ok = mbar_wait(&ctl.answered, answer_phase, &stop, kWaitNs);
+            if (!ok) {
+              give_up(&stop, p.err);
+              break;
+            }
+            answer_phase ^= 1u;
+            i = requested_block(ctl.answer);
+            if (i < 0) break;
+            fence_proxy_async_shared();  // the answer has been read before the next is written
+          }
+          if (p.stride == 0) {
+            mbar_arrive_expect_tx(&ctl.answered, 16);
+            request_block(ctl.answer, &ctl.answered);
+            asked = true;
+          }
+          some = item_of<D>(p, i, &it);
+          if (p.stride > 0) {
+            if (some) break;
+            i = i + p.stride < p.items ? i + p.stride : -1;
+          }
+        }
+        if (!ok) break;
+        if (!some) it.n = 0;
+        mbar_arrive(&item_full[turn]);
+        if (++turn == kAhead) turn = 0, turn_phase ^= 1u;
+        if (!some) break;
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
           if (it.lo[t] >= it.hi[t]) continue;
@@ -261,12 +376,25 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
                         &q_full[t]);
         }
         // in the order of their first use: keys one block ahead (with one tile, two)
-        ok = ok && load(&tk, it, it.first);
+        if (it.last > 0) ok = ok && load(&tk, it, it.first);
         if (kTiles == 1 && it.first + 1 < it.last) ok = ok && load(&tk, it, it.first + 1);
         for (int j = it.first; ok && j < it.last; ++j) {
           ok = load(&tv, it, j);
           const int ahead = j + (kTiles == 1 ? 2 : 1);
           if (ok && ahead < it.last) ok = load(&tk, it, ahead);
+        }
+        if (!ok) break;
+        if (p.stride > 0) {
+          i = i + p.stride < p.items ? i + p.stride : -1;
+        } else {
+          ok = mbar_wait(&ctl.answered, answer_phase, &stop, kWaitNs);
+          if (!ok) {
+            give_up(&stop, p.err);
+            break;
+          }
+          answer_phase ^= 1u;
+          i = requested_block(ctl.answer);
+          fence_proxy_async_shared();
         }
       }
     }
@@ -303,14 +431,15 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
           mma_bf16_ts(tmem + Z::kO + t * D, tmem + Z::kS + buf * kKeys + k * 8, b + k * (2048 / 16), i_o, more || k > 0 ? 1u : 0u);
-        mma_commit(&o_full[t]);
+        mma_commit(&o_full[buf]);
       };
       const auto advance = [&] {
         mma_commit(&kv_empty[slot]);
         if (++slot == kSlots) slot = 0, phase ^= 1u;
       };
-      for (int64_t i = blockIdx.x; ok && i < p.items && !stop; i += gridDim.x) {
-        const Item<D> it = item_of<D>(p, i);
+      for (; ok && !stop && item_ready(); item_done()) {
+        const Item &it = ctl.items[turn];
+        if (it.n == 0) break;
         if (it.last == 0) continue;
         if constexpr (kTiles == 2) {
           // block j of the keys has a slot, and is used by both tiles; values likewise
@@ -383,149 +512,180 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         }
       }
     }
-  } else if (warp == 2 && blockIdx.x == 0) {
-    bool bad = false;
-    for (int b = lane; b <= p.B; b += 32) {
-      const int qs = __ldg(p.q_starts + b), ks = __ldg(p.k_starts + b);
-      bad |= qs < 0 || qs > p.Tq || ks < 0 || ks > p.Tk;
-      if (b < p.B) bad |= __ldg(p.q_starts + b + 1) < qs || __ldg(p.k_starts + b + 1) < ks;
-    }
-    if (bad) set_error(p.err, DEV_ERR_BOUNDS);
   }
   } else {
     if constexpr (kTiles == 2) more_registers<kMany>();
-    const int t = (warp - 4) >> 2;  // tile
+    if (blockIdx.x == 0) {  // the starts are as they should be
+      bool bad = false;
+      for (int b = threadIdx.x - 128; b <= p.B; b += Z::kThreads - 128) {
+        const int qs = __ldg(p.q_starts + b), ks = __ldg(p.k_starts + b);
+        bad |= qs < 0 || qs > p.Tq || ks < 0 || ks > p.Tk;
+        if (b < p.B) bad |= __ldg(p.q_starts + b + 1) < qs || __ldg(p.k_starts + b + 1) < ks;
+      }
+      if (bad) set_error(p.err, DEV_ERR_BOUNDS);
+      __syncwarp();
+    }
+    const int t = (warp - 4) >> 3, way = (warp - 4) >> 2 & 1;
+    constexpr int kMine = kKeys / 2, kOut = D / 2;  // columns of S and O of this thread
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int row = (warp & 3) * 32 + lane;  // of the tile
-    const uint32_t t_o = tmem + lanes + Z::kO + t * D;
-    const int r_tok = row / p.heads, r_head = row - r_tok * p.heads;
+    const uint32_t t_o = tmem + lanes + Z::kO + t * D + way * kOut;
     const float scale2 = Option ? 1.f : p.scale * kLog2e;
-    int step = 0;               // S buffers used (one tile)
-    uint32_t s_phase = 0, o_count = 0;  // products with V that the tile has had
+    uint32_t step = 0;  // blocks that the tile has had
     bool ok = true;
-    for (int64_t i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
-      const Item<D> it = item_of<D>(p, i);
-      if (!it.any) continue;
-      // of the sequence (past its end: a row of no use); a row's position is below the
-      // last key's by the tokens that follow it
-      const uint32_t tok = (uint32_t)(it.tok0 + t * p.tokens) + (uint32_t)r_tok;
-      const bool mine = r_tok < p.tokens && r_head < it.heads && tok < (uint32_t)it.n;
-      const int pos = it.m - (int)((uint32_t)it.n - tok);
-      // the keys that this row sees, and those that all of the tile's rows do
-      int see_lo = 0, see_hi = it.m, all_lo = 0, all_hi = it.m;
-      if (p.causal) {
-        see_hi = max(0, min(it.m, pos + 1));
-        all_hi = max(0, min(it.m, it.m - (it.n - (it.tok0 + t * p.tokens)) + 1));
+    // The value that the row's other thread has.  Their warps share a barrier, so they
+    // stop together: a wait that gave up in one ends both here.  With two tiles a value
+    // is read before the tile's next scores are asked for, which the next value comes
+    // after; with one, whose scores run ahead, they go to two places in turn.
+    const int pair = 1 + t * 4 + (warp & 3);
+    int ex = 0;
+    const auto other = [&](float mine) {
+      exchange[ex][t * 256 + way * 128 + row] = mine;
+      ok = named_bar_and(pair, 64, ok);
+      const float f = exchange[ex][t * 256 + (way ^ 1) * 128 + row];
+      if (kTiles == 1) ex ^= 1;
+      return f;
+    };
+    const auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (!mbar_wait(bar, parity, nullptr, kWaitNs)) {
+        give_up(&stop, p.err);
+        ok = false;  // goes on, as far as the next barrier
       }
-      if (p.window > 0) {
-        const int behind = it.n - it.tok0 - (t + 1) * p.tokens;  // tokens after the tile's
-        see_lo = (int)max(INT64_C(0), min((int64_t)it.m, (int64_t)pos - p.window + 1));
-        all_lo = (int)max(INT64_C(0), (int64_t)it.m - max(behind, 0) - p.window);
-      }
-      const float slope = Option && p.slopes != nullptr && mine ? __ldg(p.slopes + it.head0 + r_head) : 0.f;
+      tc_fence_after();
+    };
+    // The tile's products with V so far.  A barrier per S buffer: when a block's scores
+    // are ready the products of the block before it in the same buffer are done, but
+    // with one tile not yet those of the other buffer's, and a wait tells only the last
+    // of a barrier's phases from the one before it.
+    const auto products_done = [&] {
+      const uint32_t n = step - 1u;
+      if (kTiles == 2) wait(&o_full[t], n & 1u);
+      else wait(&o_full[n & 1u], n >> 1 & 1u);
+    };
+    while (true) {
+      const bool got = item_ready();
+      volatile Item &it = ctl.items[turn];  // read where it is used: registers are short
+      ok = named_bar_and(pair, 64, ok && got && it.n > 0);
+      if (!ok) break;
+      // The row's token, of the sequence (past its end: a row of no use), and head.
+      // (Taken apart again behind the blocks: the asm hides that it is the same.)
+      struct Place {
+        uint32_t tok;
+        int head;
+        bool mine;
+      };
+      const auto place = [&] {
+        int r = row;
+        asm volatile("" : "+r"(r));
+        const int r_tok = r / p.heads, r_head = r - r_tok * p.heads;
+        const uint32_t tok = (uint32_t)(it.tok0 + t * p.tokens) + (uint32_t)r_tok;
+        return Place{tok, it.head0 + r_head, r_tok < p.tokens && r_head < it.heads && tok < (uint32_t)it.n};
+      };
+      // a row's position is below the last key's by the tokens that follow it
+      const int pos = it.m - (int)((uint32_t)it.n - place().tok);
+      // the keys that this row sees
+      const auto see_lo = [&] { return p.window > 0 ? (int)max(INT64_C(0), min((int64_t)it.m, (int64_t)pos - p.window + 1)) : 0; };
+      const auto see_hi = [&] { return p.causal ? max(0, min((int)it.m, pos + 1)) : (int)it.m; };
+      const float slope = Option && p.slopes != nullptr && place().mine ? __ldg(p.slopes + place().head) : 0.f;
       float ref = -INFINITY;
       uint64_t sum2 = 0;
-      const int lo = it.lo[t], hi = it.hi[t];
-      for (int j = lo; j < hi; ++j) {
-        const int buf = kTiles == 2 ? t : step & 1;
-        if (!mbar_wait(&s_full[buf], s_phase >> buf & 1u, &stop, kWaitNs)) {
-          give_up(&stop, p.err);
-          ok = false;
-          break;
-        }
-        s_phase ^= 1u << buf;
-        tc_fence_after();
-        const uint32_t t_s = tmem + lanes + Z::kS + buf * kKeys;
-        uint32_t s[kKeys];
+      for (int j = it.lo[t]; j < it.hi[t]; ++j) {
+        const int buf = kTiles == 2 ? t : (int)(step & 1u);
+        const bool masked = j < it.whole_lo[t] || j >= it.whole_hi[t];
+        wait(&s_full[buf], (kTiles == 2 ? step : step >> 1) & 1u);
+        const uint32_t t_s = tmem + lanes + Z::kS + buf * kKeys + way * kMine;
+        const int key0 = j * kKeys + way * kMine;
+        const auto hide = [&](uint32_t(&s)[32], int c0) {
+          const int from = see_lo() - key0 - c0, to = see_hi() - key0 - c0;
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 32) tmem_ld32(t_s + c, s + c);
-#pragma unroll
-        for (int c = 0; c < kKeys; c += 32) tmem_wait_ld(s + c);
-        const int key0 = j * kKeys;
-        if constexpr (Option) {
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c)
-            s[c] = __float_as_uint(option_score(__uint_as_float(s[c]), p.scale, p.softcap, slope, key0 + c - pos));
-        }
-        if (key0 < all_lo || key0 + kKeys > all_hi) {
-          const int from = see_lo - key0, to = see_hi - key0;
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c)
+          for (int c = 0; c < 32; ++c)
             if (c < from || c >= to) s[c] = __float_as_uint(-INFINITY);
+        };
+        float top[2] = {-INFINITY, -INFINITY};
+        const auto largest = [&](uint32_t(&s)[32], int c0) {
+          if constexpr (Option) option_scores(s, p.scale, p.softcap, slope, key0 + c0 - pos);
+          if (masked) hide(s, c0);
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            top[0] = max3(top[0], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            top[1] = max3(top[1], __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+          }
+        };
+        uint32_t a[32], b[kMine > 32 ? 32 : 1];
+        tmem_ld32(t_s, a);
+        tmem_wait_ld(a);
+        if constexpr (kMine > 32) tmem_ld32(t_s + 32, b);
+        largest(a, 0);
+        if constexpr (kMine > 32) {
+          tmem_wait_ld(b);
+          largest(b, 32);
         }
-        float top[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) top[c] = __uint_as_float(s[c]);
-#pragma unroll
-        for (int c = 4; c < kKeys; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
-        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale2;
+        float most = fmaxf(top[0], top[1]) * scale2;
+        tc_fence_before();
+        most = fmaxf(most, other(most));
+        tc_fence_after();
+        if (!ok) break;
         const bool move = most > ref + kMove;
         if (__any_sync(0xffffffffu, move)) {
           const float keep = !move ? 1.f : ref == -INFINITY ? 0.f : exp2_fast(ref - most);
           if (move) ref = most;
-          const uint64_t kk = pack_f32x2(keep, keep);
-          sum2 = mul_f32x2(sum2, kk);
-          if (j > lo) {
+          sum2 = mul_f32x2(sum2, pack_f32x2(keep, keep));
+          if (j > it.lo[t]) {
             // S of this block is ready, so the products with V up to the one before
             // last are done (with two tiles the last too)
-            if (kTiles == 1 && !mbar_wait(&o_full[t], (o_count - 1u) & 1u, &stop, kWaitNs)) {
-              give_up(&stop, p.err);
-              ok = false;
-              break;
-            }
-            tc_fence_after();
+            if (kTiles == 1) products_done();
+            // (8 columns at a time: the block's scores are in registers)
+#pragma unroll 1
+            for (int c = 0; c < kOut; c += 8) {
+              uint32_t o[8];
+              tmem_load8(t_o + c, o);
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(t_o + c, o);
-              tmem_wait_ld(o);
-#pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
-              tmem_st32(t_o + c, o);
+              for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
+              tmem_store8(t_o + c, o);
             }
           }
         }
         const float minus = ref == -INFINITY ? 0.f : -ref;
         const uint64_t mul = pack_f32x2(scale2, scale2), add = pack_f32x2(minus, minus);
-        uint64_t part = 0;
+        const auto weights = [&](uint32_t(&s)[32], int c0) {
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 32) {
-          uint32_t w[16];
+          for (int g = 0; g < 32; g += 16) {
+            uint32_t w[8];
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            const float2 f = unpack_f32x2(
-                fma_f32x2(pack_f32x2(__uint_as_float(s[c + x]), __uint_as_float(s[c + x + 1])), mul, add));
-            const float p0 = exp2_fast(f.x), p1 = exp2_fast(f.y);
-            part = add_f32x2(part, pack_f32x2(p0, p1));
-            w[x / 2] = bf16x2_of(p0, p1);
+            for (int x = 0; x < 16; x += 2) {
+              const uint64_t two = pack_f32x2(__uint_as_float(s[g + x]), __uint_as_float(s[g + x + 1]));
+              const float2 f = unpack_f32x2(Option ? add_f32x2(two, add) : fma_f32x2(two, mul, add));
+              const float p0 = exp2_fast(f.x), p1 = exp2_fast(f.y);
+              sum2 = add_f32x2(sum2, pack_f32x2(p0, p1));
+              w[x / 2] = bf16x2_of(p0, p1);
+            }
+            tmem_st8(tmem + lanes + Z::kS + buf * kKeys + (way * kMine + c0 + g) / 2, w);
           }
-          tmem_st16(t_s + c / 2, w);
-        }
-        sum2 = add_f32x2(sum2, part);
+        };
+        // the weights lie over scores that both threads have read
+        weights(a, 0);
+        if constexpr (kMine > 32) weights(b, 32);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
         ++step;
-        ++o_count;
       }
+      const bool blocks = it.lo[t] < it.hi[t];
+      if (blocks) products_done();
+      const float2 s2 = unpack_f32x2(sum2);
+      float sum = s2.x + s2.y;
+      sum += other(sum);
       if (!ok) break;
-      const float2 sums = unpack_f32x2(sum2);
-      const float sum = sums.x + sums.y;
       const float inv = sum > 0.f || !(sum == sum) ? 1.f / sum : 0.f;
-      if (lo < hi) {
-        if (!mbar_wait(&o_full[t], (o_count - 1u) & 1u, &stop, kWaitNs)) {
-          give_up(&stop, p.err);
-          break;
-        }
-        tc_fence_after();
-      }
-      __nv_bfloat16 *out = p.out + (it.q0 + (int64_t)tok) * p.out_stride + (int64_t)(it.head0 + r_head) * D;
+      const Place at = place();
+      const int64_t out_row = it.q0 + (int64_t)at.tok;
+      __nv_bfloat16 *out = p.out + out_row * p.out_stride + (int64_t)at.head * D + way * kOut;
       bool odd = false;
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < kOut; c += 32) {
         uint32_t o[32];
-        if (lo < hi) {
+        if (blocks) {
           tmem_ld32(t_o + c, o);
           tmem_wait_ld(o);
         }
@@ -535,24 +695,27 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
           odd |= !(fabsf(f) <= 3.402823466e38f && fabsf(g) <= 3.402823466e38f);
           o[x / 2] = bf16x2_of(f, g);
         }
-        if (mine) {
+        if (at.mine) {
 #pragma unroll
           for (int x = 0; x < 16; x += 4) *reinterpret_cast<uint4 *>(out + c + 2 * x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
         }
       }
-      if (mine && p.lse != nullptr)
-        p.lse[(it.q0 + (int64_t)tok) * p.n_heads + it.head0 + r_head] = inv == 0.f ? -INFINITY : kLn2 * (ref + log2f(sum));
+      if (at.mine && way == 0 && p.lse != nullptr)
+        p.lse[out_row * p.n_heads + at.head] = inv == 0.f ? -INFINITY : kLn2 * (ref + log2f(sum));
       __syncwarp();
-      for (uint32_t left = __ballot_sync(0xffffffffu, odd && mine); left != 0; left &= left - 1) {
+      for (uint32_t left = __ballot_sync(0xffffffffu, odd && at.mine); left != 0; left &= left - 1) {
         const int from = __ffs(left) - 1;
-        const int64_t r = it.q0 + (int64_t)__shfl_sync(0xffffffffu, tok, from);
-        const int at = __shfl_sync(0xffffffffu, pos, from);
-        const int head = it.head0 + __shfl_sync(0xffffffffu, r_head, from);
-        const int l = __shfl_sync(0xffffffffu, see_lo, from), h = __shfl_sync(0xffffffffu, see_hi, from);
+        const int64_t r = __shfl_sync(0xffffffffu, out_row, from);
+        const int r_pos = __shfl_sync(0xffffffffu, pos, from), head = __shfl_sync(0xffffffffu, at.head, from);
+        const int l = __shfl_sync(0xffffffffu, see_lo(), from), h = __shfl_sync(0xffffffffu, see_hi(), from);
         row_again<D>(p, p.q + r * p.q_stride + (int64_t)head * D, p.k + (int64_t)it.k0 * p.k_stride + (int64_t)it.kv * D,
-                     p.v + (int64_t)it.k0 * p.v_stride + (int64_t)it.kv * D, l, h, at, __shfl_sync(0xffffffffu, slope, from),
-                     p.out + r * p.out_stride + (int64_t)head * D, p.lse == nullptr ? nullptr : p.lse + r * p.n_heads + head);
+                     p.v + (int64_t)it.k0 * p.v_stride + (int64_t)it.kv * D, l, h, r_pos, __shfl_sync(0xffffffffu, slope, from),
+                     way * kOut, way * kOut + kOut, p.out + r * p.out_stride + (int64_t)head * D,
+                     p.lse == nullptr || way != 0 ? nullptr : p.lse + r * p.n_heads + head);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[turn]);
+      if (++turn == kAhead) turn = 0, turn_phase ^= 1u;
     }
   }
   __syncthreads();
@@ -576,7 +739,7 @@ bool map_rows(CUtensorMap *m, const void *p, int d, int heads, int64_t rows, int
 }
 
 template <int D>
-cudaError_t launch_d(const PrefillArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_d(PrefillArgs a, int sms, cudaStream_t s) {
   using Z = Shape<D>;
   CUtensorMap tq, tk, tv;
   // without keys nothing of k and v is read
@@ -585,21 +748,24 @@ cudaError_t launch_d(const PrefillArgs &a, int sms, cudaStream_t s) {
       !map_rows(&tk, keys ? a.k : a.q, D, keys ? a.n_kv : 1, keys ? a.Tk : 1, keys ? a.k_stride : a.q_stride, 1, Z::kKeys) ||
       !map_rows(&tv, keys ? a.v : a.q, D, keys ? a.n_kv : 1, keys ? a.Tk : 1, keys ? a.v_stride : a.q_stride, 1, Z::kKeys))
     return cudaErrorInvalidValue;
+  // a limit on the SMs: so many blocks, and every so-manieth item for each
+  a.stride = sms > 0 && sms < a.items ? sms : 0;
+  const int64_t grid = a.stride > 0 ? a.stride : a.items;
   const bool option = a.softcap > 0.f || a.slopes != nullptr || !(a.scale > 0.f);
-  return launch_pdl(option ? prefill_kernel<D, true> : prefill_kernel<D, false>, dim3((unsigned)(a.items < sms ? a.items : sms)),
-                    dim3(Z::kThreads), Z::kSmem, s, tq, tk, tv, a);
+  return launch_pdl(option ? prefill_kernel<D, true> : prefill_kernel<D, false>, dim3((unsigned)grid), dim3(Z::kThreads), smem_bytes<D>(), s,
+                    tq, tk, tv, a);
 }
 
 template <int D>
 cudaError_t ready_d() {
   for (auto k : {prefill_kernel<D, true>, prefill_kernel<D, false>}) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
     if (e != cudaSuccess) return e;
     // the softmax warps would wait forever for registers that the launch does not have
     cudaFuncAttributes at;
     e = cudaFuncGetAttributes(&at, k);
     if (e != cudaSuccess) return e;
-    if (Shape<D>::kTiles == 2 && at.numRegs * 3 < kFew + 2 * kMany) return cudaErrorInvalidKernelImage;
+    if (Shape<D>::kTiles == 2 && at.numRegs * 5 < kFew + 4 * kMany) return cudaErrorInvalidKernelImage;
   }
   return cudaSuccess;
 }

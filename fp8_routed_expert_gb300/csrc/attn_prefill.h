@@ -25,12 +25,14 @@ struct PrefillArgs {
   // The query heads of a key/value head are taken `heads` at a time, in `chunks`
   // pieces; a tile's 128 rows are the heads of `tokens` tokens.
   int heads, chunks, tokens;
-  int64_t items;  // tiles at most, times n_kv * chunks
+  int64_t items;  // tiles at most, times n_kv * chunks; below 2^31
+  int stride;     // items between one and the next of a block; 0: asked for
 };
 // Fills in heads, chunks, tokens and items.
 void plan_prefill(PrefillArgs *a, int d);
 // Readies the kernels of d.
 cudaError_t ready_prefill(int d);
+// sms: the SMs it may fill, 0 for all.
 cudaError_t launch_prefill(const PrefillArgs &a, int d, int sms, cudaStream_t s);
 
 }  // namespace fp8moe
