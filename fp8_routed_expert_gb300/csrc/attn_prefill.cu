@@ -11,20 +11,26 @@
 // whose output takes half of tensor memory).  Per block of 128 keys (64 with 256
 // elements):
 //   S = Q K^T     tcgen05.mma kind::f16, both operands in shared memory, f32 in TMEM
-//   P = exp2(S * scale - ref)    in registers, half a row per thread, no shuffles; back
-//                 to TMEM as bf16 over S
+//   P = exp2(S * scale - ref)    in registers: one thread per row, no shuffles; back to
+//                 TMEM as bf16 over S
 //   O += P V      tcgen05.mma with P from TMEM; V as it lies (rows along K)
 // The two tiles (or, with one tile, two S buffers of neighbouring blocks) alternate:
-// one is in its softmax while the other's products run.  A block's softmax has to take
-// no longer than the other's products, about 1300 cycles: a row is two threads' work,
-// which exchange their largest score (one thread per row took 1700, and held or read
-// again twice as many scores).
+// one is in its softmax while the other's products run.  So a block's softmax has to
+// take no longer than the other's products, about 1300 cycles, and while these read
+// their operands shared memory has no bandwidth left: a row is one thread's, which
+// keeps all it needs in registers and reads its scores once, 32 at a time.  (Two threads
+// per row that exchanged their largest scores, or registers that spilled, took two to
+// three times as long.)  Nothing waits for the row's largest score either: the softmax
+// reference is of the blocks before.  Where the largest so far exceeds it by 2^8 it
+// moves there, and only then is O read, scaled and written back.  A weight may so exceed
+// 2^8 for a block, which f32 sums and bf16 weights hold as exactly as one below 1; where
+// one leaves f32's range (scores that rise by 88 within a block) the row is computed
+// again (below).  Rows that have no reference yet take it from the block itself, which is
+// then read twice.  Slopes, which make scores rise from block to block, are allowed for.
 //
-// The softmax reference moves only when a score exceeds it by 2^8 (sums then hold
-// weights up to 2^8, as exact in f32 as below 1); only then is O read, scaled and
-// written back, by the row's own thread.  Weights are rounded to bf16 for the second
-// product, the matrix unit's type for bf16 values: 2^-8 of each weight at most, and
-// independent from key to key; the sum is of the f32 weights.
+// Weights are rounded to bf16 for the second product, the matrix unit's type for bf16
+// values: 2^-8 of each weight at most, and independent from key to key; the sum is of
+// the f32 weights.
 //
 // Blocks that no row sees are not visited; masks are applied in blocks that not all
 // rows see in full.  A hidden value's weight is zero, but zero times an infinity or a
@@ -35,8 +41,8 @@
 // item that has not started (cluster launch control), so no counter in memory is
 // needed and the last items are short.
 //
-// Warps: 0 asks for items and issues TMA, 1 allocates TMEM and issues the products, 4..
-// are the softmax and output warps, eight per tile.
+// Warps: 0 asks for items and issues TMA, 1 allocates TMEM and issues the products, 2..
+// are the softmax and output warps, four per tile.
 #include "attn_math.cuh"
 #include "attn_prefill.h"
 #include "common.cuh"
@@ -49,7 +55,6 @@ using namespace sm100;
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kFew = 56, kMany = 104;
 constexpr float kMove = 8.f;  // log2 of how far a score may exceed the reference
 
 template <int D>
@@ -59,7 +64,7 @@ struct Shape {
   static constexpr int kChunks = D / 64;           // boxes of 64 elements
   static constexpr int kQTile = 128 * D * 2, kSlot = kKeys * D * 2;
   static constexpr int kSlots = D == 64 ? 8 : 5;
-  static constexpr int kThreads = 128 + 256 * kTiles;
+  static constexpr int kThreads = 64 + 128 * kTiles;
   static constexpr uint32_t kS = 0, kO = 2 * kKeys;  // TMEM columns: two S, then O of each tile
 };
 
@@ -84,7 +89,6 @@ struct Control {
   Item items[kAhead];
   uint64_t q_full[kTiles], q_empty[kTiles], kv_full[kSlots], kv_empty[kSlots], s_full[2], p_full[2], o_full[2], answered,
       item_full[kAhead], item_empty[kAhead];
-  float exchange[3 - kTiles][kTiles * 256];
   uint32_t tmem;
   int stop;
 };
@@ -194,10 +198,10 @@ __device__ __forceinline__ void option_scores(uint32_t (&s)[32], float scale, fl
 
 // One row from its visible keys alone, by a warp: for rows that met values which are
 // not finite.  32 keys at a time, a lane scoring one; then lane l adds up the
-// elements l * D / 32 ... of their values.  Elements [from, to) are written.
+// elements l * D / 32 ... of their values. 
 template <int D>
 __device__ __noinline__ void row_again(const PrefillArgs &p, const __nv_bfloat16 *q, const __nv_bfloat16 *k, const __nv_bfloat16 *v,
-                                       int lo, int hi, int pos, float slope, int from, int to, __nv_bfloat16 *out, float *lse) {
+                                       int lo, int hi, int pos, float slope, __nv_bfloat16 *out, float *lse) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   float acc[E], m = -INFINITY, l = 0.f;
@@ -233,10 +237,8 @@ __device__ __noinline__ void row_again(const PrefillArgs &p, const __nv_bfloat16
       for (int e = 0; e < E; ++e) acc[e] = fmaf(wj, __bfloat162float(row[e]), acc[e]);
     }
   }
-  if (lane * E >= from && lane * E < to) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[lane * E + e] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[e] / l);
-  }
+  for (int e = 0; e < E; ++e) out[lane * E + e] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[e] / l);
   if (lse != nullptr && lane == 0) *lse = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
 }
 
@@ -260,14 +262,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
   auto &kv_full = ctl.kv_full, &kv_empty = ctl.kv_empty;
   auto &s_full = ctl.s_full, &p_full = ctl.p_full, &o_full = ctl.o_full;
   auto &item_full = ctl.item_full, &item_empty = ctl.item_empty;
-  auto &exchange = ctl.exchange;
   volatile int &stop = ctl.stop;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int t = 0; t < kTiles; ++t) mbar_init(&q_full[t], 1), mbar_init(&q_empty[t], 1);
     for (int s = 0; s < kSlots; ++s) mbar_init(&kv_full[s], 1), mbar_init(&kv_empty[s], 1);
-    for (int b = 0; b < 2; ++b) mbar_init(&s_full[b], 1), mbar_init(&p_full[b], 8), mbar_init(&o_full[b], 1);
-    for (int b = 0; b < kAhead; ++b) mbar_init(&item_full[b], 1), mbar_init(&item_empty[b], 1 + 8 * kTiles);
+    for (int b = 0; b < 2; ++b) mbar_init(&s_full[b], 1), mbar_init(&p_full[b], 4), mbar_init(&o_full[b], 1);
+    for (int b = 0; b < kAhead; ++b) mbar_init(&item_full[b], 1), mbar_init(&item_empty[b], 1 + 4 * kTiles);
     mbar_init(&ctl.answered, 1);
     stop = 0;
     fence_mbar_init();
@@ -299,12 +300,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     if (++turn == kAhead) turn = 0, turn_phase ^= 1u;
   };
 
-  // Two tiles: 640 threads start with 96 registers each, of which the softmax warps,
-  // who hold 64 scores each, take more: 128 * 56 + 512 * 104 <= 640 * 96 (checked
-  // against the build in ready_d).  Each branch asks for itself, which is where the
-  // compiler looks.
-  if (warp < 4) {
-  if constexpr (kTiles == 2) fewer_registers<kFew>();
   if (warp == 0) {
     if (lane == 0) {
       int slot = 0;
@@ -512,12 +507,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         }
       }
     }
-  }
   } else {
-    if constexpr (kTiles == 2) more_registers<kMany>();
     if (blockIdx.x == 0) {  // the starts are as they should be
       bool bad = false;
-      for (int b = threadIdx.x - 128; b <= p.B; b += Z::kThreads - 128) {
+      for (int b = threadIdx.x - 64; b <= p.B; b += Z::kThreads - 64) {
         const int qs = __ldg(p.q_starts + b), ks = __ldg(p.k_starts + b);
         bad |= qs < 0 || qs > p.Tq || ks < 0 || ks > p.Tk;
         if (b < p.B) bad |= __ldg(p.q_starts + b + 1) < qs || __ldg(p.k_starts + b + 1) < ks;
@@ -525,33 +518,22 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
       if (bad) set_error(p.err, DEV_ERR_BOUNDS);
       __syncwarp();
     }
-    const int t = (warp - 4) >> 3, way = (warp - 4) >> 2 & 1;
-    constexpr int kMine = kKeys / 2, kOut = D / 2;  // columns of S and O of this thread
+    constexpr int kParts = kKeys / 32;
+    const int t = (warp - 2) >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int row = (warp & 3) * 32 + lane;  // of the tile
-    const uint32_t t_o = tmem + lanes + Z::kO + t * D + way * kOut;
+    const uint32_t t_o = tmem + lanes + Z::kO + t * D;
+    const int r_tok = row / p.heads, r_head = row - r_tok * p.heads;
     const float scale2 = Option ? 1.f : p.scale * kLog2e;
     uint32_t step = 0;  // blocks that the tile has had
     bool ok = true;
-    // The value that the row's other thread has.  Their warps share a barrier, so they
-    // stop together: a wait that gave up in one ends both here.  With two tiles a value
-    // is read before the tile's next scores are asked for, which the next value comes
-    // after; with one, whose scores run ahead, they go to two places in turn.
-    const int pair = 1 + t * 4 + (warp & 3);
-    int ex = 0;
-    const auto other = [&](float mine) {
-      exchange[ex][t * 256 + way * 128 + row] = mine;
-      ok = named_bar_and(pair, 64, ok);
-      const float f = exchange[ex][t * 256 + (way ^ 1) * 128 + row];
-      if (kTiles == 1) ex ^= 1;
-      return f;
-    };
     const auto wait = [&](uint64_t *bar, uint32_t parity) {
-      if (!mbar_wait(bar, parity, nullptr, kWaitNs)) {
+      if (ok && !mbar_wait(bar, parity, &stop, kWaitNs)) {
         give_up(&stop, p.err);
-        ok = false;  // goes on, as far as the next barrier
+        ok = false;
       }
       tc_fence_after();
+      return ok;
     };
     // The tile's products with V so far.  A barrier per S buffer: when a block's scores
     // are ready the products of the block before it in the same buffer are done, but
@@ -559,133 +541,148 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     // of a barrier's phases from the one before it.
     const auto products_done = [&] {
       const uint32_t n = step - 1u;
-      if (kTiles == 2) wait(&o_full[t], n & 1u);
-      else wait(&o_full[n & 1u], n >> 1 & 1u);
+      return kTiles == 2 ? wait(&o_full[t], n & 1u) : wait(&o_full[n & 1u], n >> 1 & 1u);
     };
-    while (true) {
-      const bool got = item_ready();
-      volatile Item &it = ctl.items[turn];  // read where it is used: registers are short
-      ok = named_bar_and(pair, 64, ok && got && it.n > 0);
-      if (!ok) break;
-      // The row's token, of the sequence (past its end: a row of no use), and head.
-      // (Taken apart again behind the blocks: the asm hides that it is the same.)
-      struct Place {
-        uint32_t tok;
-        int head;
-        bool mine;
-      };
-      const auto place = [&] {
-        int r = row;
-        asm volatile("" : "+r"(r));
-        const int r_tok = r / p.heads, r_head = r - r_tok * p.heads;
-        const uint32_t tok = (uint32_t)(it.tok0 + t * p.tokens) + (uint32_t)r_tok;
-        return Place{tok, it.head0 + r_head, r_tok < p.tokens && r_head < it.heads && tok < (uint32_t)it.n};
-      };
-      // a row's position is below the last key's by the tokens that follow it
-      const int pos = it.m - (int)((uint32_t)it.n - place().tok);
-      // the keys that this row sees
-      const auto see_lo = [&] { return p.window > 0 ? (int)max(INT64_C(0), min((int64_t)it.m, (int64_t)pos - p.window + 1)) : 0; };
-      const auto see_hi = [&] { return p.causal ? max(0, min((int)it.m, pos + 1)) : (int)it.m; };
-      const float slope = Option && p.slopes != nullptr && place().mine ? __ldg(p.slopes + place().head) : 0.f;
-      float ref = -INFINITY;
-      uint64_t sum2 = 0;
-      for (int j = it.lo[t]; j < it.hi[t]; ++j) {
-        const int buf = kTiles == 2 ? t : (int)(step & 1u);
-        const bool masked = j < it.whole_lo[t] || j >= it.whole_hi[t];
-        wait(&s_full[buf], (kTiles == 2 ? step : step >> 1) & 1u);
-        const uint32_t t_s = tmem + lanes + Z::kS + buf * kKeys + way * kMine;
-        const int key0 = j * kKeys + way * kMine;
-        const auto hide = [&](uint32_t(&s)[32], int c0) {
-          const int from = see_lo() - key0 - c0, to = see_hi() - key0 - c0;
+    while (ok && item_ready()) {
+      const Item &shared = ctl.items[turn];
+      const struct {
+        int q0, k0, n, m, tok0, kv, head0, heads;
+      } it = {shared.q0, shared.k0, shared.n, shared.m, shared.tok0, shared.kv, shared.head0, shared.heads};
+      if (it.n == 0) break;
+      // The row's token, of the sequence (past its end: a row of no use); its position is
+      // below the last key's by the tokens that follow it.
+      const uint32_t tok = (uint32_t)(it.tok0 + t * p.tokens) + (uint32_t)r_tok;
+      const bool mine = r_tok < p.tokens && r_head < it.heads && tok < (uint32_t)it.n;
+      const int pos = it.m - (int)((uint32_t)it.n - tok);
+      // the keys that the row sees
+      const int see_lo = p.window > 0 ? (int)max(INT64_C(0), min((int64_t)it.m, (int64_t)pos - p.window + 1)) : 0;
+      const int see_hi = p.causal ? max(0, min(it.m, pos + 1)) : it.m;
+      const int lo = shared.lo[t], hi = shared.hi[t], whole_lo = shared.whole_lo[t], whole_hi = shared.whole_hi[t];
+      const float slope = Option && p.slopes != nullptr && mine ? __ldg(p.slopes + it.head0 + r_head) : 0.f;
+      // What slopes add from one block to the next.  The reference counts on it, up to
+      // 2^64 (it may then be that much above the scores); where more than 2^128 would
+      // come on top of the last block's, blocks are read twice.
+      const float rise = Option ? fmaxf(slope, 0.f) * (kLog2e * kKeys) : 0.f;
+      const bool steep = Option && __any_sync(0xffffffffu, rise > 128.f);
+      float ref = mine ? -INFINITY : 0.f;
+      float most = -INFINITY;  // of the blocks so far
+      uint64_t sum2[2] = {0, 0};
+      for (int j = lo; j < hi; ++j) {
+        const int buf = kTiles == 2 ? t : (int)(step & 1u), key0 = j * kKeys;
+        const bool masked = j < whole_lo || j >= whole_hi;
+        const uint32_t t_s = tmem + lanes + Z::kS + buf * kKeys;
+        if (!wait(&s_full[buf], (kTiles == 2 ? step : step >> 1) & 1u)) break;
+        uint32_t s[2][32];
+        tmem_ld32(t_s, s[0]);
+        const auto ready = [&](uint32_t(&x)[32], int c0) {
+          if constexpr (Option) option_scores(x, p.scale, p.softcap, slope, key0 + c0 - pos);
+          if (masked) {
+            const int from = see_lo - key0 - c0, to = see_hi - key0 - c0;
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (c < from || c >= to) s[c] = __float_as_uint(-INFINITY);
-        };
-        float top[2] = {-INFINITY, -INFINITY};
-        const auto largest = [&](uint32_t(&s)[32], int c0) {
-          if constexpr (Option) option_scores(s, p.scale, p.softcap, slope, key0 + c0 - pos);
-          if (masked) hide(s, c0);
-#pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            top[0] = max3(top[0], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-            top[1] = max3(top[1], __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+            for (int c = 0; c < 32; ++c)
+              if (c < from || c >= to) x[c] = __float_as_uint(-INFINITY);
           }
         };
-        uint32_t a[32], b[kMine > 32 ? 32 : 1];
-        tmem_ld32(t_s, a);
-        tmem_wait_ld(a);
-        if constexpr (kMine > 32) tmem_ld32(t_s + 32, b);
-        largest(a, 0);
-        if constexpr (kMine > 32) {
-          tmem_wait_ld(b);
-          largest(b, 32);
+        const auto largest = [&](const uint32_t(&x)[32], float top) {
+          float other = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            top = max3(top, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+            other = max3(other, __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
+          }
+          return fmaxf(top, other);
+        };
+        const bool twice = steep || __any_sync(0xffffffffu, ref == -INFINITY);
+        if (twice) {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 32) {
+            if (c > 0) tmem_ld32(t_s + c, s[0]);
+            tmem_wait_ld(s[0]);
+            ready(s[0], c);
+            top = largest(s[0], top);
+          }
+          tmem_ld32(t_s, s[0]);
+          most = top * scale2;
+        } else if (Option) {
+          most += fminf(rise, 64.f);
         }
-        float most = fmaxf(top[0], top[1]) * scale2;
-        tc_fence_before();
-        most = fmaxf(most, other(most));
-        tc_fence_after();
-        if (!ok) break;
         const bool move = most > ref + kMove;
         if (__any_sync(0xffffffffu, move)) {
           const float keep = !move ? 1.f : ref == -INFINITY ? 0.f : exp2_fast(ref - most);
           if (move) ref = most;
-          sum2 = mul_f32x2(sum2, pack_f32x2(keep, keep));
-          if (j > it.lo[t]) {
-            // S of this block is ready, so the products with V up to the one before
-            // last are done (with two tiles the last too)
-            if (kTiles == 1) products_done();
-            // (8 columns at a time: the block's scores are in registers)
+          sum2[0] = mul_f32x2(sum2[0], pack_f32x2(keep, keep));
+          sum2[1] = mul_f32x2(sum2[1], pack_f32x2(keep, keep));
+          if (j > lo) {
+            // with two tiles, the products with V are done up to the last block's: they
+            // came before this block's scores
+            if (kTiles == 1 && !products_done()) break;
+            tmem_wait_ld(s[0]);
 #pragma unroll 1
-            for (int c = 0; c < kOut; c += 8) {
-              uint32_t o[8];
-              tmem_load8(t_o + c, o);
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(t_o + c, o);
+              tmem_wait_ld(o);
 #pragma unroll
-              for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
-              tmem_store8(t_o + c, o);
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
+              tmem_st32(t_o + c, o);
             }
           }
         }
         const float minus = ref == -INFINITY ? 0.f : -ref;
         const uint64_t mul = pack_f32x2(scale2, scale2), add = pack_f32x2(minus, minus);
-        const auto weights = [&](uint32_t(&s)[32], int c0) {
-#pragma unroll
-          for (int g = 0; g < 32; g += 16) {
-            uint32_t w[8];
-#pragma unroll
-            for (int x = 0; x < 16; x += 2) {
-              const uint64_t two = pack_f32x2(__uint_as_float(s[g + x]), __uint_as_float(s[g + x + 1]));
-              const float2 f = unpack_f32x2(Option ? add_f32x2(two, add) : fma_f32x2(two, mul, add));
-              const float p0 = exp2_fast(f.x), p1 = exp2_fast(f.y);
-              sum2 = add_f32x2(sum2, pack_f32x2(p0, p1));
-              w[x / 2] = bf16x2_of(p0, p1);
-            }
-            tmem_st8(tmem + lanes + Z::kS + buf * kKeys + (way * kMine + c0 + g) / 2, w);
-          }
+        // A weight's steps: exponents of 32 scores, then their exp2, between which the
+        // 32 before them are added up, so that the special-function unit always has the
+        // next ones.
+        const auto add_up = [&](uint32_t(&x)[32], int c) {
+          const float p0 = __uint_as_float(x[c]), p1 = __uint_as_float(x[c + 1]);
+          sum2[c / 2 & 1] = add_f32x2(sum2[c / 2 & 1], pack_f32x2(p0, p1));
+          x[c / 2] = bf16x2_of(p0, p1);
         };
-        // the weights lie over scores that both threads have read
-        weights(a, 0);
-        if constexpr (kMine > 32) weights(b, 32);
+        float top = -INFINITY;  // beyond the reference
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          uint32_t(&x)[32] = s[part & 1], (&before)[32] = s[part & 1 ^ 1];
+          tmem_wait_ld(x);
+          ready(x, 32 * part);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const uint64_t two = pack_f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+            const float2 f = unpack_f32x2(Option ? add_f32x2(two, add) : fma_f32x2(two, mul, add));
+            x[c] = __float_as_uint(f.x), x[c + 1] = __float_as_uint(f.y);
+          }
+          top = largest(x, top);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            x[c] = __float_as_uint(exp2_in_order(__uint_as_float(x[c])));
+            x[c + 1] = __float_as_uint(exp2_in_order(__uint_as_float(x[c + 1])));
+            if (part > 0) add_up(before, c);
+          }
+          // (weights lie over scores that have been read)
+          if (part > 0) tmem_st16(t_s + 16 * (part - 1), before);
+          if (part + 1 < kParts) tmem_ld32(t_s + 32 * (part + 1), before);
+        }
+        uint32_t(&x)[32] = s[kParts - 1 & 1];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) add_up(x, c);
+        tmem_st16(t_s + 16 * (kParts - 1), x);
+        most = top - minus;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
         ++step;
       }
-      const bool blocks = it.lo[t] < it.hi[t];
-      if (blocks) products_done();
-      const float2 s2 = unpack_f32x2(sum2);
-      float sum = s2.x + s2.y;
-      sum += other(sum);
-      if (!ok) break;
+      if (!ok || (lo < hi && !products_done())) break;
+      const float2 s0 = unpack_f32x2(sum2[0]), s1 = unpack_f32x2(sum2[1]);
+      const float sum = (s0.x + s0.y) + (s1.x + s1.y);
       const float inv = sum > 0.f || !(sum == sum) ? 1.f / sum : 0.f;
-      const Place at = place();
-      const int64_t out_row = it.q0 + (int64_t)at.tok;
-      __nv_bfloat16 *out = p.out + out_row * p.out_stride + (int64_t)at.head * D + way * kOut;
-      bool odd = false;
+      __nv_bfloat16 *out = p.out + (it.q0 + (int64_t)tok) * p.out_stride + (int64_t)(it.head0 + r_head) * D;
+      bool odd = !(sum <= 3.402823466e38f);
 #pragma unroll
-      for (int c = 0; c < kOut; c += 32) {
+      for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
-        if (blocks) {
+        if (lo < hi) {
           tmem_ld32(t_o + c, o);
           tmem_wait_ld(o);
         }
@@ -695,23 +692,22 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
           odd |= !(fabsf(f) <= 3.402823466e38f && fabsf(g) <= 3.402823466e38f);
           o[x / 2] = bf16x2_of(f, g);
         }
-        if (at.mine) {
+        if (mine) {
 #pragma unroll
           for (int x = 0; x < 16; x += 4) *reinterpret_cast<uint4 *>(out + c + 2 * x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
         }
       }
-      if (at.mine && way == 0 && p.lse != nullptr)
-        p.lse[out_row * p.n_heads + at.head] = inv == 0.f ? -INFINITY : kLn2 * (ref + log2f(sum));
+      if (mine && p.lse != nullptr)
+        p.lse[(it.q0 + (int64_t)tok) * p.n_heads + it.head0 + r_head] = inv == 0.f ? -INFINITY : kLn2 * (ref + log2f(sum));
       __syncwarp();
-      for (uint32_t left = __ballot_sync(0xffffffffu, odd && at.mine); left != 0; left &= left - 1) {
+      for (uint32_t left = __ballot_sync(0xffffffffu, odd && mine); left != 0; left &= left - 1) {
         const int from = __ffs(left) - 1;
-        const int64_t r = __shfl_sync(0xffffffffu, out_row, from);
-        const int r_pos = __shfl_sync(0xffffffffu, pos, from), head = __shfl_sync(0xffffffffu, at.head, from);
-        const int l = __shfl_sync(0xffffffffu, see_lo(), from), h = __shfl_sync(0xffffffffu, see_hi(), from);
+        const int64_t r = it.q0 + (int64_t)__shfl_sync(0xffffffffu, tok, from);
+        const int at = __shfl_sync(0xffffffffu, pos, from), head = it.head0 + __shfl_sync(0xffffffffu, r_head, from);
+        const int l = __shfl_sync(0xffffffffu, see_lo, from), h = __shfl_sync(0xffffffffu, see_hi, from);
         row_again<D>(p, p.q + r * p.q_stride + (int64_t)head * D, p.k + (int64_t)it.k0 * p.k_stride + (int64_t)it.kv * D,
-                     p.v + (int64_t)it.k0 * p.v_stride + (int64_t)it.kv * D, l, h, r_pos, __shfl_sync(0xffffffffu, slope, from),
-                     way * kOut, way * kOut + kOut, p.out + r * p.out_stride + (int64_t)head * D,
-                     p.lse == nullptr || way != 0 ? nullptr : p.lse + r * p.n_heads + head);
+                     p.v + (int64_t)it.k0 * p.v_stride + (int64_t)it.kv * D, l, h, at, __shfl_sync(0xffffffffu, slope, from),
+                     p.out + r * p.out_stride + (int64_t)head * D, p.lse == nullptr ? nullptr : p.lse + r * p.n_heads + head);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&item_empty[turn]);
@@ -759,13 +755,8 @@ cudaError_t launch_d(PrefillArgs a, int sms, cudaStream_t s) {
 template <int D>
 cudaError_t ready_d() {
   for (auto k : {prefill_kernel<D, true>, prefill_kernel<D, false>}) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
     if (e != cudaSuccess) return e;
-    // the softmax warps would wait forever for registers that the launch does not have
-    cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, k);
-    if (e != cudaSuccess) return e;
-    if (Shape<D>::kTiles == 2 && at.numRegs * 5 < kFew + 4 * kMany) return cudaErrorInvalidKernelImage;
   }
   return cudaSuccess;
 }
