@@ -295,11 +295,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     give_up(&stop, p.err);
     return false;
   };
-  const auto item_done = [&] {
-    mbar_arrive(&item_empty[turn]);
-    if (++turn == kAhead) turn = 0, turn_phase ^= 1u;
-  };
-
   if (warp == 0) {
     if (lane == 0) {
       int slot = 0;
@@ -394,118 +389,113 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t i_s = idesc_bf16(128, kKeys, false), i_o = idesc_bf16(128, D, true);
-      int slot = 0, step = 0;  // step: of one tile's S buffers
-      uint32_t phase = 0, q_phase = 0, p_phase = 0;
-      bool ok = true;
-      const auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (ok && !mbar_wait(bar, parity, &stop, kWaitNs)) {
-          give_up(&stop, p.err);
-          ok = false;
-        }
-        return ok;
-      };
-      // Descriptors differ from the first tile's and slot's in their start address
-      // (16-byte units) alone; the asm keeps the compiler from holding all of them in
-      // registers.
-      const uint64_t q_desc = sw128_kmajor_desc(smem_u32(smem)), k_desc = sw128_kmajor_desc(smem_u32(ring)),
-                     v_desc = sw128_rows_k_desc(smem_u32(ring), kKeys * 128);
-      const auto scores = [&](int t, int buf, int s) {  // S[buf] = Q[t] K[slot s]^T
-        uint64_t a = q_desc + (uint64_t)(t * (Z::kQTile / 16)), b = k_desc + (uint64_t)(s * (Z::kSlot / 16));
-        asm volatile("" : "+l"(a), "+l"(b));
+    // The whole warp goes through this in step, one lane issues (see mma_bf16_ss).
+    constexpr uint32_t i_s = idesc_bf16(128, kKeys, false), i_o = idesc_bf16(128, D, true);
+    const uint32_t leader = elect_lane();
+    int slot = 0, step = 0;  // step: of one tile's S buffers
+    uint32_t phase = 0, q_phase = 0, p_phase = 0;
+    bool ok = true;
+    const auto wait = [&](uint64_t *bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &stop, kWaitNs));
+      if (!ok) give_up(&stop, p.err);
+      tc_fence_after();
+      return ok;
+    };
+    // Descriptors differ from the first tile's and slot's in their start address
+    // (16-byte units) alone.
+    const uint64_t q_desc = sw128_kmajor_desc(smem_u32(smem)), k_desc = sw128_kmajor_desc(smem_u32(ring)),
+                   v_desc = sw128_rows_k_desc(smem_u32(ring), kKeys * 128);
+    const auto scores = [&](int t, int buf, int s) {  // S[buf] = Q[t] K[slot s]^T
+      const uint64_t a = q_desc + (uint64_t)(t * (Z::kQTile / 16)), b = k_desc + (uint64_t)(s * (Z::kSlot / 16));
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_bf16_ss(tmem + Z::kS + buf * kKeys, a + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16,
-                      b + ((k >> 2) * (kKeys * 128) + (k & 3) * 32) / 16, i_s, k > 0 ? 1u : 0u);
-        mma_commit(&s_full[buf]);
-      };
-      const auto values = [&](int t, int buf, int s, bool more) {  // O[t] (+)= P[buf] V[slot s]
-        uint64_t b = v_desc + (uint64_t)(s * (Z::kSlot / 16));
-        asm volatile("" : "+l"(b));
+      for (int k = 0; k < D / 16; ++k)
+        mma_bf16_ss(leader, tmem + Z::kS + buf * kKeys, a + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16,
+                    b + ((k >> 2) * (kKeys * 128) + (k & 3) * 32) / 16, i_s, k > 0 ? 1u : 0u);
+      mma_commit_by(leader, &s_full[buf]);
+    };
+    const auto values = [&](int t, int buf, int s, bool more) {  // O[t] (+)= P[buf] V[slot s]
+      const uint64_t b = v_desc + (uint64_t)(s * (Z::kSlot / 16));
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_bf16_ts(tmem + Z::kO + t * D, tmem + Z::kS + buf * kKeys + k * 8, b + k * (2048 / 16), i_o, more || k > 0 ? 1u : 0u);
-        mma_commit(&o_full[buf]);
-      };
-      const auto advance = [&] {
-        mma_commit(&kv_empty[slot]);
-        if (++slot == kSlots) slot = 0, phase ^= 1u;
-      };
-      for (; ok && !stop && item_ready(); item_done()) {
-        const Item &it = ctl.items[turn];
-        if (it.n == 0) break;
-        if (it.last == 0) continue;
-        if constexpr (kTiles == 2) {
-          // block j of the keys has a slot, and is used by both tiles; values likewise
+      for (int k = 0; k < kKeys / 16; ++k)
+        mma_bf16_ts(leader, tmem + Z::kO + t * D, tmem + Z::kS + buf * kKeys + k * 8, b + k * (2048 / 16), i_o, more || k > 0 ? 1u : 0u);
+      mma_commit_by(leader, &o_full[buf]);
+    };
+    const auto release = [&](int s) { mma_commit_by(leader, &kv_empty[s]); };
+    const auto next_slot = [&] {
+      const int s = slot;
+      if (++slot == kSlots) slot = 0, phase ^= 1u;
+      return s;
+    };
+    while (true) {
+      if (!(ok = __all_sync(0xffffffffu, item_ready()))) break;
+      const Item &it = ctl.items[turn];
+      if (uniform(it.n) == 0) break;
+      const int first = uniform(it.first), last = uniform(it.last);
+      if (last == 0) {
+      } else if constexpr (kTiles == 2) {
+        const int lo[2] = {uniform(it.lo[0]), uniform(it.lo[1])}, hi[2] = {uniform(it.hi[0]), uniform(it.hi[1])};
+        // a block of keys has a slot, which both tiles use; of values likewise
+        const auto block_scores = [&](int t, int j, int s) {
+          if (j == lo[t]) {
+            if (!wait(&q_full[t], q_phase >> t & 1u)) return false;
+            q_phase ^= 1u << t;
+          }
+          scores(t, t, s);
+          if (hi[t] == j + 1) mma_commit_by(leader, &q_empty[t]);
+          return true;
+        };
+        if (!wait(&kv_full[slot], phase)) break;
+        int k_slot = next_slot();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (ok && lo[t] < hi[t] && lo[t] == first) block_scores(t, first, k_slot);
+        if (!ok) break;
+        release(k_slot);
+        for (int j = first; j < last; ++j) {
           if (!wait(&kv_full[slot], phase)) break;
-          tc_fence_after();
+          const int v_slot = next_slot();
+          if (j + 1 < last) {
+            if (!wait(&kv_full[slot], phase)) break;
+            k_slot = next_slot();
+          }
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (it.lo[t] < it.hi[t] && it.lo[t] == it.first) {
-              if (!wait(&q_full[t], q_phase >> t & 1u)) break;
-              q_phase ^= 1u << t;
-              tc_fence_after();
-              scores(t, t, slot);
-              if (it.hi[t] == it.first + 1) mma_commit(&q_empty[t]);
+          for (int t = 0; t < 2; ++t) {
+            if (ok && lo[t] <= j && j < hi[t]) {
+              if (wait(&p_full[t], p_phase >> t & 1u)) values(t, t, v_slot, j > lo[t]);
+              p_phase ^= 1u << t;
             }
+            if (ok && lo[t] <= j + 1 && j + 1 < hi[t]) block_scores(t, j + 1, k_slot);
+          }
           if (!ok) break;
-          advance();
-          for (int j = it.first; ok && j < it.last; ++j) {
-            const int v_slot = slot;
-            if (!wait(&kv_full[slot], phase)) break;
-            if (++slot == kSlots) slot = 0, phase ^= 1u;
-            if (j + 1 < it.last && !wait(&kv_full[slot], phase)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (it.lo[t] <= j && j < it.hi[t]) {
-                if (!wait(&p_full[t], p_phase >> t & 1u)) break;
-                p_phase ^= 1u << t;
-                tc_fence_after();
-                values(t, t, v_slot, j > it.lo[t]);
-              }
-              if (it.lo[t] <= j + 1 && j + 1 < it.hi[t]) {
-                if (j + 1 == it.lo[t]) {
-                  if (!wait(&q_full[t], q_phase >> t & 1u)) break;
-                  q_phase ^= 1u << t;
-                  tc_fence_after();
-                }
-                scores(t, t, slot);
-                if (it.hi[t] == j + 2) mma_commit(&q_empty[t]);
-              }
-            }
-            if (!ok) break;
-            mma_commit(&kv_empty[v_slot]);
-            if (j + 1 < it.last) advance();
-          }
-        } else {
-          if (!wait(&q_full[0], q_phase)) break;
-          q_phase ^= 1u;
-          for (int j = it.first; ok && j < it.last && j < it.first + 2; ++j) {
-            if (!wait(&kv_full[slot], phase)) break;
-            tc_fence_after();
-            scores(0, (step + j - it.first) & 1, slot);
-            if (j + 1 == it.last) mma_commit(&q_empty[0]);
-            advance();
-          }
-          for (int j = it.first; ok && j < it.last; ++j, ++step) {
-            const int buf = step & 1;
-            if (!wait(&kv_full[slot], phase) || !wait(&p_full[buf], p_phase >> buf & 1u)) break;
-            p_phase ^= 1u << buf;
-            tc_fence_after();
-            values(0, buf, slot, j > it.first);
-            advance();
-            if (j + 2 < it.last) {
-              if (!wait(&kv_full[slot], phase)) break;
-              tc_fence_after();
-              scores(0, buf, slot);
-              if (j + 3 == it.last) mma_commit(&q_empty[0]);
-              advance();
-            }
-          }
+          release(v_slot);
+          if (j + 1 < last) release(k_slot);
         }
+        if (!ok) break;
+      } else {
+        if (!wait(&q_full[0], q_phase)) break;
+        q_phase ^= 1u;
+        const auto block_scores = [&](int j, int buf) {
+          if (!wait(&kv_full[slot], phase)) return false;
+          const int s = next_slot();
+          scores(0, buf, s);
+          if (j + 1 == last) mma_commit_by(leader, &q_empty[0]);
+          release(s);
+          return true;
+        };
+        for (int j = first; ok && j < last && j < first + 2; ++j) block_scores(j, (step + j - first) & 1);
+        for (int j = first; ok && j < last; ++j, ++step) {
+          const int buf = step & 1;
+          if (!wait(&kv_full[slot], phase) || !wait(&p_full[buf], p_phase >> buf & 1u)) break;
+          p_phase ^= 1u << buf;
+          const int s = next_slot();
+          values(0, buf, s, j > first);
+          release(s);
+          if (j + 2 < last) block_scores(j + 2, buf);
+        }
+        if (!ok) break;
       }
+      if (lane == 0) mbar_arrive(&item_empty[turn]);
+      if (++turn == kAhead) turn = 0, turn_phase ^= 1u;
     }
   } else {
     if (blockIdx.x == 0) {  // the starts are as they should be
