@@ -41,7 +41,7 @@
 // item that has not started (cluster launch control), so no counter in memory is
 // needed and the last items are short.
 //
-// Warps: 0 asks for items and issues TMA, 1 allocates TMEM and issues the products, 2..
+// Warps: 0 issues TMA, 1 allocates TMEM and issues the products, 2 asks for items, 4..
 // are the softmax and output warps, four per tile.
 #include "attn_math.cuh"
 #include "attn_prefill.h"
@@ -64,7 +64,7 @@ struct Shape {
   static constexpr int kChunks = D / 64;           // boxes of 64 elements
   static constexpr int kQTile = 128 * D * 2, kSlot = kKeys * D * 2;
   static constexpr int kSlots = D == 64 ? 8 : 5;
-  static constexpr int kThreads = 64 + 128 * kTiles;
+  static constexpr int kThreads = 128 + 128 * kTiles;
   static constexpr uint32_t kS = 0, kO = 2 * kKeys;  // TMEM columns: two S, then O of each tile
 };
 
@@ -102,24 +102,72 @@ __device__ __forceinline__ int clamp_start(const int32_t *starts, int b, int tot
   return v < 0 ? 0 : v > total ? total : v;
 }
 
-// Item i: the items of a sequence's last tokens, which see most keys, come first.
-// Sequence b owns the places [q_starts[b] / T + b, q_starts[b + 1] / T + b + 1) for
-// its ceil(n / T) tiles of T tokens: found from the starts alone.
+// The tokens of an item.
 template <int D>
-__device__ __forceinline__ bool item_of(const PrefillArgs &p, int64_t i, Item *it) {
-  constexpr int kTiles = Shape<D>::kTiles, kKeys = Shape<D>::kKeys;
-  const int groups = p.n_kv * p.chunks, T = kTiles * p.tokens;
-  const int group = (int)(i % groups), place = (int)(p.items / groups - 1 - i / groups);
+__device__ __forceinline__ int item_tokens(const PrefillArgs &p) {
+  return Shape<D>::kTiles * p.tokens;
+}
+
+// Where the r-th piece of T tokens lies, the longest first: those at the end of a
+// sequence see most keys, so pieces go by their number within the sequence, the largest
+// first, then by sequence.  Up to 32 * kHeld sequences, of which each lane holds kHeld
+// pieces' counts; -1: no such piece.  For the whole warp.
+constexpr int kHeld = 4;
+struct Piece {
+  int b, index;
+};
+__device__ __forceinline__ Piece piece_of(const int (&counts)[kHeld], int r) {
+  const int lane = threadIdx.x & 31;
+  const auto from = [&](int level) {  // pieces of that number and above
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) n += max(0, counts[u] - level);
+    return (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+  };
+  int most = 0;
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) most = max(most, counts[u]);
+  int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
+  if (r >= from(0)) return Piece{-1, 0};
+  while (hi - lo > 1) {  // from(lo) > r >= from(hi)
+    const int mid = (lo + hi) >> 1;
+    if (from(mid) > r) lo = mid;
+    else hi = mid;
+  }
+  int k = r - from(lo + 1), b = -1;  // the k-th sequence with more than lo pieces
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) {
+    const uint32_t have = __ballot_sync(0xffffffffu, counts[u] > lo);
+    const int n = __popc(have);
+    if (b < 0 && k < n) {
+      const bool mine = (have >> lane & 1u) && __popc(have & ((1u << lane) - 1u)) == k;
+      b = 32 * u + __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+    }
+    k -= n;
+  }
+  return Piece{b, lo};
+}
+// The same for any number of sequences, in the order of their rows from the last on:
+// sequence b owns the places [q_starts[b] / T + b, q_starts[b + 1] / T + b + 1) for its
+// ceil(n / T) pieces, found from the starts alone.
+__device__ __forceinline__ Piece piece_at(const PrefillArgs &p, int place, int T) {
   int b = 0;
   for (int end = p.B; end - b > 1;) {
     const int mid = (b + end) >> 1;
     if (clamp_start(p.q_starts, mid, p.Tq) / T + mid <= place) b = mid;
     else end = mid;
   }
+  return Piece{b, place - (clamp_start(p.q_starts, b, p.Tq) / T + b)};
+}
+
+// Piece `index` of sequence b, and a group of heads; false if it has no tokens.
+template <int D>
+__device__ __forceinline__ bool item_of(const PrefillArgs &p, int b, int index, int group, Item *it) {
+  constexpr int kTiles = Shape<D>::kTiles, kKeys = Shape<D>::kKeys;
   const int q0 = clamp_start(p.q_starts, b, p.Tq), q1 = clamp_start(p.q_starts, b + 1, p.Tq);
   const int k0 = clamp_start(p.k_starts, b, p.Tk), k1 = clamp_start(p.k_starts, b + 1, p.Tk);
   const int n = q1 - q0, m = max(k1 - k0, 0);
-  const int64_t tok0 = (int64_t)(place - (q0 / T + b)) * T;
+  const int64_t tok0 = (int64_t)index * item_tokens<D>(p);
   if (tok0 < 0 || tok0 >= n) return false;
   it->q0 = q0;
   it->k0 = k0;
@@ -163,7 +211,7 @@ __device__ __forceinline__ float option_score(float s, float scale, float cap, f
 // The same for 32 neighbouring keys, the first `back` beyond the row's position.
 // Scores within 0.6 of the cap, which nearly all are, take tanh's polynomial two at a
 // time and no special-function instructions; else the warp takes tanh_f32's both ways.
-__device__ __forceinline__ void option_scores(uint32_t (&s)[32], float scale, float cap, float slope, int back) {
+__device__ __forceinline__ void option_scores(uint32_t (&s)[32], float scale, float cap, bool slopes, float slope, int back) {
   if (cap > 0.f) {
     const float unit = __fdividef(scale, cap);
     float most = 0.f;
@@ -187,13 +235,25 @@ __device__ __forceinline__ void option_scores(uint32_t (&s)[32], float scale, fl
 #pragma unroll
       for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(cap * kLog2e * tanh_f32(__uint_as_float(s[c]) * unit));
     }
-    scale = 1.f;
   } else {
-    scale *= kLog2e;
-  }
-  slope *= kLog2e;
+    const uint64_t mul = pack_f32x2(scale * kLog2e, scale * kLog2e);
 #pragma unroll
-  for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(fmaf(__uint_as_float(s[c]), scale, slope * (float)(back + c)));
+    for (int c = 0; c < 32; c += 2) {
+      const float2 f = unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), mul));
+      s[c] = __float_as_uint(f.x), s[c + 1] = __float_as_uint(f.y);
+    }
+  }
+  if (slopes) {
+    // slope * back + slope * c: off by a unit of the largest of the 32 at most
+    const float near = slope * kLog2e, far = near * (float)back;
+    const uint64_t near2 = pack_f32x2(near, near), far2 = pack_f32x2(far, far);
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      const uint64_t bias = fma_f32x2(near2, pack_f32x2((float)c, (float)(c + 1)), far2);
+      const float2 f = unpack_f32x2(add_f32x2(pack_f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), bias));
+      s[c] = __float_as_uint(f.x), s[c + 1] = __float_as_uint(f.y);
+    }
+  }
 }
 
 // One row from its visible keys alone, by a warp: for rows that met values which are
@@ -268,7 +328,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     for (int t = 0; t < kTiles; ++t) mbar_init(&q_full[t], 1), mbar_init(&q_empty[t], 1);
     for (int s = 0; s < kSlots; ++s) mbar_init(&kv_full[s], 1), mbar_init(&kv_empty[s], 1);
     for (int b = 0; b < 2; ++b) mbar_init(&s_full[b], 1), mbar_init(&p_full[b], 4), mbar_init(&o_full[b], 1);
-    for (int b = 0; b < kAhead; ++b) mbar_init(&item_full[b], 1), mbar_init(&item_empty[b], 1 + 4 * kTiles);
+    for (int b = 0; b < kAhead; ++b) mbar_init(&item_full[b], 1), mbar_init(&item_empty[b], 2 + 4 * kTiles);
     mbar_init(&ctl.answered, 1);
     stop = 0;
     fence_mbar_init();
@@ -287,7 +347,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
   pdl_wait();
   pdl_trigger();
 
-  // The items, which warp 0 writes one after another: the other roles take each once.
+  // The items, which warp 2 writes one after another: the other roles take each once.
   int turn = 0;
   uint32_t turn_phase = 0;
   const auto item_ready = [&] {  // false: it gave up
@@ -298,8 +358,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
   if (warp == 0) {
     if (lane == 0) {
       int slot = 0;
-      uint32_t phase = 0, q_phase = 0, answer_phase = 0;  // q_phase: a bit per tile
-      int64_t i = blockIdx.x;
+      uint32_t phase = 0, q_phase = 0;  // q_phase: a bit per tile
       const auto load = [&](const CUtensorMap *map, const Item &it, int block) {
         if (!mbar_wait(&kv_empty[slot], phase ^ 1u, &stop, kWaitNs)) {
           give_up(&stop, p.err);
@@ -313,43 +372,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         return true;
       };
       bool ok = true;
-      while (ok) {
-        ok = mbar_wait(&item_empty[turn], turn_phase ^ 1u, &stop, kWaitNs);
-        if (!ok) {
-          give_up(&stop, p.err);
-          break;
-        }
-        Item &it = ctl.items[turn];
-        // the next place with tokens; the one after is asked for meanwhile
-        bool some = false, asked = false;
-        while (ok && i >= 0 && !some) {
-          if (asked) {
-            ok = mbar_wait(&ctl.answered, answer_phase, &stop, kWaitNs);
-            if (!ok) {
-              give_up(&stop, p.err);
-              break;
-            }
-            answer_phase ^= 1u;
-            i = requested_block(ctl.answer);
-            if (i < 0) break;
-            fence_proxy_async_shared();  // the answer has been read before the next is written
-          }
-          if (p.stride == 0) {
-            mbar_arrive_expect_tx(&ctl.answered, 16);
-            request_block(ctl.answer, &ctl.answered);
-            asked = true;
-          }
-          some = item_of<D>(p, i, &it);
-          if (p.stride > 0) {
-            if (some) break;
-            i = i + p.stride < p.items ? i + p.stride : -1;
-          }
-        }
-        if (!ok) break;
-        if (!some) it.n = 0;
-        mbar_arrive(&item_full[turn]);
-        if (++turn == kAhead) turn = 0, turn_phase ^= 1u;
-        if (!some) break;
+      while (ok && item_ready()) {
+        const Item &it = ctl.items[turn];
+        if (it.n == 0) break;
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
           if (it.lo[t] >= it.hi[t]) continue;
@@ -374,18 +399,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
           if (ok && ahead < it.last) ok = load(&tk, it, ahead);
         }
         if (!ok) break;
-        if (p.stride > 0) {
-          i = i + p.stride < p.items ? i + p.stride : -1;
-        } else {
-          ok = mbar_wait(&ctl.answered, answer_phase, &stop, kWaitNs);
-          if (!ok) {
-            give_up(&stop, p.err);
-            break;
-          }
-          answer_phase ^= 1u;
-          i = requested_block(ctl.answer);
-          fence_proxy_async_shared();
-        }
+        mbar_arrive(&item_empty[turn]);
+        if (++turn == kAhead) turn = 0, turn_phase ^= 1u;
       }
     }
   } else if (warp == 1) {
@@ -497,10 +512,61 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
       if (lane == 0) mbar_arrive(&item_empty[turn]);
       if (++turn == kAhead) turn = 0, turn_phase ^= 1u;
     }
-  } else {
+  } else if (warp == 2) {
+    const int groups = p.n_kv * p.chunks, T = item_tokens<D>(p);
+    int counts[kHeld];
+    const bool held = p.B <= 32 * kHeld;
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const int b = 32 * u + lane;
+      counts[u] = held && b < p.B ? max(0, clamp_start(p.q_starts, b + 1, p.Tq) - clamp_start(p.q_starts, b, p.Tq) + T - 1) / T : 0;
+    }
+    int64_t i = blockIdx.x;
+    uint32_t answer_phase = 0;
+    bool ok = true, first = true;
+    while (ok) {
+      // An item is asked for once there is room to keep it: those that are kept for
+      // longer could be another block's.
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&item_empty[turn], turn_phase ^ 1u, &stop, kWaitNs)))) break;
+      Item &it = ctl.items[turn];
+      bool some = false;
+      while (ok && !some) {
+        if (!first) {
+          if (p.stride > 0) {
+            i = i + p.stride < p.items ? i + p.stride : -1;
+          } else {
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&ctl.answered, 16);
+              request_block(ctl.answer, &ctl.answered);
+            }
+            __syncwarp();
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.answered, answer_phase, &stop, kWaitNs)))) break;
+            answer_phase ^= 1u;
+            i = requested_block(ctl.answer);
+            __syncwarp();
+            if (lane == 0) fence_proxy_async_shared();  // the answer has been read before the next is written
+          }
+        }
+        first = false;
+        if (i < 0) break;
+        const int r = (int)(i / groups), group = (int)(i % groups);
+        const Piece at = held ? piece_of(counts, r) : piece_at(p, (int)(p.items / groups) - 1 - r, T);
+        some = at.b >= 0 && __shfl_sync(0xffffffffu, lane == 0 && item_of<D>(p, at.b, at.index, group, &it), 0);
+      }
+      if (!ok) break;
+      if (lane == 0) {
+        if (!some) it.n = 0;
+        mbar_arrive(&item_full[turn]);
+      }
+      __syncwarp();
+      if (!some) break;
+      if (++turn == kAhead) turn = 0, turn_phase ^= 1u;
+    }
+    if (!ok) give_up(&stop, p.err);
+  } else if (warp >= 4) {
     if (blockIdx.x == 0) {  // the starts are as they should be
       bool bad = false;
-      for (int b = threadIdx.x - 64; b <= p.B; b += Z::kThreads - 64) {
+      for (int b = threadIdx.x - 128; b <= p.B; b += Z::kThreads - 128) {
         const int qs = __ldg(p.q_starts + b), ks = __ldg(p.k_starts + b);
         bad |= qs < 0 || qs > p.Tq || ks < 0 || ks > p.Tk;
         if (b < p.B) bad |= __ldg(p.q_starts + b + 1) < qs || __ldg(p.k_starts + b + 1) < ks;
@@ -509,7 +575,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
       __syncwarp();
     }
     constexpr int kParts = kKeys / 32;
-    const int t = (warp - 2) >> 2;
+    const int t = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int row = (warp & 3) * 32 + lane;  // of the tile
     const uint32_t t_o = tmem + lanes + Z::kO + t * D;
@@ -565,7 +631,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         uint32_t s[2][32];
         tmem_ld32(t_s, s[0]);
         const auto ready = [&](uint32_t(&x)[32], int c0) {
-          if constexpr (Option) option_scores(x, p.scale, p.softcap, slope, key0 + c0 - pos);
+          if constexpr (Option) option_scores(x, p.scale, p.softcap, p.slopes != nullptr, slope, key0 + c0 - pos);
           if (masked) {
             const int from = see_lo - key0 - c0, to = see_hi - key0 - c0;
 #pragma unroll
