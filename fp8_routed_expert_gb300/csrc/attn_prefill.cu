@@ -55,6 +55,7 @@ using namespace sm100;
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kStage = 32 * 128;  // bytes in which a warp turns 64 columns of its 32 rows of outputs
 constexpr float kMove = 8.f;  // log2 of how far a score may exceed the reference
 
 template <int D>
@@ -63,7 +64,7 @@ struct Shape {
   static constexpr int kKeys = D == 256 ? 64 : 128;
   static constexpr int kChunks = D / 64;           // boxes of 64 elements
   static constexpr int kQTile = 128 * D * 2, kSlot = kKeys * D * 2;
-  static constexpr int kSlots = D == 64 ? 8 : 5;
+  static constexpr int kSlots = D == 64 ? 8 : 4;
   static constexpr int kThreads = 128 + 128 * kTiles;
   static constexpr uint32_t kS = 0, kO = 2 * kKeys;  // TMEM columns: two S, then O of each tile
 };
@@ -94,7 +95,7 @@ struct Control {
 };
 template <int D>
 constexpr size_t smem_bytes() {
-  return (size_t)Shape<D>::kTiles * Shape<D>::kQTile + (size_t)Shape<D>::kSlots * Shape<D>::kSlot + sizeof(Control<D>);
+  return (size_t)Shape<D>::kTiles * (Shape<D>::kQTile + 4 * kStage) + (size_t)Shape<D>::kSlots * Shape<D>::kSlot + sizeof(Control<D>);
 }
 
 __device__ __forceinline__ int clamp_start(const int32_t *starts, int b, int total) {
@@ -314,10 +315,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
                                                              const __grid_constant__ CUtensorMap tv, const PrefillArgs p) {
   using Z = Shape<D>;
   constexpr int kTiles = Z::kTiles, kKeys = Z::kKeys, kSlots = Z::kSlots;
-  extern __shared__ __align__(1024) uint8_t smem[];  // query tiles, key and value slots, control
+  extern __shared__ __align__(1024) uint8_t smem[];  // query tiles, key and value slots, stages, control
   uint8_t *ring = smem + kTiles * Z::kQTile;
   using Ctl = Control<D>;
-  Ctl &ctl = *reinterpret_cast<Ctl *>(ring + kSlots * Z::kSlot);
+  uint8_t *stages = ring + kSlots * Z::kSlot;
+  Ctl &ctl = *reinterpret_cast<Ctl *>(stages + 4 * kTiles * kStage);
   auto &q_full = ctl.q_full, &q_empty = ctl.q_empty;
   auto &kv_full = ctl.kv_full, &kv_empty = ctl.kv_empty;
   auto &s_full = ctl.s_full, &p_full = ctl.p_full, &o_full = ctl.o_full;
@@ -650,6 +652,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         };
         const bool twice = steep || __any_sync(0xffffffffu, ref == -INFINITY);
         if (twice) {
+          // all of the block where it is steep, else as far as each row has seen a key:
+          // the reference need not be the largest score
           float top = -INFINITY;
 #pragma unroll 1
           for (int c = 0; c < kKeys; c += 32) {
@@ -657,6 +661,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
             tmem_wait_ld(s[0]);
             ready(s[0], c);
             top = largest(s[0], top);
+            if (!steep && !__any_sync(0xffffffffu, top == -INFINITY)) break;
           }
           tmem_ld32(t_s, s[0]);
           most = top * scale2;
@@ -665,10 +670,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         }
         const bool move = most > ref + kMove;
         if (__any_sync(0xffffffffu, move)) {
-          const float keep = !move ? 1.f : ref == -INFINITY ? 0.f : exp2_fast(ref - most);
+          // in two factors: what a weight of up to 2^127 leaves may have to come down by more
+          // than the smallest factor
+          const float keep = !move ? 1.f : ref == -INFINITY ? 0.f : exp2_fast(0.5f * (ref - most));
+          const uint64_t keep2 = pack_f32x2(keep, keep);
           if (move) ref = most;
-          sum2[0] = mul_f32x2(sum2[0], pack_f32x2(keep, keep));
-          sum2[1] = mul_f32x2(sum2[1], pack_f32x2(keep, keep));
+          sum2[0] = mul_f32x2(mul_f32x2(sum2[0], keep2), keep2);
+          sum2[1] = mul_f32x2(mul_f32x2(sum2[1], keep2), keep2);
           if (j > lo) {
             // with two tiles, the products with V are done up to the last block's: they
             // came before this block's scores
@@ -680,7 +688,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
               tmem_ld32(t_o + c, o);
               tmem_wait_ld(o);
 #pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep * keep);
               tmem_st32(t_o + c, o);
             }
           }
@@ -733,36 +741,60 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
       const float2 s0 = unpack_f32x2(sum2[0]), s1 = unpack_f32x2(sum2[1]);
       const float sum = (s0.x + s0.y) + (s1.x + s1.y);
       const float inv = sum > 0.f || !(sum == sum) ? 1.f / sum : 0.f;
-      __nv_bfloat16 *out = p.out + (it.q0 + (int64_t)tok) * p.out_stride + (int64_t)(it.head0 + r_head) * D;
-      bool odd = !(sum <= 3.402823466e38f);
+      // A thread's row of outputs is written by eight lanes, 16 bytes each, so that four
+      // rows of 128 bytes leave at a time: through the warp's stage, where the 16-byte
+      // pieces of a row are exchanged by its number (a row per lane took five times as
+      // long, 32 lines per instruction).
+      const int64_t out_at = mine ? (it.q0 + (int64_t)tok) * p.out_stride + (int64_t)(it.head0 + r_head) * D : -1;
+      int64_t at[8];  // of the rows that this lane writes pieces of
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        if (lo < hi) {
-          tmem_ld32(t_o + c, o);
-          tmem_wait_ld(o);
-        }
+      for (int r = 0; r < 8; ++r) at[r] = __shfl_sync(0xffffffffu, out_at, 4 * r + (lane >> 3));
+      const uint64_t inv2 = pack_f32x2(inv, inv);
+      uint64_t odd2 = 0;  // outputs times zero: NaN where one is not finite
+      uint8_t *stage = stages + (warp - 4) * kStage;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 64) {
 #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          const float f = inv == 0.f ? 0.f : __uint_as_float(o[x]) * inv, g = inv == 0.f ? 0.f : __uint_as_float(o[x + 1]) * inv;
-          odd |= !(fabsf(f) <= 3.402823466e38f && fabsf(g) <= 3.402823466e38f);
-          o[x / 2] = bf16x2_of(f, g);
-        }
-        if (mine) {
+        for (int h = 0; h < 2; ++h) {
+          uint32_t o[32];
+          if (lo < hi) {
+            tmem_ld32(t_o + c + 32 * h, o);
+            tmem_wait_ld(o);
+          } else {
 #pragma unroll
-          for (int x = 0; x < 16; x += 4) *reinterpret_cast<uint4 *>(out + c + 2 * x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+            for (int x = 0; x < 32; ++x) o[x] = 0;
+          }
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const uint64_t two = mul_f32x2(pack_f32x2(__uint_as_float(o[x]), __uint_as_float(o[x + 1])), inv2);
+            odd2 = fma_f32x2(two, 0, odd2);
+            const float2 f = unpack_f32x2(two);
+            o[x / 2] = bf16x2_of(f.x, f.y);
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((4 * h + x) ^ (lane & 7)) * 16) =
+                make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(stage + (4 * r + (lane >> 3)) * 128 + ((lane & 7) ^ (4 * r + (lane >> 3) & 7)) * 16);
+          if (at[r] >= 0) *reinterpret_cast<uint4 *>(p.out + at[r] + c + 8 * (lane & 7)) = v;
+        }
+        __syncwarp();
       }
       if (mine && p.lse != nullptr)
         p.lse[(it.q0 + (int64_t)tok) * p.n_heads + it.head0 + r_head] = inv == 0.f ? -INFINITY : kLn2 * (ref + log2f(sum));
       __syncwarp();
-      for (uint32_t left = __ballot_sync(0xffffffffu, odd && mine); left != 0; left &= left - 1) {
+      const float2 odd = unpack_f32x2(odd2);
+      for (uint32_t left = __ballot_sync(0xffffffffu, mine && !(odd.x == 0.f && odd.y == 0.f && sum <= 3.402823466e38f)); left != 0; left &= left - 1) {
         const int from = __ffs(left) - 1;
         const int64_t r = it.q0 + (int64_t)__shfl_sync(0xffffffffu, tok, from);
-        const int at = __shfl_sync(0xffffffffu, pos, from), head = it.head0 + __shfl_sync(0xffffffffu, r_head, from);
+        const int r_pos = __shfl_sync(0xffffffffu, pos, from), head = it.head0 + __shfl_sync(0xffffffffu, r_head, from);
         const int l = __shfl_sync(0xffffffffu, see_lo, from), h = __shfl_sync(0xffffffffu, see_hi, from);
         row_again<D>(p, p.q + r * p.q_stride + (int64_t)head * D, p.k + (int64_t)it.k0 * p.k_stride + (int64_t)it.kv * D,
-                     p.v + (int64_t)it.k0 * p.v_stride + (int64_t)it.kv * D, l, h, at, __shfl_sync(0xffffffffu, slope, from),
+                     p.v + (int64_t)it.k0 * p.v_stride + (int64_t)it.kv * D, l, h, r_pos, __shfl_sync(0xffffffffu, slope, from),
                      p.out + r * p.out_stride + (int64_t)head * D, p.lse == nullptr ? nullptr : p.lse + r * p.n_heads + head);
       }
       __syncwarp();
