@@ -41,11 +41,13 @@ struct MatmulArgs {
   int blocks;   // ceil(K / 128)
   int64_t tiles;
   int splits;  // CTAs of a cluster, which share a tile's K blocks
+  int stages;  // blocks of operands in flight
   int a_rows;  // rows of an activation box
   int *err;
 };
-// Columns of a tile, and CTAs that share it.
+// Columns of a tile, CTAs that share it, and their stages.
 void split_matmul(int64_t M, int64_t N, int64_t K, int sms, int *columns, int *splits);
+int matmul_stages(int64_t M, int columns, int splits);
 cudaError_t launch_matmul(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, int columns, int sms,
                           cudaStream_t s);
 cudaError_t ready_matmul();

@@ -170,6 +170,7 @@ int moe_proj_matmul(moe_proj *p, const uint8_t *a, int64_t a_stride, const float
   MatmulArgs m{};
   int columns = 0;
   split_matmul(M, N, K, p->sms, &columns, &m.splits);
+  m.stages = matmul_stages(M, columns, m.splits);
   m.M = M;
   m.N = N;
   m.K = K;

@@ -10,10 +10,12 @@
 // product of the two scales, to f32 registers while the other buffer fills: lane =
 // row, so a thread's scale is one number per block (and 128 columns).
 //
-// A tile's K blocks may be split over the CTAs of a cluster (few tiles): each
-// leaves its sums in its shared memory, and every CTA adds a share of the tile over
-// all of them, in rank order.  Nothing is added in order of arrival, and no call
-// needs a workspace.
+// A tile's K blocks may be split over the CTAs of a cluster (few tiles): row r belongs
+// to CTA r modulo their number, each pushes its sums of the others' rows into their
+// shared memory, and behind one cluster barrier a CTA adds its rows over all of them, in
+// rank order.  (Sums left in place and read by the others took two barriers and reads
+// that wait: 333 x 1000 x 2880 in six parts 15000 cycles.)  Nothing is added in order of
+// arrival, and no call needs a workspace.
 //
 // Warps: 0 issues TMA, 1 allocates TMEM and issues the products, 2..9 add up.
 #include "common.cuh"
@@ -28,12 +30,18 @@ namespace {
 constexpr int kRows = 128, kBlock = 128, kSumWarps = 8, kThreads = 64 + 32 * kSumWarps;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
+constexpr int kMostStages = 8, kRing = 196608;  // bytes of stages, and of the sums of a cluster
+
 template <int Columns>
 struct Ring {
   static constexpr int kA = kRows * kBlock, kStage = kA + Columns * kBlock;
-  static constexpr int kStages = 196608 / kStage;
-  static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+  static constexpr size_t kSmem = kRing + 1024;
 };
+// Bytes that a cluster's sums take in each CTA: of its rows, from each of the others.
+__host__ __device__ __forceinline__ int sums_bytes(int64_t M, int columns, int splits) {
+  const int rows = M < kRows ? (int)M : kRows;
+  return splits > 1 ? (rows + splits - 1) / splits * splits * columns * 4 : 0;
+}
 
 struct Item {
   int64_t m0, n0;
@@ -75,13 +83,14 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   using R = Ring<Columns>;
   constexpr int kHalf = Columns / 2;  // columns of a summing warp
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[R::kStages], empty[R::kStages], sum_full[2], sum_empty[2];
+  __shared__ __align__(8) uint64_t full[kMostStages], empty[kMostStages], sum_full[2], sum_empty[2];
   __shared__ uint32_t tmem_sh;
   __shared__ volatile int stop;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages = p.stages;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < R::kStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
     for (int b = 0; b < 2; ++b) mbar_init(&sum_full[b], 1), mbar_init(&sum_empty[b], kSumWarps);
     stop = 0;
     fence_mbar_init();
@@ -116,34 +125,37 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
           mbar_arrive_expect_tx(&full[stage], (uint32_t)(p.a_rows + Columns) * kBlock);
           tma_load_2d(s, &ta, b * kBlock, (int32_t)it.m0, &full[stage]);
           tma_load_2d(s + R::kA, &tw, b * kBlock, (int32_t)it.n0, &full[stage]);
-          if (++stage == R::kStages) stage = 0, phase ^= 1u;
+          if (++stage == stages) stage = 0, phase ^= 1u;
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(kRows, Columns);
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, bphase = 0;
-      for (int64_t tile = first; tile < p.tiles && !stop; tile += step) {
-        const Item it = item_of<Columns>(p, tile, rank);
-        for (int b = it.b0; b < it.b1; ++b) {
-          if (!mbar_wait(&sum_empty[buf], bphase ^ 1u, &stop, kWaitNs) || !mbar_wait(&full[stage], phase, &stop, kWaitNs)) {
-            give_up(&stop, p.err);
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a = smem_u32(smem + (size_t)stage * R::kStage);
+    // the whole warp in step, one lane issues (see mma_e4m3_ss)
+    constexpr uint32_t idesc = idesc_e4m3_f32(kRows, Columns);
+    const uint32_t leader = elect_lane();
+    const uint64_t desc = sw128_kmajor_desc(smem_u32(smem));
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, bphase = 0;
+    bool ok = true;
+    const auto wait = [&](uint64_t *bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &stop, kWaitNs));
+      if (!ok) give_up(&stop, p.err);
+      return ok;
+    };
+    for (int64_t tile = first; ok && tile < p.tiles; tile += step) {
+      const Item it = item_of<Columns>(p, tile, rank);
+      for (int b = it.b0; b < it.b1; ++b) {
+        if (!wait(&sum_empty[buf], bphase ^ 1u) || !wait(&full[stage], phase)) break;
+        tc_fence_after();
+        const uint64_t a = desc + (uint64_t)(stage * (R::kStage / 16));
 #pragma unroll
-          for (int k = 0; k < kBlock / 32; ++k)
-            mma_f8f6f4(tmem + (uint32_t)(buf * Columns), sw128_kmajor_desc(a + k * 32), sw128_kmajor_desc(a + R::kA + k * 32), idesc,
-                       k > 0 ? 1u : 0u);
-          mma_commit(&empty[stage]);
-          mma_commit(&sum_full[buf]);
-          if (++stage == R::kStages) stage = 0, phase ^= 1u;
-          buf ^= 1;
-          if (buf == 0) bphase ^= 1u;
-        }
+        for (int k = 0; k < kBlock / 32; ++k)
+          mma_e4m3_ss(leader, tmem + (uint32_t)(buf * Columns), a + k * 2, a + (R::kA / 16 + k * 2), idesc, k > 0 ? 1u : 0u);
+        mma_commit_by(leader, &empty[stage]);
+        mma_commit_by(leader, &sum_full[buf]);
+        if (++stage == stages) stage = 0, phase ^= 1u;
+        buf ^= 1;
+        if (buf == 0) bphase ^= 1u;
       }
     }
   } else {
@@ -206,14 +218,17 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
           if (col + j < p.N) store8(p, row, col + j, v);
         }
       } else {
-        // [128][Columns] f32, the 16-byte pieces of a row exchanged by its number
-        // so that a warp's rows do not meet in one bank
-        float *mine = reinterpret_cast<float *>(smem) + (quarter * 32 + lane) * Columns;
+        // to the row's CTA: [rank][row / splits][Columns] f32, the 16-byte pieces of a
+        // row exchanged by its number so that a warp's rows do not meet in one bank
+        const int r = quarter * 32 + lane, owner = r % p.splits, at = r / p.splits;
+        const uint32_t base = smem_u32(smem + kRing - sums_bytes(p.M, Columns, p.splits));
+        const int held = sums_bytes(p.M, Columns, p.splits) / (p.splits * Columns * 4);
+        const uint32_t mine = map_to_rank(base + (uint32_t)((rank * held + at) * Columns * 4), (uint32_t)owner);
 #pragma unroll
         for (int j = 0; j < kHalf; j += 4) {
           const float2 f = unpack_f32x2(acc[j / 2]), g = unpack_f32x2(acc[j / 2 + 1]);
-          const int piece = (half * kHalf + j) / 4 ^ (lane & (Columns / 4 - 1));
-          *reinterpret_cast<float4 *>(mine + 4 * piece) = make_float4(f.x, f.y, g.x, g.y);
+          const int piece = (half * kHalf + j) / 4 ^ (at & (Columns / 4 - 1));
+          st_cluster16(mine + 16 * piece, f.x, f.y, g.x, g.y);
         }
       }
     }
@@ -221,23 +236,24 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   __syncwarp();
   if (p.splits > 1) {
     cluster_sync_all();
+    // a lane adds 8 columns of a row of this CTA's
     const Item it = item_of<Columns>(p, first, rank);
     const int rows = (int)(p.M - it.m0 < kRows ? p.M - it.m0 : kRows);
-    const uint32_t base = smem_u32(smem);
-    // unit u: 8 columns of a row
-    for (int u = rank + p.splits * threadIdx.x; u < rows * (Columns / 8); u += p.splits * kThreads) {
-      const int r = u / (Columns / 8), c = u % (Columns / 8) * 2;
-      if (it.n0 + 4 * c >= p.N) continue;
-      const int swap = r & 31 & (Columns / 4 - 1);
-      const uint32_t at0 = base + (uint32_t)(r * Columns + 4 * (c ^ swap)) * 4, at1 = base + (uint32_t)(r * Columns + 4 * (c + 1 ^ swap)) * 4;
+    const int held = sums_bytes(p.M, Columns, p.splits) / (p.splits * Columns * 4);
+    const float4 *sums = reinterpret_cast<const float4 *>(smem + kRing - sums_bytes(p.M, Columns, p.splits));
+    for (int u = threadIdx.x; u < held * (Columns / 8); u += kThreads) {
+      const int at = u / (Columns / 8), c = u % (Columns / 8) * 2, r = at * p.splits + rank;
+      if (r >= rows || it.n0 + 4 * c >= p.N) continue;
+      const int swap = at & (Columns / 4 - 1);
       float v[8] = {};
+#pragma unroll 2
       for (int q = 0; q < p.splits; ++q) {
-        const float4 f = ld_cluster16(map_to_rank(at0, (uint32_t)q)), g = ld_cluster16(map_to_rank(at1, (uint32_t)q));
+        const float4 *row = sums + (q * held + at) * (Columns / 4);
+        const float4 f = row[c ^ swap], g = row[c + 1 ^ swap];
         v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w, v[4] += g.x, v[5] += g.y, v[6] += g.z, v[7] += g.w;
       }
       store8(p, it.m0 + r, it.n0 + 4 * c, v);
     }
-    cluster_sync_all();  // no CTA leaves while its sums are read
   }
   __syncthreads();
   if (stop) {
@@ -277,6 +293,11 @@ cudaError_t ready_columns() {
 }
 
 }  // namespace
+
+int matmul_stages(int64_t M, int columns, int splits) {
+  const int n = (kRing - sums_bytes(M, columns, splits)) / (kRows * kBlock + columns * kBlock);
+  return n < kMostStages ? n : kMostStages;
+}
 
 void split_matmul(int64_t M, int64_t N, int64_t K, int sms, int *columns, int *splits) {
   const int64_t rows = (M + kRows - 1) / kRows, blocks = (K + kBlock - 1) / kBlock;
