@@ -38,6 +38,7 @@ struct MatmulArgs {
   const float *w_scale;  // [ceil(N / 128)][ceil(K / 128)]
   __nv_bfloat16 *out;
   int64_t out_stride;
+  bool whole_lines;  // rows of out begin 32-byte aligned
   int blocks;   // ceil(K / 128)
   int64_t tiles;
   int splits;  // CTAs of a cluster, which share a tile's K blocks

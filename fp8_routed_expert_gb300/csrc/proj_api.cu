@@ -180,6 +180,7 @@ int moe_proj_matmul(moe_proj *p, const uint8_t *a, int64_t a_stride, const float
   m.w_scale = w_scale;
   m.out = static_cast<__nv_bfloat16 *>(out);
   m.out_stride = out_stride;
+  m.whole_lines = aligned(out, 32) && out_stride % 16 == 0;
   m.blocks = (int)((K + 127) / 128);
   m.tiles = (M + 127) / 128 * ((N + columns - 1) / columns);
   m.a_rows = M < 128 ? (int)((M + 7) / 8 * 8) : 128;

@@ -6,7 +6,7 @@
 // Tile: 128 rows x Columns columns, K in steps of one block.  TMA brings 128-byte
 // rows of both operands (zeros outside the matrices, so any M, N and K), the
 // 128-byte swizzle is what tcgen05.mma kind::f8f6f4 reads, and a block's sum lands
-// in one of two TMEM buffers.  Eight warps take it from there and add it, times the
+// in one of two TMEM buffers.  The other warps take it from there and add it, times the
 // product of the two scales, to f32 registers while the other buffer fills: lane =
 // row, so a thread's scale is one number per block (and 128 columns).
 //
@@ -17,7 +17,8 @@
 // that wait: 333 x 1000 x 2880 in six parts 15000 cycles.)  Nothing is added in order of
 // arrival, and no call needs a workspace.
 //
-// Warps: 0 issues TMA, 1 allocates TMEM and issues the products, 2..9 add up.
+// Warps: 0 issues TMA, 1 allocates TMEM and issues the products, 2 copies the scales, 4..
+// add up.
 #include "common.cuh"
 #include "kernels.h"
 #include "proj.h"
@@ -27,15 +28,20 @@ namespace fp8moe {
 using namespace sm100;
 namespace {
 
-constexpr int kRows = 128, kBlock = 128, kSumWarps = 8, kThreads = 64 + 32 * kSumWarps;
+constexpr int kRows = 128, kBlock = 128;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
+// A block's scales are copied when its operands are; kHeld blocks on, the block of that
+// place has long been added up (at most kMostStages and the two TMEM buffers lie between).
+constexpr int kHeld = 16, kScales = kRows + 2;
 constexpr int kMostStages = 8, kRing = 196608;  // bytes of stages, and of the sums of a cluster
 
 template <int Columns>
 struct Ring {
+  static constexpr int kGroups = 2, kSumWarps = 4 * kGroups, kThreads = 128 + 32 * kSumWarps;
   static constexpr int kA = kRows * kBlock, kStage = kA + Columns * kBlock;
-  static constexpr size_t kSmem = kRing + 1024;
+  // the scales of kHeld blocks: 128 of rows, two of weights
+  static constexpr size_t kSmem = kRing + kHeld * kScales * 4 + 1024;
 };
 // Bytes that a cluster's sums take in each CTA: of its rows, from each of the others.
 __host__ __device__ __forceinline__ int sums_bytes(int64_t M, int columns, int splits) {
@@ -44,7 +50,7 @@ __host__ __device__ __forceinline__ int sums_bytes(int64_t M, int columns, int s
 }
 
 struct Item {
-  int64_t m0, n0;
+  int m0, n0;
   int b0, b1;  // K blocks
 };
 
@@ -52,8 +58,8 @@ template <int Columns>
 __device__ __forceinline__ Item item_of(const MatmulArgs &p, int64_t tile, int rank) {
   const int64_t m_tiles = (p.M + kRows - 1) / kRows;
   Item it;
-  it.m0 = tile % m_tiles * kRows;
-  it.n0 = tile / m_tiles * Columns;
+  it.m0 = (int)(tile % m_tiles * kRows);
+  it.n0 = (int)(tile / m_tiles * Columns);
   it.b0 = (int)((int64_t)p.blocks * rank / p.splits);
   it.b1 = (int)((int64_t)p.blocks * (rank + 1) / p.splits);
   return it;
@@ -78,20 +84,21 @@ __device__ __forceinline__ void store8(const MatmulArgs &p, int64_t row, int64_t
 }
 
 template <int Columns>
-__global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_constant__ CUtensorMap ta,
+__global__ void __launch_bounds__(Ring<Columns>::kThreads, 1) matmul_kernel(const __grid_constant__ CUtensorMap ta,
                                                              const __grid_constant__ CUtensorMap tw, const MatmulArgs p) {
   using R = Ring<Columns>;
-  constexpr int kHalf = Columns / 2;  // columns of a summing warp
+  constexpr int kMine = Columns / R::kGroups;  // columns of a summing warp
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kMostStages], empty[kMostStages], sum_full[2], sum_empty[2];
   __shared__ uint32_t tmem_sh;
   __shared__ volatile int stop;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float *scales = reinterpret_cast<float *>(smem + kRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stages = p.stages;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
-    for (int b = 0; b < 2; ++b) mbar_init(&sum_full[b], 1), mbar_init(&sum_empty[b], kSumWarps);
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1 + 32), mbar_init(&empty[s], 1);
+    for (int b = 0; b < 2; ++b) mbar_init(&sum_full[b], 1), mbar_init(&sum_empty[b], R::kSumWarps);
     stop = 0;
     fence_mbar_init();
     prefetch_tmap(&ta);
@@ -123,8 +130,8 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
           }
           uint8_t *s = smem + (size_t)stage * R::kStage;
           mbar_arrive_expect_tx(&full[stage], (uint32_t)(p.a_rows + Columns) * kBlock);
-          tma_load_2d(s, &ta, b * kBlock, (int32_t)it.m0, &full[stage]);
-          tma_load_2d(s + R::kA, &tw, b * kBlock, (int32_t)it.n0, &full[stage]);
+          tma_load_2d(s, &ta, b * kBlock, it.m0, &full[stage]);
+          tma_load_2d(s + R::kA, &tw, b * kBlock, it.n0, &full[stage]);
           if (++stage == stages) stage = 0, phase ^= 1u;
         }
       }
@@ -158,32 +165,47 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         if (buf == 0) bphase ^= 1u;
       }
     }
-  } else {
-    const int quarter = warp & 3, half = (warp - 2) >> 2;  // TMEM lanes and columns of this warp
-    const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * kHalf);
+  } else if (warp == 2) {
     const int n_blocks = (int)((p.N + 127) / 128);
+    int stage = 0;
+    uint32_t phase = 0, count = 0;
+    bool ok = true;
+    for (int64_t tile = first; ok && tile < p.tiles; tile += step) {
+      const Item it = item_of<Columns>(p, tile, rank);
+      const float *sa[4], *sw = p.w_scale + (int64_t)min((int)(it.n0 / 128) + (lane & 1), n_blocks - 1) * p.blocks;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t row = it.m0 + 32 * i + lane;
+        sa[i] = p.a_scale + (row < p.M ? row : p.M - 1) * p.a_row;
+      }
+      for (int b = it.b0; b < it.b1; ++b, ++count) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, &stop, kWaitNs));
+        if (!ok) {
+          give_up(&stop, p.err);
+          break;
+        }
+        float *to = scales + (count & (kHeld - 1)) * kScales;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) copy4(to + 32 * i + lane, sa[i] + b * p.a_block);
+        if (lane < 2) copy4(to + kRows + lane, sw + b);
+        copies_arrive(&full[stage]);
+        if (++stage == stages) stage = 0, phase ^= 1u;
+      }
+    }
+  } else if (warp >= 4) {
+    const int quarter = warp & 3, group = (warp - 4) >> 2;  // TMEM lanes and columns of this warp
+    const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(group * kMine);
+    uint32_t count = 0;
     int buf = 0;
     uint32_t bphase = 0;
     bool ok = true;
     for (int64_t tile = first; ok && tile < p.tiles; tile += step) {
       const Item it = item_of<Columns>(p, tile, rank);
-      const int64_t row = it.m0 + quarter * 32 + lane, col = it.n0 + half * kHalf;
-      const bool any = it.m0 + quarter * 32 < p.M && col < p.N;  // of the warp
-      const float *sa = p.a_scale + (row < p.M ? row : p.M - 1) * p.a_row;
-      const int nb = (int)(col / 128);
-      const float *sw = p.w_scale + (int64_t)(nb < n_blocks ? nb : n_blocks - 1) * p.blocks;
-      uint64_t acc[kHalf / 2];
+      const bool any = it.m0 + quarter * 32 < p.M && it.n0 + group * kMine < p.N;  // of the warp
+      uint64_t acc[kMine / 2];
 #pragma unroll
-      for (int j = 0; j < kHalf / 2; ++j) acc[j] = 0;
-      // the next block's scales are loaded while this one is added
-      float sa_next = it.b0 < it.b1 ? __ldg(sa + it.b0 * p.a_block) : 0.f, sw_next = it.b0 < it.b1 ? __ldg(sw + it.b0) : 0.f;
-      for (int b = it.b0; b < it.b1; ++b) {
-        const float c = sa_next * sw_next;
-        const uint64_t cc = pack_f32x2(c, c);
-        if (b + 1 < it.b1) {
-          sa_next = __ldg(sa + (b + 1) * p.a_block);
-          sw_next = __ldg(sw + b + 1);
-        }
+      for (int j = 0; j < kMine / 2; ++j) acc[j] = 0;
+      for (int b = it.b0; b < it.b1; ++b, ++count) {
         if (!mbar_wait(&sum_full[buf], bphase, &stop, kWaitNs)) {
           give_up(&stop, p.err);
           ok = false;
@@ -191,12 +213,19 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         }
         tc_fence_after();
         if (any) {
+          // (the products were of operands that came with these scales)
+          const float *sc = scales + (count & (kHeld - 1)) * kScales;
+          const float c = sc[quarter * 32 + lane] * sc[kRows + group * kMine / 128];
+          const uint64_t cc = pack_f32x2(c, c);
+          const uint32_t from = t_lane + (uint32_t)(buf * Columns);
 #pragma unroll
-          for (int ch = 0; ch < kHalf / 16; ++ch) {
-            float v[16];
-            tmem_ld_32x32b_x16(t_lane + (uint32_t)(buf * Columns + ch * 16), v);
+          for (int l = 0; l < kMine; l += 16) {
+            uint32_t v[16];
+            tmem_ld16(from + l, v);
+            tmem_wait_ld16(v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[ch * 8 + j] = fma_f32x2(pack_f32x2(v[2 * j], v[2 * j + 1]), cc, acc[ch * 8 + j]);
+            for (int j = 0; j < 16; j += 2)
+              acc[(l + j) / 2] = fma_f32x2(pack_f32x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), cc, acc[(l + j) / 2]);
           }
         }
         tc_fence_before();
@@ -205,29 +234,49 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         buf ^= 1;
         if (buf == 0) bphase ^= 1u;
       }
+      // the coordinates again, rather than held in registers through the blocks
+      int64_t again = tile;
+      asm volatile("" : "+l"(again));
+      const Item at = item_of<Columns>(p, again, rank);
+      const int64_t row = at.m0 + quarter * 32 + lane, col = at.n0 + group * kMine;
       if (!ok || !any || row >= p.M) continue;
       if (p.splits == 1) {
+        __nv_bfloat16 *out = p.out + row * p.out_stride + col;
+        // 32 bytes at a time where they lie in one line: half as many line accesses
+        if (p.whole_lines && col + kMine <= p.N) {
 #pragma unroll
-        for (int j = 0; j < kHalf; j += 8) {
-          float v[8];
+          for (int j = 0; j < kMine; j += 16) {
+            uint32_t w[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack_f32x2(acc[j / 2 + i]);
-            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+            for (int i = 0; i < 8; ++i) {
+              const float2 f = unpack_f32x2(acc[j / 2 + i]);
+              w[i] = bf16x2_of(f.x, f.y);
+            }
+            st_global32(out + j, w);
           }
-          if (col + j < p.N) store8(p, row, col + j, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kMine; j += 8) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = unpack_f32x2(acc[j / 2 + i]);
+              v[2 * i] = f.x, v[2 * i + 1] = f.y;
+            }
+            if (col + j < p.N) store8(p, row, col + j, v);
+          }
         }
       } else {
         // to the row's CTA: [rank][row / splits][Columns] f32, the 16-byte pieces of a
         // row exchanged by its number so that a warp's rows do not meet in one bank
-        const int r = quarter * 32 + lane, owner = r % p.splits, at = r / p.splits;
+        const int r = quarter * 32 + lane, owner = r % p.splits, place = r / p.splits;
         const uint32_t base = smem_u32(smem + kRing - sums_bytes(p.M, Columns, p.splits));
         const int held = sums_bytes(p.M, Columns, p.splits) / (p.splits * Columns * 4);
-        const uint32_t mine = map_to_rank(base + (uint32_t)((rank * held + at) * Columns * 4), (uint32_t)owner);
+        const uint32_t mine = map_to_rank(base + (uint32_t)((rank * held + place) * Columns * 4), (uint32_t)owner);
 #pragma unroll
-        for (int j = 0; j < kHalf; j += 4) {
+        for (int j = 0; j < kMine; j += 4) {
           const float2 f = unpack_f32x2(acc[j / 2]), g = unpack_f32x2(acc[j / 2 + 1]);
-          const int piece = (half * kHalf + j) / 4 ^ (at & (Columns / 4 - 1));
+          const int piece = (group * kMine + j) / 4 ^ (place & (Columns / 4 - 1));
           st_cluster16(mine + 16 * piece, f.x, f.y, g.x, g.y);
         }
       }
@@ -241,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     const int rows = (int)(p.M - it.m0 < kRows ? p.M - it.m0 : kRows);
     const int held = sums_bytes(p.M, Columns, p.splits) / (p.splits * Columns * 4);
     const float4 *sums = reinterpret_cast<const float4 *>(smem + kRing - sums_bytes(p.M, Columns, p.splits));
-    for (int u = threadIdx.x; u < held * (Columns / 8); u += kThreads) {
+    for (int u = threadIdx.x; u < held * (Columns / 8); u += R::kThreads) {
       const int at = u / (Columns / 8), c = u % (Columns / 8) * 2, r = at * p.splits + rank;
       if (r >= rows || it.n0 + 4 * c >= p.N) continue;
       const int swap = at & (Columns / 4 - 1);
@@ -273,7 +322,7 @@ template <int Columns>
 cudaError_t launch_columns(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, int sms, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(m.splits > 1 ? m.tiles * m.splits : m.tiles < sms ? m.tiles : sms));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Ring<Columns>::kThreads);
   cfg.dynamicSmemBytes = Ring<Columns>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
