@@ -39,18 +39,24 @@ struct MatmulArgs {
   __nv_bfloat16 *out;
   int64_t out_stride;
   bool whole_lines;  // rows of out begin 32-byte aligned
-  int blocks;   // ceil(K / 128)
-  int64_t tiles;
-  int splits;  // CTAs of a cluster, which share a tile's K blocks
-  int stages;  // blocks of operands in flight
-  int a_rows;  // rows of an activation box
+  int blocks;  // ceil(K / 128)
   int *err;
+  // plan_matmul's:
+  bool few;                       // at most 32 rows
+  int columns, splits;            // of a tile; CTAs of a cluster, which share its K blocks
+  int64_t tiles, grid;
+  int a_rows, a_bytes;            // of an activation box, and what it has of a stage
+  int held;                       // rows that a CTA of a cluster adds up
+  int stages, sums_at, scales_at, smem;  // blocks in flight; bytes into shared memory, and all of it
 };
-// Columns of a tile, CTAs that share it, and their stages.
-void split_matmul(int64_t M, int64_t N, int64_t K, int sms, int *columns, int *splits);
-int matmul_stages(int64_t M, int columns, int splits);
-cudaError_t launch_matmul(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, int columns, int sms,
-                          cudaStream_t s);
-cudaError_t ready_matmul();
+constexpr int kMostSplits = 8;
+// Resident clusters of 1, 2, ... CTAs for tiles of 64, 128 and 256 columns.
+struct MatmulFit {
+  int few[2][kMostSplits + 1], many[3][kMostSplits + 1];
+};
+cudaError_t ready_matmul(MatmulFit *fit);
+// Fills in the plan for M, N, K (blocks) on at most `sms` SMs.
+void plan_matmul(const MatmulFit &fit, int sms, MatmulArgs *m);
+cudaError_t launch_matmul(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, cudaStream_t s);
 
 }  // namespace fp8moe

@@ -12,6 +12,7 @@ using namespace fp8moe;
 
 struct moe_proj {
   int device = 0, sms = 0;
+  MatmulFit fit{};
   int *err = nullptr;
   cudaStream_t last_stream = nullptr;
 };
@@ -65,10 +66,12 @@ int moe_proj_init(moe_proj **out, int32_t device, int32_t max_sms) {
   PROJ_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device));
   PROJ_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device));
   if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
-  PROJ_TRY(ready_matmul());
+  MatmulFit fit{};
+  PROJ_TRY(ready_matmul(&fit));
   moe_proj *p = new (std::nothrow) moe_proj();
   if (p == nullptr) return MOE_ERR_NOMEM;
   p->device = device;
+  p->fit = fit;
   p->sms = max_sms > 0 && max_sms < sms ? max_sms : sms;
   if (cudaMalloc(&p->err, 256) != cudaSuccess) {
     cudaGetLastError();
@@ -168,9 +171,6 @@ int moe_proj_matmul(moe_proj *p, const uint8_t *a, int64_t a_stride, const float
   CHECK(check_scales(a_scale, scale_row_stride, scale_block_stride));
   CHECK(check_scales(w_scale, 1, 1));
   MatmulArgs m{};
-  int columns = 0;
-  split_matmul(M, N, K, p->sms, &columns, &m.splits);
-  m.stages = matmul_stages(M, columns, m.splits);
   m.M = M;
   m.N = N;
   m.K = K;
@@ -182,19 +182,18 @@ int moe_proj_matmul(moe_proj *p, const uint8_t *a, int64_t a_stride, const float
   m.out_stride = out_stride;
   m.whole_lines = aligned(out, 32) && out_stride % 16 == 0;
   m.blocks = (int)((K + 127) / 128);
-  m.tiles = (M + 127) / 128 * ((N + columns - 1) / columns);
-  m.a_rows = M < 128 ? (int)((M + 7) / 8 * 8) : 128;
   m.err = p->err;
+  plan_matmul(p->fit, p->sms, &m);
   CUtensorMap ta, tw;
   const uint64_t a_sizes[2] = {(uint64_t)K, (uint64_t)M}, a_strides[1] = {(uint64_t)a_stride};
   const uint64_t w_sizes[2] = {(uint64_t)K, (uint64_t)N}, w_strides[1] = {(uint64_t)w_stride};
-  const uint32_t a_box[2] = {128, (uint32_t)m.a_rows}, w_box[2] = {128, (uint32_t)columns};
+  const uint32_t a_box[2] = {128, (uint32_t)m.a_rows}, w_box[2] = {128, (uint32_t)m.columns};
   PROJ_TRY(cudaSetDevice(p->device));
   if (!encode_tile_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a, a_sizes, a_strides, a_box) ||
       !encode_tile_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, w, w_sizes, w_strides, w_box))
     return MOE_ERR_CUDA;
   p->last_stream = s;
-  PROJ_TRY(launch_matmul(ta, tw, m, columns, p->sms, s));
+  PROJ_TRY(launch_matmul(ta, tw, m, s));
   return MOE_OK;
 }
 

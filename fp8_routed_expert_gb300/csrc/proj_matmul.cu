@@ -10,8 +10,8 @@
 // product of the two scales, to f32 registers while the other buffer fills: lane =
 // row, so a thread's scale is one number per block (and 128 columns).
 //
-// A tile's K blocks may be split over the CTAs of a cluster (few tiles): row r belongs
-// to CTA r modulo their number, each pushes its sums of the others' rows into their
+// A tile's K blocks may be split over the CTAs of a cluster (few tiles): each CTA
+// owns as many rows, and each pushes its sums of the others' rows into their
 // shared memory, and behind one cluster barrier a CTA adds its rows over all of them, in
 // rank order.  (Sums left in place and read by the others took two barriers and reads
 // that wait: 333 x 1000 x 2880 in six parts 15000 cycles.)  Nothing is added in order of
@@ -34,20 +34,13 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // A block's scales are copied when its operands are; kHeld blocks on, the block of that
 // place has long been added up (at most kMostStages and the two TMEM buffers lie between).
 constexpr int kHeld = 16, kScales = kRows + 2;
-constexpr int kMostStages = 8, kRing = 196608;  // bytes of stages, and of the sums of a cluster
+constexpr int kMostStages = 8;
 
-template <int Columns>
+// Few: at most 32 rows, which one warp adds up, so that two CTAs fit on an SM.
+template <int Columns, bool Few>
 struct Ring {
-  static constexpr int kGroups = 2, kSumWarps = 4 * kGroups, kThreads = 128 + 32 * kSumWarps;
-  static constexpr int kA = kRows * kBlock, kStage = kA + Columns * kBlock;
-  // the scales of kHeld blocks: 128 of rows, two of weights
-  static constexpr size_t kSmem = kRing + kHeld * kScales * 4 + 1024;
+  static constexpr int kGroups = Few ? 1 : 2, kSumWarps = Few ? 1 : 8, kThreads = 128 + 32 * kSumWarps;
 };
-// Bytes that a cluster's sums take in each CTA: of its rows, from each of the others.
-__host__ __device__ __forceinline__ int sums_bytes(int64_t M, int columns, int splits) {
-  const int rows = M < kRows ? (int)M : kRows;
-  return splits > 1 ? (rows + splits - 1) / splits * splits * columns * 4 : 0;
-}
 
 struct Item {
   int m0, n0;
@@ -60,8 +53,8 @@ __device__ __forceinline__ Item item_of(const MatmulArgs &p, int64_t tile, int r
   Item it;
   it.m0 = (int)(tile % m_tiles * kRows);
   it.n0 = (int)(tile / m_tiles * Columns);
-  it.b0 = (int)((int64_t)p.blocks * rank / p.splits);
-  it.b1 = (int)((int64_t)p.blocks * (rank + 1) / p.splits);
+  it.b0 = Columns == 256 ? 0 : (int)((int64_t)p.blocks * rank / p.splits);
+  it.b1 = Columns == 256 ? p.blocks : (int)((int64_t)p.blocks * (rank + 1) / p.splits);
   return it;
 }
 
@@ -83,17 +76,21 @@ __device__ __forceinline__ void store8(const MatmulArgs &p, int64_t row, int64_t
   }
 }
 
-template <int Columns>
-__global__ void __launch_bounds__(Ring<Columns>::kThreads, 1) matmul_kernel(const __grid_constant__ CUtensorMap ta,
+template <int Columns, bool Few>
+__global__ void __launch_bounds__(Ring<Columns, Few>::kThreads, Few ? 2 : 1) matmul_kernel(const __grid_constant__ CUtensorMap ta,
                                                              const __grid_constant__ CUtensorMap tw, const MatmulArgs p) {
-  using R = Ring<Columns>;
+  using R = Ring<Columns, Few>;
   constexpr int kMine = Columns / R::kGroups;  // columns of a summing warp
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kMostStages], empty[kMostStages], sum_full[2], sum_empty[2];
   __shared__ uint32_t tmem_sh;
   __shared__ volatile int stop;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float *scales = reinterpret_cast<float *>(smem + kRing);
+  // stages, what a product of the last one may read behind it, a cluster's sums, and the
+  // scales of kHeld blocks: 128 of rows, two of weights
+  const int a_bytes = Few ? p.a_bytes : kRows * kBlock, stage_bytes = a_bytes + Columns * kBlock;
+  const float4 *sums = reinterpret_cast<const float4 *>(smem + p.sums_at);
+  float *scales = reinterpret_cast<float *>(smem + p.scales_at);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stages = p.stages;
   if (threadIdx.x == 0) {
@@ -114,8 +111,9 @@ __global__ void __launch_bounds__(Ring<Columns>::kThreads, 1) matmul_kernel(cons
   const uint32_t tmem = tmem_sh;
   pdl_wait();
   pdl_trigger();
-  const int rank = p.splits > 1 ? (int)cluster_rank() : 0;
-  const int64_t first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
+  const int splits = Columns == 256 ? 1 : p.splits;  // (tiles of 256 columns are many)
+  const int rank = splits > 1 ? (int)cluster_rank() : 0;
+  const int64_t first = blockIdx.x / splits, step = gridDim.x / splits;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -128,10 +126,10 @@ __global__ void __launch_bounds__(Ring<Columns>::kThreads, 1) matmul_kernel(cons
             give_up(&stop, p.err);
             break;
           }
-          uint8_t *s = smem + (size_t)stage * R::kStage;
+          uint8_t *s = smem + (size_t)stage * stage_bytes;
           mbar_arrive_expect_tx(&full[stage], (uint32_t)(p.a_rows + Columns) * kBlock);
           tma_load_2d(s, &ta, b * kBlock, it.m0, &full[stage]);
-          tma_load_2d(s + R::kA, &tw, b * kBlock, it.n0, &full[stage]);
+          tma_load_2d(s + a_bytes, &tw, b * kBlock, it.n0, &full[stage]);
           if (++stage == stages) stage = 0, phase ^= 1u;
         }
       }
@@ -154,10 +152,10 @@ __global__ void __launch_bounds__(Ring<Columns>::kThreads, 1) matmul_kernel(cons
       for (int b = it.b0; b < it.b1; ++b) {
         if (!wait(&sum_empty[buf], bphase ^ 1u) || !wait(&full[stage], phase)) break;
         tc_fence_after();
-        const uint64_t a = desc + (uint64_t)(stage * (R::kStage / 16));
+        const uint64_t a = desc + (uint64_t)(stage * (stage_bytes / 16)), w = a + (uint64_t)(a_bytes / 16);
 #pragma unroll
         for (int k = 0; k < kBlock / 32; ++k)
-          mma_e4m3_ss(leader, tmem + (uint32_t)(buf * Columns), a + k * 2, a + (R::kA / 16 + k * 2), idesc, k > 0 ? 1u : 0u);
+          mma_e4m3_ss(leader, tmem + (uint32_t)(buf * Columns), a + k * 2, w + k * 2, idesc, k > 0 ? 1u : 0u);
         mma_commit_by(leader, &empty[stage]);
         mma_commit_by(leader, &sum_full[buf]);
         if (++stage == stages) stage = 0, phase ^= 1u;
@@ -186,7 +184,7 @@ __global__ void __launch_bounds__(Ring<Columns>::kThreads, 1) matmul_kernel(cons
         }
         float *to = scales + (count & (kHeld - 1)) * kScales;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) copy4(to + 32 * i + lane, sa[i] + b * p.a_block);
+        for (int i = 0; i < (Few ? 1 : 4); ++i) copy4(to + 32 * i + lane, sa[i] + b * p.a_block);
         if (lane < 2) copy4(to + kRows + lane, sw + b);
         copies_arrive(&full[stage]);
         if (++stage == stages) stage = 0, phase ^= 1u;
@@ -240,7 +238,7 @@ __global__ void __launch_bounds__(Ring<Columns>::kThreads, 1) matmul_kernel(cons
       const Item at = item_of<Columns>(p, again, rank);
       const int64_t row = at.m0 + quarter * 32 + lane, col = at.n0 + group * kMine;
       if (!ok || !any || row >= p.M) continue;
-      if (p.splits == 1) {
+      if (splits == 1) {
         __nv_bfloat16 *out = p.out + row * p.out_stride + col;
         // 32 bytes at a time where they lie in one line: half as many line accesses
         if (p.whole_lines && col + kMine <= p.N) {
@@ -267,12 +265,10 @@ __global__ void __launch_bounds__(Ring<Columns>::kThreads, 1) matmul_kernel(cons
           }
         }
       } else {
-        // to the row's CTA: [rank][row / splits][Columns] f32, the 16-byte pieces of a
+        // to the row's CTA: [rank][row % held][Columns] f32, the 16-byte pieces of a
         // row exchanged by its number so that a warp's rows do not meet in one bank
-        const int r = quarter * 32 + lane, owner = r % p.splits, place = r / p.splits;
-        const uint32_t base = smem_u32(smem + kRing - sums_bytes(p.M, Columns, p.splits));
-        const int held = sums_bytes(p.M, Columns, p.splits) / (p.splits * Columns * 4);
-        const uint32_t mine = map_to_rank(base + (uint32_t)((rank * held + place) * Columns * 4), (uint32_t)owner);
+        const int r = quarter * 32 + lane, owner = r / p.held, place = r - owner * p.held;
+        const uint32_t mine = map_to_rank(smem_u32(sums + (rank * p.held + place) * (Columns / 4)), (uint32_t)owner);
 #pragma unroll
         for (int j = 0; j < kMine; j += 4) {
           const float2 f = unpack_f32x2(acc[j / 2]), g = unpack_f32x2(acc[j / 2 + 1]);
@@ -283,21 +279,19 @@ __global__ void __launch_bounds__(Ring<Columns>::kThreads, 1) matmul_kernel(cons
     }
   }
   __syncwarp();
-  if (p.splits > 1) {
+  if (splits > 1) {
     cluster_sync_all();
     // a lane adds 8 columns of a row of this CTA's
     const Item it = item_of<Columns>(p, first, rank);
     const int rows = (int)(p.M - it.m0 < kRows ? p.M - it.m0 : kRows);
-    const int held = sums_bytes(p.M, Columns, p.splits) / (p.splits * Columns * 4);
-    const float4 *sums = reinterpret_cast<const float4 *>(smem + kRing - sums_bytes(p.M, Columns, p.splits));
-    for (int u = threadIdx.x; u < held * (Columns / 8); u += R::kThreads) {
-      const int at = u / (Columns / 8), c = u % (Columns / 8) * 2, r = at * p.splits + rank;
+    for (int u = threadIdx.x; u < p.held * (Columns / 8); u += R::kThreads) {
+      const int at = u / (Columns / 8), c = u % (Columns / 8) * 2, r = rank * p.held + at;
       if (r >= rows || it.n0 + 4 * c >= p.N) continue;
       const int swap = at & (Columns / 4 - 1);
       float v[8] = {};
 #pragma unroll 2
-      for (int q = 0; q < p.splits; ++q) {
-        const float4 *row = sums + (q * held + at) * (Columns / 4);
+      for (int q = 0; q < splits; ++q) {
+        const float4 *row = sums + (q * p.held + at) * (Columns / 4);
         const float4 f = row[c ^ swap], g = row[c + 1 ^ swap];
         v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w, v[4] += g.x, v[5] += g.y, v[6] += g.z, v[7] += g.w;
       }
@@ -318,12 +312,12 @@ __global__ void __launch_bounds__(Ring<Columns>::kThreads, 1) matmul_kernel(cons
   }
 }
 
-template <int Columns>
-cudaError_t launch_columns(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, int sms, cudaStream_t s) {
+template <int Columns, bool Few>
+cudaError_t launch_one(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(m.splits > 1 ? m.tiles * m.splits : m.tiles < sms ? m.tiles : sms));
-  cfg.blockDim = dim3(Ring<Columns>::kThreads);
-  cfg.dynamicSmemBytes = Ring<Columns>::kSmem;
+  cfg.gridDim = dim3((unsigned)m.grid);
+  cfg.blockDim = dim3(Ring<Columns, Few>::kThreads);
+  cfg.dynamicSmemBytes = (size_t)m.smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -333,46 +327,95 @@ cudaError_t launch_columns(const CUtensorMap &a, const CUtensorMap &w, const Mat
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = m.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, matmul_kernel<Columns>, a, w, m);
+  return cudaLaunchKernelEx(&cfg, matmul_kernel<Columns, Few>, a, w, m);
 }
 
-template <int Columns>
-cudaError_t ready_columns() {
-  return cudaFuncSetAttribute(matmul_kernel<Columns>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Ring<Columns>::kSmem);
+// Shared memory of a CTA where one or two of them have an SM.
+constexpr int kOnePerSm = 226 * 1024, kTwoPerSm = 112 * 1024, kAround = kHeld * kScales * 4 + 1024;
+
+template <int Columns, bool Few>
+cudaError_t ready_one(int (&fit)[kMostSplits + 1]) {
+  constexpr int kSmem = Few ? kTwoPerSm : kOnePerSm;
+  const auto kernel = matmul_kernel<Columns, Few>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  for (int c = 1; e == cudaSuccess && c <= kMostSplits; ++c) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c);
+    cfg.blockDim = dim3(Ring<Columns, Few>::kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&fit[c], kernel, &cfg);
+  }
+  return e;
 }
 
 }  // namespace
 
-int matmul_stages(int64_t M, int columns, int splits) {
-  const int n = (kRing - sums_bytes(M, columns, splits)) / (kRows * kBlock + columns * kBlock);
-  return n < kMostStages ? n : kMostStages;
-}
-
-void split_matmul(int64_t M, int64_t N, int64_t K, int sms, int *columns, int *splits) {
-  const int64_t rows = (M + kRows - 1) / kRows, blocks = (K + kBlock - 1) / kBlock;
-  const auto tiles = [&](int c) { return rows * ((N + c - 1) / c); };
-  *splits = 1;
-  if (tiles(256) >= sms) {
-    *columns = 256;
-    return;
-  }
-  *columns = tiles(128) * 8 >= sms ? 128 : 64;
-  const int64_t room = sms / tiles(*columns);
-  *splits = (int)(room < 1 ? 1 : room > 8 ? 8 : room);
-  if (*splits > blocks) *splits = (int)(blocks < 1 ? 1 : blocks);
-}
-
-cudaError_t ready_matmul() {
-  for (cudaError_t e : {ready_columns<64>(), ready_columns<128>(), ready_columns<256>()})
+cudaError_t ready_matmul(MatmulFit *fit) {
+  for (cudaError_t e : {ready_one<64, true>(fit->few[0]), ready_one<128, true>(fit->few[1]), ready_one<64, false>(fit->many[0]),
+                        ready_one<128, false>(fit->many[1]), ready_one<256, false>(fit->many[2])})
     if (e != cudaSuccess) return e;
   return cudaSuccess;
 }
 
-cudaError_t launch_matmul(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, int columns, int sms, cudaStream_t s) {
-  switch (columns) {
-    case 64: return launch_columns<64>(a, w, m, sms, s);
-    case 128: return launch_columns<128>(a, w, m, sms, s);
-    default: return launch_columns<256>(a, w, m, sms, s);
+// How a product is split.  A tile's K blocks go over as many CTAs as are resident
+// together (clusters that come in a second round double the time: 48 clusters of three
+// on 46 places, 1 x 6144 x 2048, 11.3 us, 96 of three on 97 places TODO us).  The time is
+// about, in cycles of a CTA: a block 420, 560 and 1040 for 64, 128 and 256 columns, a
+// tile's start and end 3000, a cluster's exchange 2000 and what it pushes at 32 bytes.
+void plan_matmul(const MatmulFit &fit, int sms, MatmulArgs *m) {
+  const bool few = m->M <= 32;
+  const int64_t rows = (m->M + kRows - 1) / kRows;
+  double best = 0.0;
+  m->columns = 0;
+  for (int i = 0; i < (few ? 2 : 3); ++i) {
+    const int columns = 64 << i;
+    const int64_t tiles = rows * ((m->N + columns - 1) / columns);
+    const int *places = few ? fit.few[i] : fit.many[i];
+    for (int splits = 1; splits <= kMostSplits && splits <= m->blocks; ++splits) {
+      const int64_t most = (int64_t)sms * (few ? 2 : 1) / splits, resident = places[splits] < most ? places[splits] : most;
+      if (splits > 1 && (tiles > resident || columns == 256)) continue;
+      const double rounds = (double)((tiles + resident - 1) / (resident > 0 ? resident : 1));
+      const double block = columns == 64 ? 420.0 : columns == 128 ? 560.0 : 1040.0;
+      double t = rounds * ((double)((m->blocks + splits - 1) / splits) * block + 3000.0);
+      if (splits > 1) t += 2000.0 + (double)(m->M < kRows ? m->M : kRows) * columns * 4 * (splits - 1) / splits / 32.0;
+      if (m->columns == 0 || t < best) {
+        best = t;
+        m->columns = columns;
+        m->splits = splits;
+        m->tiles = tiles;
+        m->grid = splits > 1 ? tiles * splits : tiles < resident ? tiles : resident;
+      }
+    }
+  }
+  m->few = few;
+  m->a_rows = m->M < kRows ? (int)((m->M + 7) / 8 * 8) : kRows;
+  m->a_bytes = few ? m->a_rows * kBlock : kRows * kBlock;  // whole 8-row atoms of 1024 bytes
+  const int sum_rows = m->M < kRows ? (int)m->M : kRows;
+  m->held = (sum_rows + m->splits - 1) / m->splits;
+  const int sums = m->splits > 1 ? m->held * m->splits * m->columns * 4 : 0;
+  const int stage = m->a_bytes + m->columns * kBlock;
+  // a product reads 128 rows of either operand: those behind the last stage's few rows are
+  // of no use, but have to be there
+  const int behind = stage < kRows * kBlock ? kRows * kBlock - stage : 0;
+  const int room = (few ? kTwoPerSm : kOnePerSm) - kAround - sums - behind;
+  m->stages = room / stage < kMostStages ? room / stage : kMostStages;
+  m->sums_at = m->stages * stage + behind;
+  m->scales_at = m->sums_at + sums;
+  m->smem = m->scales_at + kAround;
+}
+
+cudaError_t launch_matmul(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, cudaStream_t s) {
+  if (m.few) return m.columns == 64 ? launch_one<64, true>(a, w, m, s) : launch_one<128, true>(a, w, m, s);
+  switch (m.columns) {
+    case 64: return launch_one<64, false>(a, w, m, s);
+    case 128: return launch_one<128, false>(a, w, m, s);
+    default: return launch_one<256, false>(a, w, m, s);
   }
 }
 
