@@ -209,51 +209,30 @@ __device__ __forceinline__ float option_score(float s, float scale, float cap, f
   return fmaf(slope, (float)back, s) * kLog2e;
 }
 
-// The same for 32 neighbouring keys, the first `back` beyond the row's position.
-// Scores within 0.6 of the cap, which nearly all are, take tanh's polynomial two at a
-// time and no special-function instructions; else the warp takes tanh_f32's both ways.
-__device__ __forceinline__ void option_scores(uint32_t (&s)[32], float scale, float cap, bool slopes, float slope, int back) {
-  if (cap > 0.f) {
-    const float unit = __fdividef(scale, cap);
-    float most = 0.f;
+// tanh(s * unit) of 32 scores.  Where all are below 0.6, which nearly all are, by the
+// polynomial, two at a time and without special-function instructions; else the warp
+// takes tanh_f32's both ways.
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[32], float unit) {
+  float most = 0.f;
 #pragma unroll
-    for (int c = 0; c < 32; c += 2)
-      most = max3(most, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
-    const uint64_t u2 = pack_f32x2(unit, unit), cap2 = pack_f32x2(cap * kLog2e, cap * kLog2e);
-    if (__all_sync(0xffffffffu, most * fabsf(unit) < 0.6f)) {
-      const auto both = [](float f) { return pack_f32x2(f, f); };
+  for (int c = 0; c < 32; c += 2)
+    most = max3(most, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
+  if (__all_sync(0xffffffffu, most * fabsf(unit) < 0.6f)) {
+    const uint64_t u2 = pack_f32x2(unit, unit);
+    const auto both = [](float f) { return pack_f32x2(f, f); };
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        const uint64_t y = mul_f32x2(pack_f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), u2), z = mul_f32x2(y, y);
-        uint64_t t = fma_f32x2(z, both(kTanh[4]), both(kTanh[3]));
-        t = fma_f32x2(z, t, both(kTanh[2]));
-        t = fma_f32x2(z, t, both(kTanh[1]));
-        t = fma_f32x2(z, t, both(kTanh[0]));
-        const float2 f = unpack_f32x2(mul_f32x2(fma_f32x2(mul_f32x2(y, z), t, y), cap2));
-        s[c] = __float_as_uint(f.x), s[c + 1] = __float_as_uint(f.y);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(cap * kLog2e * tanh_f32(__uint_as_float(s[c]) * unit));
+    for (int c = 0; c < 32; c += 2) {
+      const uint64_t y = mul_f32x2(pack_f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), u2), z = mul_f32x2(y, y);
+      uint64_t t = fma_f32x2(z, both(kTanh[4]), both(kTanh[3]));
+      t = fma_f32x2(z, t, both(kTanh[2]));
+      t = fma_f32x2(z, t, both(kTanh[1]));
+      t = fma_f32x2(z, t, both(kTanh[0]));
+      const float2 f = unpack_f32x2(fma_f32x2(mul_f32x2(y, z), t, y));
+      s[c] = __float_as_uint(f.x), s[c + 1] = __float_as_uint(f.y);
     }
   } else {
-    const uint64_t mul = pack_f32x2(scale * kLog2e, scale * kLog2e);
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const float2 f = unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), mul));
-      s[c] = __float_as_uint(f.x), s[c + 1] = __float_as_uint(f.y);
-    }
-  }
-  if (slopes) {
-    // slope * back + slope * c: off by a unit of the largest of the 32 at most
-    const float near = slope * kLog2e, far = near * (float)back;
-    const uint64_t near2 = pack_f32x2(near, near), far2 = pack_f32x2(far, far);
-#pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const uint64_t bias = fma_f32x2(near2, pack_f32x2((float)c, (float)(c + 1)), far2);
-      const float2 f = unpack_f32x2(add_f32x2(pack_f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), bias));
-      s[c] = __float_as_uint(f.x), s[c + 1] = __float_as_uint(f.y);
-    }
+    for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(tanh_f32(__uint_as_float(s[c]) * unit));
   }
 }
 
@@ -582,7 +561,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     const int row = (warp & 3) * 32 + lane;  // of the tile
     const uint32_t t_o = tmem + lanes + Z::kO + t * D;
     const int r_tok = row / p.heads, r_head = row - r_tok * p.heads;
-    const float scale2 = Option ? 1.f : p.scale * kLog2e;
+    const bool capped = Option && p.softcap > 0.f, sloped = Option && p.slopes != nullptr;
+    const float unit = capped ? __fdividef(p.scale, p.softcap) : 0.f;
+    const float scale2 = (capped ? p.softcap : p.scale) * kLog2e;
     uint32_t step = 0;  // blocks that the tile has had
     bool ok = true;
     const auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -616,12 +597,15 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
       const int see_lo = p.window > 0 ? (int)max(INT64_C(0), min((int64_t)it.m, (int64_t)pos - p.window + 1)) : 0;
       const int see_hi = p.causal ? max(0, min(it.m, pos + 1)) : it.m;
       const int lo = shared.lo[t], hi = shared.hi[t], whole_lo = shared.whole_lo[t], whole_hi = shared.whole_hi[t];
-      const float slope = Option && p.slopes != nullptr && mine ? __ldg(p.slopes + it.head0 + r_head) : 0.f;
+      const float slope = sloped && mine ? __ldg(p.slopes + it.head0 + r_head) : 0.f, near = slope * kLog2e;
+      const uint64_t n01 = pack_f32x2(0.f, near), n23 = pack_f32x2(2.f * near, 3.f * near), n45 = pack_f32x2(4.f * near, 5.f * near),
+                     n67 = pack_f32x2(6.f * near, 7.f * near);
       // What slopes add from one block to the next.  The reference counts on it, up to
-      // 2^64 (it may then be that much above the scores); where more than 2^128 would
-      // come on top of the last block's, blocks are read twice.
-      const float rise = Option ? fmaxf(slope, 0.f) * (kLog2e * kKeys) : 0.f;
-      const bool steep = Option && __any_sync(0xffffffffu, rise > 128.f);
+      // 2^96 (it may then be that much above the scores); where more than 2^96 would come
+      // on top, blocks are read twice.
+      const float rise = Option ? fmaxf(near, 0.f) * kKeys : 0.f;
+      const bool steep = Option && __any_sync(0xffffffffu, rise > 192.f);
+      const bool rows = __any_sync(0xffffffffu, mine);  // of use in this warp
       float ref = mine ? -INFINITY : 0.f;
       float most = -INFINITY;  // of the blocks so far
       uint64_t sum2[2] = {0, 0};
@@ -630,15 +614,43 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         const bool masked = j < whole_lo || j >= whole_hi;
         const uint32_t t_s = tmem + lanes + Z::kS + buf * kKeys;
         if (!wait(&s_full[buf], (kTiles == 2 ? step : step >> 1) & 1u)) break;
+        if (!rows) {
+          if (lane == 0) mbar_arrive(&p_full[buf]);
+          ++step;
+          continue;
+        }
         uint32_t s[2][32];
         tmem_ld32(t_s, s[0]);
-        const auto ready = [&](uint32_t(&x)[32], int c0) {
-          if constexpr (Option) option_scores(x, p.scale, p.softcap, p.slopes != nullptr, slope, key0 + c0 - pos);
+        // 32 scores in units of log2, options applied and hidden ones -infinity, less the
+        // reference.  A slope's share is near * (key - pos): of every eighth key by itself,
+        // so that it is off by a unit or two of the distance's.
+        const auto exponents = [&](uint32_t(&x)[32], int c0, float minus) {
+          if (capped) cap_scores(x, unit);
+          const uint64_t mul = pack_f32x2(scale2, scale2);
+          if (sloped) {
+            const float base = fmaf(near, (float)(key0 + c0 - pos), minus);
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float eighth = fmaf(near, (float)(c & ~7), base);
+              const uint64_t add = add_f32x2(pack_f32x2(eighth, eighth), (c & 7) == 0 ? n01 : (c & 7) == 2 ? n23 : (c & 7) == 4 ? n45 : n67);
+              const float2 f = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), mul, add));
+              x[c] = __float_as_uint(f.x), x[c + 1] = __float_as_uint(f.y);
+            }
+          } else {
+            const uint64_t add = pack_f32x2(minus, minus);
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float2 f = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), mul, add));
+              x[c] = __float_as_uint(f.x), x[c + 1] = __float_as_uint(f.y);
+            }
+          }
           if (masked) {
-            const int from = see_lo - key0 - c0, to = see_hi - key0 - c0;
+            // bit c: key c is before the row's first or behind its last
+            const int from = min(max(see_lo - key0 - c0, 0), 32), to = min(max(see_hi - key0 - c0, 0), 32);
+            const uint32_t hidden = (uint32_t)((UINT64_C(1) << from) - 1) | ~(uint32_t)((UINT64_C(1) << to) - 1);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (c < from || c >= to) x[c] = __float_as_uint(-INFINITY);
+              if (hidden >> c & 1u) x[c] = __float_as_uint(-INFINITY);
           }
         };
         const auto largest = [&](const uint32_t(&x)[32], float top) {
@@ -659,14 +671,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
           for (int c = 0; c < kKeys; c += 32) {
             if (c > 0) tmem_ld32(t_s + c, s[0]);
             tmem_wait_ld(s[0]);
-            ready(s[0], c);
+            exponents(s[0], c, 0.f);
             top = largest(s[0], top);
             if (!steep && !__any_sync(0xffffffffu, top == -INFINITY)) break;
           }
           tmem_ld32(t_s, s[0]);
-          most = top * scale2;
+          most = top;
         } else if (Option) {
-          most += fminf(rise, 64.f);
+          most += fminf(rise, 96.f);
         }
         const bool move = most > ref + kMove;
         if (__any_sync(0xffffffffu, move)) {
@@ -694,7 +706,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
           }
         }
         const float minus = ref == -INFINITY ? 0.f : -ref;
-        const uint64_t mul = pack_f32x2(scale2, scale2), add = pack_f32x2(minus, minus);
         // A weight's steps: exponents of 32 scores, then their exp2, between which the
         // 32 before them are added up, so that the special-function unit always has the
         // next ones.
@@ -708,13 +719,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         for (int part = 0; part < kParts; ++part) {
           uint32_t(&x)[32] = s[part & 1], (&before)[32] = s[part & 1 ^ 1];
           tmem_wait_ld(x);
-          ready(x, 32 * part);
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const uint64_t two = pack_f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-            const float2 f = unpack_f32x2(Option ? add_f32x2(two, add) : fma_f32x2(two, mul, add));
-            x[c] = __float_as_uint(f.x), x[c + 1] = __float_as_uint(f.y);
-          }
+          exponents(x, 32 * part, minus);
           top = largest(x, top);
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
@@ -737,7 +742,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         if (lane == 0) mbar_arrive(&p_full[buf]);
         ++step;
       }
-      if (!ok || (lo < hi && !products_done())) break;
+      if (!ok || (rows && lo < hi && !products_done())) break;
+      if (rows) {
       const float2 s0 = unpack_f32x2(sum2[0]), s1 = unpack_f32x2(sum2[1]);
       const float sum = (s0.x + s0.y) + (s1.x + s1.y);
       const float inv = sum > 0.f || !(sum == sum) ? 1.f / sum : 0.f;
@@ -796,6 +802,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         row_again<D>(p, p.q + r * p.q_stride + (int64_t)head * D, p.k + (int64_t)it.k0 * p.k_stride + (int64_t)it.kv * D,
                      p.v + (int64_t)it.k0 * p.v_stride + (int64_t)it.kv * D, l, h, r_pos, __shfl_sync(0xffffffffu, slope, from),
                      p.out + r * p.out_stride + (int64_t)head * D, p.lse == nullptr ? nullptr : p.lse + r * p.n_heads + head);
+      }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&item_empty[turn]);
