@@ -201,7 +201,11 @@ __global__ void __launch_bounds__(Group > kCta ? Group : kCta) norm_kernel(const
 template <int Group, int Vecs>
 cudaError_t launch_one(const NormArgs &a, int sms, cudaStream_t s) {
   constexpr int kThreads = Group > kCta ? Group : kCta, kRows = kThreads / Group;
-  const int64_t ctas = (a.T + kRows - 1) / kRows, most = (int64_t)sms * (2048 / kThreads) / (Vecs > 2 ? 2 : 1);
+  static const int resident = [] {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_kernel<Group, Vecs>, kThreads, 0) == cudaSuccess && n > 0 ? n : 1;
+  }();
+  const int64_t ctas = (a.T + kRows - 1) / kRows, most = (int64_t)sms * resident;
   return launch_pdl(norm_kernel<Group, Vecs>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kThreads), 0, s, a);
 }
 
@@ -217,11 +221,16 @@ cudaError_t launch_group(const NormArgs &a, int vecs, int sms, cudaStream_t s) {
 
 }  // namespace
 
+// Lanes of a row and vectors of a lane: as few idle lanes as may be, and then as many
+// lanes, which hold less each.
 cudaError_t launch_norm(const NormArgs &a, int sms, cudaStream_t s) {
   const int vecs = a.H / 8;
-  int group = 32;
-  while (group * 4 < vecs) group *= 2;  // H <= kNormColumns: 512 at most
-  const int per = (vecs + group - 1) / group;
+  int group = 0, per = 0;
+  for (int v = 1; v <= 4; ++v) {
+    int g = 32;
+    while (g < 512 && g * v < vecs) g *= 2;
+    if (g * v >= vecs && (group == 0 || g * v < group * per)) group = g, per = v;
+  }
   switch (group) {
     case 32: return launch_group<32>(a, per, sms, s);
     case 64: return launch_group<64>(a, per, sms, s);

@@ -88,10 +88,10 @@ class Projection:
         bf16 too if ``out`` is given.  Without a weight the rows are quantised as they
         are.  The scales may have any positive strides; new ones lie block by block,
         as ``matmul`` reads them fastest."""
-        T, H = x.shape
         if codes is None:
-            codes = self._new((T, H), torch.uint8, stream)
+            codes = self._new(x.shape, torch.uint8, stream)
         if scales is None:
+            T, H = x.shape
             scales = self._new((-(-H // BLOCK), T), torch.float32, stream).t()
         if residual_out is None:
             residual_out = residual
