@@ -42,7 +42,7 @@ struct MatmulArgs {
   int blocks;  // ceil(K / 128)
   int *err;
   // plan_matmul's:
-  bool few;                       // at most 32 rows
+  bool few;                       // at most 64 rows: two CTAs per SM
   int columns, splits;            // of a tile; CTAs of a cluster, which share its K blocks
   int64_t tiles, grid;
   int a_rows, a_bytes;            // of an activation box, and what it has of a stage
@@ -50,9 +50,10 @@ struct MatmulArgs {
   int stages, sums_at, scales_at, smem;  // blocks in flight; bytes into shared memory, and all of it
 };
 constexpr int kMostSplits = 8;
-// Resident clusters of 1, 2, ... CTAs for tiles of 64, 128 and 256 columns.
+// Resident clusters of 1, 2, ... CTAs: for few rows, and for tiles of 64, 128 and 256
+// columns.
 struct MatmulFit {
-  int few[2][kMostSplits + 1], many[3][kMostSplits + 1];
+  int few[kMostSplits + 1], many[3][kMostSplits + 1];
 };
 cudaError_t ready_matmul(MatmulFit *fit);
 // Fills in the plan for M, N, K (blocks) on at most `sms` SMs.

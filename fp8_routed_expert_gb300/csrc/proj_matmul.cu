@@ -36,10 +36,13 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kHeld = 16, kScales = kRows + 2;
 constexpr int kMostStages = 8;
 
-// Few: at most 32 rows, which one warp adds up, so that two CTAs fit on an SM.
-template <int Columns, bool Few>
+// Quarters: of a tile's 128 rows (TMEM's lanes by warp) that are of use.  With one or two,
+// which a warp each adds up, two CTAs of 64 columns fit on an SM (a sub-partition then has
+// four of their warps, of 128 registers each); else two warps share a quarter.
+template <int Columns, int Quarters>
 struct Ring {
-  static constexpr int kGroups = Few ? 1 : 2, kSumWarps = Few ? 1 : 8, kThreads = 128 + 32 * kSumWarps;
+  static constexpr bool kFew = Quarters < 4;
+  static constexpr int kGroups = kFew ? 1 : 2, kSumWarps = Quarters * kGroups, kThreads = 128 + 32 * kSumWarps;
 };
 
 struct Item {
@@ -76,10 +79,10 @@ __device__ __forceinline__ void store8(const MatmulArgs &p, int64_t row, int64_t
   }
 }
 
-template <int Columns, bool Few>
-__global__ void __launch_bounds__(Ring<Columns, Few>::kThreads, Few ? 2 : 1) matmul_kernel(const __grid_constant__ CUtensorMap ta,
+template <int Columns, int Quarters>
+__global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::kThreads, Quarters < 4 ? 2 : 1) matmul_kernel(const __grid_constant__ CUtensorMap ta,
                                                              const __grid_constant__ CUtensorMap tw, const MatmulArgs p) {
-  using R = Ring<Columns, Few>;
+  using R = Ring<Columns, Quarters>;
   constexpr int kMine = Columns / R::kGroups;  // columns of a summing warp
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kMostStages], empty[kMostStages], sum_full[2], sum_empty[2];
@@ -88,7 +91,7 @@ __global__ void __launch_bounds__(Ring<Columns, Few>::kThreads, Few ? 2 : 1) mat
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   // stages, what a product of the last one may read behind it, a cluster's sums, and the
   // scales of kHeld blocks: 128 of rows, two of weights
-  const int a_bytes = Few ? p.a_bytes : kRows * kBlock, stage_bytes = a_bytes + Columns * kBlock;
+  const int a_bytes = R::kFew ? p.a_bytes : kRows * kBlock, stage_bytes = a_bytes + Columns * kBlock;
   const float4 *sums = reinterpret_cast<const float4 *>(smem + p.sums_at);
   float *scales = reinterpret_cast<float *>(smem + p.scales_at);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(Ring<Columns, Few>::kThreads, Few ? 2 : 1) mat
         }
         float *to = scales + (count & (kHeld - 1)) * kScales;
 #pragma unroll
-        for (int i = 0; i < (Few ? 1 : 4); ++i) copy4(to + 32 * i + lane, sa[i] + b * p.a_block);
+        for (int i = 0; i < Quarters; ++i) copy4(to + 32 * i + lane, sa[i] + b * p.a_block);
         if (lane < 2) copy4(to + kRows + lane, sw + b);
         copies_arrive(&full[stage]);
         if (++stage == stages) stage = 0, phase ^= 1u;
@@ -312,11 +315,11 @@ __global__ void __launch_bounds__(Ring<Columns, Few>::kThreads, Few ? 2 : 1) mat
   }
 }
 
-template <int Columns, bool Few>
+template <int Columns, int Quarters>
 cudaError_t launch_one(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)m.grid);
-  cfg.blockDim = dim3(Ring<Columns, Few>::kThreads);
+  cfg.blockDim = dim3(Ring<Columns, Quarters>::kThreads);
   cfg.dynamicSmemBytes = (size_t)m.smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -327,21 +330,26 @@ cudaError_t launch_one(const CUtensorMap &a, const CUtensorMap &w, const MatmulA
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = m.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, matmul_kernel<Columns, Few>, a, w, m);
+  return cudaLaunchKernelEx(&cfg, matmul_kernel<Columns, Quarters>, a, w, m);
 }
 
 // Shared memory of a CTA where one or two of them have an SM.
 constexpr int kOnePerSm = 226 * 1024, kTwoPerSm = 112 * 1024, kAround = kHeld * kScales * 4 + 1024;
 
-template <int Columns, bool Few>
+// Stands in for a kernel in the question how many clusters are resident: the answer for
+// one that allocates TMEM is always one CTA per SM, however little it takes.
+__global__ void __launch_bounds__(256, 2) place_kernel() {}
+
+template <int Columns, int Quarters>
 cudaError_t ready_one(int (&fit)[kMostSplits + 1]) {
-  constexpr int kSmem = Few ? kTwoPerSm : kOnePerSm;
-  const auto kernel = matmul_kernel<Columns, Few>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  constexpr int kSmem = Quarters < 4 ? kTwoPerSm : kOnePerSm;
+  cudaError_t e = cudaFuncSetAttribute(matmul_kernel<Columns, Quarters>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const auto kernel = place_kernel;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   for (int c = 1; e == cudaSuccess && c <= kMostSplits; ++c) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)c);
-    cfg.blockDim = dim3(Ring<Columns, Few>::kThreads);
+    cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = kSmem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -357,33 +365,40 @@ cudaError_t ready_one(int (&fit)[kMostSplits + 1]) {
 }  // namespace
 
 cudaError_t ready_matmul(MatmulFit *fit) {
-  for (cudaError_t e : {ready_one<64, true>(fit->few[0]), ready_one<128, true>(fit->few[1]), ready_one<64, false>(fit->many[0]),
-                        ready_one<128, false>(fit->many[1]), ready_one<256, false>(fit->many[2])})
+  for (cudaError_t e : {ready_one<64, 1>(fit->few), ready_one<64, 2>(fit->few), ready_one<64, 4>(fit->many[0]), ready_one<128, 4>(fit->many[1]),
+                        ready_one<256, 4>(fit->many[2])})
     if (e != cudaSuccess) return e;
   return cudaSuccess;
 }
 
 // How a product is split.  A tile's K blocks go over as many CTAs as are resident
-// together (clusters that come in a second round double the time: 48 clusters of three
-// on 46 places, 1 x 6144 x 2048, 11.3 us, 96 of three on 97 places TODO us).  The time is
-// about, in cycles of a CTA: a block 420, 560 and 1040 for 64, 128 and 256 columns, a
-// tile's start and end 3000, a cluster's exchange 2000 and what it pushes at 32 bytes.
+// together: clusters that come in a second round double the time (48 clusters of three
+// where 46 are resident, 1 x 6144 x 2048: 11.3 us, 96 clusters of two 6.3).  The time is
+// about, in cycles: a block 420, 560 and 1040 for 64, 128 and 256 columns (260 with few
+// rows), a tile's start and end 2000, 2600 and 4000, a cluster's exchange 150 for each CTA
+// and what a CTA pushes at 12 bytes.  Against the best of all splits (us):
+//   64 x 2048 x 2048      5.3: 64 columns, 4 CTAs; 8 CTAs 6.1, alone 7.3
+//   333 x 1000 x 2880     8.4: 64, 2; 128 columns, 4 CTAs 9.2, alone 10.4 (2)
+//   512 x 4096 x 4096     15.7: 128, alone; 256 columns 19.9
+//   700 x 7000 x 512      11.8: 128, alone; 256 columns 12.8
+//   2048 x 4096 x 2048    23.8: 256, alone; 128 columns 31.0
 void plan_matmul(const MatmulFit &fit, int sms, MatmulArgs *m) {
-  const bool few = m->M <= 32;
+  const bool few = m->M <= 64;
   const int64_t rows = (m->M + kRows - 1) / kRows;
   double best = 0.0;
   m->columns = 0;
-  for (int i = 0; i < (few ? 2 : 3); ++i) {
+  for (int i = 0; i < (few ? 1 : 3); ++i) {
     const int columns = 64 << i;
     const int64_t tiles = rows * ((m->N + columns - 1) / columns);
-    const int *places = few ? fit.few[i] : fit.many[i];
+    const int *places = few ? fit.few : fit.many[i];
     for (int splits = 1; splits <= kMostSplits && splits <= m->blocks; ++splits) {
       const int64_t most = (int64_t)sms * (few ? 2 : 1) / splits, resident = places[splits] < most ? places[splits] : most;
       if (splits > 1 && (tiles > resident || columns == 256)) continue;
       const double rounds = (double)((tiles + resident - 1) / (resident > 0 ? resident : 1));
-      const double block = columns == 64 ? 420.0 : columns == 128 ? 560.0 : 1040.0;
-      double t = rounds * ((double)((m->blocks + splits - 1) / splits) * block + 3000.0);
-      if (splits > 1) t += 2000.0 + (double)(m->M < kRows ? m->M : kRows) * columns * 4 * (splits - 1) / splits / 32.0;
+      const double block = few ? 260.0 : columns == 64 ? 420.0 : columns == 128 ? 560.0 : 1040.0;
+      const double around = columns == 64 ? 2000.0 : columns == 128 ? 2600.0 : 4000.0;
+      double t = rounds * ((double)((m->blocks + splits - 1) / splits) * block + around);
+      if (splits > 1) t += 150.0 * splits + (double)(m->M < kRows ? m->M : kRows) * columns * 4 * (splits - 1) / splits / 12.0;
       if (m->columns == 0 || t < best) {
         best = t;
         m->columns = columns;
@@ -411,11 +426,11 @@ void plan_matmul(const MatmulFit &fit, int sms, MatmulArgs *m) {
 }
 
 cudaError_t launch_matmul(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, cudaStream_t s) {
-  if (m.few) return m.columns == 64 ? launch_one<64, true>(a, w, m, s) : launch_one<128, true>(a, w, m, s);
+  if (m.few) return m.M <= 32 ? launch_one<64, 1>(a, w, m, s) : launch_one<64, 2>(a, w, m, s);
   switch (m.columns) {
-    case 64: return launch_one<64, false>(a, w, m, s);
-    case 128: return launch_one<128, false>(a, w, m, s);
-    default: return launch_one<256, false>(a, w, m, s);
+    case 64: return launch_one<64, 4>(a, w, m, s);
+    case 128: return launch_one<128, 4>(a, w, m, s);
+    default: return launch_one<256, 4>(a, w, m, s);
   }
 }
 
