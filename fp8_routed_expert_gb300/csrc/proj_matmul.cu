@@ -42,8 +42,18 @@ constexpr int kMostStages = 8;
 template <int Columns, int Quarters>
 struct Ring {
   static constexpr bool kFew = Quarters < 4;
+  // blocks that are handed over at a time: what a summing warp waits, reads and answers
+  // per turn takes as long as its sums of a block (shared memory is busy with the
+  // products' operands); tiles of 256 columns fill TMEM with two blocks
+  static constexpr int kTurn = Columns == 256 ? 1 : 2;
+  static constexpr uint32_t kTmem = 2 * kTurn * Columns;
   static constexpr int kGroups = kFew ? 1 : 2, kSumWarps = Quarters * kGroups, kThreads = 128 + 32 * kSumWarps;
 };
+
+// Tiles of 256 columns: 384 threads start with 168 registers each, of which the summing
+// warps, with 128 sums each, take more: 128 * 80 + 256 * 208 <= 384 * 168 (checked against
+// the build in ready_one).  Each branch asks for itself, which is where the compiler looks.
+constexpr int kFewRegs = 80, kManyRegs = 208;
 
 struct Item {
   int m0, n0;
@@ -105,7 +115,7 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
     prefetch_tmap(&tw);
   }
   if (warp == 1) {
-    tmem_alloc(&tmem_sh, 2 * Columns);
+    tmem_alloc(&tmem_sh, R::kTmem);
     tmem_relinquish();
     tc_fence_before();
   }
@@ -118,6 +128,8 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
   const int rank = splits > 1 ? (int)cluster_rank() : 0;
   const int64_t first = blockIdx.x / splits, step = gridDim.x / splits;
 
+  if (warp < 4) {
+  if constexpr (Columns == 256) fewer_registers<kFewRegs>();
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
@@ -152,16 +164,20 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
     };
     for (int64_t tile = first; ok && tile < p.tiles; tile += step) {
       const Item it = item_of<Columns>(p, tile, rank);
-      for (int b = it.b0; b < it.b1; ++b) {
-        if (!wait(&sum_empty[buf], bphase ^ 1u) || !wait(&full[stage], phase)) break;
-        tc_fence_after();
-        const uint64_t a = desc + (uint64_t)(stage * (stage_bytes / 16)), w = a + (uint64_t)(a_bytes / 16);
+      for (int b = it.b0; ok && b < it.b1; b += R::kTurn) {
+        if (!wait(&sum_empty[buf], bphase ^ 1u)) break;
 #pragma unroll
-        for (int k = 0; k < kBlock / 32; ++k)
-          mma_e4m3_ss(leader, tmem + (uint32_t)(buf * Columns), a + k * 2, w + k * 2, idesc, k > 0 ? 1u : 0u);
-        mma_commit_by(leader, &empty[stage]);
+        for (int u = 0; u < R::kTurn; ++u) {
+          if (b + u >= it.b1 || !wait(&full[stage], phase)) break;
+          tc_fence_after();
+          const uint64_t a = desc + (uint64_t)(stage * (stage_bytes / 16)), w = a + (uint64_t)(a_bytes / 16);
+#pragma unroll
+          for (int k = 0; k < kBlock / 32; ++k)
+            mma_e4m3_ss(leader, tmem + (uint32_t)((buf * R::kTurn + u) * Columns), a + k * 2, w + k * 2, idesc, k > 0 ? 1u : 0u);
+          mma_commit_by(leader, &empty[stage]);
+          if (++stage == stages) stage = 0, phase ^= 1u;
+        }
         mma_commit_by(leader, &sum_full[buf]);
-        if (++stage == stages) stage = 0, phase ^= 1u;
         buf ^= 1;
         if (buf == 0) bphase ^= 1u;
       }
@@ -193,7 +209,9 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
         if (++stage == stages) stage = 0, phase ^= 1u;
       }
     }
-  } else if (warp >= 4) {
+  }
+  } else {
+    if constexpr (Columns == 256) more_registers<kManyRegs>();
     const int quarter = warp & 3, group = (warp - 4) >> 2;  // TMEM lanes and columns of this warp
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(group * kMine);
     uint32_t count = 0;
@@ -206,29 +224,38 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
       uint64_t acc[kMine / 2];
 #pragma unroll
       for (int j = 0; j < kMine / 2; ++j) acc[j] = 0;
-      for (int b = it.b0; b < it.b1; ++b, ++count) {
+      for (int b = it.b0; b < it.b1; b += R::kTurn) {
         if (!mbar_wait(&sum_full[buf], bphase, &stop, kWaitNs)) {
           give_up(&stop, p.err);
           ok = false;
           break;
         }
         tc_fence_after();
+        const int here = min(R::kTurn, it.b1 - b);
         if (any) {
-          // (the products were of operands that came with these scales)
-          const float *sc = scales + (count & (kHeld - 1)) * kScales;
-          const float c = sc[quarter * 32 + lane] * sc[kRows + group * kMine / 128];
-          const uint64_t cc = pack_f32x2(c, c);
-          const uint32_t from = t_lane + (uint32_t)(buf * Columns);
+          float c[R::kTurn];  // (the products were of operands that came with these scales)
 #pragma unroll
-          for (int l = 0; l < kMine; l += 16) {
-            uint32_t v[16];
-            tmem_ld16(from + l, v);
-            tmem_wait_ld16(v);
+          for (int u = 0; u < R::kTurn; ++u) {
+            const float *sc = scales + (count + u & (kHeld - 1)) * kScales;
+            c[u] = sc[quarter * 32 + lane] * sc[kRows + group * kMine / 128];
+          }
+          const uint32_t from = t_lane + (uint32_t)(buf * R::kTurn * Columns);
 #pragma unroll
-            for (int j = 0; j < 16; j += 2)
-              acc[(l + j) / 2] = fma_f32x2(pack_f32x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), cc, acc[(l + j) / 2]);
+          for (int u = 0; u < R::kTurn; ++u) {
+            if (u >= here) break;
+            const uint64_t cc = pack_f32x2(c[u], c[u]);
+#pragma unroll
+            for (int l = 0; l < kMine; l += 16) {
+              uint32_t v[16];
+              tmem_ld16(from + u * Columns + l, v);
+              tmem_wait_ld16(v);
+#pragma unroll
+              for (int j = 0; j < 16; j += 2)
+                acc[(l + j) / 2] = fma_f32x2(pack_f32x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), cc, acc[(l + j) / 2]);
+            }
           }
         }
+        count += (uint32_t)here;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sum_empty[buf]);
@@ -311,7 +338,7 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * Columns);
+    tmem_dealloc(tmem, R::kTmem);
   }
 }
 
@@ -344,6 +371,10 @@ template <int Columns, int Quarters>
 cudaError_t ready_one(int (&fit)[kMostSplits + 1]) {
   constexpr int kSmem = Quarters < 4 ? kTwoPerSm : kOnePerSm;
   cudaError_t e = cudaFuncSetAttribute(matmul_kernel<Columns, Quarters>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaFuncAttributes at;
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, matmul_kernel<Columns, Quarters>);
+  // the summing warps would wait forever for registers that the launch does not have
+  if (e == cudaSuccess && Columns == 256 && at.numRegs * 3 < kFewRegs + 2 * kManyRegs) e = cudaErrorInvalidKernelImage;
   const auto kernel = place_kernel;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   for (int c = 1; e == cudaSuccess && c <= kMostSplits; ++c) {
