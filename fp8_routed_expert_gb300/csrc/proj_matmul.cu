@@ -126,11 +126,14 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
   pdl_trigger();
   const int splits = Columns == 256 ? 1 : p.splits;  // (tiles of 256 columns are many)
   const int rank = splits > 1 ? (int)cluster_rank() : 0;
+  if (splits > 1) cluster_started();  // nothing is pushed to a CTA that does not run yet
   const int64_t first = blockIdx.x / splits, step = gridDim.x / splits;
 
-  if (warp < 4) {
-  if constexpr (Columns == 256) fewer_registers<kFewRegs>();
+  const auto few_registers = [] {
+    if constexpr (Columns == 256) fewer_registers<kFewRegs>();
+  };
   if (warp == 0) {
+    few_registers();
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
@@ -150,6 +153,7 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
       }
     }
   } else if (warp == 1) {
+    few_registers();
     // the whole warp in step, one lane issues (see mma_e4m3_ss)
     constexpr uint32_t idesc = idesc_e4m3_f32(kRows, Columns);
     const uint32_t leader = elect_lane();
@@ -183,6 +187,7 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
       }
     }
   } else if (warp == 2) {
+    few_registers();
     const int n_blocks = (int)((p.N + 127) / 128);
     int stage = 0;
     uint32_t phase = 0, count = 0;
@@ -209,7 +214,8 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
         if (++stage == stages) stage = 0, phase ^= 1u;
       }
     }
-  }
+  } else if (warp == 3) {
+    few_registers();
   } else {
     if constexpr (Columns == 256) more_registers<kManyRegs>();
     const int quarter = warp & 3, group = (warp - 4) >> 2;  // TMEM lanes and columns of this warp
@@ -262,6 +268,7 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
         buf ^= 1;
         if (buf == 0) bphase ^= 1u;
       }
+      if (splits > 1) cluster_wait_started();  // (a cluster has one tile)
       // the coordinates again, rather than held in registers through the blocks
       int64_t again = tile;
       asm volatile("" : "+l"(again));
@@ -310,6 +317,7 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
   }
   __syncwarp();
   if (splits > 1) {
+    if (warp < 4) cluster_wait_started();
     cluster_sync_all();
     // a lane adds 8 columns of a row of this CTA's
     const Item it = item_of<Columns>(p, first, rank);

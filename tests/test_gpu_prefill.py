@@ -127,6 +127,80 @@ def test_options(d, causal, window, softcap, slopes, scale):
     check(q, k, v, q0, k0, causal, softcap, sl, window, scale)
 
 
+@pytest.mark.parametrize("B", [127, 128, 129, 400])
+def test_many_sequences(B):
+    """Short sequences of 0..9 tokens, as many as a warp holds the lengths of, and more."""
+    rng = np.random.default_rng(B)
+    nq = rng.integers(0, 10, B)
+    nk = nq + rng.integers(0, 30, B) * (rng.random(B) < 0.3)
+    nq[B // 2] = 200
+    nk[B // 2] = 333
+    check(*inputs(nq.tolist(), nk.tolist(), 4, 2, 64, B, before=1, behind=1))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+def test_steep_slopes(d, causal):
+    """Distance biases that rise or fall by hundreds within a block of keys."""
+    q, k, v, q0, k0 = inputs([500, 3, 130], [600, 700, 130], 6, 1, d, d + causal)
+    sl = torch.tensor([5.0, -5.0, 1.2, -1.2, 0.9, -30.0], device=DEV)
+    check(q, k, v, q0, k0, causal, 0.0, sl)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("scale", [0.1, 0.25, -0.2, 1.0])
+def test_references_that_move_often(d, scale):
+    """Large scores in random order: what the softmax is relative to moves in many blocks,
+    while the products with the values are on their way.  The same bits each time."""
+    q, k, v, q0, k0 = inputs([400, 90], [900, 90], 6, 2, d, int(scale * 100) + d, size=3.0)
+    attn = DecodeAttention(6, 2, d)
+    out, _ = check(q, k, v, q0, k0, scale=scale, attn=attn)
+    for _ in range(10):
+        assert torch.equal(attn.prefill(q, k, v, dev(q0), dev(k0), scale=scale), out)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn(seed):
+    rng = np.random.default_rng(seed)
+    d, nkv = int(rng.choice([64, 128, 256])), int(rng.choice([1, 2, 3]))
+    nh = nkv * int(rng.choice([1, 2, 3, 5, 8, 16, 17, 20]))
+    B = int(rng.integers(1, 6))
+    nq = rng.integers(0, 300, B)
+    nk = np.maximum(0, nq + rng.integers(-50, 400, B) * (rng.random(B) < 0.5))
+    window = int(rng.choice([0, 0, 1, 17, 128, 129, 500]))
+    sl = torch.from_numpy(rng.normal(size=nh).astype(np.float32)).to(DEV) if rng.random() < 0.3 else None
+    check(*inputs(nq.tolist(), nk.tolist(), nh, nkv, d, seed, before=int(rng.integers(0, 3)), behind=int(rng.integers(0, 3)), size=1.5),
+          causal=bool(rng.random() < 0.8), softcap=float(rng.choice([0.0, 0.0, 3.0, 40.0])), slopes=sl, window=window)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_nan_that_every_row_sees(d):
+    q, k, v, q0, k0 = inputs([260], [260], 4, 2, d, 8)
+    v = v.clone()
+    v[0, 1, 5] = float("nan")
+    attn = DecodeAttention(4, 2, d)
+    out = f64(attn.prefill(q, k, v, dev(q0), dev(k0)))
+    v[0, 1, 5] = 0
+    clean = f64(attn.prefill(q, k, v, dev(q0), dev(k0)))
+    assert np.isnan(out[:, 2:, 5]).all() and np.isfinite(out[:, :2]).all()
+    keep = np.delete(out[:, 2:], 5, 2)
+    assert (np.abs(keep - np.delete(clean[:, 2:], 5, 2)) <= 2.0 ** -6 * np.abs(clean).max()).all()
+
+
+def test_two_calls_at_once_on_one_context():
+    q, k, v, q0, k0 = inputs([1500, 700], [1500, 700], 8, 2, 128, 77)
+    qs, ks = dev(q0), dev(k0)
+    attn = DecodeAttention(8, 2, 128)
+    want = attn.prefill(q, k, v, qs, ks)
+    outs = [torch.empty_like(want) for _ in range(6)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i, o in enumerate(outs):
+        attn.prefill(q, k, v, qs, ks, out=o, stream=side if i % 2 else None)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs) and attn.status() == 0
+
+
 def test_strided_rows_and_heads():
     """Slices of a fused projection's rows, and outputs within wider rows."""
     g = gen(11)

@@ -164,6 +164,27 @@ def test_matmul(proj, M, N, K):
     check_matmul(proj, *make(gen(M + N + K), M, N, K))
 
 
+@pytest.mark.parametrize("seed", range(30))
+def test_matmul_drawn(proj, seed):
+    """Sizes over every way of splitting: few rows, clusters, tiles of each width."""
+    rng = np.random.default_rng(seed)
+    M = int(np.exp(rng.uniform(0, np.log([20, 70, 300, 1500][seed % 4]))))
+    N, K = int(np.exp(rng.uniform(np.log(8), np.log(5000)))), int(np.exp(rng.uniform(np.log(16), np.log(4000))))
+    few = Projection(max_sms=int(rng.choice([1, 5, 40]))) if seed % 5 == 0 else proj
+    a, sa, w, sw = make(gen(seed), M, N, K, pad=int(rng.choice([0, 0, 32])))
+    got = check_matmul(few, a, sa, w, sw)
+    assert torch.equal(few.matmul(a, sa, w, sw), got)
+
+
+@pytest.mark.parametrize("M", [1, 31, 32, 33, 64, 65, 128, 129])
+def test_matmul_rows_at_the_borders(proj, M):
+    g = gen(M)
+    a, sa, w, sw = make(g, M, 520, 1100)
+    wide = torch.full((M + 2, 528), 9.0, dtype=torch.bfloat16, device=DEV)
+    check_matmul(proj, a, sa, w, sw, wide[1:-1, :520])
+    assert (wide[0] == 9).all() and (wide[-1] == 9).all() and (wide[:, 520:] == 9).all()
+
+
 def test_matmul_strides(proj):
     """Rows within wider ones, scales in either order, output within wider rows."""
     g = gen(5)
