@@ -27,6 +27,7 @@ struct moe_attn {
   int sms = 0;                // of the device
   int *err = nullptr;
   uint64_t *turns = nullptr;  // [rope_dim / 2]
+  PrefillFit prefill;
   DecodePlan wide, narrow;    // groups as large as may be, and of 8 heads at most
   // moe_attn_decode's workspace
   int group = 1, max_ctas = 0;
@@ -251,12 +252,14 @@ int moe_attn_init(moe_attn **out, const moe_attn_config *cfg) {
   ATTN_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, cfg->device));
   ATTN_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, cfg->device));
   if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
-  ATTN_TRY(ready_prefill(cfg->head_dim));
+  PrefillFit fit;
+  ATTN_TRY(ready_prefill(cfg->head_dim, &fit));
   moe_attn *a = new (std::nothrow) moe_attn();
   if (a == nullptr) return MOE_ERR_NOMEM;
   a->cfg = *cfg;
   a->cfg.rope_freqs = nullptr;  // the caller's array is not kept
   a->sms = sms;
+  a->prefill = fit;
   const int use = cfg->max_sms > 0 && cfg->max_sms < sms ? cfg->max_sms : sms;
   const int per_kv = cfg->n_heads / cfg->n_kv_heads;
   a->wide.group = decode_group(per_kv, cfg->head_dim, false);
@@ -551,7 +554,7 @@ int moe_attn_prefill(moe_attn *a, const void *q, int64_t q_stride, int64_t Tq, c
   r.out_stride = out_stride;
   r.lse = lse;
   r.err = a->err;
-  plan_prefill(&r, c.head_dim);
+  plan_prefill(&r, c.head_dim, c.max_sms > 0 && c.max_sms < a->sms ? c.max_sms : a->sms, a->prefill);
   if (r.items > INT64_C(0x7fffffff)) return MOE_ERR_SHAPE;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   ATTN_TRY(cudaSetDevice(c.device));

@@ -42,7 +42,9 @@
 //
 // A launch has a block per item, the longest first; a running one asks for the next
 // item that has not started (cluster launch control), so no counter in memory is
-// needed and the last items are short.
+// needed and the last items are short.  Where a call has so few items that whole clusters
+// of CTAs are resident for each, a cluster shares an item's blocks and joins the parts
+// through distributed shared memory (plan_prefill, Parts).
 //
 // Warps: 0 issues TMA, 1 allocates TMEM and issues the products, 2 asks for items, 4..
 // are the softmax and output warps, four per tile.
@@ -94,7 +96,7 @@ struct Control {
   Item items[kAhead];
   uint64_t q_full[kTiles], q_empty[kTiles], kv_full[kSlots], kv_empty[kSlots], s_full[2], p_full[2], o_full[2], answered,
       item_full[kAhead], item_empty[kAhead];
-  uint32_t tmem;
+  uint32_t tmem, odd[4];  // odd: rows of this CTA's share whose output is not finite
   int stop;
 };
 template <int D>
@@ -165,9 +167,10 @@ __device__ __forceinline__ Piece piece_at(const PrefillArgs &p, int place, int T
   return Piece{b, place - (clamp_start(p.q_starts, b, p.Tq) / T + b)};
 }
 
-// Piece `index` of sequence b, and a group of heads; false if it has no tokens.
-template <int D>
-__device__ __forceinline__ bool item_of(const PrefillArgs &p, int b, int index, int group, Item *it) {
+// Piece `index` of sequence b, and a group of heads; false if it has no tokens.  Of an
+// item that is split, the turns of CTA `rank`.
+template <int D, bool Split>
+__device__ __forceinline__ bool item_of(const PrefillArgs &p, int b, int index, int group, int rank, Item *it) {
   constexpr int kTiles = Shape<D>::kTiles, kKeys = Shape<D>::kKeys;
   const int q0 = clamp_start(p.q_starts, b, p.Tq), q1 = clamp_start(p.q_starts, b + 1, p.Tq);
   const int k0 = clamp_start(p.k_starts, b, p.Tk), k1 = clamp_start(p.k_starts, b + 1, p.Tk);
@@ -214,6 +217,14 @@ __device__ __forceinline__ bool item_of(const PrefillArgs &p, int b, int index, 
       it->lo[t] = last - hi, it->hi[t] = last - lo;
       it->whole_lo[t] = last - whole_hi, it->whole_hi[t] = last - whole_lo;
     }
+  }
+  if constexpr (Split) {  // this CTA's turns
+    const int64_t turns = it->last;
+    it->first = (int)(turns * rank / p.splits);
+    it->last = (int)(turns * (rank + 1) / p.splits);
+    if (it->first == it->last) it->first = it->last = 0;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) it->lo[t] = max(it->lo[t], it->first), it->hi[t] = min(it->hi[t], it->last);
   }
   return true;
 }
@@ -298,13 +309,96 @@ __device__ __noinline__ void row_again(const PrefillArgs &p, const __nv_bfloat16
   if (lse != nullptr && lane == 0) *lse = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
 }
 
+// An item that a cluster's CTAs have split (few items): its rows are shared out, `held`
+// neighbouring ones to a CTA, and each CTA pushes its part of a row, the output of its
+// keys alone and (reference, log2 of the sum), to the row's CTA: [rank][row % held] over
+// the slots of keys and values and over the queries, which nobody needs any longer.
+struct PartStats {
+  float ref, log;  // kNoPart: the part has no blocks, and its output is not there
+};
+constexpr float kNoPart = -3e38f;
+struct Parts {
+  int rows, held;  // held * splits is a tile's or two tiles' rows at most: splits is a power of two
+  template <int D>
+  __device__ __forceinline__ static Parts of(const PrefillArgs &p, int n, int tok0) {
+    static_assert(Shape<D>::kTiles * 128 * D * 4 <= Shape<D>::kSlots * Shape<D>::kSlot, "parts fit");
+    const int rows = min(item_tokens<D>(p), n - tok0) * p.heads;
+    return Parts{rows, (rows + p.splits - 1) / p.splits};
+  }
+};
+
 __device__ __forceinline__ void give_up(volatile int *stop, int *err) {
   *stop = 1;
   set_error(err, DEV_ERR_TIMEOUT);
 }
 
-// Option: scores need more than a positive scale (a cap, slopes, another scale).
-template <int D, bool Option>
+// The rows of this CTA's share from the cluster's parts; by all its threads.
+template <int D>
+__device__ __noinline__ void join_parts(const PrefillArgs &p, Control<D> &ctl, uint8_t *smem, uint8_t *ring, int rank) {
+  const Item &it = ctl.items[0];
+  const Parts parts = Parts::of<D>(p, it.n, it.tok0);
+  const auto used = [&](int r) { return r < parts.rows && r % p.heads < it.heads; };
+  // A thread per 8 elements of a row: the part that adds most to the sum counts as one.
+  for (int u = threadIdx.x; u < parts.held * (D / 8); u += Shape<D>::kThreads) {
+    const int place = u / (D / 8), e = u % (D / 8) * 8, r = rank * parts.held + place;
+    if (!used(r)) continue;
+    const PartStats *stats = reinterpret_cast<const PartStats *>(smem) + place;
+    const float *o = reinterpret_cast<const float *>(ring) + place * D + e;
+    PartStats best = {-INFINITY, 0.f};
+#pragma unroll 4
+    for (int c = 0; c < p.splits; ++c) {
+      const PartStats s = stats[c * parts.held];
+      if (s.ref + s.log > best.ref + best.log) best = s;
+    }
+    const bool none = best.ref == -INFINITY;  // (where a part has no blocks too)
+    float acc[8] = {}, total = 0.f, odd = 0.f;
+#pragma unroll 2
+    for (int c = 0; c < p.splits; ++c) {
+      const PartStats s = stats[c * parts.held];
+      if (s.log == kNoPart) continue;
+      const float w = none ? 0.f : exp2_fast((s.ref - best.ref) + (s.log - best.log));
+      total += w;
+      const float4 f = *reinterpret_cast<const float4 *>(o + c * parts.held * D), g = *reinterpret_cast<const float4 *>(o + c * parts.held * D + 4);
+      const float v[8] = {f.x, f.y, f.z, f.w, g.x, g.y, g.z, g.w};
+      if (!(s.log < 200.f)) odd = NAN;  // the sum is not finite
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        odd = fmaf(v[x], 0.f, odd);  // (of a part whose keys all weigh nothing too)
+        acc[x] = fmaf(v[x], w, acc[x]);
+      }
+    }
+    const float inv = total > 0.f ? 1.f / total : 0.f;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      acc[x] *= inv;
+      odd = fmaf(acc[x], 0.f, odd);
+    }
+    if (!(odd == 0.f)) atomicOr(&ctl.odd[place / 32], 1u << (place % 32));
+    const int64_t at = it.q0 + (int64_t)it.tok0 + r / p.heads;
+    const int h = it.head0 + r % p.heads;
+    *reinterpret_cast<uint4 *>(p.out + at * p.out_stride + (int64_t)h * D + e) =
+        make_uint4(bf16x2_of(acc[0], acc[1]), bf16x2_of(acc[2], acc[3]), bf16x2_of(acc[4], acc[5]), bf16x2_of(acc[6], acc[7]));
+    if (e == 0 && p.lse != nullptr) p.lse[at * p.n_heads + h] = total > 0.f ? kLn2 * (best.ref + (best.log + log2f(total))) : -INFINITY;
+  }
+  __syncthreads();
+  for (int place = threadIdx.x >> 5; place < parts.held; place += Shape<D>::kThreads / 32) {
+    const int r = rank * parts.held + place, tok = it.tok0 + r / p.heads, h = it.head0 + r % p.heads;
+    if (!(ctl.odd[place / 32] >> (place % 32) & 1u) || !used(r)) continue;
+    const int64_t at = it.q0 + (int64_t)tok;
+    const int pos = it.m - (it.n - tok);
+    const int see_lo = p.window > 0 ? (int)max(INT64_C(0), min((int64_t)it.m, (int64_t)pos - p.window + 1)) : 0;
+    const int see_hi = p.causal ? max(0, min(it.m, pos + 1)) : it.m;
+    row_again<D>(p, p.q + at * p.q_stride + (int64_t)h * D, p.k + (int64_t)it.k0 * p.k_stride + (int64_t)it.kv * D,
+                 p.v + (int64_t)it.k0 * p.v_stride + (int64_t)it.kv * D, see_lo, see_hi, pos,
+                 p.slopes != nullptr ? __ldg(p.slopes + h) : 0.f, p.out + at * p.out_stride + (int64_t)h * D,
+                 p.lse == nullptr ? nullptr : p.lse + at * p.n_heads + h);
+  }
+}
+
+// Option: scores need more than a positive scale (a cap, slopes, another scale).  Split:
+// a cluster has one item (as a branch at run time it cost the loops registers: 4 x 1000
+// capped queries of 256 elements 156 us, so 168).
+template <int D, bool Option, bool Split>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tq,
                                                              const __grid_constant__ CUtensorMap tk,
                                                              const __grid_constant__ CUtensorMap tv, const PrefillArgs p) {
@@ -328,6 +422,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     for (int b = 0; b < kAhead; ++b) mbar_init(&item_full[b], 1), mbar_init(&item_empty[b], 2 + 4 * kTiles);
     mbar_init(&ctl.answered, 1);
     stop = 0;
+    if (Split)
+      for (int i = 0; i < 4; ++i) ctl.odd[i] = 0;
     fence_mbar_init();
     prefetch_tmap(&tq);
     prefetch_tmap(&tk);
@@ -343,6 +439,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
   const uint32_t tmem = ctl.tmem;
   pdl_wait();
   pdl_trigger();
+  const int rank = Split ? (int)cluster_rank() : 0;
+  bool met = false;  // this warp has been at the cluster's first barrier
 
   // The items, which warp 2 writes one after another: the other roles take each once.
   int turn = 0;
@@ -388,7 +486,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
                         &q_full[t]);
         }
         // in the order of their first use: keys one block ahead (with one tile, two)
-        if (it.last > 0) ok = ok && load(&tk, it, it.first);
+        if (it.first < it.last) ok = ok && load(&tk, it, it.first);
         if (kTiles == 1 && it.first + 1 < it.last) ok = ok && load(&tk, it, it.first + 1);
         for (int j = it.first; ok && j < it.last; ++j) {
           ok = load(&tv, it, j);
@@ -443,7 +541,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
       const Item &it = ctl.items[turn];
       if (uniform(it.n) == 0) break;
       const int first = uniform(it.first), last = uniform(it.last);
-      if (last == 0) {
+      if (first == last) {
       } else if constexpr (kTiles == 2) {
         const int lo[2] = {uniform(it.lo[0]), uniform(it.lo[1])}, hi[2] = {uniform(it.hi[0]), uniform(it.hi[1])};
         // a block of keys has a slot, which both tiles use; of values likewise
@@ -518,7 +616,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
       const int b = 32 * u + lane;
       counts[u] = held && b < p.B ? max(0, clamp_start(p.q_starts, b + 1, p.Tq) - clamp_start(p.q_starts, b, p.Tq) + T - 1) / T : 0;
     }
-    int64_t i = blockIdx.x;
+    int64_t i = Split ? blockIdx.x / p.splits : blockIdx.x;
     uint32_t answer_phase = 0;
     bool ok = true, first = true;
     while (ok) {
@@ -529,7 +627,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
       bool some = false;
       while (ok && !some) {
         if (!first) {
-          if (p.stride > 0) {
+          if (Split) {
+            i = -1;
+          } else if (p.stride > 0) {
             i = i + p.stride < p.items ? i + p.stride : -1;
           } else {
             if (lane == 0) {
@@ -548,7 +648,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         if (i < 0) break;
         const int r = (int)(i / groups), group = (int)(i % groups);
         const Piece at = held ? piece_of(counts, r) : piece_at(p, (int)(p.items / groups) - 1 - r, T);
-        some = at.b >= 0 && __shfl_sync(0xffffffffu, lane == 0 && item_of<D>(p, at.b, at.index, group, &it), 0);
+        some = at.b >= 0 && __shfl_sync(0xffffffffu, lane == 0 && item_of<D, Split>(p, at.b, at.index, group, rank, &it), 0);
       }
       if (!ok) break;
       if (lane == 0) {
@@ -768,6 +868,44 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
       if (rows) {
       const float2 s0 = unpack_f32x2(sum2[0]), s1 = unpack_f32x2(sum2[1]);
       const float sum = (s0.x + s0.y) + (s1.x + s1.y);
+      if constexpr (Split) {
+        const Parts parts = Parts::of<D>(p, it.n, it.tok0);
+        __syncwarp();
+        cluster_sync_all();  // nobody's keys, values and queries are needed any more
+        met = true;
+        const int r = t * p.tokens * p.heads + row, owner = r / parts.held, slot = rank * parts.held + r - owner * parts.held;
+        const bool push = row < p.tokens * p.heads && r < parts.rows;
+        const uint32_t to_stats = push ? map_to_rank(smem_u32(smem), (uint32_t)owner) : 0u;
+        const uint32_t to = push ? map_to_rank(smem_u32(ring), (uint32_t)owner) + (uint32_t)slot * (D * 4) : 0u;
+        if (push) st_cluster8(to_stats + 8 * slot, ref, lo < hi ? log2f(sum) : kNoPart);
+        const float inv = sum > 0.f || !(sum == sum) ? 1.f / sum : 0.f;
+        if (lo < hi) {
+          // by way of the warp's stage, as outputs are below: four rows of 128 bytes at a time
+          uint32_t at[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) at[i] = __shfl_sync(0xffffffffu, to, 4 * i + (lane >> 3));
+          uint8_t *stage = stages + (warp - 4) * kStage;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_o + c, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * inv);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              *reinterpret_cast<uint4 *>(stage + lane * 128 + (x ^ (lane & 7)) * 16) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 f = *reinterpret_cast<const float4 *>(stage + (4 * i + (lane >> 3)) * 128 + ((lane & 7) ^ (4 * i + (lane >> 3) & 7)) * 16);
+              if (at[i] != 0) st_cluster16(at[i] + 4 * c + 16 * (lane & 7), f.x, f.y, f.z, f.w);
+            }
+            __syncwarp();
+          }
+        }
+        break;
+      }
       const float inv = sum > 0.f || !(sum == sum) ? 1.f / sum : 0.f;
       // A thread's row of outputs is written by eight lanes, 16 bytes each, so that four
       // rows of 128 bytes leave at a time: through the warp's stage, where the 16-byte
@@ -831,6 +969,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
       if (++turn == kAhead) turn = 0, turn_phase ^= 1u;
     }
   }
+  if constexpr (Split) {
+    // the barriers are met by every warp, whether it gave up or not
+    __syncwarp();
+    if (!met) cluster_sync_all();
+    cluster_sync_all();  // the parts are there
+    if (!stop && ctl.items[0].n > 0) join_parts<D>(p, ctl, smem, ring, rank);
+  }
   __syncthreads();
   if (stop) {
     // copies and products in flight land before the memory goes away
@@ -862,17 +1007,47 @@ cudaError_t launch_d(PrefillArgs a, int sms, cudaStream_t s) {
       !map_rows(&tv, keys ? a.v : a.q, D, keys ? a.n_kv : 1, keys ? a.Tk : 1, keys ? a.v_stride : a.q_stride, 1, Z::kKeys))
     return cudaErrorInvalidValue;
   // a limit on the SMs: so many blocks, and every so-manieth item for each
-  a.stride = sms > 0 && sms < a.items ? sms : 0;
-  const int64_t grid = a.stride > 0 ? a.stride : a.items;
+  a.stride = a.splits == 1 && sms > 0 && sms < a.items ? sms : 0;
   const bool option = a.softcap > 0.f || a.slopes != nullptr || !(a.scale > 0.f);
-  return launch_pdl(option ? prefill_kernel<D, true> : prefill_kernel<D, false>, dim3((unsigned)grid), dim3(Z::kThreads), smem_bytes<D>(), s,
-                    tq, tk, tv, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.stride > 0 ? a.stride : a.items * a.splits));
+  cfg.blockDim = dim3(Z::kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<D>();
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.splits > 1 ? 2 : 1;
+  if (a.splits > 1) return cudaLaunchKernelEx(&cfg, option ? prefill_kernel<D, true, true> : prefill_kernel<D, false, true>, tq, tk, tv, a);
+  return cudaLaunchKernelEx(&cfg, option ? prefill_kernel<D, true, false> : prefill_kernel<D, false, false>, tq, tk, tv, a);
 }
 
 template <int D>
-cudaError_t ready_d() {
-  for (auto k : {prefill_kernel<D, true>, prefill_kernel<D, false>}) {
+cudaError_t ready_d(PrefillFit *fit) {
+  for (auto k : {prefill_kernel<D, true, false>, prefill_kernel<D, false, false>, prefill_kernel<D, true, true>, prefill_kernel<D, false, true>}) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
+    if (e != cudaSuccess) return e;
+  }
+  // (one CTA fills an SM's shared memory, whichever the kernel)
+  for (auto k : {prefill_kernel<D, true, true>, prefill_kernel<D, false, true>}) {
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (int i = 0; e == cudaSuccess && i < kSplitSizes; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(2u << i);
+      cfg.blockDim = dim3(Shape<D>::kThreads);
+      cfg.dynamicSmemBytes = smem_bytes<D>();
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2u << i;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&fit->clusters[i], k, &cfg);
+    }
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -880,7 +1055,7 @@ cudaError_t ready_d() {
 
 }  // namespace
 
-void plan_prefill(PrefillArgs *a, int d) {
+void plan_prefill(PrefillArgs *a, int d, int sms, const PrefillFit &fit) {
   // pieces of at most 16 heads, as even as may be
   const int per_kv = a->n_heads / a->n_kv;
   a->chunks = (per_kv + 15) / 16;
@@ -888,9 +1063,35 @@ void plan_prefill(PrefillArgs *a, int d) {
   a->tokens = 128 / a->heads;
   const int T = a->tokens * (d == 256 ? 1 : 2);
   a->items = ((int64_t)a->Tq / T + a->B) * a->n_kv * a->chunks;
+  // Few items leave SMs idle: a cluster then shares an item's blocks, where all clusters are
+  // resident at once and the blocks that a CTA is spared take longer than the join.  By the
+  // sequences' mean lengths, which are what the host knows; times in ns, of two full
+  // tiles.  us without and with (d 128 unless told):
+  //   1 query, 8001 keys, 32/8 heads        88   20.8 (8)
+  //   64 queries, 2064 keys, 32/8           32.7 22.4 (4)
+  //   128 queries, 8128 keys, 32/8          103  40.1 (4)
+  //   128 queries, 4128 keys, 16/8, d 256   62.2 28.8 (4)
+  //   1000 queries, 5000 keys, 16/1         66.0 48.2 (2)
+  //   1 query, 501 keys, 16/16              11.4 10.0 (4)
+  //   500 queries and keys, 16/16           13.5 15.5 (4), 18.4 (2): not taken
+  a->splits = 1;
+  const int keys = d == 256 ? 64 : 128;
+  const int64_t mean_q = (a->Tq + a->B - 1) / a->B, tokens = mean_q < T ? mean_q : T;
+  int64_t blocks = ((int64_t)a->Tk / a->B + keys - 1) / keys;
+  if (a->window > 0 && (a->window + tokens) / keys + 2 < blocks) blocks = (a->window + tokens) / keys + 2;
+  const int64_t block_ns = d == 256 ? 900 : 1500, join_ns = 2000 + 8000 * tokens / T;
+  int64_t best = blocks * block_ns;
+  for (int i = 0; i < kSplitSizes; ++i) {
+    const int splits = 2 << i;
+    const int64_t resident = fit.clusters[i] < sms / splits ? fit.clusters[i] : sms / splits;
+    const int64_t ns = (blocks + splits - 1) / splits * block_ns + join_ns;
+    if (a->items <= resident && ns < best) best = ns, a->splits = splits;
+  }
 }
 
-cudaError_t ready_prefill(int d) { return d == 64 ? ready_d<64>() : d == 128 ? ready_d<128>() : ready_d<256>(); }
+cudaError_t ready_prefill(int d, PrefillFit *fit) {
+  return d == 64 ? ready_d<64>(fit) : d == 128 ? ready_d<128>(fit) : ready_d<256>(fit);
+}
 
 cudaError_t launch_prefill(const PrefillArgs &a, int d, int sms, cudaStream_t s) {
   return d == 64 ? launch_d<64>(a, sms, s) : d == 128 ? launch_d<128>(a, sms, s) : launch_d<256>(a, sms, s);

@@ -27,11 +27,17 @@ struct PrefillArgs {
   int heads, chunks, tokens;
   int64_t items;  // tiles at most, times n_kv * chunks; below 2^31
   int stride;     // items between one and the next of a block; 0: asked for
+  int splits;     // CTAs of a cluster that share an item's blocks; 1: a block of the launch has whole ones
 };
-// Fills in heads, chunks, tokens and items.
-void plan_prefill(PrefillArgs *a, int d);
+// Clusters of 2, 4, 8 and 16 that are resident together.
+constexpr int kSplitSizes = 4;
+struct PrefillFit {
+  int clusters[kSplitSizes] = {};
+};
+// Fills in heads, chunks, tokens, items and splits, for so many SMs.
+void plan_prefill(PrefillArgs *a, int d, int sms, const PrefillFit &fit);
 // Readies the kernels of d.
-cudaError_t ready_prefill(int d);
+cudaError_t ready_prefill(int d, PrefillFit *fit);
 // sms: the SMs it may fill, 0 for all.
 cudaError_t launch_prefill(const PrefillArgs &a, int d, int sms, cudaStream_t s);
 

@@ -537,9 +537,10 @@ int moe_attn_decode_clusters(const moe_attn *a, const moe_paged_kv *kv, int64_t 
  *   slopes  : device f32 [n_heads] or NULL.
  *   out     : device bf16 rows like q; must not overlap q, k or v.
  *   lse     : device f32 [Tq, n_heads] contiguous, or NULL.
- * B <= 2^20.  The order of the sums follows from the sizes, the lengths and the
- * options alone: the same call gives the same bits.  No workspace is used but the
- * context's error flag.
+ * B <= 2^20.  Where few tiles of queries would leave SMs idle, clusters of up to 16
+ * CTAs share a tile's keys.  The order of the sums follows from the sizes, the
+ * lengths, the options and max_sms alone: the same call gives the same bits.  No
+ * workspace is used but the context's error flag.
  */
 int moe_attn_prefill(moe_attn *a, const void *q, int64_t q_stride, int64_t Tq, const void *k, int64_t k_stride,
                      const void *v, int64_t v_stride, int64_t Tk, const int32_t *q_starts,

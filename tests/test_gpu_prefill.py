@@ -327,6 +327,74 @@ def test_few_sms_give_the_same_bits():
     assert torch.equal(DecodeAttention(4, 4, 128, max_sms=3).prefill(q, k, v, dev(q0), dev(k0)), want)
 
 
+# Few queries and many keys: a cluster's CTAs share an item's keys.
+SPLIT = [
+    ([1], [3000], 8, 8, 128), ([1], [20001], 16, 1, 128), ([37], [2500], 8, 2, 128), ([64], [2064], 16, 4, 64),
+    ([20, 90], [3000, 1000], 8, 2, 256), ([1, 0, 64, 3], [3000, 0, 64, 2000], 8, 2, 128), ([5, 18, 19], [900, 5000, 901], 21, 3, 64),
+    ([9], [4000], 33, 1, 128), ([2] * 9, [1000 + 333 * i for i in range(9)], 2, 2, 256), ([300], [5000], 4, 1, 64), ([65], [129 * 64], 4, 4, 128),
+]
+
+
+@pytest.mark.parametrize("nq,nk,nh,nkv,d", SPLIT)
+def test_few_queries_and_many_keys(nq, nk, nh, nkv, d):
+    check(*inputs(nq, nk, nh, nkv, d, sum(nk) + nh, before=3, behind=5))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal,window,softcap,slopes", [
+    (False, 0, 0.0, None), (True, 1, 0.0, None), (True, 1500, 0.0, None), (False, 700, 3.0, None), (True, 0, 20.0, None),
+    (True, 0, 0.0, [0.5, 0.25, 0.001, -0.3, 0.0, 2.0]), (False, 0, 2.0, [0.01, -0.01, 0.001, -0.001, 0.0, 1e-4])])
+def test_few_queries_and_many_keys_with_options(d, causal, window, softcap, slopes):
+    q, k, v, q0, k0 = inputs([20, 1, 0, 40], [4000, 3333, 9, 2000], 6, 2, d, window + d, behind=2, size=2.0)
+    check(q, k, v, q0, k0, causal, softcap, None if slopes is None else torch.tensor(slopes, device=DEV), window)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("at", [0, 1500, 2990])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_hidden_values_of_shared_keys(d, at, what):
+    """The last query sees a value that is not finite, the others' outputs are as without it."""
+    q, k, v, q0, k0 = inputs([10], [2991], 4, 2, d, at + d)
+    attn = DecodeAttention(4, 2, d)
+    clean, lse = attn.prefill(q, k, v, dev(q0), dev(k0), window=2982 if at == 0 else 0, lse=torch.empty(10, 4, device=DEV))
+    v = v.clone()
+    v[at] = what
+    out, lse2 = attn.prefill(q, k, v, dev(q0), dev(k0), window=2982 if at == 0 else 0, lse=torch.empty(10, 4, device=DEV))
+    seen = torch.tensor([(at == 0 and i == 0) or (at == 1500) or (at == 2990 and i == 9) for i in range(10)], device=DEV)
+    assert torch.isfinite(out[~seen]).all() and not torch.isfinite(out[seen]).any() and torch.isfinite(lse2).all()
+    # a row that met a value that is not finite is computed again, with f32 weights: both outputs are
+    # within 2^-8 (|out| + sum p |v|) of the exact one, and sum p |v| is about 0.8
+    assert (out[~seen].float() - clean[~seen].float()).abs().max() < 0.02 if (~seen).any() else True
+    assert (lse2 - lse).abs().max() < 1e-4 and attn.status() == 0
+
+
+def test_shared_keys_on_streams_and_in_graphs():
+    q, k, v, q0, k0 = inputs([64, 1], [2064, 4000], 16, 4, 128, 5)
+    qs, ks = dev(q0), dev(k0)
+    attn = DecodeAttention(16, 4, 128)
+    want = attn.prefill(q, k, v, qs, ks).clone()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [torch.empty_like(want) for _ in range(24)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        attn.prefill(q, k, v, qs, ks, out=o, stream=streams[i % 3])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    g = torch.cuda.CUDAGraph()
+    out = torch.empty_like(want)
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            attn.prefill(q, k, v, qs, ks, out=out)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+    qs.copy_(dev([0, 3, 65]))  # read on the device
+    ks.copy_(dev([0, 0, 6064]))
+    g.replay()
+    assert torch.equal(out, attn.prefill(q, k, v, qs, ks)) and (out[:3] == 0).all() and attn.status() == 0
+
+
 def test_chunks_of_a_prompt_through_the_cache():
     """A prompt in chunks, each with the keys and values read back from the pages, is
     the prompt at once; its last token is the decode step's."""
