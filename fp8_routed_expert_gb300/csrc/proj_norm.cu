@@ -14,6 +14,10 @@
 // neighbouring lanes hold the 128 columns of a block, whose largest value is four
 // shuffles away.  A CTA keeps its columns' weights in registers over its rows, and
 // the next row's loads are issued before this row is finished.
+//
+// 4096 rows of 6144, with residual, bf16 and e4m3 outputs: 38 us, 5.97 TB/s, 88% of the
+// measured copy rate (issue slots 47%); 2048 rows of 16384 5.86 TB/s.  One row of 2048 takes
+// 1.65 us, which is a launch with one chain of loads and one of shuffles.
 #include "common.cuh"
 #include "kernels.h"
 #include "proj.h"
@@ -222,7 +226,9 @@ cudaError_t launch_group(const NormArgs &a, int vecs, int sms, cudaStream_t s) {
 }  // namespace
 
 // Lanes of a row and vectors of a lane: as few idle lanes as may be, and then as many
-// lanes, which hold less each.
+// lanes, which hold less each (one row of 2048 by 256 lanes 1.65 us, by 64 lanes of four
+// vectors 2.9).  The grid is what is resident: more CTAs than that load their weights
+// again (777 rows of 2880 5.1 us, so 4.6).
 cudaError_t launch_norm(const NormArgs &a, int sms, cudaStream_t s) {
   const int vecs = a.H / 8;
   int group = 0, per = 0;
