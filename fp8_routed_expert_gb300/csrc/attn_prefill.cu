@@ -243,30 +243,36 @@ __device__ __forceinline__ float option_score(float s, float scale, float cap, f
   return fmaf(slope, (float)back, s) * kLog2e;
 }
 
-// tanh(s * unit) of 32 scores.  Where all are below 0.6, which nearly all are, by the
-// polynomial, two at a time and without special-function instructions; else the warp
-// takes tanh_f32's both ways.
+// Caps up to here: cap tanh(y) = cap - 2 cap / (1 + e^2y), off by 2^-21 of the cap (the
+// score's unit) at most.  Above it tanh itself, whose error goes with the score.
+constexpr float kUsualCap = 4096.f;
+
+// 1 / (1 + 2^(s * unit)) of 32 scores, unit = 2 log2(e) scale / cap; or tanh(s * unit), unit =
+// scale / cap.  Four scores share a reciprocal (of a product below 2^121: from 2^30 on the
+// fraction no longer tells from zero): 8192 tokens, 16/8 heads of 64, 128 and 256
+// elements, 340, 362 and 438 us; two to a reciprocal 373, 373 and 462, one each 360, 369
+// and 531; tanh by a polynomial where all 32 are small 393, 419 and 487.  A NaN so reaches three
+// neighbours; the row is computed again in any case.
+template <bool Usual>
 __device__ __forceinline__ void cap_scores(uint32_t (&s)[32], float unit) {
-  float most = 0.f;
-#pragma unroll
-  for (int c = 0; c < 32; c += 2)
-    most = max3(most, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
-  if (__all_sync(0xffffffffu, most * fabsf(unit) < 0.6f)) {
-    const uint64_t u2 = pack_f32x2(unit, unit);
-    const auto both = [](float f) { return pack_f32x2(f, f); };
-#pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const uint64_t y = mul_f32x2(pack_f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), u2), z = mul_f32x2(y, y);
-      uint64_t t = fma_f32x2(z, both(kTanh[4]), both(kTanh[3]));
-      t = fma_f32x2(z, t, both(kTanh[2]));
-      t = fma_f32x2(z, t, both(kTanh[1]));
-      t = fma_f32x2(z, t, both(kTanh[0]));
-      const float2 f = unpack_f32x2(fma_f32x2(mul_f32x2(y, z), t, y));
-      s[c] = __float_as_uint(f.x), s[c + 1] = __float_as_uint(f.y);
-    }
-  } else {
+  if constexpr (!Usual) {
 #pragma unroll
     for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(tanh_f32(__uint_as_float(s[c]) * unit));
+    return;
+  }
+  const uint64_t u2 = pack_f32x2(unit, unit), one = pack_f32x2(1.f, 1.f);
+#pragma unroll
+  for (int c = 0; c < 32; c += 4) {
+    const auto power = [&](int k) {
+      const float2 x = unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), u2));
+      return add_f32x2(pack_f32x2(exp2_fast(min_nan(x.x, 30.f)), exp2_fast(min_nan(x.y, 30.f))), one);
+    };
+    const uint64_t f = power(c), g = power(c + 2), fg = mul_f32x2(f, g);
+    const float2 q = unpack_f32x2(fg);
+    const float r = rcp_fast(q.x * q.y);
+    const uint64_t t = mul_f32x2(pack_f32x2(q.y, q.x), pack_f32x2(r, r));
+    const float2 a = unpack_f32x2(mul_f32x2(t, g)), b = unpack_f32x2(mul_f32x2(t, f));
+    s[c] = __float_as_uint(a.x), s[c + 1] = __float_as_uint(a.y), s[c + 2] = __float_as_uint(b.x), s[c + 3] = __float_as_uint(b.y);
   }
 }
 
@@ -402,10 +408,12 @@ __device__ __noinline__ void join_parts(const PrefillArgs &p, Control<D> &ctl, u
   }
 }
 
-// Option: scores need more than a positive scale (a cap, slopes, another scale).  Split:
-// a cluster has one item (as a branch at run time it cost the loops registers: 4 x 1000
-// capped queries of 256 elements 156 us, so 168).
-template <int D, bool Option, bool Split>
+// Options: scores need more than a positive scale (a cap, slopes, another scale); kFar with a
+// cap above kUsualCap.  Split: a cluster has one item.  (As branches at run time either
+// cost the loops registers: 4 x 1000 capped queries of 256 elements 141 us, 157 with the
+// caps' two ways, 168 with the split before that.)
+enum Options { kNone, kSome, kFar };
+template <int D, Options Kind, bool Split>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tq,
                                                              const __grid_constant__ CUtensorMap tk,
                                                              const __grid_constant__ CUtensorMap tv, const PrefillArgs p) {
@@ -684,9 +692,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     const int row = (warp & 3) * 32 + lane;  // of the tile
     const uint32_t t_o = tmem + lanes + Z::kO + t * D;
     const int r_tok = row / p.heads, r_head = row - r_tok * p.heads;
+    constexpr bool Option = Kind != kNone, usual = Kind != kFar;
     const bool capped = Option && p.softcap > 0.f, sloped = Option && p.slopes != nullptr;
-    const float unit = capped ? __fdividef(p.scale, p.softcap) : 0.f;
-    const float scale2 = (capped ? p.softcap : p.scale) * kLog2e;
+    const float unit = capped ? (usual ? 2.f * kLog2e : 1.f) * (p.scale / p.softcap) : 0.f;
+    const float scale2 = (!capped ? p.scale : usual ? -2.f * p.softcap : p.softcap) * kLog2e, offset = capped && usual ? p.softcap * kLog2e : 0.f;
     uint32_t step = 0;  // blocks that the tile has had
     bool ok = true;
     const auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -751,7 +760,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         // reference.  A slope's share is near * (key - pos): of every eighth key by itself,
         // so that it is off by a unit or two of the distance's.
         const auto exponents = [&](uint32_t(&x)[32], int c0, float minus) {
-          if (capped) cap_scores(x, unit);
+          if (capped) cap_scores<usual>(x, unit), minus += offset;
           const uint64_t mul = pack_f32x2(scale2, scale2);
           if (sloped) {
             const float base = fmaf(near, (float)(key0 + c0 - pos), minus);
@@ -1015,7 +1024,7 @@ cudaError_t launch_d(PrefillArgs a, int sms, cudaStream_t s) {
     return cudaErrorInvalidValue;
   // a limit on the SMs: so many blocks, and every so-manieth item for each
   a.stride = a.splits == 1 && sms > 0 && sms < a.items ? sms : 0;
-  const bool option = a.softcap > 0.f || a.slopes != nullptr || !(a.scale > 0.f);
+  const Options kind = a.softcap > kUsualCap ? kFar : a.softcap > 0.f || a.slopes != nullptr || !(a.scale > 0.f) ? kSome : kNone;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.stride > 0 ? a.stride : a.items * a.splits));
   cfg.blockDim = dim3(Z::kThreads);
@@ -1029,18 +1038,22 @@ cudaError_t launch_d(PrefillArgs a, int sms, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.splits > 1 ? 2 : 1;
-  if (a.splits > 1) return cudaLaunchKernelEx(&cfg, option ? prefill_kernel<D, true, true> : prefill_kernel<D, false, true>, tq, tk, tv, a);
-  return cudaLaunchKernelEx(&cfg, option ? prefill_kernel<D, true, false> : prefill_kernel<D, false, false>, tq, tk, tv, a);
+  const auto kernel = a.splits > 1   ? kind == kNone ? prefill_kernel<D, kNone, true> : prefill_kernel<D, kSome, true>
+                      : kind == kNone ? prefill_kernel<D, kNone, false>
+                      : kind == kSome ? prefill_kernel<D, kSome, false>
+                                      : prefill_kernel<D, kFar, false>;
+  return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, a);
 }
 
 template <int D>
 cudaError_t ready_d(PrefillFit *fit) {
-  for (auto k : {prefill_kernel<D, true, false>, prefill_kernel<D, false, false>, prefill_kernel<D, true, true>, prefill_kernel<D, false, true>}) {
+  for (auto k : {prefill_kernel<D, kNone, false>, prefill_kernel<D, kSome, false>, prefill_kernel<D, kFar, false>, prefill_kernel<D, kNone, true>,
+                 prefill_kernel<D, kSome, true>}) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
     if (e != cudaSuccess) return e;
   }
   // (one CTA fills an SM's shared memory, whichever the kernel)
-  for (auto k : {prefill_kernel<D, true, true>, prefill_kernel<D, false, true>}) {
+  for (auto k : {prefill_kernel<D, kNone, true>, prefill_kernel<D, kSome, true>}) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     for (int i = 0; e == cudaSuccess && i < kSplitSizes; ++i) {
       cudaLaunchConfig_t cfg = {};
@@ -1083,12 +1096,12 @@ void plan_prefill(PrefillArgs *a, int d, int sms, const PrefillFit &fit) {
   //   500 queries and keys, 16/16           13.5 15.5 (4), 18.4 (2): not taken
   a->splits = 1;
   const int keys = d == 256 ? 64 : 128;
-  const int64_t mean_q = (a->Tq + a->B - 1) / a->B, tokens = mean_q < T ? mean_q : T;
+  const int64_t mean_q = ((int64_t)a->Tq + a->B - 1) / a->B, tokens = mean_q < T ? mean_q : T;
   int64_t blocks = ((int64_t)a->Tk / a->B + keys - 1) / keys;
   if (a->window > 0 && (a->window + tokens) / keys + 2 < blocks) blocks = (a->window + tokens) / keys + 2;
   const int64_t block_ns = d == 256 ? 900 : 1500, join_ns = 2000 + 8000 * tokens / T;
   int64_t best = blocks * block_ns;
-  for (int i = 0; i < kSplitSizes; ++i) {
+  for (int i = 0; i < kSplitSizes && a->softcap <= kUsualCap; ++i) {  // (a cap above it is rare)
     const int splits = 2 << i;
     const int64_t resident = fit.clusters[i] < sms / splits ? fit.clusters[i] : sms / splits;
     const int64_t ns = (blocks + splits - 1) / splits * block_ns + join_ns;

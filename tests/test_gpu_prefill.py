@@ -327,6 +327,21 @@ def test_few_sms_give_the_same_bits():
     assert torch.equal(DecodeAttention(4, 4, 128, max_sms=3).prefill(q, k, v, dev(q0), dev(k0)), want)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("cap", [4096.0, 4097.0, 1e6, 1e30])
+def test_caps_far_above_the_scores(d, cap):
+    """|s| < 40 makes s - cap tanh(s / cap) at most 40^3 / (3 cap^2) < 2e-3: the same outputs as without a
+    cap, weights off by that and by the cap's own error, 2^-21 cap where the cap is at most 4096."""
+    q, k, v, q0, k0 = inputs([150, 9], [200, 700], 4, 2, d, 77)
+    attn = DecodeAttention(4, 2, d)
+    want, wlse = attn.prefill(q, k, v, dev(q0), dev(k0), lse=torch.empty(159, 4, device=DEV))
+    out, lse = attn.prefill(q, k, v, dev(q0), dev(k0), softcap=cap, lse=torch.empty(159, 4, device=DEV))
+    off = 40 ** 3 / (3 * cap * cap) + (2.0 ** -21 * cap if cap <= 4096 else 0) + 2.0 ** -18
+    size = torch.from_numpy(A.prefill(f64(q), f64(k), f64(v), q0, k0, d ** -0.5)[2]).to(DEV)  # sum p |v|
+    assert ((lse - wlse).abs() <= off + 2 * U * wlse.abs()).all()
+    assert ((out.double() - want.double()).abs() <= 2 * 2.0 ** -8 * want.double().abs() + (2 * 2.0 ** -8 + 2 * off) * size).all()
+
+
 # Few queries and many keys: a cluster's CTAs share an item's keys.
 SPLIT = [
     ([1], [3000], 8, 8, 128), ([1], [20001], 16, 1, 128), ([37], [2500], 8, 2, 128), ([64], [2064], 16, 4, 64),
