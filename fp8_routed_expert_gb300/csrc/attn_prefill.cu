@@ -28,7 +28,7 @@
 // again (below).  Rows that have no reference yet take it from the block itself, which is
 // then read twice.  With slopes, which lower the scores of far keys, blocks go from the
 // last to the first: the first reference is then the largest (forwards it moves, and O is
-// rewritten, in every block: 8192 tokens, 16 heads of 128 elements, 305 us, so 242).
+// rewritten, in every block: 8192 tokens, 16 heads of 128 elements, 305 us, so 245 at that step).
 // Without them forwards is 3% faster, as an item's two tiles start together.
 //
 // What bounds it: 16384 tokens, 32 heads over 8 of 128 elements, take 1350 us, 1630
@@ -36,7 +36,7 @@
 // products take about the same time.  With 256 elements 1365 TFLOP/s (one tile), with 64
 // 995 (the exponentials are twice as many per product).  12 prompts of up to 2048 in 109
 // us: the tensor cores are busy 47% of it, as masked blocks cost twice, and an item has
-// few of them to spread its first and last steps over; 60 of up to 700 with slopes 118.
+// few of them to spread its first and last steps over; 60 of up to 700 with slopes 100.
 //
 // Weights are rounded to bf16 for the second product, the matrix unit's type for bf16
 // values: 2^-8 of each weight at most, and independent from key to key; the sum is of
@@ -408,11 +408,12 @@ __device__ __noinline__ void join_parts(const PrefillArgs &p, Control<D> &ctl, u
   }
 }
 
-// Options: scores need more than a positive scale (a cap, slopes, another scale); kFar with a
-// cap above kUsualCap.  Split: a cluster has one item.  (As branches at run time either
-// cost the loops registers: 4 x 1000 capped queries of 256 elements 141 us, 157 with the
-// caps' two ways, 168 with the split before that.)
-enum Options { kNone, kSome, kFar };
+// What scores need beyond a scale: nothing, slopes, a cap (and slopes), a cap above kUsualCap
+// (and slopes).  Split: a cluster has one item.  (As branches at run time
+// these cost the loops registers: 4 x 1000 capped queries of 256 elements 141 us, 157 with
+// the caps' two ways, 168 with the split before that; 60 prompts of up to 700
+// with slopes 115, so 100.)
+enum Options { kNone, kSloped, kCapped, kFar };
 template <int D, Options Kind, bool Split>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tq,
                                                              const __grid_constant__ CUtensorMap tk,
@@ -693,7 +694,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     const uint32_t t_o = tmem + lanes + Z::kO + t * D;
     const int r_tok = row / p.heads, r_head = row - r_tok * p.heads;
     constexpr bool Option = Kind != kNone, usual = Kind != kFar;
-    const bool capped = Option && p.softcap > 0.f, sloped = Option && p.slopes != nullptr;
+    constexpr bool capped = Kind >= kCapped;
+    const bool sloped = Kind == kSloped || (capped && p.slopes != nullptr);
     const float unit = capped ? (usual ? 2.f * kLog2e : 1.f) * (p.scale / p.softcap) : 0.f;
     const float scale2 = (!capped ? p.scale : usual ? -2.f * p.softcap : p.softcap) * kLog2e, offset = capped && usual ? p.softcap * kLog2e : 0.f;
     uint32_t step = 0;  // blocks that the tile has had
@@ -1024,7 +1026,7 @@ cudaError_t launch_d(PrefillArgs a, int sms, cudaStream_t s) {
     return cudaErrorInvalidValue;
   // a limit on the SMs: so many blocks, and every so-manieth item for each
   a.stride = a.splits == 1 && sms > 0 && sms < a.items ? sms : 0;
-  const Options kind = a.softcap > kUsualCap ? kFar : a.softcap > 0.f || a.slopes != nullptr || !(a.scale > 0.f) ? kSome : kNone;
+  const Options kind = a.softcap > kUsualCap ? kFar : a.softcap > 0.f ? kCapped : a.slopes != nullptr ? kSloped : kNone;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.stride > 0 ? a.stride : a.items * a.splits));
   cfg.blockDim = dim3(Z::kThreads);
@@ -1038,22 +1040,23 @@ cudaError_t launch_d(PrefillArgs a, int sms, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.splits > 1 ? 2 : 1;
-  const auto kernel = a.splits > 1   ? kind == kNone ? prefill_kernel<D, kNone, true> : prefill_kernel<D, kSome, true>
-                      : kind == kNone ? prefill_kernel<D, kNone, false>
-                      : kind == kSome ? prefill_kernel<D, kSome, false>
-                                      : prefill_kernel<D, kFar, false>;
-  return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, a);
+  const auto whole = kind == kNone ? prefill_kernel<D, kNone, false>
+                     : kind == kSloped ? prefill_kernel<D, kSloped, false>
+                     : kind == kCapped ? prefill_kernel<D, kCapped, false>
+                                       : prefill_kernel<D, kFar, false>;
+  const auto split = kind == kNone ? prefill_kernel<D, kNone, true> : kind == kSloped ? prefill_kernel<D, kSloped, true> : prefill_kernel<D, kCapped, true>;
+  return cudaLaunchKernelEx(&cfg, a.splits > 1 ? split : whole, tq, tk, tv, a);
 }
 
 template <int D>
 cudaError_t ready_d(PrefillFit *fit) {
-  for (auto k : {prefill_kernel<D, kNone, false>, prefill_kernel<D, kSome, false>, prefill_kernel<D, kFar, false>, prefill_kernel<D, kNone, true>,
-                 prefill_kernel<D, kSome, true>}) {
+  for (auto k : {prefill_kernel<D, kNone, false>, prefill_kernel<D, kSloped, false>, prefill_kernel<D, kCapped, false>, prefill_kernel<D, kFar, false>,
+                 prefill_kernel<D, kNone, true>, prefill_kernel<D, kSloped, true>, prefill_kernel<D, kCapped, true>}) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
     if (e != cudaSuccess) return e;
   }
   // (one CTA fills an SM's shared memory, whichever the kernel)
-  for (auto k : {prefill_kernel<D, kNone, true>, prefill_kernel<D, kSome, true>}) {
+  for (auto k : {prefill_kernel<D, kNone, true>, prefill_kernel<D, kSloped, true>, prefill_kernel<D, kCapped, true>}) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     for (int i = 0; e == cudaSuccess && i < kSplitSizes; ++i) {
       cudaLaunchConfig_t cfg = {};
