@@ -58,6 +58,6 @@ struct MatmulFit {
 cudaError_t ready_matmul(MatmulFit *fit);
 // Fills in the plan for M, N, K (blocks) on at most `sms` SMs.
 void plan_matmul(const MatmulFit &fit, int sms, MatmulArgs *m);
-cudaError_t launch_matmul(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, cudaStream_t s);
+cudaError_t launch_matmul(const CUtensorMap &a, const CUtensorMap &w, const CUtensorMap &o, const MatmulArgs &m, cudaStream_t s);
 
 }  // namespace fp8moe

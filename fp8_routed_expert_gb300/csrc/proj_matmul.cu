@@ -13,11 +13,16 @@
 // What bounds it.  Few rows: launch, one chain of loads, products, sums and, where tiles
 // are split, the exchange: 1 x 6144 x 2048 takes 6.3 to 7.2 us where the weights alone take
 // 1.9 at the copy rate, 64 x 8192 x 4096 10.4 of 5.1.  Many: 4096 x 8192 x 6144 takes
-// 173 us, 2380 TFLOP/s, with the tensor cores busy 55% of the time and a block of 128 x
-// 256 in 1000 cycles, of which its products take about 520.  The rest goes with the sums: they
-// read every block's 128 KB from TMEM while products update TMEM too, and neither more
-// summing warps (16: 200 to 217 us) nor loads that run ahead of the sums (196; of 32
-// columns, which spill, 219 and more) made that shorter.
+// 162 to 164 us, 2530 TFLOP/s: a block of 128 x 256 in about 880 cycles, of which its
+// products take 520.  A summing warp waits 140 of them and adds up for 650 (its packed FMAs
+// alone take 290 of a sub-partition's issue); between tiles go 2500.  16 summing warps
+// (200 to 217 us) were no faster.
+//
+// Outputs of tiles of 256 columns leave by TMA from boxes in shared memory, which takes
+// one block in flight of the ring: a row per lane stored 32 bytes at a time, the tile's end
+// took 8000 cycles, in which the products run two blocks ahead at most (173 us, so 169;
+// 4000 x 8000 x 208 27.3, so 22.2).  The narrower tiles' rows are short: through shared
+// memory 512 x 4096 x 4096 took 14.8 instead of 13.7.
 //
 // A tile's K blocks may be split over the CTAs of a cluster (few tiles): each CTA
 // owns as many rows, and each pushes its sums of the others' rows into their
@@ -45,6 +50,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // between.
 constexpr int kHeld = 16, kScales = kRows + 2;
 constexpr int kMostStages = 8;
+constexpr int kOutBytes = 32 * 128 * 2;  // a summing warp's outputs of a tile of 256 columns
 
 // Quarters: of a tile's 128 rows (TMEM's lanes by warp) that are of use.  With one or two,
 // which a warp each adds up, two CTAs of 64 columns fit on an SM (a sub-partition then has
@@ -101,7 +107,8 @@ __device__ __forceinline__ void store8(const MatmulArgs &p, int64_t row, int64_t
 
 template <int Columns, int Quarters>
 __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::kThreads, Quarters < 4 ? 2 : 1) matmul_kernel(const __grid_constant__ CUtensorMap ta,
-                                                             const __grid_constant__ CUtensorMap tw, const MatmulArgs p) {
+                                                             const __grid_constant__ CUtensorMap tw,
+                                                             const __grid_constant__ CUtensorMap to, const MatmulArgs p) {
   using R = Ring<Columns, Quarters>;
   constexpr int kMine = Columns / R::kGroups;  // columns of a summing warp
   extern __shared__ uint8_t smem_raw[];
@@ -248,6 +255,11 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
         }
         tc_fence_after();
         const int here = min(R::kTurn, it.b1 - b);
+        const auto give_back = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sum_empty[buf]);
+        };
         if (any) {
           float c[R::kTurn];  // (the products were of operands that came with these scales)
 #pragma unroll
@@ -256,25 +268,43 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
             c[u] = sc[quarter * 32 + lane] * sc[kRows + group * kMine / 128];
           }
           const uint32_t from = t_lane + (uint32_t)(buf * R::kTurn * Columns);
-#pragma unroll
-          for (int u = 0; u < R::kTurn; ++u) {
-            if (u >= here) break;
-            const uint64_t cc = pack_f32x2(c[u], c[u]);
+          if constexpr (Columns == 256) {
+            // the next 16 columns on their way while these are added, and the buffer given
+            // back before the last are (4096 x 8192 x 6144: 169 us, so 164; the narrow
+            // tiles' warps take turns by themselves: 512 x 4096 x 4096 13.6, so 14.6)
+            const uint64_t cc = pack_f32x2(c[0], c[0]);
+            uint32_t v[2][16];
+            tmem_ld16(from, v[0]);
+            tmem_wait_ld16(v[0]);
 #pragma unroll
             for (int l = 0; l < kMine; l += 16) {
-              uint32_t v[16];
-              tmem_ld16(from + u * Columns + l, v);
-              tmem_wait_ld16(v);
+              uint32_t(&x)[16] = v[l / 16 & 1], (&next)[16] = v[l / 16 & 1 ^ 1];
+              if (l + 16 < kMine) tmem_ld16(from + l + 16, next);
+              if (l + 16 == kMine) give_back();
 #pragma unroll
               for (int j = 0; j < 16; j += 2)
-                acc[(l + j) / 2] = fma_f32x2(pack_f32x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), cc, acc[(l + j) / 2]);
+                acc[(l + j) / 2] = fma_f32x2_in_order(pack_f32x2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), cc, acc[(l + j) / 2]);
+              if (l + 16 < kMine) tmem_wait_ld16(next);
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < R::kTurn; ++u) {
+              if (u >= here) break;
+              const uint64_t cc = pack_f32x2(c[u], c[u]);
+#pragma unroll
+              for (int l = 0; l < kMine; l += 16) {
+                uint32_t v[16];
+                tmem_ld16(from + u * Columns + l, v);
+                tmem_wait_ld16(v);
+#pragma unroll
+                for (int j = 0; j < 16; j += 2)
+                  acc[(l + j) / 2] = fma_f32x2(pack_f32x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), cc, acc[(l + j) / 2]);
+              }
             }
           }
         }
         count += (uint32_t)here;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sum_empty[buf]);
+        if (Columns < 256 || !any) give_back();
         buf ^= 1;
         if (buf == 0) bphase ^= 1u;
       }
@@ -284,6 +314,32 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
       asm volatile("" : "+l"(again));
       const Item at = item_of<Columns>(p, again, rank);
       const int64_t row = at.m0 + quarter * 32 + lane, col = at.n0 + group * kMine;
+      if constexpr (Columns == 256) {
+        // 64 columns at a time into the warp's boxes, which leave by themselves
+        if (!ok || !any) continue;
+        if (lane == 0) bulk_wait_read<0>();  // the tile before
+        __syncwarp();
+        uint8_t *box = smem + p.sums_at + (warp - 4) * kOutBytes;
+#pragma unroll
+        for (int j = 0; j < kMine; j += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack_f32x2(acc[j / 2 + i]);
+            w[i] = bf16x2_of(f.x, f.y);
+          }
+          *reinterpret_cast<uint4 *>(box + j / 64 * 4096 + lane * 128 + ((j / 8 & 7) ^ (lane & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+          for (int j = 0; j < kMine; j += 64)
+            if (col + j < p.N) tma_store_2d(&to, box + j / 64 * 4096, (int)col + j, at.m0 + quarter * 32);
+          bulk_commit();
+        }
+        continue;
+      }
       if (!ok || !any || row >= p.M) continue;
       if (splits == 1) {
         __nv_bfloat16 *out = p.out + row * p.out_stride + col;
@@ -324,6 +380,7 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
         }
       }
     }
+    if (Columns == 256 && lane == 0) bulk_wait<0>();
   }
   __syncwarp();
   if (splits > 1) {
@@ -361,7 +418,7 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
 }
 
 template <int Columns, int Quarters>
-cudaError_t launch_one(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, cudaStream_t s) {
+cudaError_t launch_one(const CUtensorMap &a, const CUtensorMap &w, const CUtensorMap &o, const MatmulArgs &m, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)m.grid);
   cfg.blockDim = dim3(Ring<Columns, Quarters>::kThreads);
@@ -375,7 +432,7 @@ cudaError_t launch_one(const CUtensorMap &a, const CUtensorMap &w, const MatmulA
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = m.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, matmul_kernel<Columns, Quarters>, a, w, m);
+  return cudaLaunchKernelEx(&cfg, matmul_kernel<Columns, Quarters>, a, w, o, m);
 }
 
 // Shared memory of a CTA where one or two of them have an SM.
@@ -423,14 +480,15 @@ cudaError_t ready_matmul(MatmulFit *fit) {
 // How a product is split.  A tile's K blocks go over as many CTAs as are resident
 // together: clusters that come in a second round double the time (48 clusters of three
 // where 46 are resident, 1 x 6144 x 2048: 11.3 us, 96 clusters of two 6.3).  The time is
-// about, in cycles: a block 420, 560 and 1040 for 64, 128 and 256 columns (260 with few
-// rows), a tile's start and end 2000, 2600 and 4000, a cluster's exchange 150 for each CTA
+// about, in cycles: a block 420, 560 and 880 for 64, 128 and 256 columns (260 with few
+// rows), a tile's start and end 2000, 2600 and 2500, a cluster's exchange 150 for each CTA
 // and what a CTA pushes at 12 bytes.  Against the best of all splits (us):
 //   64 x 2048 x 2048      5.3: 64 columns, 4 CTAs; 8 CTAs 6.1, alone 7.3
 //   333 x 1000 x 2880     8.4: 64, 2; 128 columns, 4 CTAs 9.2, alone 10.4 (2)
-//   512 x 4096 x 4096     15.7: 128, alone; 256 columns 19.9
-//   700 x 7000 x 512      11.8: 128, alone; 256 columns 12.8
-//   2048 x 4096 x 2048    23.8: 256, alone; 128 columns 31.0
+//   512 x 4096 x 4096     13.9: 128, alone; 256 columns 18.7
+//   700 x 512 x 7008      11.4: 128, 5; 64, 2 CTAs 12.2; 128 alone 14.4 (2)
+//   800 x 7000 x 400      10.9: 256, alone; 128 columns 11.7
+//   2048 x 2048 x 4096    19.5: 256, alone; 128 columns 24.7
 void plan_matmul(const MatmulFit &fit, int sms, MatmulArgs *m) {
   const bool few = m->M <= 64;
   const int64_t rows = (m->M + kRows - 1) / kRows;
@@ -444,8 +502,8 @@ void plan_matmul(const MatmulFit &fit, int sms, MatmulArgs *m) {
       const int64_t most = (int64_t)sms * (few ? 2 : 1) / splits, resident = places[splits] < most ? places[splits] : most;
       if (splits > 1 && (tiles > resident || columns == 256)) continue;
       const double rounds = (double)((tiles + resident - 1) / (resident > 0 ? resident : 1));
-      const double block = few ? 260.0 : columns == 64 ? 420.0 : columns == 128 ? 560.0 : 1040.0;
-      const double around = columns == 64 ? 2000.0 : columns == 128 ? 2600.0 : 4000.0;
+      const double block = few ? 260.0 : columns == 64 ? 420.0 : columns == 128 ? 560.0 : 880.0;
+      const double around = columns == 64 ? 2000.0 : columns == 128 ? 2600.0 : 2500.0;
       double t = rounds * ((double)((m->blocks + splits - 1) / splits) * block + around);
       if (splits > 1) t += 150.0 * splits + (double)(m->M < kRows ? m->M : kRows) * columns * 4 * (splits - 1) / splits / 12.0;
       if (m->columns == 0 || t < best) {
@@ -462,7 +520,7 @@ void plan_matmul(const MatmulFit &fit, int sms, MatmulArgs *m) {
   m->a_bytes = few ? m->a_rows * kBlock : kRows * kBlock;  // whole 8-row atoms of 1024 bytes
   const int sum_rows = m->M < kRows ? (int)m->M : kRows;
   m->held = (sum_rows + m->splits - 1) / m->splits;
-  const int sums = m->splits > 1 ? m->held * m->splits * m->columns * 4 : 0;
+  const int sums = m->columns == 256 ? 8 * kOutBytes : m->splits > 1 ? m->held * m->splits * m->columns * 4 : 0;
   const int stage = m->a_bytes + m->columns * kBlock;
   // a product reads 128 rows of either operand: those behind the last stage's few rows are
   // of no use, but have to be there
@@ -474,12 +532,12 @@ void plan_matmul(const MatmulFit &fit, int sms, MatmulArgs *m) {
   m->smem = m->scales_at + kAround;
 }
 
-cudaError_t launch_matmul(const CUtensorMap &a, const CUtensorMap &w, const MatmulArgs &m, cudaStream_t s) {
-  if (m.few) return m.M <= 32 ? launch_one<64, 1>(a, w, m, s) : launch_one<64, 2>(a, w, m, s);
+cudaError_t launch_matmul(const CUtensorMap &a, const CUtensorMap &w, const CUtensorMap &o, const MatmulArgs &m, cudaStream_t s) {
+  if (m.few) return m.M <= 32 ? launch_one<64, 1>(a, w, o, m, s) : launch_one<64, 2>(a, w, o, m, s);
   switch (m.columns) {
-    case 64: return launch_one<64, 4>(a, w, m, s);
-    case 128: return launch_one<128, 4>(a, w, m, s);
-    default: return launch_one<256, 4>(a, w, m, s);
+    case 64: return launch_one<64, 4>(a, w, o, m, s);
+    case 128: return launch_one<128, 4>(a, w, o, m, s);
+    default: return launch_one<256, 4>(a, w, o, m, s);
   }
 }
 
