@@ -187,13 +187,13 @@ int moe_proj_matmul(moe_proj *p, const uint8_t *a, int64_t a_stride, const float
   CUtensorMap ta, tw, to;
   const uint64_t a_sizes[2] = {(uint64_t)K, (uint64_t)M}, a_strides[1] = {(uint64_t)a_stride};
   const uint64_t w_sizes[2] = {(uint64_t)K, (uint64_t)N}, w_strides[1] = {(uint64_t)w_stride};
-  const uint64_t o_sizes[2] = {(uint64_t)N, (uint64_t)M}, o_strides[1] = {(uint64_t)out_stride * 2};
+  const uint64_t o_sizes[2] = {(uint64_t)(N & ~INT64_C(7)), (uint64_t)M}, o_strides[1] = {(uint64_t)out_stride * 2};
   const uint32_t a_box[2] = {128, (uint32_t)m.a_rows}, w_box[2] = {128, (uint32_t)m.columns}, o_box[2] = {64, 32};
   PROJ_TRY(cudaSetDevice(p->device));
   if (!encode_tile_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a, a_sizes, a_strides, a_box) ||
       !encode_tile_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, w, w_sizes, w_strides, w_box))
     return MOE_ERR_CUDA;
-  if (m.columns < 256) to = tw;  // (only the widest tiles' outputs leave by TMA)
+  if (m.columns < 256) to = tw;  // (only the widest tiles' outputs leave by TMA, N well above 8)
   else if (!encode_tile_map(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, o_sizes, o_strides, o_box)) return MOE_ERR_CUDA;
   p->last_stream = s;
   PROJ_TRY(launch_matmul(ta, tw, to, m, s));

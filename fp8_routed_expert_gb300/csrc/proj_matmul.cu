@@ -315,7 +315,8 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
       const Item at = item_of<Columns>(p, again, rank);
       const int64_t row = at.m0 + quarter * 32 + lane, col = at.n0 + group * kMine;
       if constexpr (Columns == 256) {
-        // 64 columns at a time into the warp's boxes, which leave by themselves
+        // 64 columns at a time into the warp's boxes, which leave by themselves, but for up to
+        // seven last columns: a box is cut off at 16 bytes, which would reach behind the row
         if (!ok || !any) continue;
         if (lane == 0) bulk_wait_read<0>();  // the tile before
         __syncwarp();
@@ -330,12 +331,17 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
           }
           *reinterpret_cast<uint4 *>(box + j / 64 * 4096 + lane * 128 + ((j / 8 & 7) ^ (lane & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        const int rest = (int)(p.N & 7), j = (int)(p.N - rest - col);
+        if (rest != 0 && j >= 0 && j < kMine && row < p.M) {
+          const uint16_t *last = reinterpret_cast<const uint16_t *>(box + j / 64 * 4096 + lane * 128 + ((j / 8 & 7) ^ (lane & 7)) * 16);
+          for (int i = 0; i < rest; ++i) p.out[row * p.out_stride + col + j + i] = __ushort_as_bfloat16(last[i]);
+        }
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
 #pragma unroll
           for (int j = 0; j < kMine; j += 64)
-            if (col + j < p.N) tma_store_2d(&to, box + j / 64 * 4096, (int)col + j, at.m0 + quarter * 32);
+            if (col + j < (p.N & ~INT64_C(7))) tma_store_2d(&to, box + j / 64 * 4096, (int)col + j, at.m0 + quarter * 32);
           bulk_commit();
         }
         continue;

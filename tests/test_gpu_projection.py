@@ -185,6 +185,16 @@ def test_matmul_rows_at_the_borders(proj, M):
     assert (wide[0] == 9).all() and (wide[-1] == 9).all() and (wide[:, 520:] == 9).all()
 
 
+@pytest.mark.parametrize("M,N", [(1300, 2100), (1281, 2049), (1313, 2064), (2000, 2239), (4000, 257)])
+def test_matmul_outputs_of_wide_tiles_stay_in_their_rows(proj, M, N):
+    """Tiles of 256 columns whose last rows and columns lie outside, within wider rows."""
+    a, sa, w, sw = make(gen(M), M, N, 300)
+    wide = torch.full((M + 2, -(-N // 8) * 8 + 24), 9.0, dtype=torch.bfloat16, device=DEV)
+    got = check_matmul(proj, a, sa, w, sw, wide[1:-1, 8:8 + N])
+    assert (wide[0] == 9).all() and (wide[-1] == 9).all() and (wide[:, :8] == 9).all() and (wide[:, 8 + N:] == 9).all()
+    assert torch.equal(proj.matmul(a, sa, w, sw), got)
+
+
 def test_matmul_strides(proj):
     """Rows within wider ones, scales in either order, output within wider rows."""
     g = gen(5)
