@@ -239,7 +239,7 @@ __device__ __forceinline__ bool item_of(const PrefillArgs &p, int b, int index, 
 // A row's score after the products: in units of log2, options applied.
 __device__ __forceinline__ float option_score(float s, float scale, float cap, float slope, int back) {
   s *= scale;
-  if (cap > 0.f) s = cap * tanh_f32(__fdividef(s, cap));
+  if (cap > 0.f) s = cap * tanh_f32(s / cap);
   return fmaf(slope, (float)back, s) * kLog2e;
 }
 
@@ -1055,22 +1055,23 @@ cudaError_t ready_d(PrefillFit *fit) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
     if (e != cudaSuccess) return e;
   }
-  // (one CTA fills an SM's shared memory, whichever the kernel)
   for (auto k : {prefill_kernel<D, kNone, true>, prefill_kernel<D, kSloped, true>, prefill_kernel<D, kCapped, true>}) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    for (int i = 0; e == cudaSuccess && i < kSplitSizes; ++i) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(2u << i);
-      cfg.blockDim = dim3(Shape<D>::kThreads);
-      cfg.dynamicSmemBytes = smem_bytes<D>();
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2u << i;
-      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      e = cudaOccupancyMaxActiveClusters(&fit->clusters[i], k, &cfg);
-    }
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  // (one CTA fills an SM's shared memory, so the answer is the same for each kernel)
+  for (int i = 0; i < kSplitSizes; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2u << i);
+    cfg.blockDim = dim3(Shape<D>::kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<D>();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2u << i;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&fit->clusters[i], prefill_kernel<D, kNone, true>, &cfg);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

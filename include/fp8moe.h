@@ -525,6 +525,7 @@ int moe_attn_decode_clusters(const moe_attn *a, const moe_paged_kv *kv, int64_t 
  * A query with no visible key gives out = 0 and lse = -infinity.  Rows outside the
  * sequences are not read as keys or values of any, and out and lse are left as they
  * are there.  What hidden keys and values hold does not matter, NaN included.
+ * A cap of at most 4096 is off by 2^-21 of it at most, one above by as much of the score.
  * Sums and softmax statistics are f32; for their product with the values, weights
  * are rounded to bf16 (2^-8 of each at most, as the output is); out is rounded to bf16.
  *   q       : device bf16 [Tq, n_heads, d] rows as for moe_attn_norm_rope (a slice of
