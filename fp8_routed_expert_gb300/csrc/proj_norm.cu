@@ -21,8 +21,10 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "proj.h"
+#include "tcgen05_ops.cuh"
 
 namespace fp8moe {
+using namespace sm100;
 namespace {
 
 constexpr int kCta = 256;  // threads, unless a row takes more
@@ -51,6 +53,30 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // above 2^120 (infinite and NaN ones too), or below 2^-90 where eps does not
 // outweigh it.
 __device__ __forceinline__ bool beyond(float ss, float eps) { return !(ss <= 0x1p120f) || (ss < 0x1p-90f && eps < 0x1p-90f); }
+
+// Quotients y / s to f32 for s from 2^-90 on, rounded once as a division's are (those
+// below 2^-10, whose code is zero, may be off by a unit).  Times the rounded inverse
+// alone, values next to a tie of two codes go to the other one, a code in 2000.  Markstein
+// (1990): a quotient within a unit, corrected by its residual times the correctly rounded
+// inverse, is the rounded one; the first product may be off by 1.5 units, so it is
+// corrected twice.  4096 rows of 6144 take 38.1 us as without (777 of 2880 4.9, so 4.5); a
+// division each takes 42.4 (8.7).  Zeros keep their sign, and an infinity becomes a NaN, as the format has
+// none.
+struct Divisor {
+  uint64_t s, inv, minus;
+  __device__ __forceinline__ explicit Divisor(float v) : s(pack_f32x2(v, v)) {
+    const float i = 1.f / v;
+    inv = pack_f32x2(i, i);
+    minus = pack_f32x2(-i, -i);
+  }
+  __device__ __forceinline__ float2 quotients(float y0, float y1) const {
+    const uint64_t y = pack_f32x2(-y0, -y1);
+    uint64_t q = mul_f32x2(pack_f32x2(y0, y1), inv);
+    q = fma_f32x2(fma_f32x2(q, s, y), minus, q);
+    q = fma_f32x2(fma_f32x2(q, s, y), minus, q);
+    return unpack_f32x2(q);
+  }
+};
 
 // Sum over the group's lanes, the same bits in each.  Groups of more than a warp
 // pass the CTA's barrier once; *odd tells, alike for all that share a barrier,
@@ -185,14 +211,18 @@ __global__ void __launch_bounds__(Group > kCta ? Group : kCta) norm_kernel(const
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
         // a scale is a normal number, so that its inverse is one too
-        const float scale = am > 0.f ? fmaxf(am / 448.f, 0x1p-126f) : 1.f, inv = 1.f / scale;
+        const float scale = am > 0.f ? fmaxf(am / 448.f, 0x1p-126f) : 1.f;
+        float divisor = scale;
+        if (scale < 0x1p-90f) {  // residuals below would leave f32: y and the divisor at 2^64 times their size
+          divisor *= 0x1p64f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[i][j] *= 0x1p64f;
+        }
+        const Divisor by(divisor);
         uint32_t c[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // y / scale; an infinity becomes a NaN (y * 0), the format has none
-          const float2 q = make_float2(fmaf(y[i][2 * j], 0.f, y[i][2 * j] * inv), fmaf(y[i][2 * j + 1], 0.f, y[i][2 * j + 1] * inv));
-          c[j] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
-        }
+        for (int j = 0; j < 4; ++j)
+          c[j] = __nv_cvt_float2_to_fp8x2(by.quotients(y[i][2 * j], y[i][2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
         if (t < a.T && v < vecs) {
           *reinterpret_cast<uint2 *>(a.codes + t * a.codes_stride + 8 * v) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
           if ((v & 15) == 0) a.scales[t * a.scale_row + (v >> 4) * a.scale_block] = scale;

@@ -317,3 +317,19 @@ def test_refusals(proj):
     p.close()
     with pytest.raises(ValueError):
         p.norm(x)
+
+
+@pytest.mark.parametrize("T,H,size", [(300, 1000, 1.0), (40, 6144, 3.0), (1, 2048, 1e3), (65, 16384, 1e-4), (900, 136, 1e-33), (50, 512, 1e-36), (50, 512, 1e-38),
+                                      (70, 256, 1e35)])
+def test_codes_are_those_of_the_quotient(proj, T, H, size):
+    """Rows quantised as they are: scale and quotient are one f32 division each, and the code the
+    quotient's nearest, so every bit follows."""
+    x = rows(gen(T), T, H, size)
+    x[0, 5], x[-1, 7] = 0.0, -0.0
+    codes, scales = proj.norm_quant(x)
+    y = x.float().cpu().numpy()
+    s = np.stack([np.abs(y[:, c:c + 128]).max(1) for c in range(0, H, 128)], 1) / np.float32(448)
+    s = np.where(s == 0, np.float32(1), np.maximum(s, np.float32(2.0 ** -126)))
+    assert s.dtype == np.float32 and (scales.cpu().numpy() == s).all()
+    want = torch.from_numpy(y / P.spread(s, H)).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(codes.cpu(), want)
