@@ -60,8 +60,8 @@ __device__ __forceinline__ bool beyond(float ss, float eps) { return !(ss <= 0x1
 // (1990): a quotient within a unit, corrected by its residual times the correctly rounded
 // inverse, is the rounded one; the first product may be off by 1.5 units, so it is
 // corrected twice.  4096 rows of 6144 take 38.1 us as without (777 of 2880 4.9, so 4.5); a
-// division each takes 42.4 (8.7).  Zeros keep their sign, and an infinity becomes a NaN, as the format has
-// none.
+// division each takes 42.4 (8.7).  Zeros keep their sign, and an infinity becomes a NaN, as
+// the format has none.
 struct Divisor {
   uint64_t s, inv, minus;
   __device__ __forceinline__ explicit Divisor(float v) : s(pack_f32x2(v, v)) {
@@ -184,10 +184,11 @@ __global__ void __launch_bounds__(Group > kCta ? Group : kCta) norm_kernel(const
         eps = a.eps * pre * pre;
       }
       const float r = rsqrtf(fmaf(ss, n, eps));
+      // the normed value first: 1 / rms times a weight may leave f32 where the output does not
 #pragma unroll
       for (int i = 0; i < Vecs; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[i][j] *= r * w[i][j];
+        for (int j = 0; j < 8; ++j) y[i][j] = y[i][j] * r * w[i][j];
     }
     turn ^= 1;
     if (t < a.T) {

@@ -333,3 +333,15 @@ def test_codes_are_those_of_the_quotient(proj, T, H, size):
     assert s.dtype == np.float32 and (scales.cpu().numpy() == s).all()
     want = torch.from_numpy(y / P.spread(s, H)).to(torch.float8_e4m3fn).view(torch.uint8)
     assert torch.equal(codes.cpu(), want)
+
+
+@pytest.mark.parametrize("H", [64, 1000, 4096])
+def test_norm_with_weights_far_from_one(proj, H):
+    """Rows and weights whose products are ordinary numbers, though 1 / rms times a weight is not
+    one; eps 0."""
+    g = gen(H)
+    for size, weight in ((1e-12, 1e30), (1e15, 1e-30), (1e-30, 1e20), (1e25, 1e-20)):
+        x = (torch.randn(9, H, generator=g, device=DEV) * size).to(torch.bfloat16)
+        w = (torch.rand(H, generator=g, device=DEV) + 0.5) * weight
+        y = P.norm(f64(x), f64(w), 0.0)
+        close(proj.norm(x, w, eps=0.0), y, (2.0 ** -8 + 32 * U) * np.abs(y))
