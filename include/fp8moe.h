@@ -614,7 +614,10 @@ int moe_proj_norm(moe_proj *p, const void *x, int64_t x_stride, const void *resi
  * moe_proj_matmul - product of e4m3 rows with e4m3 weights:
  *   out[m, n] = bf16( sum over blocks b of 128 of K of
  *       a_scale[m, b] * w_scale[n / 128, b] * sum over k in b of a[m, k] * w[n, k] )
- * Sums are f32, rounded once at the end.
+ * Sums are f32, rounded once at the end.  The product of a block's two scales is
+ * formed first, in f32: scales as moe_proj_norm and the experts' format have them
+ * stay well within, but one below 2^-126 keeps fewer bits, and one beyond f32 gives
+ * infinities or NaN, whatever the result would be.
  *   a       : device u8 e4m3 codes, row m at m * a_stride, 16-byte aligned, a_stride
  *             a multiple of 16 and at least K.
  *   a_scale : device f32, as moe_proj_norm writes them.

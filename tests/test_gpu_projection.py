@@ -345,3 +345,27 @@ def test_norm_with_weights_far_from_one(proj, H):
         w = (torch.rand(H, generator=g, device=DEV) + 0.5) * weight
         y = P.norm(f64(x), f64(w), 0.0)
         close(proj.norm(x, w, eps=0.0), y, (2.0 ** -8 + 32 * U) * np.abs(y))
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 300, 700), (50, 200, 300), (200, 130, 640), (300, 1100, 400), (1500, 1500, 300)])
+def test_matmul_scales_at_the_ends_of_f32(proj, M, N, K):
+    """A block's two scales multiply to normal f32 numbers, down to the smallest and up to where the
+    results end, though one of them or both are far outside.  Half a step of results below bf16's
+    normal ones is 2^-134."""
+    def check(a, sa, w, sw):
+        want, size = P.matmul(a.cpu().numpy(), f64(sa), w.cpu().numpy(), f64(sw))
+        close(proj.matmul(a, sa, w, sw), want, 2.0 ** -8 * np.abs(want) + (K / 4 + K / 64 + 24) * U * size + 2.0 ** -134)
+        assert proj.status() == 0 and np.abs(want).max() < 3e38
+
+    g = gen(M)
+    a, sa, w, sw = make(g, M, N, K)
+    sa, sw = sa.clamp(0.5, 2.0), (sw * 1e4).clamp(0.5, 2.0)
+    a[(a & 0x7F) == 0] = 0x38
+    # 2^-124 / 4 is the smallest normal number; subnormal scales on either side
+    for da, dw in ((2.0 ** -62, 2.0 ** -62), (2.0 ** -140, 2.0 ** 16), (2.0 ** 20, 2.0 ** -144), (2.0 ** -124, 1.0), (2.0 ** 100, 2.0 ** -60), (2.0 ** 50, 2.0 ** 50)):
+        check(a, sa * da, w, sw * dw)
+    # zeros and scales that are not finite stay in their rows
+    s0 = sa.clone()
+    s0[0], s0[1] = 0.0, float("inf")
+    got = proj.matmul(a, s0, w, sw)
+    assert (got[0] == 0).all() and not torch.isfinite(got[1]).any() and torch.equal(got[2:], proj.matmul(a, sa, w, sw)[2:])
