@@ -446,3 +446,28 @@ def test_refusals():
     attn.close()
     with pytest.raises(ValueError):
         attn.prefill(q, k, v, qs, ks)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal,softcap,slope", [(True, 0.0, 0.0), (False, 0.0, 0.0), (True, 0.0, 2.0 ** -20), (True, 64.0, 0.0), (True, 300.0, 0.0)])
+@pytest.mark.parametrize("at", [[300], [0, 300], [5, 140, 141, 700]])
+def test_a_key_that_has_all_of_the_weight(d, causal, softcap, slope, at):
+    """One key's score is 25 to 45 above all others', whose weights together stay below 1000 e^-25 < 2^-26: the
+    output is its value to the bit, however the weights were rounded.  Several such keys share one value."""
+    q, k, v, q0, k0 = inputs([300, 40], [900, 800], 4, 2, d, d + len(at))
+    g = gen(5)
+    k, v = torch.zeros_like(k), (torch.rand(v.shape, generator=g, device=DEV) + 1).to(torch.bfloat16)
+    q = torch.zeros_like(q)
+    q[..., 0] = 25 + 20 * torch.rand(q.shape[:2], generator=g, device=DEV)
+    q[..., 1] = torch.rand(q.shape[:2], generator=g, device=DEV)
+    for start in (0, 900):
+        for j in at:
+            k[start + j, :, :2] = 1.0
+            v[start + j] = v[start + at[0]]
+    attn = DecodeAttention(4, 2, d)
+    sl = torch.full((4,), slope, device=DEV) if slope else None
+    out = attn.prefill(q, k, v, dev(q0), dev(k0), causal=causal, scale=1.0, softcap=softcap, slopes=sl)
+    for start, a, e, n in ((0, 0, 300, 900), (900, 300, 340, 800)):
+        first = a if not causal else max(a, a + at[0] - (n - (e - a)))
+        want = v[start + at[0]].repeat_interleave(2, 0)
+        assert (out[first:e] == want).all(), int((out[first:e] != want).sum())
