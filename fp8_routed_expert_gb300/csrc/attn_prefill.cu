@@ -248,21 +248,45 @@ __device__ __forceinline__ float option_score(float s, float scale, float cap, f
   return fmaf(slope, (float)back, s) * kLog2e;
 }
 
-// Caps up to here: cap tanh(y) = cap - 2 cap / (1 + e^2y), off by 2^-21 of the cap (the
-// score's unit) at most.  Above it tanh itself, whose error goes with the score.
-constexpr float kUsualCap = 4096.f;
+// Caps up to here: cap tanh(y) = cap - 2 cap / (1 + e^2y).  The quotient is off by seven
+// halves of a step or less (its sum with 1, four products, a reciprocal of two) and what
+// the power of two adds, and the constants and the difference by a few more: 2^-19 of the
+// cap, which at 128 is 2.4e-4 of a score.  Above it tanh itself, whose error goes with the
+// score, 2^-20 of it.  (8192 tokens, 16/8 heads of 64, 128 and 256 elements, a cap of 400:
+// 386, 410 and 468 us, with the cap's way 334, 359 and 443.)
+constexpr float kUsualCap = 128.f;
 
 // 1 / (1 + 2^(s * unit)) of 32 scores, unit = 2 log2(e) scale / cap; or tanh(s * unit), unit =
 // scale / cap.  Four scores share a reciprocal (of a product below 2^121: from 2^30 on the
 // fraction no longer tells from zero): 8192 tokens, 16/8 heads of 64, 128 and 256
 // elements, 340, 362 and 438 us; two to a reciprocal 373, 373 and 462, one each 360, 369
-// and 531; tanh by a polynomial where all 32 are small 393, 419 and 487.  A NaN so reaches three
+// and 531.  tanh without its polynomial: 693, 717 and 1078.  A NaN so reaches three
 // neighbours; the row is computed again in any case.
 template <bool Usual>
 __device__ __forceinline__ void cap_scores(uint32_t (&s)[32], float unit) {
   if constexpr (!Usual) {
+    // Where all 32 are below 0.6, which nearly all are under so high a cap, by the
+    // polynomial, two at a time; else the warp takes tanh_f32's both ways.
+    float most = 0.f;
 #pragma unroll
-    for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(tanh_f32(__uint_as_float(s[c]) * unit));
+    for (int c = 0; c < 32; c += 2) most = max3(most, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
+    if (__all_sync(0xffffffffu, most * fabsf(unit) < 0.6f)) {
+      const uint64_t u2 = pack_f32x2(unit, unit);
+      const auto both = [](float f) { return pack_f32x2(f, f); };
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        const uint64_t y = mul_f32x2(pack_f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), u2), z = mul_f32x2(y, y);
+        uint64_t t = fma_f32x2(z, both(kTanh[4]), both(kTanh[3]));
+        t = fma_f32x2(z, t, both(kTanh[2]));
+        t = fma_f32x2(z, t, both(kTanh[1]));
+        t = fma_f32x2(z, t, both(kTanh[0]));
+        const float2 f = unpack_f32x2(fma_f32x2(mul_f32x2(y, z), t, y));
+        s[c] = __float_as_uint(f.x), s[c + 1] = __float_as_uint(f.y);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(tanh_f32(__uint_as_float(s[c]) * unit));
+    }
     return;
   }
   const uint64_t u2 = pack_f32x2(unit, unit), one = pack_f32x2(1.f, 1.f);
@@ -1053,18 +1077,21 @@ cudaError_t launch_d(PrefillArgs a, int sms, cudaStream_t s) {
                      : kind == kSloped ? prefill_kernel<D, kSloped, false>
                      : kind == kCapped ? prefill_kernel<D, kCapped, false>
                                        : prefill_kernel<D, kFar, false>;
-  const auto split = kind == kNone ? prefill_kernel<D, kNone, true> : kind == kSloped ? prefill_kernel<D, kSloped, true> : prefill_kernel<D, kCapped, true>;
+  const auto split = kind == kNone ? prefill_kernel<D, kNone, true>
+                     : kind == kSloped ? prefill_kernel<D, kSloped, true>
+                     : kind == kCapped ? prefill_kernel<D, kCapped, true>
+                                       : prefill_kernel<D, kFar, true>;
   return cudaLaunchKernelEx(&cfg, a.splits > 1 ? split : whole, tq, tk, tv, a);
 }
 
 template <int D>
 cudaError_t ready_d(PrefillFit *fit) {
   for (auto k : {prefill_kernel<D, kNone, false>, prefill_kernel<D, kSloped, false>, prefill_kernel<D, kCapped, false>, prefill_kernel<D, kFar, false>,
-                 prefill_kernel<D, kNone, true>, prefill_kernel<D, kSloped, true>, prefill_kernel<D, kCapped, true>}) {
+                 prefill_kernel<D, kNone, true>, prefill_kernel<D, kSloped, true>, prefill_kernel<D, kCapped, true>, prefill_kernel<D, kFar, true>}) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
     if (e != cudaSuccess) return e;
   }
-  for (auto k : {prefill_kernel<D, kNone, true>, prefill_kernel<D, kSloped, true>, prefill_kernel<D, kCapped, true>}) {
+  for (auto k : {prefill_kernel<D, kNone, true>, prefill_kernel<D, kSloped, true>, prefill_kernel<D, kCapped, true>, prefill_kernel<D, kFar, true>}) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
@@ -1114,7 +1141,7 @@ void plan_prefill(PrefillArgs *a, int d, int sms, const PrefillFit &fit) {
   if (a->window > 0 && (a->window + tokens) / keys + 2 < blocks) blocks = (a->window + tokens) / keys + 2;
   const int64_t block_ns = d == 256 ? 900 : 1500, join_ns = 2000 + 8000 * tokens / T;
   int64_t best = blocks * block_ns;
-  for (int i = 0; i < kSplitSizes && a->softcap <= kUsualCap; ++i) {  // (a cap above it is rare)
+  for (int i = 0; i < kSplitSizes; ++i) {
     const int splits = 2 << i;
     const int64_t resident = fit.clusters[i] < sms / splits ? fit.clusters[i] : sms / splits;
     const int64_t ns = (blocks + splits - 1) / splits * block_ns + join_ns;

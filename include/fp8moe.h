@@ -525,9 +525,10 @@ int moe_attn_decode_clusters(const moe_attn *a, const moe_paged_kv *kv, int64_t 
  * A query with no visible key gives out = 0 and lse = -infinity.  Rows outside the
  * sequences are not read as keys or values of any, and out and lse are left as they
  * are there.  What hidden keys and values hold does not matter, NaN included.
- * A cap of at most 4096 is off by 2^-21 of it at most, one above by as much of the score.
  * Sums and softmax statistics are f32; for their product with the values, weights
  * are rounded to bf16 (2^-8 of each at most, as the output is); out is rounded to bf16.
+ * A cap of at most 128 makes a score off by 2^-19 of the cap at most, one above by 2^-20
+ * of the score.
  *   q       : device bf16 [Tq, n_heads, d] rows as for moe_attn_norm_rope (a slice of
  *             a fused projection's rows is fine), Tq <= 2^31 - 1.
  *   k, v    : device bf16 [Tk, n_kv_heads, d] rows like q, Tk <= 2^31 - 1.

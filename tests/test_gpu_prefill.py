@@ -471,3 +471,33 @@ def test_a_key_that_has_all_of_the_weight(d, causal, softcap, slope, at):
         first = a if not causal else max(a, a + at[0] - (n - (e - a)))
         want = v[start + at[0]].repeat_interleave(2, 0)
         assert (out[first:e] == want).all(), int((out[first:e] != want).sum())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("nk", [700, 5])
+@pytest.mark.parametrize("cap", [2.0, 30.0, 50.0, 100.0, 127.9, 129.0, 400.0, 1000.0, 4096.0, 5000.0, 1e5])
+def test_caps_at_the_stated_bound(d, nk, cap):
+    """A score is off by 2^-19 of a cap up to 128 and by 2^-20 of itself above, with the sums' and the exponentials'
+    own errors; lse is off by as much, an output by the weights' 2^-8 and twice the scores'."""
+    q, k, v, q0, k0 = inputs([150, 9], [nk + 150, nk], 4, 2, d, int(cap) + nk, size=2.0)
+    q[::7] *= 3
+    attn = DecodeAttention(4, 2, d)
+    out, lse = attn.prefill(q, k, v, dev(q0), dev(k0), softcap=cap, lse=torch.empty(159, 4, device=DEV))
+    Q, K, V = f64(q), f64(k), f64(v)
+    want, wlse, size = A.prefill(Q, K, V, q0, k0, d ** -0.5, softcap=cap)
+    n = 0
+    for b in range(2):
+        for h in range(4):
+            a, e, c, f = q0[b], q0[b + 1], k0[b], k0[b + 1]
+            reach = (np.abs(Q[a:e, h]) @ np.abs(K[c:f, h // 2]).T).max(1) * d ** -0.5
+            s = np.abs(Q[a:e, h] @ K[c:f, h // 2].T).max(1) * d ** -0.5
+            off = (d / 2 + 16) * U * reach + (2.0 ** -19 * cap if cap <= 128 else 2.0 ** -20 * np.minimum(s, cap))
+            off = off + 2.0 ** -20 + ((f - c) / 2 + 64) * U
+            z, o, wz = f64(lse)[a:e, h], f64(out)[a:e, h], wlse[a:e, h]
+            assert (np.isneginf(z) == np.isneginf(wz)).all()  # no visible key
+            z, wz = (np.where(np.isneginf(x), 0.0, x) for x in (z, wz))
+            assert (np.abs(z - wz) <= off + 2 * U * np.abs(wz)).all(), (np.abs(z - wz) / off).max()
+            tol = 2.0 ** -8 * np.abs(want[a:e, h]) + (2.0 ** -8 + 2 * off[:, None]) * size[a:e, h]
+            assert (np.abs(o - want[a:e, h]) <= tol).all()
+            n += 1
+    assert n == 8 and attn.status() == 0
