@@ -50,7 +50,8 @@
 // Blocks that no row sees are not visited; masks are applied in blocks that not all
 // rows see in full.  A hidden value's weight is zero, but zero times an infinity or a
 // NaN is not: a row whose output is not finite is computed again from its visible
-// keys alone, one warp per row (row_again).
+// keys alone, one warp per row (row_again), which is slow but bounded (the
+// limit of the other roles' waits counts on it).
 //
 // A launch has a block per item, the longest first; a running one asks for the next
 // item that has not started (cluster launch control), so no counter in memory is
@@ -71,7 +72,9 @@ namespace fp8moe {
 using namespace sm100;
 namespace {
 
-constexpr uint64_t kWaitNs = 2000000000ull;
+// A wait's limit: two seconds, and what a warp's 32 rows take where they are computed
+// again (row_again), 5 us for each key, four times over: the other roles wait meanwhile.
+constexpr uint64_t kWaitNs = 2000000000ull, kWaitNsPerKey = 20000ull;
 constexpr int kStage = 32 * 128;  // bytes in which a warp turns 64 columns of its 32 rows of outputs
 constexpr float kMove = 8.f;  // log2 of how far a score may exceed the reference
 
@@ -307,11 +310,16 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[32], float unit) {
 
 // One row from its visible keys alone, by a warp: for rows that met values which are
 // not finite.  32 keys at a time, a lane scoring one; then lane l adds up the
-// elements l * D / 32 ... of their values. 
+// elements l * D / 32 ... of their values, sixteen keys on their way.  Two to five us for 32
+// keys, a hundred times what they take in a tile: 4096 tokens, 8 heads of 128 elements, whose
+// first value is a NaN 13.4 ms instead of 0.12 (18.8 with a key at a time).
 template <int D>
 __device__ __noinline__ void row_again(const PrefillArgs &p, const __nv_bfloat16 *q, const __nv_bfloat16 *k, const __nv_bfloat16 *v,
                                        int lo, int hi, int pos, float slope, __nv_bfloat16 *out, float *lse) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, kAtOnce = 16;
+  struct alignas(2 * E) Part {
+    uint32_t two[E / 2];
+  };
   const int lane = threadIdx.x & 31;
   float acc[E], m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -322,7 +330,7 @@ __device__ __noinline__ void row_again(const PrefillArgs &p, const __nv_bfloat16
     if (lane < here) {
       const __nv_bfloat16 *row = k + (int64_t)(j0 + lane) * p.k_stride;
       s = 0.f;
-#pragma unroll 4
+#pragma unroll 8
       for (int e = 0; e < D; e += 8) {
         const uint4 a = *reinterpret_cast<const uint4 *>(q + e), b = *reinterpret_cast<const uint4 *>(row + e);
 #pragma unroll
@@ -339,11 +347,21 @@ __device__ __noinline__ void row_again(const PrefillArgs &p, const __nv_bfloat16
     l = fmaf(l, keep, warp_sum(w));
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= keep;
-    for (int j = 0; j < here; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, w, j);
-      const __nv_bfloat16 *row = v + (int64_t)(j0 + j) * p.v_stride + lane * E;
+    const __nv_bfloat16 *first = v + (int64_t)j0 * p.v_stride + lane * E;
+#pragma unroll 1
+    for (int j = 0; j < here; j += kAtOnce) {
+      Part x[kAtOnce];
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(wj, __bfloat162float(row[e]), acc[e]);
+      for (int u = 0; u < kAtOnce; ++u) x[u] = *reinterpret_cast<const Part *>(first + (int64_t)min(j + u, here - 1) * p.v_stride);
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const float wj = __shfl_sync(0xffffffffu, w, j + u);
+        if (j + u < here) {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            acc[e] = fmaf(wj, e % 2 == 0 ? bf16_bits_to_float(x[u].two[e / 2] & 0xffffu) : __uint_as_float(x[u].two[e / 2] & 0xffff0000u), acc[e]);
+        }
+      }
     }
   }
 #pragma unroll
@@ -491,7 +509,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
   int turn = 0;
   uint32_t turn_phase = 0;
   const auto item_ready = [&] {  // false: it gave up
-    if (mbar_wait(&item_full[turn], turn_phase, nullptr, kWaitNs)) return true;
+    if (mbar_wait(&item_full[turn], turn_phase, nullptr, p.wait_ns)) return true;
     give_up(&stop, p.err);
     return false;
   };
@@ -500,7 +518,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
       int slot = 0;
       uint32_t phase = 0, q_phase = 0;  // q_phase: a bit per tile
       const auto load = [&](const CUtensorMap *map, const Item &it, int j) {
-        if (!mbar_wait(&kv_empty[slot], phase ^ 1u, &stop, kWaitNs)) {
+        if (!mbar_wait(&kv_empty[slot], phase ^ 1u, &stop, p.wait_ns)) {
           give_up(&stop, p.err);
           return false;
         }
@@ -518,7 +536,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
           if (it.lo[t] >= it.hi[t]) continue;
-          if (!mbar_wait(&q_empty[t], (q_phase >> t & 1u) ^ 1u, &stop, kWaitNs)) {
+          if (!mbar_wait(&q_empty[t], (q_phase >> t & 1u) ^ 1u, &stop, p.wait_ns)) {
             give_up(&stop, p.err);
             ok = false;
             break;
@@ -551,7 +569,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     uint32_t phase = 0, q_phase = 0, p_phase = 0;
     bool ok = true;
     const auto wait = [&](uint64_t *bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &stop, kWaitNs));
+      ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &stop, p.wait_ns));
       if (!ok) give_up(&stop, p.err);
       tc_fence_after();
       return ok;
@@ -667,7 +685,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     while (ok) {
       // An item is asked for once there is room to keep it: those that are kept for
       // longer could be another block's.
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&item_empty[turn], turn_phase ^ 1u, &stop, kWaitNs)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&item_empty[turn], turn_phase ^ 1u, &stop, p.wait_ns)))) break;
       Item &it = ctl.items[turn];
       bool some = false;
       while (ok && !some) {
@@ -682,7 +700,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
               request_block(ctl.answer, &ctl.answered);
             }
             __syncwarp();
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.answered, answer_phase, &stop, kWaitNs)))) break;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctl.answered, answer_phase, &stop, p.wait_ns)))) break;
             answer_phase ^= 1u;
             i = requested_block(ctl.answer);
             __syncwarp();
@@ -730,7 +748,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     uint32_t step = 0;  // blocks that the tile has had
     bool ok = true;
     const auto wait = [&](uint64_t *bar, uint32_t parity) {
-      if (ok && !mbar_wait(bar, parity, &stop, kWaitNs)) {
+      if (ok && !mbar_wait(bar, parity, &stop, p.wait_ns)) {
         give_up(&stop, p.err);
         ok = false;
       }
@@ -1058,6 +1076,7 @@ cudaError_t launch_d(PrefillArgs a, int sms, cudaStream_t s) {
       !map_rows(&tv, keys ? a.v : a.q, D, keys ? a.n_kv : 1, keys ? a.Tk : 1, keys ? a.v_stride : a.q_stride, 1, Z::kKeys))
     return cudaErrorInvalidValue;
   // a limit on the SMs: so many blocks, and every so-manieth item for each
+  a.wait_ns = kWaitNs + kWaitNsPerKey * (uint64_t)a.Tk;
   a.stride = a.splits == 1 && sms > 0 && sms < a.items ? sms : 0;
   const Options kind = a.softcap > kUsualCap ? kFar : a.softcap > 0.f ? kCapped : a.slopes != nullptr ? kSloped : kNone;
   cudaLaunchConfig_t cfg = {};

@@ -22,6 +22,7 @@ struct PrefillArgs {
   int64_t out_stride;
   float *lse;
   int *err;
+  uint64_t wait_ns;  // the limit of a wait
   // The query heads of a key/value head are taken `heads` at a time, in `chunks`
   // pieces; a tile's 128 rows are the heads of `tokens` tokens.
   int heads, chunks, tokens;

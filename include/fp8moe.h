@@ -524,7 +524,10 @@ int moe_attn_decode_clusters(const moe_attn *a, const moe_paged_kv *kv, int64_t 
  *   out[i, h] = softmax(s) V,  lse[i, h] = log(sum_j exp(s_j)).
  * A query with no visible key gives out = 0 and lse = -infinity.  Rows outside the
  * sequences are not read as keys or values of any, and out and lse are left as they
- * are there.  What hidden keys and values hold does not matter, NaN included.
+ * are there.  What hidden keys and values hold does not matter, NaN included; but a row
+ * that meets infinities or NaN, hidden ones in blocks that it reads or visible ones, and
+ * one whose scores rise by more than 88 within a block, is computed a second time, a
+ * hundred times as slowly.
  * Sums and softmax statistics are f32; for their product with the values, weights
  * are rounded to bf16 (2^-8 of each at most, as the output is); out is rounded to bf16.
  * A cap of at most 128 makes a score off by 2^-19 of the cap at most, one above by 2^-20

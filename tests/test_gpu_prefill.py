@@ -501,3 +501,31 @@ def test_caps_at_the_stated_bound(d, nk, cap):
             assert (np.abs(o - want[a:e, h]) <= tol).all()
             n += 1
     assert n == 8 and attn.status() == 0
+
+
+def test_rows_computed_again_for_seconds_are_not_a_hang():
+    """One SM, three items: 32 rows over 1.4 million keys whose first value is a NaN take about 3 s to compute
+    again, while the other roles wait for the next item's first block; nothing gives up (a wait's limit grows
+    with the keys) and the other sequence's outputs are as without the first."""
+    n, d = 1_400_000, 64
+    q, k, v, q0, k0 = inputs([32, 300], [n, 300], 1, 1, d, 4)
+    attn = DecodeAttention(1, 1, d, max_sms=1)
+    want, wlse = attn.prefill(q, k, v, dev([32, 332]), dev([n, n + 300]), lse=torch.zeros(332, 1, device=DEV))
+    v = v.clone()
+    v[0, 0, 3] = float("nan")
+    out, lse = attn.prefill(q, k, v, dev(q0), dev(k0), lse=torch.zeros(332, 1, device=DEV))
+    assert attn.status() == 0
+    assert torch.equal(out[32:], want[32:]) and torch.equal(lse[32:], wlse[32:])
+    assert torch.isnan(out[:32, 0, 3]).all()
+    # the others' exact values, with f32 weights and sums of 1.4 million
+    s = q[:32, 0].double() @ k[:n, 0].double().t() * d ** -0.5
+    p = torch.arange(32, device=DEV)[:, None] + n - 32
+    s.masked_fill_(torch.arange(n, device=DEV)[None] > p, -float("inf"))
+    z = torch.logsumexp(s, 1, keepdim=True)
+    w = torch.exp(s - z)
+    v[0, 0, 3] = 0
+    o, size = w @ v[:n, 0].double(), w @ v[:n, 0].double().abs()
+    off = 2.0 ** -16 + (n / 32 + 64) * U  # exponentials, then a sum of n / 32 groups of 32
+    keep = [e for e in range(d) if e != 3]
+    assert ((out[:32, 0].double() - o).abs() <= 2.0 ** -8 * o.abs() + off * size)[:, keep].all()
+    assert ((lse[:32] - z).abs() <= off + 2 * U * z.abs()).all()
