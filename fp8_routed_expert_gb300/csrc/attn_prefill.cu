@@ -746,14 +746,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     const float unit = capped ? (usual ? 2.f * kLog2e : 1.f) * (p.scale / p.softcap) : 0.f;
     const float scale2 = (!capped ? p.scale : usual ? -2.f * p.softcap : p.softcap) * kLog2e, offset = capped && usual ? p.softcap * kLog2e : 0.f;
     uint32_t step = 0;  // blocks that the tile has had
-    bool ok = true;
+    // A lane that gives up goes on with the others, over whatever there is, to where the
+    // warp votes on it, behind the item's blocks (a warp that was split would not get through
+    // its collective instructions, and a vote for each block cost 2% of short prompts).
     const auto wait = [&](uint64_t *bar, uint32_t parity) {
-      if (ok && !mbar_wait(bar, parity, &stop, p.wait_ns)) {
-        give_up(&stop, p.err);
-        ok = false;
-      }
+      if (!mbar_wait(bar, parity, &stop, p.wait_ns) && !stop) give_up(&stop, p.err);
       tc_fence_after();
-      return ok;
     };
     // The tile's products with V so far.  A barrier per S buffer: when a block's scores
     // are ready the products of the block before it in the same buffer are done, but
@@ -761,9 +759,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     // of a barrier's phases from the one before it.
     const auto products_done = [&] {
       const uint32_t n = step - 1u;
-      return kTiles == 2 ? wait(&o_full[t], n & 1u) : wait(&o_full[n & 1u], n >> 1 & 1u);
+      kTiles == 2 ? wait(&o_full[t], n & 1u) : wait(&o_full[n & 1u], n >> 1 & 1u);
     };
-    while (ok && item_ready()) {
+    while (__all_sync(0xffffffffu, item_ready())) {
       const Item &shared = ctl.items[turn];
       const struct {
         int q0, k0, n, m, tok0, kv, head0, heads;
@@ -798,7 +796,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         const int buf = kTiles == 2 ? t : (int)(step & 1u);
         const bool masked = j < whole_lo || j >= whole_hi;
         const uint32_t t_s = tmem + lanes + Z::kS + buf * kKeys;
-        if (!wait(&s_full[buf], (kTiles == 2 ? step : step >> 1) & 1u)) break;
+        wait(&s_full[buf], (kTiles == 2 ? step : step >> 1) & 1u);
         if (!rows) {
           if (lane == 0) mbar_arrive(&p_full[buf]);
           ++step;
@@ -881,7 +879,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
           if (j > lo) {
             // with two tiles, the products with V are done up to the last block's: they
             // came before this block's scores
-            if (kTiles == 1 && !products_done()) break;
+            if (kTiles == 1) products_done();
             tmem_wait_ld(s[0]);
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -933,7 +931,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         if (lane == 0) mbar_arrive(&p_full[buf]);
         ++step;
       }
-      if (!ok || (rows && lo < hi && !products_done())) break;
+      if (rows && lo < hi) products_done();
+      if (__any_sync(0xffffffffu, stop != 0)) break;
       if (rows) {
       const float2 s0 = unpack_f32x2(sum2[0]), s1 = unpack_f32x2(sum2[1]);
       const float sum = (s0.x + s0.y) + (s1.x + s1.y);

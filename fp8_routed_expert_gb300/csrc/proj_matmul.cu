@@ -248,9 +248,9 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
 #pragma unroll
       for (int j = 0; j < kMine / 2; ++j) acc[j] = 0;
       for (int b = it.b0; b < it.b1; b += R::kTurn) {
-        if (!mbar_wait(&sum_full[buf], bphase, &stop, kWaitNs)) {
+        // (to the vote: a warp that was split would not get through its collective instructions)
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sum_full[buf], bphase, &stop, kWaitNs)))) {
           give_up(&stop, p.err);
-          ok = false;
           break;
         }
         tc_fence_after();
