@@ -798,6 +798,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
         const uint32_t t_s = tmem + lanes + Z::kS + buf * kKeys;
         wait(&s_full[buf], (kTiles == 2 ? step : step >> 1) & 1u);
         if (!rows) {
+          tc_fence_before();  // of the outputs that the warp read where the products now go
           if (lane == 0) mbar_arrive(&p_full[buf]);
           ++step;
           continue;
