@@ -124,8 +124,8 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stages = p.stages;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1 + 32), mbar_init(&empty[s], 1);
-    for (int b = 0; b < 2; ++b) mbar_init(&sum_full[b], 1), mbar_init(&sum_empty[b], R::kSumWarps);
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1 + 32), mbar_init(&empty[s], 2);
+    for (int b = 0; b < 2; ++b) mbar_init(&sum_full[b], 2), mbar_init(&sum_empty[b], R::kSumWarps);
     stop = 0;
     fence_mbar_init();
     prefetch_tmap(&ta);
@@ -196,9 +196,13 @@ __global__ void __launch_bounds__(Quarters < 4 ? 256 : Ring<Columns, Quarters>::
           for (int k = 0; k < kBlock / 32; ++k)
             mma_e4m3_ss(leader, tmem + (uint32_t)((buf * R::kTurn + u) * Columns), a + k * 2, w + k * 2, idesc, k > 0 ? 1u : 0u);
           mma_commit_by(leader, &empty[stage]);
+          if (lane == 0) mbar_arrive(&empty[stage]);
           if (++stage == stages) stage = 0, phase ^= 1u;
         }
         mma_commit_by(leader, &sum_full[buf]);
+        // The scales, which other warps copy and read, pass through this one: commits tell of
+        // products alone, a thread's own arrival hands on what it has waited for.
+        if (lane == 0) mbar_arrive(&sum_full[buf]);
         buf ^= 1;
         if (buf == 0) bphase ^= 1u;
       }
