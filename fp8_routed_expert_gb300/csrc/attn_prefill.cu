@@ -724,16 +724,17 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) prefill_kernel(const __
     }
     if (!ok) give_up(&stop, p.err);
   } else if (warp >= 4) {
-    if (blockIdx.x == 0) {  // the starts are as they should be
-      bool bad = false;
-      for (int b = threadIdx.x - 128; b <= p.B; b += Z::kThreads - 128) {
-        const int qs = __ldg(p.q_starts + b), ks = __ldg(p.k_starts + b);
-        bad |= qs < 0 || qs > p.Tq || ks < 0 || ks > p.Tk;
-        if (b < p.B) bad |= __ldg(p.q_starts + b + 1) < qs || __ldg(p.k_starts + b + 1) < ks;
-      }
-      if (bad) set_error(p.err, DEV_ERR_BOUNDS);
-      __syncwarp();
+    // The starts are as they should be: each block that runs looks at all of them, while its
+    // first scores are on their way, as which blocks run is not known (another may take over
+    // any that has not started).
+    bool bad = false;
+    for (int b = threadIdx.x - 128; b <= p.B; b += Z::kThreads - 128) {
+      const int qs = __ldg(p.q_starts + b), ks = __ldg(p.k_starts + b);
+      bad |= qs < 0 || qs > p.Tq || ks < 0 || ks > p.Tk;
+      if (b < p.B) bad |= __ldg(p.q_starts + b + 1) < qs || __ldg(p.k_starts + b + 1) < ks;
     }
+    if (bad) set_error(p.err, DEV_ERR_BOUNDS);
+    __syncwarp();
     constexpr int kParts = kKeys / 32;
     const int t = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
