@@ -29,7 +29,8 @@ struct NormArgs {
   float *scales;  // of row t and block b: t * scale_row + b * scale_block
   int64_t scale_row, scale_block;
 };
-cudaError_t launch_norm(const NormArgs &a, int sms, cudaStream_t s);
+// limit: the SMs it may fill, 0 for all `sms`.
+cudaError_t launch_norm(const NormArgs &a, int sms, int limit, cudaStream_t s);
 
 struct MatmulArgs {
   int64_t M, N, K;
@@ -56,8 +57,8 @@ struct MatmulFit {
   int few[kMostSplits + 1], many[3][kMostSplits + 1];
 };
 cudaError_t ready_matmul(MatmulFit *fit);
-// Fills in the plan for M, N, K (blocks) on at most `sms` SMs.
-void plan_matmul(const MatmulFit &fit, int sms, MatmulArgs *m);
+// Fills in the plan for M, N, K (blocks) on `sms` SMs, or on at most `limit` unless that is 0.
+void plan_matmul(const MatmulFit &fit, int sms, int limit, MatmulArgs *m);
 cudaError_t launch_matmul(const CUtensorMap &a, const CUtensorMap &w, const CUtensorMap &o, const MatmulArgs &m, cudaStream_t s);
 
 }  // namespace fp8moe

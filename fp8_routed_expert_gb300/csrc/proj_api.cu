@@ -12,6 +12,7 @@ using namespace fp8moe;
 
 struct moe_proj {
   int device = 0, sms = 0;
+  int limit = 0;  // SMs that a call may fill, 0 for all
   MatmulFit fit{};
   int *err = nullptr;
   cudaStream_t last_stream = nullptr;
@@ -72,7 +73,8 @@ int moe_proj_init(moe_proj **out, int32_t device, int32_t max_sms) {
   if (p == nullptr) return MOE_ERR_NOMEM;
   p->device = device;
   p->fit = fit;
-  p->sms = max_sms > 0 && max_sms < sms ? max_sms : sms;
+  p->sms = sms;
+  p->limit = max_sms < sms ? max_sms : 0;
   if (cudaMalloc(&p->err, 256) != cudaSuccess) {
     cudaGetLastError();
     delete p;
@@ -148,7 +150,7 @@ int moe_proj_norm(moe_proj *p, const void *x, int64_t x_stride, const void *resi
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   PROJ_TRY(cudaSetDevice(p->device));
   p->last_stream = s;
-  PROJ_TRY(launch_norm(a, p->sms, s));
+  PROJ_TRY(launch_norm(a, p->sms, p->limit, s));
   return MOE_OK;
 }
 
@@ -183,7 +185,7 @@ int moe_proj_matmul(moe_proj *p, const uint8_t *a, int64_t a_stride, const float
   m.whole_lines = aligned(out, 32) && out_stride % 16 == 0;
   m.blocks = (int)((K + 127) / 128);
   m.err = p->err;
-  plan_matmul(p->fit, p->sms, &m);
+  plan_matmul(p->fit, p->sms, p->limit, &m);
   CUtensorMap ta, tw, to;
   const uint64_t a_sizes[2] = {(uint64_t)K, (uint64_t)M}, a_strides[1] = {(uint64_t)a_stride};
   const uint64_t w_sizes[2] = {(uint64_t)K, (uint64_t)N}, w_strides[1] = {(uint64_t)w_stride};

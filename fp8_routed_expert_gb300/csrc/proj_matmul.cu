@@ -499,7 +499,7 @@ cudaError_t ready_matmul(MatmulFit *fit) {
 //   700 x 512 x 7008      11.4: 128, 5; 64, 2 CTAs 12.2; 128 alone 14.4 (2)
 //   800 x 7000 x 400      10.9: 256, alone; 128 columns 11.7
 //   2048 x 2048 x 4096    19.5: 256, alone; 128 columns 24.7
-void plan_matmul(const MatmulFit &fit, int sms, MatmulArgs *m) {
+void plan_matmul(const MatmulFit &fit, int sms, int limit, MatmulArgs *m) {
   const bool few = m->M <= 64;
   const int64_t rows = (m->M + kRows - 1) / kRows;
   double best = 0.0;
@@ -509,7 +509,8 @@ void plan_matmul(const MatmulFit &fit, int sms, MatmulArgs *m) {
     const int64_t tiles = rows * ((m->N + columns - 1) / columns);
     const int *places = few ? fit.few : fit.many[i];
     for (int splits = 1; splits <= kMostSplits && splits <= m->blocks; ++splits) {
-      const int64_t most = (int64_t)sms * (few ? 2 : 1) / splits, resident = places[splits] < most ? places[splits] : most;
+      // (with a limit a CTA per SM: two would go to an SM each while others are idle)
+      const int64_t most = (limit > 0 ? limit : (int64_t)sms * (few ? 2 : 1)) / splits, resident = places[splits] < most ? places[splits] : most;
       if (splits > 1 && (tiles > resident || columns == 256)) continue;
       const double rounds = (double)((tiles + resident - 1) / (resident > 0 ? resident : 1));
       const double block = few ? 260.0 : columns == 64 ? 420.0 : columns == 128 ? 560.0 : 880.0;

@@ -234,23 +234,24 @@ __global__ void __launch_bounds__(Group > kCta ? Group : kCta) norm_kernel(const
 }
 
 template <int Group, int Vecs>
-cudaError_t launch_one(const NormArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_one(const NormArgs &a, int sms, int limit, cudaStream_t s) {
   constexpr int kThreads = Group > kCta ? Group : kCta, kRows = kThreads / Group;
   static const int resident = [] {
     int n = 0;
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_kernel<Group, Vecs>, kThreads, 0) == cudaSuccess && n > 0 ? n : 1;
   }();
-  const int64_t ctas = (a.T + kRows - 1) / kRows, most = (int64_t)sms * resident;
+  // with a limit a CTA per SM: more than one would go to an SM each while others are idle
+  const int64_t ctas = (a.T + kRows - 1) / kRows, most = limit > 0 ? limit : (int64_t)sms * resident;
   return launch_pdl(norm_kernel<Group, Vecs>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kThreads), 0, s, a);
 }
 
 template <int Group>
-cudaError_t launch_group(const NormArgs &a, int vecs, int sms, cudaStream_t s) {
+cudaError_t launch_group(const NormArgs &a, int vecs, int sms, int limit, cudaStream_t s) {
   switch (vecs) {
-    case 1: return launch_one<Group, 1>(a, sms, s);
-    case 2: return launch_one<Group, 2>(a, sms, s);
-    case 3: return launch_one<Group, 3>(a, sms, s);
-    default: return launch_one<Group, 4>(a, sms, s);
+    case 1: return launch_one<Group, 1>(a, sms, limit, s);
+    case 2: return launch_one<Group, 2>(a, sms, limit, s);
+    case 3: return launch_one<Group, 3>(a, sms, limit, s);
+    default: return launch_one<Group, 4>(a, sms, limit, s);
   }
 }
 
@@ -260,7 +261,7 @@ cudaError_t launch_group(const NormArgs &a, int vecs, int sms, cudaStream_t s) {
 // lanes, which hold less each (one row of 2048 by 256 lanes 1.65 us, by 64 lanes of four
 // vectors 2.9).  The grid is what is resident: more CTAs than that load their weights
 // again (777 rows of 2880 5.1 us, so 4.6).
-cudaError_t launch_norm(const NormArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_norm(const NormArgs &a, int sms, int limit, cudaStream_t s) {
   const int vecs = a.H / 8;
   int group = 0, per = 0;
   for (int v = 1; v <= 4; ++v) {
@@ -269,11 +270,11 @@ cudaError_t launch_norm(const NormArgs &a, int sms, cudaStream_t s) {
     if (g * v >= vecs && (group == 0 || g * v < group * per)) group = g, per = v;
   }
   switch (group) {
-    case 32: return launch_group<32>(a, per, sms, s);
-    case 64: return launch_group<64>(a, per, sms, s);
-    case 128: return launch_group<128>(a, per, sms, s);
-    case 256: return launch_group<256>(a, per, sms, s);
-    default: return launch_group<512>(a, per, sms, s);
+    case 32: return launch_group<32>(a, per, sms, limit, s);
+    case 64: return launch_group<64>(a, per, sms, limit, s);
+    case 128: return launch_group<128>(a, per, sms, limit, s);
+    case 256: return launch_group<256>(a, per, sms, limit, s);
+    default: return launch_group<512>(a, per, sms, limit, s);
   }
 }
 

@@ -19,7 +19,7 @@ BLOCK = 128  # columns (and rows of the weights) that share a scale
 
 class Projection:
     """A context of one device (moe_proj_init); ``max_sms``: the SMs a call may fill,
-    0 for all.
+    and the CTAs that it has at most, 0 for all.
 
     ``stream`` of a call is the torch stream, or its handle, that its kernels run on
     (None: the current one).  Outputs that are not given are allocated from that

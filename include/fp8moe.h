@@ -565,7 +565,8 @@ typedef struct moe_proj moe_proj; /* opaque; owned by the library */
 
 /*
  * moe_proj_init - a context of `device` (its error flag is all it owns); max_sms:
- * the SMs a call may fill, 0 for all.  Errors: MOE_ERR_ARG (out NULL),
+ * the SMs a call may fill, 0 for all (a limit is one of CTAs too: each of the call's may
+ * be on an SM of its own).  Errors: MOE_ERR_ARG (out NULL),
  * MOE_ERR_SHAPE (negative; both before any CUDA call), MOE_ERR_UNSUPPORTED,
  * MOE_ERR_CUDA, MOE_ERR_NOMEM.  On error *out is set to NULL and nothing is leaked.
  * Calls on one context may overlap on the GPU.

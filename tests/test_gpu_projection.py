@@ -13,6 +13,8 @@ Tolerances, from the arithmetic (u = 2^-24, half a step of f32):
     CTA of a cluster: (K / 4 + K / 64 + 24) u of the magnitudes, half a step 2^-8 of
     the output.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -369,3 +371,48 @@ def test_matmul_scales_at_the_ends_of_f32(proj, M, N, K):
     s0[0], s0[1] = 0.0, float("inf")
     got = proj.matmul(a, s0, w, sw)
     assert (got[0] == 0).all() and not torch.isfinite(got[1]).any() and torch.equal(got[2:], proj.matmul(a, sa, w, sw)[2:])
+
+
+def grids(run):
+    """CTAs of the kernels that `run` launches, as a graph that captures them has them."""
+    class Params(ctypes.Structure):
+        _fields_ = [("func", ctypes.c_void_p), *((n, ctypes.c_uint) for n in ("gx", "gy", "gz", "bx", "by", "bz", "shared")),
+                    *((n, ctypes.c_void_p) for n in ("params", "extra", "kern", "ctx"))]
+
+    run()
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g):
+        run()
+    cuda, handle, n = ctypes.CDLL("libcuda.so.1"), ctypes.c_void_p(g.raw_cuda_graph()), ctypes.c_size_t()
+    assert cuda.cuGraphGetNodes(handle, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert cuda.cuGraphGetNodes(handle, nodes, ctypes.byref(n)) == 0
+    found = []
+    for node in nodes:
+        kind, p = ctypes.c_int(-1), Params()
+        assert cuda.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        if kind.value == 0:  # a kernel
+            assert cuda.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), ctypes.byref(p)) == 0
+            found.append(p.gx * p.gy * p.gz)
+    return found
+
+
+@pytest.mark.parametrize("limit", [1, 5, 40])
+def test_a_limit_on_the_sms_is_one_of_ctas(proj, limit):
+    few, g = Projection(max_sms=limit), gen(limit)
+    for T, H in ((900, 640), (4000, 2048), (3, 64), (2000, 16384)):
+        x = rows(g, T, H)
+        n = grids(lambda: few.norm(x))
+        assert len(n) == 1 and 1 <= n[0] <= limit, n
+        assert torch.equal(few.norm(x), proj.norm(x))
+    for M, N, K in ((1, 4096, 2048), (33, 6000, 1000), (64, 700, 4000), (100, 512, 2048), (333, 1000, 2880), (2000, 2048, 512)):
+        args = make(g, M, N, K)
+        n = grids(lambda: few.matmul(*args))
+        assert len(n) == 1 and 1 <= n[0] <= limit, (M, N, K, n)
+        check_matmul(few, *args)
+    attn = DecodeAttention(8, 2, 128, max_sms=limit)
+    for Tq, Tk in ((1, 3000), (700, 700), (1000, 5000)):
+        q, k = rows(g, Tq, 1024).view(Tq, 8, 128), rows(g, Tk, 256).view(Tk, 2, 128)
+        starts = [torch.tensor([0, t], dtype=torch.int32, device=DEV) for t in (Tq, Tk)]
+        n = grids(lambda: attn.prefill(q, k, k, *starts))
+        assert len(n) == 1 and 1 <= n[0] <= limit, (Tq, Tk, n)
