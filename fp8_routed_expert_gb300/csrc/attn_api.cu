@@ -27,7 +27,8 @@ struct moe_attn {
   int sms = 0;                // of the device
   int *err = nullptr;
   uint64_t *turns = nullptr;  // [rope_dim / 2]
-  PrefillFit prefill;
+  PrefillFit prefill;         // asked for by the first prompt: many contexts decode alone
+  bool prefill_ready = false;
   DecodePlan wide, narrow;    // groups as large as may be, and of 8 heads at most
   // moe_attn_decode's workspace
   int group = 1, max_ctas = 0;
@@ -252,14 +253,11 @@ int moe_attn_init(moe_attn **out, const moe_attn_config *cfg) {
   ATTN_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, cfg->device));
   ATTN_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, cfg->device));
   if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
-  PrefillFit fit;
-  ATTN_TRY(ready_prefill(cfg->head_dim, &fit));
   moe_attn *a = new (std::nothrow) moe_attn();
   if (a == nullptr) return MOE_ERR_NOMEM;
   a->cfg = *cfg;
   a->cfg.rope_freqs = nullptr;  // the caller's array is not kept
   a->sms = sms;
-  a->prefill = fit;
   const int use = cfg->max_sms > 0 && cfg->max_sms < sms ? cfg->max_sms : sms;
   const int per_kv = cfg->n_heads / cfg->n_kv_heads;
   a->wide.group = decode_group(per_kv, cfg->head_dim, false);
@@ -531,6 +529,11 @@ int moe_attn_prefill(moe_attn *a, const void *q, int64_t q_stride, int64_t Tq, c
   CHECK(check_rows(out, out_stride, c.n_heads, c.head_dim));
   if (!q_starts || !k_starts) return MOE_ERR_ARG;
   if (!aligned(q_starts, 4) || !aligned(k_starts, 4) || !aligned(slopes, 4) || !aligned(lse, 4)) return MOE_ERR_ALIGN;
+  ATTN_TRY(cudaSetDevice(c.device));
+  if (!a->prefill_ready) {
+    ATTN_TRY(ready_prefill(c.head_dim, &a->prefill));
+    a->prefill_ready = true;
+  }
   PrefillArgs r{};
   r.q = static_cast<const __nv_bfloat16 *>(q);
   r.k = static_cast<const __nv_bfloat16 *>(k);
@@ -557,7 +560,6 @@ int moe_attn_prefill(moe_attn *a, const void *q, int64_t q_stride, int64_t Tq, c
   plan_prefill(&r, c.head_dim, c.max_sms > 0 && c.max_sms < a->sms ? c.max_sms : a->sms, a->prefill);
   if (r.items > INT64_C(0x7fffffff)) return MOE_ERR_SHAPE;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  ATTN_TRY(cudaSetDevice(c.device));
   a->last_stream = s;
   ATTN_TRY(launch_prefill(r, c.head_dim, c.max_sms > 0 && c.max_sms < a->sms ? c.max_sms : 0, s));
   return MOE_OK;

@@ -529,3 +529,15 @@ def test_rows_computed_again_for_seconds_are_not_a_hang():
     keep = [e for e in range(d) if e != 3]
     assert ((out[:32, 0].double() - o).abs() <= 2.0 ** -8 * o.abs() + off * size)[:, keep].all()
     assert ((lse[:32] - z).abs() <= off + 2 * U * z.abs()).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_the_first_prompt_of_a_context_may_be_captured(d):
+    """A context readies the prompts' kernels at its first prompt, which may be a captured one."""
+    q, k, v, q0, k0 = inputs([70, 1], [300, 2000], 4, 2, d, 6)
+    qs, ks, out = dev(q0), dev(k0), torch.zeros_like(q)
+    attn, g = DecodeAttention(4, 2, d), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        attn.prefill(q, k, v, qs, ks, out=out)
+    g.replay()
+    assert torch.equal(out, DecodeAttention(4, 2, d).prefill(q, k, v, qs, ks)) and attn.status() == 0
