@@ -20,8 +20,10 @@ import pytest
 import torch
 
 from fp8_routed_expert_gb300 import DecodeAttention, MoELayer, Projection
-from oracle import E4M3_TABLE
+from harness import check_output
+from oracle import E4M3_TABLE, moe_forward
 from oracle import projection as P
+from test_gpu_prefill import check as check_prompts
 
 pytestmark = pytest.mark.gpu
 
@@ -416,3 +418,49 @@ def test_a_limit_on_the_sms_is_one_of_ctas(proj, limit):
         starts = [torch.tensor([0, t], dtype=torch.int32, device=DEV) for t in (Tq, Tk)]
         n = grids(lambda: attn.prefill(q, k, k, *starts))
         assert len(n) == 1 and 1 <= n[0] <= limit, (Tq, Tk, n)
+
+
+def test_a_block_step_by_step():
+    """The same steps, each against its oracle on what the step before it gave: both residual sums, the codes of
+    both norms and of the attention's output, the attention, the projections, the norms' bf16 rows and the experts."""
+    g, proj = gen(41), Projection()
+    T, H, nh, nkv, d, I = 170, 512, 4, 2, 128, 256
+    x, res = rows(g, T, H), rows(g, T, H, 0.5)
+    w1, w2 = (torch.rand(H, generator=g, device=DEV) + 0.5 for _ in range(2))
+    wq, wo = e4m3(g, (nh + 2 * nkv) * d, H), e4m3(g, H, nh * d)
+    sq = torch.rand(nh + 2 * nkv, H // 128, generator=g, device=DEV) * 0.0008
+    so = torch.rand(H // 128, nh * d // 128, generator=g, device=DEV) * 0.02
+    starts = np.array([0, 90, 170], np.int32)
+
+    def product(got, c, s, w, sw):
+        want, size = P.matmul(c.cpu().numpy(), f64(s), w.cpu().numpy(), f64(sw))
+        k = c.shape[1]
+        close(got, want, 2.0 ** -8 * np.abs(want) + (k / 4 + k / 64 + 24) * U * size)
+
+    total = (x.float() + res.float()).to(torch.bfloat16)
+    c, s = proj.norm_quant(x, w1, residual=res)
+    assert torch.equal(res, total)
+    check_codes(c, s, P.norm(f64(total), f64(w1), 1e-6))
+    qkv = proj.matmul(c, s, wq, sq)
+    product(qkv, c, s, wq, sq)
+    q, k, v = qkv.view(T, -1, d).split([nh, nkv, nkv], dim=1)
+    o, _ = check_prompts(q, k, v, starts, starts)
+    co, s_o = proj.norm_quant(o.view(T, -1))
+    check_codes(co, s_o, f64(o.view(T, -1)))
+    y = proj.matmul(co, s_o, wo, so)
+    product(y, co, s_o, wo, so)
+    total = (y.float() + res.float()).to(torch.bfloat16)
+    assert not torch.equal(total, res)  # the projection matters
+    h = proj.norm(y, w2, residual=res)
+    assert torch.equal(res, total)
+    want = P.norm(f64(total), f64(w2), 1e-6)
+    close(h, want, (2.0 ** -8 + 32 * U) * np.abs(want))
+    router, w13, w2e = torch.randn(8, H, generator=g, device=DEV), e4m3(g, 8, 2 * I, H), e4m3(g, 8, H, I)
+    s13 = torch.rand(8, 2 * I // 128, H // 128, generator=g, device=DEV) * 0.001
+    s2 = torch.rand(8, H // 128, I // 128, generator=g, device=DEV) * 0.01
+    layer = MoELayer(T, H, 8, I, 2, 0)
+    z = layer.forward(h, router, None, w13, s13, w2e, s2, 2)
+    host = [t.cpu().numpy() for t in (router, w13, s13, w2e, s2)]
+    ref = moe_forward(h.view(torch.int16).cpu().numpy().view(np.uint16), host[0], None, *host[1:], 2)
+    check_output(z.view(torch.int16).cpu().numpy().view(np.uint16), ref)
+    assert proj.status() == 0 and layer.status() == 0
