@@ -3,8 +3,10 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 from oracle import E4M3_TABLE
+from oracle import paged_attention as D
 from oracle import prefill_attention as A
 from oracle import projection as P
 
@@ -92,3 +94,29 @@ def test_matmul_against_loops():
         terms = [E4M3_TABLE[a[m, k]] * sa[m, k // 128] * E4M3_TABLE[w[n, k]] * sw[n // 128, k // 128] for k in range(K)]
         assert abs(out[m, n] - math.fsum(terms)) <= 1e-12 * size[m, n]
     assert (size >= np.abs(out)).all()
+
+
+def test_prefill_last_token_against_the_paged_decode_oracle():
+    rng = np.random.default_rng(8)
+    q, k, v = rng.normal(size=(9, 6, 16)), rng.normal(size=(30, 2, 16)), rng.normal(size=(30, 2, 16))
+    for window, softcap, slopes in ((0, 0.0, None), (7, 0.0, None), (0, 3.0, None), (11, 2.0, [0.5, -0.25, 0.0, 1.0, 0.125, 2.0])):
+        out, lse, size = A.prefill(q, k, v, [0, 9], [0, 30], 0.25, True, softcap, slopes, window)
+        want, wlse, mag, _ = D.decode(q[8:], [k], [v], [30], None, 0.25, softcap, slopes, window)
+        assert np.allclose(out[8:], want, atol=1e-14) and np.allclose(lse[8:], wlse, atol=1e-13) and np.allclose(size[8:], mag, atol=1e-14)
+
+
+def test_codes_of_the_quotient_against_torch():
+    """The codes of a row are torch's conversion of the f32 quotient, for every scale a row of bf16 can have."""
+    rng = np.random.default_rng(9)
+    x = torch.from_numpy(rng.normal(size=(200, 256)) * np.exp(rng.normal(size=(200, 1)) * 20)).to(torch.bfloat16)
+    y = x.double().numpy()
+    s = P.block_scales(y)
+    assert (P.spread(s, 256)[:, ::128] == s).all()
+    s32 = (np.abs(y.astype(np.float32)).reshape(200, 2, 128).max(2) / np.float32(448)).astype(np.float32)
+    assert (np.abs(s32 - s) <= 2.0 ** -24 * s).all()
+    q = (y.astype(np.float32) / np.repeat(s32, 128, 1)).astype(np.float32)
+    codes = torch.from_numpy(q).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert (D.e4m3_round(q.astype(np.float64)) == codes).all()
+    table = np.asarray(E4M3_TABLE, np.float64)
+    top = np.abs(table[codes]).reshape(200, 2, 128).max(2)
+    assert (top == 448).all()
