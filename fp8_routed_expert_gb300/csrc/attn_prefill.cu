@@ -31,12 +31,16 @@
 // rewritten, in every block: 8192 tokens, 16 heads of 128 elements, 305 us, so 245 at that step).
 // Without them forwards is 3% faster, as an item's two tiles start together.
 //
-// What bounds it: 16384 tokens, 32 heads over 8 of 128 elements, take 1350 us, 1630
-// TFLOP/s, 85% of the measured bf16 rate; a warp's softmax of a block and the other tile's
-// products take about the same time.  With 256 elements 1365 TFLOP/s (one tile), with 64
-// 995 (the exponentials are twice as many per product).  12 prompts of up to 2048 in 109
-// us: the tensor cores are busy 47% of it, as masked blocks cost twice, and an item has
-// few of them to spread its first and last steps over; 60 of up to 700 with slopes 100.
+// What bounds it: 16384 tokens, 32 heads over 8 of 128 elements, take 1355 to 1415 us in
+// bursts of a few milliseconds, 1560 to 1620 TFLOP/s or 81 to 85% of the measured bf16 rate
+// of a burst, and 1450 back to back, 89% of the sustained rate; a warp's softmax of a block
+// and the other tile's products take about the same time.  8192 tokens, 16 heads over 8:
+// 1460 TFLOP/s, with 256 elements 1370 (one tile), with 64 885 (the exponentials are twice
+// as many per product).  12 prompts of up to 2048 in 110 us: the tensor cores are busy 45%
+// of it, as masked blocks cost twice, and an item has few of them to spread its first and
+// last steps over; 60 of up to 700 with slopes 102.  The few registers that some kernels
+// spill are an item's, not a block's (5 local loads per warp and item, 0.1% of the
+// instructions); those of shared items without options take 8 per warp and block, 1.3%.
 //
 // Weights are rounded to bf16 for the second product, the matrix unit's type for bf16
 // values: 2^-8 of each weight at most.  More bits would take a second product with what

@@ -11,9 +11,10 @@
 // buffer fills: lane = row, so a thread's scale is one number per block (and 128 columns).
 //
 // What bounds it.  Few rows: launch, one chain of loads, products, sums and, where tiles
-// are split, the exchange: 1 x 6144 x 2048 takes 6.3 to 7.2 us where the weights alone take
-// 1.9 at the copy rate, 64 x 8192 x 4096 10.4 of 5.1.  Many: 4096 x 8192 x 6144 takes
-// 162 to 164 us, 2530 TFLOP/s: a block of 128 x 256 in about 880 cycles, of which its
+// are split, the exchange: 1 x 6144 x 2048 takes 7.0 to 7.4 us where the weights alone take
+// 1.9 at the copy rate, 64 x 8192 x 4096 10.5 of 5.1.  Many: 4096 x 8192 x 6144 takes
+// 165 to 168 us in bursts of a few milliseconds, 2480 TFLOP/s, and 172 to 177 back to back,
+// where the clocks come down: a block of 128 x 256 in about 880 cycles, of which its
 // products take 520.  A summing warp waits 140 of them and adds up for 650 (its packed FMAs
 // alone take 290 of a sub-partition's issue); between tiles go 2500.  16 summing warps
 // (200 to 217 us) were no faster.
@@ -488,17 +489,19 @@ cudaError_t ready_matmul(MatmulFit *fit) {
 }
 
 // How a product is split.  A tile's K blocks go over as many CTAs as are resident
-// together: clusters that come in a second round double the time (48 clusters of three
-// where 46 are resident, 1 x 6144 x 2048: 11.3 us, 96 clusters of two 6.3).  The time is
+// together: clusters that come in a second round double the time.  The time is
 // about, in cycles: a block 420, 560 and 880 for 64, 128 and 256 columns (260 with few
 // rows), a tile's start and end 2000, 2600 and 2500, a cluster's exchange 150 for each CTA
 // and what a CTA pushes at 12 bytes.  Against the best of all splits (us):
-//   64 x 2048 x 2048      5.3: 64 columns, 4 CTAs; 8 CTAs 6.1, alone 7.3
-//   333 x 1000 x 2880     8.4: 64, 2; 128 columns, 4 CTAs 9.2, alone 10.4 (2)
-//   512 x 4096 x 4096     13.9: 128, alone; 256 columns 18.7
-//   700 x 512 x 7008      11.4: 128, 5; 64, 2 CTAs 12.2; 128 alone 14.4 (2)
-//   800 x 7000 x 400      10.9: 256, alone; 128 columns 11.7
-//   2048 x 2048 x 4096    19.5: 256, alone; 128 columns 24.7
+//   64 x 2048 x 2048      5.5: 64 columns, 4 CTAs; 3 CTAs 5.9, 8 CTAs 6.5, 2 CTAs 6.4
+//   16 x 4096 x 4096      6.6: 64, 4; 3 CTAs 7.4, 2 CTAs 8.1, alone 11.1
+//   333 x 1000 x 2880     8.2: 64, 2; 128 columns, 4 CTAs 9.1; 64 alone 9.3
+//   512 x 4096 x 4096     14.2: 128, alone; 256 columns 18.9
+//   700 x 512 x 7008      11.4: 128, 5; 64, 2 CTAs 12.3; 128, 2 CTAs 14.4
+//   800 x 7000 x 400      10.9: 256, alone; 128 columns 11.9
+//   2048 x 2048 x 4096    19.8: 256, alone; 128 columns 25.2
+//   1 x 6144 x 2048       7.0: 64, 3, where 2 CTAs take 6.3 and one 7.2: the largest miss
+// of these, the others are the best.
 void plan_matmul(const MatmulFit &fit, int sms, int limit, MatmulArgs *m) {
   const bool few = m->M <= 64;
   const int64_t rows = (m->M + kRows - 1) / kRows;
