@@ -108,6 +108,7 @@ def lib():
         "moe_attn_decode_clusters": ([vp, vp, i64, i64], ctypes.c_int),
         "moe_attn_prefill": ([vp, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i64, i32, f32, f32, vp, i32, vp, i64, vp,
                               vp], ctypes.c_int),
+        "moe_attn_prefill_bits": ([vp, i32], ctypes.c_int),
         "moe_proj_init": ([ctypes.POINTER(ctypes.c_void_p), i32, i32], ctypes.c_int),
         "moe_proj_free": ([vp], None),
         "moe_proj_status": ([vp], ctypes.c_int),

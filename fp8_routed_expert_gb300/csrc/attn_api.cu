@@ -28,7 +28,8 @@ struct moe_attn {
   int *err = nullptr;
   uint64_t *turns = nullptr;  // [rope_dim / 2]
   PrefillFit prefill;         // asked for by the first prompt: many contexts decode alone
-  bool prefill_ready = false;
+  int prefill_bits = 8;       // of the prompts' weights
+  int prefill_ready = 0;      // bits of the kernels that are ready
   DecodePlan wide, narrow;    // groups as large as may be, and of 8 heads at most
   // moe_attn_decode's workspace
   int group = 1, max_ctas = 0;
@@ -316,6 +317,13 @@ void moe_attn_free(moe_attn *a) {
   delete a;
 }
 
+int moe_attn_prefill_bits(moe_attn *a, int32_t bits) {
+  if (a == nullptr) return MOE_ERR_ARG;
+  if (bits != 8 && bits != 16) return MOE_ERR_SHAPE;
+  a->prefill_bits = bits;
+  return MOE_OK;
+}
+
 int moe_attn_status(moe_attn *a) {
   if (a == nullptr) return MOE_ERR_ARG;
   ATTN_TRY(cudaSetDevice(a->cfg.device));
@@ -530,9 +538,9 @@ int moe_attn_prefill(moe_attn *a, const void *q, int64_t q_stride, int64_t Tq, c
   if (!q_starts || !k_starts) return MOE_ERR_ARG;
   if (!aligned(q_starts, 4) || !aligned(k_starts, 4) || !aligned(slopes, 4) || !aligned(lse, 4)) return MOE_ERR_ALIGN;
   ATTN_TRY(cudaSetDevice(c.device));
-  if (!a->prefill_ready) {
-    ATTN_TRY(ready_prefill(c.head_dim, &a->prefill));
-    a->prefill_ready = true;
+  if ((a->prefill_ready & a->prefill_bits) == 0) {
+    ATTN_TRY(ready_prefill(c.head_dim, a->prefill_bits, &a->prefill));
+    a->prefill_ready |= a->prefill_bits;
   }
   PrefillArgs r{};
   r.q = static_cast<const __nv_bfloat16 *>(q);
@@ -561,7 +569,7 @@ int moe_attn_prefill(moe_attn *a, const void *q, int64_t q_stride, int64_t Tq, c
   if (r.items > INT64_C(0x7fffffff)) return MOE_ERR_SHAPE;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   a->last_stream = s;
-  ATTN_TRY(launch_prefill(r, c.head_dim, c.max_sms > 0 && c.max_sms < a->sms ? c.max_sms : 0, s));
+  ATTN_TRY(launch_prefill(r, c.head_dim, a->prefill_bits, c.max_sms > 0 && c.max_sms < a->sms ? c.max_sms : 0, s));
   return MOE_OK;
 }
 

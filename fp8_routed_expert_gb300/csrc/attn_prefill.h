@@ -37,9 +37,9 @@ struct PrefillFit {
 };
 // Fills in heads, chunks, tokens, items and splits, for so many SMs.
 void plan_prefill(PrefillArgs *a, int d, int sms, const PrefillFit &fit);
-// Readies the kernels of d.
-cudaError_t ready_prefill(int d, PrefillFit *fit);
+// Readies the kernels of d whose weights keep 8 or 16 bits.
+cudaError_t ready_prefill(int d, int bits, PrefillFit *fit);
 // sms: the SMs it may fill, 0 for all.
-cudaError_t launch_prefill(const PrefillArgs &a, int d, int sms, cudaStream_t s);
+cudaError_t launch_prefill(const PrefillArgs &a, int d, int bits, int sms, cudaStream_t s);
 
 }  // namespace fp8moe

@@ -529,7 +529,8 @@ int moe_attn_decode_clusters(const moe_attn *a, const moe_paged_kv *kv, int64_t 
  * one whose scores rise by more than 88 within a block, is computed a second time, a
  * hundred times as slowly.
  * Sums and softmax statistics are f32; for their product with the values, weights
- * are rounded to bf16 (2^-8 of each at most, as the output is); out is rounded to bf16.
+ * are rounded to bf16 (2^-8 of each at most, as the output is), or keep 16 bits if
+ * the caller chooses (moe_attn_prefill_bits); out is rounded to bf16.
  * A cap of at most 128 makes a score off by 2^-19 of the cap at most, one above by 2^-20
  * of the score.
  *   q       : device bf16 [Tq, n_heads, d] rows as for moe_attn_norm_rope (a slice of
@@ -552,6 +553,13 @@ int moe_attn_prefill(moe_attn *a, const void *q, int64_t q_stride, int64_t Tq, c
                      const int32_t *k_starts, int64_t B, int32_t causal, float scale, float softcap,
                      const float *slopes, int32_t window, void *out, int64_t out_stride, float *lse,
                      void *stream);
+
+/*
+ * moe_attn_prefill_bits - the bits that the weights of later moe_attn_prefill calls
+ * keep for their product with the values: 8 (the default: 2^-8 of each weight is lost
+ * at most) or 16 (2^-15), which takes 1.1 to 1.5 times as long.  Others: MOE_ERR_SHAPE.
+ */
+int moe_attn_prefill_bits(moe_attn *a, int32_t bits);
 
 /*
  * Projections around the attention and the MoE, in the experts' weight format

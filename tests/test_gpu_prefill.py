@@ -13,7 +13,7 @@ import numpy as np
 import pytest
 import torch
 
-from fp8_routed_expert_gb300 import C, DecodeAttention, PagedKVCache
+from fp8_routed_expert_gb300 import C, DecodeAttention, PagedKVCache, lib
 from oracle import prefill_attention as A
 
 pytestmark = pytest.mark.gpu
@@ -541,3 +541,74 @@ def test_the_first_prompt_of_a_context_may_be_captured(d):
         attn.prefill(q, k, v, qs, ks, out=out)
     g.replay()
     assert torch.equal(out, DecodeAttention(4, 2, d).prefill(q, k, v, qs, ks)) and attn.status() == 0
+
+
+def check16(q, k, v, q0, k0, causal=True, softcap=0.0, slopes=None, window=0, scale=None):
+    """Weights of 16 bits: each is off by 2^-15 at most besides the scores' errors, so that outputs that are small
+    beside their terms keep far more than 8 bits of these."""
+    nh, d = q.shape[1:]
+    attn = DecodeAttention(nh, k.shape[1], d, prefill_bits=16)
+    lse = torch.zeros(q.shape[:2], device=DEV)
+    out, _ = attn.prefill(q, k, v, dev(q0), dev(k0), causal=causal, softcap=softcap, slopes=slopes, window=window, scale=scale, lse=lse)
+    assert attn.status() == 0
+    real, sl = d ** -0.5 if scale is None else scale, None if slopes is None else f64(slopes)
+    Q, K, V = f64(q), f64(k), f64(v)
+    want, wlse, size = A.prefill(Q, K, V, q0, k0, real, causal, softcap, sl, window)
+    o, z = f64(out), f64(lse)
+    for b in range(len(q0) - 1):
+        a, e, c, f = q0[b], q0[b + 1], k0[b], k0[b + 1]
+        for h in range(nh if e > a else 0):
+            reach = (np.abs(Q[a:e, h]) @ np.abs(K[c:f, h // (nh // k.shape[1])]).T).max() * abs(real) if f > c else 0.0
+            far = 0.0 if sl is None else abs(sl[h]) * max(f - c, e - a)
+            off = (d / 2 + 16) * U * reach + (2.0 ** -19 * softcap if softcap <= 128 else 2.0 ** -20 * reach) + 4 * U * far
+            off += 2.0 ** -20 + ((f - c) / 2 + 64) * U
+            none = np.isneginf(wlse[a:e, h])
+            assert (np.isneginf(z[a:e, h]) == none).all()
+            w, wz = want[a:e, h], np.where(none, 0, wlse[a:e, h])
+            assert (np.abs(np.where(none, 0, z[a:e, h]) - wz) <= off + 2 * U * np.abs(wz)).all()
+            bad = np.abs(o[a:e, h] - w) > 2.0 ** -8 * np.abs(w) + (2.0 ** -15 + 2 * off) * size[a:e, h]
+            assert not bad.any(), (b, h, int(bad.sum()))
+    return attn, out
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("nq,nk,nh,nkv", [([1], [1], 2, 2), ([64, 65, 0, 1], [64, 65, 0, 129], 4, 1), ([150, 1, 0, 260, 40], [420, 1, 9, 260, 10], 6, 2),
+                                          ([20, 90], [3000, 1000], 8, 2), ([700], [700], 2, 2), ([40, 41], [90, 41], 17, 1)])
+def test_weights_of_sixteen_bits(d, nq, nk, nh, nkv):
+    check16(*inputs(nq, nk, nh, nkv, d, sum(nk) + d, before=2, behind=3))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal,window,softcap,slopes,scale,size", [
+    (False, 0, 0.0, False, None, 1.0), (True, 100, 0.0, False, None, 2.0), (True, 0, 20.0, False, None, 2.0), (True, 0, 200.0, True, None, 2.0),
+    (True, 0, 0.0, True, None, 1.0), (True, 0, 0.0, False, 0.25, 3.0), (False, 37, 5.0, True, -0.2, 1.0)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_weights_of_sixteen_bits_with_options(d, causal, window, softcap, slopes, scale, size, shared):
+    q, k, v, q0, k0 = inputs([20] if shared else [150, 260], [4000] if shared else [420, 260], 6, 2, d, window + d, behind=2, size=size)
+    sl = torch.tensor([0.5, 0.25, 0.125, -0.01, 0.0, 2.0], device=DEV) if slopes else None
+    check16(q, k, v, q0, k0, causal, softcap, sl, window, scale)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_sixteen_bits_special_values_and_bits_on_demand(d):
+    """A NaN that some rows see, infinities in hidden places; the same bits in a graph and after a turn of 8 bits."""
+    q, k, v, q0, k0 = inputs([300, 50, 9], [300, 50, 2000], 4, 2, d, 3)
+    attn, want = check16(q, k, v, q0, k0)
+    qs, ks = dev(q0), dev(k0)
+    with pytest.raises(RuntimeError):
+        DecodeAttention(4, 2, d, prefill_bits=12)
+    eight = DecodeAttention(4, 2, d).prefill(q, k, v, qs, ks)
+    assert not torch.equal(eight, want) and (eight.float() - want.float()).abs().max() < 2.0 ** -6 * 5
+    assert lib().moe_attn_prefill_bits(attn.handle, 8) == 0
+    assert torch.equal(attn.prefill(q, k, v, qs, ks), eight)
+    assert lib().moe_attn_prefill_bits(attn.handle, 16) == 0
+    out, g = torch.zeros_like(q), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        attn.prefill(q, k, v, qs, ks, out=out)
+    g.replay()
+    assert torch.equal(out, want)
+    v = v.clone()
+    v[100, 0, 3], v[349, 1, 0] = float("nan"), float("inf")  # seen by rows 100.. of two heads, by the last row of the second sequence
+    got = attn.prefill(q, k, v, qs, ks)
+    assert torch.isnan(got[100:300, :2, 3]).all() and torch.isfinite(got[:100]).all() and torch.isfinite(got[300:349]).all()
+    assert (got[349, 2:, 0] == float("inf")).all() and torch.isfinite(got[:, 2:, 1:]).all() and attn.status() == 0

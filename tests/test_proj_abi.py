@@ -158,3 +158,8 @@ def test_outputs_come_from_the_memory_of_the_calls_stream(monkeypatch):
             made.clear(), ran.clear()
             call(given)
             assert made == [used] * outputs and ran == [used] and current == [5]
+
+
+def test_bits_of_the_prompts_weights(L, ctx):
+    assert L.moe_attn_prefill_bits(None, 8) == ARG
+    assert [L.moe_attn_prefill_bits(ctx, b) for b in (0, 7, 9, 32, -8)] == [SHAPE] * 5
